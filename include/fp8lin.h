@@ -54,6 +54,8 @@
  *     wherever a transposed copy (or a GEMM operand) has them as its row
  *     length.  In practice: M, K, N multiples of 16.
  *   - Inputs are NaN-free by contract; NaN propagation is not specified.
+ *     The 4-bit operands and the gradient calls say below what they do with
+ *     NaN and infinities, and which sizes and alignments they take.
  *   - Per-device set-up (kernel shared-memory attributes, occupancy counts,
  *     the device address of fp8lin_amax_noalloc's static array) is done by
  *     the first call on each device and kept for the life of the process,
@@ -455,6 +457,144 @@ fp8lin_status fp8lin_step_host(const void* x_h, const void* w_h, const void* dy_
                                cudaStream_t compute, cudaStream_t h2d, cudaStream_t d2h,
                                int wait);
 
+/* ---- 4-bit operands ---------------------------------------------------- */
+
+/* Microscaled 4-bit floating point: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives) that share a scale over a block of consecutive values
+ * of a row.
+ *   NVFP4  blocks of 16, e4m3 block scales, one fp32 scale a tensor:
+ *            S = fl32(448 / max(amax, eps)), inv = fl32(1 / S)  (fp8lin_scale
+ *                of an e4m3 state: dynamic, delayed or precomputed)
+ *            c = e4m3(fl32(b * S)),  b = max |x| over the block
+ *            q = e2m1(fl32(x * r)),  r = fl32(fl32(6 * S) / c), 0 where c is 0
+ *          a value is q * c * fl32(inv / 6)
+ *   MXFP4  blocks of 32, power-of-two block scales (one byte, E):
+ *            E = max(e - 2, 0), e the exponent field of b; 255 for inf / NaN
+ *            q = e2m1(x * 2^(127 - E))
+ *          a value is q * 2^(E - 127)
+ * All conversions round to nearest even and saturate, so the bytes are
+ * defined bit for bit.  A NaN makes its block's scale NaN; in NVFP4 a NaN or
+ * an infinity anywhere makes every value of the tensor decode to NaN. */
+typedef enum { FP8LIN_NVFP4 = 0, FP8LIN_MXFP4 = 1 } fp8lin_fp4_fmt;
+
+/* A [rows, cols] tensor in 4 bits.  The struct is host memory; the pointers
+ * are caller-owned device buffers.
+ *   codes      [rows, ld bytes]: two codes a byte, the even column in the low
+ *              half; ld a multiple of 16, at least ceil(cols / 32) * 16.  Codes
+ *              past cols, up to the next multiple of 32, are 0.
+ *   scales     fp8lin_fp4_scale_bytes(rows, cols, fmt) bytes: tiles of 512
+ *              bytes, one for 128 rows x 4 blocks, block (r, k) of a tile at
+ *              byte (r % 32) * 16 + (r / 32) * 4 + k; the tiles of 128 rows
+ *              lie one after another along the row.  Scales past rows or past
+ *              the last block are 0.
+ *   inv_scale  NVFP4: fp32[1], the inverse of the tensorwise scale (the
+ *              inv_scale of the state that the tensor was quantised with);
+ *              MXFP4: NULL
+ * codes and scales 16-byte aligned. */
+typedef struct fp8lin_fp4_tensor {
+  uint8_t* codes;
+  uint8_t* scales;
+  const float* inv_scale;
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;
+  int32_t fmt;
+} fp8lin_fp4_tensor;
+
+/* Bytes of the scales of a [rows, cols] tensor (0 for a negative size or an
+ * unknown format). */
+size_t fp8lin_fp4_scale_bytes(int64_t rows, int64_t cols, int32_t fmt);
+
+/* Quantise the bf16 [rows, cols] tensor x (any row stride ld >= cols, any
+ * sizes, 2-byte alignment; 16-byte aligned rows load faster) into out
+ * ([rows, cols], blocks along x's rows), out_t ([cols, rows], blocks along x's
+ * columns: the copy a backward contracts over) or both; one of them may be
+ * NULL.  Both must have the same fmt.
+ * st: NVFP4, an e4m3 scaling state whose inv_scale is the inv_scale of out and
+ * out_t.  Dynamic: the amax of x is computed (amax_algo; PRECOMPUTED takes
+ * *st->amax as it is), then S and inv are written.  Delayed: S is *st->scale,
+ * the amax is recorded in the same pass (amax init first while needs_init is
+ * set), as in fp8lin_cast_delayed.  MXFP4: NULL.
+ * An empty tensor leaves the state as an amax of 0 does.  EINVAL where out's
+ * or out_t's sizes are not x's. */
+fp8lin_status fp8lin_fp4_quantise(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                                  fp8lin_scaling_state* st, const fp8lin_fp4_tensor* out,
+                                  const fp8lin_fp4_tensor* out_t, void* ws, cudaStream_t stream);
+
+/* The values t stands for, into out ([rows, cols], row stride ldo, any
+ * alignment of its element): fl32(fl32(q * c) * fl32(inv / 6)), or
+ * q * 2^(E - 127), rounded once more to bf16 unless f32 is nonzero (fp32
+ * out). */
+fp8lin_status fp8lin_fp4_dequantise(const fp8lin_fp4_tensor* t, void* out, int64_t ldo,
+                                    int32_t f32, cudaStream_t stream);
+
+/* d[m, n] = bf16(alpha * sum_k a[m, k] * b[n, k]) over the values without
+ * their tensorwise scales, accumulated in fp32 on the tensor cores, with
+ * alpha = fl32(inv_a / 6) * fl32(inv_b / 6) (NVFP4) or 1 (MXFP4).  a [M, K] and
+ * b [N, K] have the same fmt and cols.  d: bf16 [M, N], row stride ldd >= N, any
+ * alignment (16-byte aligned rows store faster).  K == 0 writes zeros. */
+fp8lin_status fp8lin_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
+                              int64_t ldd, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* y = x W^T with x quantised on the way: fp8lin_fp4_quantise of x into x4,
+ * then fp8lin_fp4_gemm of x4 and w4 into y -- the Linear of a model whose
+ * weights are kept in 4 bits.  x: bf16 [x4->rows, x4->cols], row stride ldx. */
+fp8lin_status fp8lin_fp4_linear(const void* x, int64_t ldx, fp8lin_scaling_state* sx,
+                                const fp8lin_fp4_tensor* x4, const fp8lin_fp4_tensor* w4, void* y,
+                                int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Forward of a Linear in 4 bits: x ([M, K] dense) into x4 and x4t, W ([N, K]
+ * dense) into w4 and w4t, y = x4 . w4^T (bf16 [M, N] dense).  w == NULL uses w4
+ * as an earlier call left it.  x4t and w4t are what fp8lin_fp4_backward
+ * needs; either may be NULL where no backward follows.  sx, sw: NVFP4 states,
+ * NULL for MXFP4. */
+fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_state* sx,
+                                 fp8lin_scaling_state* sw, const fp8lin_fp4_tensor* x4,
+                                 const fp8lin_fp4_tensor* x4t, const fp8lin_fp4_tensor* w4,
+                                 const fp8lin_fp4_tensor* w4t, void* y, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream);
+
+/* Backward of a Linear in 4 bits: dY ([M, N] dense) into dy4 and dy4t, then
+ *   dX = dy4 . w4t^T   (bf16 [M, K] dense, skipped if dx == NULL)
+ *   dW = dy4t . x4t^T  (bf16 [N, K] dense, skipped if dw == NULL). */
+fp8lin_status fp8lin_fp4_backward(const void* dy, fp8lin_scaling_state* sdy,
+                                  const fp8lin_fp4_tensor* dy4, const fp8lin_fp4_tensor* dy4t,
+                                  const fp8lin_fp4_tensor* w4t, const fp8lin_fp4_tensor* x4t,
+                                  void* dx, void* dw, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
+/* ---- gradient norm and clipping ------------------------------------------ */
+
+/* One tensor of a list: n dense values at g (device, aligned to its element)
+ * and, for fp8lin_grad_clip, n values at out (out == g: in place).  g_f32,
+ * out_f32: fp32 where nonzero, else bf16. */
+typedef struct fp8lin_grad {
+  const void* g;
+  void* out;
+  int64_t n;
+  int32_t g_f32;
+  int32_t out_f32;
+} fp8lin_grad;
+
+/* *norm = sqrt(sum over the list of g^2), fp32.  Squares are added in fp32
+ * within a thread and in fp64 above that, in a fixed order (the same list
+ * gives the same bits).  An empty list gives 0; NaN and infinities show in the
+ * norm.  The list is host memory, read during the call only. */
+fp8lin_status fp8lin_grad_norm(const fp8lin_grad* grads, int32_t count, float* norm, void* ws,
+                               size_t ws_bytes, cudaStream_t stream);
+
+/* out = g * min(1, max_norm / (*norm + eps)) for every tensor of the list,
+ * with *norm as fp8lin_grad_norm (or a reduction over ranks) left it on the
+ * device.  A NaN norm makes every value NaN; an infinite one makes every
+ * finite value 0.  out may be g itself; no other overlap is allowed. */
+fp8lin_status fp8lin_grad_clip(const fp8lin_grad* grads, int32_t count, const float* norm,
+                               float max_norm, float eps, cudaStream_t stream);
+
+/* fp8lin_grad_norm, then fp8lin_grad_clip. */
+fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, float max_norm,
+                                    float eps, float* norm, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
 /* ---- measurement hooks ------------------------------------------------ */
 
 /* Count of kernels this library has launched in the process. */
@@ -472,6 +612,9 @@ enum {
   FP8LIN_PROF_SMALL_M = 5,   /* a few-token product fused with its casts */
   FP8LIN_PROF_KINDS = 6
 };
+/* The 4-bit quantisations count as CAST (CAST_FUSED where they compute the
+ * amax too), the 4-bit products as GEMM, the gradient norm as AMAX and the
+ * gradient scaling as SCALE. */
 void fp8lin_profile_enable(int on);
 fp8lin_status fp8lin_profile_collect(double* ms, int64_t* count);
 

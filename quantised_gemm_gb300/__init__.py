@@ -28,7 +28,7 @@ import torch
 from . import _lib
 from ._lib import (AMAX_ATOMIC, AMAX_AUTO, AMAX_PRECOMPUTED, AMAX_REDUCTION, AMAX_SINGLE_PASS,
                    DELAYED, DYNAMIC,
-                   E4M3, E5M2, Fp8linError, PROF_KINDS)
+                   E4M3, E5M2, Fp8linError, MXFP4, NVFP4, PROF_KINDS)
 
 __all__ = [
     "E4M3", "E5M2", "AMAX_ATOMIC", "AMAX_REDUCTION", "AMAX_SINGLE_PASS", "AMAX_AUTO",
@@ -40,6 +40,8 @@ __all__ = [
     "profile_enable", "profile_collect", "profile_launches", "Fp8Linear", "link_linears", "library", "Float8Linear",
     "Float8LinearConfig", "CastConfig", "convert_to_float8_training",
     "sync_float8_amax_and_scale_history",
+    "NVFP4", "MXFP4", "Fp4Tensor", "Fp4Linear", "fp4_quantise", "fp4_dequantise", "fp4_gemm",
+    "fp4_linear", "grad_norm", "clip_grads", "clip_grad_norm",
 ]
 
 
@@ -338,3 +340,6 @@ def profile_launches(capacity: int = 8192) -> list:
 from .linear import Fp8Linear, link_linears  # noqa: E402
 from .nn import (CastConfig, Float8Linear, Float8LinearConfig,  # noqa: E402
                  convert_to_float8_training, sync_float8_amax_and_scale_history)
+from .fp4 import (Fp4Linear, Fp4Tensor, fp4_dequantise, fp4_gemm, fp4_linear,  # noqa: E402
+                  fp4_quantise)
+from .clip import clip_grad_norm, clip_grads, grad_norm  # noqa: E402

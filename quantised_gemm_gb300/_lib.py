@@ -20,6 +20,8 @@ E4M3, E5M2 = 0, 1
 AMAX_ATOMIC, AMAX_REDUCTION, AMAX_SINGLE_PASS, AMAX_AUTO, AMAX_PRECOMPUTED = 0, 1, 2, 3, 4
 # fp8lin_scaling
 DYNAMIC, DELAYED = 0, 1
+# fp8lin_fp4_fmt
+NVFP4, MXFP4 = 0, 1
 # profile kinds
 PROF_KINDS = ("amax", "scale", "cast", "cast_fused", "gemm", "small_m")
 
@@ -50,6 +52,30 @@ class StepSlotC(ctypes.Structure):
     ]
 
 
+class Fp4TensorC(ctypes.Structure):
+    """Mirror of struct fp8lin_fp4_tensor."""
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("inv_scale", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("fmt", ctypes.c_int32),
+    ]
+
+
+class GradC(ctypes.Structure):
+    """Mirror of struct fp8lin_grad."""
+    _fields_ = [
+        ("g", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("g_f32", ctypes.c_int32),
+        ("out_f32", ctypes.c_int32),
+    ]
+
+
 class Fp8linError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -67,6 +93,9 @@ _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _ST = ctypes.POINTER(ScalingStateC)
+_T4 = ctypes.POINTER(Fp4TensorC)
+_GR = ctypes.POINTER(GradC)
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "fp8lin_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -96,6 +125,16 @@ _SIGNATURES = {
                                        _P, _P, _P, _P, _P, _SZ, _P]),
     "fp8lin_step_host": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _ST, _ST, _ST,
                                         ctypes.POINTER(StepSlotC), _P, _P, _P, ctypes.c_int]),
+    "fp8lin_fp4_scale_bytes": (_SZ, [_I64, _I64, _I32]),
+    "fp8lin_fp4_quantise": (ctypes.c_int, [_P, _I64, _I64, _I64, _ST, _T4, _T4, _P, _P]),
+    "fp8lin_fp4_dequantise": (ctypes.c_int, [_T4, _P, _I64, _I32, _P]),
+    "fp8lin_fp4_gemm": (ctypes.c_int, [_T4, _T4, _P, _I64, _P, _SZ, _P]),
+    "fp8lin_fp4_linear": (ctypes.c_int, [_P, _I64, _ST, _T4, _T4, _P, _I64, _P, _SZ, _P]),
+    "fp8lin_fp4_forward": (ctypes.c_int, [_P, _P, _ST, _ST, _T4, _T4, _T4, _T4, _P, _P, _SZ, _P]),
+    "fp8lin_fp4_backward": (ctypes.c_int, [_P, _ST, _T4, _T4, _T4, _T4, _P, _P, _P, _SZ, _P]),
+    "fp8lin_grad_norm": (ctypes.c_int, [_GR, _I32, _P, _P, _SZ, _P]),
+    "fp8lin_grad_clip": (ctypes.c_int, [_GR, _I32, _P, _F, _F, _P]),
+    "fp8lin_grad_clip_norm": (ctypes.c_int, [_GR, _I32, _F, _F, _P, _P, _SZ, _P]),
     "fp8lin_launch_count": (ctypes.c_uint64, []),
     "fp8lin_profile_enable": (None, [ctypes.c_int]),
     "fp8lin_profile_collect": (ctypes.c_int, [_P, _P]),

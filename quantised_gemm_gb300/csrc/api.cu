@@ -408,6 +408,29 @@ cudaError_t current_device_info(DeviceInfo* info) {
   return cudaSuccess;
 }
 
+namespace {
+
+// Calls run(list, n) over the gradients that match, at most kClipMaxTensors at a time.
+template <typename Match, typename Run>
+fp8lin_status for_lists(const fp8lin_grad* grads, int32_t count, Match match, Run run) {
+  GradTensor list[kClipMaxTensors];
+  int n = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (grads[i].n == 0 || !match(grads[i])) continue;
+    if (n == kClipMaxTensors) {
+      fp8lin_status s = run(list, n);
+      if (s != FP8LIN_OK) return s;
+      n = 0;
+    }
+    list[n].g = grads[i].g;
+    list[n].out = grads[i].out;
+    list[n].n = grads[i].n;
+    ++n;
+  }
+  return n > 0 ? run(list, n) : FP8LIN_OK;
+}
+
+}  // namespace
 }  // namespace fp8lin
 
 using namespace fp8lin;
@@ -1072,6 +1095,397 @@ fp8lin_status fp8lin_step_host(const void* x_h, const void* w_h, const void* dy_
   if (wait && (e = cudaStreamWaitEvent(compute, d.ev[kOutDone], 0)) != cudaSuccess)
     return cuda_fail(e);
   return FP8LIN_OK;
+}
+
+// ---- 4-bit operands
+
+namespace {
+
+constexpr int64_t kFp4MaxDim = (int64_t(1) << 31) - 256;
+
+bool valid_fp4(int32_t fmt) { return fmt == FP8LIN_NVFP4 || fmt == FP8LIN_MXFP4; }
+
+// A 4-bit tensor that a call reads or writes.
+fp8lin_status check_fp4(const fp8lin_fp4_tensor* t) {
+  if (t == nullptr || t->rows < 0 || t->cols < 0) return FP8LIN_EINVAL;
+  if (!valid_fp4(t->fmt)) return FP8LIN_EUNSUPPORTED;
+  if (t->rows > kFp4MaxDim || t->cols > kFp4MaxDim) return FP8LIN_EUNSUPPORTED;
+  if ((t->fmt == FP8LIN_NVFP4) != (t->inv_scale != nullptr)) return FP8LIN_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(t->inv_scale) & 3u) != 0) return FP8LIN_EINVAL;
+  if (t->rows == 0 || t->cols == 0) return FP8LIN_OK;
+  if (t->codes == nullptr || t->scales == nullptr || !aligned16(t->codes) || !aligned16(t->scales))
+    return FP8LIN_EINVAL;
+  if (t->ld % 16 != 0 || t->ld < (t->cols + 31) / 32 * 16) return FP8LIN_EINVAL;
+  return FP8LIN_OK;
+}
+
+Fp4View fp4_view(const fp8lin_fp4_tensor* t) {
+  Fp4View v;
+  if (t != nullptr && t->rows > 0 && t->cols > 0) {
+    v.codes = t->codes;
+    v.scales = t->scales;
+    v.ld = t->ld;
+  }
+  return v;
+}
+
+// The source and the destinations of a quantisation.
+fp8lin_status check_quantise(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                             const fp8lin_scaling_state* st, const fp8lin_fp4_tensor* out,
+                             const fp8lin_fp4_tensor* out_t, const void* ws) {
+  if (rows < 0 || cols < 0 || (out == nullptr && out_t == nullptr)) return FP8LIN_EINVAL;
+  const int32_t fmt = (out != nullptr ? out : out_t)->fmt;
+  if (!valid_fp4(fmt)) return FP8LIN_EUNSUPPORTED;
+  fp8lin_status s;
+  if (fmt == FP8LIN_NVFP4) {
+    if ((s = check_state(st, false)) != FP8LIN_OK) return s;
+    if (st->fmt != FP8LIN_E4M3) return FP8LIN_EUNSUPPORTED;
+  } else if (st != nullptr) {
+    return FP8LIN_EINVAL;
+  }
+  if (out != nullptr) {
+    if ((s = check_fp4(out)) != FP8LIN_OK) return s;
+    if (out->rows != rows || out->cols != cols) return FP8LIN_EINVAL;
+  }
+  if (out_t != nullptr) {
+    if ((s = check_fp4(out_t)) != FP8LIN_OK) return s;
+    if (out_t->rows != cols || out_t->cols != rows || out_t->fmt != fmt) return FP8LIN_EINVAL;
+  }
+  for (const fp8lin_fp4_tensor* t : {out, out_t})
+    if (t != nullptr && st != nullptr && t->inv_scale != st->inv_scale) return FP8LIN_EINVAL;
+  if (!ws_ok(ws)) return FP8LIN_EINVAL;
+  if (rows > 0 && cols > 0) {
+    if (x == nullptr || (reinterpret_cast<uintptr_t>(x) & 1u) != 0 || ld < cols)
+      return FP8LIN_EINVAL;
+    if (((rows + 127) / 128) > kFp4MaxDim / ((cols + 127) / 128)) return FP8LIN_EUNSUPPORTED;
+  }
+  return FP8LIN_OK;
+}
+
+// amax of a tensor that need not have whole aligned vectors.
+fp8lin_status fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t ld, float* amax,
+                       int32_t algo, void* ws, const DeviceInfo& dev, cudaStream_t stream) {
+  if (rows == 0 || cols == 0 || check_bf16(x, rows, cols, ld) == FP8LIN_OK)
+    return do_amax(x, rows, cols, ld, amax,
+                   algo == FP8LIN_AMAX_REDUCTION ? algo : int32_t(FP8LIN_AMAX_ATOMIC), ws, dev,
+                   stream);
+  ProfScope ps(FP8LIN_PROF_AMAX, stream);
+  cudaError_t e = launch_fp4_amax(static_cast<const uint16_t*>(x), rows, cols, ld,
+                                  ws_u32(ws, kWsAtomicAccOffset), ws_u32(ws, kWsAtomicTicketOffset),
+                                  reinterpret_cast<uint32_t*>(amax), dev, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+fp8lin_status run_quantise(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                           fp8lin_scaling_state* st, const fp8lin_fp4_tensor* out,
+                           const fp8lin_fp4_tensor* out_t, void* ws, const DeviceInfo& dev,
+                           cudaStream_t stream) {
+  const bool empty = rows == 0 || cols == 0;
+  Fp4QuantArgs q;
+  q.x = static_cast<const uint16_t*>(x);
+  q.rows = rows;
+  q.cols = cols;
+  q.ld = ld;
+  q.fmt = (out != nullptr ? out : out_t)->fmt;
+  q.out = fp4_view(out);
+  q.out_t = fp4_view(out_t);
+  if (st != nullptr) {
+    q.eps = st->eps;
+    const bool delayed = st->kind == FP8LIN_DELAYED;
+    const bool init = delayed && st->needs_init;
+    if (init || (!delayed && st->amax_algo != FP8LIN_AMAX_PRECOMPUTED)) {
+      fp8lin_status s = fp4_amax(x, rows, cols, ld, st->amax, st->amax_algo, ws, dev, stream);
+      if (s != FP8LIN_OK) return s;
+    }
+    if (init || (!delayed && empty)) {
+      ProfScope ps(FP8LIN_PROF_SCALE, stream);
+      cudaError_t e = launch_scale(st->amax, st->scale, st->inv_scale, nullptr, nullptr, 1, false,
+                                   st->fmt, st->eps, stream);
+      if (e != cudaSuccess) return cuda_fail(e);
+      st->needs_init = 0;
+    }
+    if (delayed) {
+      if (empty) {
+        cudaError_t e = cudaMemsetAsync(st->amax, 0, sizeof(float), stream);
+        return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+      }
+      q.scale_in = st->scale;
+      q.amax_rec = reinterpret_cast<uint32_t*>(st->amax);
+      q.rec_acc = ws_u32(ws, kWsAtomicAccOffset);
+      q.rec_ticket = ws_u32(ws, kWsAtomicTicketOffset);
+    } else {
+      q.amax_in = st->amax;
+      q.scale_out = st->scale;
+      q.inv_out = st->inv_scale;
+    }
+  }
+  if (empty) return FP8LIN_OK;
+  ProfScope ps(FP8LIN_PROF_CAST, stream);
+  cudaError_t e = launch_fp4_quantise(q, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+fp8lin_status check_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, const void* d,
+                             int64_t ldd, const void* ws, size_t ws_bytes) {
+  fp8lin_status s;
+  if ((s = check_fp4(a)) != FP8LIN_OK) return s;
+  if ((s = check_fp4(b)) != FP8LIN_OK) return s;
+  if (a->cols != b->cols || a->fmt != b->fmt) return FP8LIN_EINVAL;
+  if (!ws_ok(ws) || ws_bytes < kWsFixedBytes) return FP8LIN_EINVAL;
+  if (a->rows > 0 && b->rows > 0 &&
+      (d == nullptr || (reinterpret_cast<uintptr_t>(d) & 1u) != 0 || ldd < b->rows))
+    return FP8LIN_EINVAL;
+  return FP8LIN_OK;
+}
+
+fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
+                           int64_t ldd, void* ws, size_t ws_bytes, const DeviceInfo& dev,
+                           cudaStream_t stream) {
+  (void)ws_bytes;
+  if (a->rows == 0 || b->rows == 0) return FP8LIN_OK;
+  if (a->cols == 0) {
+    cudaError_t e = cudaMemset2DAsync(d, static_cast<size_t>(ldd) * 2, 0,
+                                      static_cast<size_t>(b->rows) * 2,
+                                      static_cast<size_t>(a->rows), stream);
+    return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+  }
+  Fp4GemmArgs g;
+  g.a = fp4_view(a);
+  g.b = fp4_view(b);
+  g.fmt = a->fmt;
+  g.M = a->rows;
+  g.N = b->rows;
+  g.K = a->cols;
+  g.inv_a = a->inv_scale;
+  g.inv_b = b->inv_scale;
+  g.d = d;
+  g.ldd = ldd;
+  g.ws_error = ws_error(ws);
+  ProfScope ps(FP8LIN_PROF_GEMM, stream);
+  cudaError_t e = launch_fp4_gemm(g, dev, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+// Whether two 4-bit tensors are one tensor and its transpose, by their sizes.
+bool fp4_transposed(const fp8lin_fp4_tensor* t, const fp8lin_fp4_tensor* tt) {
+  return t->rows == tt->cols && t->cols == tt->rows && t->fmt == tt->fmt;
+}
+
+}  // namespace
+
+size_t fp8lin_fp4_scale_bytes(int64_t rows, int64_t cols, int32_t fmt) {
+  if (rows < 0 || cols < 0 || !valid_fp4(fmt)) return 0;
+  return static_cast<size_t>((rows + 127) / 128) *
+         static_cast<size_t>(fp4_scale_ktiles(cols, fmt)) * 512;
+}
+
+fp8lin_status fp8lin_fp4_quantise(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                                  fp8lin_scaling_state* st, const fp8lin_fp4_tensor* out,
+                                  const fp8lin_fp4_tensor* out_t, void* ws, cudaStream_t stream) {
+  fp8lin_status s = check_quantise(x, rows, cols, ld, st, out, out_t, ws);
+  if (s != FP8LIN_OK) return s;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  return run_quantise(x, rows, cols, ld, st, out, out_t, ws, dev, stream);
+}
+
+fp8lin_status fp8lin_fp4_dequantise(const fp8lin_fp4_tensor* t, void* out, int64_t ldo, int32_t f32,
+                                    cudaStream_t stream) {
+  fp8lin_status s = check_fp4(t);
+  if (s != FP8LIN_OK) return s;
+  if (t->rows == 0 || t->cols == 0) return FP8LIN_OK;
+  if (out == nullptr || (reinterpret_cast<uintptr_t>(out) & (f32 ? 3u : 1u)) != 0 || ldo < t->cols)
+    return FP8LIN_EINVAL;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  ProfScope ps(FP8LIN_PROF_CAST, stream);
+  cudaError_t e = launch_fp4_dequantise(fp4_view(t), t->fmt, t->inv_scale, t->rows, t->cols, out,
+                                        ldo, f32 != 0, dev, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+fp8lin_status fp8lin_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
+                              int64_t ldd, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  fp8lin_status s = check_fp4_gemm(a, b, d, ldd, ws, ws_bytes);
+  if (s != FP8LIN_OK) return s;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  return run_fp4_gemm(a, b, d, ldd, ws, ws_bytes, dev, stream);
+}
+
+fp8lin_status fp8lin_fp4_linear(const void* x, int64_t ldx, fp8lin_scaling_state* sx,
+                                const fp8lin_fp4_tensor* x4, const fp8lin_fp4_tensor* w4, void* y,
+                                int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (x4 == nullptr) return FP8LIN_EINVAL;
+  fp8lin_status s = check_quantise(x, x4->rows, x4->cols, ldx, sx, x4, nullptr, ws);
+  if (s != FP8LIN_OK) return s;
+  if ((s = check_fp4_gemm(x4, w4, y, ldy, ws, ws_bytes)) != FP8LIN_OK) return s;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  s = run_quantise(x, x4->rows, x4->cols, ldx, sx, x4, nullptr, ws, dev, stream);
+  if (s != FP8LIN_OK) return s;
+  return run_fp4_gemm(x4, w4, y, ldy, ws, ws_bytes, dev, stream);
+}
+
+fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_state* sx,
+                                 fp8lin_scaling_state* sw, const fp8lin_fp4_tensor* x4,
+                                 const fp8lin_fp4_tensor* x4t, const fp8lin_fp4_tensor* w4,
+                                 const fp8lin_fp4_tensor* w4t, void* y, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream) {
+  if (x4 == nullptr || w4 == nullptr) return FP8LIN_EINVAL;
+  const int64_t M = x4->rows, K = x4->cols, N = w4->rows;
+  fp8lin_status s = check_quantise(x, M, K, K, sx, x4, x4t, ws);
+  if (s != FP8LIN_OK) return s;
+  if (w != nullptr && (s = check_quantise(w, N, K, K, sw, w4, w4t, ws)) != FP8LIN_OK) return s;
+  if (w == nullptr && sw != nullptr && sw->kind == FP8LIN_DELAYED && sw->needs_init)
+    return FP8LIN_EINVAL;
+  if ((s = check_fp4_gemm(x4, w4, y, N, ws, ws_bytes)) != FP8LIN_OK) return s;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  if ((s = run_quantise(x, M, K, K, sx, x4, x4t, ws, dev, stream)) != FP8LIN_OK) return s;
+  if (w != nullptr &&
+      (s = run_quantise(w, N, K, K, sw, w4, w4t, ws, dev, stream)) != FP8LIN_OK)
+    return s;
+  return run_fp4_gemm(x4, w4, y, N, ws, ws_bytes, dev, stream);
+}
+
+fp8lin_status fp8lin_fp4_backward(const void* dy, fp8lin_scaling_state* sdy,
+                                  const fp8lin_fp4_tensor* dy4, const fp8lin_fp4_tensor* dy4t,
+                                  const fp8lin_fp4_tensor* w4t, const fp8lin_fp4_tensor* x4t,
+                                  void* dx, void* dw, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  if (dx == nullptr && dw == nullptr) return FP8LIN_OK;
+  if ((dx != nullptr && dy4 == nullptr) || (dw != nullptr && dy4t == nullptr)) return FP8LIN_EINVAL;
+  if (dx == nullptr) dy4 = nullptr;    // a copy that no product reads is not made
+  if (dw == nullptr) dy4t = nullptr;
+  const int64_t M = dy4 != nullptr ? dy4->rows : dy4t->cols;
+  const int64_t N = dy4 != nullptr ? dy4->cols : dy4t->rows;
+  if (dy4 != nullptr && dy4t != nullptr && !fp4_transposed(dy4, dy4t)) return FP8LIN_EINVAL;
+  fp8lin_status s = check_quantise(dy, M, N, N, sdy, dy4, dy4t, ws);
+  if (s != FP8LIN_OK) return s;
+  if (dx != nullptr &&
+      (w4t == nullptr || (s = check_fp4_gemm(dy4, w4t, dx, w4t->rows, ws, ws_bytes)) != FP8LIN_OK))
+    return w4t == nullptr ? FP8LIN_EINVAL : s;
+  if (dw != nullptr &&
+      (x4t == nullptr || (s = check_fp4_gemm(dy4t, x4t, dw, x4t->rows, ws, ws_bytes)) != FP8LIN_OK))
+    return x4t == nullptr ? FP8LIN_EINVAL : s;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  if ((s = run_quantise(dy, M, N, N, sdy, dy4, dy4t, ws, dev, stream)) != FP8LIN_OK) return s;
+  if (dx != nullptr &&
+      (s = run_fp4_gemm(dy4, w4t, dx, w4t->rows, ws, ws_bytes, dev, stream)) != FP8LIN_OK)
+    return s;
+  if (dw != nullptr) return run_fp4_gemm(dy4t, x4t, dw, x4t->rows, ws, ws_bytes, dev, stream);
+  return FP8LIN_OK;
+}
+
+// ---- gradient norm and clipping
+
+namespace {
+
+fp8lin_status check_grads(const fp8lin_grad* grads, int32_t count, bool outs) {
+  if (count < 0 || (count > 0 && grads == nullptr)) return FP8LIN_EINVAL;
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8lin_grad& t = grads[i];
+    if (t.n < 0) return FP8LIN_EINVAL;
+    if (t.n == 0) continue;
+    if (t.g == nullptr || (reinterpret_cast<uintptr_t>(t.g) & (t.g_f32 ? 3u : 1u)) != 0)
+      return FP8LIN_EINVAL;
+    if (!outs) continue;
+    if (t.out == nullptr || (reinterpret_cast<uintptr_t>(t.out) & (t.out_f32 ? 3u : 1u)) != 0)
+      return FP8LIN_EINVAL;
+    if (t.out == t.g && (t.out_f32 != 0) != (t.g_f32 != 0)) return FP8LIN_EINVAL;
+  }
+  return FP8LIN_OK;
+}
+
+fp8lin_status run_grad_norm(const fp8lin_grad* grads, int32_t count, float* norm, void* ws,
+                            const DeviceInfo& dev, cudaStream_t stream) {
+  double* partials = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsPartialOffset);
+  double* total = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsNormTotalOffset);
+  uint32_t* ticket = ws_u32(ws, kWsAtomicTicketOffset);
+  int64_t of[2] = {0, 0};
+  for (int32_t i = 0; i < count; ++i)
+    if (grads[i].n > 0) ++of[grads[i].g_f32 != 0];
+  int64_t launches = 0;
+  for (int64_t n : of) launches += (n + kClipMaxTensors - 1) / kClipMaxTensors;
+  if (launches == 0) {
+    cudaError_t e = cudaMemsetAsync(norm, 0, sizeof(float), stream);
+    return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+  }
+  int64_t k = 0;
+  for (int f32 = 0; f32 < 2; ++f32) {
+    fp8lin_status s = for_lists(
+        grads, count, [&](const fp8lin_grad& t) { return (t.g_f32 != 0) == (f32 != 0); },
+        [&](const GradTensor* list, int n) {
+          ProfScope ps(FP8LIN_PROF_AMAX, stream);
+          cudaError_t e = launch_grad_norm(list, n, f32 == 0, k == 0, k == launches - 1, partials,
+                                           total, ticket, norm, dev, stream);
+          ++k;
+          return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+        });
+    if (s != FP8LIN_OK) return s;
+  }
+  return FP8LIN_OK;
+}
+
+fp8lin_status run_grad_clip(const fp8lin_grad* grads, int32_t count, const float* norm,
+                            float max_norm, float eps, const DeviceInfo& dev,
+                            cudaStream_t stream) {
+  for (int kind = 0; kind < 4; ++kind) {
+    const bool f32 = (kind & 1) != 0, out_f32 = (kind & 2) != 0;
+    fp8lin_status s = for_lists(
+        grads, count,
+        [&](const fp8lin_grad& t) { return (t.g_f32 != 0) == f32 && (t.out_f32 != 0) == out_f32; },
+        [&](const GradTensor* list, int n) {
+          ProfScope ps(FP8LIN_PROF_SCALE, stream);
+          cudaError_t e =
+              launch_grad_scale(list, n, !f32, !out_f32, norm, max_norm, eps, dev, stream);
+          return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+        });
+    if (s != FP8LIN_OK) return s;
+  }
+  return FP8LIN_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+fp8lin_status fp8lin_grad_norm(const fp8lin_grad* grads, int32_t count, float* norm, void* ws,
+                               size_t ws_bytes, cudaStream_t stream) {
+  fp8lin_status s = check_grads(grads, count, false);
+  if (s != FP8LIN_OK) return s;
+  if (norm == nullptr || !aligned4(norm) || !ws_ok(ws) || ws_bytes < kWsFixedBytes)
+    return FP8LIN_EINVAL;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  return run_grad_norm(grads, count, norm, ws, dev, stream);
+}
+
+fp8lin_status fp8lin_grad_clip(const fp8lin_grad* grads, int32_t count, const float* norm,
+                               float max_norm, float eps, cudaStream_t stream) {
+  fp8lin_status s = check_grads(grads, count, true);
+  if (s != FP8LIN_OK) return s;
+  if (norm == nullptr || !aligned4(norm) || !(max_norm >= 0.0f) || !(eps >= 0.0f))
+    return FP8LIN_EINVAL;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  return run_grad_clip(grads, count, norm, max_norm, eps, dev, stream);
+}
+
+fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, float max_norm,
+                                    float eps, float* norm, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream) {
+  fp8lin_status s = check_grads(grads, count, true);
+  if (s != FP8LIN_OK) return s;
+  if (norm == nullptr || !aligned4(norm) || !ws_ok(ws) || ws_bytes < kWsFixedBytes ||
+      !(max_norm >= 0.0f) || !(eps >= 0.0f))
+    return FP8LIN_EINVAL;
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  if ((s = run_grad_norm(grads, count, norm, ws, dev, stream)) != FP8LIN_OK) return s;
+  return run_grad_clip(grads, count, norm, max_norm, eps, dev, stream);
 }
 
 uint64_t fp8lin_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

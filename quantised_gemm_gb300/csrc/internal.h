@@ -20,6 +20,7 @@ constexpr size_t kWsGemmAmaxAccOffset = 200;     // uint32: GEMM output amax acc
 constexpr size_t kWsGemmAmaxTicketOffset = 204;  // uint32: GEMM epilogue warps arrived
 constexpr size_t kWsSmallBAmaxOffset = 208;      // uint32: few-token product, token-side amax
 constexpr size_t kWsAmax2Offset = 212;           // uint32: paired single pass, x's amax bits
+constexpr size_t kWsNormTotalOffset = 216;       // double: gradient norm, sum of earlier launches
 constexpr size_t kWsScratchBegin = 64;    // [64, 256): self-cleaning counters
 constexpr size_t kWsPartialOffset = 256;  // uint32[kMaxPartials]: REDUCTION partial maxima
 constexpr int kMaxPartials = 4096;
@@ -303,5 +304,80 @@ void describe_group_plan(int64_t Ma, int64_t Na, int64_t Ka, int64_t Mb, int64_t
 
 // Workspace bytes the tail K split can use at most on a device with num_sms SMs.
 size_t gemm_split_workspace_bytes(int num_sms);
+
+// ---- 4-bit operands (fp4_quant.cu, fp4_gemm.cu)
+
+// Codes [rows, ld bytes] (two a byte, low half first) and their block scales
+// in 512-byte tiles (include/fp8lin.h, fp8lin_fp4_tensor).
+struct Fp4View {
+  uint8_t* codes = nullptr;
+  uint8_t* scales = nullptr;
+  int64_t ld = 0;
+};
+constexpr int fp4_block(int fmt) { return fmt == 0 ? 16 : 32; }
+constexpr int64_t fp4_scale_ktiles(int64_t cols, int fmt) {
+  return ((cols + fp4_block(fmt) - 1) / fp4_block(fmt) + 3) / 4;
+}
+
+// Quantise a bf16 tensor (NVFP4: fmt 0, MXFP4: fmt 1) into out, out_t (its
+// transpose) or both.  NVFP4 takes its tensorwise scale from amax_in (and
+// writes scale_out, inv_out) or from scale_in; amax_rec records the amax
+// through the two self-cleaning words.
+struct Fp4QuantArgs {
+  const uint16_t* x;
+  int64_t rows, cols, ld;
+  int fmt;
+  const float* amax_in = nullptr;
+  const float* scale_in = nullptr;
+  float eps = 0.0f;
+  float* scale_out = nullptr;
+  float* inv_out = nullptr;
+  uint32_t* amax_rec = nullptr;
+  uint32_t* rec_acc = nullptr;
+  uint32_t* rec_ticket = nullptr;
+  Fp4View out, out_t;
+};
+cudaError_t launch_fp4_quantise(const Fp4QuantArgs& a, cudaStream_t stream);
+// amax of a tensor of any alignment, width and row stride.
+cudaError_t launch_fp4_amax(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
+                            uint32_t* acc, uint32_t* ticket, uint32_t* out, const DeviceInfo& dev,
+                            cudaStream_t stream);
+cudaError_t launch_fp4_dequantise(const Fp4View& t, int fmt, const float* inv, int64_t rows,
+                                  int64_t cols, void* out, int64_t ldo, bool f32,
+                                  const DeviceInfo& dev, cudaStream_t stream);
+
+// D [M, N] = A [M, K] . B [N, K]^T, both in the same 4-bit format, fp32
+// accumulation; bf16 D of any row stride and 2-byte alignment.
+struct Fp4GemmArgs {
+  Fp4View a, b;
+  int fmt;
+  int64_t M, N, K;
+  const float* inv_a;   // NVFP4
+  const float* inv_b;
+  void* d;
+  int64_t ldd;
+  int* ws_error;
+};
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStream_t stream);
+
+// ---- gradient norm and clipping (grad_clip.cu)
+
+constexpr int kClipMaxTensors = 384;   // of one launch
+constexpr int kClipMaxPartials = kMaxPartials / 2;
+struct GradTensor {
+  const void* g;
+  void* out;
+  int64_t n;
+};
+// The 2-norm of the tensors of one or several launches: each launch sums its
+// CTAs' partial sums in a fixed order into *total (first: from 0), and the
+// last writes sqrt(*total) to norm.
+cudaError_t launch_grad_norm(const GradTensor* t, int n, bool bf16, bool first, bool last,
+                             double* partials, double* total, uint32_t* ticket, float* norm,
+                             const DeviceInfo& dev, cudaStream_t stream);
+// out = g * min(1, max_norm / (norm + eps)).
+cudaError_t launch_grad_scale(const GradTensor* t, int n, bool bf16, bool out_bf16,
+                              const float* norm, float max_norm, float eps, const DeviceInfo& dev,
+                              cudaStream_t stream);
 
 }  // namespace fp8lin

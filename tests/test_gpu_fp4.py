@@ -1,0 +1,396 @@
+"""4-bit quantisation, products and the 4-bit Linear on the GPU against the
+64-bit oracle: every code and scale byte equal, values within their type's
+rounding, products within the library's GEMM bound."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import assert_within_bound, bf16_to_f64, to_dev_bf16
+from oracle import fp4 as o4
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [o4.NVFP4, o4.MXFP4]
+SIZES = [(1, 1), (1, 16), (2, 33), (16, 4096), (31, 15), (33, 47), (127, 64), (128, 128), (129, 65),
+         (130, 200), (255, 513), (640, 1600), (1009, 1531)]
+
+
+def make(rows, cols, seed, std=1.0):
+    """bf16 bits and their 64-bit values: normal, with large values, blocks of
+    zeros and values far below their block's maximum."""
+    g = np.random.default_rng(seed)
+    x = (g.normal(size=(rows, cols)) * std).astype(np.float32)
+    x[g.random((rows, cols)) < 1e-3] *= 40
+    x[g.random((rows, cols)) < 1e-2] *= 1e-6
+    x[:, : cols // 5] *= (g.random((rows, 1)) < 0.9)
+    bits = (x.view(np.uint32) >> 16).astype(np.uint16)
+    return bits, (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def dirty(q, rows, cols, fmt, state=None):
+    t = q.Fp4Tensor(rows, cols, fmt, state=state)
+    t.codes.fill_(0xA5)
+    t.scales.fill_(0x5A)
+    return t
+
+
+def check_bytes(t, x, scale, what):
+    codes, sc = o4.quantise(x, t.fmt, scale)
+    assert np.array_equal(t.codes.cpu().numpy(), o4.pack(codes, x.shape[1])), what + ": codes"
+    assert np.array_equal(t.scales.cpu().numpy(), o4.tile_scales(sc)), what + ": scales"
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_quantise_bytes(rows, cols, fmt):
+    import quantised_gemm_gb300 as q
+    bits, x = make(rows, cols, rows * 7 + cols)
+    xd = to_dev_bf16(bits)
+    ws = q.Workspace()
+    a = dirty(q, rows, cols, fmt)
+    at = dirty(q, cols, rows, fmt, a.state)
+    s, inv = o4.tensor_scale(np.abs(x).max())
+    q.fp4_quantise(xd, a, at, ws)
+    check_bytes(a, x, s, "both")
+    check_bytes(at, np.ascontiguousarray(x.T), s, "both, transposed")
+    if fmt == o4.NVFP4:
+        assert float(a.state.scale) == s and float(a.state.inv_scale) == inv
+        assert float(a.state.amax) == np.abs(x).max()
+    b = dirty(q, rows, cols, fmt)
+    q.fp4_quantise(xd, b, None, ws)
+    check_bytes(b, x, s, "out alone")
+    bt = dirty(q, cols, rows, fmt)
+    q.fp4_quantise(xd, None, bt, ws)
+    check_bytes(bt, np.ascontiguousarray(x.T), s, "out_t alone")
+    # The values: bf16 is one more rounding, fp32 within the two roundings of its products.
+    codes, sc = o4.quantise(x, fmt, s)
+    v = o4.values(codes, sc, fmt, cols, inv)
+    got = q.fp4_dequantise(a, torch.empty((rows, cols), dtype=torch.float32, device="cuda"))
+    assert np.all(np.abs(got.cpu().numpy().astype(np.float64) - v) <= 2.0 ** -23 * np.abs(v))
+    got = q.fp4_dequantise(a, torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda"))
+    assert np.all(np.abs(bf16_to_f64(got) - v) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(v))
+    q.check(ws)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+@pytest.mark.parametrize("offset,width", [(0, 4), (1, 0), (3, 5), (8, 16)])
+def test_strided_rows(fmt, offset, width):
+    import quantised_gemm_gb300 as q
+    rows, cols = 70, 177
+    bits, x = make(rows, cols + offset + width, 11)
+    wide = to_dev_bf16(bits)
+    x = np.ascontiguousarray(x[:, offset:offset + cols])
+    a = dirty(q, rows, cols, fmt)
+    at = dirty(q, cols, rows, fmt, a.state)
+    ws = q.Workspace()
+    q.fp4_quantise(wide[:, offset:offset + cols], a, at, ws)
+    s, inv = o4.tensor_scale(np.abs(x).max())
+    check_bytes(a, x, s, "strided")
+    check_bytes(at, np.ascontiguousarray(x.T), s, "strided, transposed")
+    codes, sc = o4.quantise(x, fmt, s)
+    v = o4.values(codes, sc, fmt, cols, inv)
+    for dtype in (torch.float32, torch.bfloat16):
+        room = torch.full((rows, cols + offset + width), 7.0, dtype=dtype, device="cuda")
+        q.fp4_dequantise(a, room[:, offset:offset + cols])
+        got = room.float().cpu().numpy()
+        assert np.all(np.abs(got[:, offset:offset + cols] - v) <= 2.0 ** -7 * np.abs(v))
+        assert np.all(got[:, :offset] == 7) and np.all(got[:, offset + cols:] == 7)
+
+
+@pytest.mark.parametrize("algo", ["atomic", "reduction", "precomputed", "single_pass", "auto"])
+def test_dynamic_algorithms(algo):
+    import quantised_gemm_gb300 as q
+    algos = dict(atomic=q.AMAX_ATOMIC, reduction=q.AMAX_REDUCTION, precomputed=q.AMAX_PRECOMPUTED,
+                 single_pass=q.AMAX_SINGLE_PASS, auto=q.AMAX_AUTO)
+    for rows, cols in ((48, 160), (48, 161), (2048, 512)):
+        bits, x = make(rows, cols, 21)
+        a = dirty(q, rows, cols, q.NVFP4)
+        a.state.amax_algo = algos[algo]
+        amax = np.abs(x).max()
+        if algo == "precomputed":
+            amax *= 2
+            a.state.amax.fill_(float(amax))
+        q.fp4_quantise(to_dev_bf16(bits), a, None, q.Workspace())
+        check_bytes(a, x, o4.tensor_scale(amax)[0], algo)
+
+
+def test_delayed_scaling():
+    import quantised_gemm_gb300 as q
+    rows, cols = 65, 130
+    st = q.ScalingState(q.E4M3, q.DELAYED, history_len=3)
+    a = dirty(q, rows, cols, q.NVFP4, st)
+    at = dirty(q, cols, rows, q.NVFP4, st)
+    ws = q.Workspace()
+    history, scale = [0.0] * 3, None
+    for step in range(5):
+        bits, x = make(rows, cols, 40 + step, std=1.0 + 3 * step)
+        amax = np.abs(x).max()
+        if scale is None:
+            scale = o4.tensor_scale(amax)[0]  # the first cast takes its own amax
+        q.fp4_quantise(to_dev_bf16(bits), a, at, ws)
+        check_bytes(a, x, scale, "step %d" % step)
+        check_bytes(at, np.ascontiguousarray(x.T), scale, "step %d, transposed" % step)
+        assert float(st.amax) == amax and not st.needs_init
+        q.scale(st)
+        history[step % 3] = amax
+        scale = o4.tensor_scale(max(history))[0]
+        assert float(st.scale) == scale
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_nan_and_infinity(fmt, bad):
+    import quantised_gemm_gb300 as q
+    x = torch.ones((40, 100), dtype=torch.bfloat16, device="cuda")
+    x[5, 70] = bad
+    a = q.Fp4Tensor(40, 100, fmt)
+    at = q.Fp4Tensor(100, 40, fmt, state=a.state)
+    q.fp4_quantise(x, a, at, q.Workspace())
+    v = q.fp4_dequantise(a, torch.empty((40, 100), device="cuda")).cpu()
+    vt = q.fp4_dequantise(at, torch.empty((100, 40), device="cuda")).cpu()
+    if fmt == o4.NVFP4:  # the tensorwise scale is gone
+        assert torch.isnan(v).all() and torch.isnan(vt).all()
+    else:  # only the blocks that hold it
+        want = torch.ones(40, 100)
+        want[5, 64:96] = float("nan")
+        assert torch.equal(torch.isnan(v), torch.isnan(want)) and (v[~torch.isnan(v)] == 1).all()
+        want = torch.ones(100, 40)
+        want[70, 0:32] = float("nan")
+        assert torch.equal(torch.isnan(vt), torch.isnan(want)) and (vt[~torch.isnan(vt)] == 1).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+def test_zeros_subnormals_and_the_largest(fmt):
+    import quantised_gemm_gb300 as q
+    rows = np.zeros((6, 64), np.uint16)
+    rows[1] = 0x8000                       # -0
+    rows[2] = 0x0001                       # the smallest subnormal
+    rows[3, ::2], rows[3, 1::2] = 0x7F7F, 0xFF7F   # the largest magnitudes
+    rows[4] = 0x0080                       # the smallest normal
+    rows[5, 0] = 0x3F80
+    for sel in ([0, 1], [2, 4], [3], [0, 2, 4, 5], [0, 1, 2, 3, 4, 5]):
+        bits = np.ascontiguousarray(rows[sel])
+        x = (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+        a = dirty(q, len(sel), 64, fmt)
+        q.fp4_quantise(to_dev_bf16(bits), a, None, q.Workspace())
+        check_bytes(a, x, o4.tensor_scale(np.abs(x).max())[0], str(sel))
+
+
+def test_empty_tensors():
+    import quantised_gemm_gb300 as q
+    ws = q.Workspace()
+    for fmt in FORMATS:
+        for rows, cols in ((0, 64), (5, 0), (0, 0)):
+            a = q.Fp4Tensor(rows, cols, fmt)
+            q.fp4_quantise(torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda"), a, None, ws)
+            if a.state is not None:
+                assert float(a.state.amax) == 0 and float(a.state.scale) == o4.tensor_scale(0.0)[0]
+            q.fp4_dequantise(a, torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda"))
+        a, b = q.Fp4Tensor(5, 0, fmt), q.Fp4Tensor(7, 0, fmt)
+        for t in (a, b):
+            if t.state is not None:
+                t.state.inv_scale.fill_(1.0)
+        out = torch.full((5, 9), 3.0, dtype=torch.bfloat16, device="cuda")
+        q.fp4_gemm(a, b, out[:, :7], ws)   # an empty sum is zero
+        assert (out[:, :7] == 0).all() and (out[:, 7:] == 3).all()
+        e = q.Fp4Tensor(0, 64, fmt)
+        q.fp4_gemm(e, q.Fp4Tensor(7, 64, fmt), torch.empty((0, 7), dtype=torch.bfloat16,
+                                                           device="cuda"), ws)
+
+
+# ---------------------------------------------------------------- products
+
+
+def quantised(q, rows, cols, fmt, seed, std=1.0):
+    """A 4-bit tensor on the device and its exact values without and with the tensorwise factor."""
+    bits, x = make(rows, cols, seed, std)
+    t = q.Fp4Tensor(rows, cols, fmt)
+    q.fp4_quantise(to_dev_bf16(bits), t, None, q.Workspace())
+    s, inv = o4.tensor_scale(np.abs(x).max())
+    codes, sc = o4.quantise(x, fmt, s)
+    return t, o4.values(codes, sc, fmt, cols, inv)
+
+
+PRODUCTS = [(1, 1, 1), (1, 16, 64), (1, 130, 4096), (2, 257, 100), (16, 128, 256), (17, 96, 31),
+            (32, 4096, 1600), (33, 200, 1000), (64, 129, 513), (65, 384, 640), (100, 100, 100),
+            (128, 128, 128), (129, 127, 257), (256, 256, 256), (300, 1000, 1531), (777, 333, 96),
+            (1024, 512, 4096), (515, 2049, 2048)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+def test_product(M, N, K, fmt):
+    import quantised_gemm_gb300 as q
+    a, va = quantised(q, M, K, fmt, 100 + M)
+    b, vb = quantised(q, N, K, fmt, 200 + N, std=0.02)
+    ws = q.Workspace()
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q.fp4_gemm(a, b, out, ws)
+    q.check(ws)
+    assert_within_bound(bf16_to_f64(out), va @ vb.T, np.abs(va) @ np.abs(vb).T, "fp4 product")
+    # Rows with a stride and no alignment: the same bits, and nothing beside them.
+    room = torch.full((M, N + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    q.fp4_gemm(a, b, room[:, 1:N + 1], ws)
+    assert torch.equal(room[:, 1:N + 1], out)
+    assert (room[:, 0] == 5).all() and (room[:, N + 1:] == 5).all()
+    again = torch.empty_like(out)
+    q.fp4_gemm(a, b, again, ws)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+def test_product_of_small_whole_numbers_is_exact(fmt):
+    # Values 0, +-1, +-2 in blocks whose maximum is 2: a product of whole numbers below 2^8.
+    import quantised_gemm_gb300 as q
+    g = np.random.default_rng(8)
+    M, N, K = 150, 140, 48
+    xs = []
+    for rows in (M, N):
+        x = g.integers(-2, 3, (rows, K)).astype(np.float32)
+        x[:, ::16] = 2
+        xs.append(x)
+    ts = []
+    for x in xs:
+        t = q.Fp4Tensor(x.shape[0], K, fmt)
+        if t.state is not None:
+            t.state.amax_algo = q.AMAX_PRECOMPUTED
+            t.state.amax.fill_(2 * 448.0 / 384.0)  # S = 192: c = 384 stands for 2, 6 is 2's code
+        q.fp4_quantise(torch.from_numpy(x).to(torch.bfloat16).cuda(), t, None, q.Workspace())
+        ts.append(t)
+    vals = [q.fp4_dequantise(t, torch.empty(t.rows, K, device="cuda")).cpu().numpy().astype(np.float64)
+            for t in ts]
+    out = q.fp4_gemm(ts[0], ts[1], torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), q.Workspace())
+    ref = vals[0] @ vals[1].T
+    assert_within_bound(bf16_to_f64(out), ref, np.abs(vals[0]) @ np.abs(vals[1]).T, "whole numbers")
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+def test_nan_reaches_its_row_only(fmt):
+    import quantised_gemm_gb300 as q
+    a, va = quantised(q, 200, 320, fmt, 5)
+    b, vb = quantised(q, 150, 320, fmt, 6)
+    sc = a.scales.view(-1, 512)
+    sc[0, (40 % 32) * 16 + (40 // 32) * 4 + 1] = 0x7F if fmt == o4.NVFP4 else 0xFF  # row 40, block 1
+    out = q.fp4_gemm(a, b, torch.empty((200, 150), dtype=torch.bfloat16, device="cuda"), q.Workspace())
+    nan = torch.isnan(out).cpu()
+    assert nan[40].all() and nan.sum() == 150
+
+
+@pytest.mark.parametrize("M", [1, 16, 200])
+def test_product_on_another_stream(M):
+    import quantised_gemm_gb300 as q
+    bits, x = make(M, 512, 9)
+    w, vw = quantised(q, 256, 512, o4.NVFP4, 10)
+    x4, ws = q.Fp4Tensor(M, 512, o4.NVFP4), q.Workspace()
+    xd = to_dev_bf16(bits)
+    y0 = torch.empty((M, 256), dtype=torch.bfloat16, device="cuda")
+    q.fp4_linear(xd, x4, w, y0, ws)
+    torch.cuda.synchronize()
+    y1 = torch.empty_like(y0)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        src = xd.clone()
+        q.fp4_linear(src, x4, w, y1, ws)
+    side.synchronize()
+    assert torch.equal(y0, y1)
+
+
+def test_linear_in_a_graph():
+    import quantised_gemm_gb300 as q
+    w, vw = quantised(q, 320, 640, o4.NVFP4, 12)
+    x4, ws = q.Fp4Tensor(4, 640, o4.NVFP4), q.Workspace()
+    x = torch.zeros((4, 640), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((4, 320), dtype=torch.bfloat16, device="cuda")
+    q.fp4_linear(x, x4, w, y, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.fp4_linear(x, x4, w, y, ws)
+    for seed in (1, 2):
+        bits, xv = make(4, 640, seed)
+        x.copy_(to_dev_bf16(bits))
+        g.replay()
+        want = torch.empty_like(y)
+        q.fp4_linear(x, q.Fp4Tensor(4, 640, o4.NVFP4), w, want, q.Workspace())
+        assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------- the Linear
+
+
+@pytest.mark.parametrize("fmt,scaling", [(0, "dynamic"), (0, "delayed"), (1, "dynamic")])
+@pytest.mark.parametrize("M,K,N", [(1, 64, 48), (48, 160, 96), (130, 257, 131), (256, 512, 384)])
+def test_linear_forward_backward(M, K, N, fmt, scaling):
+    import quantised_gemm_gb300 as q
+    lin = q.Fp4Linear(M, K, N, fmt=fmt, scaling=scaling)
+    xb, x = make(M, K, 1)
+    wb, w = make(N, K, 2, std=0.05)
+    db, dy = make(M, N, 3, std=1e-3)
+    y = lin.forward(to_dev_bf16(xb), to_dev_bf16(wb))
+    dx, dw = lin.backward(to_dev_bf16(db))
+    q.check(lin.ws)
+
+    def val(v):
+        s, inv = o4.tensor_scale(np.abs(v).max())
+
+        def one(m):
+            c, sc = o4.quantise(np.ascontiguousarray(m), fmt, s)
+            return o4.values(c, sc, fmt, m.shape[1], inv)
+        return one(v), one(v.T)
+
+    (x4, x4t), (w4, w4t), (d4, d4t) = val(x), val(w), val(dy)
+    for got, a, b, what in ((y, x4, w4, "y"), (dx, d4, w4t, "dX"), (dw, d4t, x4t, "dW")):
+        assert_within_bound(bf16_to_f64(got), a @ b.T, np.abs(a) @ np.abs(b).T, what)
+    lin.sync_scales()
+    only = lin.backward(to_dev_bf16(db), need_dw=False)
+    assert only[1] is None and (scaling == "delayed" or torch.equal(only[0], dx))
+
+
+def test_cached_weight():
+    import quantised_gemm_gb300 as q
+    lin = q.Fp4Linear(32, 128, 64, cache_weight=True)
+    xb, _ = make(32, 128, 1)
+    wb, _ = make(64, 128, 2)
+    x, w = to_dev_bf16(xb), to_dev_bf16(wb)
+    y = lin.forward(x, w).clone()
+    n0 = q.launch_count()
+    assert torch.equal(lin.forward(x, w), y)
+    cached = q.launch_count() - n0
+    w.mul_(2.0)
+    n0 = q.launch_count()
+    y2 = lin.forward(x, w)
+    assert q.launch_count() - n0 > cached
+    assert torch.equal(y2, y * 2)
+
+
+def test_python_refusals():
+    import quantised_gemm_gb300 as q
+    ws = q.Workspace()
+    x = torch.zeros((16, 32), dtype=torch.bfloat16, device="cuda")
+    a = q.Fp4Tensor(16, 32)
+    with pytest.raises(TypeError):
+        q.fp4_quantise(x.float(), a, None, ws)
+    with pytest.raises(ValueError):
+        q.fp4_quantise(x.cpu(), a, None, ws)
+    with pytest.raises(ValueError):
+        q.fp4_quantise(x.t(), q.Fp4Tensor(32, 16), None, ws)       # columns not contiguous
+    with pytest.raises(ValueError):
+        q.fp4_quantise(x, None, None, ws)
+    with pytest.raises(ValueError):
+        q.fp4_quantise(x, a, q.Fp4Tensor(32, 16), ws)              # two states
+    with pytest.raises(q.Fp8linError):
+        q.fp4_quantise(x, q.Fp4Tensor(16, 48), None, ws)
+    with pytest.raises(ValueError):
+        q.fp4_gemm(a, q.Fp4Tensor(8, 32), torch.empty((16, 9), dtype=torch.bfloat16, device="cuda"), ws)
+    with pytest.raises(q.Fp8linError):
+        q.fp4_gemm(a, q.Fp4Tensor(8, 32, q.MXFP4),
+                   torch.empty((16, 8), dtype=torch.bfloat16, device="cuda"), ws)
+    with pytest.raises(ValueError):
+        q.Fp4Tensor(16, 32, q.MXFP4, state=a.state)
+    with pytest.raises(ValueError):
+        q.Fp4Tensor(16, 32, codes=torch.zeros((16, 8), dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        q.Fp4Linear(16, 16, 16, fmt=q.MXFP4, scaling="delayed")
+    with pytest.raises(ValueError):
+        q.Fp4Linear(16, 32, 16).forward(x[:8], torch.zeros((16, 32), dtype=torch.bfloat16,
+                                                           device="cuda"))
