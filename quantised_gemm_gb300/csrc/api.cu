@@ -1240,7 +1240,7 @@ fp8lin_status check_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor
 
 fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
                            int64_t ldd, void* ws, size_t ws_bytes, const DeviceInfo& dev,
-                           cudaStream_t stream) {
+                           cudaStream_t stream, bool b_early = false) {
   (void)ws_bytes;
   if (a->rows == 0 || b->rows == 0) return FP8LIN_OK;
   if (a->cols == 0) {
@@ -1261,6 +1261,7 @@ fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* 
   g.d = d;
   g.ldd = ldd;
   g.ws_error = ws_error(ws);
+  g.b_early = b_early;
   ProfScope ps(FP8LIN_PROF_GEMM, stream);
   cudaError_t e = launch_fp4_gemm(g, dev, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
@@ -1324,7 +1325,8 @@ fp8lin_status fp8lin_fp4_linear(const void* x, int64_t ldx, fp8lin_scaling_state
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
   s = run_quantise(x, x4->rows, x4->cols, ldx, sx, x4, nullptr, ws, dev, stream);
   if (s != FP8LIN_OK) return s;
-  return run_fp4_gemm(x4, w4, y, ldy, ws, ws_bytes, dev, stream);
+  // The launch before the product is x's quantisation, which does not write w4.
+  return run_fp4_gemm(x4, w4, y, ldy, ws, ws_bytes, dev, stream, x4->rows > 0 && x4->cols > 0);
 }
 
 fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_state* sx,

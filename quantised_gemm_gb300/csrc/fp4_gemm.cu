@@ -28,6 +28,7 @@ constexpr int kBKBytes = 128;       // bytes of K per stage and row
 constexpr int kBK = 256;            // values of K per stage
 constexpr int kMmaK = 64;           // K of one MMA
 constexpr int kScTile = 512;        // bytes of a scale tile: 128 rows x 4 blocks
+constexpr int kScElems = kScTile / 8;  // its 8-byte elements, as the tensor maps see it
 constexpr int kThreads = 192;       // producer, MMA, 4 epilogue warps
 
 // Scale tiles of a stage along K: 64 values of K each (NVFP4), or 128 (MXFP4).
@@ -38,8 +39,6 @@ constexpr int stage_ktiles() {
 
 struct Fp4GemmParams {
   int64_t M, N, K;            // A has M rows, B has N rows
-  const uint8_t* sca;         // scale tiles
-  const uint8_t* scb;
   const float* inv_a;
   const float* inv_b;
   uint16_t* d;
@@ -85,9 +84,37 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// One scale tile, shared memory -> four columns of tensor memory.
+// The same over a CTA pair.
+template <int kFmt>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if constexpr (kFmt == 0)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// One scale tile, shared memory -> four columns of tensor memory (the pair
+// form: in both CTAs, each from its own shared memory).
 __device__ __forceinline__ void copy_scale_tile(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+__device__ __forceinline__ void copy_scale_tile_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                : "memory");
 }
 
@@ -98,14 +125,17 @@ __device__ __forceinline__ uint64_t smem_desc_scale(uint32_t saddr) {
          (static_cast<uint64_t>(8) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
-// Contiguous bulk copy global -> shared, counted in bytes on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
-      : "memory");
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// A bounded wait of the whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag));
 }
 
 __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag, int code) {
@@ -113,57 +143,42 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
   *abort_flag = 1;
 }
 
-template <int BN, int STAGES>
-struct Cfg {
+// ------------------------------------------------------------------ few tiles
+//
+// One 128 x BN tile of D^T a cluster: A, the operand that fills the MMA's 128
+// rows, is the weight, and B the tokens, BN of them.  The cluster's CTAs
+// share the K loop: each multiplies its share of the stages into an fp32
+// partial, leaves it in shared memory, and after a cluster barrier each CTA
+// adds up its part of the tile over all partials in rank order -- the same
+// bits every time -- and writes D.  No workspace and no second launch.
+//
+// Bound by reading the weight (0.56 bytes a value): the split brings enough
+// CTAs, two an SM, to keep that many loads in flight.  With `early` the
+// preceding kernel of the stream is known not to write A, so its first
+// stages are loaded before that kernel has finished.
+template <int kFmt, int BN, int STAGES>
+struct FewCfg {
   static constexpr int kABytes = kBM * kBKBytes;
   static constexpr int kBBytes = BN * kBKBytes;
-  static constexpr int kScBytes = 4 * kScTile;  // of one operand and stage
+  static constexpr int kScBytes = stage_ktiles<kFmt>() * kScTile;
   static constexpr int kStageBytes = kABytes + kBBytes + 2 * kScBytes;
-  // Two accumulators, then four columns a scale tile for A and for B.
-  static constexpr int kSfa = 2 * BN;
+  static constexpr int kSfa = BN;
   static constexpr int kSfb = kSfa + 16;
-  static constexpr int kTmemCols = kSfb + 16 <= 128 ? 128 : kSfb + 16 <= 256 ? 256 : 512;
+  static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : BN + 32 <= 128 ? 128 : 256;
   static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes + 256;
   static_assert(BN % 16 == 0 && BN <= 128, "one row of scale tiles for B");
+  static_assert(STAGES * (kABytes + kBBytes) >= kBM * BN * 4, "the partial fits the stages");
+  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs an SM");
 };
 
-// One accumulator chunk (this lane's row, 16 columns from col0), scaled and
-// rounded to bf16.  kTrans: the kernel's rows are D's columns.
-template <bool kTrans>
-__device__ __forceinline__ void store_chunk(const uint32_t (&r)[16], float alpha,
-                                            const Fp4GemmParams& p, int64_t row, int64_t col0) {
-  if (row >= p.M) return;
-  if constexpr (kTrans) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (col0 + j < p.N)
-        p.d[(col0 + j) * p.ldd + row] = static_cast<uint16_t>(
-            cvt_bf16x2(__fmul_rn(__uint_as_float(r[j]), alpha), 0.0f) & 0xFFFFu);
-  } else {
-    uint16_t* dst = p.d + row * p.ldd + col0;
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v0, v1;
-      mul2_rn(r[2 * j], r[2 * j + 1], alpha, v0, v1);
-      w[j] = cvt_bf16x2(v0, v1);
-    }
-    if (p.vec && col0 + 16 <= p.N) {
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (col0 + j < p.N) dst[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-    }
-  }
-}
-
-template <int kFmt, int BN, int STAGES, bool kTrans>
-__global__ void __launch_bounds__(kThreads, 1)
-    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ Fp4GemmParams p) {
-  using C = Cfg<BN, STAGES>;
+template <int kFmt, int BN, int STAGES>
+__global__ void __launch_bounds__(kThreads, 2)
+    gemm_fp4_few_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSa,
+                        const __grid_constant__ CUtensorMap tmSb,
+                        const __grid_constant__ Fp4GemmParams p, const int split, const bool early) {
+  using C = FewCfg<kFmt, BN, STAGES>;
   constexpr int kKt = stage_ktiles<kFmt>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -174,34 +189,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sSb = sSa + STAGES * C::kScBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(sSb + STAGES * C::kScBytes);
   uint64_t* empty = full + STAGES;
-  uint64_t* acc_full = empty + STAGES;  // [2]
-  uint64_t* acc_empty = acc_full + 2;   // [2]
-  uint64_t* drain = acc_empty + 2;      // [1]
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* drain = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(sizeof(uint64_t) * (2 * STAGES + 5) + 8 <= 256, "barrier block");
+  float* partial = reinterpret_cast<float*>(sA);  // [BN][128] over the stages, once the MMAs are done
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t num_n = (p.N + BN - 1) / BN;
-  const int64_t num_tiles = ((p.M + kBM - 1) / kBM) * num_n;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t tile = blockIdx.x / split;
+  const int64_t num_n = (p.N + BN - 1) / BN;  // tiles of tokens
+  const int m_blk = static_cast<int>(tile / num_n), n_blk = static_cast<int>(tile % num_n);
   const int num_kb = static_cast<int>((p.K + kBK - 1) / kBK);
-  const int ktiles = static_cast<int>((p.K + kBK / kKt - 1) / (kBK / kKt));  // scale tiles along K
+  const int per = (num_kb + split - 1) / split;
+  const int kb0 = min(num_kb, rank * per), nkb = min(num_kb, kb0 + per) - kb0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], 4);
-    }
+    mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_map(&tmA);
-    tma_prefetch_map(&tmB);
   }
+  auto load_a = [&](int stage, int kb) {
+    mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
+    tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], kb * kBKBytes, m_blk * kBM);
+    tma_load_2d(sSa + stage * C::kScBytes, &tmSa, &full[stage], kb * kKt * kScElems, m_blk);
+  };
+  if (early && threadIdx.x == 0)
+    for (int i = 0; i < nkb && i < STAGES; ++i) load_a(i, kb0 + i);
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
@@ -216,149 +235,148 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t fills[STAGES];
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) fills[s] = 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
-        const int m_blk = static_cast<int>(t / num_n), n_blk = static_cast<int>(t % num_n);
+      int i = 0;
+      for (; i < nkb; ++i) {
+        const int stage = i % STAGES, kb = kb0 + i;
+        if (i >= STAGES && !mbar_wait_bounded(&empty[stage], (i / STAGES - 1) & 1u, abort_flag)) break;
+        if (!early || i >= STAGES) load_a(stage, kb);
+        tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * kBKBytes, n_blk * BN);
         // B's scale tile holds 128 rows: BN of them belong to this tile.
-        const uint8_t* sa = p.sca + static_cast<int64_t>(m_blk) * ktiles * kScTile;
-        const uint8_t* sb = p.scb + static_cast<int64_t>(n_blk) * ktiles * kScTile;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int kt0 = kb * kKt;
-          const uint32_t sc_bytes = static_cast<uint32_t>(min(kKt, ktiles - kt0)) * kScTile;
-          mbar_arrive_expect_tx(&full[stage], C::kABytes + C::kBBytes + 2 * sc_bytes);
-          tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], kb * kBKBytes, m_blk * kBM);
-          tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * kBKBytes, n_blk * BN);
-          bulk_load(sSa + stage * C::kScBytes, sa + static_cast<int64_t>(kt0) * kScTile, sc_bytes,
-                    &full[stage]);
-          bulk_load(sSb + stage * C::kScBytes, sb + static_cast<int64_t>(kt0) * kScTile, sc_bytes,
-                    &full[stage]);
-#pragma unroll
-          for (int s = 0; s < STAGES; ++s)
-            if (s == stage) ++fills[s];
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+        tma_load_2d(sSb + stage * C::kScBytes, &tmSb, &full[stage], kb * kKt * kScElems,
+                    n_blk * BN / 128);
       }
-      if (!ok) {
+      if (i < nkb) {
         record_error(p.err, abort_flag, kErrGemmProducerWait);
+        // Let the copies in flight land before the CTA exits.
         volatile int never = 0;
-#pragma unroll
-        for (int s = 0; s < STAGES; ++s)
-          if (fills[s] > 0) mbar_wait_bounded(&full[s], (fills[s] - 1) & 1u, &never);
+        for (int j = max(0, i - STAGES); j < i; ++j)
+          mbar_wait_bounded(&full[j % STAGES], (j / STAGES) & 1u, &never);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      bool ok = true;
-      bool issued = false;
-      for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
-        if (!mbar_wait_bounded(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait_bounded(&full[stage], phase, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const int nkt = min(kKt, ktiles - kb * kKt);
-          const int steps = static_cast<int>(min(int64_t(4), (p.K - int64_t(kb) * kBK + kMmaK - 1) / kMmaK));
-          const uint64_t a_desc = smem_desc_k_sw128(smem_addr(sA + stage * C::kABytes));
-          const uint64_t b_desc = smem_desc_k_sw128(smem_addr(sB + stage * C::kBBytes));
-          const uint64_t sa_desc = smem_desc_scale(smem_addr(sSa + stage * C::kScBytes));
-          const uint64_t sb_desc = smem_desc_scale(smem_addr(sSb + stage * C::kScBytes));
-          // Copies and MMAs of one thread run in the order they are issued.
-          for (int i = 0; i < nkt; ++i) {
-            copy_scale_tile(tmem_base + C::kSfa + 4 * i, sa_desc + static_cast<uint64_t>(i * (kScTile >> 4)));
-            copy_scale_tile(tmem_base + C::kSfb + 4 * i, sb_desc + static_cast<uint64_t>(i * (kScTile >> 4)));
-          }
+    // The tile's tokens may start inside a scale tile: 32 rows a column.
+    const uint32_t sfb = tmem_base + C::kSfb + static_cast<uint32_t>(n_blk * BN % 128 / 32);
+    bool ok = true;
+    int i = 0;
+    for (; i < nkb; ++i) {
+      const int stage = i % STAGES;
+      ok = warp_wait(&full[stage], (i / STAGES) & 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint64_t a_desc = smem_desc_k_sw128(smem_addr(sA + stage * C::kABytes));
+      const uint64_t b_desc = smem_desc_k_sw128(smem_addr(sB + stage * C::kBBytes));
+      const uint64_t sa_desc = smem_desc_scale(smem_addr(sSa + stage * C::kScBytes));
+      const uint64_t sb_desc = smem_desc_scale(smem_addr(sSb + stage * C::kScBytes));
+      const int64_t left = p.K - int64_t(kb0 + i) * kBK;
+      const int steps = left >= kBK ? 4 : static_cast<int>((left + kMmaK - 1) / kMmaK);
+      if (elect_one()) {
+        // Copies and MMAs of one thread run in the order they are issued.
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= steps) break;  // the rest of the stage lies past K: its scales are not loaded
-            const int kt = kFmt == 0 ? k : k >> 1;
-            const uint32_t idesc = make_idesc_fp4<kFmt>(kBM, BN, kFmt == 0 ? 0u : 2u * (k & 1));
-            mma_fp4<kFmt>(d_tmem, a_desc + static_cast<uint64_t>(2 * k),
+        for (int t = 0; t < kKt; ++t) {
+          copy_scale_tile(tmem_base + C::kSfa + 4 * t, sa_desc + static_cast<uint64_t>(t * (kScTile >> 4)));
+          copy_scale_tile(tmem_base + C::kSfb + 4 * t, sb_desc + static_cast<uint64_t>(t * (kScTile >> 4)));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int kt = kFmt == 0 ? k : k >> 1;
+          const uint32_t idesc = make_idesc_fp4<kFmt>(kBM, BN, kFmt == 0 ? 0u : 2u * (k & 1));
+          if (k < steps)  // the rest of the stage lies past K
+            mma_fp4<kFmt>(tmem_base, a_desc + static_cast<uint64_t>(2 * k),
                           b_desc + static_cast<uint64_t>(2 * k), idesc, tmem_base + C::kSfa + 4 * kt,
-                          tmem_base + C::kSfb + 4 * kt, (kb > 0 || k > 0) ? 1u : 0u);
-          }
-          issued = true;
-          mma_commit(&empty[stage]);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+                          sfb + 4 * kt, (i > 0 || k > 0) ? 1u : 0u);
         }
-        if (!ok) break;
-        mma_commit(&acc_full[acc]);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        if (i + STAGES < nkb) mma_commit(&empty[stage]);  // no load follows into the other stages
       }
-      if (!ok) {
+      __syncwarp();
+    }
+    if (elect_one()) {
+      if (ok) {
+        mma_commit(acc_full);
+      } else {
         record_error(p.err, abort_flag, kErrGemmMmaWait);
-        if (issued) {
+        if (i > 0) {
           volatile int never = 0;
           mma_commit(drain);
           mbar_wait_bounded(drain, 0, &never);
         }
       }
     }
-  } else {
+    __syncwarp();
+  }
+
+  const int cols = static_cast<int>(min(int64_t(BN), p.N - int64_t(n_blk) * BN));  // live tokens
+  const int64_t row0 = static_cast<int64_t>(m_blk) * kBM;
+  const float alpha =
+      kFmt == 0 ? __fmul_rn(__fdiv_rn(*p.inv_a, 6.0f), __fdiv_rn(*p.inv_b, 6.0f)) : 1.0f;
+  uint16_t* d = p.d + static_cast<int64_t>(n_blk) * BN * p.ldd + row0;
+  if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;  // TMEM lanes this warp may read
-    const float alpha =
-        kFmt == 0 ? __fmul_rn(__fdiv_rn(*p.inv_a, 6.0f), __fdiv_rn(*p.inv_b, 6.0f)) : 1.0f;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int64_t t = blockIdx.x; t < num_tiles; t += gridDim.x) {
-      const int64_t m_blk = t / num_n, n_blk = t % num_n;
-      const bool ready =
-          __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag));
-      if (!ready) {
-        if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
-        break;
-      }
+    const int r = quarter * 32 + lane;
+    const bool ready = warp_wait(acc_full, 0, abort_flag);
+    if (!ready) {
+      if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
+    } else {
       tc_fence_after_sync();
-      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                             static_cast<uint32_t>(acc * BN);
-      const int64_t row = m_blk * kBM + quarter * 32 + lane;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN / 16; ++c) {
-        uint32_t r[16];
-        tmem_load_16cols(t_row + c * 16, r);
+      for (int c0 = 0; c0 < cols; c0 += 16) {
+        uint32_t v[16];
+        tmem_load_16cols(t_row + c0, v);
         tmem_load_wait();
-        store_chunk<kTrans>(r, alpha, p, row, n_blk * BN + c * 16);
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
+        if (split > 1) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            partial[(c0 + j) * kBM + r] = nkb > 0 ? __uint_as_float(v[j]) : 0.0f;
+        } else if (row0 + r < p.M) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < cols)
+              d[(c0 + j) * p.ldd + r] = static_cast<uint16_t>(
+                  cvt_bf16x2(__fmul_rn(__uint_as_float(v[j]), alpha), 0.0f) & 0xFFFFu);
+        }
       }
     }
   }
-
+  if (split > 1) {
+    tc_fence_before_sync();
+    cluster_sync_all();  // every partial is in place
+    // Rows of the tile are dealt to the cluster's CTAs, four a thread.
+    const int quads = kBM / split / 4, mine = rank * (kBM / split);
+    const uint32_t base = smem_addr(partial);
+    const bool wide = p.vec && row0 + kBM <= p.M;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < quads * cols; e += kThreads) {
+      const int c = e / quads, r = mine + e % quads * 4;
+      const uint32_t at = base + static_cast<uint32_t>(c * kBM + r) * 4u;
+      float4 v[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < split) v[s] = ld_shared_cluster_f32x4(map_to_cta(at, s));
+      float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < split) {
+          sum[0] += v[s].x;
+          sum[1] += v[s].y;
+          sum[2] += v[s].z;
+          sum[3] += v[s].w;
+        }
+      const uint32_t lo = cvt_bf16x2(__fmul_rn(sum[0], alpha), __fmul_rn(sum[1], alpha));
+      const uint32_t hi = cvt_bf16x2(__fmul_rn(sum[2], alpha), __fmul_rn(sum[3], alpha));
+      uint16_t* dst = d + c * p.ldd + r;
+      if (wide) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (row0 + r + j < p.M)
+            dst[j] = static_cast<uint16_t>((j < 2 ? lo : hi) >> (16 * (j & 1)));
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while its partial is read
+  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -368,55 +386,511 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int kFmt, int BN, int STAGES, bool kTrans>
-cudaError_t run_one(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p,
-                    const DeviceInfo& dev, cudaStream_t stream) {
-  using C = Cfg<BN, STAGES>;
-  CUtensorMap tmA, tmB;
-  // A row's codes to the end of its last 32 values: zero past that.
-  const uint64_t inner = static_cast<uint64_t>((p.K + 31) / 32 * 16);
-  if (!make_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, inner, p.M, a.ld, kBKBytes, kBM,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, inner, p.N, b.ld, kBKBytes, BN,
-                   CU_TENSOR_MAP_SWIZZLE_128B))
-    return map_failed("fp4 gemm operand");
-  auto* kernel = gemm_fp4_kernel<kFmt, BN, STAGES, kTrans>;
-  static std::mutex mu;
-  static bool done[64] = {};
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev.device]) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(C::kSmemBytes));
-      if (e != cudaSuccess) return e;
-      done[dev.device] = true;
+// 32 rows x 64 columns of the accumulator (this lane's row in ra and rb),
+// scaled, rounded to bf16 and staged in shared memory as the 128-byte TMA
+// swizzle has them.  Rows that are 16-byte aligned leave by TMA (clipped to
+// D); others two bytes a lane, consecutive lanes on consecutive columns.
+__device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32_t (&rb)[32],
+                                          float alpha, uint8_t* box, const CUtensorMap* tmD,
+                                          const Fp4GemmParams& p, int row0, int64_t col0, int lane) {
+  uint32_t w[32];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float v0, v1;
+    mul2_rn(ra[2 * j], ra[2 * j + 1], alpha, v0, v1);
+    w[j] = cvt_bf16x2(v0, v1);
+    mul2_rn(rb[2 * j], rb[2 * j + 1], alpha, v0, v1);
+    w[16 + j] = cvt_bf16x2(v0, v1);
+  }
+  if (lane == 0) bulk_wait_group_read<0>();  // the box's last store has read it
+  __syncwarp();
+  const int sw = lane & 7;
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ sw) << 4)) =
+        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  if (p.vec) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tmD, box, static_cast<int32_t>(col0), row0);
+      bulk_commit_group();
+    }
+    return;
+  }
+  __syncwarp();
+  const int rows = static_cast<int>(min(int64_t(32), p.M - row0));
+  uint16_t* dst = p.d + static_cast<int64_t>(row0) * p.ldd + col0;
+  const bool in0 = col0 + lane < p.N, in1 = col0 + lane + 32 < p.N;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    const uint8_t* src = box + r * 128 + (lane & 7) * 2;
+    const uint16_t v0 = *reinterpret_cast<const uint16_t*>(src + (((lane >> 3) ^ (r & 7)) << 4));
+    const uint16_t v1 = *reinterpret_cast<const uint16_t*>(src + (((lane >> 3) + 4 ^ (r & 7)) << 4));
+    if (r < rows) {
+      if (in0) dst[r * p.ldd + lane] = v0;
+      if (in1) dst[r * p.ldd + lane + 32] = v1;
     }
   }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ CTA pairs
+//
+// Two CTAs share a 256 x BN tile as in the 8-bit pair kernel: each loads its
+// 128 rows of A and half of B's rows, and the even CTA issues
+// tcgen05.mma.cta_group::2 over both.  Each CTA's tensor memory holds the
+// scales of its own rows of A and of all BN rows of B, so both load B's scale
+// tiles whole.  BN rows of B that start inside a scale tile (BN = 192) use
+// the columns from their first 32-row group on.
+//
+// Two accumulators of BN columns and the scales have to fit 512 columns of
+// tensor memory.  Where they do not (BN = 256), the accumulators overlap by
+// kShared columns: the epilogue reads those first and announces them on
+// `shared_free`, and the next tile's MMAs wait for that.
+template <int kFmt, int BN, int STAGES, int EPI>
+struct PairCfg {
+  static constexpr int kKt = stage_ktiles<kFmt>();
+  static constexpr int kRowTiles = 2;                    // rows of scale tiles under BN rows of B
+  static constexpr int kABytes = kBM * kBKBytes;
+  static constexpr int kBBytes = BN / 2 * kBKBytes;
+  static constexpr int kSaBytes = kKt * kScTile;
+  static constexpr int kSbBytes = kRowTiles * kKt * kScTile;
+  static constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;
+  static constexpr int kSfCols = 4 * kKt * (1 + kRowTiles);
+  static constexpr int kSfa = 512 - kSfCols;
+  static constexpr int kSfb = kSfa + 4 * kKt;
+  static constexpr int kAcc1 = 2 * BN <= kSfa ? BN : kSfa - BN;  // second accumulator's first column
+  static constexpr bool kOverlap = kAcc1 < BN;
+  static constexpr int kBoxBytes = 32 * 128;             // 32 rows x 64 bf16 columns
+  static constexpr int kGroups = BN / 64 / (EPI / 4);    // boxes an epilogue warp writes
+  static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes +
+                                       static_cast<size_t>(EPI) * kBoxBytes + 256;
+  static_assert(BN % 64 == 0 && BN <= 256 && kBBytes % 1024 == 0, "tile");
+  static_assert(BN / 64 % (EPI / 4) == 0, "the epilogue warps of a quarter share the boxes");
+  static_assert(!kOverlap || BN - kAcc1 <= 64, "the overlap lies in one box");
+  static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+};
+
+// The t-th tile.  The larger operand is read once and the smaller again and
+// again from L2: with at least as many columns as rows, all rows of tiles
+// within a column of them; else groups of four rows of tiles, column by
+// column.  8192 x 14336 x 4096: 159.9 us against 169.4 in groups of four;
+// 16384 x 4096 x 4096: 95.4 us against 98.6 by whole columns.
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int64_t t, int64_t num_m, int64_t num_n, int64_t group) {
+  const int64_t g = t / (group * num_n);
+  const int64_t r = t - g * group * num_n;
+  const int64_t rows = min(group, num_m - g * group);
+  return {static_cast<int>(g * group + r % rows), static_cast<int>(r / rows)};
+}
+
+template <int kFmt, int BN, int STAGES, int EPI>
+__global__ void __launch_bounds__(64 + 32 * EPI, 1)
+    gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmSa,
+                         const __grid_constant__ CUtensorMap tmSb,
+                         const __grid_constant__ CUtensorMap tmD,
+                         const __grid_constant__ Fp4GemmParams p) {
+  using C = PairCfg<kFmt, BN, STAGES, EPI>;
+  constexpr int kKt = C::kKt;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * C::kABytes;
+  uint8_t* sEpi = sB + STAGES * C::kBBytes;
+  uint8_t* sSa = sEpi + EPI * C::kBoxBytes;
+  uint8_t* sSb = sSa + STAGES * C::kSaBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sSb + STAGES * C::kSbBytes);  // even CTA: both CTAs' loads
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;   // [2]
+  uint64_t* acc_empty = acc_full + 2;    // [2] even CTA: every epilogue warp of the pair
+  uint64_t* shared_free = acc_empty + 2;  // [1] even CTA, with overlapping accumulators
+  uint64_t* drain = shared_free + 1;     // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // Written by the peer CTA before the closing cluster barrier: whether it
+  // gave up, and (odd CTA -> even CTA) how many loads it issued into a stage.
+  volatile uint32_t* peer_abort = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
+  volatile uint32_t* peer_fills = peer_abort + 1;      // [STAGES]
+  volatile uint32_t* own_fills = peer_fills + STAGES;  // [STAGES]
+  static_assert(sizeof(uint64_t) * (2 * STAGES + 6) + sizeof(uint32_t) * (3 + 2 * STAGES) <= 256,
+                "barrier block");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t pair = cluster_id_x(), num_pairs = cluster_count_x();
+  const int64_t num_n = (p.N + BN - 1) / BN;
+  const int64_t num_m = (p.M + 2 * kBM - 1) / (2 * kBM);
+  const int64_t num_tiles = num_m * num_n;
+  const int64_t group = p.N >= p.M ? num_m : 4;
+  const int num_kb = static_cast<int>((p.K + kBK - 1) / kBK);
+  // MMAs of the last stage; what follows K is zero in the codes and is not multiplied.
+  const int last_steps = static_cast<int>((p.K - int64_t(num_kb - 1) * kBK + kMmaK - 1) / kMmaK);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 2 * EPI);
+    }
+    mbar_init(shared_free, 2 * EPI);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *peer_abort = 0;
+    for (int s = 0; s < STAGES; ++s) peer_fills[s] = own_fills[s] = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&tmA);
+    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&tmSa);
+    tma_prefetch_map(&tmSb);
+    tma_prefetch_map(&tmD);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync_all();  // barriers of both CTAs initialised before any remote use
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producers (both CTAs)
+    if (lane == 0) {
+      uint32_t fills[STAGES];
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) fills[s] = 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t t = pair; ok && t < num_tiles; t += num_pairs) {
+        const TileAt at = tile_at(t, num_m, num_n, group);
+        const int m0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM;
+        const int n0 = at.n * BN;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_even = map_to_cta(smem_addr(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+          tma_load_2d_pair(sA + stage * C::kABytes, &tmA, full_even, kb * kBKBytes, m0);
+          tma_load_2d_pair(sB + stage * C::kBBytes, &tmB, full_even, kb * kBKBytes,
+                           n0 + static_cast<int>(rank) * (BN / 2));
+          tma_load_2d_pair(sSa + stage * C::kSaBytes, &tmSa, full_even, kb * kKt * kScElems,
+                           m0 / kBM);
+          tma_load_2d_pair(sSb + stage * C::kSbBytes, &tmSb, full_even, kb * kKt * kScElems,
+                           n0 / 128);
+#pragma unroll
+          for (int s = 0; s < STAGES; ++s)
+            if (s == stage) ++fills[s];
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) record_error(p.err, abort_flag, kErrGemmProducerWait);
+      if (rank == 1) {
+        const uint32_t even_fills = map_to_cta(smem_addr(const_cast<uint32_t*>(peer_fills)), 0);
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) st_shared_cluster_u32(even_fills + 4u * s, fills[s]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) own_fills[s] = fills[s];
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    // The whole warp runs the loop and one elected lane issues, so that the
+    // operands of the copies and MMAs stay in uniform registers.
+    if (rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0, shared_phase = 0;
+      bool ok = true;
+      bool issued = false;
+      for (int64_t t = pair; ok && t < num_tiles; t += num_pairs) {
+        ok = warp_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag);
+        if constexpr (C::kOverlap) {
+          // The columns shared with the tile before this one (none before the first).
+          if (ok && issued) {
+            ok = warp_wait(shared_free, shared_phase, abort_flag);
+            shared_phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAcc1);
+        const uint32_t sfb =
+            tmem_base + C::kSfb +
+            static_cast<uint32_t>(tile_at(t, num_m, num_n, group).n * BN % 128 / 32);
+        for (int kb = 0; kb < num_kb; ++kb) {
+          ok = warp_wait(&full[stage], phase, abort_flag);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t a_desc = smem_desc_k_sw128(smem_addr(sA + stage * C::kABytes));
+          const uint64_t b_desc = smem_desc_k_sw128(smem_addr(sB + stage * C::kBBytes));
+          const uint64_t sa_desc = smem_desc_scale(smem_addr(sSa + stage * C::kSaBytes));
+          const uint64_t sb_desc = smem_desc_scale(smem_addr(sSb + stage * C::kSbBytes));
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < kKt; ++i) {
+              copy_scale_tile_pair(tmem_base + C::kSfa + 4 * i,
+                                   sa_desc + static_cast<uint64_t>(i * (kScTile >> 4)));
+#pragma unroll
+              for (int r = 0; r < C::kRowTiles; ++r)
+                copy_scale_tile_pair(
+                    tmem_base + C::kSfb + 4 * (i * C::kRowTiles + r),
+                    sb_desc + static_cast<uint64_t>((r * kKt + i) * (kScTile >> 4)));
+            }
+            auto step = [&](int k) {
+              const int kt = kFmt == 0 ? k : k >> 1;
+              const uint32_t idesc =
+                  make_idesc_fp4<kFmt>(2 * kBM, BN, kFmt == 0 ? 0u : 2u * (k & 1));
+              mma_fp4_pair<kFmt>(d_tmem, a_desc + static_cast<uint64_t>(2 * k),
+                                 b_desc + static_cast<uint64_t>(2 * k), idesc,
+                                 tmem_base + C::kSfa + 4 * kt, sfb + 4 * C::kRowTiles * kt,
+                                 (kb > 0 || k > 0) ? 1u : 0u);
+            };
+            if (kb + 1 < num_kb || last_steps == 4) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) step(k);
+            } else {
+#pragma unroll 1
+              for (int k = 0; k < last_steps; ++k) step(k);
+            }
+            mma_commit_pair_multicast(&empty[stage], 0x3);
+          }
+          __syncwarp();
+          issued = true;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit_pair_multicast(&acc_full[acc], 0x3);
+        __syncwarp();
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok && elect_one()) {
+        record_error(p.err, abort_flag, kErrGemmMmaWait);
+        if (issued) {
+          volatile int never = 0;
+          mma_commit_pair_multicast(drain, 0x1);
+          mbar_wait_bounded(drain, 0, &never);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int part = (warp - 2) >> 2;  // which of the quarter's warps (0 when EPI == 4)
+    const float alpha =
+        kFmt == 0 ? __fmul_rn(__fdiv_rn(*p.inv_a, 6.0f), __fdiv_rn(*p.inv_b, 6.0f)) : 1.0f;
+    const uint32_t acc_empty_even = map_to_cta(smem_addr(acc_empty), 0);
+    const uint32_t shared_free_even = map_to_cta(smem_addr(shared_free), 0);
+    uint8_t* box = sEpi + (warp - 2) * C::kBoxBytes;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int64_t t = pair; t < num_tiles; t += num_pairs) {
+      const TileAt at = tile_at(t, num_m, num_n, group);
+      const int row0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM + quarter * 32;
+      const int64_t n0 = static_cast<int64_t>(at.n) * BN;
+      const bool ready =
+          __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag));
+      if (!ready) {
+        if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                             static_cast<uint32_t>(acc * C::kAcc1);
+#pragma unroll 1
+      for (int g = 0; g < C::kGroups; ++g) {
+        // The first accumulator's shared columns are its last, the second's its first.
+        const int i = part * C::kGroups + (C::kOverlap && acc == 0 ? C::kGroups - 1 - g : g);
+        const int64_t col0 = n0 + 64 * i;
+        const bool live = row0 < p.M && col0 < p.N;
+        uint32_t ra[32], rb[32];
+        if (live) {
+          tmem_load_32cols(t_row + 64 * i, ra);
+          tmem_load_32cols(t_row + 64 * i + 32, rb);
+          tmem_load_wait();
+        }
+        if (g == 0 || g == C::kGroups - 1) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (C::kOverlap && g == 0) mbar_arrive_cluster(shared_free_even);
+            if (g == C::kGroups - 1) mbar_arrive_cluster(acc_empty_even + 8u * acc);
+          }
+        }
+        if (live) store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  __syncwarp();
+  __syncthreads();  // every role of this CTA is done: its abort flag is final
+  if (threadIdx.x == 0)
+    st_shared_cluster_u32(map_to_cta(smem_addr(const_cast<uint32_t*>(peer_abort)), rank ^ 1u),
+                          *abort_flag != 0 ? 1u : 0u);
+  tc_fence_before_sync();
+  cluster_sync_all();  // no CTA leaves while its peer may still read its shared memory
+  // After a failure, loads may be in flight: the even CTA balances each
+  // stage's last phase (its full[] counts both CTAs' bytes) and waits,
+  // bounded, for it, as the 8-bit pair kernel does.
+  if (*abort_flag != 0 || *peer_abort != 0) {
+    if (rank == 0 && threadIdx.x == 0) {
+      volatile int never = 0;
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t fe = own_fills[s], fo = peer_fills[s];
+        if (fo > fe) mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+        if (fe > fo) mbar_complete_tx(&full[s], C::kStageBytes);
+        const uint32_t last = fe > fo ? fe : fo;
+        if (last > 0) mbar_wait_bounded(&full[s], (last - 1) & 1u, &never);
+      }
+    }
+    cluster_sync_all();
+  }
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// Shared memory of a kernel instance, allowed once a device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, const DeviceInfo& dev, bool (&done)[64]) {
+  static std::mutex mu;
+  if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev.device]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
+  done[dev.device] = e == cudaSuccess;
+  return e;
+}
+
+// Codes of one operand: boxes of 128 bytes of K.  The rows end at their last
+// 32 values; the box is zero past that, and past the last row.
+bool make_code_map(CUtensorMap* map, const Fp4View& v, int64_t rows, int64_t K, int box_rows) {
+  return make_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, v.codes,
+                     static_cast<uint64_t>((K + 31) / 32 * 16), static_cast<uint64_t>(rows),
+                     static_cast<uint64_t>(v.ld), kBKBytes, static_cast<uint32_t>(box_rows),
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scale tiles of one operand, a row of tiles for 128 rows: boxes of a
+// stage's tiles along K and `box_rows` rows of tiles, zero past the last.
+template <int kFmt>
+bool make_scale_map(CUtensorMap* map, const Fp4View& v, int64_t rows, int64_t K, int box_rows) {
+  const uint64_t elems = static_cast<uint64_t>(fp4_scale_ktiles(K, kFmt)) * kScElems;
+  return make_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, v.scales, elems,
+                     static_cast<uint64_t>((rows + 127) / 128), elems * 8,
+                     stage_ktiles<kFmt>() * kScElems, static_cast<uint32_t>(box_rows),
+                     CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// The K split of the few-tile kernel: a power of two, at most `most` CTAs and
+// at least two stages each.
+int few_split(int64_t tiles, int64_t K, int64_t most) {
+  const int64_t num_kb = (K + kBK - 1) / kBK;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= most && num_kb >= split * 4) split *= 2;
+  return split;
+}
+
+template <int kFmt, int BN, int STAGES>
+cudaError_t run_few(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev,
+                    cudaStream_t stream) {
+  using C = FewCfg<kFmt, BN, STAGES>;
+  p.M = g.N;
+  p.N = g.M;
+  CUtensorMap tmA, tmB, tmSa, tmSb;
+  if (!make_code_map(&tmA, g.b, p.M, p.K, kBM) || !make_code_map(&tmB, g.a, p.N, p.K, BN) ||
+      !make_scale_map<kFmt>(&tmSa, g.b, p.M, p.K, 1) || !make_scale_map<kFmt>(&tmSb, g.a, p.N, p.K, 1))
+    return map_failed("fp4 gemm operand");
+  auto* kernel = gemm_fp4_few_kernel<kFmt, BN, STAGES>;
+  static bool done[64] = {};
+  cudaError_t e = allow_smem(kernel, C::kSmemBytes, dev, done);
+  if (e != cudaSuccess) return e;
   const int64_t tiles = ((p.M + kBM - 1) / kBM) * ((p.N + BN - 1) / BN);
-  const unsigned grid = static_cast<unsigned>(tiles < dev.num_sms ? tiles : dev.num_sms);
-  set_error_site("gemm_fp4_kernel");
-  return launch_kernel(kernel, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, 1, false, tmA, tmB,
-                       p);
+  // Two CTAs an SM where the weight's loads bound it (up to 32 tokens); one
+  // where the partials are larger: 64 x 4096 x 4096 6.7 us against 8.3.
+  const int split = few_split(tiles, p.K, (BN <= 32 ? 2 : 1) * int64_t(dev.num_sms));
+  set_error_site("gemm_fp4_few_kernel");
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * split)), dim3(kThreads),
+                       C::kSmemBytes, stream, split, false, tmA, tmB, tmSa, tmSb, p, split,
+                       g.b_early);
+}
+
+template <int kFmt, int BN, int STAGES, int EPI>
+cudaError_t run_pair(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p,
+                     const DeviceInfo& dev, cudaStream_t stream) {
+  using C = PairCfg<kFmt, BN, STAGES, EPI>;
+  CUtensorMap tmA, tmB, tmSa, tmSb, tmD;
+  if (!make_code_map(&tmA, a, p.M, p.K, kBM) || !make_code_map(&tmB, b, p.N, p.K, BN / 2) ||
+      !make_scale_map<kFmt>(&tmSa, a, p.M, p.K, 1) ||
+      !make_scale_map<kFmt>(&tmSb, b, p.N, p.K, C::kRowTiles))
+    return map_failed("fp4 pair gemm operand");
+  // Rows that TMA cannot store are written from shared memory: no map then.
+  if (!p.vec)
+    tmD = tmA;
+  else if (!make_map_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.d, static_cast<uint64_t>(p.N),
+                        static_cast<uint64_t>(p.M), static_cast<uint64_t>(p.ldd) * 2, 64, 32,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
+    return map_failed("fp4 pair gemm output");
+  auto* kernel = gemm_fp4_pair_kernel<kFmt, BN, STAGES, EPI>;
+  static bool done[64] = {};
+  cudaError_t e = allow_smem(kernel, C::kSmemBytes, dev, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + BN - 1) / BN);
+  const int64_t slots = dev.num_sms / 2;
+  const unsigned pairs = static_cast<unsigned>(tiles < slots ? tiles : slots);
+  set_error_site("gemm_fp4_pair_kernel");
+  return launch_kernel(kernel, dim3(2 * pairs), dim3(64 + 32 * EPI), C::kSmemBytes, stream, 2, false,
+                       tmA, tmB, tmSa, tmSb, tmD, p);
 }
 
 template <int kFmt>
 cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev,
                     cudaStream_t stream) {
-  if (g.M <= 128) {
-    // Few rows: the weight's rows fill the MMA's 128, the tokens are its columns.
-    p.M = g.N;
-    p.N = g.M;
-    p.sca = g.b.scales;
-    p.scb = g.a.scales;
-    p.inv_a = g.inv_b;
-    p.inv_b = g.inv_a;
-    if (g.M <= 16) return run_one<kFmt, 16, 8, true>(g.b, g.a, p, dev, stream);
-    if (g.M <= 32) return run_one<kFmt, 32, 8, true>(g.b, g.a, p, dev, stream);
-    if (g.M <= 64) return run_one<kFmt, 64, 6, true>(g.b, g.a, p, dev, stream);
-    return run_one<kFmt, 128, 5, true>(g.b, g.a, p, dev, stream);
-  }
-  return run_one<kFmt, 128, 5, false>(g.a, g.b, p, dev, stream);
+  // The few-tile kernel while its tiles are one wave, two CTAs an SM:
+  // 512 x 4096 x 4096 takes 10.6 us there and 12.5 us in pairs, 1024 x 4096 x
+  // 4096 (two waves) 20.1 and 12.9.
+  if (g.M <= 16) return run_few<kFmt, 16, 4>(g, p, dev, stream);
+  if (g.M <= 32) return run_few<kFmt, 32, 4>(g, p, dev, stream);
+  if ((g.M + 63) / 64 * ((g.N + kBM - 1) / kBM) <= 2 * int64_t(dev.num_sms))
+    return run_few<kFmt, 64, 3>(g, p, dev, stream);
+  // Eight epilogue warps where writing a tile takes as long as multiplying
+  // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
+  // 777 x 4801 x 1600 11.5 us against 13.3, 12288 x 6400 x 1600 69.4 against
+  // 70.5, but 8192 x 14336 x 4096 171 against 161.
+  if (!p.vec || g.K < 10 * kBK) return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, dev, stream);
+  return run_pair<kFmt, 256, 5, 4>(g.a, g.b, p, dev, stream);
 }
 
 }  // namespace
@@ -426,8 +900,6 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStr
   p.M = g.M;
   p.N = g.N;
   p.K = g.K;
-  p.sca = g.a.scales;
-  p.scb = g.b.scales;
   p.inv_a = g.inv_a;
   p.inv_b = g.inv_b;
   p.d = static_cast<uint16_t*>(g.d);

@@ -357,6 +357,7 @@ struct Fp4GemmArgs {
   void* d;
   int64_t ldd;
   int* ws_error;
+  bool b_early = false;  // the kernel before this one in the stream does not write b
 };
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStream_t stream);
 

@@ -307,6 +307,16 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_saddr
   return v;
 }
 
+// 16-byte load from shared memory of a CTA of the cluster.
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_saddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_saddr)
+               : "memory");
+  return v;
+}
+
 // 32-bit store into shared memory of a CTA of the cluster (address from
 // map_to_cta); a later cluster barrier makes it visible there.
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_saddr, uint32_t v) {
