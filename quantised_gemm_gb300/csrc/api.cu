@@ -1401,29 +1401,42 @@ fp8lin_status check_grads(const fp8lin_grad* grads, int32_t count, bool outs) {
   return FP8LIN_OK;
 }
 
+double* norm_partials(void* ws) {
+  return reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsPartialOffset);
+}
+
+// left: null, or where a single launch may leave its partial sums for the
+// scaling; then their number, else 0.
 fp8lin_status run_grad_norm(const fp8lin_grad* grads, int32_t count, float* norm, void* ws,
-                            const DeviceInfo& dev, cudaStream_t stream) {
-  double* partials = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsPartialOffset);
-  double* total = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsNormTotalOffset);
-  uint32_t* ticket = ws_u32(ws, kWsAtomicTicketOffset);
+                            const DeviceInfo& dev, cudaStream_t stream, int* left) {
+  GradNormArgs a;
+  a.partials = norm_partials(ws);
+  a.total = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsNormTotalOffset);
+  a.ticket = ws_u32(ws, kWsAtomicTicketOffset);
+  a.norm = norm;
   int64_t of[2] = {0, 0};
   for (int32_t i = 0; i < count; ++i)
     if (grads[i].n > 0) ++of[grads[i].g_f32 != 0];
   int64_t launches = 0;
   for (int64_t n : of) launches += (n + kClipMaxTensors - 1) / kClipMaxTensors;
+  if (left != nullptr) *left = 0;
   if (launches == 0) {
     cudaError_t e = cudaMemsetAsync(norm, 0, sizeof(float), stream);
     return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
   }
+  a.leave = left != nullptr && launches == 1;
   int64_t k = 0;
   for (int f32 = 0; f32 < 2; ++f32) {
+    a.bf16 = f32 == 0;
     fp8lin_status s = for_lists(
         grads, count, [&](const fp8lin_grad& t) { return (t.g_f32 != 0) == (f32 != 0); },
         [&](const GradTensor* list, int n) {
           ProfScope ps(FP8LIN_PROF_AMAX, stream);
-          cudaError_t e = launch_grad_norm(list, n, f32 == 0, k == 0, k == launches - 1, partials,
-                                           total, ticket, norm, dev, stream);
-          ++k;
+          a.first = k == 0;
+          a.last = ++k == launches;
+          int grid = 0;
+          cudaError_t e = launch_grad_norm(list, n, a, dev, stream, &grid);
+          if (a.leave) *left = grid;
           return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
         });
     if (s != FP8LIN_OK) return s;
@@ -1431,18 +1444,18 @@ fp8lin_status run_grad_norm(const fp8lin_grad* grads, int32_t count, float* norm
   return FP8LIN_OK;
 }
 
-fp8lin_status run_grad_clip(const fp8lin_grad* grads, int32_t count, const float* norm,
-                            float max_norm, float eps, const DeviceInfo& dev,
-                            cudaStream_t stream) {
+fp8lin_status run_grad_clip(const fp8lin_grad* grads, int32_t count, GradScaleArgs a,
+                            const DeviceInfo& dev, cudaStream_t stream) {
   for (int kind = 0; kind < 4; ++kind) {
     const bool f32 = (kind & 1) != 0, out_f32 = (kind & 2) != 0;
+    a.bf16 = !f32;
+    a.out_bf16 = !out_f32;
     fp8lin_status s = for_lists(
         grads, count,
         [&](const fp8lin_grad& t) { return (t.g_f32 != 0) == f32 && (t.out_f32 != 0) == out_f32; },
         [&](const GradTensor* list, int n) {
           ProfScope ps(FP8LIN_PROF_SCALE, stream);
-          cudaError_t e =
-              launch_grad_scale(list, n, !f32, !out_f32, norm, max_norm, eps, dev, stream);
+          cudaError_t e = launch_grad_scale(list, n, a, dev, stream);
           return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
         });
     if (s != FP8LIN_OK) return s;
@@ -1462,7 +1475,7 @@ fp8lin_status fp8lin_grad_norm(const fp8lin_grad* grads, int32_t count, float* n
     return FP8LIN_EINVAL;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  return run_grad_norm(grads, count, norm, ws, dev, stream);
+  return run_grad_norm(grads, count, norm, ws, dev, stream, nullptr);
 }
 
 fp8lin_status fp8lin_grad_clip(const fp8lin_grad* grads, int32_t count, const float* norm,
@@ -1473,7 +1486,11 @@ fp8lin_status fp8lin_grad_clip(const fp8lin_grad* grads, int32_t count, const fl
     return FP8LIN_EINVAL;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  return run_grad_clip(grads, count, norm, max_norm, eps, dev, stream);
+  GradScaleArgs a = {};
+  a.norm = const_cast<float*>(norm);  // only read: count is 0
+  a.max_norm = max_norm;
+  a.eps = eps;
+  return run_grad_clip(grads, count, a, dev, stream);
 }
 
 fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, float max_norm,
@@ -1486,8 +1503,13 @@ fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, flo
     return FP8LIN_EINVAL;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  if ((s = run_grad_norm(grads, count, norm, ws, dev, stream)) != FP8LIN_OK) return s;
-  return run_grad_clip(grads, count, norm, max_norm, eps, dev, stream);
+  GradScaleArgs a = {};
+  a.norm = norm;
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.partials = norm_partials(ws);
+  if ((s = run_grad_norm(grads, count, norm, ws, dev, stream, &a.count)) != FP8LIN_OK) return s;
+  return run_grad_clip(grads, count, a, dev, stream);
 }
 
 uint64_t fp8lin_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

@@ -3,15 +3,21 @@
 //   norm = sqrt(sum_t sum_i g_t[i]^2),  out_t[i] = g_t[i] * min(1, max_norm / (norm + eps)).
 //
 // Bound by memory: the norm reads every gradient once, the scaling reads and
-// writes it once.  The list travels in the kernel's parameters (no table on
-// the device, so the calls can be captured and the tensors may move from call
-// to call).  The list is cut into chunks of kChunk values; a CTA takes chunks
-// round-robin and finds a chunk's tensor by bisection.  Squares are added in
-// fp32 within a thread's share of a chunk and in fp64 from there on, always
-// in the same order: the norm has the same bits for the same list.
+// writes it once.  738 M fp32 values: 434 us and 899 us, 6.8 and 6.6 TB/s;
+// 31 M bf16 values into fp32: 44 us together, of which 27 us is the traffic.
+// The list travels in the kernel's parameters (no table on the device, so the
+// calls can be captured and the tensors may move from call to call).  It is
+// cut into chunks, and each CTA takes a run of them, so all CTAs read alike
+// whatever the tensors' sizes.  The scaling walks its runs from their ends,
+// where the norm stopped, and adds up the norm's partial sums itself where
+// one launch made them all (a last CTA that does it costs 4 us more).
+// Squares are added in fp32 over kUnroll vectors of a thread, in pairs of
+// fp32 numbers within a CTA and in fp64 from there on, always in the same
+// order: the norm has the same bits for the same list.
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -19,8 +25,9 @@
 namespace fp8lin {
 namespace {
 
-constexpr int kClipThreads = 256;
-constexpr int kChunk = 16384;   // values of a chunk: 8 rounds of 8 values a thread
+constexpr int kClipThreads = 512;
+constexpr int kChunk = 2048;    // values of a chunk
+constexpr int kUnroll = 4;      // 16-byte loads a thread has in flight
 constexpr int kSmallList = 32;  // tensors of the short parameter block
 
 template <int kMax>
@@ -77,12 +84,11 @@ __device__ __forceinline__ bool aligned(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-// Sum over the block in a fixed order; the result in thread 0.
+// Sum over the block in fp64, in a fixed order; the result in thread 0.
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double red[kClipThreads / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.0;
@@ -91,23 +97,74 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-// One thread's share of the squares of n values, added up in Acc.
-template <bool kBf16, typename Acc>
-__device__ __forceinline__ Acc square_sum(const uint8_t* base, int n) {
-  constexpr int kN = Vec<kBf16>::kN;
-  Acc s = 0;
-  int done = 0;
-  if (aligned(base)) {
-    const int vecs = n / kN;
-    const uint4* v = reinterpret_cast<const uint4*>(base);
-    for (int i = threadIdx.x; i < vecs; i += 4 * kClipThreads) {
-      uint4 u[4];
+// The sum of the CTAs' partial sums by the block's first four warps, in a
+// fixed order; the result in thread 0.
+__device__ __forceinline__ double sum_partials(const double* partials, int count) {
+  constexpr int kPer = kClipMaxPartials / 128;
+  __shared__ double red[4];
+  if (threadIdx.x < 128) {
+    double part[kPer], all = 0.0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kPer; ++k) {  // all loads in flight together
+      const int i = threadIdx.x + 128 * k;
+      part[k] = i < count ? __ldcg(partials + i) : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (128 * k < count) all += part[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_down_sync(0xFFFFFFFFu, all, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = all;
+  }
+  __syncthreads();
+  return threadIdx.x == 0 ? (red[0] + red[1]) + (red[2] + red[3]) : 0.0;
+}
+
+// A CTA's run of chunks is a piece of one tensor or of several; walk() calls
+// fn(tensor, first value, values) for each piece.
+template <int kMax, typename Fn>
+__device__ __forceinline__ void walk(const TensorList<kMax>& l, Fn fn) {
+  int64_t c = l.chunks * blockIdx.x / gridDim.x;
+  const int64_t end = l.chunks * (blockIdx.x + 1) / gridDim.x;
+  if (c >= end) return;
+  for (int t = find_tensor(l, c); c < end; ++t) {
+    const int64_t begin = (c - l.first[t]) * kChunk;
+    const int64_t stop = min(l.n[t], (end - l.first[t]) * kChunk);
+    fn(t, begin, stop - begin);
+    c = l.first[t] + (l.n[t] + kChunk - 1) / kChunk;
+  }
+}
+
+// An unevaluated sum hi + lo of fp32 numbers >= 0: 48 bits at fp32 rates
+// (this GPU adds two fp64 numbers a clock and SM).
+struct Pair {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float x) {  // Knuth's exact sum
+    const float t = __fadd_rn(hi, x);
+    const float z = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(x, z)));
+    hi = t;
+  }
+};
+
+// fn(square sum of kUnroll vectors or of one value) over this thread's share
+// of n values; the squares of one call are added in Acc.
+template <bool kBf16, typename Acc, typename Fn>
+__device__ __forceinline__ void square_sums(const uint8_t* base, int64_t n, Fn fn) {
+  constexpr int kN = Vec<kBf16>::kN;
+  int64_t done = 0;
+  if (aligned(base)) {
+    const int64_t vecs = n / kN;
+    const uint4* v = reinterpret_cast<const uint4*>(base);
+    for (int64_t i = threadIdx.x; i < vecs; i += kUnroll * kClipThreads) {
+      uint4 u[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
         u[k] = i + k * kClipThreads < vecs ? __ldg(v + i + k * kClipThreads)
                                            : make_uint4(0, 0, 0, 0);
+      Acc s = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kUnroll; ++k) {
         const Vec<kBf16> x(u[k]);
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
@@ -115,50 +172,82 @@ __device__ __forceinline__ Acc square_sum(const uint8_t* base, int n) {
           s = fma(y, y, s);
         }
       }
+      fn(s);
     }
     done = vecs * kN;
   }
-  for (int i = done + threadIdx.x; i < n; i += kClipThreads) {
+  for (int64_t i = done + threadIdx.x; i < n; i += kClipThreads) {
     const Acc y = load_one<kBf16>(base, i);
-    s = fma(y, y, s);
+    fn(y * y);
   }
-  return s;
 }
 
+// What a norm launch does with the CTAs' partial sums.
+enum NormEnd : int {
+  kLeave = 0,   // leaves them for the scaling, which adds them up itself
+  kCarry = 1,   // the last CTA adds them to *total
+  kFinish = 2,  // the last CTA adds them up (and *total, unless first) and writes the norm
+};
+
 template <bool kBf16, int kMax>
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, 2048 / kClipThreads)
     grad_norm_kernel(const __grid_constant__ TensorList<kMax> l, double* partials, double* total,
-                     uint32_t* ticket, float* norm, bool first, bool last) {
+                     uint32_t* ticket, float* norm, bool first, int end) {
   griddep_wait();
   griddep_launch_dependents();
+  Pair acc;
+  walk(l, [&](int t, int64_t begin, int64_t n) {
+    square_sums<kBf16, float>(static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4), n,
+                              [&](float s) { acc.add(s); });
+  });
   double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
-    const int t = find_tensor(l, c);
-    const int64_t begin = (c - l.first[t]) * kChunk;
-    const int64_t left = l.n[t] - begin;
-    const int n = static_cast<int>(left < kChunk ? left : kChunk);
-    const uint8_t* base = static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4);
-    const float s = square_sum<kBf16, float>(base, n);
-    // Squares of values above 1.8e19 overflow fp32: those shares again in fp64.
-    sum += isinf(s) ? square_sum<kBf16, double>(base, n) : static_cast<double>(s);
+  // Squares that may overflow fp32 (values from 1e15 on, infinities, NaN):
+  // the CTA's share again in fp64.
+  if (__syncthreads_or(!(acc.hi < 1e30f))) {
+    walk(l, [&](int t, int64_t begin, int64_t n) {
+      square_sums<kBf16, double>(static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4), n,
+                                 [&](double s) { sum += s; });
+    });
+    sum = block_sum(sum);
+  } else {
+    __shared__ float2 warp_sum[kClipThreads / 32];
+    auto warp_add = [&](int from) {
+#pragma unroll
+      for (int o = from; o > 0; o >>= 1) {
+        const float hi = __shfl_down_sync(0xFFFFFFFFu, acc.hi, o);
+        const float lo = __shfl_down_sync(0xFFFFFFFFu, acc.lo, o);
+        acc.add(hi);
+        acc.lo = __fadd_rn(acc.lo, lo);
+      }
+    };
+    warp_add(16);
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = make_float2(acc.hi, acc.lo);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const float2 w = threadIdx.x < kClipThreads / 32 ? warp_sum[threadIdx.x] : make_float2(0, 0);
+      acc.hi = w.x;
+      acc.lo = w.y;
+      warp_add(kClipThreads / 64);
+      sum = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
+    }
   }
-  sum = block_sum(sum);
   __shared__ bool is_last;
   if (threadIdx.x == 0) {
     partials[blockIdx.x] = sum;
-    __threadfence();
-    is_last = atomicAdd(ticket, 1u) == gridDim.x - 1u;
+    if (end != kLeave) {
+      __threadfence();
+      is_last = atomicAdd(ticket, 1u) == gridDim.x - 1u;
+    }
   }
+  if (end == kLeave) return;
   __syncthreads();
   if (!is_last) return;
   __threadfence();
-  double all = 0.0;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kClipThreads) all += __ldcg(partials + i);
-  all = block_sum(all);
+  double all = sum_partials(partials, gridDim.x);
   if (threadIdx.x == 0) {
     *ticket = 0u;
     if (!first) all += *total;
-    if (last)
+    if (end == kFinish)
       *norm = static_cast<float>(sqrt(all));
     else
       *total = all;
@@ -166,68 +255,76 @@ __global__ void __launch_bounds__(kClipThreads)
 }
 
 template <bool kBf16, bool kOutBf16, int kMax>
-__global__ void __launch_bounds__(kClipThreads)
-    grad_scale_kernel(const __grid_constant__ TensorList<kMax> l, const float* norm, float max_norm,
-                      float eps) {
+__global__ void __launch_bounds__(kClipThreads, 2048 / kClipThreads)
+    grad_scale_kernel(const __grid_constant__ TensorList<kMax> l, float* norm, float max_norm,
+                      float eps, const double* partials, int count) {
   griddep_wait();
   griddep_launch_dependents();
-  const float q = __fdiv_rn(max_norm, __fadd_rn(*norm, eps));
+  float length;
+  if (count > 0) {  // the norm launch left its partial sums
+    __shared__ float shared_length;
+    const double all = sum_partials(partials, count);
+    if (threadIdx.x == 0) {
+      shared_length = static_cast<float>(sqrt(all));
+      if (blockIdx.x == 0) *norm = shared_length;
+    }
+    __syncthreads();
+    length = shared_length;
+  } else {
+    length = *norm;
+  }
+  const float q = __fdiv_rn(max_norm, __fadd_rn(length, eps));
   const float coef = q > 1.0f ? 1.0f : q;  // a NaN norm makes every gradient NaN
-  constexpr int kN = Vec<kBf16>::kN;
-  for (int64_t c0 = blockIdx.x; c0 < l.chunks; c0 += gridDim.x) {
-    // From the end of the list: what the norm read last may still be in L2.
-    const int64_t c = l.chunks - 1 - c0;
-    const int t = find_tensor(l, c);
+  // A thread's vector: 16 bytes of the wider of the two types.
+  constexpr int kN = kBf16 && kOutBf16 ? 8 : 4;
+  using In = std::conditional_t<kBf16 && !kOutBf16, uint2, uint4>;
+  walk(l, [&](int t, int64_t begin, int64_t n) {
     // In place, a factor of one leaves the values as they are.
-    if (kBf16 == kOutBf16 && coef == 1.0f && l.g[t] == l.out[t]) continue;
-    const int64_t begin = (c - l.first[t]) * kChunk;
-    const int64_t left = l.n[t] - begin;
-    const int n = static_cast<int>(left < kChunk ? left : kChunk);
+    if (kBf16 == kOutBf16 && coef == 1.0f && l.g[t] == l.out[t]) return;
     const uint8_t* base = static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4);
     uint8_t* dst = static_cast<uint8_t*>(l.out[t]) + begin * (kOutBf16 ? 2 : 4);
-    int done = 0;
-    if (aligned(base) && aligned(dst)) {
-      const int vecs = n / kN;
-      const uint4* v = reinterpret_cast<const uint4*>(base);
-      for (int i0 = threadIdx.x; i0 < vecs; i0 += 4 * kClipThreads) {
-        uint4 u[4];
+    const int64_t vecs = aligned(base) && aligned(dst) ? n / kN : 0;
+    const In* v = reinterpret_cast<const In*>(base);
+    // From the end: what the norm read last is still in L2.
+    for (int64_t top = vecs; top > 0; top -= kUnroll * kClipThreads) {
+      In u[kUnroll];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (i0 + k * kClipThreads < vecs) u[k] = v[i0 + k * kClipThreads];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = i0 + k * kClipThreads;
-          if (i >= vecs) break;
-          const Vec<kBf16> x(u[k]);
-          if constexpr (kOutBf16 && kBf16) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = cvt_bf16x2(__fmul_rn(x.v[2 * j], coef), __fmul_rn(x.v[2 * j + 1], coef));
-            reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          } else if constexpr (kOutBf16) {
-            reinterpret_cast<uint2*>(dst)[i] =
-                make_uint2(cvt_bf16x2(__fmul_rn(x.v[0], coef), __fmul_rn(x.v[1], coef)),
-                           cvt_bf16x2(__fmul_rn(x.v[2], coef), __fmul_rn(x.v[3], coef)));
-          } else {
-#pragma unroll
-            for (int j = 0; j < kN / 4; ++j)
-              reinterpret_cast<float4*>(dst)[i * (kN / 4) + j] =
-                  make_float4(__fmul_rn(x.v[4 * j], coef), __fmul_rn(x.v[4 * j + 1], coef),
-                              __fmul_rn(x.v[4 * j + 2], coef), __fmul_rn(x.v[4 * j + 3], coef));
-          }
-        }
+      for (int k = 0; k < kUnroll; ++k) {
+        const int64_t i = top - 1 - k * kClipThreads - threadIdx.x;
+        if (i >= 0) u[k] = v[i];
       }
-      done = vecs * kN;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int64_t i = top - 1 - k * kClipThreads - threadIdx.x;
+        if (i < 0) break;
+        float x[kN];
+        if constexpr (kBf16) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&u[k]);
+#pragma unroll
+          for (int j = 0; j < kN / 2; ++j) mul2_rn(w[j] << 16, w[j] & 0xFFFF0000u, coef, x[2 * j], x[2 * j + 1]);
+        } else {
+          mul2_rn(u[k].x, u[k].y, coef, x[0], x[1]);
+          mul2_rn(u[k].z, u[k].w, coef, x[2], x[3]);
+        }
+        if constexpr (!kOutBf16)
+          __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[0], x[1], x[2], x[3]));
+        else if constexpr (kN == 8)
+          __stcs(reinterpret_cast<uint4*>(dst) + i,
+                 make_uint4(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3]), cvt_bf16x2(x[4], x[5]),
+                            cvt_bf16x2(x[6], x[7])));
+        else
+          __stcs(reinterpret_cast<uint2*>(dst) + i,
+                 make_uint2(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3])));
+      }
     }
-    for (int i = done + threadIdx.x; i < n; i += kClipThreads) {
+    for (int64_t i = vecs * kN + threadIdx.x; i < n; i += kClipThreads) {
       const float x = __fmul_rn(load_one<kBf16>(base, i), coef);
       if constexpr (kOutBf16)
         reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(cvt_bf16x2(x, 0.0f) & 0xFFFFu);
       else
         reinterpret_cast<float*>(dst)[i] = x;
     }
-  }
+  });
 }
 
 template <int kMax>
@@ -248,60 +345,55 @@ TensorList<kMax> make_list(const GradTensor* t, int n) {
 }
 
 unsigned clip_grid(int64_t chunks, const DeviceInfo& dev) {
-  int64_t most = 8 * int64_t(dev.num_sms);
+  int64_t most = 2048 / kClipThreads * int64_t(dev.num_sms);  // all resident at once
   if (most > kClipMaxPartials) most = kClipMaxPartials;
   const int64_t g = chunks < most ? chunks : most;
   return static_cast<unsigned>(g > 0 ? g : 1);
 }
 
 template <int kMax>
-cudaError_t norm_list(const GradTensor* t, int n, bool bf16, bool first, bool last,
-                      double* partials, double* total, uint32_t* ticket, float* norm,
-                      const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t norm_list(const GradTensor* t, int n, const GradNormArgs& a, const DeviceInfo& dev,
+                      cudaStream_t stream, int* grid_out) {
   const TensorList<kMax> l = make_list<kMax>(t, n);
   const dim3 grid(clip_grid(l.chunks, dev)), block(kClipThreads);
-  return bf16 ? launch_kernel(grad_norm_kernel<true, kMax>, grid, block, 0, stream, 1, false, l,
-                              partials, total, ticket, norm, first, last)
-              : launch_kernel(grad_norm_kernel<false, kMax>, grid, block, 0, stream, 1, false, l,
-                              partials, total, ticket, norm, first, last);
+  *grid_out = static_cast<int>(grid.x);
+  const int end = a.leave ? kLeave : a.last ? kFinish : kCarry;
+  return a.bf16 ? launch_kernel(grad_norm_kernel<true, kMax>, grid, block, 0, stream, 1, false, l,
+                                a.partials, a.total, a.ticket, a.norm, a.first, end)
+                : launch_kernel(grad_norm_kernel<false, kMax>, grid, block, 0, stream, 1, false, l,
+                                a.partials, a.total, a.ticket, a.norm, a.first, end);
 }
 
 template <int kMax>
-cudaError_t scale_list(const GradTensor* t, int n, bool bf16, bool out_bf16, const float* norm,
-                       float max_norm, float eps, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t scale_list(const GradTensor* t, int n, const GradScaleArgs& a, const DeviceInfo& dev,
+                       cudaStream_t stream) {
   const TensorList<kMax> l = make_list<kMax>(t, n);
-  if (l.chunks == 0) return cudaSuccess;
   const dim3 grid(clip_grid(l.chunks, dev)), block(kClipThreads);
-  if (bf16)
-    return out_bf16 ? launch_kernel(grad_scale_kernel<true, true, kMax>, grid, block, 0, stream, 1,
-                                    false, l, norm, max_norm, eps)
-                    : launch_kernel(grad_scale_kernel<true, false, kMax>, grid, block, 0, stream, 1,
-                                    false, l, norm, max_norm, eps);
-  return out_bf16 ? launch_kernel(grad_scale_kernel<false, true, kMax>, grid, block, 0, stream, 1,
-                                  false, l, norm, max_norm, eps)
-                  : launch_kernel(grad_scale_kernel<false, false, kMax>, grid, block, 0, stream, 1,
-                                  false, l, norm, max_norm, eps);
+  auto run = [&](auto* kernel) {
+    return launch_kernel(kernel, grid, block, 0, stream, 1, false, l, a.norm, a.max_norm, a.eps,
+                         static_cast<const double*>(a.partials), a.count);
+  };
+  if (a.bf16)
+    return a.out_bf16 ? run(grad_scale_kernel<true, true, kMax>)
+                      : run(grad_scale_kernel<true, false, kMax>);
+  return a.out_bf16 ? run(grad_scale_kernel<false, true, kMax>)
+                    : run(grad_scale_kernel<false, false, kMax>);
 }
 
 }  // namespace
 
-cudaError_t launch_grad_norm(const GradTensor* t, int n, bool bf16, bool first, bool last,
-                             double* partials, double* total, uint32_t* ticket, float* norm,
-                             const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_grad_norm(const GradTensor* t, int n, const GradNormArgs& a,
+                             const DeviceInfo& dev, cudaStream_t stream, int* grid) {
   set_error_site("grad_norm_kernel");
-  return n <= kSmallList ? norm_list<kSmallList>(t, n, bf16, first, last, partials, total, ticket,
-                                                 norm, dev, stream)
-                         : norm_list<kClipMaxTensors>(t, n, bf16, first, last, partials, total,
-                                                      ticket, norm, dev, stream);
+  return n <= kSmallList ? norm_list<kSmallList>(t, n, a, dev, stream, grid)
+                         : norm_list<kClipMaxTensors>(t, n, a, dev, stream, grid);
 }
 
-cudaError_t launch_grad_scale(const GradTensor* t, int n, bool bf16, bool out_bf16,
-                              const float* norm, float max_norm, float eps, const DeviceInfo& dev,
-                              cudaStream_t stream) {
+cudaError_t launch_grad_scale(const GradTensor* t, int n, const GradScaleArgs& a,
+                              const DeviceInfo& dev, cudaStream_t stream) {
   set_error_site("grad_scale_kernel");
-  return n <= kSmallList ? scale_list<kSmallList>(t, n, bf16, out_bf16, norm, max_norm, eps, dev, stream)
-                         : scale_list<kClipMaxTensors>(t, n, bf16, out_bf16, norm, max_norm, eps,
-                                                       dev, stream);
+  return n <= kSmallList ? scale_list<kSmallList>(t, n, a, dev, stream)
+                         : scale_list<kClipMaxTensors>(t, n, a, dev, stream);
 }
 
 }  // namespace fp8lin

@@ -364,21 +364,36 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStr
 // ---- gradient norm and clipping (grad_clip.cu)
 
 constexpr int kClipMaxTensors = 384;   // of one launch
-constexpr int kClipMaxPartials = kMaxPartials / 2;
+constexpr int kClipMaxPartials = 1024;  // CTAs of a norm launch; doubles at kWsPartialOffset
+static_assert(kClipMaxPartials * sizeof(double) <= kMaxPartials * sizeof(uint32_t), "partials");
 struct GradTensor {
   const void* g;
   void* out;
   int64_t n;
 };
-// The 2-norm of the tensors of one or several launches: each launch sums its
-// CTAs' partial sums in a fixed order into *total (first: from 0), and the
-// last writes sqrt(*total) to norm.
-cudaError_t launch_grad_norm(const GradTensor* t, int n, bool bf16, bool first, bool last,
-                             double* partials, double* total, uint32_t* ticket, float* norm,
-                             const DeviceInfo& dev, cudaStream_t stream);
-// out = g * min(1, max_norm / (norm + eps)).
-cudaError_t launch_grad_scale(const GradTensor* t, int n, bool bf16, bool out_bf16,
-                              const float* norm, float max_norm, float eps, const DeviceInfo& dev,
-                              cudaStream_t stream);
+// The 2-norm of the tensors of one or several launches: each launch adds its
+// CTAs' partial sums in a fixed order to *total (first: from 0), and the last
+// writes the root to norm.  leave: the partial sums (*grid of them) stay for
+// the scaling to add up.
+struct GradNormArgs {
+  bool bf16, first, last, leave;
+  double* partials;
+  double* total;
+  uint32_t* ticket;
+  float* norm;
+};
+cudaError_t launch_grad_norm(const GradTensor* t, int n, const GradNormArgs& a,
+                             const DeviceInfo& dev, cudaStream_t stream, int* grid);
+// out = g * min(1, max_norm / (norm + eps)); count > 0: the norm is that of
+// `count` partial sums, and is written to norm.
+struct GradScaleArgs {
+  bool bf16, out_bf16;
+  float* norm;
+  float max_norm, eps;
+  const double* partials;
+  int count;
+};
+cudaError_t launch_grad_scale(const GradTensor* t, int n, const GradScaleArgs& a,
+                              const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace fp8lin
