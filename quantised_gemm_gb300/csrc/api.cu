@@ -1297,11 +1297,10 @@ fp8lin_status fp8lin_fp4_dequantise(const fp8lin_fp4_tensor* t, void* out, int64
   if (t->rows == 0 || t->cols == 0) return FP8LIN_OK;
   if (out == nullptr || (reinterpret_cast<uintptr_t>(out) & (f32 ? 3u : 1u)) != 0 || ldo < t->cols)
     return FP8LIN_EINVAL;
-  DeviceInfo dev;
-  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  if (((t->rows + 31) / 32) > kFp4MaxDim / ((t->cols + 127) / 128)) return FP8LIN_EUNSUPPORTED;
   ProfScope ps(FP8LIN_PROF_CAST, stream);
   cudaError_t e = launch_fp4_dequantise(fp4_view(t), t->fmt, t->inv_scale, t->rows, t->cols, out,
-                                        ldo, f32 != 0, dev, stream);
+                                        ldo, f32 != 0, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 

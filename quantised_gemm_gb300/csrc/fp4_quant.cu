@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -29,18 +30,28 @@ namespace {
 
 constexpr int kQThreads = 256;
 constexpr int kQTile = 128;       // tile: 128 rows x 128 columns
-constexpr int kPitch = 66;        // words of a shared bf16 tile row (64 used)
-constexpr int kOutPitch = 80;     // bytes of a staged row of transposed codes (64 used)
+constexpr int kPitch = 68;        // words of a shared bf16 tile row (64 used)
 
-// Two fp32 -> two e2m1 codes in a byte (round to nearest even, saturating);
-// lo in the low half.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "mov.b16 %0, {b, 0};\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
+// Eight fp32 -> eight e2m1 codes (round to nearest even, saturating), v[0] in
+// the lowest four bits.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// The larger magnitude of two bf16 pairs, each half with a sign that means
+// nothing; a NaN wins.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -85,14 +96,14 @@ __device__ __forceinline__ float fp4_tensor_scale(float amax, float eps) {
 }
 
 // Scale code and multiplier of one block from its maximum magnitude (bf16
-// bits).  s: the tensorwise scale, s6 = fl32(6 s) (NVFP4 only).
+// bits).  NVFP4: s is the tensorwise scale, and table holds the 128
+// multipliers fl32(fl32(6 s) / c).
 template <int kFmt>
-__device__ __forceinline__ uint32_t block_scale(uint32_t max_bits, float s, float s6, float& r) {
+__device__ __forceinline__ uint32_t block_scale(uint32_t max_bits, float s, const float* table,
+                                                float& r) {
   if constexpr (kFmt == 0) {
-    const float b = __uint_as_float(max_bits << 16);
-    const uint32_t c = cvt_fp8x2<0>(__fmul_rn(b, s), 0.0f) & 0xFFu;
-    const float cf = e4m3_to_f32(c);
-    r = c == 0 ? 0.0f : __fdiv_rn(s6, cf);
+    const uint32_t c = cvt_fp8x2<0>(__fmul_rn(__uint_as_float(max_bits << 16), s), 0.0f) & 0xFFu;
+    r = table[c];
     return c;
   } else {
     const uint32_t e = max_bits >> 7;  // the sign bit is masked off
@@ -103,11 +114,15 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t max_bits, float s, floa
   }
 }
 
+// How a tensor's rows lie: every 16 values 32-byte aligned, 16-byte aligned,
+// or neither.
+enum RowAlign : int { kScalar = 0, kAlign16 = 1, kAlign32 = 2 };
+
 // Eight values of a row as bf16 pairs: one 16-byte load, or element by
 // element where the row ends inside it or the rows are not 16-byte aligned.
-template <bool kVec>
+template <int kAlign>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t col, int64_t cols) {
-  if (kVec && col + 8 <= cols) return ld_stream_v4(row + col);
+  if (kAlign != kScalar && col + 8 <= cols) return ld_stream_v4(row + col);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -115,21 +130,59 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t col, int64_t
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint32_t absmax8(uint32_t m, const uint4& v) {
-  m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
-  return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+// Sixteen values of a row (zero past its end): whole 32-byte sectors with one
+// load where they are aligned.
+template <int kAlign>
+__device__ __forceinline__ void load16(const uint16_t* row, int64_t col, int64_t cols,
+                                       uint4 (&v)[2]) {
+  if (kAlign == kAlign32 && col + 16 <= cols) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                   "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                 : "l"(row + col));
+    return;
+  }
+  v[0] = v[1] = make_uint4(0, 0, 0, 0);
+  if (col < cols) v[0] = load8<kAlign>(row, col, cols);
+  if (col + 8 < cols) v[1] = load8<kAlign>(row, col + 8, cols);
 }
 
-__device__ __forceinline__ uint32_t code2(uint32_t pair, float r) {
-  float lo, hi;
-  mul2_rn(pair << 16, pair & 0xFFFF0000u, r, lo, hi);
-  return cvt_e2m1x2(lo, hi);
+// Thirty-two aligned bytes in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t max8(const uint4& v) {
+  return max_magnitude(max_magnitude(v.x, v.y), max_magnitude(v.z, v.w));
+}
+
+// The magnitude bits of the larger half of a pair.
+__device__ __forceinline__ uint32_t larger_half(uint32_t pair) {
+  return max(pair & 0x7FFFu, (pair >> 16) & 0x7FFFu);
 }
 
 __device__ __forceinline__ uint32_t code8(const uint4& v, float r) {
-  return code2(v.x, r) | (code2(v.y, r) << 8) | (code2(v.z, r) << 16) | (code2(v.w, r) << 24);
+  float f[8];
+  mul2_rn(v.x << 16, v.x & 0xFFFF0000u, r, f[0], f[1]);
+  mul2_rn(v.y << 16, v.y & 0xFFFF0000u, r, f[2], f[3]);
+  mul2_rn(v.z << 16, v.z & 0xFFFF0000u, r, f[4], f[5]);
+  mul2_rn(v.w << 16, v.w & 0xFFFF0000u, r, f[6], f[7]);
+  return cvt_e2m1x8(f);
+}
+
+// Eight values, one from each word: its low or its high half.
+template <int kHalf>
+__device__ __forceinline__ uint32_t code8_of(const uint32_t* w, float r) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t a = kHalf == 0 ? w[2 * j] << 16 : w[2 * j] & 0xFFFF0000u;
+    const uint32_t b = kHalf == 0 ? w[2 * j + 1] << 16 : w[2 * j + 1] & 0xFFFF0000u;
+    mul2_rn(a, b, r, f[2 * j], f[2 * j + 1]);
+  }
+  return cvt_e2m1x8(f);
 }
 
 // The tensor's amax joins a maximum over the CTAs; the last one publishes it
@@ -145,10 +198,10 @@ __device__ __forceinline__ void join_amax(uint32_t bits, uint32_t* acc, uint32_t
   }
 }
 
-// Block-wide maximum of per-thread magnitude pairs, as fp32 bits in thread 0.
-__device__ __forceinline__ uint32_t block_max_bits(uint32_t pair) {
+// Block-wide maximum of per-thread magnitudes, as fp32 bits in thread 0.
+__device__ __forceinline__ uint32_t block_max_bits(uint32_t bits) {
   __shared__ uint32_t red[kQThreads / 32];
-  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(pair & 0xFFFFu, pair >> 16));
+  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bits);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   uint32_t all = 0;
@@ -181,28 +234,22 @@ struct QuantParams {
 // an element and copy.  Each thread holds 16 consecutive values of four rows
 // (rows 32 apart, so that its scale bytes are 16 consecutive bytes of a scale
 // tile); the transposed copy reads the tile again from shared memory, 32 rows
-// x 2 columns a thread, and stages its codes so that they leave 64 bytes a row.
-template <int kFmt, bool kTrans, bool kVec>
+// x 2 columns a thread, and stages its codes so that they leave 64 bytes a
+// row.  Shared rows are 16 bytes longer than the tile's, and the halves of
+// 32 bytes and the staged chunks are permuted, so that no access conflicts.
+template <int kFmt, bool kTrans, int kAlign>
 __global__ void __launch_bounds__(kQThreads) fp4_quantise_kernel(const QuantParams p) {
   constexpr int kBlock = kFmt == 0 ? 16 : 32;
   constexpr int kTileBlocks = 4 * kBlock;  // columns of one 512-byte scale tile
   __shared__ __align__(16) uint32_t tile[kTrans ? kQTile * kPitch : 1];
-  __shared__ __align__(16) uint8_t stage[kTrans ? kQTile * kOutPitch : 16];
+  __shared__ __align__(16) uint8_t stage[kTrans ? kQTile * 64 : 16];
   __shared__ __align__(16) uint8_t sc_stage[kTrans ? 1024 : 16];
+  __shared__ float table[kFmt == 0 ? 128 : 1];
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
   const int64_t row0 = tr * kQTile, col0 = tc * kQTile;
-  float s = 0.0f, s6 = 0.0f;
-  if constexpr (kFmt == 0) {
-    s = p.amax_in != nullptr ? fp4_tensor_scale(*p.amax_in, p.eps) : *p.scale_in;
-    s6 = __fmul_rn(6.0f, s);
-    if (p.scale_out != nullptr && blockIdx.x == 0 && tid == 0) {
-      *p.scale_out = s;
-      *p.inv_out = __fdiv_rn(1.0f, s);
-    }
-  }
   const int b = lane & 7;                    // 16-column group of the tile
   const int rr = warp * 4 + (lane >> 3);     // row modulo 32
   const int64_t col = col0 + b * 16;
@@ -211,34 +258,38 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantise_kernel(const QuantPara
   for (int i = 0; i < 4; ++i) {
     const int64_t row = row0 + rr + 32 * i;
     v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-    if (row < p.rows) {
-      const uint16_t* src = p.x + row * p.ld;
-      if (col < p.cols) v[i][0] = load8<kVec>(src, col, p.cols);
-      if (col + 8 < p.cols) v[i][1] = load8<kVec>(src, col + 8, p.cols);
+    if (row < p.rows) load16<kAlign>(p.x + row * p.ld, col, p.cols, v[i]);
+  }
+  float s = 0.0f;
+  if constexpr (kFmt == 0) {
+    s = p.amax_in != nullptr ? fp4_tensor_scale(*p.amax_in, p.eps) : *p.scale_in;
+    if (tid < 128)
+      table[tid] = tid == 0 ? 0.0f : __fdiv_rn(__fmul_rn(6.0f, s), e4m3_to_f32(tid));
+    if (p.scale_out != nullptr && blockIdx.x == 0 && tid == 0) {
+      *p.scale_out = s;
+      *p.inv_out = __fdiv_rn(1.0f, s);
     }
   }
   if constexpr (kTrans) {
+    const int flip = b >> 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t* dst = tile + (rr + 32 * i) * kPitch + b * 8;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<uint2*>(dst + 4 * h) = make_uint2(v[i][h].x, v[i][h].y);
-        *reinterpret_cast<uint2*>(dst + 4 * h + 2) = make_uint2(v[i][h].z, v[i][h].w);
-      }
+      *reinterpret_cast<uint4*>(dst + 4 * flip) = flip ? v[i][1] : v[i][0];
+      *reinterpret_cast<uint4*>(dst + 4 * (flip ^ 1)) = flip ? v[i][0] : v[i][1];
     }
   }
+  if constexpr (kTrans || kFmt == 0) __syncthreads();
   uint32_t all = 0;
   uint32_t word[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t m2 = absmax8(absmax8(0, v[i][0]), v[i][1]);
-    if (p.amax_rec != nullptr) all = __vmaxu2(all, m2);
+    uint32_t m = larger_half(max_magnitude(max8(v[i][0]), max8(v[i][1])));
+    all = max(all, m);
     if (p.codes == nullptr) continue;  // uniform
-    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
     if constexpr (kFmt == 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     float r;
-    const uint32_t c = block_scale<kFmt>(m, s, s6, r);
+    const uint32_t c = block_scale<kFmt>(m, s, table, r);
     const int64_t row = row0 + rr + 32 * i;
     if (row < p.rows && col < ((p.cols + 31) & ~int64_t(31)))
       *reinterpret_cast<uint2*>(p.codes + row * p.ld4 + (col >> 1)) =
@@ -260,44 +311,39 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantise_kernel(const QuantPara
           make_uint4(word[0], word[1], word[2], word[3]);
   }
   if constexpr (kTrans) {
-    __syncthreads();
     const int pair = lane + 32 * (warp & 1);  // columns 2 pair, 2 pair + 1
     const int rg = warp >> 1;                 // rows 32 rg .. 32 rg + 31
     const uint32_t* src = tile + (rg * 32) * kPitch + pair;
     uint32_t w[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) w[j] = src[j * kPitch];
-    uint32_t m2[2] = {0, 0};
+    uint32_t m2[2] = {w[0], w[16]};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) m2[j >> 4] = __vmaxu2(m2[j >> 4], w[j] & 0x7FFF7FFFu);
-    if constexpr (kFmt == 1) m2[0] = m2[1] = __vmaxu2(m2[0], m2[1]);
+    for (int j = 1; j < 16; ++j) {
+      m2[0] = max_magnitude(m2[0], w[j]);
+      m2[1] = max_magnitude(m2[1], w[16 + j]);
+    }
+    if constexpr (kFmt == 1) m2[0] = m2[1] = max_magnitude(m2[0], m2[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // the low column, then the high one
       uint32_t out[4];
       const int c = 2 * pair + h;
+      float r = 0.0f;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {  // 16 rows each
-        const uint32_t m = h == 0 ? m2[g] & 0xFFFFu : m2[g] >> 16;
-        float r;
-        const uint32_t sc = block_scale<kFmt>(m, s, s6, r);
-        // transposed tile: row c, block 2 rg + g (NVFP4) or rg (MXFP4)
-        const int blk = kFmt == 0 ? 2 * rg + g : rg;
-        if (kFmt == 0 || g == 0)
+        if (kFmt == 0 || g == 0) {
+          const uint32_t sc = block_scale<kFmt>((h == 0 ? m2[g] : m2[g] >> 16) & 0x7FFFu, s, table, r);
+          // transposed tile: row c, block 2 rg + g (NVFP4) or rg (MXFP4)
+          const int blk = kFmt == 0 ? 2 * rg + g : rg;
           sc_stage[(blk >> 2) * 512 + (c & 31) * 16 + (c >> 5) * 4 + (blk & 3)] =
               static_cast<uint8_t>(sc);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t word8 = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a = w[16 * g + 8 * q + 2 * j], d = w[16 * g + 8 * q + 2 * j + 1];
-            // rows 2j and 2j + 1 of this column side by side
-            word8 |= code2(__byte_perm(a, d, h == 0 ? 0x5410 : 0x7632), r) << (8 * j);
-          }
-          out[2 * g + q] = word8;
         }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          out[2 * g + q] = h == 0 ? code8_of<0>(w + 16 * g + 8 * q, r)
+                                  : code8_of<1>(w + 16 * g + 8 * q, r);
       }
-      *reinterpret_cast<uint4*>(stage + c * kOutPitch + rg * 16) =
+      *reinterpret_cast<uint4*>(stage + pair * 128 + (((h * 4 + rg) ^ (pair & 7)) << 4)) =
           make_uint4(out[0], out[1], out[2], out[3]);
     }
     __syncthreads();
@@ -308,7 +354,8 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantise_kernel(const QuantPara
       const int64_t byte = (row0 >> 1) + chunk * 16;
       if (col0 + c < p.cols && byte < code_bytes)
         *reinterpret_cast<uint4*>(p.codes_t + (col0 + c) * p.ld4_t + byte) =
-            *reinterpret_cast<const uint4*>(stage + c * kOutPitch + chunk * 16);
+            *reinterpret_cast<const uint4*>(
+                stage + (c >> 1) * 128 + ((((c & 1) * 4 + chunk) ^ ((c >> 1) & 7)) << 4));
     }
     constexpr int kScTiles = kFmt == 0 ? 2 : 1;
     if (tid < 32 * kScTiles) {
@@ -341,60 +388,82 @@ __global__ void __launch_bounds__(kQThreads)
   if (threadIdx.x == 0) join_amax(bits, acc, ticket, out, gridDim.x);
 }
 
-// Codes back to values: 16 values a thread.
-template <int kFmt, typename Out, bool kVec>
+// 2^(code - 127) of an MXFP4 scale: 0 is the subnormal 2^-127, 255 a NaN.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t code) {
+  return __uint_as_float(code == 0 ? 0x00400000u : code == 255 ? 0x7FC00000u : code << 23);
+}
+
+template <int kAlign>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8]) {
+  if constexpr (kAlign == kAlign32) {
+    store32(p, w);
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Codes back to values: a 128 x 128 tile a CTA, 16 values of four rows a
+// thread, whose scales are one 16-byte load.
+template <int kFmt, typename Out, int kAlign>
 __global__ void __launch_bounds__(kQThreads)
     fp4_dequantise_kernel(const uint8_t* codes, const uint8_t* scales, const float* inv,
-                          int64_t rows, int64_t cols, int64_t ld4, Out* out, int64_t ldo) {
+                          int64_t rows, int64_t cols, int64_t ld4, Out* out, int64_t ldo,
+                          int64_t tiles_c) {
   constexpr int kBlock = kFmt == 0 ? 16 : 32;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t groups = (cols + 15) >> 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const int b = lane & 7, rr = warp * 4 + (lane >> 3);
+  const int64_t col = tc * kQTile + b * 16;
+  if (col >= cols) return;
   const int64_t ktiles = ((cols + kBlock - 1) / kBlock + 3) >> 2;
+  const uint4 sc = *reinterpret_cast<const uint4*>(
+      scales + (tr * ktiles + col / (4 * kBlock)) * 512 + rr * 16);
+  const int shift = 8 * (kFmt == 0 ? b & 3 : b >> 1);
+  uint2 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = tr * kQTile + rr + 32 * i;
+    q[i] = row < rows ? *reinterpret_cast<const uint2*>(codes + row * ld4 + (col >> 1))
+                      : make_uint2(0, 0);
+  }
   const float d = kFmt == 0 ? __fdiv_rn(*inv, 6.0f) : 1.0f;
-  const int64_t total = rows * groups;
-  for (int64_t i = blockIdx.x * int64_t(kQThreads) + threadIdx.x; i < total;
-       i += int64_t(gridDim.x) * kQThreads) {
-    const int64_t row = i / groups, g = i - row * groups;
-    const int64_t blk = g * 16 / kBlock;
-    const uint32_t code = scales[((row >> 7) * ktiles + (blk >> 2)) * 512 + (row & 31) * 16 +
-                                 ((row >> 5) & 3) * 4 + (blk & 3)];
-    float c;
-    if constexpr (kFmt == 0)
-      c = e4m3_to_f32(code);
-    else  // 2^(code - 127): 0 is the subnormal 2^-127, 255 a NaN
-      c = code == 0 ? __uint_as_float(0x00400000u)
-                    : __uint_as_float(code == 255 ? 0x7FC00000u : code << 23);
-    const uint2 q = *reinterpret_cast<const uint2*>(codes + row * ld4 + g * 8);
+  const uint32_t words[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = tr * kQTile + rr + 32 * i;
+    if (row >= rows) break;
+    const uint32_t code = (words[i] >> shift) & 0xFFu;
+    const float c = kFmt == 0 ? e4m3_to_f32(code) : e8m0_to_f32(code);
     float v[16];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 f = f16x2_to_f32x2(cvt_f16x2_e2m1x2(((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 0xFFu));
-      v[2 * j] = __fmul_rn(f.x, c);
-      v[2 * j + 1] = __fmul_rn(f.y, c);
-      if constexpr (kFmt == 0) {
-        v[2 * j] = __fmul_rn(v[2 * j], d);
-        v[2 * j + 1] = __fmul_rn(v[2 * j + 1], d);
-      }
+      const float2 f = f16x2_to_f32x2(
+          cvt_f16x2_e2m1x2(((j < 4 ? q[i].x : q[i].y) >> (8 * (j & 3))) & 0xFFu));
+      mul2_rn(__float_as_uint(f.x), __float_as_uint(f.y), c, v[2 * j], v[2 * j + 1]);
+      if constexpr (kFmt == 0)
+        mul2_rn(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), d, v[2 * j], v[2 * j + 1]);
     }
-    Out* dst = out + row * ldo + g * 16;
-    if (kVec && g * 16 + 16 <= cols) {
+    Out* dst = out + row * ldo + col;
+    if (col + 16 <= cols) {
       if constexpr (sizeof(Out) == 4) {
+        uint32_t w[2][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          reinterpret_cast<float4*>(dst)[j] =
-              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < 16; ++j) w[j >> 3][j & 7] = __float_as_uint(v[j]);
+        store_words<kAlign>(dst, w[0]);
+        store_words<kAlign>(dst + 8, w[1]);
       } else {
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          reinterpret_cast<uint4*>(dst)[j] = make_uint4(
-              cvt_bf16x2(v[8 * j], v[8 * j + 1]), cvt_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-              cvt_bf16x2(v[8 * j + 4], v[8 * j + 5]), cvt_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+        for (int j = 0; j < 8; ++j) w[j] = cvt_bf16x2(v[2 * j], v[2 * j + 1]);
+        store_words<kAlign>(dst, w);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        if (g * 16 + j < cols) {
+        if (col + j < cols) {
           if constexpr (sizeof(Out) == 4)
             dst[j] = v[j];
           else
@@ -404,16 +473,56 @@ __global__ void __launch_bounds__(kQThreads)
   }
 }
 
-template <int kFmt, bool kTrans>
-cudaError_t launch_quant(const QuantParams& p, unsigned grid, bool vec, cudaStream_t stream) {
-  return vec ? launch_kernel(fp4_quantise_kernel<kFmt, kTrans, true>, dim3(grid), dim3(kQThreads), 0,
-                             stream, 1, false, p)
-             : launch_kernel(fp4_quantise_kernel<kFmt, kTrans, false>, dim3(grid), dim3(kQThreads),
-                             0, stream, 1, false, p);
+// The same for rows that are not 16-byte aligned: consecutive lanes write
+// consecutive values, 32 rows a CTA.
+template <int kFmt, typename Out>
+__global__ void __launch_bounds__(kQThreads)
+    fp4_dequantise_ragged_kernel(const uint8_t* codes, const uint8_t* scales, const float* inv,
+                                 int64_t rows, int64_t cols, int64_t ld4, Out* out, int64_t ldo,
+                                 int64_t tiles_c) {
+  constexpr int kBlock = kFmt == 0 ? 16 : 32;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const int64_t ktiles = ((cols + kBlock - 1) / kBlock + 3) >> 2;
+  const float d = kFmt == 0 ? __fdiv_rn(*inv, 6.0f) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = warp + 8 * i;
+    const int64_t row = tr * 32 + r;
+    if (row >= rows) break;
+    const uint8_t* row_scales = scales + (tr >> 2) * ktiles * 512 + r * 16 + (tr & 3) * 4;
+#pragma unroll
+    for (int j = 0; j < kQTile / 32; ++j) {
+      const int64_t col = tc * kQTile + 32 * j + lane;
+      if (col >= cols) continue;
+      const int64_t blk = col / kBlock;
+      const uint32_t code = row_scales[(blk >> 2) * 512 + (blk & 3)];
+      const uint32_t q = codes[row * ld4 + (col >> 1)];
+      const float2 f = f16x2_to_f32x2(cvt_f16x2_e2m1x2(q));
+      float v = __fmul_rn((col & 1) != 0 ? f.y : f.x,
+                          kFmt == 0 ? e4m3_to_f32(code) : e8m0_to_f32(code));
+      if constexpr (kFmt == 0) v = __fmul_rn(v, d);
+      if constexpr (sizeof(Out) == 4)
+        out[row * ldo + col] = v;
+      else
+        out[row * ldo + col] = static_cast<Out>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+    }
+  }
 }
 
-bool rows_vectorised(const void* p, int64_t ld, int elem) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * elem) % 16 == 0;
+template <int kFmt, bool kTrans>
+cudaError_t launch_quant(const QuantParams& p, unsigned grid, int align, cudaStream_t stream) {
+  auto* kernel = align == kAlign32   ? fp4_quantise_kernel<kFmt, kTrans, kAlign32>
+                 : align == kAlign16 ? fp4_quantise_kernel<kFmt, kTrans, kAlign16>
+                                     : fp4_quantise_kernel<kFmt, kTrans, kScalar>;
+  return launch_kernel(kernel, dim3(grid), dim3(kQThreads), 0, stream, 1, false, p);
+}
+
+int row_align(const void* p, int64_t ld, int elem) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * elem);
+  return (bits & 31u) == 0 ? kAlign32 : (bits & 15u) == 0 ? kAlign16 : kScalar;
 }
 
 }  // namespace
@@ -450,7 +559,8 @@ cudaError_t launch_fp4_quantise(const Fp4QuantArgs& a, cudaStream_t stream) {
   p.ld4_t = a.out_t.ld;
   p.tiles_c = (a.cols + kQTile - 1) / kQTile;
   const int64_t grid = (a.rows + kQTile - 1) / kQTile * p.tiles_c;
-  const bool vec = rows_vectorised(a.x, a.ld, 2), trans = a.out_t.codes != nullptr;
+  const int vec = row_align(a.x, a.ld, 2);
+  const bool trans = a.out_t.codes != nullptr;
   set_error_site("fp4_quantise_kernel");
   const unsigned g = static_cast<unsigned>(grid);
   if (a.fmt == 0)
@@ -460,23 +570,26 @@ cudaError_t launch_fp4_quantise(const Fp4QuantArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_fp4_dequantise(const Fp4View& t, int fmt, const float* inv, int64_t rows,
                                   int64_t cols, void* out, int64_t ldo, bool f32,
-                                  const DeviceInfo& dev, cudaStream_t stream) {
-  const int64_t want = (rows * ((cols + 15) / 16) + kQThreads - 1) / kQThreads;
-  const int64_t most = 16 * int64_t(dev.num_sms);
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(kQThreads);
-  const bool vec = rows_vectorised(out, ldo, f32 ? 4 : 2);
+                                  cudaStream_t stream) {
+  const int64_t tiles_c = (cols + kQTile - 1) / kQTile;
+  const int align = row_align(out, ldo, f32 ? 4 : 2);
+  const int64_t tile_rows = align == kScalar ? 32 : kQTile;
+  const dim3 grid(static_cast<unsigned>((rows + tile_rows - 1) / tile_rows * tiles_c));
   set_error_site("fp4_dequantise_kernel");
-#define FP8LIN_DEQUANT(FMT, OUT, VEC)                                                            \
-  launch_kernel(fp4_dequantise_kernel<FMT, OUT, VEC>, grid, block, 0, stream, 1, false,          \
-                static_cast<const uint8_t*>(t.codes), static_cast<const uint8_t*>(t.scales), inv, \
-                rows, cols, t.ld, static_cast<OUT*>(out), ldo)
-  if (fmt == 0) {
-    if (f32) return vec ? FP8LIN_DEQUANT(0, float, true) : FP8LIN_DEQUANT(0, float, false);
-    return vec ? FP8LIN_DEQUANT(0, uint16_t, true) : FP8LIN_DEQUANT(0, uint16_t, false);
-  }
-  if (f32) return vec ? FP8LIN_DEQUANT(1, float, true) : FP8LIN_DEQUANT(1, float, false);
-  return vec ? FP8LIN_DEQUANT(1, uint16_t, true) : FP8LIN_DEQUANT(1, uint16_t, false);
-#undef FP8LIN_DEQUANT
+  auto run = [&](auto* scalar, auto* align16, auto* align32, auto* dst) {
+    auto* kernel = align == kAlign32 ? align32 : align == kAlign16 ? align16 : scalar;
+    return launch_kernel(kernel, grid, dim3(kQThreads), 0, stream, 1, false,
+                         static_cast<const uint8_t*>(t.codes), static_cast<const uint8_t*>(t.scales),
+                         inv, rows, cols, t.ld, dst, ldo, tiles_c);
+  };
+  auto run_type = [&](auto* dst) {
+    using Out = std::remove_pointer_t<decltype(dst)>;
+    return fmt == 0 ? run(fp4_dequantise_ragged_kernel<0, Out>, fp4_dequantise_kernel<0, Out, kAlign16>,
+                          fp4_dequantise_kernel<0, Out, kAlign32>, dst)
+                    : run(fp4_dequantise_ragged_kernel<1, Out>, fp4_dequantise_kernel<1, Out, kAlign16>,
+                          fp4_dequantise_kernel<1, Out, kAlign32>, dst);
+  };
+  return f32 ? run_type(static_cast<float*>(out)) : run_type(static_cast<uint16_t*>(out));
 }
 
 }  // namespace fp8lin

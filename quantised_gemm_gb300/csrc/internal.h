@@ -344,7 +344,7 @@ cudaError_t launch_fp4_amax(const uint16_t* x, int64_t rows, int64_t cols, int64
                             cudaStream_t stream);
 cudaError_t launch_fp4_dequantise(const Fp4View& t, int fmt, const float* inv, int64_t rows,
                                   int64_t cols, void* out, int64_t ldo, bool f32,
-                                  const DeviceInfo& dev, cudaStream_t stream);
+                                  cudaStream_t stream);
 
 // D [M, N] = A [M, K] . B [N, K]^T, both in the same 4-bit format, fp32
 // accumulation; bf16 D of any row stride and 2-byte alignment.
