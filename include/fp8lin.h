@@ -511,8 +511,9 @@ size_t fp8lin_fp4_scale_bytes(int64_t rows, int64_t cols, int32_t fmt);
  * columns: the copy a backward contracts over) or both; one of them may be
  * NULL.  Both must have the same fmt.
  * st: NVFP4, an e4m3 scaling state whose inv_scale is the inv_scale of out and
- * out_t.  Dynamic: the amax of x is computed (amax_algo; PRECOMPUTED takes
- * *st->amax as it is), then S and inv are written.  Delayed: S is *st->scale,
+ * out_t.  Dynamic: the amax of x is computed (PRECOMPUTED takes *st->amax as
+ * it is; the other amax_algo values give the same bits, in one launch or two
+ * as the size has it), then S and inv are written.  Delayed: S is *st->scale,
  * the amax is recorded in the same pass (amax init first while needs_init is
  * set), as in fp8lin_cast_delayed.  MXFP4: NULL.
  * An empty tensor leaves the state as an amax of 0 does.  EINVAL where out's

@@ -1157,72 +1157,116 @@ fp8lin_status check_quantise(const void* x, int64_t rows, int64_t cols, int64_t 
   if (rows > 0 && cols > 0) {
     if (x == nullptr || (reinterpret_cast<uintptr_t>(x) & 1u) != 0 || ld < cols)
       return FP8LIN_EINVAL;
-    if (((rows + 127) / 128) > kFp4MaxDim / ((cols + 127) / 128)) return FP8LIN_EUNSUPPORTED;
+    // Half a launch's CTAs: two tensors may share one.
+    if (((rows + 127) / 128) > kFp4MaxDim / 2 / ((cols + 127) / 128)) return FP8LIN_EUNSUPPORTED;
   }
   return FP8LIN_OK;
 }
 
-// amax of a tensor that need not have whole aligned vectors.
-fp8lin_status fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t ld, float* amax,
-                       int32_t algo, void* ws, const DeviceInfo& dev, cudaStream_t stream) {
-  if (rows == 0 || cols == 0 || check_bf16(x, rows, cols, ld) == FP8LIN_OK)
-    return do_amax(x, rows, cols, ld, amax,
-                   algo == FP8LIN_AMAX_REDUCTION ? algo : int32_t(FP8LIN_AMAX_ATOMIC), ws, dev,
-                   stream);
-  ProfScope ps(FP8LIN_PROF_AMAX, stream);
-  cudaError_t e = launch_fp4_amax(static_cast<const uint16_t*>(x), rows, cols, ld,
-                                  ws_u32(ws, kWsAtomicAccOffset), ws_u32(ws, kWsAtomicTicketOffset),
-                                  reinterpret_cast<uint32_t*>(amax), dev, stream);
+// One tensor's quantisation.
+struct QuantJob {
+  const void* x;
+  int64_t rows, cols, ld;
+  fp8lin_scaling_state* st;
+  const fp8lin_fp4_tensor* out;
+  const fp8lin_fp4_tensor* out_t;
+};
+
+bool empty_job(const QuantJob& j) { return j.rows == 0 || j.cols == 0; }
+
+// An empty tensor's state: as an amax of 0 leaves it.
+fp8lin_status quantise_empty(const QuantJob& j, cudaStream_t stream) {
+  if (j.st == nullptr) return FP8LIN_OK;
+  cudaError_t e = cudaSuccess;
+  const bool delayed = j.st->kind == FP8LIN_DELAYED;
+  if (delayed || j.st->amax_algo != FP8LIN_AMAX_PRECOMPUTED)
+    e = cudaMemsetAsync(j.st->amax, 0, sizeof(float), stream);
+  if (e == cudaSuccess && (!delayed || j.st->needs_init)) {
+    ProfScope ps(FP8LIN_PROF_SCALE, stream);
+    e = launch_scale(j.st->amax, j.st->scale, j.st->inv_scale, nullptr, nullptr, 1, false,
+                     j.st->fmt, j.st->eps, stream);
+    j.st->needs_init = 0;
+  }
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 
-fp8lin_status run_quantise(const void* x, int64_t rows, int64_t cols, int64_t ld,
-                           fp8lin_scaling_state* st, const fp8lin_fp4_tensor* out,
-                           const fp8lin_fp4_tensor* out_t, void* ws, const DeviceInfo& dev,
-                           cudaStream_t stream) {
-  const bool empty = rows == 0 || cols == 0;
+Fp4QuantArgs quant_args(const QuantJob& j, void* ws) {
   Fp4QuantArgs q;
-  q.x = static_cast<const uint16_t*>(x);
-  q.rows = rows;
-  q.cols = cols;
-  q.ld = ld;
-  q.fmt = (out != nullptr ? out : out_t)->fmt;
-  q.out = fp4_view(out);
-  q.out_t = fp4_view(out_t);
-  if (st != nullptr) {
-    q.eps = st->eps;
-    const bool delayed = st->kind == FP8LIN_DELAYED;
-    const bool init = delayed && st->needs_init;
-    if (init || (!delayed && st->amax_algo != FP8LIN_AMAX_PRECOMPUTED)) {
-      fp8lin_status s = fp4_amax(x, rows, cols, ld, st->amax, st->amax_algo, ws, dev, stream);
-      if (s != FP8LIN_OK) return s;
+  q.x = static_cast<const uint16_t*>(j.x);
+  q.rows = j.rows;
+  q.cols = j.cols;
+  q.ld = j.ld;
+  q.fmt = (j.out != nullptr ? j.out : j.out_t)->fmt;
+  q.out = fp4_view(j.out);
+  q.out_t = fp4_view(j.out_t);
+  if (j.st == nullptr) return q;
+  q.eps = j.st->eps;
+  if (j.st->kind == FP8LIN_DELAYED && !j.st->needs_init) {
+    q.scale_in = j.st->scale;
+    q.amax_rec = reinterpret_cast<uint32_t*>(j.st->amax);
+    q.rec_acc = ws_u32(ws, kWsAtomicAccOffset);
+    q.rec_ticket = ws_u32(ws, kWsAtomicTicketOffset);
+    return q;
+  }
+  // Dynamic scaling, and delayed scaling's first step.
+  q.scale_out = j.st->scale;
+  q.inv_out = j.st->inv_scale;
+  if (j.st->kind == FP8LIN_DYNAMIC && j.st->amax_algo == FP8LIN_AMAX_PRECOMPUTED) {
+    q.amax_in = j.st->amax;
+  } else {
+    q.find_amax = true;
+    q.amax_out = j.st->amax;
+  }
+  return q;
+}
+
+// One or two tensors, in as few launches as they allow: two of one format go
+// through one amax and one quantisation (x and W of 256 x 4096 x 4096: the
+// small one's launches are hidden), unless both record a delayed amax through
+// the workspace's one pair of words.
+fp8lin_status run_quantise(const QuantJob* jobs, int n, void* ws, const DeviceInfo& dev,
+                           cudaStream_t stream) {
+  Fp4QuantArgs q[2];
+  fp8lin_status s;
+  if (n == 2) {
+    bool apart = empty_job(jobs[0]) || empty_job(jobs[1]);
+    if (!apart) {
+      for (int i = 0; i < 2; ++i) q[i] = quant_args(jobs[i], ws);
+      apart = q[0].fmt != q[1].fmt || (q[0].out_t.codes != nullptr) != (q[1].out_t.codes != nullptr) ||
+              (q[0].amax_rec != nullptr && q[1].amax_rec != nullptr);
     }
-    if (init || (!delayed && empty)) {
-      ProfScope ps(FP8LIN_PROF_SCALE, stream);
-      cudaError_t e = launch_scale(st->amax, st->scale, st->inv_scale, nullptr, nullptr, 1, false,
-                                   st->fmt, st->eps, stream);
+    if (apart) {
+      if ((s = run_quantise(jobs, 1, ws, dev, stream)) != FP8LIN_OK) return s;
+      return run_quantise(jobs + 1, 1, ws, dev, stream);
+    }
+  } else {
+    if (empty_job(jobs[0])) return quantise_empty(jobs[0], stream);
+    q[0] = quant_args(jobs[0], ws);
+    if (fp4_quantise_small_fits(q[0])) {
+      ProfScope ps(FP8LIN_PROF_CAST_FUSED, stream);
+      cudaError_t e = launch_fp4_quantise_small(q[0], stream);
       if (e != cudaSuccess) return cuda_fail(e);
-      st->needs_init = 0;
-    }
-    if (delayed) {
-      if (empty) {
-        cudaError_t e = cudaMemsetAsync(st->amax, 0, sizeof(float), stream);
-        return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
-      }
-      q.scale_in = st->scale;
-      q.amax_rec = reinterpret_cast<uint32_t*>(st->amax);
-      q.rec_acc = ws_u32(ws, kWsAtomicAccOffset);
-      q.rec_ticket = ws_u32(ws, kWsAtomicTicketOffset);
-    } else {
-      q.amax_in = st->amax;
-      q.scale_out = st->scale;
-      q.inv_out = st->inv_scale;
+      jobs[0].st->needs_init = 0;
+      return FP8LIN_OK;
     }
   }
-  if (empty) return FP8LIN_OK;
+  uint32_t* partials = ws_u32(ws, kWsPartialOffset);
+  int num_partials[2] = {0, 0};
+  if (q[0].find_amax || (n == 2 && q[1].find_amax)) {
+    // A tensor that needs no amax beside one that does is left out.
+    const int first = q[0].find_amax ? 0 : 1;
+    const int count = n == 2 && q[0].find_amax && q[1].find_amax ? 2 : 1;
+    ProfScope ps(FP8LIN_PROF_AMAX, stream);
+    cudaError_t e = launch_fp4_amax(q + first, count, partials + first * (kMaxPartials / 2),
+                                    num_partials + first, dev, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   ProfScope ps(FP8LIN_PROF_CAST, stream);
-  cudaError_t e = launch_fp4_quantise(q, stream);
-  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+  cudaError_t e = launch_fp4_quantise(q, n, partials, num_partials, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  for (int i = 0; i < n; ++i)
+    if (jobs[i].st != nullptr) jobs[i].st->needs_init = 0;
+  return FP8LIN_OK;
 }
 
 fp8lin_status check_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, const void* d,
@@ -1287,7 +1331,8 @@ fp8lin_status fp8lin_fp4_quantise(const void* x, int64_t rows, int64_t cols, int
   if (s != FP8LIN_OK) return s;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  return run_quantise(x, rows, cols, ld, st, out, out_t, ws, dev, stream);
+  const QuantJob job = {x, rows, cols, ld, st, out, out_t};
+  return run_quantise(&job, 1, ws, dev, stream);
 }
 
 fp8lin_status fp8lin_fp4_dequantise(const fp8lin_fp4_tensor* t, void* out, int64_t ldo, int32_t f32,
@@ -1322,8 +1367,8 @@ fp8lin_status fp8lin_fp4_linear(const void* x, int64_t ldx, fp8lin_scaling_state
   if ((s = check_fp4_gemm(x4, w4, y, ldy, ws, ws_bytes)) != FP8LIN_OK) return s;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  s = run_quantise(x, x4->rows, x4->cols, ldx, sx, x4, nullptr, ws, dev, stream);
-  if (s != FP8LIN_OK) return s;
+  const QuantJob job = {x, x4->rows, x4->cols, ldx, sx, x4, nullptr};
+  if ((s = run_quantise(&job, 1, ws, dev, stream)) != FP8LIN_OK) return s;
   // The launch before the product is x's quantisation, which does not write w4.
   return run_fp4_gemm(x4, w4, y, ldy, ws, ws_bytes, dev, stream, x4->rows > 0 && x4->cols > 0);
 }
@@ -1343,10 +1388,8 @@ fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_st
   if ((s = check_fp4_gemm(x4, w4, y, N, ws, ws_bytes)) != FP8LIN_OK) return s;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  if ((s = run_quantise(x, M, K, K, sx, x4, x4t, ws, dev, stream)) != FP8LIN_OK) return s;
-  if (w != nullptr &&
-      (s = run_quantise(w, N, K, K, sw, w4, w4t, ws, dev, stream)) != FP8LIN_OK)
-    return s;
+  const QuantJob jobs[2] = {{x, M, K, K, sx, x4, x4t}, {w, N, K, K, sw, w4, w4t}};
+  if ((s = run_quantise(jobs, w != nullptr ? 2 : 1, ws, dev, stream)) != FP8LIN_OK) return s;
   return run_fp4_gemm(x4, w4, y, N, ws, ws_bytes, dev, stream);
 }
 
@@ -1372,7 +1415,8 @@ fp8lin_status fp8lin_fp4_backward(const void* dy, fp8lin_scaling_state* sdy,
     return x4t == nullptr ? FP8LIN_EINVAL : s;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  if ((s = run_quantise(dy, M, N, N, sdy, dy4, dy4t, ws, dev, stream)) != FP8LIN_OK) return s;
+  const QuantJob job = {dy, M, N, N, sdy, dy4, dy4t};
+  if ((s = run_quantise(&job, 1, ws, dev, stream)) != FP8LIN_OK) return s;
   if (dx != nullptr &&
       (s = run_fp4_gemm(dy4, w4t, dx, w4t->rows, ws, ws_bytes, dev, stream)) != FP8LIN_OK)
     return s;

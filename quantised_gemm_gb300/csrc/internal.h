@@ -320,16 +320,19 @@ constexpr int64_t fp4_scale_ktiles(int64_t cols, int fmt) {
 }
 
 // Quantise a bf16 tensor (NVFP4: fmt 0, MXFP4: fmt 1) into out, out_t (its
-// transpose) or both.  NVFP4 takes its tensorwise scale from amax_in (and
-// writes scale_out, inv_out) or from scale_in; amax_rec records the amax
+// transpose) or both.  NVFP4's tensorwise scale comes from the tensor's own
+// amax (find_amax), from amax_in or from scale_in; amax_out, scale_out and
+// inv_out are written where they are not null; amax_rec records the amax
 // through the two self-cleaning words.
 struct Fp4QuantArgs {
   const uint16_t* x;
   int64_t rows, cols, ld;
   int fmt;
+  bool find_amax = false;
   const float* amax_in = nullptr;
   const float* scale_in = nullptr;
   float eps = 0.0f;
+  float* amax_out = nullptr;
   float* scale_out = nullptr;
   float* inv_out = nullptr;
   uint32_t* amax_rec = nullptr;
@@ -337,11 +340,17 @@ struct Fp4QuantArgs {
   uint32_t* rec_ticket = nullptr;
   Fp4View out, out_t;
 };
-cudaError_t launch_fp4_quantise(const Fp4QuantArgs& a, cudaStream_t stream);
-// amax of a tensor of any alignment, width and row stride.
-cudaError_t launch_fp4_amax(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
-                            uint32_t* acc, uint32_t* ticket, uint32_t* out, const DeviceInfo& dev,
-                            cudaStream_t stream);
+// A small tensor that needs its amax, in one launch.
+bool fp4_quantise_small_fits(const Fp4QuantArgs& a);
+cudaError_t launch_fp4_quantise_small(const Fp4QuantArgs& a, cudaStream_t stream);
+// One or two tensors' largest magnitudes, a partial maximum a CTA in the
+// workspace (kMaxPartials / 2 words a tensor), and their number.
+cudaError_t launch_fp4_amax(const Fp4QuantArgs* a, int n, uint32_t* partials, int* num_partials,
+                            const DeviceInfo& dev, cudaStream_t stream);
+// One or two tensors of one format (both with a transposed copy, or neither),
+// with the partials of launch_fp4_amax for those with find_amax.
+cudaError_t launch_fp4_quantise(const Fp4QuantArgs* a, int n, const uint32_t* partials,
+                                const int* num_partials, cudaStream_t stream);
 cudaError_t launch_fp4_dequantise(const Fp4View& t, int fmt, const float* inv, int64_t rows,
                                   int64_t cols, void* out, int64_t ldo, bool f32,
                                   cudaStream_t stream);
