@@ -475,8 +475,8 @@ struct PairCfg {
 // The t-th tile.  The larger operand is read once and the smaller again and
 // again from L2: with at least as many columns as rows, all rows of tiles
 // within a column of them; else groups of four rows of tiles, column by
-// column.  8192 x 14336 x 4096: 159.9 us against 169.4 in groups of four;
-// 16384 x 4096 x 4096: 95.4 us against 98.6 by whole columns.
+// column.  8192 x 14336 x 4096: 6 % less time than in groups of four;
+// 16384 x 4096 x 4096: 3 % less than by whole columns.
 struct TileAt {
   int m, n;
 };
@@ -737,8 +737,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            if (C::kOverlap && g == 0) mbar_arrive_cluster(shared_free_even);
-            if (g == C::kGroups - 1) mbar_arrive_cluster(acc_empty_even + 8u * acc);
+            if (C::kOverlap && g == 0) mbar_arrive_cluster_tmem(shared_free_even);
+            if (g == C::kGroups - 1) mbar_arrive_cluster_tmem(acc_empty_even + 8u * acc);
           }
         }
         if (live) store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
@@ -879,17 +879,17 @@ template <int kFmt>
 cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev,
                     cudaStream_t stream) {
   // The few-tile kernel while its tiles are one wave, two CTAs an SM:
-  // 512 x 4096 x 4096 takes 10.6 us there and 12.5 us in pairs, 1024 x 4096 x
-  // 4096 (two waves) 20.1 and 12.9.
+  // 512 x 4096 x 4096 takes 10.6 us there and 11.7 us in pairs, 1024 x 4096 x
+  // 4096 (two waves) 20.0 and 11.7.
   if (g.M <= 16) return run_few<kFmt, 16, 4>(g, p, dev, stream);
   if (g.M <= 32) return run_few<kFmt, 32, 4>(g, p, dev, stream);
   if ((g.M + 63) / 64 * ((g.N + kBM - 1) / kBM) <= 2 * int64_t(dev.num_sms))
     return run_few<kFmt, 64, 3>(g, p, dev, stream);
-  // Eight epilogue warps where writing a tile takes as long as multiplying
+  // Eight epilogue warps where writing a tile takes longer than multiplying
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
-  // 777 x 4801 x 1600 11.5 us against 13.3, 12288 x 6400 x 1600 69.4 against
-  // 70.5, but 8192 x 14336 x 4096 171 against 161.
-  if (!p.vec || g.K < 10 * kBK) return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, dev, stream);
+  // 4096 x 4096 x 512 11.3 us against 13.1, 777 x 4801 x 1600 10.3 against
+  // 12.3, but 12288 x 6400 x 1600 62.6 against 58.3.
+  if (!p.vec || g.K <= 2 * kBK) return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, dev, stream);
   return run_pair<kFmt, 256, 5, 4>(g.a, g.b, p, dev, stream);
 }
 

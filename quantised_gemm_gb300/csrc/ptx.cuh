@@ -335,6 +335,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_saddr) {
                : "memory");
 }
 
+// The same with a release at CTA scope, which waits for no memory operation of
+// this thread outside the CTA: for an arrival that hands over tensor memory,
+// ordered by the tcgen05 fences around it.  The cluster-scope release costs
+// about a microsecond beside TMA stores in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_saddr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr)
+               : "memory");
+}
+
 // TMA load into this CTA's shared memory whose completion is counted on an
 // mbarrier that may live in the peer CTA of the pair (cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map,
