@@ -163,26 +163,61 @@ __device__ __forceinline__ uint32_t larger_half(uint32_t pair) {
   return max(pair & 0x7FFFu, (pair >> 16) & 0x7FFFu);
 }
 
-__device__ __forceinline__ uint32_t code8(const uint4& v, float r) {
-  float f[8];
-  mul2_rn(v.x << 16, v.x & 0xFFFF0000u, r, f[0], f[1]);
-  mul2_rn(v.y << 16, v.y & 0xFFFF0000u, r, f[2], f[3]);
-  mul2_rn(v.z << 16, v.z & 0xFFFF0000u, r, f[4], f[5]);
-  mul2_rn(v.w << 16, v.w & 0xFFFF0000u, r, f[6], f[7]);
+// One half of a bf16 pair times r in fp32.  The widening is an addition of -0
+// in mixed precision, which keeps zeros' signs and leaves the integer pipe to
+// the conversions; MXFP4's powers of two are bf16 numbers, so there the
+// product is part of it, and exact.
+template <int kFmt, int kHalf>
+__device__ __forceinline__ float widen(uint32_t pair, float r) {
+  float f;
+  if constexpr (kFmt == 0) {
+    if constexpr (kHalf == 0)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, lo, %2;\n\t}"
+          : "=f"(f)
+          : "r"(pair), "f"(-0.0f));
+    else
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 %0, hi, %2;\n\t}"
+          : "=f"(f)
+          : "r"(pair), "f"(-0.0f));
+  } else {
+    const uint16_t m = static_cast<uint16_t>(__float_as_uint(r) >> 16);
+    if constexpr (kHalf == 0)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tfma.rn.f32.bf16 %0, lo, %2, %3;\n\t}"
+          : "=f"(f)
+          : "r"(pair), "h"(m), "f"(-0.0f));
+    else
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tfma.rn.f32.bf16 %0, hi, %2, %3;\n\t}"
+          : "=f"(f)
+          : "r"(pair), "h"(m), "f"(-0.0f));
+  }
+  return f;
+}
+
+template <int kFmt>
+__device__ __forceinline__ uint32_t codes_of(float (&f)[8], float r) {
+  if constexpr (kFmt == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      mul2_rn(__float_as_uint(f[2 * j]), __float_as_uint(f[2 * j + 1]), r, f[2 * j], f[2 * j + 1]);
+  }
   return cvt_e2m1x8(f);
 }
 
+template <int kFmt>
+__device__ __forceinline__ uint32_t code8(const uint4& v, float r) {
+  float f[8] = {widen<kFmt, 0>(v.x, r), widen<kFmt, 1>(v.x, r), widen<kFmt, 0>(v.y, r),
+                widen<kFmt, 1>(v.y, r), widen<kFmt, 0>(v.z, r), widen<kFmt, 1>(v.z, r),
+                widen<kFmt, 0>(v.w, r), widen<kFmt, 1>(v.w, r)};
+  return codes_of<kFmt>(f, r);
+}
+
 // Eight values, one from each word: its low or its high half.
-template <int kHalf>
+template <int kFmt, int kHalf>
 __device__ __forceinline__ uint32_t code8_of(const uint32_t* w, float r) {
   float f[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t a = kHalf == 0 ? w[2 * j] << 16 : w[2 * j] & 0xFFFF0000u;
-    const uint32_t b = kHalf == 0 ? w[2 * j + 1] << 16 : w[2 * j + 1] & 0xFFFF0000u;
-    mul2_rn(a, b, r, f[2 * j], f[2 * j + 1]);
-  }
-  return cvt_e2m1x8(f);
+  for (int j = 0; j < 8; ++j) f[j] = widen<kFmt, kHalf>(w[j], r);
+  return codes_of<kFmt>(f, r);
 }
 
 // The tensor's amax joins a maximum over the CTAs; the last one publishes it
@@ -220,8 +255,8 @@ struct QuantParams {
   uint8_t* codes_t;
   uint8_t* scales_t;
   int64_t ld4_t;
-  int64_t tiles_c;         // 128-column tiles of a row of tiles
-  int64_t tiles;
+  uint32_t tiles_c;        // 128-column tiles of a row of tiles
+  uint32_t tiles;
 };
 struct QuantPair {
   QuantParams p[2];        // the second tensor's tiles follow the first's
@@ -238,13 +273,13 @@ struct QuantSmem {
 
 // This thread's part of a tile: 16 values of four rows, 32 rows apart.
 template <int kAlign>
-__device__ __forceinline__ void load_tile(const QuantParams& p, int64_t tr, int64_t tc,
+__device__ __forceinline__ void load_tile(const QuantParams& p, uint32_t tr, uint32_t tc,
                                           uint4 (&v)[4][2]) {
   const int lane = threadIdx.x & 31, rr = (threadIdx.x >> 5) * 4 + (lane >> 3);
-  const int64_t col = tc * kQTile + (lane & 7) * 16;
+  const int64_t col = int64_t(tc) * kQTile + (lane & 7) * 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t row = tr * kQTile + rr + 32 * i;
+    const int64_t row = int64_t(tr) * kQTile + rr + 32 * i;
     v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
     if (row < p.rows) load16<kAlign>(p.x + row * p.ld, col, p.cols, v[i]);
   }
@@ -279,13 +314,13 @@ __device__ __forceinline__ void fill_table(float s, float* table) {
 // The codes and scales of one tile held in v; returns the largest magnitude.
 // sm.table is filled; the call synchronises before it reads it.
 template <int kFmt, bool kTrans>
-__device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, int64_t tr, int64_t tc,
+__device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, uint32_t tr, uint32_t tc,
                                                   float s, const uint4 (&v)[4][2],
                                                   QuantSmem<kFmt, kTrans>& sm) {
   constexpr int kBlock = kFmt == 0 ? 16 : 32;
   constexpr int kTileBlocks = 4 * kBlock;  // columns of one 512-byte scale tile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row0 = tr * kQTile, col0 = tc * kQTile;
+  const int64_t row0 = int64_t(tr) * kQTile, col0 = int64_t(tc) * kQTile;
   const int b = lane & 7;                    // 16-column group of the tile
   const int rr = warp * 4 + (lane >> 3);     // row modulo 32
   const int64_t col = col0 + b * 16;
@@ -312,7 +347,7 @@ __device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, int64_t 
     const int64_t row = row0 + rr + 32 * i;
     if (row < p.rows && col < ((p.cols + 31) & ~int64_t(31)))
       *reinterpret_cast<uint2*>(p.codes + row * p.ld4 + (col >> 1)) =
-          make_uint2(code8(v[i][0], r), code8(v[i][1], r));
+          make_uint2(code8<kFmt>(v[i][0], r), code8<kFmt>(v[i][1], r));
     // Four block scales of one scale tile's row, low block first.
     constexpr int kStep = kFmt == 0 ? 1 : 2;
     uint32_t w = c << (8 * ((b / kStep) & 3));
@@ -326,7 +361,7 @@ __device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, int64_t 
     const int64_t kt = col / kTileBlocks;
     const bool first = kFmt == 0 ? (b & 3) == 0 : b == 0;
     if (first && kt < ktiles)
-      *reinterpret_cast<uint4*>(p.scales + (tr * ktiles + kt) * 512 + rr * 16) =
+      *reinterpret_cast<uint4*>(p.scales + (int64_t(tr) * ktiles + kt) * 512 + rr * 16) =
           make_uint4(word[0], word[1], word[2], word[3]);
   }
   if constexpr (kTrans) {
@@ -359,8 +394,8 @@ __device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, int64_t 
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-          out[2 * g + q] = h == 0 ? code8_of<0>(w + 16 * g + 8 * q, r)
-                                  : code8_of<1>(w + 16 * g + 8 * q, r);
+          out[2 * g + q] = h == 0 ? code8_of<kFmt, 0>(w + 16 * g + 8 * q, r)
+                                  : code8_of<kFmt, 1>(w + 16 * g + 8 * q, r);
       }
       *reinterpret_cast<uint4*>(sm.stage + pair * 128 + (((h * 4 + rg) ^ (pair & 7)) << 4)) =
           make_uint4(out[0], out[1], out[2], out[3]);
@@ -380,9 +415,9 @@ __device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, int64_t 
     if (tid < 32 * kScTiles) {
       const int64_t nblk = (p.rows + kBlock - 1) / kBlock;
       const int64_t ktiles = (nblk + 3) >> 2;
-      const int64_t kt = tr * kScTiles + (tid >> 5);
+      const int64_t kt = int64_t(tr) * kScTiles + (tid >> 5);
       if (kt < ktiles)
-        *reinterpret_cast<uint4*>(p.scales_t + (tc * ktiles + kt) * 512 + (tid & 31) * 16) =
+        *reinterpret_cast<uint4*>(p.scales_t + (int64_t(tc) * ktiles + kt) * 512 + (tid & 31) * 16) =
             *reinterpret_cast<const uint4*>(sm.scales + tid * 16);
     }
   }
@@ -404,8 +439,8 @@ __global__ void __launch_bounds__(kQThreads)
   griddep_launch_dependents();
   const bool second = blockIdx.x >= pair.p[0].tiles;
   const QuantParams& p = pair.p[second];
-  const int64_t t = blockIdx.x - (second ? pair.p[0].tiles : 0);
-  const int64_t tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
+  const uint32_t t = blockIdx.x - (second ? pair.p[0].tiles : 0);
+  const uint32_t tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
   uint4 v[4][2];
   load_tile<kAlign>(p, tr, tc, v);
   float s = 0.0f;
@@ -496,7 +531,7 @@ __global__ void __launch_bounds__(kQThreads)
   __shared__ __align__(16) QuantSmem<0, kTrans> sm;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
+  const uint32_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
   const uint32_t m = share_max<kAlign, 8>(a, threadIdx.x >> 5, kQThreads / 32);
   uint4 v[4][2];
   load_tile<kAlign>(p, tr, tc, v);
@@ -528,23 +563,23 @@ template <int kFmt, typename Out, int kAlign>
 __global__ void __launch_bounds__(kQThreads)
     fp4_dequantise_kernel(const uint8_t* codes, const uint8_t* scales, const float* inv,
                           int64_t rows, int64_t cols, int64_t ld4, Out* out, int64_t ldo,
-                          int64_t tiles_c) {
+                          uint32_t tiles_c) {
   constexpr int kBlock = kFmt == 0 ? 16 : 32;
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const uint32_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
   const int b = lane & 7, rr = warp * 4 + (lane >> 3);
-  const int64_t col = tc * kQTile + b * 16;
+  const int64_t col = int64_t(tc) * kQTile + b * 16;
   if (col >= cols) return;
   const int64_t ktiles = ((cols + kBlock - 1) / kBlock + 3) >> 2;
   const uint4 sc = *reinterpret_cast<const uint4*>(
-      scales + (tr * ktiles + col / (4 * kBlock)) * 512 + rr * 16);
+      scales + (int64_t(tr) * ktiles + col / (4 * kBlock)) * 512 + rr * 16);
   const int shift = 8 * (kFmt == 0 ? b & 3 : b >> 1);
   uint2 q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t row = tr * kQTile + rr + 32 * i;
+    const int64_t row = int64_t(tr) * kQTile + rr + 32 * i;
     q[i] = row < rows ? *reinterpret_cast<const uint2*>(codes + row * ld4 + (col >> 1))
                       : make_uint2(0, 0);
   }
@@ -552,7 +587,7 @@ __global__ void __launch_bounds__(kQThreads)
   const uint32_t words[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t row = tr * kQTile + rr + 32 * i;
+    const int64_t row = int64_t(tr) * kQTile + rr + 32 * i;
     if (row >= rows) break;
     const uint32_t code = (words[i] >> shift) & 0xFFu;
     const float c = kFmt == 0 ? e4m3_to_f32(code) : e8m0_to_f32(code);
@@ -598,23 +633,23 @@ template <int kFmt, typename Out>
 __global__ void __launch_bounds__(kQThreads)
     fp4_dequantise_ragged_kernel(const uint8_t* codes, const uint8_t* scales, const float* inv,
                                  int64_t rows, int64_t cols, int64_t ld4, Out* out, int64_t ldo,
-                                 int64_t tiles_c) {
+                                 uint32_t tiles_c) {
   constexpr int kBlock = kFmt == 0 ? 16 : 32;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const uint32_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
   const int64_t ktiles = ((cols + kBlock - 1) / kBlock + 3) >> 2;
   const float d = kFmt == 0 ? __fdiv_rn(*inv, 6.0f) : 1.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = warp + 8 * i;
-    const int64_t row = tr * 32 + r;
+    const int64_t row = int64_t(tr) * 32 + r;
     if (row >= rows) break;
-    const uint8_t* row_scales = scales + (tr >> 2) * ktiles * 512 + r * 16 + (tr & 3) * 4;
+    const uint8_t* row_scales = scales + int64_t(tr >> 2) * ktiles * 512 + r * 16 + (tr & 3) * 4;
 #pragma unroll
     for (int j = 0; j < kQTile / 32; ++j) {
-      const int64_t col = tc * kQTile + 32 * j + lane;
+      const int64_t col = int64_t(tc) * kQTile + 32 * j + lane;
       if (col >= cols) continue;
       const int64_t blk = col / kBlock;
       const uint32_t code = row_scales[(blk >> 2) * 512 + (blk & 3)];
@@ -657,8 +692,8 @@ QuantParams quant_params(const Fp4QuantArgs& a) {
   p.codes_t = a.out_t.codes;
   p.scales_t = a.out_t.scales;
   p.ld4_t = a.out_t.ld;
-  p.tiles_c = (a.cols + kQTile - 1) / kQTile;
-  p.tiles = (a.rows + kQTile - 1) / kQTile * p.tiles_c;
+  p.tiles_c = static_cast<uint32_t>((a.cols + kQTile - 1) / kQTile);
+  p.tiles = static_cast<uint32_t>((a.rows + kQTile - 1) / kQTile) * p.tiles_c;
   return p;
 }
 
@@ -766,7 +801,7 @@ cudaError_t launch_fp4_dequantise(const Fp4View& t, int fmt, const float* inv, i
     auto* kernel = align == kAlign32 ? align32 : align == kAlign16 ? align16 : scalar;
     return launch_kernel(kernel, grid, dim3(kQThreads), 0, stream, 1, false,
                          static_cast<const uint8_t*>(t.codes), static_cast<const uint8_t*>(t.scales),
-                         inv, rows, cols, t.ld, dst, ldo, tiles_c);
+                         inv, rows, cols, t.ld, dst, ldo, static_cast<uint32_t>(tiles_c));
   };
   auto run_type = [&](auto* dst) {
     using Out = std::remove_pointer_t<decltype(dst)>;
