@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "fp4_quant.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -143,6 +144,72 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
   *abort_flag = 1;
 }
 
+// The epilogue of one tile for one of four warps: its 32 rows of the
+// accumulator to D, or, where the K loop is shared, to the CTA's partial.
+__device__ __forceinline__ void few_epilogue(const Fp4GemmParams& p, uint32_t tmem_base, float* partial,
+                                             bool shared, bool any, int64_t row0, int cols,
+                                             float alpha, uint16_t* d, int quarter, int lane) {
+  const int r = quarter * 32 + lane;
+  const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+  for (int c0 = 0; c0 < cols; c0 += 16) {
+    uint32_t v[16];
+    tmem_load_16cols(t_row + c0, v);
+    tmem_load_wait();
+    if (shared) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        partial[(c0 + j) * kBM + r] = any ? __uint_as_float(v[j]) : 0.0f;
+    } else if (row0 + r < p.M) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c0 + j < cols)
+          d[(c0 + j) * p.ldd + r] = static_cast<uint16_t>(
+              cvt_bf16x2(__fmul_rn(__uint_as_float(v[j]), alpha), 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+// This CTA's part of a tile, added up over the cluster's partials in rank
+// order.
+__device__ __forceinline__ void join_partials(const Fp4GemmParams& p, const float* partial, int split,
+                                              int rank, int64_t row0, int cols, float alpha,
+                                              uint16_t* d) {
+  // Rows of the tile are dealt to the cluster's CTAs, four a thread.
+  const int quads = kBM / split / 4, mine = rank * (kBM / split);
+  const uint32_t base = smem_addr(partial);
+  const bool wide = p.vec && row0 + kBM <= p.M;
+#pragma unroll 2
+  for (int e = threadIdx.x; e < quads * cols; e += blockDim.x) {
+    const int c = e / quads, r = mine + e % quads * 4;
+    const uint32_t at = base + static_cast<uint32_t>(c * kBM + r) * 4u;
+    float4 v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < split) v[s] = ld_shared_cluster_f32x4(map_to_cta(at, s));
+    float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+    for (int s = 1; s < 8; ++s)
+      if (s < split) {
+        sum[0] += v[s].x;
+        sum[1] += v[s].y;
+        sum[2] += v[s].z;
+        sum[3] += v[s].w;
+      }
+    const uint32_t lo = cvt_bf16x2(__fmul_rn(sum[0], alpha), __fmul_rn(sum[1], alpha));
+    const uint32_t hi = cvt_bf16x2(__fmul_rn(sum[2], alpha), __fmul_rn(sum[3], alpha));
+    uint16_t* dst = d + c * p.ldd + r;
+    if (wide) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (row0 + r + j < p.M)
+          dst[j] = static_cast<uint16_t>((j < 2 ? lo : hi) >> (16 * (j & 1)));
+    }
+  }
+}
+
 // ------------------------------------------------------------------ few tiles
 //
 // One 128 x BN tile of D^T a cluster: A, the operand that fills the MMA's 128
@@ -219,8 +286,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], kb * kBKBytes, m_blk * kBM);
     tma_load_2d(sSa + stage * C::kScBytes, &tmSa, &full[stage], kb * kKt * kScElems, m_blk);
   };
-  if (early && threadIdx.x == 0)
+  if (threadIdx.x == 0) {  // the weight's first stages, before anything else
+    if (!early) griddep_wait();
     for (int i = 0; i < nkb && i < STAGES; ++i) load_a(i, kb0 + i);
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
@@ -239,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (; i < nkb; ++i) {
         const int stage = i % STAGES, kb = kb0 + i;
         if (i >= STAGES && !mbar_wait_bounded(&empty[stage], (i / STAGES - 1) & 1u, abort_flag)) break;
-        if (!early || i >= STAGES) load_a(stage, kb);
+        if (i >= STAGES) load_a(stage, kb);
         tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * kBKBytes, n_blk * BN);
         // B's scale tile holds 128 rows: BN of them belong to this tile.
         tma_load_2d(sSb + stage * C::kScBytes, &tmSb, &full[stage], kb * kKt * kScElems,
@@ -313,68 +382,324 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;  // TMEM lanes this warp may read
-    const int r = quarter * 32 + lane;
     const bool ready = warp_wait(acc_full, 0, abort_flag);
     if (!ready) {
       if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
     } else {
       tc_fence_after_sync();
-      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll 1
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        uint32_t v[16];
-        tmem_load_16cols(t_row + c0, v);
-        tmem_load_wait();
-        if (split > 1) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            partial[(c0 + j) * kBM + r] = nkb > 0 ? __uint_as_float(v[j]) : 0.0f;
-        } else if (row0 + r < p.M) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < cols)
-              d[(c0 + j) * p.ldd + r] = static_cast<uint16_t>(
-                  cvt_bf16x2(__fmul_rn(__uint_as_float(v[j]), alpha), 0.0f) & 0xFFFFu);
-        }
-      }
+      few_epilogue(p, tmem_base, partial, split > 1, nkb > 0, row0, cols, alpha, d, quarter, lane);
     }
   }
   if (split > 1) {
     tc_fence_before_sync();
     cluster_sync_all();  // every partial is in place
-    // Rows of the tile are dealt to the cluster's CTAs, four a thread.
-    const int quads = kBM / split / 4, mine = rank * (kBM / split);
-    const uint32_t base = smem_addr(partial);
-    const bool wide = p.vec && row0 + kBM <= p.M;
-#pragma unroll 2
-    for (int e = threadIdx.x; e < quads * cols; e += kThreads) {
-      const int c = e / quads, r = mine + e % quads * 4;
-      const uint32_t at = base + static_cast<uint32_t>(c * kBM + r) * 4u;
-      float4 v[8];
+    join_partials(p, partial, split, rank, row0, cols, alpha, d);
+    cluster_sync_all();  // no CTA leaves while its partial is read
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ few tokens, quantised on the way
+//
+// The few-tile product of up to 32 tokens straight from their bf16 values:
+// one launch instead of a quantisation and a product.  While the first stages
+// of the weight are on their way, each CTA quantises its K slice of the
+// tokens into shared memory, in the places that the codes and scale tiles of
+// a stage have; a cluster covers all of K, so its CTAs join their maxima for
+// the tensorwise scale.  The first tile's cluster also writes the quantised
+// tokens and their state.  Every thread holds its values in registers between
+// the maximum and the conversion, which is what bounds the slice.
+constexpr int kFusedThreads = 256;
+constexpr int kFusedUnits = 4 * kFusedThreads;  // of 16 values, of a CTA
+constexpr size_t kFusedSmemHalf = 114688;       // two CTAs an SM
+constexpr size_t kFusedSmemFull = 229376;       // one
+
+template <int kFmt, int BN>
+struct FusedCfg {
+  static constexpr int kABytes = kBM * kBKBytes;
+  static constexpr int kBBytes = BN * kBKBytes;                  // of a K block
+  static constexpr int kScBytes = stage_ktiles<kFmt>() * kScTile;
+  static constexpr int kRingBytes = kABytes + kScBytes;          // of a stage
+  static constexpr int kMaxStages = 10;
+  static constexpr int kFixed = 1024 + 512 + 256;                // alignment, table, barriers
+  static constexpr int kSfa = BN;
+  static constexpr int kSfb = kSfa + 16;
+  static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : 128;
+  // Stages beside the tokens of nkb K blocks (the partial needs one stage).
+  static int stages(int64_t nkb, size_t smem) {
+    const int64_t left = int64_t(smem) - kFixed - nkb * (kBBytes + kScBytes);
+    const int64_t n = left / kRingBytes;
+    return static_cast<int>(n < 0 ? 0 : n > nkb ? nkb : n > kMaxStages ? kMaxStages : n);
+  }
+  static_assert(kABytes >= kBM * BN * 4, "the partial fits one stage of A");
+};
+
+struct FusedTokens {
+  const uint16_t* x;
+  int64_t ldx;
+  const float* amax_in;    // NVFP4: precomputed amax, or
+  const float* scale_in;   // the stored scale, or (neither) the tokens' own amax
+  float eps;
+  float* amax_out;         // each may be null
+  float* scale_out;
+  float* inv_out;
+  uint8_t* codes;          // the quantised tokens
+  int64_t ld4;
+  uint8_t* scales;
+};
+
+template <int kFmt, int BN, int kAlign>
+__global__ void __launch_bounds__(kFusedThreads, 2)
+    gemm_fp4_fused_kernel(const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ CUtensorMap tmSa,
+                          const __grid_constant__ Fp4GemmParams p,
+                          const __grid_constant__ FusedTokens x, const int split, const int stages) {
+  using C = FusedCfg<kFmt, BN>;
+  constexpr int kKt = stage_ktiles<kFmt>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int m_blk = static_cast<int>(blockIdx.x / split);
+  const int num_kb = static_cast<int>((p.K + kBK - 1) / kBK);
+  const int per = (num_kb + split - 1) / split;
+  const int kb0 = min(num_kb, rank * per), nkb = min(num_kb, kb0 + per) - kb0;
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + stages * C::kABytes;    // [per] K blocks of the tokens' codes
+  uint8_t* sSa = sB + per * C::kBBytes;
+  uint8_t* sSb = sSa + stages * C::kScBytes;  // [per] K blocks of their scale tiles
+  float* table = reinterpret_cast<float*>(sSb + per * C::kScBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(table + 128);
+  uint64_t* empty = full + C::kMaxStages;
+  uint64_t* acc_full = empty + C::kMaxStages;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* red = tmem_slot + 2;   // [8] warps' maxima
+  uint32_t* cta_max = red + 8;     // read by the cluster
+  float* partial = reinterpret_cast<float*>(sA);
+
+  auto load_a = [&](int stage, int kb) {
+    mbar_arrive_expect_tx(&full[stage], C::kRingBytes);
+    tma_load_2d(sA + stage * C::kABytes, &tmA, &full[stage], kb * kBKBytes, m_blk * kBM);
+    tma_load_2d(sSa + stage * C::kScBytes, &tmSa, &full[stage], kb * kKt * kScElems, m_blk);
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ------------------------------------------------------------ the tokens
+  // Their loads go out before the weight's, behind which they would wait.
+  const int row_units = nkb * 16, units = static_cast<int>(p.N) * row_units;
+  const int64_t col0 = static_cast<int64_t>(kb0) * kBK;
+  auto load_units = [&](uint4 (&v)[4][2], int per_row, int count, int64_t first) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s < split) v[s] = ld_shared_cluster_f32x4(map_to_cta(at, s));
-      float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < split) {
-          sum[0] += v[s].x;
-          sum[1] += v[s].y;
-          sum[2] += v[s].z;
-          sum[3] += v[s].w;
-        }
-      const uint32_t lo = cvt_bf16x2(__fmul_rn(sum[0], alpha), __fmul_rn(sum[1], alpha));
-      const uint32_t hi = cvt_bf16x2(__fmul_rn(sum[2], alpha), __fmul_rn(sum[3], alpha));
-      uint16_t* dst = d + c * p.ldd + r;
-      if (wide) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (row0 + r + j < p.M)
-            dst[j] = static_cast<uint16_t>((j < 2 ? lo : hi) >> (16 * (j & 1)));
+    for (int k = 0; k < 4; ++k) {
+      const int u = threadIdx.x + k * kFusedThreads;
+      v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+      if (u < count) {
+        const int row = u / per_row, c = u - row * per_row;
+        load16<kAlign>(x.x + row * x.ldx, first + c * 16, p.K, v[k]);
       }
     }
+  };
+  // The tensorwise maximum: every CTA's own where all tokens fit its
+  // registers, else the cluster's.
+  const int all_units = static_cast<int>(p.N) * num_kb * 16;
+  const bool find = kFmt == 0 && x.amax_in == nullptr;
+  const bool whole = split == 1 || all_units <= kFusedUnits;
+  uint4 v[4][2], w[4][2];
+  load_units(v, row_units, units, col0);
+  if (find && whole && split > 1) load_units(w, num_kb * 16, all_units, 0);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < nkb && i < stages; ++i) load_a(i, kb0 + i);
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  // Scale tiles hold 128 rows; those past the tokens are zero.
+  for (int i = threadIdx.x; i < nkb * C::kScBytes / 16; i += kFusedThreads)
+    reinterpret_cast<uint4*>(sSb)[i] = make_uint4(0, 0, 0, 0);
+  uint32_t m = 0;
+  if (find && whole && split > 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m = max(m, larger_half(max_magnitude(max8(w[k][0]), max8(w[k][1]))));
+  }
+  uint32_t largest[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    largest[k] = larger_half(max_magnitude(max8(v[k][0]), max8(v[k][1])));
+    m = max(m, largest[k]);
+  }
+  float s = 0.0f, inv = 1.0f;
+  if constexpr (kFmt == 0) {
+    float amax = 0.0f;
+    if (!find) {
+      amax = *x.amax_in;
+    } else {
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if (lane == 0) red[warp] = m;
+      __syncthreads();
+      uint32_t all = red[0];
+#pragma unroll
+      for (int w = 1; w < kFusedThreads / 32; ++w) all = max(all, red[w]);
+      if (!whole) {
+        if (threadIdx.x == 0) *cta_max = all;
+        cluster_sync_all();
+        for (int r = 0; r < split; ++r)
+          all = max(all, ld_shared_cluster_u32(map_to_cta(smem_addr(cta_max), r)));
+      }
+      amax = __uint_as_float(all << 16);
+    }
+    s = x.scale_in != nullptr ? *x.scale_in : fp4_tensor_scale(amax, x.eps);
+    inv = x.scale_in != nullptr ? *p.inv_b : __fdiv_rn(1.0f, s);
+    fill_table(s, table);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      if (x.amax_out != nullptr) *x.amax_out = amax;
+      if (x.scale_out != nullptr) {
+        *x.scale_out = s;
+        *x.inv_out = inv;
+      }
+    }
+  }
+  __syncthreads();  // the table is filled and the scale tiles are zero
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int u = threadIdx.x + k * kFusedThreads;
+    // A block of 32 is two units of neighbouring lanes.
+    const uint32_t top =
+        kFmt == 0 ? largest[k] : max(largest[k], __shfl_xor_sync(0xFFFFFFFFu, largest[k], 1));
+    float r;
+    const uint32_t sc = block_scale<kFmt>(top, s, table, r);
+    const uint2 codes = make_uint2(code8<kFmt>(v[k][0], r), code8<kFmt>(v[k][1], r));
+    if (u >= units) continue;
+    const int row = u / row_units, c = u - row * row_units;
+    const int kb = c >> 4, byte = (c & 15) * 8;  // of a 128-byte swizzled row
+    *reinterpret_cast<uint2*>(sB + kb * C::kBBytes + row * kBKBytes +
+                              (((byte >> 4) ^ (row & 7)) << 4) + (byte & 8)) = codes;
+    const int blk = kFmt == 0 ? c & 15 : (c & 15) >> 1;
+    if (kFmt == 0 || (c & 1) == 0)
+      sSb[kb * C::kScBytes + (blk >> 2) * kScTile + row * 16 + (blk & 3)] = static_cast<uint8_t>(sc);
+    const int64_t col = col0 + c * 16;
+    if (m_blk == 0 && col < (p.K + 31) / 32 * 32)
+      *reinterpret_cast<uint2*>(x.codes + row * x.ld4 + (col >> 1)) = codes;
+  }
+  fence_proxy_async_shared();  // the tensor core reads what was written here
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  if (m_blk == 0) {
+    const int64_t ktiles = (p.K + kBK / kKt - 1) / (kBK / kKt), first = static_cast<int64_t>(kb0) * kKt;
+    const int mine = static_cast<int>(min(ktiles - first, static_cast<int64_t>(nkb) * kKt)) * (kScTile / 16);
+    for (int i = threadIdx.x; i < mine; i += kFusedThreads)
+      reinterpret_cast<uint4*>(x.scales + first * kScTile)[i] = reinterpret_cast<const uint4*>(sSb)[i];
+  }
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int i = min(nkb, stages);
+      for (; i < nkb; ++i) {
+        if (!mbar_wait_bounded(&empty[i % stages], (i / stages - 1) & 1u, abort_flag)) break;
+        load_a(i % stages, kb0 + i);
+      }
+      if (i < nkb) {
+        record_error(p.err, abort_flag, kErrGemmProducerWait);
+        volatile int never = 0;
+        for (int j = max(0, i - stages); j < i; ++j)
+          mbar_wait_bounded(&full[j % stages], (j / stages) & 1u, &never);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    bool ok = true;
+    int i = 0, stage = 0;
+    uint32_t phase = 0;
+    for (; i < nkb; ++i) {
+      ok = warp_wait(&full[stage], phase, abort_flag);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint64_t a_desc = smem_desc_k_sw128(smem_addr(sA + stage * C::kABytes));
+      const uint64_t b_desc = smem_desc_k_sw128(smem_addr(sB + i * C::kBBytes));
+      const uint64_t sa_desc = smem_desc_scale(smem_addr(sSa + stage * C::kScBytes));
+      const uint64_t sb_desc = smem_desc_scale(smem_addr(sSb + i * C::kScBytes));
+      const int64_t left = p.K - int64_t(kb0 + i) * kBK;
+      const int steps = left >= kBK ? 4 : static_cast<int>((left + kMmaK - 1) / kMmaK);
+      if (elect_one()) {
+#pragma unroll
+        for (int t = 0; t < kKt; ++t) {
+          copy_scale_tile(tmem_base + C::kSfa + 4 * t, sa_desc + static_cast<uint64_t>(t * (kScTile >> 4)));
+          copy_scale_tile(tmem_base + C::kSfb + 4 * t, sb_desc + static_cast<uint64_t>(t * (kScTile >> 4)));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int kt = kFmt == 0 ? k : k >> 1;
+          const uint32_t idesc = make_idesc_fp4<kFmt>(kBM, BN, kFmt == 0 ? 0u : 2u * (k & 1));
+          if (k < steps)
+            mma_fp4<kFmt>(tmem_base, a_desc + static_cast<uint64_t>(2 * k),
+                          b_desc + static_cast<uint64_t>(2 * k), idesc, tmem_base + C::kSfa + 4 * kt,
+                          tmem_base + C::kSfb + 4 * kt, (i > 0 || k > 0) ? 1u : 0u);
+        }
+        if (i + stages < nkb) mma_commit(&empty[stage]);
+      }
+      __syncwarp();
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (elect_one()) {
+      if (ok) {
+        mma_commit(acc_full);
+      } else {
+        record_error(p.err, abort_flag, kErrGemmMmaWait);
+        if (i > 0) {
+          volatile int never = 0;
+          mma_commit(drain);
+          mbar_wait_bounded(drain, 0, &never);
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  const int cols = static_cast<int>(p.N);
+  const int64_t row0 = static_cast<int64_t>(m_blk) * kBM;
+  const float alpha =
+      kFmt == 0 ? __fmul_rn(__fdiv_rn(*p.inv_a, 6.0f), __fdiv_rn(inv, 6.0f)) : 1.0f;
+  uint16_t* d = p.d + row0;
+  if (warp >= 2 && warp < 6) {
+    // ------------------------------------------------------------ epilogue
+    const bool ready = warp_wait(acc_full, 0, abort_flag);
+    if (!ready) {
+      if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
+    } else {
+      tc_fence_after_sync();
+      few_epilogue(p, tmem_base, partial, split > 1, nkb > 0, row0, cols, alpha, d, warp & 3, lane);
+    }
+  }
+  if (split > 1) {
+    tc_fence_before_sync();
+    cluster_sync_all();  // every partial is in place
+    join_partials(p, partial, split, rank, row0, cols, alpha, d);
     cluster_sync_all();  // no CTA leaves while its partial is read
   }
   __syncwarp();
@@ -847,6 +1172,66 @@ cudaError_t run_few(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
                        g.b_early);
 }
 
+// How the fused product runs these sizes; stages 0: it does not.
+struct FusedPlan {
+  int split, per, stages;
+};
+
+template <int kFmt, int BN>
+FusedPlan plan_fused(const Fp4GemmArgs& g, const DeviceInfo& dev) {
+  using C = FusedCfg<kFmt, BN>;
+  const int64_t num_kb = (g.K + kBK - 1) / kBK, tiles = (g.N + kBM - 1) / kBM;
+  // Tiles for most SMs: one CTA each, with all of its shared memory for loads
+  // in flight and nothing to join.
+  if (2 * tiles > dev.num_sms && g.M * num_kb * 16 <= kFusedUnits) {
+    const int n = C::stages(num_kb, kFusedSmemFull);
+    if (n >= num_kb || n >= 6) return {1, static_cast<int>(num_kb), n};
+  }
+  const int split = few_split(tiles, g.K, 2 * int64_t(dev.num_sms));
+  const int64_t per = (num_kb + split - 1) / split;
+  if (g.M * per * 16 > kFusedUnits) return {split, 0, 0};  // the values would not stay in registers
+  const int n = C::stages(per, kFusedSmemHalf);
+  return {split, static_cast<int>(per), n >= per || n >= 3 ? n : 0};
+}
+
+template <int kFmt, int BN>
+cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams p,
+                      const DeviceInfo& dev, cudaStream_t stream) {
+  using C = FusedCfg<kFmt, BN>;
+  p.M = g.N;
+  p.N = g.M;
+  const FusedPlan f = plan_fused<kFmt, BN>(g, dev);
+  CUtensorMap tmA, tmSa;
+  if (!make_code_map(&tmA, g.b, p.M, p.K, kBM) || !make_scale_map<kFmt>(&tmSa, g.b, p.M, p.K, 1))
+    return map_failed("fp4 gemm operand");
+  FusedTokens t;
+  t.x = x.x;
+  t.ldx = x.ld;
+  t.amax_in = x.amax_in;
+  t.scale_in = x.scale_in;
+  t.eps = x.eps;
+  // A stored scale's call records the amax beside it.
+  t.amax_out = x.scale_in != nullptr ? reinterpret_cast<float*>(x.amax_rec) : x.amax_out;
+  t.scale_out = x.scale_out;
+  t.inv_out = x.inv_out;
+  t.codes = x.out.codes;
+  t.ld4 = x.out.ld;
+  t.scales = x.out.scales;
+  const int align = row_align(x.x, x.ld, 2);
+  auto* kernel = align == kAlign32   ? gemm_fp4_fused_kernel<kFmt, BN, kAlign32>
+                 : align == kAlign16 ? gemm_fp4_fused_kernel<kFmt, BN, kAlign16>
+                                     : gemm_fp4_fused_kernel<kFmt, BN, kScalar>;
+  static bool done[3][64] = {};
+  cudaError_t e = allow_smem(kernel, kFusedSmemFull, dev, done[align]);
+  if (e != cudaSuccess) return e;
+  const size_t bytes = C::kFixed + static_cast<size_t>(f.stages) * C::kRingBytes +
+                       static_cast<size_t>(f.per) * (C::kBBytes + C::kScBytes);
+  const int64_t tiles = (p.M + kBM - 1) / kBM;
+  set_error_site("gemm_fp4_fused_kernel");
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * f.split)), dim3(kFusedThreads),
+                       bytes, stream, f.split, false, tmA, tmSa, p, t, f.split, f.stages);
+}
+
 template <int kFmt, int BN, int STAGES, int EPI>
 cudaError_t run_pair(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p,
                      const DeviceInfo& dev, cudaStream_t stream) {
@@ -895,7 +1280,9 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
 
 }  // namespace
 
-cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStream_t stream) {
+namespace {
+
+Fp4GemmParams base_params(const Fp4GemmArgs& g) {
   Fp4GemmParams p;
   p.M = g.M;
   p.N = g.N;
@@ -906,7 +1293,37 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStr
   p.ldd = g.ldd;
   p.err = g.ws_error;
   p.vec = (reinterpret_cast<uintptr_t>(g.d) & 15u) == 0 && g.ldd % 8 == 0;
+  return p;
+}
+
+// The few-tile kernels take the weight as their A.
+Fp4GemmParams swapped(Fp4GemmParams p) {
+  const float* a = p.inv_a;
+  p.inv_a = p.inv_b;
+  p.inv_b = a;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStream_t stream) {
+  const Fp4GemmParams p = base_params(g);
   return g.fmt == 0 ? run_fmt<0>(g, p, dev, stream) : run_fmt<1>(g, p, dev, stream);
+}
+
+bool fp4_fused_fits(const Fp4GemmArgs& g, const DeviceInfo& dev) {
+  if (g.M > 32) return false;
+  const FusedPlan f = g.fmt == 0 ? (g.M <= 16 ? plan_fused<0, 16>(g, dev) : plan_fused<0, 32>(g, dev))
+                                 : (g.M <= 16 ? plan_fused<1, 16>(g, dev) : plan_fused<1, 32>(g, dev));
+  return f.stages > 0;
+}
+
+cudaError_t launch_fp4_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, const DeviceInfo& dev,
+                             cudaStream_t stream) {
+  const Fp4GemmParams p = swapped(base_params(g));
+  if (g.fmt == 0)
+    return g.M <= 16 ? run_fused<0, 16>(g, x, p, dev, stream) : run_fused<0, 32>(g, x, p, dev, stream);
+  return g.M <= 16 ? run_fused<1, 16>(g, x, p, dev, stream) : run_fused<1, 32>(g, x, p, dev, stream);
 }
 
 }  // namespace fp8lin

@@ -369,6 +369,11 @@ struct Fp4GemmArgs {
   bool b_early = false;  // the kernel before this one in the stream does not write b
 };
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStream_t stream);
+// x's quantisation and the product in one launch, for few tokens (g.a: x's
+// 4-bit tensor, written; g.b: the weight), where the sizes fit.
+bool fp4_fused_fits(const Fp4GemmArgs& g, const DeviceInfo& dev);
+cudaError_t launch_fp4_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, const DeviceInfo& dev,
+                             cudaStream_t stream);
 
 // ---- gradient norm and clipping (grad_clip.cu)
 

@@ -74,16 +74,17 @@ class Fp4Tensor:
 
 def _matrix(t: torch.Tensor, name: str, dtype=torch.bfloat16):
     """(pointer, rows, cols, row stride) of a 2-D CUDA tensor with unit column stride."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be 2-D" % name)
-    rows, cols = t.shape
-    ld = t.stride(0)
-    if cols > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
-    if rows <= 1:
-        ld = max(ld, cols)
-    elif ld < cols:
-        raise ValueError("%s must not have overlapping rows" % name)
+    if ld < cols:
+        if rows > 1:
+            raise ValueError("%s must not have overlapping rows" % name)
+        ld = cols
     return _dev(t, name, dtype), rows, cols, ld
 
 

@@ -137,6 +137,70 @@ def test_delayed_scaling():
         assert float(st.scale) == scale
 
 
+@pytest.mark.parametrize("fmt,kind", [(0, "precomputed"), (0, "delayed"), (1, None)])
+@pytest.mark.parametrize("rows,cols", [(4100, 2000), (2048, 4096), (8000, 1160)])
+def test_many_tiles_equal_few(rows, cols, fmt, kind):
+    """A tensor of many tiles against the same rows quantised 384 at a time
+    (both held to the oracle at smaller sizes above)."""
+    import quantised_gemm_gb300 as q
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn((rows, cols), generator=g, device="cuda").to(torch.bfloat16)
+    amax = float(x.abs().max())
+    ws = q.Workspace()
+
+    def states():
+        if fmt == 1:
+            return None
+        if kind == "delayed":
+            st = q.ScalingState(q.E4M3, q.DELAYED, 4)
+            st.needs_init = 0
+            st.scale.fill_(o4.tensor_scale(amax)[0])
+            st.inv_scale.fill_(o4.tensor_scale(amax)[1])
+        else:
+            st = q.ScalingState(q.E4M3, amax_algo=q.AMAX_PRECOMPUTED)
+            st.amax.fill_(amax)
+        return st
+
+    def values(part, r):
+        st = states()
+        a, at = dirty(q, r, cols, fmt, st), dirty(q, cols, r, fmt, st)
+        q.fp4_quantise(part, a, at, ws)
+        if kind == "delayed":
+            assert float(st.amax) == float(part.abs().max())
+        return (q.fp4_dequantise(a, torch.empty((r, cols), device="cuda")),
+                q.fp4_dequantise(at, torch.empty((cols, r), device="cuda")))
+
+    whole, whole_t = values(x, rows)
+    for r0 in range(0, rows, 384):
+        r = min(384, rows - r0)
+        v, vt = values(x[r0:r0 + r], r)
+        assert torch.equal(whole[r0:r0 + r], v) and torch.equal(whole_t[:, r0:r0 + r], vt)
+    q.check(ws)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+def test_large_linear_equals_its_parts(fmt):
+    """x and W of many tiles in the forward's one quantisation against two calls."""
+    import quantised_gemm_gb300 as q
+    M, K, N = 1100, 2048, 3000
+    lin = q.Fp4Linear(M, K, N, fmt=fmt)
+    x = torch.randn((M, K), device="cuda").to(torch.bfloat16)
+    w = (torch.randn((N, K), device="cuda") * 0.02).to(torch.bfloat16)
+    lin.forward(x, w)
+    ws = q.Workspace()
+    for t, tt, src in ((lin.x4, lin.x4t, x), (lin.w4, lin.w4t, w)):
+        r, c = src.shape
+        a = dirty(q, r, c, fmt)
+        at = dirty(q, c, r, fmt, a.state)
+        q.fp4_quantise(src, a, at, ws)
+        assert torch.equal(a.codes, t.codes) and torch.equal(a.scales, t.scales)
+        assert torch.equal(at.codes, tt.codes) and torch.equal(at.scales, tt.scales)
+        if a.state is not None:
+            for name in ("amax", "scale", "inv_scale"):
+                assert torch.equal(getattr(a.state, name), getattr(t.state, name))
+    assert torch.equal(lin.y, q.fp4_gemm(lin.x4, lin.w4, torch.empty_like(lin.y), ws))
+
+
 @pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_nan_and_infinity(fmt, bad):
@@ -274,6 +338,58 @@ def test_nan_reaches_its_row_only(fmt):
     out = q.fp4_gemm(a, b, torch.empty((200, 150), dtype=torch.bfloat16, device="cuda"), q.Workspace())
     nan = torch.isnan(out).cpu()
     assert nan[40].all() and nan.sum() == 150
+
+
+@pytest.mark.parametrize("fmt,kind", [(0, "dynamic"), (0, "precomputed"), (0, "delayed"), (1, None)])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 257, 4096), (2, 128, 100), (3, 5000, 300), (8, 96, 2048),
+                                   (1, 9000, 14336), (16, 130, 1000), (17, 640, 513), (32, 4096, 4096),
+                                   (32, 33, 31), (5, 40000, 512)])
+def test_linear_of_few_tokens_equals_its_parts(M, N, K, fmt, kind):
+    """One launch: the quantised tokens, their state and y are those of the
+    quantisation and the product by themselves, bit for bit."""
+    import quantised_gemm_gb300 as q
+    bits, x = make(M, K, 60 + M)
+    xd = to_dev_bf16(bits)
+    w = q.Fp4Tensor(N, K, fmt)
+    g = torch.Generator(device="cuda").manual_seed(70)
+    q.fp4_quantise((torch.randn((N, K), generator=g, device="cuda") * 0.02).to(torch.bfloat16), w, None,
+                   q.Workspace())
+    amax = np.abs(x).max()
+
+    def tokens():
+        st = None
+        if fmt == 0:
+            st = q.ScalingState(q.E4M3, q.DELAYED if kind == "delayed" else q.DYNAMIC, 2,
+                                q.AMAX_PRECOMPUTED if kind == "precomputed" else q.AMAX_AUTO)
+            st.amax.fill_(float(amax) if kind == "precomputed" else 9e9)
+        return dirty(q, M, K, fmt, st)
+
+    for step in range(2 if kind == "delayed" else 1):  # the first delayed call takes its own amax
+        a, b = (tokens(), tokens()) if step == 0 else (a, b)
+        ws = q.Workspace()
+        y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        q.fp4_linear(xd, a, w, y, ws)
+        q.check(ws)
+        q.fp4_quantise(xd, b, None, ws)
+        want = q.fp4_gemm(b, w, torch.empty_like(y), ws)
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+        if a.state is not None:
+            assert a.state.needs_init == 0
+            for name in ("amax", "scale", "inv_scale"):
+                assert torch.equal(getattr(a.state, name), getattr(b.state, name)), name
+        assert torch.equal(y, want)
+        xd = xd * 2
+    if K > 8:  # tokens with a stride, y's rows unaligned
+        wide = torch.zeros((M, K + 5), dtype=torch.bfloat16, device="cuda")
+        wide[:, 3:3 + K] = to_dev_bf16(bits)
+        room = torch.full((M, N + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+        c = tokens()
+        q.fp4_linear(wide[:, 3:3 + K], c, w, room[:, 1:N + 1], q.Workspace())
+        d = tokens()
+        q.fp4_quantise(to_dev_bf16(bits), d, None, ws)
+        assert torch.equal(c.codes, d.codes) and torch.equal(c.scales, d.scales)
+        assert torch.equal(room[:, 1:N + 1], q.fp4_gemm(d, w, torch.empty_like(y), ws))
+        assert (room[:, 0] == 5).all() and (room[:, N + 1:] == 5).all()
 
 
 @pytest.mark.parametrize("M", [1, 16, 200])
