@@ -1283,7 +1283,7 @@ fp8lin_status check_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor
 }
 
 Fp4GemmArgs fp4_gemm_args(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
-                          int64_t ldd, void* ws) {
+                          int64_t ldd, void* ws, size_t ws_bytes) {
   Fp4GemmArgs g;
   g.a = fp4_view(a);
   g.b = fp4_view(b);
@@ -1296,13 +1296,18 @@ Fp4GemmArgs fp4_gemm_args(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b
   g.d = d;
   g.ldd = ldd;
   g.ws_error = ws_error(ws);
+  if (ws_bytes > kWsSplitOffset) {
+    g.ws_tickets = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsTicketOffset);
+    g.ws_split = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsSplitOffset);
+    g.ws_split_bytes = ws_bytes - kWsSplitOffset;
+  }
   return g;
 }
 
 // b_early: the launch before this one in the stream does not write b.
 fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
-                           int64_t ldd, void* ws, const DeviceInfo& dev, cudaStream_t stream,
-                           bool b_early = false) {
+                           int64_t ldd, void* ws, size_t ws_bytes, const DeviceInfo& dev,
+                           cudaStream_t stream, bool b_early = false) {
   if (a->rows == 0 || b->rows == 0) return FP8LIN_OK;
   if (a->cols == 0) {
     cudaError_t e = cudaMemset2DAsync(d, static_cast<size_t>(ldd) * 2, 0,
@@ -1310,7 +1315,7 @@ fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* 
                                       static_cast<size_t>(a->rows), stream);
     return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
   }
-  Fp4GemmArgs g = fp4_gemm_args(a, b, d, ldd, ws);
+  Fp4GemmArgs g = fp4_gemm_args(a, b, d, ldd, ws, ws_bytes);
   g.b_early = b_early;
   ProfScope ps(FP8LIN_PROF_GEMM, stream);
   cudaError_t e = launch_fp4_gemm(g, dev, stream);
@@ -1320,10 +1325,11 @@ fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* 
 // y = x . w4^T with x quantised into x4: one launch for a few tokens, else the
 // quantisation and the product.
 fp8lin_status run_fp4_linear(const QuantJob& job, const fp8lin_fp4_tensor* w4, void* y, int64_t ldy,
-                             void* ws, const DeviceInfo& dev, cudaStream_t stream) {
+                             void* ws, size_t ws_bytes, const DeviceInfo& dev,
+                             cudaStream_t stream) {
   const bool empty = empty_job(job);
   if (!empty && w4->rows > 0) {
-    const Fp4GemmArgs g = fp4_gemm_args(job.out, w4, y, ldy, ws);
+    const Fp4GemmArgs g = fp4_gemm_args(job.out, w4, y, ldy, ws, ws_bytes);
     if (fp4_fused_fits(g, dev)) {
       ProfScope ps(FP8LIN_PROF_SMALL_M, stream);
       cudaError_t e = launch_fp4_fused(g, quant_args(job, ws), dev, stream);
@@ -1335,7 +1341,7 @@ fp8lin_status run_fp4_linear(const QuantJob& job, const fp8lin_fp4_tensor* w4, v
   fp8lin_status s;
   if ((s = run_quantise(&job, 1, ws, dev, stream)) != FP8LIN_OK) return s;
   // The launch before the product is x's quantisation, which does not write w4.
-  return run_fp4_gemm(job.out, w4, y, ldy, ws, dev, stream, !empty);
+  return run_fp4_gemm(job.out, w4, y, ldy, ws, ws_bytes, dev, stream, !empty);
 }
 
 // Whether two 4-bit tensors are one tensor and its transpose, by their sizes.
@@ -1382,7 +1388,7 @@ fp8lin_status fp8lin_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tenso
   if (s != FP8LIN_OK) return s;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
-  return run_fp4_gemm(a, b, d, ldd, ws, dev, stream);
+  return run_fp4_gemm(a, b, d, ldd, ws, ws_bytes, dev, stream);
 }
 
 fp8lin_status fp8lin_fp4_linear(const void* x, int64_t ldx, fp8lin_scaling_state* sx,
@@ -1395,7 +1401,7 @@ fp8lin_status fp8lin_fp4_linear(const void* x, int64_t ldx, fp8lin_scaling_state
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
   const QuantJob job = {x, x4->rows, x4->cols, ldx, sx, x4, nullptr};
-  return run_fp4_linear(job, w4, y, ldy, ws, dev, stream);
+  return run_fp4_linear(job, w4, y, ldy, ws, ws_bytes, dev, stream);
 }
 
 fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_state* sx,
@@ -1415,7 +1421,7 @@ fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_st
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
   const QuantJob jobs[2] = {{x, M, K, K, sx, x4, x4t}, {w, N, K, K, sw, w4, w4t}};
   if ((s = run_quantise(jobs, w != nullptr ? 2 : 1, ws, dev, stream)) != FP8LIN_OK) return s;
-  return run_fp4_gemm(x4, w4, y, N, ws, dev, stream);
+  return run_fp4_gemm(x4, w4, y, N, ws, ws_bytes, dev, stream);
 }
 
 fp8lin_status fp8lin_fp4_backward(const void* dy, fp8lin_scaling_state* sdy,
@@ -1443,9 +1449,9 @@ fp8lin_status fp8lin_fp4_backward(const void* dy, fp8lin_scaling_state* sdy,
   const QuantJob job = {dy, M, N, N, sdy, dy4, dy4t};
   if ((s = run_quantise(&job, 1, ws, dev, stream)) != FP8LIN_OK) return s;
   if (dx != nullptr &&
-      (s = run_fp4_gemm(dy4, w4t, dx, w4t->rows, ws, dev, stream)) != FP8LIN_OK)
+      (s = run_fp4_gemm(dy4, w4t, dx, w4t->rows, ws, ws_bytes, dev, stream)) != FP8LIN_OK)
     return s;
-  if (dw != nullptr) return run_fp4_gemm(dy4t, x4t, dw, x4t->rows, ws, dev, stream);
+  if (dw != nullptr) return run_fp4_gemm(dy4t, x4t, dw, x4t->rows, ws, ws_bytes, dev, stream);
   return FP8LIN_OK;
 }
 

@@ -46,6 +46,13 @@ struct Fp4GemmParams {
   int64_t ldd;
   int* err;
   bool vec;                   // D's rows take 16-byte stores
+  // Pair kernel: tiles [0, t_full) run whole, each one after them as s_tail
+  // slices of the K loop that join through fp32 partials and tickets (two
+  // ints for each epilogue warp of a tile, zero between launches).
+  int64_t t_full;
+  int s_tail;
+  float* partials;
+  int* tickets;
 };
 
 // Instruction descriptor of kind::mxf4nvf4 / kind::mxf4: e2m1 operands, both
@@ -773,6 +780,9 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
 // tensor memory.  Where they do not (BN = 256), the accumulators overlap by
 // kShared columns: the epilogue reads those first and announces them on
 // `shared_free`, and the next tile's MMAs wait for that.
+//
+// Where the last wave of tiles fills at most half of the pairs and the K loop
+// is long, each of its tiles runs as slices of the K loop on several pairs.
 template <int kFmt, int BN, int STAGES, int EPI>
 struct PairCfg {
   static constexpr int kKt = stage_ktiles<kFmt>();
@@ -810,6 +820,86 @@ __device__ __forceinline__ TileAt tile_at(int64_t t, int64_t num_m, int64_t num_
   const int64_t r = t - g * group * num_n;
   const int64_t rows = min(group, num_m - g * group);
   return {static_cast<int>(g * group + r % rows), static_cast<int>(r / rows)};
+}
+
+// The t-th unit of work: a whole tile, or a slice of a tail tile's K loop.
+struct Unit {
+  int64_t tile;
+  int kb0, kb1, slice;
+  bool sliced;
+};
+__device__ __forceinline__ Unit unit_at(const Fp4GemmParams& p, int64_t t, int num_kb) {
+  if (t < p.t_full) return {t, 0, num_kb, 0, false};
+  const int64_t v = t - p.t_full;
+  const int per = (num_kb + p.s_tail - 1) / p.s_tail;
+  const int slice = static_cast<int>(v % p.s_tail);
+  const int kb0 = min(num_kb, slice * per);
+  return {p.t_full + v / p.s_tail, kb0, min(num_kb, kb0 + per), slice, true};
+}
+
+// One box of a slice's accumulator: 16-byte stores, lane after lane.
+__device__ __forceinline__ void store_partial(float* region, const uint32_t (&ra)[32],
+                                              const uint32_t (&rb)[32], int lane) {
+  uint4* dst = reinterpret_cast<uint4*>(region) + lane;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    __stcg(dst + q * 32, make_uint4(ra[4 * q], ra[4 * q + 1], ra[4 * q + 2], ra[4 * q + 3]));
+    __stcg(dst + (8 + q) * 32, make_uint4(rb[4 * q], rb[4 * q + 1], rb[4 * q + 2], rb[4 * q + 3]));
+  }
+}
+
+// Adds one slice's partial of a box to the accumulator in ra and rb.
+__device__ __forceinline__ void add_partial(const float* region, uint32_t (&ra)[32],
+                                            uint32_t (&rb)[32], int lane) {
+  const float4* src = reinterpret_cast<const float4*>(region) + lane;
+  float4 v[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) v[q] = __ldcg(src + q * 32);  // all in flight
+  auto add = [](uint32_t& r, float x) { r = __float_as_uint(__uint_as_float(r) + x); };
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    uint32_t* r = q < 8 ? ra + 4 * q : rb + 4 * (q - 8);
+    add(r[0], v[q].x);
+    add(r[1], v[q].y);
+    add(r[2], v[q].z);
+    add(r[3], v[q].w);
+  }
+}
+
+// Announce this warp's partials and wait, bounded, for those of the other
+// slices.  The slices of a tile are the last units of different pairs, all
+// resident, so the wait cannot block on itself.
+__device__ __forceinline__ bool wait_for_slices(int* ticket, int slices, volatile int* abort_flag,
+                                                int lane) {
+  __threadfence();
+  __syncwarp();
+  bool in = true;
+  if (lane == 0) {
+    atomicAdd(ticket, 1);
+    const uint64_t t0 = global_timer_ns();
+    int seen;
+    while (true) {
+      asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(ticket) : "memory");
+      if (seen >= slices) break;
+      if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
+        in = false;
+        break;
+      }
+      __nanosleep(64);
+    }
+  }
+  in = __shfl_sync(0xFFFFFFFFu, in ? 1 : 0, 0) != 0;
+  __threadfence();
+  return in;
+}
+
+// The last slice to finish clears both counters for the next call.
+__device__ __forceinline__ void finish_slices(int* ticket, int slices, int lane) {
+  __syncwarp();
+  if (lane == 0 && atomicAdd(ticket + 1, 1) == slices - 1) {
+    atomicExch(ticket, 0);
+    atomicExch(ticket + 1, 0);
+  }
 }
 
 template <int kFmt, int BN, int STAGES, int EPI>
@@ -854,6 +944,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
   const int64_t num_tiles = num_m * num_n;
   const int64_t group = p.N >= p.M ? num_m : 4;
   const int num_kb = static_cast<int>((p.K + kBK - 1) / kBK);
+  const int64_t num_units = p.t_full + (num_tiles - p.t_full) * p.s_tail;
   // MMAs of the last stage; what follows K is zero in the codes and is not multiplied.
   const int last_steps = static_cast<int>((p.K - int64_t(num_kb - 1) * kBK + kMmaK - 1) / kMmaK);
 
@@ -898,11 +989,12 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int64_t t = pair; ok && t < num_tiles; t += num_pairs) {
-        const TileAt at = tile_at(t, num_m, num_n, group);
+      for (int64_t t = pair; ok && t < num_units; t += num_pairs) {
+        const Unit u = unit_at(p, t, num_kb);
+        const TileAt at = tile_at(u.tile, num_m, num_n, group);
         const int m0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM;
         const int n0 = at.n * BN;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
             ok = false;
             break;
@@ -946,7 +1038,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       uint32_t acc_phase = 0, shared_phase = 0;
       bool ok = true;
       bool issued = false;
-      for (int64_t t = pair; ok && t < num_tiles; t += num_pairs) {
+      for (int64_t t = pair; ok && t < num_units; t += num_pairs) {
         ok = warp_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag);
         if constexpr (C::kOverlap) {
           // The columns shared with the tile before this one (none before the first).
@@ -957,11 +1049,12 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
         }
         if (!ok) break;
         tc_fence_after_sync();
+        const Unit u = unit_at(p, t, num_kb);
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAcc1);
         const uint32_t sfb =
             tmem_base + C::kSfb +
-            static_cast<uint32_t>(tile_at(t, num_m, num_n, group).n * BN % 128 / 32);
-        for (int kb = 0; kb < num_kb; ++kb) {
+            static_cast<uint32_t>(tile_at(u.tile, num_m, num_n, group).n * BN % 128 / 32);
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           ok = warp_wait(&full[stage], phase, abort_flag);
           if (!ok) break;
           tc_fence_after_sync();
@@ -987,7 +1080,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
               mma_fp4_pair<kFmt>(d_tmem, a_desc + static_cast<uint64_t>(2 * k),
                                  b_desc + static_cast<uint64_t>(2 * k), idesc,
                                  tmem_base + C::kSfa + 4 * kt, sfb + 4 * C::kRowTiles * kt,
-                                 (kb > 0 || k > 0) ? 1u : 0u);
+                                 (kb > u.kb0 || k > 0) ? 1u : 0u);
             };
             if (kb + 1 < num_kb || last_steps == 4) {
 #pragma unroll
@@ -1033,8 +1126,18 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
     uint8_t* box = sEpi + (warp - 2) * C::kBoxBytes;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int64_t t = pair; t < num_tiles; t += num_pairs) {
-      const TileAt at = tile_at(t, num_m, num_n, group);
+    // This warp's place among the epilogue warps of the tail tiles, and one of
+    // its boxes' partial (2048 floats) of a slice.
+    auto warp_slot = [&](const Unit& u) {
+      return static_cast<int>(u.tile - p.t_full) * 2 * EPI + static_cast<int>(rank) * EPI + part * 4 + quarter;
+    };
+    auto partial_of = [&](const Unit& u, int slice, int i) {
+      const int64_t tail = (u.tile - p.t_full) * p.s_tail + slice;
+      return p.partials + ((tail * 8 + static_cast<int>(rank) * 4 + quarter) * (BN / 64) + i) * 2048;
+    };
+    for (int64_t t = pair; t < num_units; t += num_pairs) {
+      const Unit u = unit_at(p, t, num_kb);
+      const TileAt at = tile_at(u.tile, num_m, num_n, group);
       const int row0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM + quarter * 32;
       const int64_t n0 = static_cast<int64_t>(at.n) * BN;
       const bool ready =
@@ -1052,8 +1155,10 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
         const int i = part * C::kGroups + (C::kOverlap && acc == 0 ? C::kGroups - 1 - g : g);
         const int64_t col0 = n0 + 64 * i;
         const bool live = row0 < p.M && col0 < p.N;
+        // A slice keeps every s_tail-th box of a warp and hands over the others.
+        const bool kept = u.sliced && i % p.s_tail == u.slice;
         uint32_t ra[32], rb[32];
-        if (live) {
+        if (live && !kept) {
           tmem_load_32cols(t_row + 64 * i, ra);
           tmem_load_32cols(t_row + 64 * i + 32, rb);
           tmem_load_wait();
@@ -1066,7 +1171,28 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
             if (g == C::kGroups - 1) mbar_arrive_cluster_tmem(acc_empty_even + 8u * acc);
           }
         }
-        if (live) store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
+        if (live && !u.sliced) store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
+        if (live && u.sliced && !kept) store_partial(partial_of(u, u.slice, i), ra, rb, lane);
+      }
+      if (u.sliced && row0 < p.M) {
+        // The pair's last unit: its accumulator stays where it is.
+        int* ticket = p.tickets + 2 * warp_slot(u);
+        if (!wait_for_slices(ticket, p.s_tail, abort_flag, lane)) {
+          if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
+          break;
+        }
+        for (int i = part * C::kGroups; i < (part + 1) * C::kGroups; ++i) {
+          const int64_t col0 = n0 + 64 * i;
+          if (i % p.s_tail != u.slice || col0 >= p.N) continue;
+          uint32_t ra[32], rb[32];
+          tmem_load_32cols(t_row + 64 * i, ra);
+          tmem_load_32cols(t_row + 64 * i + 32, rb);
+          tmem_load_wait();
+          for (int o = 0; o < p.s_tail; ++o)  // always in this order
+            if (o != u.slice) add_partial(partial_of(u, o, i), ra, rb, lane);
+          store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
+        }
+        finish_slices(ticket, p.s_tail, lane);
       }
       if (++acc == 2) {
         acc = 0;
@@ -1232,8 +1358,14 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
                        bytes, stream, f.split, false, tmA, tmSa, p, t, f.split, f.stages);
 }
 
+// K blocks of a tile that slicing the last wave has to save: joining the
+// slices costs about 5 us, a block takes 0.34.  4096 x 4096 x 16384: 89.6 us
+// against 95.8, 6400 x 1600 x 12288 51.8 against 56.7, but 4096 x 4096 x 4096
+// 32.0 against 30.0.
+constexpr int kTailMinBlocks = 16;
+
 template <int kFmt, int BN, int STAGES, int EPI>
-cudaError_t run_pair(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p,
+cudaError_t run_pair(const Fp4View& a, const Fp4View& b, Fp4GemmParams p, size_t split_bytes,
                      const DeviceInfo& dev, cudaStream_t stream) {
   using C = PairCfg<kFmt, BN, STAGES, EPI>;
   CUtensorMap tmA, tmB, tmSa, tmSb, tmD;
@@ -1254,7 +1386,20 @@ cudaError_t run_pair(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p,
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + BN - 1) / BN);
   const int64_t slots = dev.num_sms / 2;
-  const unsigned pairs = static_cast<unsigned>(tiles < slots ? tiles : slots);
+  p.t_full = tiles;
+  p.s_tail = 1;
+  const int64_t tail = tiles % slots, num_kb = (p.K + kBK - 1) / kBK;
+  if (tail > 0 && p.partials != nullptr) {
+    int64_t ways = slots / tail < 4 ? slots / tail : 4;
+    const int64_t fit = static_cast<int64_t>(split_bytes) / (tail * 2 * kBM * BN * 4);
+    if (fit < ways) ways = fit;
+    if (ways >= 2 && num_kb * (ways - 1) >= kTailMinBlocks * ways && tail * 4 * EPI <= kWsTickets) {
+      p.t_full = tiles - tail;
+      p.s_tail = static_cast<int>(ways);
+    }
+  }
+  const int64_t units = p.t_full + (tiles - p.t_full) * p.s_tail;
+  const unsigned pairs = static_cast<unsigned>(units < slots ? units : slots);
   set_error_site("gemm_fp4_pair_kernel");
   return launch_kernel(kernel, dim3(2 * pairs), dim3(64 + 32 * EPI), C::kSmemBytes, stream, 2, false,
                        tmA, tmB, tmSa, tmSb, tmD, p);
@@ -1274,8 +1419,8 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
   // 4096 x 4096 x 512 11.3 us against 13.1, 777 x 4801 x 1600 10.3 against
   // 12.3, but 12288 x 6400 x 1600 62.6 against 58.3.
-  if (!p.vec || g.K <= 2 * kBK) return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, dev, stream);
-  return run_pair<kFmt, 256, 5, 4>(g.a, g.b, p, dev, stream);
+  if (!p.vec || g.K <= 2 * kBK) return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
+  return run_pair<kFmt, 256, 5, 4>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
 }
 
 }  // namespace
@@ -1292,6 +1437,8 @@ Fp4GemmParams base_params(const Fp4GemmArgs& g) {
   p.d = static_cast<uint16_t*>(g.d);
   p.ldd = g.ldd;
   p.err = g.ws_error;
+  p.partials = g.ws_split;
+  p.tickets = g.ws_tickets;
   p.vec = (reinterpret_cast<uintptr_t>(g.d) & 15u) == 0 && g.ldd % 8 == 0;
   return p;
 }

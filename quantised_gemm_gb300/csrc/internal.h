@@ -367,6 +367,9 @@ struct Fp4GemmArgs {
   int64_t ldd;
   int* ws_error;
   bool b_early = false;  // the kernel before this one in the stream does not write b
+  int* ws_tickets = nullptr;  // as GemmArgs': no K split of a last wave without
+  float* ws_split = nullptr;
+  size_t ws_split_bytes = 0;
 };
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& g, const DeviceInfo& dev, cudaStream_t stream);
 // x's quantisation and the product in one launch, for few tokens (g.a: x's

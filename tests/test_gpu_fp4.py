@@ -303,6 +303,42 @@ def test_product(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+@pytest.mark.parametrize("M,N,K", [(2300, 2400, 6000), (1030, 1400, 8192), (4096, 1600, 5000),
+                                   (2049, 513, 20000)])
+def test_product_split_over_its_last_wave(M, N, K, fmt):
+    """Long K loops whose last tiles run as slices: the same as a workspace
+    without room for partials gives, within the bound, and the same bits again."""
+    import quantised_gemm_gb300 as q
+    from quantised_gemm_gb300 import _lib
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def one(rows, std):
+        t = q.Fp4Tensor(rows, K, fmt)
+        q.fp4_quantise((torch.randn((rows, K), generator=g, device="cuda") * std).to(torch.bfloat16), t,
+                       None, q.Workspace())
+        return t, q.fp4_dequantise(t, torch.empty((rows, K), device="cuda"))
+
+    (a, va), (b, vb) = one(M, 1.0), one(N, 0.02)
+    ws = q.Workspace()
+    out = q.fp4_gemm(a, b, torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), ws)
+    q.check(ws)
+    ref = (va.double() @ vb.double().t()).cpu().numpy()
+    s = (va.abs().double() @ vb.abs().double().t()).cpu().numpy()
+    assert_within_bound(bf16_to_f64(out), ref, s, "split product")
+    for _ in range(3):
+        assert torch.equal(q.fp4_gemm(a, b, torch.empty_like(out), ws), out)
+    room = torch.full((M, N + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    q.fp4_gemm(a, b, room[:, 1:N + 1], ws)
+    assert (room[:, 0] == 5).all() and (room[:, N + 1:] == 5).all()
+    assert_within_bound(bf16_to_f64(room[:, 1:N + 1]), ref, s, "split product, unaligned rows")
+    whole = torch.empty_like(out)
+    st = q.library().fp8lin_fp4_gemm(a._ref, b._ref, whole.data_ptr(), N, ws.ptr, 32768, q._stream())
+    assert st == _lib.OK
+    assert_within_bound(bf16_to_f64(whole), ref, s, "whole product")
+    q.check(ws)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
 def test_product_of_small_whole_numbers_is_exact(fmt):
     # Values 0, +-1, +-2 in blocks whose maximum is 2: a product of whole numbers below 2^8.
     import quantised_gemm_gb300 as q
