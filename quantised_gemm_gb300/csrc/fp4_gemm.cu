@@ -509,7 +509,6 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
     fence_barrier_init();
   }
   griddep_wait();
-  griddep_launch_dependents();
 
   // ------------------------------------------------------------ the tokens
   // Their loads go out before the weight's, behind which they would wait.
@@ -587,6 +586,9 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
     }
   }
   __syncthreads();  // the table is filled and the scale tiles are zero
+  // Only now that this CTA has its tensor memory: a CTA of the next launch
+  // that took the last of it while waiting for this grid would never get on.
+  griddep_launch_dependents();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int u = threadIdx.x + k * kFusedThreads;

@@ -303,8 +303,8 @@ def test_product(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
-@pytest.mark.parametrize("M,N,K", [(2300, 2400, 6000), (1030, 1400, 8192), (4096, 1600, 5000),
-                                   (2049, 513, 20000)])
+@pytest.mark.parametrize("M,N,K", [(2300, 2400, 6000), (4096, 1600, 9000), (2500, 2500, 7000),
+                                   (1030, 1400, 8192), (2049, 513, 20000)])
 def test_product_split_over_its_last_wave(M, N, K, fmt):
     """Long K loops whose last tiles run as slices: the same as a workspace
     without room for partials gives, within the bound, and the same bits again."""
@@ -505,14 +505,14 @@ def test_cached_weight():
     wb, _ = make(64, 128, 2)
     x, w = to_dev_bf16(xb), to_dev_bf16(wb)
     y = lin.forward(x, w).clone()
-    n0 = q.launch_count()
+    kept = lin.w4.codes.clone()
+    lin.w4.codes.zero_()
+    assert (lin.forward(x, w) == 0).all()      # the weight's 4-bit copy is used as it is
+    lin.w4.codes.copy_(kept)
     assert torch.equal(lin.forward(x, w), y)
-    cached = q.launch_count() - n0
-    w.mul_(2.0)
-    n0 = q.launch_count()
-    y2 = lin.forward(x, w)
-    assert q.launch_count() - n0 > cached
-    assert torch.equal(y2, y * 2)
+    w.mul_(2.0)                                # a new version of w is quantised
+    lin.w4.codes.zero_()
+    assert torch.equal(lin.forward(x, w), y * 2)
 
 
 def test_python_refusals():
