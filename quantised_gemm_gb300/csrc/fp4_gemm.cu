@@ -151,22 +151,37 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
   *abort_flag = 1;
 }
 
+// Where a K loop is shared by a cluster, its CTAs own the rows of the tile in
+// turn: `split` parts of kBM / split rows.  Each CTA's `joined` holds the
+// partials of its own rows, [split][BN][rows] floats, which the CTAs write
+// into it: one cluster barrier, and nothing is read across CTAs.
+template <int BN>
+constexpr size_t joined_bytes(int split) {
+  return split > 1 ? static_cast<size_t>(kBM) * BN * 4 : 0;
+}
+
 // The epilogue of one tile for one of four warps: its 32 rows of the
-// accumulator to D, or, where the K loop is shared, to the CTA's partial.
-__device__ __forceinline__ void few_epilogue(const Fp4GemmParams& p, uint32_t tmem_base, float* partial,
-                                             bool shared, bool any, int64_t row0, int cols,
+// accumulator to D, or, where the K loop is shared, to their owners.
+template <int BN>
+__device__ __forceinline__ void few_epilogue(const Fp4GemmParams& p, uint32_t tmem_base, float* joined,
+                                             int split, int rank, bool any, int64_t row0, int cols,
                                              float alpha, uint16_t* d, int quarter, int lane) {
   const int r = quarter * 32 + lane;
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+  const int rows = kBM / split;
+  const uint32_t to = split > 1 ? map_to_cta(smem_addr(joined + (rank * BN * rows + r % rows)),
+                                             static_cast<uint32_t>(r / rows))
+                                : 0u;
 #pragma unroll 1
   for (int c0 = 0; c0 < cols; c0 += 16) {
     uint32_t v[16];
     tmem_load_16cols(t_row + c0, v);
     tmem_load_wait();
-    if (shared) {
+    if (split > 1) {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        partial[(c0 + j) * kBM + r] = any ? __uint_as_float(v[j]) : 0.0f;
+        if (c0 + j < cols)
+          st_shared_cluster_u32(to + static_cast<uint32_t>((c0 + j) * rows) * 4u, any ? v[j] : 0u);
     } else if (row0 + r < p.M) {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
@@ -177,34 +192,28 @@ __device__ __forceinline__ void few_epilogue(const Fp4GemmParams& p, uint32_t tm
   }
 }
 
-// This CTA's part of a tile, added up over the cluster's partials in rank
-// order.
-__device__ __forceinline__ void join_partials(const Fp4GemmParams& p, const float* partial, int split,
+// This CTA's rows of a tile, added up over the partials in rank order, four
+// rows a thread.
+template <int BN>
+__device__ __forceinline__ void join_partials(const Fp4GemmParams& p, const float* joined, int split,
                                               int rank, int64_t row0, int cols, float alpha,
                                               uint16_t* d) {
-  // Rows of the tile are dealt to the cluster's CTAs, four a thread.
-  const int quads = kBM / split / 4, mine = rank * (kBM / split);
-  const uint32_t base = smem_addr(partial);
+  const int rows = kBM / split, quads = rows / 4;
   const bool wide = p.vec && row0 + kBM <= p.M;
-#pragma unroll 2
   for (int e = threadIdx.x; e < quads * cols; e += blockDim.x) {
-    const int c = e / quads, r = mine + e % quads * 4;
-    const uint32_t at = base + static_cast<uint32_t>(c * kBM + r) * 4u;
-    float4 v[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-      if (s < split) v[s] = ld_shared_cluster_f32x4(map_to_cta(at, s));
-    float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-    for (int s = 1; s < 8; ++s)
-      if (s < split) {
-        sum[0] += v[s].x;
-        sum[1] += v[s].y;
-        sum[2] += v[s].z;
-        sum[3] += v[s].w;
-      }
-    const uint32_t lo = cvt_bf16x2(__fmul_rn(sum[0], alpha), __fmul_rn(sum[1], alpha));
-    const uint32_t hi = cvt_bf16x2(__fmul_rn(sum[2], alpha), __fmul_rn(sum[3], alpha));
+    const int c = e / quads, q = e % quads * 4;
+    const float* src = joined + c * rows + q;
+    float4 sum = *reinterpret_cast<const float4*>(src);
+    for (int s = 1; s < split; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(src + s * BN * rows);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    const uint32_t lo = cvt_bf16x2(__fmul_rn(sum.x, alpha), __fmul_rn(sum.y, alpha));
+    const uint32_t hi = cvt_bf16x2(__fmul_rn(sum.z, alpha), __fmul_rn(sum.w, alpha));
+    const int r = rank * rows + q;
     uint16_t* dst = d + c * p.ldd + r;
     if (wide) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
@@ -222,9 +231,11 @@ __device__ __forceinline__ void join_partials(const Fp4GemmParams& p, const floa
 // One 128 x BN tile of D^T a cluster: A, the operand that fills the MMA's 128
 // rows, is the weight, and B the tokens, BN of them.  The cluster's CTAs
 // share the K loop: each multiplies its share of the stages into an fp32
-// partial, leaves it in shared memory, and after a cluster barrier each CTA
-// adds up its part of the tile over all partials in rank order -- the same
+// partial and writes the rows of it to their owners' shared memory; after a
+// cluster barrier each CTA adds up its own rows in rank order -- the same
 // bits every time -- and writes D.  No workspace and no second launch.
+// (Reading the other CTAs' partials after the barrier instead took 1.5 us
+// more of 32 x 4096 x 14336.)
 //
 // Bound by reading the weight (0.56 bytes a value): the split brings enough
 // CTAs, two an SM, to keep that many loads in flight.  With `early` the
@@ -241,8 +252,8 @@ struct FewCfg {
   static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : BN + 32 <= 128 ? 128 : 256;
   static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes + 256;
   static_assert(BN % 16 == 0 && BN <= 128, "one row of scale tiles for B");
-  static_assert(STAGES * (kABytes + kBBytes) >= kBM * BN * 4, "the partial fits the stages");
-  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs an SM");
+  // Two CTAs an SM; with tiles of 64 columns a shared K loop has one.
+  static_assert(2 * (kSmemBytes + (BN <= 32 ? joined_bytes<BN>(2) : 0) + 1024) <= 233472, "fits");
 };
 
 template <int kFmt, int BN, int STAGES>
@@ -261,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* sB = sA + STAGES * C::kABytes;
   uint8_t* sSa = sB + STAGES * C::kBBytes;
   uint8_t* sSb = sSa + STAGES * C::kScBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSb + STAGES * C::kScBytes);
+  float* joined = reinterpret_cast<float*>(sSb + STAGES * C::kScBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(joined) + joined_bytes<BN>(split));
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* drain = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* partial = reinterpret_cast<float*>(sA);  // [BN][128] over the stages, once the MMAs are done
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -304,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if (split > 1) cluster_started_arrive();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();
   griddep_launch_dependents();
@@ -381,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   }
 
+  __syncwarp();
+  if (split > 1) cluster_started_wait();  // before anything is written to another CTA
   const int cols = static_cast<int>(min(int64_t(BN), p.N - int64_t(n_blk) * BN));  // live tokens
   const int64_t row0 = static_cast<int64_t>(m_blk) * kBM;
   const float alpha =
@@ -394,14 +408,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
     } else {
       tc_fence_after_sync();
-      few_epilogue(p, tmem_base, partial, split > 1, nkb > 0, row0, cols, alpha, d, quarter, lane);
+      few_epilogue<BN>(p, tmem_base, joined, split, rank, nkb > 0, row0, cols, alpha, d, quarter, lane);
     }
   }
   if (split > 1) {
     tc_fence_before_sync();
-    cluster_sync_all();  // every partial is in place
-    join_partials(p, partial, split, rank, row0, cols, alpha, d);
-    cluster_sync_all();  // no CTA leaves while its partial is read
+    cluster_sync_all();  // every partial is with its rows' owner
+    join_partials<BN>(p, joined, split, rank, row0, cols, alpha, d);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -438,13 +451,13 @@ struct FusedCfg {
   static constexpr int kSfa = BN;
   static constexpr int kSfb = kSfa + 16;
   static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : 128;
-  // Stages beside the tokens of nkb K blocks (the partial needs one stage).
-  static int stages(int64_t nkb, size_t smem) {
-    const int64_t left = int64_t(smem) - kFixed - nkb * (kBBytes + kScBytes);
+  // Stages beside the tokens of nkb K blocks.
+  static int stages(int64_t nkb, int split, size_t smem) {
+    const int64_t left = int64_t(smem) - kFixed - int64_t(joined_bytes<BN>(split)) -
+                         nkb * (kBBytes + kScBytes);
     const int64_t n = left / kRingBytes;
     return static_cast<int>(n < 0 ? 0 : n > nkb ? nkb : n > kMaxStages ? kMaxStages : n);
   }
-  static_assert(kABytes >= kBM * BN * 4, "the partial fits one stage of A");
 };
 
 struct FusedTokens {
@@ -482,7 +495,8 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
   uint8_t* sB = sA + stages * C::kABytes;    // [per] K blocks of the tokens' codes
   uint8_t* sSa = sB + per * C::kBBytes;
   uint8_t* sSb = sSa + stages * C::kScBytes;  // [per] K blocks of their scale tiles
-  float* table = reinterpret_cast<float*>(sSb + per * C::kScBytes);
+  float* joined = reinterpret_cast<float*>(sSb + per * C::kScBytes);
+  float* table = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(joined) + joined_bytes<BN>(split));
   uint64_t* full = reinterpret_cast<uint64_t*>(table + 128);
   uint64_t* empty = full + C::kMaxStages;
   uint64_t* acc_full = empty + C::kMaxStages;
@@ -491,7 +505,6 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* red = tmem_slot + 2;   // [8] warps' maxima
   uint32_t* cta_max = red + 8;     // read by the cluster
-  float* partial = reinterpret_cast<float*>(sA);
 
   auto load_a = [&](int stage, int kb) {
     mbar_arrive_expect_tx(&full[stage], C::kRingBytes);
@@ -508,6 +521,8 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  __syncwarp();
+  if (split > 1) cluster_started_arrive();
   griddep_wait();
 
   // ------------------------------------------------------------ the tokens
@@ -542,6 +557,8 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
   // Scale tiles hold 128 rows; those past the tokens are zero.
   for (int i = threadIdx.x; i < nkb * C::kScBytes / 16; i += kFusedThreads)
     reinterpret_cast<uint4*>(sSb)[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+  if (split > 1) cluster_started_wait();  // before anything is written to another CTA
   uint32_t m = 0;
   if (find && whole && split > 1) {
 #pragma unroll
@@ -702,14 +719,13 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
       if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
     } else {
       tc_fence_after_sync();
-      few_epilogue(p, tmem_base, partial, split > 1, nkb > 0, row0, cols, alpha, d, warp & 3, lane);
+      few_epilogue<BN>(p, tmem_base, joined, split, rank, nkb > 0, row0, cols, alpha, d, warp & 3, lane);
     }
   }
   if (split > 1) {
     tc_fence_before_sync();
-    cluster_sync_all();  // every partial is in place
-    join_partials(p, partial, split, rank, row0, cols, alpha, d);
-    cluster_sync_all();  // no CTA leaves while its partial is read
+    cluster_sync_all();  // every partial is with its rows' owner
+    join_partials<BN>(p, joined, split, rank, row0, cols, alpha, d);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -1288,7 +1304,7 @@ cudaError_t run_few(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
     return map_failed("fp4 gemm operand");
   auto* kernel = gemm_fp4_few_kernel<kFmt, BN, STAGES>;
   static bool done[64] = {};
-  cudaError_t e = allow_smem(kernel, C::kSmemBytes, dev, done);
+  cudaError_t e = allow_smem(kernel, C::kSmemBytes + joined_bytes<BN>(2), dev, done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((p.M + kBM - 1) / kBM) * ((p.N + BN - 1) / BN);
   // Two CTAs an SM where the weight's loads bound it (up to 32 tokens); one
@@ -1296,8 +1312,8 @@ cudaError_t run_few(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   const int split = few_split(tiles, p.K, (BN <= 32 ? 2 : 1) * int64_t(dev.num_sms));
   set_error_site("gemm_fp4_few_kernel");
   return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * split)), dim3(kThreads),
-                       C::kSmemBytes, stream, split, false, tmA, tmB, tmSa, tmSb, p, split,
-                       g.b_early);
+                       C::kSmemBytes + joined_bytes<BN>(split), stream, split, false, tmA, tmB, tmSa,
+                       tmSb, p, split, g.b_early);
 }
 
 // How the fused product runs these sizes; stages 0: it does not.
@@ -1312,13 +1328,13 @@ FusedPlan plan_fused(const Fp4GemmArgs& g, const DeviceInfo& dev) {
   // Tiles for most SMs: one CTA each, with all of its shared memory for loads
   // in flight and nothing to join.
   if (2 * tiles > dev.num_sms && g.M * num_kb * 16 <= kFusedUnits) {
-    const int n = C::stages(num_kb, kFusedSmemFull);
+    const int n = C::stages(num_kb, 1, kFusedSmemFull);
     if (n >= num_kb || n >= 6) return {1, static_cast<int>(num_kb), n};
   }
   const int split = few_split(tiles, g.K, 2 * int64_t(dev.num_sms));
   const int64_t per = (num_kb + split - 1) / split;
   if (g.M * per * 16 > kFusedUnits) return {split, 0, 0};  // the values would not stay in registers
-  const int n = C::stages(per, kFusedSmemHalf);
+  const int n = C::stages(per, split, kFusedSmemHalf);
   return {split, static_cast<int>(per), n >= per || n >= 3 ? n : 0};
 }
 
@@ -1352,7 +1368,8 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
   static bool done[3][64] = {};
   cudaError_t e = allow_smem(kernel, kFusedSmemFull, dev, done[align]);
   if (e != cudaSuccess) return e;
-  const size_t bytes = C::kFixed + static_cast<size_t>(f.stages) * C::kRingBytes +
+  const size_t bytes = C::kFixed + joined_bytes<BN>(f.split) +
+                       static_cast<size_t>(f.stages) * C::kRingBytes +
                        static_cast<size_t>(f.per) * (C::kBBytes + C::kScBytes);
   const int64_t tiles = (p.M + kBM - 1) / kBM;
   set_error_site("gemm_fp4_fused_kernel");
@@ -1414,7 +1431,7 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   // 512 x 4096 x 4096 takes 10.6 us there and 11.7 us in pairs, 1024 x 4096 x
   // 4096 (two waves) 20.0 and 11.7.
   if (g.M <= 16) return run_few<kFmt, 16, 4>(g, p, dev, stream);
-  if (g.M <= 32) return run_few<kFmt, 32, 4>(g, p, dev, stream);
+  if (g.M <= 32) return run_few<kFmt, 32, kFmt == 0 ? 3 : 4>(g, p, dev, stream);
   if ((g.M + 63) / 64 * ((g.N + kBM - 1) / kBM) <= 2 * int64_t(dev.num_sms))
     return run_few<kFmt, 64, 3>(g, p, dev, stream);
   // Eight epilogue warps where writing a tile takes longer than multiplying
