@@ -141,6 +141,25 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The two halves of a cluster barrier, without ordering memory: after the
+// wait, every CTA of the cluster has started, and its shared memory may be
+// written.
+__device__ __forceinline__ void cluster_started_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on a barrier of the pair with a release at CTA scope, which waits for
+// no memory operation of this thread outside the CTA: for an arrival that
+// hands over tensor memory, ordered by the tcgen05 fences around it.  The
+// cluster-scope release costs about a microsecond beside TMA stores in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_saddr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr)
+               : "memory");
+}
+
 // A bounded wait of the whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag));

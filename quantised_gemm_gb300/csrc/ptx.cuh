@@ -293,15 +293,6 @@ __device__ __forceinline__ void cluster_sync_all() {
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The two halves, without ordering memory: after the wait, every CTA of the
-// cluster has started, and its shared memory may be written.
-__device__ __forceinline__ void cluster_started_arrive() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_started_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Address of the same shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t local_saddr, uint32_t rank) {
   uint32_t r;
@@ -313,16 +304,6 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t local_saddr, uint32_t ra
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_saddr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_saddr) : "memory");
-  return v;
-}
-
-// 16-byte load from shared memory of a CTA of the cluster.
-__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_saddr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_saddr)
-               : "memory");
   return v;
 }
 
@@ -341,15 +322,6 @@ __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) 
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_saddr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr)
-               : "memory");
-}
-
-// The same with a release at CTA scope, which waits for no memory operation of
-// this thread outside the CTA: for an arrival that hands over tensor memory,
-// ordered by the tcgen05 fences around it.  The cluster-scope release costs
-// about a microsecond beside TMA stores in flight.
-__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_saddr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr)
                : "memory");
 }
 
