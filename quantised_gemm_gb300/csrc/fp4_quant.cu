@@ -286,17 +286,21 @@ struct AmaxParams {
   int64_t rows, cols, ld;
   uint32_t* partials;
   int ctas;
+  int lanes_log2;  // lanes of a warp that share a row
 };
 struct AmaxPair {
   AmaxParams p[2];
 };
 
 // The largest magnitude of a thread's share of a tensor: warp `first` of
-// `warps` takes 512 values of a row at a time, kLoads of these in flight.
+// `warps` takes 512 values at a time, kLoads of these in flight: of one row,
+// or 16 values a lane of several narrow ones.
 template <int kAlign, int kLoads>
 __device__ __forceinline__ uint32_t share_max(const AmaxParams& p, int64_t first, int64_t warps) {
-  const int64_t per_row = (p.cols + 511) >> 9, total = p.rows * per_row;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, lg = p.lanes_log2;
+  const int64_t per_row = (p.cols + (16 << lg) - 1) >> (4 + lg);
+  const int64_t total = ((p.rows + (32 >> lg) - 1) >> (5 - lg)) * per_row;
+  const int own_row = lane >> lg, own_col = (lane & ((1 << lg) - 1)) * 16;
   uint32_t m = 0;
   for (int64_t i = first; i < total; i += kLoads * warps) {
     uint4 v[kLoads][2];
@@ -304,10 +308,10 @@ __device__ __forceinline__ uint32_t share_max(const AmaxParams& p, int64_t first
     for (int k = 0; k < kLoads; ++k) {
       v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
       const int64_t seg = i + k * warps;
-      if (seg < total) {
-        const int64_t row = p.rows == 1 ? 0 : seg / per_row;
-        load16<kAlign>(p.x + row * p.ld, (seg - row * per_row) * 512 + lane * 16, p.cols, v[k]);
-      }
+      const int64_t group = p.rows == 1 ? 0 : per_row == 1 ? seg : seg / per_row;
+      const int64_t row = (group << (5 - lg)) + own_row;
+      if (seg < total && row < p.rows)
+        load16<kAlign>(p.x + row * p.ld, ((seg - group * per_row) << (4 + lg)) + own_col, p.cols, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < kLoads; ++k)
@@ -514,6 +518,8 @@ AmaxParams amax_params(const Fp4QuantArgs& a) {
   p.rows = one ? 1 : a.rows;
   p.cols = one ? a.rows * a.cols : a.cols;
   p.ld = one ? 0 : a.ld;
+  p.lanes_log2 = 5;
+  while (p.lanes_log2 > 0 && p.cols <= (8 << p.lanes_log2)) --p.lanes_log2;
   return p;
 }
 

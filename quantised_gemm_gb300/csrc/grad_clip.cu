@@ -13,7 +13,8 @@
 // one launch made them all (a last CTA that does it costs 4 us more).
 // Squares are added in fp32 over kUnroll vectors of a thread, in pairs of
 // fp32 numbers within a CTA and in fp64 from there on, always in the same
-// order: the norm has the same bits for the same list.
+// order: the norm has the same bits for the same list.  A CTA whose squares
+// leave fp32's range goes over its share again with scaled values.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -84,19 +85,6 @@ __device__ __forceinline__ bool aligned(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-// Sum over the block in fp64, in a fixed order; the result in thread 0.
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double red[kClipThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-  if (threadIdx.x == 0)
-    for (int w = 0; w < kClipThreads / 32; ++w) s += red[w];
-  return s;
-}
-
 // The sum of the CTAs' partial sums by the block's first four warps, in a
 // fixed order; the result in thread 0.
 __device__ __forceinline__ double sum_partials(const double* partials, int count) {
@@ -147,10 +135,12 @@ struct Pair {
   }
 };
 
-// fn(square sum of kUnroll vectors or of one value) over this thread's share
-// of n values; the squares of one call are added in Acc.
-template <bool kBf16, typename Acc, typename Fn>
-__device__ __forceinline__ void square_sums(const uint8_t* base, int64_t n, Fn fn) {
+// Adds the squares of this thread's share of n values, times scale first
+// where kScaled, to acc: in fp32 over kUnroll vectors, then in the pair.  The
+// values' bits are collected in `any`.
+template <bool kBf16, bool kScaled>
+__device__ __forceinline__ void square_sums(const uint8_t* base, int64_t n, float scale, Pair& acc,
+                                            uint32_t& any) {
   constexpr int kN = Vec<kBf16>::kN;
   int64_t done = 0;
   if (aligned(base)) {
@@ -162,23 +152,26 @@ __device__ __forceinline__ void square_sums(const uint8_t* base, int64_t n, Fn f
       for (int k = 0; k < kUnroll; ++k)
         u[k] = i + k * kClipThreads < vecs ? __ldg(v + i + k * kClipThreads)
                                            : make_uint4(0, 0, 0, 0);
-      Acc s = 0;
+      float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
+        if (!kScaled) any |= u[k].x | u[k].y | u[k].z | u[k].w;
         const Vec<kBf16> x(u[k]);
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-          const Acc y = x.v[j];
-          s = fma(y, y, s);
+          const float y = kScaled ? __fmul_rn(x.v[j], scale) : x.v[j];
+          s = __fmaf_rn(y, y, s);
         }
       }
-      fn(s);
+      acc.add(s);
     }
     done = vecs * kN;
   }
   for (int64_t i = done + threadIdx.x; i < n; i += kClipThreads) {
-    const Acc y = load_one<kBf16>(base, i);
-    fn(y * y);
+    const float x = load_one<kBf16>(base, i);
+    if (!kScaled) any |= __float_as_uint(x);
+    const float y = kScaled ? __fmul_rn(x, scale) : x;
+    acc.add(__fmul_rn(y, y));
   }
 }
 
@@ -196,40 +189,52 @@ __global__ void __launch_bounds__(kClipThreads, 2048 / kClipThreads)
   griddep_wait();
   griddep_launch_dependents();
   Pair acc;
+  uint32_t any = 0;
   walk(l, [&](int t, int64_t begin, int64_t n) {
-    square_sums<kBf16, float>(static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4), n,
-                              [&](float s) { acc.add(s); });
+    square_sums<kBf16, false>(static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4), n, 1.0f,
+                              acc, any);
   });
-  double sum = 0.0;
-  // Squares that may overflow fp32 (values from 1e15 on, infinities, NaN):
-  // the CTA's share again in fp64.
+  // Squares that may overflow (values from 1e15 on, infinities, NaN) or that
+  // may lose bits to underflow (all below 1e-14, though not all zero): the
+  // share again, its values times a power of two that keeps any sum of them
+  // in range.
+  float scale = 1.0f;
   if (__syncthreads_or(!(acc.hi < 1e30f))) {
+    scale = 0x1p-80f;
+  } else if (__syncthreads_and(acc.hi < 1e-28f) &&
+             __syncthreads_or((any & (kBf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) != 0)) {
+    scale = 0x1p100f;
+  }
+  if (scale != 1.0f) {
+    acc = Pair();
     walk(l, [&](int t, int64_t begin, int64_t n) {
-      square_sums<kBf16, double>(static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4), n,
-                                 [&](double s) { sum += s; });
+      square_sums<kBf16, true>(static_cast<const uint8_t*>(l.g[t]) + begin * (kBf16 ? 2 : 4), n,
+                               scale, acc, any);
     });
-    sum = block_sum(sum);
-  } else {
-    __shared__ float2 warp_sum[kClipThreads / 32];
-    auto warp_add = [&](int from) {
+  }
+  __shared__ float2 warp_sum[kClipThreads / 32];
+  auto warp_add = [&](int from) {
 #pragma unroll
-      for (int o = from; o > 0; o >>= 1) {
-        const float hi = __shfl_down_sync(0xFFFFFFFFu, acc.hi, o);
-        const float lo = __shfl_down_sync(0xFFFFFFFFu, acc.lo, o);
-        acc.add(hi);
-        acc.lo = __fadd_rn(acc.lo, lo);
-      }
-    };
-    warp_add(16);
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = make_float2(acc.hi, acc.lo);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      const float2 w = threadIdx.x < kClipThreads / 32 ? warp_sum[threadIdx.x] : make_float2(0, 0);
-      acc.hi = w.x;
-      acc.lo = w.y;
-      warp_add(kClipThreads / 64);
-      sum = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
+    for (int o = from; o > 0; o >>= 1) {
+      const float hi = __shfl_down_sync(0xFFFFFFFFu, acc.hi, o);
+      const float lo = __shfl_down_sync(0xFFFFFFFFu, acc.lo, o);
+      acc.add(hi);
+      acc.lo = __fadd_rn(acc.lo, lo);
     }
+  };
+  warp_add(16);
+  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = make_float2(acc.hi, acc.lo);
+  __syncthreads();
+  double sum = 0.0;
+  if (threadIdx.x < 32) {
+    const float2 w = threadIdx.x < kClipThreads / 32 ? warp_sum[threadIdx.x] : make_float2(0, 0);
+    acc.hi = w.x;
+    acc.lo = w.y;
+    warp_add(kClipThreads / 64);
+    // An infinite sum has lost its error terms.
+    sum = isinf(acc.hi) ? acc.hi : static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
+    const double back = 1.0 / scale;  // a power of two
+    sum *= back * back;
   }
   __shared__ bool is_last;
   if (threadIdx.x == 0) {

@@ -184,7 +184,7 @@ class Fp4Linear:
 
     def __init__(self, M: int, K: int, N: int, *, fmt: int = NVFP4, scaling: str = "dynamic",
                  history_len: int = 16, amax_algo: int = AMAX_AUTO, eps: float = 1e-12,
-                 cache_weight: bool = False, device="cuda"):
+                 device="cuda"):
         kind = {"dynamic": DYNAMIC, "delayed": DELAYED}[scaling]
         if fmt == MXFP4 and kind == DELAYED:
             raise ValueError("MXFP4 has no tensorwise scale to delay")
@@ -205,18 +205,15 @@ class Fp4Linear:
         self.dw = torch.empty((N, K), **bf)
         self.ws = Workspace(M, K, N, device=device)
         self.sx, self.sw, self.sdy = self.x4.state, self.w4.state, self.dy4.state
-        # cache_weight: quantise W only when it changed since the last time
-        # (its storage or its in-place version counter).
-        self.cache_weight = cache_weight
-        self._w_key = None
+        self._has_w = False  # w4 and w4t hold a weight at sw's scale
 
-    def forward(self, x: torch.Tensor, w: torch.Tensor, stream=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, w: torch.Tensor | None, stream=None) -> torch.Tensor:
+        """y = x W^T; w = None: the weight of the last forward that was given
+        one, without quantising it again (micro-batches of one step)."""
         px = _dense(x, "x", self.M, self.K)
-        pw = _dense(w, "w", self.N, self.K)
-        key = ((id(w), w.data_ptr(), w._version, tuple(w.shape), w.device)
-               if self.cache_weight else None)
-        if key is not None and key == self._w_key:
-            pw = None
+        if w is None and not self._has_w:
+            raise ValueError("w is required: no weight has been quantised at the present scale")
+        pw = None if w is None else _dense(w, "w", self.N, self.K)
         st = _load().fp8lin_fp4_forward(
             px, pw, _state_arg(self.sx), _state_arg(self.sw), self.x4._ref, self.x4t._ref,
             self.w4._ref, self.w4t._ref, self.y.data_ptr(), self.ws.ptr, self.ws.nbytes,
@@ -224,8 +221,9 @@ class Fp4Linear:
         for s in (self.sx, self.sw):
             if s is not None:
                 s._pull()
+        if w is not None:
+            self._has_w = st == 0
         _lib.check(st, "fp8lin_fp4_forward")
-        self._w_key = key
         return self.y
 
     def backward(self, dy: torch.Tensor, need_dx: bool = True, need_dw: bool = True, stream=None):
@@ -240,11 +238,11 @@ class Fp4Linear:
 
     def sync_scales(self, stream=None):
         """Delayed scaling: push this step's amaxes into the histories and
-        recompute the scales; a cached W is stale after that."""
+        recompute the scales; the next forward needs its weight again."""
         delayed = [s for s in (self.sx, self.sw, self.sdy) if s is not None and s.kind == DELAYED]
         if delayed:
             scale_many(delayed, stream)
-            self._w_key = None
+            self._has_w = False
 
     def step(self, x, w, dy, stream=None):
         """One forward + backward (+ delayed sync)."""

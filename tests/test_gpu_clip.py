@@ -19,8 +19,8 @@ def norm64(grads):
 
 
 def check(q, grads, max_norm, outs=None):
-    """One call against fp64.  A thread adds at most 64 + 64 squares of a
-    chunk in fp32, each sum within 128 * 2^-24 of its squares' total, so the
+    """One call against fp64.  A thread adds at most 32 squares at a time in
+    fp32, each sum within 128 * 2^-24 of its squares' total, so the
     norm within half that; the factor adds three roundings, the value one."""
     want = norm64(grads)
     before = [g.clone() for g in grads]
@@ -106,6 +106,29 @@ def test_large_values_do_not_overflow():
                                                                device="cuda")]
     norm = q.grad_norm(g, torch.empty(1, device="cuda"), q.Workspace())
     assert abs(float(norm) / norm64(g) - 1) < 1e-6
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [1e-13, 1e-20, 1e-30, 1e-37])
+def test_small_values_do_not_underflow(scale, dtype):
+    import quantised_gemm_gb300 as q
+    grads = grads_of([(5000,), (333, 7), (3,)], (dtype,), 8, scale)
+    grads.append(torch.zeros(100_000, dtype=dtype, device="cuda"))
+    want = norm64(grads)
+    norm = torch.empty(1, device="cuda")
+    q.grad_norm(grads, norm, q.Workspace())
+    assert abs(float(norm) - want) <= (64 * 2.0 ** -24 + 2.0 ** -23) * want
+
+
+def test_small_values_beside_large_ones():
+    import quantised_gemm_gb300 as q
+    grads = grads_of([(5000,)], (torch.float32,), 9, 1e-25) + \
+        grads_of([(3000,)], (torch.float32,), 10, 1e18) + grads_of([(4000,)], (torch.float32,), 11)
+    for part in (grads, grads[::2], grads[:1], grads[1:]):
+        norm = torch.empty(1, device="cuda")
+        q.grad_norm(part, norm, q.Workspace())
+        want = norm64(part)
+        assert abs(float(norm) - want) <= (64 * 2.0 ** -24 + 2.0 ** -23) * want
 
 
 def test_empty_lists_and_tensors():

@@ -97,6 +97,22 @@ def test_strided_rows(fmt, offset, width):
         assert np.all(got[:, :offset] == 7) and np.all(got[:, offset + cols:] == 7)
 
 
+@pytest.mark.parametrize("rows,cols", [(5000, 1), (5000, 16), (9001, 17), (2000, 64), (1500, 100), (700, 130),
+                                       (600, 256), (601, 257)])
+def test_narrow_strided_rows_find_their_largest(rows, cols):
+    import quantised_gemm_gb300 as q
+    bits, x = make(rows, cols + 16, 12)
+    ws = q.Workspace()
+    for r, c in ((0, 0), (rows - 1, cols - 1), (rows // 2, cols // 2)):
+        y, b = x[:, :cols].copy(), bits.copy()
+        y[r, c], b[r, c] = -1000.0, 0xC47A
+        b[:, cols:] = 0x7F80                      # beside the rows: infinities
+        a = dirty(q, rows, cols, q.NVFP4)
+        q.fp4_quantise(to_dev_bf16(b)[:, :cols], a, None, ws)
+        assert float(a.state.amax) == 1000.0
+        check_bytes(a, y, o4.tensor_scale(1000.0)[0], "narrow")
+
+
 @pytest.mark.parametrize("algo", ["atomic", "reduction", "precomputed", "single_pass", "auto"])
 def test_dynamic_algorithms(algo):
     import quantised_gemm_gb300 as q
@@ -498,21 +514,28 @@ def test_linear_forward_backward(M, K, N, fmt, scaling):
     assert only[1] is None and (scaling == "delayed" or torch.equal(only[0], dx))
 
 
-def test_cached_weight():
+def test_kept_weight():
     import quantised_gemm_gb300 as q
-    lin = q.Fp4Linear(32, 128, 64, cache_weight=True)
+    lin = q.Fp4Linear(32, 128, 64)
     xb, _ = make(32, 128, 1)
     wb, _ = make(64, 128, 2)
     x, w = to_dev_bf16(xb), to_dev_bf16(wb)
+    with pytest.raises(ValueError):
+        lin.forward(x, None)                   # no weight yet
     y = lin.forward(x, w).clone()
     kept = lin.w4.codes.clone()
     lin.w4.codes.zero_()
-    assert (lin.forward(x, w) == 0).all()      # the weight's 4-bit copy is used as it is
+    assert (lin.forward(x, None) == 0).all()   # the weight's 4-bit copy is used as it is
     lin.w4.codes.copy_(kept)
-    assert torch.equal(lin.forward(x, w), y)
-    w.mul_(2.0)                                # a new version of w is quantised
+    assert torch.equal(lin.forward(x, None), y)
     lin.w4.codes.zero_()
-    assert torch.equal(lin.forward(x, w), y * 2)
+    assert torch.equal(lin.forward(x, w * 2.0), y * 2)  # a weight that is given is quantised
+    lin = q.Fp4Linear(32, 128, 64, scaling="delayed")
+    lin.step(x, w, x[:, :64].contiguous())
+    with pytest.raises(ValueError):
+        lin.forward(x, None)                   # its scale has moved on
+    lin.forward(x, w)
+    lin.forward(x, None)
 
 
 def test_python_refusals():
