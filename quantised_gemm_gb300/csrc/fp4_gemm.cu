@@ -820,6 +820,13 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
 //
 // Where the last wave of tiles fills at most half of the pairs and the K loop
 // is long, each of its tiles runs as slices of the K loop on several pairs.
+//
+// Bound by the tensor cores: 8192 x 14336 x 4096 takes 138 us in NVFP4 (7.0
+// PFLOP/s) and 132 us in MXFP4 (7.3), which copies half as many scale tiles;
+// the MMAs alone, without loads, take 133.  16384 x 4096 x 4096: 82 and 79 us.
+// With short K loops (12288 x 6400 x 1600: 57 us) writing D bounds it.  Tiles
+// of 128 and 192 columns need more loads an MMA than L2 delivers, and a second
+// box for each epilogue warp's stores slows the MMAs by 1 %.
 template <int kFmt, int BN, int STAGES, int EPI>
 struct PairCfg {
   static constexpr int kKt = stage_ktiles<kFmt>();
@@ -847,8 +854,8 @@ struct PairCfg {
 // The t-th tile.  The larger operand is read once and the smaller again and
 // again from L2: with at least as many columns as rows, all rows of tiles
 // within a column of them; else groups of four rows of tiles, column by
-// column.  8192 x 14336 x 4096: 6 % less time than in groups of four;
-// 16384 x 4096 x 4096: 3 % less than by whole columns.
+// column.  8192 x 14336 x 4096: 137.6 us, 144.0 in groups of four; 16384 x
+// 4096 x 4096: 82.1 us, 83.5 by whole columns.
 struct TileAt {
   int m, n;
 };
@@ -1019,23 +1026,25 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producers (both CTAs)
-    if (lane == 0) {
-      uint32_t fills[STAGES];
+    // The whole warp runs the loop and one elected lane issues, as below: one
+    // lane alone took 45 ns more a K block, which bound the kernel.
+    uint32_t fills[STAGES];
 #pragma unroll
-      for (int s = 0; s < STAGES; ++s) fills[s] = 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int64_t t = pair; ok && t < num_units; t += num_pairs) {
-        const Unit u = unit_at(p, t, num_kb);
-        const TileAt at = tile_at(u.tile, num_m, num_n, group);
-        const int m0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM;
-        const int n0 = at.n * BN;
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+    for (int s = 0; s < STAGES; ++s) fills[s] = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t t = pair; ok && t < num_units; t += num_pairs) {
+      const Unit u = unit_at(p, t, num_kb);
+      const TileAt at = tile_at(u.tile, num_m, num_n, group);
+      const int m0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM;
+      const int n0 = at.n * BN;
+      for (int kb = u.kb0; kb < u.kb1; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t full_even = map_to_cta(smem_addr(&full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
           tma_load_2d_pair(sA + stage * C::kABytes, &tmA, full_even, kb * kBKBytes, m0);
@@ -1045,15 +1054,18 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                            m0 / kBM);
           tma_load_2d_pair(sSb + stage * C::kSbBytes, &tmSb, full_even, kb * kKt * kScElems,
                            n0 / 128);
+        }
+        __syncwarp();
 #pragma unroll
-          for (int s = 0; s < STAGES; ++s)
-            if (s == stage) ++fills[s];
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        for (int s = 0; s < STAGES; ++s)
+          if (s == stage) ++fills[s];
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
+    }
+    if (lane == 0) {
       if (!ok) record_error(p.err, abort_flag, kErrGemmProducerWait);
       if (rank == 1) {
         const uint32_t even_fills = map_to_cta(smem_addr(const_cast<uint32_t*>(peer_fills)), 0);
@@ -1397,9 +1409,9 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
 }
 
 // K blocks of a tile that slicing the last wave has to save: joining the
-// slices costs about 5 us, a block takes 0.34.  4096 x 4096 x 16384: 89.6 us
-// against 95.8, 6400 x 1600 x 12288 51.8 against 56.7, but 4096 x 4096 x 4096
-// 32.0 against 30.0.
+// slices costs about 5 us, a block takes 0.3.  4096 x 4096 x 16384: 78.8 us
+// against 82.6, 6400 x 1600 x 12288 46.7 against 49.2, but 4096 x 4096 x 4096
+// 28.8 against 26.2.
 constexpr int kTailMinBlocks = 16;
 
 template <int kFmt, int BN, int STAGES, int EPI>
@@ -1455,9 +1467,11 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
     return run_few<kFmt, 64, 3>(g, p, dev, stream);
   // Eight epilogue warps where writing a tile takes longer than multiplying
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
-  // 4096 x 4096 x 512 11.3 us against 13.1, 777 x 4801 x 1600 10.3 against
-  // 12.3, but 12288 x 6400 x 1600 62.6 against 58.3.
-  if (!p.vec || g.K <= 2 * kBK) return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
+  // 4096 x 4096 x 512 12.0 us against 13.1, 8192 x 8192 x 1024 37.2 against
+  // 39.5, 777 x 4801 x 1600 10.3 against 12.3, but 8192 x 8192 x 2048 55.5
+  // against 51.3.
+  if (!p.vec || g.K <= 4 * kBK)
+    return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
   return run_pair<kFmt, 256, 5, 4>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
 }
 
