@@ -260,6 +260,11 @@ __device__ __forceinline__ void join_partials(const Fp4GemmParams& p, const floa
 // CTAs, two an SM, to keep that many loads in flight.  With `early` the
 // preceding kernel of the stream is known not to write A, so its first
 // stages are loaded before that kernel has finished.
+//
+// 32 x 4096 x 14336 9.5 us in NVFP4, the weight at 3.5 TB/s (the launch and
+// the join take 4 us of it); 1 x 4096 x 4096 5.6 us; 128 x 4096 x 4096 7.7 and
+// 512 x 4096 x 4096 10.4 us, where every 64 tokens read the weight from L2
+// again.
 template <int kFmt, int BN, int STAGES>
 struct FewCfg {
   static constexpr int kABytes = kBM * kBKBytes;
@@ -454,6 +459,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // the tensorwise scale.  The first tile's cluster also writes the quantised
 // tokens and their state.  Every thread holds its values in registers between
 // the maximum and the conversion, which is what bounds the slice.
+// Bound by reading the weight and by the launch: 1 x 14336 x 4096 in 7.5 us,
+// 4.4 TB/s (9.9 us in two launches); 16 x 4096 x 4096 8.9 us, 10.4 in two.
 constexpr int kFusedThreads = 256;
 constexpr int kFusedUnits = 4 * kFusedThreads;  // of 16 values, of a CTA
 constexpr size_t kFusedSmemHalf = 114688;       // two CTAs an SM

@@ -273,6 +273,10 @@ __device__ __forceinline__ void quantise_cta(const QuantParams& p, uint32_t t,
 // x 2 columns a thread, and stages its codes so that they leave 64 bytes a
 // row.  Shared rows are 16 bytes longer than the tile's, and the halves of
 // 32 bytes and the staged chunks are permuted, so that no access conflicts.
+// 65536 x 4096, MXFP4: 95 us without the transposed copy, 7.2 TB/s; 133 us
+// with it, 6.2 TB/s.  Smaller tensors ramp up and down for longer than they
+// run at that rate: 14336 x 4096 33 us, 5.4 TB/s, four CTAs an SM that wait
+// for their loads, the conversions (60 % of the issue slots) and each other.
 // Every parameter is at a constant address, so the code stands once for each
 // tensor, and a single one has a kernel without the second: with indexed
 // parameters 14336 x 4096 (MXFP4, both copies) took 35.1 us instead of 33.3.
@@ -289,7 +293,8 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // Largest magnitudes (bf16 bits) of one or two tensors, one a CTA, for the
-// quantisation to join: no atomics and no last CTA.
+// quantisation to join: no atomics and no last CTA.  Bound by reading them:
+// 65536 x 4096 in 93 us, 5.8 TB/s.
 struct AmaxParams {
   const uint16_t* x;
   int64_t rows, cols, ld;
@@ -351,8 +356,9 @@ __global__ void __launch_bounds__(kQThreads)
 
 // A small tensor with dynamic NVFP4 scaling in one launch: every CTA finds
 // the whole tensor's maximum (from L2, but for the first) before it quantises
-// its tile.  16 x 4096: 5.6 us against 7.3 us by a cluster of eight CTAs that
-// join their maxima, and against two launches.
+// its tile.  Bound by the launch and two round trips to memory: 16 x 4096 in
+// 5.6 us back to back, against 7.3 us by a cluster of eight CTAs that join
+// their maxima, and about the same by two launches.
 constexpr int64_t kSmallElems = 65536;
 
 template <bool kTrans, int kAlign>
@@ -389,7 +395,8 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8]) {
 }
 
 // Codes back to values: a 128 x 128 tile a CTA, 16 values of four rows a
-// thread, whose scales are one 16-byte load.
+// thread, whose scales are one 16-byte load.  Bound by memory: 14336 x 4096
+// into bf16 in 24 us, 6.1 TB/s.
 template <int kFmt, typename Out, int kAlign>
 __global__ void __launch_bounds__(kQThreads)
     fp4_dequantise_kernel(const uint8_t* codes, const uint8_t* scales, const float* inv,
@@ -459,7 +466,8 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // The same for rows that are not 16-byte aligned: consecutive lanes write
-// consecutive values, 32 rows a CTA.
+// consecutive values, 32 rows a CTA.  1009 x 1531 in about 4 us, most of it
+// the launch.
 template <int kFmt, typename Out>
 __global__ void __launch_bounds__(kQThreads)
     fp4_dequantise_ragged_kernel(const uint8_t* codes, const uint8_t* scales, const float* inv,
