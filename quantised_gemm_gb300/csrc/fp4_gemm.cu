@@ -459,8 +459,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 // the tensorwise scale.  The first tile's cluster also writes the quantised
 // tokens and their state.  Every thread holds its values in registers between
 // the maximum and the conversion, which is what bounds the slice.
-// Bound by reading the weight and by the launch: 1 x 14336 x 4096 in 7.5 us,
-// 4.4 TB/s (9.9 us in two launches); 16 x 4096 x 4096 8.9 us, 10.4 in two.
+// Bound by reading the weight and by the launch.  In a graph, NVFP4: 1 x 14336
+// x 4096 9.1 us, 3.6 TB/s (10.2 in two launches), 1 x 4096 x 4096 5.7 us (6.4),
+// 32 x 4096 x 4096 8.3 us (11.0); MXFP4: 4.5 us (5.9) and 7.1 us (6.6, but two
+// launches take the host 2 us longer).  What does not need the launches before
+// this one is done before the wait for them: 2 us of each.
 constexpr int kFusedThreads = 256;
 constexpr int kFusedUnits = 4 * kFusedThreads;  // of 16 values, of a CTA
 constexpr size_t kFusedSmemHalf = 114688;       // two CTAs an SM
@@ -549,6 +552,14 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
   }
   __syncwarp();
   if (split > 1) cluster_started_arrive();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  // Scale tiles hold 128 rows; those past the tokens are zero.
+  for (int i = threadIdx.x; i < nkb * C::kScBytes / 16; i += kFusedThreads)
+    reinterpret_cast<uint4*>(sSb)[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
   griddep_wait();
 
   // ------------------------------------------------------------ the tokens
@@ -576,27 +587,21 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
   if (find && whole && split > 1) load_units(w, num_kb * 16, all_units, 0);
   if (threadIdx.x == 0)
     for (int i = 0; i < nkb && i < stages; ++i) load_a(i, kb0 + i);
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
-    tmem_relinquish();
-  }
-  // Scale tiles hold 128 rows; those past the tokens are zero.
-  for (int i = threadIdx.x; i < nkb * C::kScBytes / 16; i += kFusedThreads)
-    reinterpret_cast<uint4*>(sSb)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
   if (split > 1) cluster_started_wait();  // before anything is written to another CTA
-  uint32_t m = 0;
+  uint32_t largest[4], pairs = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t own = max_magnitude(max8(v[k][0]), max8(v[k][1]));
+    pairs = max_magnitude(pairs, own);
+    largest[k] = larger_half(own);
+  }
   if (find && whole && split > 1) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      m = max(m, larger_half(max_magnitude(max8(w[k][0]), max8(w[k][1]))));
+      pairs = max_magnitude(pairs, max_magnitude(max8(w[k][0]), max8(w[k][1])));
   }
-  uint32_t largest[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    largest[k] = larger_half(max_magnitude(max8(v[k][0]), max8(v[k][1])));
-    m = max(m, largest[k]);
-  }
+  uint32_t m = larger_half(pairs);
   float s = 0.0f, inv = 1.0f;
   if constexpr (kFmt == 0) {
     float amax = 0.0f;
