@@ -276,12 +276,14 @@ struct FewCfg {
   static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : BN + 32 <= 128 ? 128 : 256;
   static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes + 256;
   static_assert(BN % 16 == 0 && BN <= 128, "one row of scale tiles for B");
-  // Two CTAs an SM; with tiles of 64 columns a shared K loop has one.
-  static_assert(2 * (kSmemBytes + (BN <= 32 ? joined_bytes<BN>(2) : 0) + 1024) <= 233472, "fits");
+  // Two CTAs an SM, or one with a deep ring.
+  static constexpr int kPerSm = STAGES <= 4 ? 2 : 1;
+  static_assert(kPerSm * (kSmemBytes + (BN <= 32 || kPerSm == 1 ? joined_bytes<BN>(2) : 0) + 1024) <= 233472,
+                "fits");
 };
 
 template <int kFmt, int BN, int STAGES>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, FewCfg<kFmt, BN, STAGES>::kPerSm)
     gemm_fp4_few_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmSa,
@@ -1467,6 +1469,8 @@ cudaError_t run_pair(const Fp4View& a, const Fp4View& b, Fp4GemmParams p, size_t
                        tmA, tmB, tmSa, tmSb, tmD, p);
 }
 
+constexpr int64_t kDeepK = 24 * kBK;
+
 template <int kFmt>
 cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev,
                     cudaStream_t stream) {
@@ -1475,8 +1479,13 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   // 4096 (two waves) 20.0 and 11.7.
   if (g.M <= 16) return run_few<kFmt, 16, 4>(g, p, dev, stream);
   if (g.M <= 32) return run_few<kFmt, 32, kFmt == 0 ? 3 : 4>(g, p, dev, stream);
-  if ((g.M + 63) / 64 * ((g.N + kBM - 1) / kBM) <= 2 * int64_t(dev.num_sms))
-    return run_few<kFmt, 64, 3>(g, p, dev, stream);
+  const int64_t tiles = (g.M + 63) / 64 * ((g.N + kBM - 1) / kBM);
+  // Long K loops, one CTA an SM: the second CTA's shared memory as stages too.
+  // 256 x 4096 x 16384: 22.8 us against 27.2, 256 x 4096 x 6144 11.1 against
+  // 11.8, but 256 x 4096 x 4096 8.8 against 8.6.
+  if (tiles <= dev.num_sms && g.K >= kDeepK)
+    return run_few<kFmt, 64, 6>(g, p, dev, stream);
+  if (tiles <= 2 * int64_t(dev.num_sms)) return run_few<kFmt, 64, 3>(g, p, dev, stream);
   // Eight epilogue warps where writing a tile takes longer than multiplying
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
   // 4096 x 4096 x 512 12.0 us against 13.1, 8192 x 8192 x 1024 37.2 against

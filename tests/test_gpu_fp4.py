@@ -294,7 +294,8 @@ def quantised(q, rows, cols, fmt, seed, std=1.0):
 PRODUCTS = [(1, 1, 1), (1, 16, 64), (1, 130, 4096), (2, 257, 100), (16, 128, 256), (17, 96, 31),
             (32, 4096, 1600), (33, 200, 1000), (64, 129, 513), (65, 384, 640), (100, 100, 100),
             (128, 128, 128), (129, 127, 257), (256, 256, 256), (300, 1000, 1531), (777, 333, 96),
-            (1024, 512, 4096), (515, 2049, 2048)]
+            (1024, 512, 4096), (515, 2049, 2048), (70, 200, 6200), (250, 1000, 6144), (129, 130, 9001),
+            (2600, 1400, 1000)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
