@@ -772,7 +772,8 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
 // 32 rows x 64 columns of the accumulator (this lane's row in ra and rb),
 // scaled, rounded to bf16 and staged in shared memory as the 128-byte TMA
 // swizzle has them.  Rows that are 16-byte aligned leave by TMA (clipped to
-// D); others two bytes a lane, consecutive lanes on consecutive columns.
+// D); others, and a row's end inside 16 bytes, two bytes a lane, consecutive
+// lanes on consecutive columns.
 __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32_t (&rb)[32],
                                           float alpha, uint8_t* box, const CUtensorMap* tmD,
                                           const Fp4GemmParams& p, int row0, int64_t col0, int lane) {
@@ -792,7 +793,8 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
   for (int q = 0; q < 8; ++q)
     *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ sw) << 4)) =
         make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  if (p.vec) {
+  // TMA writes whole 16 bytes, past the last column too.
+  if (p.vec && (col0 + 64 <= p.N || (p.N & 7) == 0)) {
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) {

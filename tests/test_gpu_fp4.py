@@ -295,7 +295,7 @@ PRODUCTS = [(1, 1, 1), (1, 16, 64), (1, 130, 4096), (2, 257, 100), (16, 128, 256
             (32, 4096, 1600), (33, 200, 1000), (64, 129, 513), (65, 384, 640), (100, 100, 100),
             (128, 128, 128), (129, 127, 257), (256, 256, 256), (300, 1000, 1531), (777, 333, 96),
             (1024, 512, 4096), (515, 2049, 2048), (70, 200, 6200), (250, 1000, 6144), (129, 130, 9001),
-            (2600, 1400, 1000)]
+            (2600, 1400, 1000), (2100, 2101, 300), (1300, 4099, 2000)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
@@ -314,6 +314,11 @@ def test_product(M, N, K, fmt):
     q.fp4_gemm(a, b, room[:, 1:N + 1], ws)
     assert torch.equal(room[:, 1:N + 1], out)
     assert (room[:, 0] == 5).all() and (room[:, N + 1:] == 5).all()
+    # Rows aligned to 16 bytes that end inside 16 bytes.
+    room = torch.full((M + 1, -(-N // 8) * 8 + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    q.fp4_gemm(a, b, room[:M, :N], ws)
+    assert torch.equal(room[:M, :N], out)
+    assert (room[:M, N:] == 5).all() and (room[M] == 5).all()
     again = torch.empty_like(out)
     q.fp4_gemm(a, b, again, ws)
     assert torch.equal(again, out)
