@@ -125,12 +125,12 @@ __device__ __forceinline__ void write_state(const QuantParams& p, float amax, fl
   }
 }
 
-// The codes and scales of one tile held in v; returns the largest magnitude.
+// The codes and scales of one tile held in v.
 // sm.table is filled; the call synchronises before it reads it.
 template <int kFmt, bool kTrans>
-__device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, uint32_t tr, uint32_t tc,
-                                                  float s, const uint4 (&v)[4][2],
-                                                  QuantSmem<kFmt, kTrans>& sm) {
+__device__ __forceinline__ void quantise_tile(const QuantParams& p, uint32_t tr, uint32_t tc,
+                                              float s, const uint4 (&v)[4][2],
+                                              QuantSmem<kFmt, kTrans>& sm) {
   constexpr int kBlock = kFmt == 0 ? 16 : 32;
   constexpr int kTileBlocks = 4 * kBlock;  // columns of one 512-byte scale tile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -148,13 +148,11 @@ __device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, uint32_t
     }
   }
   if constexpr (kTrans || kFmt == 0) __syncthreads();
-  uint32_t all = 0;
   uint32_t word[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (p.codes == nullptr) break;  // uniform
     uint32_t m = larger_half(max_magnitude(max8(v[i][0]), max8(v[i][1])));
-    all = max(all, m);
-    if (p.codes == nullptr) continue;  // uniform
     if constexpr (kFmt == 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     float r;
     const uint32_t c = block_scale<kFmt>(m, s, sm.table, r);
@@ -235,11 +233,11 @@ __device__ __forceinline__ uint32_t quantise_tile(const QuantParams& p, uint32_t
             *reinterpret_cast<const uint4*>(sm.scales + tid * 16);
     }
   }
-  return all;
 }
 
-// Tile t of a tensor.
-template <int kFmt, bool kTrans, int kAlign>
+// Tile t of a tensor; kRecord: with its amax for delayed scaling, where the
+// tensor has that.
+template <int kFmt, bool kTrans, int kAlign, bool kRecord>
 __device__ __forceinline__ void quantise_cta(const QuantParams& p, uint32_t t,
                                              QuantSmem<kFmt, kTrans>& sm) {
   const uint32_t tr = t / p.tiles_c, tc = t - tr * p.tiles_c;
@@ -259,9 +257,16 @@ __device__ __forceinline__ void quantise_cta(const QuantParams& p, uint32_t t,
     fill_table(s, sm.table);
     if (t == 0 && threadIdx.x == 0) write_state(p, amax, s);
   }
-  const uint32_t all = quantise_tile<kFmt, kTrans>(p, tr, tc, s, v, sm);
-  if (p.amax_rec != nullptr) {
-    const uint32_t bits = block_max(all, sm.red) << 16;
+  uint32_t m = 0;
+  if (kRecord) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max_magnitude(m, max_magnitude(max8(v[i][0]), max8(v[i][1])));
+  }
+  quantise_tile<kFmt, kTrans>(p, tr, tc, s, v, sm);
+  if (kRecord && p.amax_rec != nullptr) {
+    // Last: at the start the CTA's warps would wait for the atomics (65536 x
+    // 4096: 106 us against 101).
+    const uint32_t bits = block_max(larger_half(m), sm.red) << 16;
     if (threadIdx.x == 0) join_amax(bits, p.rec_acc, p.rec_ticket, p.amax_rec, p.tiles);
   }
 }
@@ -280,16 +285,18 @@ __device__ __forceinline__ void quantise_cta(const QuantParams& p, uint32_t t,
 // Every parameter is at a constant address, so the code stands once for each
 // tensor, and a single one has a kernel without the second: with indexed
 // parameters 14336 x 4096 (MXFP4, both copies) took 35.1 us instead of 33.3.
-template <int kFmt, bool kTrans, int kAlign, bool kPair>
-__global__ void __launch_bounds__(kQThreads)
+// The recording of an amax is a kernel of its own too.  Five CTAs an SM
+// without the transposed copy: 65536 x 4096 (NVFP4) 99 us, 102 with four.
+template <int kFmt, bool kTrans, int kAlign, bool kPair, bool kRecord>
+__global__ void __launch_bounds__(kQThreads, kTrans || kPair || kAlign == kScalar ? 4 : 5)
     fp4_quantise_kernel(const __grid_constant__ QuantPair pair) {
   __shared__ __align__(16) QuantSmem<kFmt, kTrans> sm;
   griddep_wait();
   griddep_launch_dependents();
   if (!kPair || blockIdx.x < pair.p[0].tiles)
-    quantise_cta<kFmt, kTrans, kAlign>(pair.p[0], blockIdx.x, sm);
+    quantise_cta<kFmt, kTrans, kAlign, kRecord>(pair.p[0], blockIdx.x, sm);
   else
-    quantise_cta<kFmt, kTrans, kAlign>(pair.p[1], blockIdx.x - pair.p[0].tiles, sm);
+    quantise_cta<kFmt, kTrans, kAlign, kRecord>(pair.p[1], blockIdx.x - pair.p[0].tiles, sm);
 }
 
 // Largest magnitudes (bf16 bits) of one or two tensors, one a CTA, for the
@@ -563,11 +570,11 @@ AmaxParams amax_params(const Fp4QuantArgs& a) {
   return p;
 }
 
-template <int kFmt, bool kTrans, bool kPair>
+template <int kFmt, bool kTrans, bool kPair, bool kRecord>
 auto* quant_kernel(int align) {
-  return align == kAlign32   ? fp4_quantise_kernel<kFmt, kTrans, kAlign32, kPair>
-         : align == kAlign16 ? fp4_quantise_kernel<kFmt, kTrans, kAlign16, kPair>
-                             : fp4_quantise_kernel<kFmt, kTrans, kScalar, kPair>;
+  return align == kAlign32   ? fp4_quantise_kernel<kFmt, kTrans, kAlign32, kPair, kRecord>
+         : align == kAlign16 ? fp4_quantise_kernel<kFmt, kTrans, kAlign16, kPair, kRecord>
+                             : fp4_quantise_kernel<kFmt, kTrans, kScalar, kPair, kRecord>;
 }
 
 template <bool kTrans>
@@ -637,11 +644,15 @@ cudaError_t launch_fp4_quantise(const Fp4QuantArgs* a, int n, const uint32_t* pa
     tiles += pair.p[i].tiles;
   }
   const bool trans = a[0].out_t.codes != nullptr;
+  const bool record = a[0].amax_rec != nullptr || (n == 2 && a[1].amax_rec != nullptr);
   set_error_site("fp4_quantise_kernel");
   auto pick = [&](auto two) {
     constexpr bool kPair = decltype(two)::value;
-    return a[0].fmt == 0 ? (trans ? quant_kernel<0, true, kPair>(align) : quant_kernel<0, false, kPair>(align))
-                         : (trans ? quant_kernel<1, true, kPair>(align) : quant_kernel<1, false, kPair>(align));
+    if (a[0].fmt != 0)
+      return trans ? quant_kernel<1, true, kPair, false>(align) : quant_kernel<1, false, kPair, false>(align);
+    if (record)
+      return trans ? quant_kernel<0, true, kPair, true>(align) : quant_kernel<0, false, kPair, true>(align);
+    return trans ? quant_kernel<0, true, kPair, false>(align) : quant_kernel<0, false, kPair, false>(align);
   };
   auto* kernel = n == 2 ? pick(std::true_type()) : pick(std::false_type());
   return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles)), dim3(kQThreads), 0, stream, 1,

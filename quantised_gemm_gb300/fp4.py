@@ -63,13 +63,21 @@ class Fp4Tensor:
         self.inv_scale = state.inv_scale if state is not None else inv_scale
         if self.inv_scale is not None and self.inv_scale.numel() != 1:
             raise ValueError("inv_scale must have one element")
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales = codes, scales
         c = _lib.Fp4TensorC()
         c.codes, c.scales = _dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8)
         c.inv_scale = _dev(self.inv_scale, "inv_scale", torch.float32)
         c.rows, c.cols, c.ld, c.fmt = rows, cols, (codes.stride(0) if rows > 1 else codes.shape[1]), fmt
         self._c = c
         self._ref = ctypes.byref(c)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._scales
 
 
 def _matrix(t: torch.Tensor, name: str, dtype=torch.bfloat16):
