@@ -493,6 +493,7 @@ struct FusedCfg {
 
 struct FusedTokens {
   const uint16_t* x;
+  Span span;
   int64_t ldx;
   const float* amax_in;    // NVFP4: precomputed amax, or
   const float* scale_in;   // the stored scale, or (neither) the tokens' own amax
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
       v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
       if (u < count) {
         const int row = u / per_row, c = u - row * per_row;
-        load16<kAlign>(x.x + row * x.ldx, first + c * 16, p.K, v[k]);
+        load16<kAlign>(x.x + row * x.ldx, first + c * 16, p.K, x.span, v[k]);
       }
     }
   };
@@ -1397,6 +1398,7 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
     return map_failed("fp4 gemm operand");
   FusedTokens t;
   t.x = x.x;
+  t.span = span_of(x.x, x.rows, x.cols, x.ld);
   t.ldx = x.ld;
   t.amax_in = x.amax_in;
   t.scale_in = x.scale_in;

@@ -55,6 +55,7 @@ __device__ __forceinline__ void join_amax(uint32_t bits, uint32_t* acc, uint32_t
 
 struct QuantParams {
   const uint16_t* x;
+  Span span;
   int64_t rows, cols, ld;
   // NVFP4's tensorwise scale: from the maximum of the amax kernel's partials,
   // from an amax, or (delayed scaling) as it is.
@@ -101,7 +102,7 @@ __device__ __forceinline__ void load_tile(const QuantParams& p, uint32_t tr, uin
   for (int i = 0; i < 4; ++i) {
     const int64_t row = int64_t(tr) * kQTile + rr + 32 * i;
     v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-    if (row < p.rows) load16<kAlign>(p.x + row * p.ld, col, p.cols, v[i]);
+    if (row < p.rows) load16<kAlign>(p.x + row * p.ld, col, p.cols, p.span, v[i]);
   }
 }
 
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kQThreads, kTrans || kPair || kAlign == kScala
 // 65536 x 4096 in 91 us, 5.9 TB/s.
 struct AmaxParams {
   const uint16_t* x;
+  Span span;
   int64_t rows, cols, ld;
   uint32_t* partials;
   int ctas;
@@ -330,7 +332,7 @@ __device__ __forceinline__ uint32_t share_max(const AmaxParams& p, int64_t first
       for (int k = 0; k < kLoads; ++k) {
         v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
         const int64_t col = c + k * step + lane * 16;
-        if (col < p.cols) load16<kAlign>(p.x, col, p.cols, v[k]);
+        if (col < p.cols) load16<kAlign>(p.x, col, p.cols, p.span, v[k]);
       }
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
@@ -351,7 +353,8 @@ __device__ __forceinline__ uint32_t share_max(const AmaxParams& p, int64_t first
       const int64_t group = per_row == 1 ? seg : seg / per_row;
       const int64_t row = (group << (5 - lg)) + own_row;
       if (seg < total && row < p.rows)
-        load16<kAlign>(p.x + row * p.ld, ((seg - group * per_row) << (4 + lg)) + own_col, p.cols, v[k]);
+        load16<kAlign>(p.x + row * p.ld, ((seg - group * per_row) << (4 + lg)) + own_col, p.cols, p.span,
+                       v[k]);
     }
 #pragma unroll
     for (int k = 0; k < kLoads; ++k)
@@ -534,6 +537,7 @@ __global__ void __launch_bounds__(kQThreads)
 QuantParams quant_params(const Fp4QuantArgs& a) {
   QuantParams p = {};
   p.x = a.x;
+  p.span = span_of(a.x, a.rows, a.cols, a.ld);
   p.rows = a.rows;
   p.cols = a.cols;
   p.ld = a.ld;
@@ -562,6 +566,7 @@ AmaxParams amax_params(const Fp4QuantArgs& a) {
   AmaxParams p = {};
   const bool one = a.ld == a.cols;
   p.x = a.x;
+  p.span = span_of(a.x, a.rows, a.cols, a.ld);
   p.rows = one ? 1 : a.rows;
   p.cols = one ? a.rows * a.cols : a.cols;
   p.ld = one ? 0 : a.ld;

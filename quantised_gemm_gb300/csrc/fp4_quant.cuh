@@ -108,11 +108,53 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t col, int64_t
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Sixteen values at p from the three aligned 16-byte vectors that they lie in;
+// zero from the left-th on.
+__device__ __forceinline__ void load16_shifted(const uint16_t* p, int64_t left, uint4 (&v)[2]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint4* vec = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+  const uint4 a = __ldg(vec), b = __ldg(vec + 1), c = __ldg(vec + 2);
+  uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  const bool two = (at & 8) != 0, one = (at & 4) != 0;
+#pragma unroll
+  for (int j = 0; j < 10; ++j) w[j] = two ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 9; ++j) w[j] = one ? w[j + 1] : w[j];
+  const uint32_t half = (at & 2) != 0 ? 16u : 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], half);
+  if (left < 16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = left >= 2 * j + 2 ? w[j] : left == 2 * j + 1 ? w[j] & 0xFFFFu : 0u;
+  }
+  v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Where the bytes of a tensor begin and end.
+struct Span {
+  const uint16_t* begin;
+  const uint16_t* end;
+};
+__host__ __device__ __forceinline__ Span span_of(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld) {
+  return {x, x + (rows - 1) * ld + cols};
+}
+
 // Sixteen values of a row (zero past its end): whole 32-byte sectors with one
-// load where they are aligned.
+// load where they are aligned; where rows are not, by the aligned vectors
+// around them as long as these lie within the tensor.
 template <int kAlign>
-__device__ __forceinline__ void load16(const uint16_t* row, int64_t col, int64_t cols,
+__device__ __forceinline__ void load16(const uint16_t* row, int64_t col, int64_t cols, const Span& in,
                                        uint4 (&v)[2]) {
+  if (kAlign == kScalar) {
+    const uint16_t* p = row + col;
+    const uintptr_t low = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15);
+    if (low >= reinterpret_cast<uintptr_t>(in.begin) && low + 48 <= reinterpret_cast<uintptr_t>(in.end)) {
+      load16_shifted(p, cols - col, v);
+      return;
+    }
+  }
   if (kAlign == kAlign32 && col + 16 <= cols) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
