@@ -1526,7 +1526,7 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   // Eight epilogue warps where writing a tile takes longer than multiplying
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
   // 4096 x 4096 x 512 12.0 us against 13.1, 8192 x 8192 x 1024 37.2 against
-  // 39.5, 777 x 4801 x 1600 10.3 against 12.3, but 8192 x 8192 x 2048 55.5
+  // 39.5, 777 x 4801 x 1600 9.5 against 11.4, but 8192 x 8192 x 2048 55.5
   // against 51.3.
   if (!p.vec || g.K <= 4 * kBK)
     return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
