@@ -315,30 +315,37 @@ struct AmaxPair {
   AmaxParams p[2];
 };
 
+// share_max() of a contiguous tensor, which is one row: no rows' arithmetic
+// (16 x 4096 by one CTA: 1.4 us less).
+template <int kAlign, int kLoads>
+__device__ __forceinline__ uint32_t contiguous_max(const AmaxParams& p, int64_t first, int64_t warps) {
+  uint32_t m2 = 0;
+  const int64_t step = warps * 512;
+  for (int64_t c = first * 512; c < p.cols; c += kLoads * step) {
+    uint4 v[kLoads][2];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+      const int64_t col = c + k * step + (threadIdx.x & 31) * 16;
+      if (col < p.cols) load16<kAlign>(p.x, col, p.cols, p.span, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k)
+      m2 = max_magnitude(m2, max_magnitude(max8(v[k][0]), max8(v[k][1])));
+  }
+  return larger_half(m2);
+}
+
 // The largest magnitude of a thread's share of a tensor: warp `first` of
 // `warps` takes 512 values at a time, kLoads of these in flight: of one row,
-// or 16 values a lane of several narrow ones.  Contiguous tensors, one row
-// here, have a loop without the rows' arithmetic: 16 x 4096 by one CTA 1.4 us
-// less.
+// or 16 values a lane of several narrow ones.
 template <int kAlign, int kLoads>
 __device__ __forceinline__ uint32_t share_max(const AmaxParams& p, int64_t first, int64_t warps) {
   const int lane = threadIdx.x & 31, lg = p.lanes_log2;
-  if (p.rows == 1) {  // contiguous
-    uint32_t m2 = 0;
-    const int64_t step = warps * 512;
-    for (int64_t c = first * 512; c < p.cols; c += kLoads * step) {
-      uint4 v[kLoads][2];
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-        const int64_t col = c + k * step + lane * 16;
-        if (col < p.cols) load16<kAlign>(p.x, col, p.cols, p.span, v[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k)
-        m2 = max_magnitude(m2, max_magnitude(max8(v[k][0]), max8(v[k][1])));
-    }
-    return larger_half(m2);
+  if (p.rows == 1) {
+    if (kAlign == kScalar && (reinterpret_cast<uintptr_t>(p.x) & 31u) == 0)
+      return contiguous_max<kAlign32, kLoads>(p, first, warps);
+    return contiguous_max<kAlign, kLoads>(p, first, warps);
   }
   const int64_t per_row = (p.cols + (16 << lg) - 1) >> (4 + lg);
   const int64_t total = ((p.rows + (32 >> lg) - 1) >> (5 - lg)) * per_row;
@@ -388,7 +395,9 @@ __global__ void __launch_bounds__(kQThreads)
 // its tile.  Bound by the launch and two round trips to memory: 16 x 4096 in
 // 3.3 us back to back in a graph (two launches: 4.1), where a cluster of eight
 // CTAs that join their maxima took 1.7 us more than this.
-constexpr int64_t kSmallElems = 65536;
+// 96 x 1024 by a call from Python 5.7 us against 7.3 us in two launches, in a
+// graph 4.2 and 4.0; 128 x 2048 7.9 and 7.3.
+constexpr int64_t kSmallElems = 98304;
 
 template <bool kTrans, int kAlign>
 __global__ void __launch_bounds__(kQThreads)
