@@ -94,7 +94,7 @@ _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _ST = ctypes.POINTER(ScalingStateC)
 _T4 = ctypes.POINTER(Fp4TensorC)
-_GR = ctypes.POINTER(GradC)
+_GR = ctypes.c_void_p  # GradC array, or its address
 _F = ctypes.c_float
 
 _SIGNATURES = {

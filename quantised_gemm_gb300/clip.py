@@ -9,6 +9,8 @@ grad_norm() and clip_grads().
 """
 from __future__ import annotations
 
+import array
+
 import torch
 
 from . import _lib
@@ -30,26 +32,30 @@ def _same_dense(a: torch.Tensor, b: torch.Tensor) -> bool:
     return all(s == 1 or t == u for s, t, u in zip(a.shape, a.stride(), b.stride()))
 
 
+_F32 = {torch.bfloat16: 0, torch.float32: 1}
+
+
 def _list(grads, outs):
-    grads = [g for g in grads]
+    """(array of fp8lin_grad, as 64-bit words; its length; the outputs)."""
+    grads = list(grads)
     outs = grads if outs is None else list(outs)
     if len(outs) != len(grads):
         raise ValueError("outs must have one tensor for each gradient")
-    arr = (_lib.GradC * max(1, len(grads)))()
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if not g.is_cuda or not o.is_cuda:
-            raise ValueError("gradients must be CUDA tensors")
-        f32, of32 = g.dtype == torch.float32, o.dtype == torch.float32
-        if not (f32 or g.dtype == torch.bfloat16) or not (of32 or o.dtype == torch.bfloat16):
+    words = array.array("Q")  # g, out, n, g_f32 | out_f32 << 32
+    for g, o in zip(grads, outs):
+        f32 = _F32.get(g.dtype)
+        of32 = f32 if o is g else _F32.get(o.dtype)
+        if f32 is None or of32 is None:
             raise TypeError("gradients must be bf16 or fp32, got %s, %s" % (g.dtype, o.dtype))
+        if not (g.is_cuda and (o is g or o.is_cuda)):
+            raise ValueError("gradients must be CUDA tensors")
         if o is not g and o.shape != g.shape:
             raise ValueError("an output must have its gradient's shape")
-        if not _same_dense(g, o):
+        if not (g.is_contiguous() and (o is g or o.is_contiguous())) and not _same_dense(g, o):
             raise ValueError("a gradient must be dense, and its output in the same order")
-        c = arr[i]
-        c.g, c.out, c.n = g.data_ptr(), o.data_ptr(), g.numel()
-        c.g_f32, c.out_f32 = f32, of32
-    return arr, len(grads), outs
+        at = g.data_ptr()
+        words.extend((at, at if o is g else o.data_ptr(), g.numel(), f32 | of32 << 32))
+    return words, len(grads), outs
 
 
 def _norm_ptr(norm: torch.Tensor) -> int:
@@ -61,8 +67,8 @@ def _norm_ptr(norm: torch.Tensor) -> int:
 def grad_norm(grads, norm: torch.Tensor, ws: Workspace, stream=None) -> torch.Tensor:
     """norm (fp32[1]) = the 2-norm of all gradients together."""
     arr, n, _ = _list(grads, None)
-    _lib.check(_load().fp8lin_grad_norm(arr, n, _norm_ptr(norm), ws.ptr, ws.nbytes,
-                                        _stream(stream)), "fp8lin_grad_norm")
+    _lib.check(_load().fp8lin_grad_norm(arr.buffer_info()[0], n, _norm_ptr(norm), ws.ptr,
+                                        ws.nbytes, _stream(stream)), "fp8lin_grad_norm")
     return norm
 
 
@@ -71,8 +77,8 @@ def clip_grads(grads, max_norm: float, norm: torch.Tensor, *, outs=None, eps: fl
     """Scale every gradient by min(1, max_norm / (norm + eps)), in place or
     into outs (bf16 or fp32, e.g. an optimizer's fp32 buffers)."""
     arr, n, outs = _list(grads, outs)
-    _lib.check(_load().fp8lin_grad_clip(arr, n, _norm_ptr(norm), max_norm, eps, _stream(stream)),
-               "fp8lin_grad_clip")
+    _lib.check(_load().fp8lin_grad_clip(arr.buffer_info()[0], n, _norm_ptr(norm), max_norm, eps,
+                                        _stream(stream)), "fp8lin_grad_clip")
     return outs
 
 
@@ -81,6 +87,7 @@ def clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, ws: Workspace, *,
     """grad_norm() and clip_grads() in one call; returns the norm before
     clipping (on the device)."""
     arr, n, _ = _list(grads, outs)
-    _lib.check(_load().fp8lin_grad_clip_norm(arr, n, max_norm, eps, _norm_ptr(norm), ws.ptr,
-                                             ws.nbytes, _stream(stream)), "fp8lin_grad_clip_norm")
+    st = _load().fp8lin_grad_clip_norm(arr.buffer_info()[0], n, max_norm, eps, _norm_ptr(norm),
+                                       ws.ptr, ws.nbytes, _stream(stream))
+    _lib.check(st, "fp8lin_grad_clip_norm")
     return norm
