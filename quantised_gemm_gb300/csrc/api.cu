@@ -1298,6 +1298,7 @@ Fp4GemmArgs fp4_gemm_args(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b
   g.ws_error = ws_error(ws);
   if (ws_bytes > kWsSplitOffset) {
     g.ws_tickets = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsTicketOffset);
+    g.ws_begun = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsSlicesOffset);
     g.ws_split = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsSplitOffset);
     g.ws_split_bytes = ws_bytes - kWsSplitOffset;
   }

@@ -47,12 +47,15 @@ struct Fp4GemmParams {
   int* err;
   bool vec;                   // D's rows take 16-byte stores
   // Pair kernel: tiles [0, t_full) run whole, each one after them as s_tail
-  // slices of the K loop that join through fp32 partials and tickets (two
-  // ints for each epilogue warp of a tile, zero between launches).
+  // slices of the K loop that join through fp32 partials, tickets (two ints
+  // for each epilogue warp of a tile) and the numbers of pairs with a slice
+  // that have begun and that are done; all counters are zero between launches.
   int64_t t_full;
   int s_tail;
+  int slice_pairs;  // pairs whose last unit is a slice: the first ones
   float* partials;
   int* tickets;
+  int* begun;       // [2]: begun, done
 };
 
 // Instruction descriptor of kind::mxf4nvf4 / kind::mxf4: e2m1 operands, both
@@ -775,8 +778,9 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
 // swizzle has them.  Rows that are 16-byte aligned leave by TMA (clipped to
 // D); others, and a row's end inside 16 bytes, four bytes a lane where the row
 // is aligned to that and two elsewhere, consecutive lanes on consecutive
-// columns: 6183 x 2821 x 176 in 18.5 us (21.4 by two bytes only), x 2822 in 16.0,
-// x 2824, by TMA, in 10.9.
+// columns: 6183 x 2821 x 176 in 17.7 us, x 2822 in 15.3, x 2824, by TMA, in
+// 11.0.  The loops are unrolled no further than eight epilogue warps' registers
+// go (twice as far: 20.7, 15.9 and 11.2).
 __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32_t (&rb)[32],
                                           float alpha, uint8_t* box, const CUtensorMap* tmD,
                                           const Fp4GemmParams& p, int row0, int64_t col0, int lane) {
@@ -825,23 +829,23 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
     if (alternate) {
       uint16_t* even_to = dst + odd * p.ldd;
       uint16_t* odd_to = dst + (odd ^ 1) * p.ldd;
-#pragma unroll 4
+#pragma unroll 2
       for (int r = 0; r < 32; r += 2, even_to += 2 * p.ldd, odd_to += 2 * p.ldd) {
         words(r + odd, even_to);
         halves(r + (odd ^ 1), odd_to);
       }
     } else if (odd == 0) {
-#pragma unroll 8
+#pragma unroll 4
       for (int r = 0; r < 32; ++r, dst += p.ldd) words(r, dst);
     } else {
-#pragma unroll 8
+#pragma unroll 4
       for (int r = 0; r < 32; ++r, dst += p.ldd) halves(r, dst);
     }
     __syncwarp();
     return;
   }
   const bool in0 = col0 + lane < p.N, in1 = col0 + lane + 32 < p.N;
-#pragma unroll 8
+#pragma unroll 4
   for (int r = 0; r < 32; ++r) {
     const uint8_t* src = box + r * 128 + (lane & 7) * 2;
     const uint16_t v0 = *reinterpret_cast<const uint16_t*>(src + (((lane >> 3) ^ (r & 7)) << 4));
@@ -870,9 +874,15 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
 //
 // Where the last wave of tiles fills at most half of the pairs and the K loop
 // is long, each of its tiles runs as slices of the K loop on several pairs.
+// A slice waits for the others of its tile only once every pair with a slice
+// has begun.  Until then -- fewer SMs than the launch counted on, or another
+// stream's kernels on them -- it leaves all of its partials and goes, and the
+// last one to arrive adds up what was left: no slice waits for one that may
+// need its SM to start.  Products without slices have a kernel without that
+// code (8192 x 14336 x 4096, MXFP4: 131 us, 134 with it).
 //
-// Bound by the tensor cores: 8192 x 14336 x 4096 takes 138 us in NVFP4 (7.0
-// PFLOP/s) and 132 us in MXFP4 (7.3), which copies half as many scale tiles;
+// Bound by the tensor cores: 8192 x 14336 x 4096 takes 137 us in NVFP4 (7.0
+// PFLOP/s) and 131 us in MXFP4 (7.3), which copies half as many scale tiles;
 // the MMAs alone, without loads, take 133.  16384 x 4096 x 4096: 82 and 79 us.
 // With short K loops (12288 x 6400 x 1600: 57 us) writing D bounds it.  Tiles
 // of 128 and 192 columns need more loads an MMA than L2 delivers, and a second
@@ -922,8 +932,9 @@ struct Unit {
   int kb0, kb1, slice;
   bool sliced;
 };
+template <bool kSliced>
 __device__ __forceinline__ Unit unit_at(const Fp4GemmParams& p, int64_t t, int num_kb) {
-  if (t < p.t_full) return {t, 0, num_kb, 0, false};
+  if (!kSliced || t < p.t_full) return {t, 0, num_kb, 0, false};
   const int64_t v = t - p.t_full;
   const int per = (num_kb + p.s_tail - 1) / p.s_tail;
   const int slice = static_cast<int>(v % p.s_tail);
@@ -931,7 +942,7 @@ __device__ __forceinline__ Unit unit_at(const Fp4GemmParams& p, int64_t t, int n
   return {p.t_full + v / p.s_tail, kb0, min(num_kb, kb0 + per), slice, true};
 }
 
-// One box of a slice's accumulator: 16-byte stores, lane after lane.
+// One box of a slice's accumulator: 16-byte accesses, lane after lane.
 __device__ __forceinline__ void store_partial(float* region, const uint32_t (&ra)[32],
                                               const uint32_t (&rb)[32], int lane) {
   uint4* dst = reinterpret_cast<uint4*>(region) + lane;
@@ -939,6 +950,20 @@ __device__ __forceinline__ void store_partial(float* region, const uint32_t (&ra
   for (int q = 0; q < 8; ++q) {
     __stcg(dst + q * 32, make_uint4(ra[4 * q], ra[4 * q + 1], ra[4 * q + 2], ra[4 * q + 3]));
     __stcg(dst + (8 + q) * 32, make_uint4(rb[4 * q], rb[4 * q + 1], rb[4 * q + 2], rb[4 * q + 3]));
+  }
+}
+
+__device__ __forceinline__ void load_partial(const float* region, uint32_t (&ra)[32],
+                                             uint32_t (&rb)[32], int lane) {
+  const uint4* src = reinterpret_cast<const uint4*>(region) + lane;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    uint32_t* r = q < 8 ? ra + 4 * q : rb + 4 * (q - 8);
+    const uint4 v = __ldcg(src + q * 32);
+    r[0] = v.x;
+    r[1] = v.y;
+    r[2] = v.z;
+    r[3] = v.w;
   }
 }
 
@@ -960,21 +985,40 @@ __device__ __forceinline__ void add_partial(const float* region, uint32_t (&ra)[
   }
 }
 
-// Announce this warp's partials and wait, bounded, for those of the other
-// slices.  The slices of a tile are the last units of different pairs, all
-// resident, so the wait cannot block on itself.
-__device__ __forceinline__ bool wait_for_slices(int* ticket, int slices, volatile int* abort_flag,
-                                                int lane) {
+// A ticket counts the slices that have arrived in units of kArrived; below
+// them it has a bit for each slice that left its own boxes too.
+constexpr int kArrived = 256;
+
+// Whether every pair with a slice is running.  None of them waits for anything
+// but the other slices, so a slice may then wait for these.
+__device__ __forceinline__ bool all_begun(const int* begun, int pairs, int lane) {
+  int seen = 0;
+  if (lane == 0)
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(begun) : "memory");
+  return __shfl_sync(0xFFFFFFFFu, seen, 0) >= pairs;
+}
+
+// Announce this warp's partials; the ticket before it.
+__device__ __forceinline__ int announce_slice(int* ticket, int add, int lane) {
   __threadfence();
   __syncwarp();
+  int before = 0;
+  if (lane == 0) before = atomicAdd(ticket, add);
+  before = __shfl_sync(0xFFFFFFFFu, before, 0);
+  __threadfence();
+  return before;
+}
+
+// Wait, bounded, for the partials of all slices.
+__device__ __forceinline__ bool wait_for_slices(const int* ticket, int slices, volatile int* abort_flag,
+                                                int lane) {
   bool in = true;
   if (lane == 0) {
-    atomicAdd(ticket, 1);
     const uint64_t t0 = global_timer_ns();
     int seen;
     while (true) {
       asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(ticket) : "memory");
-      if (seen >= slices) break;
+      if (seen >= slices * kArrived) break;
       if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
         in = false;
         break;
@@ -996,7 +1040,7 @@ __device__ __forceinline__ void finish_slices(int* ticket, int slices, int lane)
   }
 }
 
-template <int kFmt, int BN, int STAGES, int EPI>
+template <int kFmt, int BN, int STAGES, int EPI, bool kSliced>
 __global__ void __launch_bounds__(64 + 32 * EPI, 1)
     gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB,
@@ -1038,7 +1082,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
   const int64_t num_tiles = num_m * num_n;
   const int64_t group = p.N >= p.M ? num_m : 4;
   const int num_kb = static_cast<int>((p.K + kBK - 1) / kBK);
-  const int64_t num_units = p.t_full + (num_tiles - p.t_full) * p.s_tail;
+  const int64_t num_units = kSliced ? p.t_full + (num_tiles - p.t_full) * p.s_tail : num_tiles;
   // MMAs of the last stage; what follows K is zero in the codes and is not multiplied.
   const int last_steps = static_cast<int>((p.K - int64_t(num_kb - 1) * kBK + kMmaK - 1) / kMmaK);
 
@@ -1073,6 +1117,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();
   griddep_launch_dependents();
+  if (kSliced && rank == 0 && threadIdx.x == 64 && pair < p.slice_pairs) atomicAdd(p.begun, 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producers (both CTAs)
@@ -1085,7 +1130,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t t = pair; ok && t < num_units; t += num_pairs) {
-      const Unit u = unit_at(p, t, num_kb);
+      const Unit u = unit_at<kSliced>(p, t, num_kb);
       const TileAt at = tile_at(u.tile, num_m, num_n, group);
       const int m0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM;
       const int n0 = at.n * BN;
@@ -1148,7 +1193,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
         }
         if (!ok) break;
         tc_fence_after_sync();
-        const Unit u = unit_at(p, t, num_kb);
+        const Unit u = unit_at<kSliced>(p, t, num_kb);
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAcc1);
         const uint32_t sfb =
             tmem_base + C::kSfb +
@@ -1235,7 +1280,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       return p.partials + ((tail * 8 + static_cast<int>(rank) * 4 + quarter) * (BN / 64) + i) * 2048;
     };
     for (int64_t t = pair; t < num_units; t += num_pairs) {
-      const Unit u = unit_at(p, t, num_kb);
+      const Unit u = unit_at<kSliced>(p, t, num_kb);
       const TileAt at = tile_at(u.tile, num_m, num_n, group);
       const int row0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM + quarter * 32;
       const int64_t n0 = static_cast<int64_t>(at.n) * BN;
@@ -1248,14 +1293,16 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(acc * C::kAcc1);
+      const bool meet = kSliced && u.sliced && all_begun(p.begun, p.slice_pairs, lane);
 #pragma unroll 1
       for (int g = 0; g < C::kGroups; ++g) {
         // The first accumulator's shared columns are its last, the second's its first.
         const int i = part * C::kGroups + (C::kOverlap && acc == 0 ? C::kGroups - 1 - g : g);
         const int64_t col0 = n0 + 64 * i;
         const bool live = row0 < p.M && col0 < p.N;
-        // A slice keeps every s_tail-th box of a warp and hands over the others.
-        const bool kept = u.sliced && i % p.s_tail == u.slice;
+        // A slice owns every s_tail-th box of a warp and hands over the others;
+        // its own too where it may not wait for the other slices.
+        const bool kept = meet && i % p.s_tail == u.slice;
         uint32_t ra[32], rb[32];
         if (live && !kept) {
           tmem_load_32cols(t_row + 64 * i, ra);
@@ -1270,25 +1317,39 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
             if (g == C::kGroups - 1) mbar_arrive_cluster_tmem(acc_empty_even + 8u * acc);
           }
         }
-        if (live && !u.sliced) store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
-        if (live && u.sliced && !kept) store_partial(partial_of(u, u.slice, i), ra, rb, lane);
+        if (live && !(kSliced && u.sliced)) store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
+        if constexpr (kSliced)
+          if (live && u.sliced && !kept) store_partial(partial_of(u, u.slice, i), ra, rb, lane);
       }
-      if (u.sliced && row0 < p.M) {
-        // The pair's last unit: its accumulator stays where it is.
+      if (kSliced && u.sliced && row0 < p.M) {
+        // The pair's last unit: its accumulator stays where it is.  A box is
+        // its owner's partial plus the others in order, whoever adds them up:
+        // the owner, or the last slice to arrive if the owner has left.
         int* ticket = p.tickets + 2 * warp_slot(u);
-        if (!wait_for_slices(ticket, p.s_tail, abort_flag, lane)) {
+        const int own = meet ? 0 : 1 << u.slice;
+        const int before = announce_slice(ticket, kArrived + own, lane);
+        if (meet && !wait_for_slices(ticket, p.s_tail, abort_flag, lane)) {
           if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
           break;
         }
+        const bool last = before >= (p.s_tail - 1) * kArrived;
+        const int left = last ? (before | own) & (kArrived - 1) : 0;
+#pragma unroll 1
         for (int i = part * C::kGroups; i < (part + 1) * C::kGroups; ++i) {
           const int64_t col0 = n0 + 64 * i;
-          if (i % p.s_tail != u.slice || col0 >= p.N) continue;
+          const int owner = i % p.s_tail;
+          const bool kept = meet && owner == u.slice;
+          if ((!kept && (left >> owner & 1) == 0) || col0 >= p.N) continue;
           uint32_t ra[32], rb[32];
-          tmem_load_32cols(t_row + 64 * i, ra);
-          tmem_load_32cols(t_row + 64 * i + 32, rb);
-          tmem_load_wait();
-          for (int o = 0; o < p.s_tail; ++o)  // always in this order
-            if (o != u.slice) add_partial(partial_of(u, o, i), ra, rb, lane);
+          if (kept) {
+            tmem_load_32cols(t_row + 64 * i, ra);
+            tmem_load_32cols(t_row + 64 * i + 32, rb);
+            tmem_load_wait();
+          } else {
+            load_partial(partial_of(u, owner, i), ra, rb, lane);
+          }
+          for (int o = 0; o < p.s_tail; ++o)
+            if (o != owner) add_partial(partial_of(u, o, i), ra, rb, lane);
           store_box(ra, rb, alpha, box, &tmD, p, row0, col0, lane);
         }
         finish_slices(ticket, p.s_tail, lane);
@@ -1325,6 +1386,12 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
     }
     cluster_sync_all();
   }
+  // The last pair with a slice clears both numbers for the next launch.
+  if (kSliced && rank == 0 && threadIdx.x == 64 && pair < p.slice_pairs &&
+      atomicAdd(p.begun + 1, 1) == p.slice_pairs - 1) {
+    atomicExch(p.begun, 0);
+    atomicExch(p.begun + 1, 0);
+  }
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, 512);
@@ -1342,6 +1409,34 @@ cudaError_t allow_smem(Kernel kernel, size_t bytes, const DeviceInfo& dev, bool 
                                              static_cast<int>(bytes));
   done[dev.device] = e == cudaSuccess;
   return e;
+}
+
+// The same for a kernel of CTA pairs, and how many pairs are resident at once.
+template <typename Kernel>
+cudaError_t pair_setup(Kernel kernel, size_t bytes, int threads, const DeviceInfo& dev, int (&slots)[64],
+                       bool (&done)[64]) {
+  const cudaError_t e = allow_smem(kernel, bytes, dev, done);
+  if (e != cudaSuccess) return e;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (slots[dev.device] > 0) return cudaSuccess;
+  cudaLaunchConfig_t probe = {};
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = 2;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  probe.gridDim = dim3(2 * (dev.num_sms / 2));
+  probe.blockDim = dim3(threads);
+  probe.dynamicSmemBytes = bytes;
+  probe.attrs = &cluster;
+  probe.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &probe) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = dev.num_sms / 2;
+  }
+  slots[dev.device] = n;
+  return cudaSuccess;
 }
 
 // Codes of one operand: boxes of 128 bytes of K.  The rows end at their last
@@ -1465,9 +1560,20 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
 // 28.8 against 26.2.
 constexpr int kTailMinBlocks = 16;
 
-template <int kFmt, int BN, int STAGES, int EPI>
-cudaError_t run_pair(const Fp4View& a, const Fp4View& b, Fp4GemmParams p, size_t split_bytes,
-                     const DeviceInfo& dev, cudaStream_t stream) {
+template <int kFmt, int BN, int STAGES, int EPI, bool kSliced>
+cudaError_t pair_slots(const DeviceInfo& dev, int64_t* slots) {
+  static bool done[64] = {};
+  static int resident[64] = {};
+  const cudaError_t e = pair_setup(gemm_fp4_pair_kernel<kFmt, BN, STAGES, EPI, kSliced>,
+                                   PairCfg<kFmt, BN, STAGES, EPI>::kSmemBytes, 64 + 32 * EPI, dev,
+                                   resident, done);
+  if (e == cudaSuccess) *slots = resident[dev.device];
+  return e;
+}
+
+template <int kFmt, int BN, int STAGES, int EPI, bool kSliced>
+cudaError_t run_pair(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p, const DeviceInfo& dev,
+                     cudaStream_t stream) {
   using C = PairCfg<kFmt, BN, STAGES, EPI>;
   CUtensorMap tmA, tmB, tmSa, tmSb, tmD;
   if (!make_code_map(&tmA, a, p.M, p.K, kBM) || !make_code_map(&tmB, b, p.N, p.K, BN / 2) ||
@@ -1481,29 +1587,32 @@ cudaError_t run_pair(const Fp4View& a, const Fp4View& b, Fp4GemmParams p, size_t
                         static_cast<uint64_t>(p.M), static_cast<uint64_t>(p.ldd) * 2, 64, 32,
                         CU_TENSOR_MAP_SWIZZLE_128B))
     return map_failed("fp4 pair gemm output");
-  auto* kernel = gemm_fp4_pair_kernel<kFmt, BN, STAGES, EPI>;
-  static bool done[64] = {};
-  cudaError_t e = allow_smem(kernel, C::kSmemBytes, dev, done);
+  int64_t slots = 0;
+  const cudaError_t e = pair_slots<kFmt, BN, STAGES, EPI, kSliced>(dev, &slots);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + BN - 1) / BN);
-  const int64_t slots = dev.num_sms / 2;
-  p.t_full = tiles;
-  p.s_tail = 1;
-  const int64_t tail = tiles % slots, num_kb = (p.K + kBK - 1) / kBK;
-  if (tail > 0 && p.partials != nullptr) {
-    int64_t ways = slots / tail < 4 ? slots / tail : 4;
-    const int64_t fit = static_cast<int64_t>(split_bytes) / (tail * 2 * kBM * BN * 4);
-    if (fit < ways) ways = fit;
-    if (ways >= 2 && num_kb * (ways - 1) >= kTailMinBlocks * ways && tail * 4 * EPI <= kWsTickets) {
-      p.t_full = tiles - tail;
-      p.s_tail = static_cast<int>(ways);
-    }
-  }
-  const int64_t units = p.t_full + (tiles - p.t_full) * p.s_tail;
+  const int64_t units = p.t_full + p.slice_pairs;
   const unsigned pairs = static_cast<unsigned>(units < slots ? units : slots);
   set_error_site("gemm_fp4_pair_kernel");
-  return launch_kernel(kernel, dim3(2 * pairs), dim3(64 + 32 * EPI), C::kSmemBytes, stream, 2, false,
-                       tmA, tmB, tmSa, tmSb, tmD, p);
+  return launch_kernel(gemm_fp4_pair_kernel<kFmt, BN, STAGES, EPI, kSliced>, dim3(2 * pairs),
+                       dim3(64 + 32 * EPI), C::kSmemBytes, stream, 2, false, tmA, tmB, tmSa, tmSb,
+                       tmD, p);
+}
+
+// Whole tiles, and the last wave's as K slices where that saves more than it costs.
+void plan_tail(Fp4GemmParams& p, int64_t slots, int BN, size_t split_bytes) {
+  const int64_t tiles = ((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + BN - 1) / BN);
+  p.t_full = tiles;
+  p.s_tail = 1;
+  p.slice_pairs = 0;
+  const int64_t tail = tiles % slots, num_kb = (p.K + kBK - 1) / kBK;
+  if (tail == 0 || p.partials == nullptr) return;
+  int64_t ways = slots / tail < 4 ? slots / tail : 4;
+  const int64_t fit = static_cast<int64_t>(split_bytes) / (tail * 2 * kBM * BN * 4);
+  if (fit < ways) ways = fit;
+  if (ways < 2 || num_kb * (ways - 1) < kTailMinBlocks * ways || tail * 16 > kWsTickets) return;
+  p.t_full = tiles - tail;
+  p.s_tail = static_cast<int>(ways);
+  p.slice_pairs = static_cast<int>(tail * ways);  // t_full is a multiple of slots, or 0
 }
 
 constexpr int64_t kDeepK = 24 * kBK;
@@ -1523,14 +1632,20 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   if (tiles <= dev.num_sms && g.K >= kDeepK)
     return run_few<kFmt, 64, 6>(g, p, dev, stream);
   if (tiles <= 2 * int64_t(dev.num_sms)) return run_few<kFmt, 64, 3>(g, p, dev, stream);
+  constexpr int kTileN = 256, kStages = 5;
+  int64_t slots = 0;
+  const cudaError_t e = pair_slots<kFmt, kTileN, kStages, 4, true>(dev, &slots);
+  if (e != cudaSuccess) return e;
+  plan_tail(p, slots, kTileN, g.ws_split_bytes);
+  if (p.s_tail > 1) return run_pair<kFmt, kTileN, kStages, 4, true>(g.a, g.b, p, dev, stream);
   // Eight epilogue warps where writing a tile takes longer than multiplying
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
   // 4096 x 4096 x 512 12.0 us against 13.1, 8192 x 8192 x 1024 37.2 against
   // 39.5, 777 x 4801 x 1600 9.5 against 11.4, but 8192 x 8192 x 2048 55.5
   // against 51.3.
   if (!p.vec || g.K <= 4 * kBK)
-    return run_pair<kFmt, 256, 5, 8>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
-  return run_pair<kFmt, 256, 5, 4>(g.a, g.b, p, g.ws_split_bytes, dev, stream);
+    return run_pair<kFmt, kTileN, kStages, 8, false>(g.a, g.b, p, dev, stream);
+  return run_pair<kFmt, kTileN, kStages, 4, false>(g.a, g.b, p, dev, stream);
 }
 
 }  // namespace
@@ -1549,6 +1664,7 @@ Fp4GemmParams base_params(const Fp4GemmArgs& g) {
   p.err = g.ws_error;
   p.partials = g.ws_split;
   p.tickets = g.ws_tickets;
+  p.begun = g.ws_begun;
   p.vec = (reinterpret_cast<uintptr_t>(g.d) & 15u) == 0 && g.ldd % 8 == 0;
   return p;
 }

@@ -21,6 +21,7 @@ constexpr size_t kWsGemmAmaxTicketOffset = 204;  // uint32: GEMM epilogue warps 
 constexpr size_t kWsSmallBAmaxOffset = 208;      // uint32: few-token product, token-side amax
 constexpr size_t kWsAmax2Offset = 212;           // uint32: paired single pass, x's amax bits
 constexpr size_t kWsNormTotalOffset = 216;       // double: gradient norm, sum of earlier launches
+constexpr size_t kWsSlicesOffset = 224;          // int32[2]: 4-bit product, pairs with a K slice begun, done
 constexpr size_t kWsScratchBegin = 64;    // [64, 256): self-cleaning counters
 constexpr size_t kWsPartialOffset = 256;  // uint32[kMaxPartials]: REDUCTION partial maxima
 constexpr int kMaxPartials = 4096;
@@ -368,6 +369,7 @@ struct Fp4GemmArgs {
   int* ws_error;
   bool b_early = false;  // the kernel before this one in the stream does not write b
   int* ws_tickets = nullptr;  // as GemmArgs': no K split of a last wave without
+  int* ws_begun = nullptr;
   float* ws_split = nullptr;
   size_t ws_split_bytes = 0;
 };
