@@ -490,11 +490,18 @@ typedef enum { FP8LIN_NVFP4 = 0, FP8LIN_MXFP4 = 1 } fp8lin_fp4_fmt;
  *   inv_scale  NVFP4: fp32[1], the inverse of the tensorwise scale (the
  *              inv_scale of the state that the tensor was quantised with);
  *              MXFP4: NULL
+ *   own_inv    NVFP4: NULL, or fp32[1] of this tensor's own.  Quantisation
+ *              writes the inverse scale that it used there too, and products
+ *              and read-back take it from there, so that the codes keep their
+ *              values when the state moves on (a delayed state's next scale,
+ *              another tensor quantised with it).  With NULL they read
+ *              *inv_scale as it is at that time.  MXFP4: NULL
  * codes and scales 16-byte aligned. */
 typedef struct fp8lin_fp4_tensor {
   uint8_t* codes;
   uint8_t* scales;
   const float* inv_scale;
+  float* own_inv;
   int64_t rows;
   int64_t cols;
   int64_t ld;

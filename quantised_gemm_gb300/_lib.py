@@ -58,6 +58,7 @@ class Fp4TensorC(ctypes.Structure):
         ("codes", ctypes.c_void_p),
         ("scales", ctypes.c_void_p),
         ("inv_scale", ctypes.c_void_p),
+        ("own_inv", ctypes.c_void_p),
         ("rows", ctypes.c_int64),
         ("cols", ctypes.c_int64),
         ("ld", ctypes.c_int64),

@@ -1112,6 +1112,8 @@ fp8lin_status check_fp4(const fp8lin_fp4_tensor* t) {
   if (t->rows > kFp4MaxDim || t->cols > kFp4MaxDim) return FP8LIN_EUNSUPPORTED;
   if ((t->fmt == FP8LIN_NVFP4) != (t->inv_scale != nullptr)) return FP8LIN_EINVAL;
   if ((reinterpret_cast<uintptr_t>(t->inv_scale) & 3u) != 0) return FP8LIN_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(t->own_inv) & 3u) != 0) return FP8LIN_EINVAL;
+  if (t->fmt == FP8LIN_MXFP4 && t->own_inv != nullptr) return FP8LIN_EINVAL;
   if (t->rows == 0 || t->cols == 0) return FP8LIN_OK;
   if (t->codes == nullptr || t->scales == nullptr || !aligned16(t->codes) || !aligned16(t->scales))
     return FP8LIN_EINVAL;
@@ -1127,6 +1129,11 @@ Fp4View fp4_view(const fp8lin_fp4_tensor* t) {
     v.ld = t->ld;
   }
   return v;
+}
+
+// The inverse scale that a tensor's codes were made with.
+const float* inv_of(const fp8lin_fp4_tensor* t) {
+  return t->own_inv != nullptr ? t->own_inv : t->inv_scale;
 }
 
 // The source and the destinations of a quantisation.
@@ -1187,6 +1194,9 @@ fp8lin_status quantise_empty(const QuantJob& j, cudaStream_t stream) {
                      j.st->fmt, j.st->eps, stream);
     j.st->needs_init = 0;
   }
+  for (const fp8lin_fp4_tensor* t : {j.out, j.out_t})
+    if (e == cudaSuccess && t != nullptr && t->own_inv != nullptr)
+      e = cudaMemcpyAsync(t->own_inv, j.st->inv_scale, sizeof(float), cudaMemcpyDeviceToDevice, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 
@@ -1201,8 +1211,11 @@ Fp4QuantArgs quant_args(const QuantJob& j, void* ws) {
   q.out_t = fp4_view(j.out_t);
   if (j.st == nullptr) return q;
   q.eps = j.st->eps;
+  if (j.out != nullptr) q.own_inv = j.out->own_inv;
+  if (j.out_t != nullptr) q.own_inv_t = j.out_t->own_inv;
   if (j.st->kind == FP8LIN_DELAYED && !j.st->needs_init) {
     q.scale_in = j.st->scale;
+    q.inv_in = j.st->inv_scale;
     q.amax_rec = reinterpret_cast<uint32_t*>(j.st->amax);
     q.rec_acc = ws_u32(ws, kWsAtomicAccOffset);
     q.rec_ticket = ws_u32(ws, kWsAtomicTicketOffset);
@@ -1291,8 +1304,8 @@ Fp4GemmArgs fp4_gemm_args(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b
   g.M = a->rows;
   g.N = b->rows;
   g.K = a->cols;
-  g.inv_a = a->inv_scale;
-  g.inv_b = b->inv_scale;
+  g.inv_a = inv_of(a);
+  g.inv_b = inv_of(b);
   g.d = d;
   g.ldd = ldd;
   g.ws_error = ws_error(ws);
@@ -1378,7 +1391,7 @@ fp8lin_status fp8lin_fp4_dequantise(const fp8lin_fp4_tensor* t, void* out, int64
     return FP8LIN_EINVAL;
   if (((t->rows + 31) / 32) > kFp4MaxDim / ((t->cols + 127) / 128)) return FP8LIN_EUNSUPPORTED;
   ProfScope ps(FP8LIN_PROF_CAST, stream);
-  cudaError_t e = launch_fp4_dequantise(fp4_view(t), t->fmt, t->inv_scale, t->rows, t->cols, out,
+  cudaError_t e = launch_fp4_dequantise(fp4_view(t), t->fmt, inv_of(t), t->rows, t->cols, out,
                                         ldo, f32 != 0, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }

@@ -500,10 +500,12 @@ struct FusedTokens {
   int64_t ldx;
   const float* amax_in;    // NVFP4: precomputed amax, or
   const float* scale_in;   // the stored scale, or (neither) the tokens' own amax
+  const float* inv_in;     // beside scale_in
   float eps;
   float* amax_out;         // each may be null
   float* scale_out;
   float* inv_out;
+  float* own_inv;          // of the quantised tokens
   uint8_t* codes;          // the quantised tokens
   int64_t ld4;
   uint8_t* scales;
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
       amax = __uint_as_float(all << 16);
     }
     s = x.scale_in != nullptr ? *x.scale_in : fp4_tensor_scale(amax, x.eps);
-    inv = x.scale_in != nullptr ? *p.inv_b : __fdiv_rn(1.0f, s);
+    inv = x.scale_in != nullptr ? *x.inv_in : __fdiv_rn(1.0f, s);
     fill_table(s, table);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       if (x.amax_out != nullptr) *x.amax_out = amax;
@@ -637,6 +639,7 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
         *x.scale_out = s;
         *x.inv_out = inv;
       }
+      if (x.own_inv != nullptr) *x.own_inv = inv;
     }
   }
   __syncthreads();  // the table is filled and the scale tiles are zero
@@ -1530,11 +1533,13 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
   t.ldx = x.ld;
   t.amax_in = x.amax_in;
   t.scale_in = x.scale_in;
+  t.inv_in = x.inv_in;
   t.eps = x.eps;
   // A stored scale's call records the amax beside it.
   t.amax_out = x.scale_in != nullptr ? reinterpret_cast<float*>(x.amax_rec) : x.amax_out;
   t.scale_out = x.scale_out;
   t.inv_out = x.inv_out;
+  t.own_inv = x.own_inv;
   t.codes = x.out.codes;
   t.ld4 = x.out.ld;
   t.scales = x.out.scales;

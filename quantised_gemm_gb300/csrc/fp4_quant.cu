@@ -63,10 +63,13 @@ struct QuantParams {
   int num_partials;
   const float* amax_in;
   const float* scale_in;
+  const float* inv_in;
   float eps;
   float* amax_out;         // each may be null; written by the tensor's first CTA
   float* scale_out;
   float* inv_out;
+  float* own_inv;          // of the tensor and its transposed copy
+  float* own_inv_t;
   uint32_t* amax_rec;      // delayed scaling: the tensor's amax, through the two words
   uint32_t* rec_acc;
   uint32_t* rec_ticket;
@@ -117,13 +120,17 @@ __device__ __forceinline__ uint32_t block_max(uint32_t bits, uint32_t* red) {
   return all;
 }
 
-// State of a dynamically scaled tensor.
+// State of a dynamically scaled tensor, and the inverse scale that the copies
+// keep for themselves.
 __device__ __forceinline__ void write_state(const QuantParams& p, float amax, float s) {
+  const float inv = p.scale_in != nullptr ? *p.inv_in : __fdiv_rn(1.0f, s);
   if (p.amax_out != nullptr) *p.amax_out = amax;
   if (p.scale_out != nullptr) {
     *p.scale_out = s;
-    *p.inv_out = __fdiv_rn(1.0f, s);
+    *p.inv_out = inv;
   }
+  if (p.own_inv != nullptr) *p.own_inv = inv;
+  if (p.own_inv_t != nullptr) *p.own_inv_t = inv;
 }
 
 // The codes and scales of one tile held in v.
@@ -589,10 +596,13 @@ QuantParams quant_params(const Fp4QuantArgs& a) {
   p.ld = a.ld;
   p.amax_in = a.amax_in;
   p.scale_in = a.scale_in;
+  p.inv_in = a.inv_in;
   p.eps = a.eps;
   p.amax_out = a.amax_out;
   p.scale_out = a.scale_out;
   p.inv_out = a.inv_out;
+  p.own_inv = a.own_inv;
+  p.own_inv_t = a.own_inv_t;
   p.amax_rec = a.amax_rec;
   p.rec_acc = a.rec_acc;
   p.rec_ticket = a.rec_ticket;

@@ -323,8 +323,9 @@ constexpr int64_t fp4_scale_ktiles(int64_t cols, int fmt) {
 // Quantise a bf16 tensor (NVFP4: fmt 0, MXFP4: fmt 1) into out, out_t (its
 // transpose) or both.  NVFP4's tensorwise scale comes from the tensor's own
 // amax (find_amax), from amax_in or from scale_in; amax_out, scale_out and
-// inv_out are written where they are not null; amax_rec records the amax
-// through the two self-cleaning words.
+// inv_out are written where they are not null, and so are own_inv and own_inv_t
+// with the inverse scale used (inv_in's with scale_in); amax_rec records the
+// amax through the two self-cleaning words.
 struct Fp4QuantArgs {
   const uint16_t* x;
   int64_t rows, cols, ld;
@@ -332,10 +333,13 @@ struct Fp4QuantArgs {
   bool find_amax = false;
   const float* amax_in = nullptr;
   const float* scale_in = nullptr;
+  const float* inv_in = nullptr;
   float eps = 0.0f;
   float* amax_out = nullptr;
   float* scale_out = nullptr;
   float* inv_out = nullptr;
+  float* own_inv = nullptr;    // of out
+  float* own_inv_t = nullptr;  // of out_t
   uint32_t* amax_rec = nullptr;
   uint32_t* rec_acc = nullptr;
   uint32_t* rec_ticket = nullptr;

@@ -30,9 +30,11 @@ class Fp4Tensor:
 
     codes: uint8 [rows, ceil(cols / 32) * 16]; scales: uint8, 512-byte tiles
     of 128 rows x 4 blocks.  Both are allocated (zero) unless given.  An NVFP4
-    tensor has the inverse tensorwise scale of ``state`` (made here unless
-    given; a tensor and its transposed copy share one), or ``inv_scale``
-    (fp32[1]) for a tensor that is only read."""
+    tensor is quantised with ``state`` (made here unless given; a tensor and
+    its transposed copy share one) and keeps the inverse scale that its codes
+    were made with in ``inv_scale`` (fp32[1]), so it may be used after the
+    state has moved on.  A tensor that is only read is given ``inv_scale``
+    instead of a state."""
 
     def __init__(self, rows: int, cols: int, fmt: int = NVFP4, *, state: ScalingState | None = None,
                  codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
@@ -60,13 +62,17 @@ class Fp4Tensor:
         if fmt == NVFP4 and state is None and inv_scale is None:
             state = ScalingState(E4M3, DYNAMIC, amax_algo=AMAX_AUTO, device=codes.device)
         self.state = state
-        self.inv_scale = state.inv_scale if state is not None else inv_scale
+        self.inv_scale = state.inv_scale.clone() if state is not None else inv_scale
         if self.inv_scale is not None and self.inv_scale.numel() != 1:
             raise ValueError("inv_scale must have one element")
         self._codes, self._scales = codes, scales
         c = _lib.Fp4TensorC()
         c.codes, c.scales = _dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8)
-        c.inv_scale = _dev(self.inv_scale, "inv_scale", torch.float32)
+        if state is not None:
+            c.inv_scale = _dev(state.inv_scale, "inv_scale", torch.float32)
+            c.own_inv = self.inv_scale.data_ptr()
+        else:
+            c.inv_scale = _dev(self.inv_scale, "inv_scale", torch.float32)
         c.rows, c.cols, c.ld, c.fmt = rows, cols, (codes.stride(0) if rows > 1 else codes.shape[1]), fmt
         self._c = c
         self._ref = ctypes.byref(c)

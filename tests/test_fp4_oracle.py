@@ -184,3 +184,16 @@ def test_gradient_refusals(lib):
     assert call(grad(), w=None) == L.EINVAL
     assert lib.fp8lin_grad_norm(grad(), 1, norm, None, nb, None) == L.EINVAL
     assert lib.fp8lin_grad_clip(grad(), 1, None, 1.0, 1e-6, None) == L.EINVAL
+
+
+def test_own_inverse_scale_refusals(lib):
+    import quantised_gemm_gb300._lib as L
+    p, ws = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x200000)
+    nb = lib.fp8lin_workspace_bytes(0, 0, 0)
+    b = _t4(32, 48)
+    for bad in (_t4(16, 48, own_inv=0x50002), _t4(16, 48, fmt=1, own_inv=0x50000)):
+        b.fmt, b.inv_scale = bad.fmt, bad.inv_scale
+        assert lib.fp8lin_fp4_dequantise(ctypes.byref(bad), p, 48, 0, None) == L.EINVAL
+        assert lib.fp8lin_fp4_gemm(ctypes.byref(bad), ctypes.byref(b), p, 32, ws, nb, None) == L.EINVAL
+        st = None if bad.fmt else ctypes.byref(_state())
+        assert lib.fp8lin_fp4_quantise(p, 16, 48, 48, st, ctypes.byref(bad), None, ws, None) == L.EINVAL
