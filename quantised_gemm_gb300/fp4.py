@@ -220,6 +220,7 @@ class Fp4Linear:
         self.ws = Workspace(M, K, N, device=device)
         self.sx, self.sw, self.sdy = self.x4.state, self.w4.state, self.dy4.state
         self._has_w = False  # w4 and w4t hold a weight at sw's scale
+        self._has_x = False  # x4t and w4t hold what a forward multiplied
 
     def forward(self, x: torch.Tensor, w: torch.Tensor | None, stream=None) -> torch.Tensor:
         """y = x W^T; w = None: the weight of the last forward that was given
@@ -237,10 +238,14 @@ class Fp4Linear:
                 s._pull()
         if w is not None:
             self._has_w = st == 0
+        self._has_x = st == 0
         _lib.check(st, "fp8lin_fp4_forward")
         return self.y
 
     def backward(self, dy: torch.Tensor, need_dx: bool = True, need_dw: bool = True, stream=None):
+        """dX and dW of the last forward."""
+        if not self._has_x:
+            raise ValueError("no forward has run: there is nothing to differentiate")
         st = _load().fp8lin_fp4_backward(
             _dense(dy, "dy", self.M, self.N), _state_arg(self.sdy), self.dy4._ref, self.dy4t._ref,
             self.w4t._ref, self.x4t._ref, self.dx.data_ptr() if need_dx else None,

@@ -93,3 +93,14 @@ def test_empty_tensor_has_its_states_scale():
     t = q.Fp4Tensor(0, 64)
     q.fp4_quantise(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), t, None, q.Workspace())
     assert torch.equal(t.inv_scale, t.state.inv_scale) and float(t.inv_scale) == o4.tensor_scale(0.0)[1]
+
+
+@pytest.mark.parametrize("fmt", [q.NVFP4, q.MXFP4], ids=["nv", "mx"])
+def test_backward_needs_a_forward(fmt):
+    lin = q.Fp4Linear(16, 32, 48, fmt=fmt)
+    x, w, dy = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((16, 32), (48, 32), (16, 48)))
+    with pytest.raises(ValueError):
+        lin.backward(dy)
+    lin.forward(x, w)
+    dx, dw = lin.backward(dy)
+    assert (dx == 48).all() and (dw == 16).all()
