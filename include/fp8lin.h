@@ -593,8 +593,11 @@ fp8lin_status fp8lin_grad_norm(const fp8lin_grad* grads, int32_t count, float* n
 
 /* out = g * min(1, max_norm / (*norm + eps)) for every tensor of the list,
  * with *norm as fp8lin_grad_norm (or a reduction over ranks) left it on the
- * device.  A NaN norm makes every value NaN; an infinite one makes every
- * finite value 0.  out may be g itself; no other overlap is allowed. */
+ * device.  The factor is 1 wherever *norm + eps <= max_norm: with max_norm
+ * infinite nothing is clipped, whatever the norm but NaN, and gradients that
+ * are all zero stay so.  A NaN norm makes every value NaN; an infinite one,
+ * with max_norm finite, makes every finite value 0.  out may be g itself; no
+ * other overlap is allowed. */
 fp8lin_status fp8lin_grad_clip(const fp8lin_grad* grads, int32_t count, const float* norm,
                                float max_norm, float eps, cudaStream_t stream);
 

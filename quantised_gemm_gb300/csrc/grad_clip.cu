@@ -278,8 +278,10 @@ __global__ void __launch_bounds__(kClipThreads, 2048 / kClipThreads)
   } else {
     length = *norm;
   }
-  const float q = __fdiv_rn(max_norm, __fadd_rn(length, eps));
-  const float coef = q > 1.0f ? 1.0f : q;  // a NaN norm makes every gradient NaN
+  // A comparison, not the smaller of 1 and the quotient: inf / inf (nothing is
+  // to be clipped) and 0 / 0 would be NaN.  A NaN norm makes every gradient NaN.
+  const float bound = __fadd_rn(length, eps);
+  const float coef = bound <= max_norm ? 1.0f : __fdiv_rn(max_norm, bound);
   // A thread's vector: 16 bytes of the wider of the two types.
   constexpr int kN = kBf16 && kOutBf16 ? 8 : 4;
   using In = std::conditional_t<kBf16 && !kOutBf16, uint2, uint4>;

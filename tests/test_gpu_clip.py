@@ -201,3 +201,34 @@ def test_python_refusals():
         q.clip_grad_norm([x.view(2, 4)], 1.0, norm, ws, outs=[torch.empty(4, 2, device="cuda").t()])
     with pytest.raises(q.Fp8linError):
         q.clip_grad_norm([x], -1.0, norm, ws)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_an_infinite_largest_norm_clips_nothing(dtype, in_place):
+    import quantised_gemm_gb300 as q
+    ws = q.Workspace()
+    for special in (1.0, float("inf"), float("-inf"), float("nan")):
+        g = [torch.randn(3000, device="cuda").to(dtype), torch.ones(10, dtype=dtype, device="cuda")]
+        g[0][77] = special
+        kept = [t.clone() for t in g]
+        outs = None if in_place else [torch.empty_like(t) for t in g]
+        norm = torch.empty(1, device="cuda")
+        q.clip_grad_norm(g, float("inf"), norm, ws, outs=outs)
+        assert math.isnan(float(norm)) if math.isnan(special) else math.isinf(float(norm)) == math.isinf(special)
+        for got, was in zip(g if in_place else outs, kept):
+            if math.isnan(special):
+                assert torch.isnan(got).all()
+            else:
+                assert torch.equal(got, was)
+        q.clip_grads(kept, float("inf"), norm)
+        if not math.isnan(special):
+            assert float(kept[0][77]) == special
+
+
+def test_zero_gradients_stay_zero_without_room():
+    import quantised_gemm_gb300 as q
+    g, norm = [torch.zeros(100, device="cuda")], torch.empty(1, device="cuda")
+    for outs in (None, [torch.ones(100, device="cuda")]):
+        q.clip_grad_norm(g, 0.0, norm, q.Workspace(), outs=outs, eps=0.0)
+        assert float(norm) == 0 and ((g if outs is None else outs)[0] == 0).all()
