@@ -402,9 +402,17 @@ __global__ void __launch_bounds__(kQThreads)
 // its tile.  Bound by the launch and two round trips to memory: 16 x 4096 in
 // 3.3 us back to back in a graph (two launches: 4.1), where a cluster of eight
 // CTAs that join their maxima took 1.7 us more than this.
-// 96 x 1024 by a call from Python 5.7 us against 7.3 us in two launches, in a
-// graph 4.2 and 4.0; 128 x 2048 7.9 and 7.3.
-constexpr int64_t kSmallElems = 98304;
+// What it costs is the scan, in segments of 512 values that a warp loads at a
+// time, and every tile's CTA scans all of them.  In a graph and by a call from
+// Python, against two launches: 24 x 4096 (192 segments, 32 tiles) 3.8 and 5.6
+// us against 3.7 and 7.7, 1 x 32768 (64, 256 tiles) 3.6 and 5.8 against 3.7 and
+// 7.6, but 4 x 24576 (192, 192 tiles) 4.6 against 3.7 and 1 x 98304 (192, 768
+// tiles) 10.6 and 10.8 against 5.2 and 7.6.  Rows with a stride, or not aligned,
+// cost more a segment: 128 x 256 in wider rows (64) 4.5 against 4.6, 16 x 4096
+// in wider rows (128) 6.7 against 4.3, 310 x 310 (310) 20 against 7.7.
+constexpr int64_t kSmallSegments = 192;
+constexpr int64_t kSmallSegmentsStrided = 64;
+constexpr int64_t kSmallScans = 24576;  // segments times tiles
 
 template <bool kTrans, int kAlign>
 __global__ void __launch_bounds__(kQThreads)
@@ -631,6 +639,13 @@ AmaxParams amax_params(const Fp4QuantArgs& a) {
   return p;
 }
 
+// The warp's loads of 512 values that share_max() makes of a tensor.
+int64_t scan_segments(const AmaxParams& p) {
+  if (p.rows == 1) return (p.cols + 511) / 512;
+  const int64_t per_row = (p.cols + (16 << p.lanes_log2) - 1) >> (4 + p.lanes_log2);
+  return ((p.rows + (32 >> p.lanes_log2) - 1) >> (5 - p.lanes_log2)) * per_row;
+}
+
 template <int kFmt, bool kTrans, bool kPair, bool kRecord>
 auto* quant_kernel(int align) {
   return align == kAlign32   ? fp4_quantise_kernel<kFmt, kTrans, kAlign32, kPair, kRecord>
@@ -648,7 +663,13 @@ auto* small_kernel(int align) {
 }  // namespace
 
 bool fp4_quantise_small_fits(const Fp4QuantArgs& a) {
-  return a.fmt == 0 && a.find_amax && a.rows * a.cols <= kSmallElems;
+  if (a.fmt != 0 || !a.find_amax) return false;
+  const AmaxParams p = amax_params(a);
+  const bool whole = p.rows == 1 && ((reinterpret_cast<uintptr_t>(a.x) & 31u) == 0 ||
+                                     row_align(a.x, a.ld, 2) != kScalar);
+  const int64_t segments = scan_segments(p);
+  if (segments > (whole ? kSmallSegments : kSmallSegmentsStrided)) return false;
+  return segments * (((a.rows + kQTile - 1) / kQTile) * ((a.cols + kQTile - 1) / kQTile)) <= kSmallScans;
 }
 
 cudaError_t launch_fp4_quantise_small(const Fp4QuantArgs& a, cudaStream_t stream) {
@@ -675,7 +696,8 @@ cudaError_t launch_fp4_amax(const Fp4QuantArgs* a, int n, uint32_t* partials, in
     const int own = row_align(a[i].x, pair.p[i].ld, 2);
     align = own < align ? own : align;
     const int64_t size = a[i].rows * a[i].cols;
-    const int64_t want = (size + 16383) / 16384, share = most * size / all + 1;
+    // Four segments a warp: 16384 values, or fewer in narrow rows.
+    const int64_t want = (scan_segments(pair.p[i]) + 31) / 32, share = most * size / all + 1;
     pair.p[i].ctas = static_cast<int>(want < share ? want : share);
     pair.p[i].partials = partials + i * (kMaxPartials / 2);
     num_partials[i] = pair.p[i].ctas;

@@ -345,7 +345,8 @@ struct Fp4QuantArgs {
   uint32_t* rec_ticket = nullptr;
   Fp4View out, out_t;
 };
-// A small tensor that needs its amax, in one launch.
+// A tensor that needs its amax and is small enough for every tile's CTA to
+// find it: one launch.
 bool fp4_quantise_small_fits(const Fp4QuantArgs& a);
 cudaError_t launch_fp4_quantise_small(const Fp4QuantArgs& a, cudaStream_t stream);
 // One or two tensors' largest magnitudes, a partial maximum a CTA in the

@@ -575,3 +575,25 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         q.Fp4Linear(16, 32, 16).forward(x[:8], torch.zeros((16, 32), dtype=torch.bfloat16,
                                                            device="cuda"))
+
+
+# Rows and columns, columns beside them, values before the first, launches.
+@pytest.mark.parametrize("rows,cols,beside,before,launches", [
+    (16, 4096, 0, 0, 1), (24, 4096, 0, 0, 1), (1, 32768, 0, 0, 1), (128, 256, 8, 0, 1), (100, 100, 1, 0, 1),
+    (2048, 1, 7, 0, 1), (1, 98304, 0, 0, 2), (98304, 1, 0, 0, 2), (98304, 1, 7, 0, 2), (4, 24576, 0, 0, 2),
+    (310, 310, 1, 0, 2), (16, 4096, 8, 0, 2), (24, 4095, 0, 1, 2), (5000, 1, 7, 0, 2), (2049, 1, 7, 0, 2)])
+def test_one_launch_where_scanning_the_tensor_is_cheap(rows, cols, beside, before, launches):
+    """Every tile's CTA of the one-launch form scans the whole tensor, so its
+    cost is the scan's loads times the tiles, not the values."""
+    import quantised_gemm_gb300 as q
+    bits, x = make(rows, cols + beside, 31)
+    x = np.ascontiguousarray(x[:, :cols])
+    room = torch.zeros(before + bits.size, dtype=torch.bfloat16, device="cuda")
+    room[before:] = to_dev_bf16(bits).view(-1)
+    xd = room[before:].view(rows, cols + beside)[:, :cols]
+    a, ws = dirty(q, rows, cols, q.NVFP4), q.Workspace()
+    n0 = q.launch_count()
+    q.fp4_quantise(xd, a, None, ws)
+    assert q.launch_count() - n0 == launches
+    check_bytes(a, x, o4.tensor_scale(np.abs(x).max())[0], "bytes")
+    assert float(a.state.amax) == np.abs(x).max()
