@@ -276,9 +276,9 @@ struct FewCfg {
   static constexpr int kStageBytes = kABytes + kBBytes + 2 * kScBytes;
   static constexpr int kSfa = BN;
   static constexpr int kSfb = kSfa + 16;
-  static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : BN + 32 <= 128 ? 128 : 256;
+  static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : 128;
   static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes + 256;
-  static_assert(BN % 16 == 0 && BN <= 128, "one row of scale tiles for B");
+  static_assert(BN % 16 == 0 && BN + 32 <= 128, "one row of scale tiles for B");
   // Two CTAs an SM, or one with a deep ring.
   static constexpr int kPerSm = STAGES <= 4 ? 2 : 1;
   static_assert(kPerSm * (kSmemBytes + (BN <= 32 || kPerSm == 1 ? joined_bytes<BN>(2) : 0) + 1024) <= 233472,
@@ -484,7 +484,8 @@ struct FusedCfg {
   static constexpr int kFixed = 1024 + 512 + 256;                // alignment, table, barriers
   static constexpr int kSfa = BN;
   static constexpr int kSfb = kSfa + 16;
-  static constexpr int kTmemCols = BN + 32 <= 64 ? 64 : 128;
+  static constexpr int kTmemCols = 64;
+  static_assert(BN + 32 <= kTmemCols, "accumulator and scales");
   // Stages beside the tokens of nkb K blocks.
   static int stages(int64_t nkb, int split, size_t smem) {
     const int64_t left = int64_t(smem) - kFixed - int64_t(joined_bytes<BN>(split)) -
@@ -867,13 +868,12 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
 // 128 rows of A and half of B's rows, and the even CTA issues
 // tcgen05.mma.cta_group::2 over both.  Each CTA's tensor memory holds the
 // scales of its own rows of A and of all BN rows of B, so both load B's scale
-// tiles whole.  BN rows of B that start inside a scale tile (BN = 192) use
-// the columns from their first 32-row group on.
+// tiles whole.
 //
-// Two accumulators of BN columns and the scales have to fit 512 columns of
-// tensor memory.  Where they do not (BN = 256), the accumulators overlap by
-// kShared columns: the epilogue reads those first and announces them on
-// `shared_free`, and the next tile's MMAs wait for that.
+// Two accumulators of BN = 256 columns and the scales do not fit the 512 columns
+// of tensor memory, so the accumulators overlap by BN - kAcc1: the epilogue
+// reads the shared columns first and announces them on `shared_free`, and the
+// next tile's MMAs wait for that.
 //
 // Where the last wave of tiles fills at most half of the pairs and the K loop
 // is long, each of its tiles runs as slices of the K loop on several pairs.
@@ -902,15 +902,14 @@ struct PairCfg {
   static constexpr int kSfCols = 4 * kKt * (1 + kRowTiles);
   static constexpr int kSfa = 512 - kSfCols;
   static constexpr int kSfb = kSfa + 4 * kKt;
-  static constexpr int kAcc1 = 2 * BN <= kSfa ? BN : kSfa - BN;  // second accumulator's first column
-  static constexpr bool kOverlap = kAcc1 < BN;
+  static constexpr int kAcc1 = kSfa - BN;                // second accumulator's first column
   static constexpr int kBoxBytes = 32 * 128;             // 32 rows x 64 bf16 columns
   static constexpr int kGroups = BN / 64 / (EPI / 4);    // boxes an epilogue warp writes
   static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes +
                                        static_cast<size_t>(EPI) * kBoxBytes + 256;
-  static_assert(BN % 64 == 0 && BN <= 256 && kBBytes % 1024 == 0, "tile");
+  static_assert(BN % 128 == 0 && BN <= 256 && kBBytes % 1024 == 0, "tile, whole scale tiles");
   static_assert(BN / 64 % (EPI / 4) == 0, "the epilogue warps of a quarter share the boxes");
-  static_assert(!kOverlap || BN - kAcc1 <= 64, "the overlap lies in one box");
+  static_assert(kAcc1 < BN && BN - kAcc1 <= 64, "the overlap lies in one box");
   static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -1065,7 +1064,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;   // [2]
   uint64_t* acc_empty = acc_full + 2;    // [2] even CTA: every epilogue warp of the pair
-  uint64_t* shared_free = acc_empty + 2;  // [1] even CTA, with overlapping accumulators
+  uint64_t* shared_free = acc_empty + 2;  // [1] even CTA: the accumulators' shared columns
   uint64_t* drain = shared_free + 1;     // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -1187,20 +1186,15 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       bool issued = false;
       for (int64_t t = pair; ok && t < num_units; t += num_pairs) {
         ok = warp_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag);
-        if constexpr (C::kOverlap) {
-          // The columns shared with the tile before this one (none before the first).
-          if (ok && issued) {
-            ok = warp_wait(shared_free, shared_phase, abort_flag);
-            shared_phase ^= 1u;
-          }
+        // The columns shared with the tile before this one (none before the first).
+        if (ok && issued) {
+          ok = warp_wait(shared_free, shared_phase, abort_flag);
+          shared_phase ^= 1u;
         }
         if (!ok) break;
         tc_fence_after_sync();
         const Unit u = unit_at<kSliced>(p, t, num_kb);
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAcc1);
-        const uint32_t sfb =
-            tmem_base + C::kSfb +
-            static_cast<uint32_t>(tile_at(u.tile, num_m, num_n, group).n * BN % 128 / 32);
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           ok = warp_wait(&full[stage], phase, abort_flag);
           if (!ok) break;
@@ -1226,7 +1220,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                   make_idesc_fp4<kFmt>(2 * kBM, BN, kFmt == 0 ? 0u : 2u * (k & 1));
               mma_fp4_pair<kFmt>(d_tmem, a_desc + static_cast<uint64_t>(2 * k),
                                  b_desc + static_cast<uint64_t>(2 * k), idesc,
-                                 tmem_base + C::kSfa + 4 * kt, sfb + 4 * C::kRowTiles * kt,
+                                 tmem_base + C::kSfa + 4 * kt,
+                                 tmem_base + C::kSfb + 4 * C::kRowTiles * kt,
                                  (kb > u.kb0 || k > 0) ? 1u : 0u);
             };
             if (kb + 1 < num_kb || last_steps == 4) {
@@ -1300,7 +1295,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
 #pragma unroll 1
       for (int g = 0; g < C::kGroups; ++g) {
         // The first accumulator's shared columns are its last, the second's its first.
-        const int i = part * C::kGroups + (C::kOverlap && acc == 0 ? C::kGroups - 1 - g : g);
+        const int i = part * C::kGroups + (acc == 0 ? C::kGroups - 1 - g : g);
         const int64_t col0 = n0 + 64 * i;
         const bool live = row0 < p.M && col0 < p.N;
         // A slice owns every s_tail-th box of a warp and hands over the others;
@@ -1316,7 +1311,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            if (C::kOverlap && g == 0) mbar_arrive_cluster_tmem(shared_free_even);
+            if (g == 0) mbar_arrive_cluster_tmem(shared_free_even);
             if (g == C::kGroups - 1) mbar_arrive_cluster_tmem(acc_empty_even + 8u * acc);
           }
         }
