@@ -473,15 +473,21 @@ fp8lin_status fp8lin_step_host(const void* x_h, const void* w_h, const void* dy_
  *            q = e2m1(x * 2^(127 - E))
  *          a value is q * 2^(E - 127)
  * All conversions round to nearest even and saturate, so the bytes are
- * defined bit for bit.  A NaN makes its block's scale NaN; in NVFP4 a NaN or
- * an infinity anywhere makes every value of the tensor decode to NaN. */
+ * defined bit for bit.  A NaN makes its block's scale NaN, and so does an
+ * infinity in MXFP4.  In NVFP4 a tensor that is scaled by its own amax decodes
+ * to NaN everywhere if it holds a NaN or an infinity; with a scale from
+ * elsewhere (delayed, precomputed) a NaN takes its block with it and an
+ * infinity saturates to the largest value, and a recorded amax shows them:
+ * an infinity makes every value NaN while it is in the history, and
+ * fp8lin_scale leaves open what it makes of a NaN. */
 typedef enum { FP8LIN_NVFP4 = 0, FP8LIN_MXFP4 = 1 } fp8lin_fp4_fmt;
 
 /* A [rows, cols] tensor in 4 bits.  The struct is host memory; the pointers
  * are caller-owned device buffers.
  *   codes      [rows, ld bytes]: two codes a byte, the even column in the low
  *              half; ld a multiple of 16, at least ceil(cols / 32) * 16.  Codes
- *              past cols, up to the next multiple of 32, are 0.
+ *              past cols, up to the next multiple of 32, are 0 (unless the
+ *              tensorwise scale is NaN: then the padding may hold NaN too).
  *   scales     fp8lin_fp4_scale_bytes(rows, cols, fmt) bytes: tiles of 512
  *              bytes, one for 128 rows x 4 blocks, block (r, k) of a tile at
  *              byte (r % 32) * 16 + (r / 32) * 4 + k; the tiles of 128 rows

@@ -14,9 +14,9 @@
 //
 // Every product and quotient is one fp32 rounding, and the conversions round
 // to nearest even and saturate, so the bytes are defined bit for bit.  A NaN
-// makes its block's scale NaN (0x7F, 0xFF); in NVFP4 a NaN or an infinity
-// anywhere also makes the tensorwise scale NaN or 0, so every value decodes
-// to NaN.
+// makes its block's scale NaN (0x7F, 0xFF).  In NVFP4 a NaN or an infinity
+// also makes a tensorwise scale of the tensor's own amax NaN or 0, so every
+// value decodes to NaN; beside a scale from elsewhere an infinity saturates.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -597,3 +597,90 @@ def test_one_launch_where_scanning_the_tensor_is_cheap(rows, cols, beside, befor
     assert q.launch_count() - n0 == launches
     check_bytes(a, x, o4.tensor_scale(np.abs(x).max())[0], "bytes")
     assert float(a.state.amax) == np.abs(x).max()
+
+
+@pytest.mark.parametrize("kind", ["delayed", "precomputed"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_nan_and_infinity_at_a_stored_scale(bad, kind):
+    """A NaN takes its block with it, an infinity saturates, the rest stays;
+    the recorded amax shows both (fp8lin_scale leaves open what it makes of a
+    NaN; an infinity leaves no scale)."""
+    import quantised_gemm_gb300 as q
+    rows, cols = 40, 100
+    s, inv = o4.tensor_scale(1.0)
+    x = torch.ones((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[5, 70] = bad
+    st = q.ScalingState(q.E4M3, q.DELAYED, 1) if kind == "delayed" else \
+        q.ScalingState(q.E4M3, amax_algo=q.AMAX_PRECOMPUTED)
+    st.needs_init = 0
+    st.amax.fill_(1.0), st.scale.fill_(s), st.inv_scale.fill_(inv)
+    a, at = q.Fp4Tensor(rows, cols, state=st), q.Fp4Tensor(cols, rows, state=st)
+    ws = q.Workspace()
+    q.fp4_quantise(x, a, at, ws)
+    one = np.float32(6 * 448) * (np.float32(inv) / np.float32(6))   # 1 and the largest value alike
+    for t, (r, c), width in ((a, (5, 70), 64), (at, (70, 5), 0)):
+        v = q.fp4_dequantise(t, torch.empty((t.rows, t.cols), device="cuda")).cpu()
+        want = torch.full(v.shape, float(one))
+        if bad == bad:
+            want[r, c] = float(one) * (1 if bad > 0 else -1)
+        else:
+            want[r, width:width + 16] = bad
+        assert torch.equal(torch.nan_to_num(v, nan=7.0), torch.nan_to_num(want, nan=7.0))
+    if kind == "delayed":
+        assert torch.equal(torch.nan_to_num(st.amax.cpu(), 7.0), torch.nan_to_num(torch.tensor([abs(bad)]), 7.0))
+        if bad == bad:
+            q.scale(st)
+            b = q.Fp4Tensor(rows, cols, state=st)
+            q.fp4_quantise(torch.ones_like(x), b, None, ws)
+            assert torch.isnan(q.fp4_dequantise(b, torch.empty((rows, cols), device="cuda"))).all()
+    # Few tokens: quantised in the product's launch, the same bytes and products.
+    w, _ = quantised(q, 130, cols, q.NVFP4, 3)
+    st.amax.fill_(1.0), st.scale.fill_(s), st.inv_scale.fill_(inv)
+    few, part = q.Fp4Tensor(8, cols, state=st), q.Fp4Tensor(8, cols, state=st)
+    y = q.fp4_linear(x[:8], few, w, torch.empty((8, 130), dtype=torch.bfloat16, device="cuda"), ws)
+    st.amax.fill_(1.0)
+    q.fp4_quantise(x[:8], part, None, ws)
+    assert torch.equal(few.codes, part.codes) and torch.equal(few.scales, part.scales)
+    want = q.fp4_gemm(part, w, torch.empty_like(y), ws)
+    assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(y.nan_to_num(), want.nan_to_num())
+    assert torch.isnan(y[5]).all() == (bad != bad) and not torch.isnan(y[:5]).any()
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=["nv", "mx"])
+@pytest.mark.parametrize("M,N,K", [(1, 100, 300), (20, 200, 500), (130, 257, 513), (1300, 1500, 700)])
+def test_codes_with_a_longer_row_stride(M, N, K, fmt):
+    import quantised_gemm_gb300 as q
+    ws = q.Workspace()
+
+    def pair(rows, cols, state=None):
+        """A tensor in wider rows of codes, and the whole rows."""
+        ld = -(-cols // 32) * 16
+        room = torch.full((rows, ld + 48), 0xA5, dtype=torch.uint8, device="cuda")
+        t = q.Fp4Tensor(rows, cols, fmt, state=state, codes=room[:, 16:16 + ld])
+        return t, (room[:, :16], room[:, 16 + ld:])
+
+    dense, wide = {}, {}
+    for name, rows, std in (("a", M, 1.0), ("b", N, 0.05)):
+        bits, x = make(rows, K, 80 + rows, std)
+        t, sides = pair(rows, K)
+        tt, sides_t = pair(K, rows, t.state)
+        q.fp4_quantise(to_dev_bf16(bits), t, tt, ws)
+        s, _ = o4.tensor_scale(np.abs(x).max())
+        check_bytes(t, x, s, name)
+        check_bytes(tt, np.ascontiguousarray(x.T), s, name + ", transposed")
+        assert all((p == 0xA5).all() for p in sides + sides_t)
+        d = dirty(q, rows, K, fmt)
+        q.fp4_quantise(to_dev_bf16(bits), d, None, ws)
+        for dtype in (torch.float32, torch.bfloat16):
+            v, w = (q.fp4_dequantise(i, torch.empty((rows, K), dtype=dtype, device="cuda")) for i in (t, d))
+            assert torch.equal(v, w)
+        wide[name], dense[name] = t, d
+        if name == "a":
+            xd = to_dev_bf16(bits)
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    want = q.fp4_gemm(dense["a"], dense["b"], out, ws).clone()
+    assert torch.equal(q.fp4_gemm(wide["a"], wide["b"], out, ws), want)
+    x4, sides = pair(M, K)
+    assert torch.equal(q.fp4_linear(xd, x4, wide["b"], out, ws), want)
+    assert torch.equal(x4.codes, dense["a"].codes) and all((p == 0xA5).all() for p in sides)
+    q.check(ws)
