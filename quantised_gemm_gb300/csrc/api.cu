@@ -1427,14 +1427,15 @@ fp8lin_status fp8lin_fp4_forward(const void* x, const void* w, fp8lin_scaling_st
   const int64_t M = x4->rows, K = x4->cols, N = w4->rows;
   fp8lin_status s = check_quantise(x, M, K, K, sx, x4, x4t, ws);
   if (s != FP8LIN_OK) return s;
-  if (w != nullptr && (s = check_quantise(w, N, K, K, sw, w4, w4t, ws)) != FP8LIN_OK) return s;
-  if (w == nullptr && sw != nullptr && sw->kind == FP8LIN_DELAYED && sw->needs_init)
+  const bool given = w != nullptr || N == 0 || K == 0;  // an empty W has no address
+  if (given && (s = check_quantise(w, N, K, K, sw, w4, w4t, ws)) != FP8LIN_OK) return s;
+  if (!given && sw != nullptr && sw->kind == FP8LIN_DELAYED && sw->needs_init)
     return FP8LIN_EINVAL;
   if ((s = check_fp4_gemm(x4, w4, y, N, ws, ws_bytes)) != FP8LIN_OK) return s;
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
   const QuantJob jobs[2] = {{x, M, K, K, sx, x4, x4t}, {w, N, K, K, sw, w4, w4t}};
-  if ((s = run_quantise(jobs, w != nullptr ? 2 : 1, ws, dev, stream)) != FP8LIN_OK) return s;
+  if ((s = run_quantise(jobs, given ? 2 : 1, ws, dev, stream)) != FP8LIN_OK) return s;
   return run_fp4_gemm(x4, w4, y, N, ws, ws_bytes, dev, stream);
 }
 

@@ -104,3 +104,20 @@ def test_backward_needs_a_forward(fmt):
     lin.forward(x, w)
     dx, dw = lin.backward(dy)
     assert (dx == 48).all() and (dw == 16).all()
+
+
+@pytest.mark.parametrize("fmt,scaling", [(q.NVFP4, "dynamic"), (q.NVFP4, "delayed"), (q.MXFP4, "dynamic")])
+@pytest.mark.parametrize("M,K,N", [(0, 64, 48), (5, 0, 48), (5, 64, 0), (0, 0, 0)])
+def test_empty_linear(M, K, N, fmt, scaling):
+    lin = q.Fp4Linear(M, K, N, fmt=fmt, scaling=scaling)
+    x, w, dy = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((M, K), (N, K), (M, N)))
+    for _ in range(2):
+        for t in (lin.y, lin.dx, lin.dw):
+            t.fill_(3.0)
+        y = lin.forward(x, w)
+        dx, dw = lin.backward(dy)
+        lin.sync_scales()
+        q.check(lin.ws)
+        assert (y == 0).all() and (dx == 0).all() and (dw == 0).all()
+    for st in (lin.sx, lin.sw):   # (an empty dX and dW leave dY alone)
+        assert st is None or st.needs_init == 0
