@@ -49,6 +49,11 @@
  *     Device-side waits are bounded: a wait that runs out records a code in
  *     the workspace and the kernel returns; fp8lin_check() reports it as
  *     FP8LIN_ETIMEOUT.  Nothing traps on the device.
+ *   - Streams: the 8-bit products that split K, and those of a few tokens,
+ *     wait for other CTAs of their own launch and count on the whole GPU.  Two
+ *     of them at the same time on different streams may each hold SMs that
+ *     the other needs until the waits run out, so keep them on one stream.
+ *     The 4-bit operands and the gradient calls have no such limit.
  *   - Alignment: every device pointer 16-byte aligned; bf16 row strides a
  *     multiple of 8 elements; columns a multiple of 16; rows a multiple of 16
  *     wherever a transposed copy (or a GEMM operand) has them as its row
@@ -590,8 +595,11 @@ typedef struct fp8lin_grad {
   int32_t out_f32;
 } fp8lin_grad;
 
-/* *norm = sqrt(sum over the list of g^2), fp32.  Squares are added in fp32
- * within a thread and in fp64 above that, in a fixed order (the same list
+/* *norm = sqrt(sum over the list of g^2), fp32.  Squares are added in fp32 over
+ * the few vectors that a thread loads together, in pairs of fp32 numbers (48
+ * bits) within a CTA and in fp64 from there on; a CTA whose squares would leave
+ * fp32's range, at either end, adds those of its values times a power of two.
+ * The order is fixed by the list's sizes, types and alignments (the same list
  * gives the same bits).  An empty list gives 0; NaN and infinities show in the
  * norm.  The list is host memory, read during the call only. */
 fp8lin_status fp8lin_grad_norm(const fp8lin_grad* grads, int32_t count, float* norm, void* ws,
