@@ -48,14 +48,14 @@ struct Fp4GemmParams {
   bool vec;                   // D's rows take 16-byte stores
   // Pair kernel: tiles [0, t_full) run whole, each one after them as s_tail
   // slices of the K loop that join through fp32 partials, tickets (two ints
-  // for each epilogue warp of a tile) and the numbers of pairs with a slice
-  // that have begun and that are done; all counters are zero between launches.
+  // for each epilogue warp of a tile) and the number of pairs with a slice that
+  // have begun; all counters are zero between launches.
   int64_t t_full;
   int s_tail;
   int slice_pairs;  // pairs whose last unit is a slice: the first ones
   float* partials;
   int* tickets;
-  int* begun;       // [2]: begun, done
+  int* begun;       // [2]: those that have begun, epilogue warps that have read it
 };
 
 // Instruction descriptor of kind::mxf4nvf4 / kind::mxf4: e2m1 operands, both
@@ -991,46 +991,54 @@ __device__ __forceinline__ void add_partial(const float* region, uint32_t (&ra)[
 // them it has a bit for each slice that left its own boxes too.
 constexpr int kArrived = 256;
 
-// Whether every pair with a slice is running.  None of them waits for anything
-// but the other slices, so a slice may then wait for these.
-__device__ __forceinline__ bool all_begun(const int* begun, int pairs, int lane) {
+// Whether every pair with a slice is running: none of them waits for anything
+// but the other slices, so a slice may then wait for these.  The last of the
+// launch's epilogue warps to ask clears both counters for the next one.
+__device__ __forceinline__ bool all_begun(int* begun, int pairs, int warps, int lane) {
   int seen = 0;
-  if (lane == 0)
-    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(begun) : "memory");
+  if (lane == 0) {
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(begun) : "memory");
+    if (atomicAdd(begun + 1, 1) == pairs * warps - 1) {
+      atomicExch(begun, 0);
+      atomicExch(begun + 1, 0);
+    }
+  }
   return __shfl_sync(0xFFFFFFFFu, seen, 0) >= pairs;
 }
 
-// Announce this warp's partials; the ticket before it.
-__device__ __forceinline__ int announce_slice(int* ticket, int add, int lane) {
+// Announce this warp's partials, and wait, bounded, for those of all slices:
+// the ticket then, or -1.
+__device__ __forceinline__ int wait_for_slices(int* ticket, int slices, volatile int* abort_flag,
+                                               int lane) {
   __threadfence();
   __syncwarp();
-  int before = 0;
-  if (lane == 0) before = atomicAdd(ticket, add);
-  before = __shfl_sync(0xFFFFFFFFu, before, 0);
-  __threadfence();
-  return before;
-}
-
-// Wait, bounded, for the partials of all slices.
-__device__ __forceinline__ bool wait_for_slices(const int* ticket, int slices, volatile int* abort_flag,
-                                                int lane) {
-  bool in = true;
+  int seen = 0;
   if (lane == 0) {
+    atomicAdd(ticket, kArrived);
     const uint64_t t0 = global_timer_ns();
-    int seen;
     while (true) {
       asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(ticket) : "memory");
       if (seen >= slices * kArrived) break;
       if (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
-        in = false;
+        seen = -1;
         break;
       }
       __nanosleep(64);
     }
   }
-  in = __shfl_sync(0xFFFFFFFFu, in ? 1 : 0, 0) != 0;
+  __syncwarp();  // lane 0's acquire holds for the warp
+  return __shfl_sync(0xFFFFFFFFu, seen, 0);
+}
+
+// The same without the wait; the ticket with this slice.
+__device__ __forceinline__ int leave_slice(int* ticket, int slice, int lane) {
   __threadfence();
-  return in;
+  __syncwarp();
+  int seen = 0;
+  if (lane == 0) seen = atomicAdd(ticket, kArrived + (1 << slice)) + kArrived + (1 << slice);
+  seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+  __threadfence();
+  return seen;
 }
 
 // The last slice to finish clears both counters for the next call.
@@ -1282,6 +1290,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       const TileAt at = tile_at(u.tile, num_m, num_n, group);
       const int row0 = at.m * 2 * kBM + static_cast<int>(rank) * kBM + quarter * 32;
       const int64_t n0 = static_cast<int64_t>(at.n) * BN;
+      // Asked while the slice's MMAs run, which hides the counter's round trips.
+      const bool meet = kSliced && u.sliced && all_begun(p.begun, p.slice_pairs, 2 * EPI, lane);
       const bool ready =
           __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag));
       if (!ready) {
@@ -1291,7 +1301,6 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(acc * C::kAcc1);
-      const bool meet = kSliced && u.sliced && all_begun(p.begun, p.slice_pairs, lane);
 #pragma unroll 1
       for (int g = 0; g < C::kGroups; ++g) {
         // The first accumulator's shared columns are its last, the second's its first.
@@ -1322,16 +1331,22 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       if (kSliced && u.sliced && row0 < p.M) {
         // The pair's last unit: its accumulator stays where it is.  A box is
         // its owner's partial plus the others in order, whoever adds them up:
-        // the owner, or the last slice to arrive if the owner has left.
+        // the owner, or, where that has left, the first slice that waited, or
+        // the last one to arrive if none did.
         int* ticket = p.tickets + 2 * warp_slot(u);
-        const int own = meet ? 0 : 1 << u.slice;
-        const int before = announce_slice(ticket, kArrived + own, lane);
-        if (meet && !wait_for_slices(ticket, p.s_tail, abort_flag, lane)) {
-          if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
-          break;
+        const int all = (1 << p.s_tail) - 1;
+        int left;
+        if (meet) {
+          const int seen = wait_for_slices(ticket, p.s_tail, abort_flag, lane);
+          if (seen < 0) {
+            if (lane == 0) record_error(p.err, abort_flag, kErrGemmEpilogueWait);
+            break;
+          }
+          left = seen & (kArrived - 1);
+          if (__ffs(~left & all) - 1 != u.slice) left = 0;
+        } else {
+          left = leave_slice(ticket, u.slice, lane) == p.s_tail * kArrived + all ? all : 0;
         }
-        const bool last = before >= (p.s_tail - 1) * kArrived;
-        const int left = last ? (before | own) & (kArrived - 1) : 0;
 #pragma unroll 1
         for (int i = part * C::kGroups; i < (part + 1) * C::kGroups; ++i) {
           const int64_t col0 = n0 + 64 * i;
@@ -1383,12 +1398,6 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
       }
     }
     cluster_sync_all();
-  }
-  // The last pair with a slice clears both numbers for the next launch.
-  if (kSliced && rank == 0 && threadIdx.x == 64 && pair < p.slice_pairs &&
-      atomicAdd(p.begun + 1, 1) == p.slice_pairs - 1) {
-    atomicExch(p.begun, 0);
-    atomicExch(p.begun + 1, 0);
   }
   if (warp == 1) {
     tc_fence_after_sync();
@@ -1554,12 +1563,6 @@ cudaError_t run_fused(const Fp4GemmArgs& g, const Fp4QuantArgs& x, Fp4GemmParams
                        bytes, stream, f.split, false, tmA, tmSa, p, t, f.split, f.stages);
 }
 
-// K blocks of a tile that slicing the last wave has to save: joining the
-// slices costs about 5 us, a block takes 0.3.  4096 x 4096 x 16384: 78.8 us
-// against 82.6, 6400 x 1600 x 12288 46.7 against 49.2, but 4096 x 4096 x 4096
-// 28.8 against 26.2.
-constexpr int kTailMinBlocks = 16;
-
 template <int kFmt, int BN, int STAGES, int EPI, bool kSliced>
 cudaError_t pair_slots(const DeviceInfo& dev, int64_t* slots) {
   static bool done[64] = {};
@@ -1598,8 +1601,22 @@ cudaError_t run_pair(const Fp4View& a, const Fp4View& b, const Fp4GemmParams& p,
                        tmD, p);
 }
 
+// What joining the slices of the last wave costs, in K blocks of a tile: 6 us
+// for two or four slices and 8 for three, whose warps have two boxes to add up
+// in one slice and one in the others; four have more to wait for where TMA
+// cannot write y's rows.  A block takes 0.3 us, 0.43 where the rows of codes
+// are not whole 128-byte lines.  Sliced against whole, us, around the limits:
+//   4096 x 1600 (two slices)   8192 25.1 24.2, 10240 28.3 28.3, 12288 31.8 32.6
+//   2560 x 2560 (three)        8192 25.5 24.1, 10240 28.3 28.4, 12288 31.3 32.6
+//   2500 x 2504 (three)        7000 28.7 29.1;  2500 x 2500: 30.8 30.2
+//   2304 x 2304 (four)         6144 21.2 20.0, 7168 22.2 22.0, 8192 23.4 24.2
+//   2200 x 2250 (four)         8192 28.3 25.7, 12288 32.4 34.1
+int join_blocks(int64_t ways, bool vec) {
+  return ways == 2 ? 20 : ways == 3 ? 26 : vec ? 21 : 31;
+}
+
 // Whole tiles, and the last wave's as K slices where that saves more than it costs.
-void plan_tail(Fp4GemmParams& p, int64_t slots, int BN, size_t split_bytes) {
+void plan_tail(Fp4GemmParams& p, int64_t slots, int BN, size_t split_bytes, bool whole_lines) {
   const int64_t tiles = ((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + BN - 1) / BN);
   p.t_full = tiles;
   p.s_tail = 1;
@@ -1609,7 +1626,8 @@ void plan_tail(Fp4GemmParams& p, int64_t slots, int BN, size_t split_bytes) {
   int64_t ways = slots / tail < 4 ? slots / tail : 4;
   const int64_t fit = static_cast<int64_t>(split_bytes) / (tail * 2 * kBM * BN * 4);
   if (fit < ways) ways = fit;
-  if (ways < 2 || num_kb * (ways - 1) < kTailMinBlocks * ways || tail * 16 > kWsTickets) return;
+  if (ways < 2 || tail * 32 > kWsTickets) return;
+  if (num_kb * (ways - 1) * (whole_lines ? 30 : 43) < join_blocks(ways, p.vec) * 30 * ways) return;
   p.t_full = tiles - tail;
   p.s_tail = static_cast<int>(ways);
   p.slice_pairs = static_cast<int>(tail * ways);  // t_full is a multiple of slots, or 0
@@ -1636,13 +1654,15 @@ cudaError_t run_fmt(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   int64_t slots = 0;
   const cudaError_t e = pair_slots<kFmt, kTileN, kStages, 4, true>(dev, &slots);
   if (e != cudaSuccess) return e;
-  plan_tail(p, slots, kTileN, g.ws_split_bytes);
-  if (p.s_tail > 1) return run_pair<kFmt, kTileN, kStages, 4, true>(g.a, g.b, p, dev, stream);
+  plan_tail(p, slots, kTileN, g.ws_split_bytes, ((g.a.ld | g.b.ld) & 127) == 0);
+  if (p.s_tail > 1)
+    return p.vec ? run_pair<kFmt, kTileN, kStages, 4, true>(g.a, g.b, p, dev, stream)
+                 : run_pair<kFmt, kTileN, kStages, 8, true>(g.a, g.b, p, dev, stream);
   // Eight epilogue warps where writing a tile takes longer than multiplying
   // it -- a short K, or rows that TMA cannot store -- and four elsewhere:
-  // 4096 x 4096 x 512 12.0 us against 13.1, 8192 x 8192 x 1024 37.2 against
-  // 39.5, 777 x 4801 x 1600 9.5 against 11.4, but 8192 x 8192 x 2048 55.5
-  // against 51.3.
+  // 4096 x 4096 x 512 11.1 us against 13.2, 8192 x 8192 x 1024 35.9 against
+  // 37.7, 777 x 4801 x 1600 9.8 against 11.6, but 8192 x 8192 x 2048 55.1
+  // against 50.9.
   if (!p.vec || g.K <= 4 * kBK)
     return run_pair<kFmt, kTileN, kStages, 8, false>(g.a, g.b, p, dev, stream);
   return run_pair<kFmt, kTileN, kStages, 4, false>(g.a, g.b, p, dev, stream);

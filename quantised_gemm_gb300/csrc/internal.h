@@ -21,7 +21,7 @@ constexpr size_t kWsGemmAmaxTicketOffset = 204;  // uint32: GEMM epilogue warps 
 constexpr size_t kWsSmallBAmaxOffset = 208;      // uint32: few-token product, token-side amax
 constexpr size_t kWsAmax2Offset = 212;           // uint32: paired single pass, x's amax bits
 constexpr size_t kWsNormTotalOffset = 216;       // double: gradient norm, sum of earlier launches
-constexpr size_t kWsSlicesOffset = 224;          // int32[2]: 4-bit product, pairs with a K slice begun, done
+constexpr size_t kWsSlicesOffset = 224;          // int32[2]: 4-bit product, pairs with a K slice begun, warps that asked
 constexpr size_t kWsScratchBegin = 64;    // [64, 256): self-cleaning counters
 constexpr size_t kWsPartialOffset = 256;  // uint32[kMaxPartials]: REDUCTION partial maxima
 constexpr int kMaxPartials = 4096;
