@@ -879,9 +879,9 @@ __device__ __forceinline__ void store_box(const uint32_t (&ra)[32], const uint32
 // is long, each of its tiles runs as slices of the K loop on several pairs.
 // A slice waits for the others of its tile only once every pair with a slice
 // has begun.  Until then -- fewer SMs than the launch counted on, or another
-// stream's kernels on them -- it leaves all of its partials and goes, and the
-// last one to arrive adds up what was left: no slice waits for one that may
-// need its SM to start.  Products without slices have a kernel without that
+// stream's kernels on them -- it leaves all of its partials and goes, and
+// another one adds up what was left: no slice waits for one that may need its
+// SM to start.  Products without slices have a kernel without that
 // code (8192 x 14336 x 4096, MXFP4: 131 us, 134 with it).
 //
 // Bound by the tensor cores: 8192 x 14336 x 4096 takes 137 us in NVFP4 (7.0
