@@ -53,14 +53,15 @@
  *     wait for other CTAs of their own launch and count on the whole GPU.  Two
  *     of them at the same time on different streams may each hold SMs that
  *     the other needs until the waits run out, so keep them on one stream.
- *     The 4-bit operands and the gradient calls have no such limit.
+ *     The 4-bit operands, the gradient calls and the layer norm have no such
+ *     limit.
  *   - Alignment: every device pointer 16-byte aligned; bf16 row strides a
  *     multiple of 8 elements; columns a multiple of 16; rows a multiple of 16
  *     wherever a transposed copy (or a GEMM operand) has them as its row
  *     length.  In practice: M, K, N multiples of 16.
  *   - Inputs are NaN-free by contract; NaN propagation is not specified.
- *     The 4-bit operands and the gradient calls say below what they do with
- *     NaN and infinities, and which sizes and alignments they take.
+ *     The 4-bit operands, the gradient calls and the layer norm say below what
+ *     they do with NaN and infinities, and which sizes and alignments they take.
  *   - Per-device set-up (kernel shared-memory attributes, occupancy counts,
  *     the device address of fp8lin_amax_noalloc's static array) is done by
  *     the first call on each device and kept for the life of the process,
@@ -620,6 +621,48 @@ fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, flo
                                     float eps, float* norm, void* ws, size_t ws_bytes,
                                     cudaStream_t stream);
 
+/* ---- layer norm ----------------------------------------------------------- */
+
+/* The norm before a Linear, over rows of bf16 values:
+ *   h = bf16(x + r)  where r is given, else h = x
+ *   mean = sum_j h_j / cols,  rstd = 1 / sqrt(sum_j (h_j - mean)^2 / cols + eps)
+ *   y = bf16((h - mean) * rstd * w + b)
+ * with sums and statistics in fp32.  x, r (the residual; NULL: none), h (written
+ * where r is given, else NULL) and y: [rows, cols], any row stride >= cols and
+ * any alignment of their elements (16-byte aligned rows are faster); cols from 1
+ * to 16384.  w, b: [cols], fp32 where param_f32 is nonzero, else bf16; b may be
+ * NULL.  stats: NULL, or fp32[2 * rows], the rows' means and then their rstd: what
+ * the backward needs beside h.  eps >= 0.
+ * y_amax: NULL, or fp32[1] that receives max |y| over the stored values (0 for
+ * no rows; it needs ws): point it at the amax of the following Linear's input
+ * state and give that state FP8LIN_AMAX_PRECOMPUTED.
+ * h may be x or r, and y may be x or h, with the same stride; no other overlap is
+ * allowed.  A NaN or an infinity in a row makes that row of y NaN and no other;
+ * the amax shows it. */
+fp8lin_status fp8lin_layer_norm(const void* x, int64_t ldx, const void* r, int64_t ldr, void* h,
+                                int64_t ldh, const void* w, const void* b, int32_t param_f32,
+                                int64_t rows, int64_t cols, float eps, void* y, int64_t ldy,
+                                float* stats, float* y_amax, void* ws, cudaStream_t stream);
+
+/* Backward of the norm, from its output's gradient dy, its h (x here) and stats:
+ *   xhat = (x - mean) * rstd,  g = dy * w
+ *   dx = bf16(rstd * (g - mean_j(g) - xhat * mean_j(g * xhat)) + dres)
+ *   dw = sum over the rows of dy * xhat,  db = sum over the rows of dy
+ * dres: NULL, or the gradient that h receives past the norm (bf16 [rows, cols]):
+ * dx is then the gradient of x and of r alike.  dx, dw, db: each may be NULL; dw
+ * and db [cols] have w's type (param_f32).  Column sums are fp32, first over the
+ * rows of a CTA and then over the CTAs, in an order that the sizes fix: the same
+ * call gives the same bits.  No rows give zeros in dw and db.
+ * dx_amax: NULL, or fp32[1] that receives max |dx| (it needs dx): the amax of the
+ * grad_output state of the Linear whose output x is.
+ * dx may be dy or dres with the same stride; no other overlap is allowed. */
+fp8lin_status fp8lin_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                         const void* w, int32_t param_f32, const float* stats,
+                                         int64_t rows, int64_t cols, const void* dres,
+                                         int64_t lddres, void* dx, int64_t lddx, void* dw, void* db,
+                                         float* dx_amax, void* ws, size_t ws_bytes,
+                                         cudaStream_t stream);
+
 /* ---- measurement hooks ------------------------------------------------ */
 
 /* Count of kernels this library has launched in the process. */
@@ -638,8 +681,8 @@ enum {
   FP8LIN_PROF_KINDS = 6
 };
 /* The 4-bit quantisations count as CAST (CAST_FUSED where they compute the
- * amax too), the 4-bit products as GEMM, the gradient norm as AMAX and the
- * gradient scaling as SCALE. */
+ * amax too), the 4-bit products as GEMM, the gradient norm as AMAX, the
+ * gradient scaling as SCALE, and the layer norm and its backward as CAST. */
 void fp8lin_profile_enable(int on);
 fp8lin_status fp8lin_profile_collect(double* ms, int64_t* count);
 

@@ -42,6 +42,7 @@ __all__ = [
     "sync_float8_amax_and_scale_history",
     "NVFP4", "MXFP4", "Fp4Tensor", "Fp4Linear", "fp4_quantise", "fp4_dequantise", "fp4_gemm",
     "fp4_linear", "grad_norm", "clip_grads", "clip_grad_norm",
+    "LayerNorm", "layer_norm", "layer_norm_backward",
 ]
 
 
@@ -343,3 +344,4 @@ from .nn import (CastConfig, Float8Linear, Float8LinearConfig,  # noqa: E402
 from .fp4 import (Fp4Linear, Fp4Tensor, fp4_dequantise, fp4_gemm, fp4_linear,  # noqa: E402
                   fp4_quantise)
 from .clip import clip_grad_norm, clip_grads, grad_norm  # noqa: E402
+from .norm import LayerNorm, layer_norm, layer_norm_backward  # noqa: E402

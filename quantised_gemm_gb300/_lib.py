@@ -136,6 +136,10 @@ _SIGNATURES = {
     "fp8lin_grad_norm": (ctypes.c_int, [_GR, _I32, _P, _P, _SZ, _P]),
     "fp8lin_grad_clip": (ctypes.c_int, [_GR, _I32, _P, _F, _F, _P]),
     "fp8lin_grad_clip_norm": (ctypes.c_int, [_GR, _I32, _F, _F, _P, _P, _SZ, _P]),
+    "fp8lin_layer_norm": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I64, _I64, _F,
+                                         _P, _I64, _P, _P, _P, _P]),
+    "fp8lin_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _I64, _I64, _P,
+                                                  _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
     "fp8lin_launch_count": (ctypes.c_uint64, []),
     "fp8lin_profile_enable": (None, [ctypes.c_int]),
     "fp8lin_profile_collect": (ctypes.c_int, [_P, _P]),

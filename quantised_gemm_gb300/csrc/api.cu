@@ -1601,6 +1601,136 @@ fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, flo
   return run_grad_clip(grads, count, a, dev, stream);
 }
 
+// ---- layer norm
+
+namespace {
+
+// A bf16 [rows, cols] tensor of any stride and alignment that a call needs.
+bool bf16_rows_ok(const void* p, int64_t cols, int64_t ld) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 1u) == 0 && ld >= cols;
+}
+
+bool param_ok(const void* p, int32_t f32) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0;
+}
+
+fp8lin_status zero_async(void* p, size_t bytes, cudaStream_t stream) {
+  if (p == nullptr) return FP8LIN_OK;
+  cudaError_t e = cudaMemsetAsync(p, 0, bytes, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+fp8lin_status fp8lin_layer_norm(const void* x, int64_t ldx, const void* r, int64_t ldr, void* h,
+                                int64_t ldh, const void* w, const void* b, int32_t param_f32,
+                                int64_t rows, int64_t cols, float eps, void* y, int64_t ldy,
+                                float* stats, float* y_amax, void* ws, cudaStream_t stream) {
+  if (rows < 0 || cols < 0 || !(eps >= 0.0f)) return FP8LIN_EINVAL;
+  if (cols < 1 || cols > kNormMaxCols) return FP8LIN_EUNSUPPORTED;
+  if (!aligned4(stats) || !aligned4(y_amax) || (y_amax != nullptr && !ws_ok(ws)))
+    return FP8LIN_EINVAL;
+  if ((r == nullptr) != (h == nullptr)) return FP8LIN_EINVAL;
+  if (!param_ok(w, param_f32) || (b != nullptr && !param_ok(b, param_f32))) return FP8LIN_EINVAL;
+  if (rows > 0) {
+    if (!bf16_rows_ok(x, cols, ldx) || !bf16_rows_ok(y, cols, ldy)) return FP8LIN_EINVAL;
+    if (r != nullptr && (!bf16_rows_ok(r, cols, ldr) || !bf16_rows_ok(h, cols, ldh)))
+      return FP8LIN_EINVAL;
+  }
+  DeviceInfo dev;
+  fp8lin_status s = get_dev(&dev);
+  if (s != FP8LIN_OK) return s;
+  if (rows == 0) return zero_async(y_amax, sizeof(float), stream);
+  LayerNormArgs a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.r = static_cast<const uint16_t*>(r);
+  a.ldr = ldr;
+  a.h = static_cast<uint16_t*>(h);
+  a.ldh = ldh;
+  a.w = w;
+  a.b = b;
+  a.param_f32 = param_f32 != 0;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.y = static_cast<uint16_t*>(y);
+  a.ldy = ldy;
+  a.stats = stats;
+  if (y_amax != nullptr) {
+    a.amax = reinterpret_cast<uint32_t*>(y_amax);
+    a.acc = ws_u32(ws, kWsAtomicAccOffset);
+    a.ticket = ws_u32(ws, kWsAtomicTicketOffset);
+  }
+  ProfScope ps(FP8LIN_PROF_CAST, stream);
+  cudaError_t e = launch_layer_norm(a, dev, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+fp8lin_status fp8lin_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                         const void* w, int32_t param_f32, const float* stats,
+                                         int64_t rows, int64_t cols, const void* dres,
+                                         int64_t lddres, void* dx, int64_t lddx, void* dw, void* db,
+                                         float* dx_amax, void* ws, size_t ws_bytes,
+                                         cudaStream_t stream) {
+  if (rows < 0 || cols < 0) return FP8LIN_EINVAL;
+  if (cols < 1 || cols > kNormMaxCols) return FP8LIN_EUNSUPPORTED;
+  if (!param_ok(w, param_f32) || (dw != nullptr && !param_ok(dw, param_f32)) ||
+      (db != nullptr && !param_ok(db, param_f32)))
+    return FP8LIN_EINVAL;
+  if (!aligned4(dx_amax) || (dx_amax != nullptr && dx == nullptr && rows > 0)) return FP8LIN_EINVAL;
+  // Partial column sums need room for four groups (the rows that a CTA takes).
+  const size_t room = sizeof(float) * 2 * 4 * static_cast<size_t>(cols);
+  if (!ws_ok(ws) || ws_bytes < kWsSplitOffset + room) return FP8LIN_EINVAL;
+  if (rows > 0) {
+    if (!bf16_rows_ok(dy, cols, lddy) || !bf16_rows_ok(x, cols, ldx)) return FP8LIN_EINVAL;
+    if (dres != nullptr && !bf16_rows_ok(dres, cols, lddres)) return FP8LIN_EINVAL;
+    if (dx != nullptr && !bf16_rows_ok(dx, cols, lddx)) return FP8LIN_EINVAL;
+    if (stats == nullptr || !aligned4(stats)) return FP8LIN_EINVAL;
+  }
+  DeviceInfo dev;
+  fp8lin_status s = get_dev(&dev);
+  if (s != FP8LIN_OK) return s;
+  if (rows == 0) {
+    const size_t bytes = static_cast<size_t>(cols) * (param_f32 ? 4 : 2);
+    if ((s = zero_async(dw, bytes, stream)) != FP8LIN_OK) return s;
+    if ((s = zero_async(db, bytes, stream)) != FP8LIN_OK) return s;
+    return zero_async(dx_amax, sizeof(float), stream);
+  }
+  if (dx == nullptr && dw == nullptr && db == nullptr) return FP8LIN_OK;
+  LayerNormBackwardArgs a = {};
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.lddy = lddy;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.w = w;
+  a.param_f32 = param_f32 != 0;
+  a.stats = stats;
+  a.rows = rows;
+  a.cols = cols;
+  a.dres = static_cast<const uint16_t*>(dres);
+  a.lddres = lddres;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.lddx = lddx;
+  a.dw = dw;
+  a.db = db;
+  if (dx_amax != nullptr) {
+    a.amax = reinterpret_cast<uint32_t*>(dx_amax);
+    a.acc = ws_u32(ws, kWsAtomicAccOffset);
+    a.ticket = ws_u32(ws, kWsAtomicTicketOffset);
+  }
+  a.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsSplitOffset);
+  a.ws_bytes = ws_bytes - kWsSplitOffset;
+  int launches = 0;
+  cudaError_t e;
+  {
+    ProfScope ps(FP8LIN_PROF_CAST, stream);
+    e = launch_layer_norm_backward(a, dev, stream, &launches);
+  }
+  if (launches > 1) g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
 uint64_t fp8lin_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 void fp8lin_profile_enable(int on) {

@@ -420,4 +420,52 @@ struct GradScaleArgs {
 cudaError_t launch_grad_scale(const GradTensor* t, int n, const GradScaleArgs& a,
                               const DeviceInfo& dev, cudaStream_t stream);
 
+// ---- layer norm (layer_norm.cu)
+
+constexpr int64_t kNormMaxCols = 16384;
+struct LayerNormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* r;  // null: no residual, and h is not written
+  int64_t ldr;
+  uint16_t* h;
+  int64_t ldh;
+  const void* w;  // fp32 where param_f32, else bf16; b may be null
+  const void* b;
+  bool param_f32;
+  int64_t rows, cols;
+  float eps;
+  uint16_t* y;
+  int64_t ldy;
+  float* stats;     // null, or the rows' means and then their inverse deviations
+  uint32_t* amax;   // null, or max |y| through the two self-cleaning words
+  uint32_t* acc;
+  uint32_t* ticket;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+struct LayerNormBackwardArgs {
+  const uint16_t* dy;
+  int64_t lddy;
+  const uint16_t* x;
+  int64_t ldx;
+  const void* w;
+  bool param_f32;  // of w, dw and db
+  const float* stats;
+  int64_t rows, cols;
+  const uint16_t* dres;  // null: nothing is added
+  int64_t lddres;
+  uint16_t* dx;  // dx, dw, db: null where not wanted
+  int64_t lddx;
+  void* dw;
+  void* db;
+  uint32_t* amax;
+  uint32_t* acc;
+  uint32_t* ticket;
+  float* ws;  // partial column sums: room for those of one CTA at least
+  size_t ws_bytes;
+};
+cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const DeviceInfo& dev,
+                                       cudaStream_t stream, int* launches);
+
 }  // namespace fp8lin

@@ -1,0 +1,150 @@
+// rows.cuh -- eight consecutive bf16 values of a row a thread, at any alignment.
+//
+// A row may begin at any multiple of two bytes.  A thread then reads the two
+// aligned 16-byte vectors that its values lie in and shifts them into place
+// (the second is its neighbour's first, so it comes from L1), and a warp
+// writes aligned vectors again, each of its own values and its neighbour's.
+// An aligned vector that holds a value of the tensor lies in memory that may
+// be read, whatever its other bytes belong to.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace fp8lin {
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = bf16lo_to_f32(w[j]);
+    v[2 * j + 1] = bf16hi_to_f32(w[j]);
+  }
+}
+
+__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&v)[8]) {
+  return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
+                    cvt_bf16x2(v[6], v[7]));
+}
+
+// Values off .. off + 7 of the sixteen in lo, hi.
+__device__ __forceinline__ uint4 shift_values(const uint4& lo, const uint4& hi, uint32_t off) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (off & 4u) {
+#pragma unroll
+    for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+  }
+  if (off & 2u) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+  }
+  if (off & 1u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The first n of eight values, the others 0.
+__device__ __forceinline__ uint4 first_values(uint4 u, int n) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (n <= 2 * j) w[j] = 0;
+    if (n == 2 * j + 1) w[j] &= 0xFFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// How many of the eight values from column c on lie in a row of `cols`.
+__device__ __forceinline__ int values_at(int64_t c, int64_t cols) {
+  const int64_t n = cols - c;
+  return n <= 0 ? 0 : n >= 8 ? 8 : static_cast<int>(n);
+}
+
+// The n values at p, the others 0.  kAligned: p is 16-byte aligned and n 0 or 8.
+template <bool kAligned>
+__device__ __forceinline__ uint4 load_values(const uint16_t* p, int n) {
+  if (n == 0) return make_uint4(0, 0, 0, 0);
+  if constexpr (kAligned) {
+    return *reinterpret_cast<const uint4*>(p);
+  } else {
+    const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
+    const uint4* v = reinterpret_cast<const uint4*>(p - off);
+    const uint4 lo = v[0];
+    uint4 hi = make_uint4(0, 0, 0, 0);
+    if (static_cast<int>(off) + n > 8) hi = v[1];
+    return first_values(shift_values(lo, hi, off), n);
+  }
+}
+
+__device__ __forceinline__ uint16_t value_of(const uint4& u, int i) {
+  const uint32_t w = i < 4 ? (i < 2 ? u.x : u.y) : (i < 6 ? u.z : u.w);
+  return static_cast<uint16_t>(i & 1 ? w >> 16 : w & 0xFFFFu);
+}
+
+// The lanes' values to p, n of them each; lane l's p lies 16 bytes behind lane
+// l - 1's, and no lane has values where one before it has fewer than eight.
+// All lanes of the warp call it.
+template <bool kAligned>
+__device__ __forceinline__ void store_values(uint16_t* p, const uint4& u, int n) {
+  if constexpr (kAligned) {
+    if (n > 0) *reinterpret_cast<uint4*>(p) = u;
+  } else {
+    const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
+    const int lane = static_cast<int>(threadIdx.x & 31u);
+    uint4 before;
+    before.x = __shfl_up_sync(0xFFFFFFFFu, u.x, 1);
+    before.y = __shfl_up_sync(0xFFFFFFFFu, u.y, 1);
+    before.z = __shfl_up_sync(0xFFFFFFFFu, u.z, 1);
+    before.w = __shfl_up_sync(0xFFFFFFFFu, u.w, 1);
+    const int n_before = __shfl_up_sync(0xFFFFFFFFu, n, 1);
+    // The aligned vector at p - off: the last `off` values of the lane before,
+    // then the first 8 - off of this one.
+    const int own = 8 - static_cast<int>(off);
+    const uint4 v = shift_values(before, u, off == 0 ? 0 : own);
+    if (off == 0 && n == 8) {
+      *reinterpret_cast<uint4*>(p) = u;
+    } else if (off != 0 && lane > 0 && n_before == 8 && n >= own) {
+      *reinterpret_cast<uint4*>(p - off) = v;
+    } else {
+      for (int i = 0; i < own && i < n; ++i) p[i] = value_of(u, i);
+      if (lane > 0)
+        for (int i = own; i < n_before; ++i) p[i - 8] = value_of(before, i);
+    }
+    if (lane == 31)
+      for (int i = own; i < n; ++i) p[i] = value_of(u, i);
+  }
+}
+
+// Eight parameters (bf16 or fp32) from p on, n of them in the tensor.
+template <typename P>
+__device__ __forceinline__ void load_params(const P* p, int n, float (&v)[8]) {
+  constexpr bool kBf16 = sizeof(P) == 2;
+  if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+    const uint4* q = reinterpret_cast<const uint4*>(p);
+    const uint4 a = __ldg(q);
+    if constexpr (kBf16) {
+      bf16x8_to_f32(a, v);
+    } else {
+      const uint4 b = __ldg(q + 1);
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.0f;
+    if (j < n) {
+      if constexpr (kBf16)
+        v[j] = bf16lo_to_f32(p[j]);
+      else
+        v[j] = p[j];
+    }
+  }
+}
+
+}  // namespace fp8lin

@@ -164,19 +164,30 @@ class _NullCtx:
         return False
 
 
-def link_linears(prev: Fp8Linear, nxt: Fp8Linear):
-    """Chain two Linears, nxt consuming prev's output: nxt's input is
+def link_linears(prev, nxt):
+    """Chain two layers, nxt consuming prev's output: nxt's input is
     ``prev.y`` and prev's grad_output is ``nxt.dx``.  prev's forward GEMM then
     writes max |y| straight into nxt's input amax, and nxt's dX GEMM writes
     max |dX| into prev's grad_output amax, both from their epilogues; the two
     states switch to AMAX_PRECOMPUTED, so each of those casts reads its tensor
     once instead of twice.  Both states must use dynamic scaling, and the
-    caller must feed exactly prev.y / nxt.dx to the linked layer."""
+    caller must feed exactly prev.y / nxt.dx to the linked layer.
+
+    One of the two may be a LayerNorm, which delivers its maxima and takes
+    none; an Fp4Linear in NVFP4 may take a LayerNorm's."""
     if prev.N != nxt.K or prev.M != nxt.M:
         raise ValueError("prev [M, N] output must be nxt's [M, K] input")
-    if nxt.sx.kind != DYNAMIC or prev.sdy.kind != DYNAMIC:
-        raise ValueError("a producer-computed amax needs dynamic scaling")
-    nxt.sx.amax_algo = AMAX_PRECOMPUTED
-    prev.sdy.amax_algo = AMAX_PRECOMPUTED
-    prev.y_amax_to = nxt.sx.amax
-    nxt.dx_amax_to = prev.sdy.amax
+    takes_x, takes_dy = getattr(nxt, "sx", None), getattr(prev, "sdy", None)
+    if takes_x is None and takes_dy is None:
+        raise ValueError("neither layer casts what the other one gives")
+    for state, giver, to in ((takes_x, prev, "y_amax_to"), (takes_dy, nxt, "dx_amax_to")):
+        if state is not None and not hasattr(giver, to):
+            raise ValueError("%s does not deliver the amax of its output" % type(giver).__name__)
+        if state is not None and state.kind != DYNAMIC:
+            raise ValueError("a producer-computed amax needs dynamic scaling")
+    if takes_x is not None:
+        takes_x.amax_algo = AMAX_PRECOMPUTED
+        prev.y_amax_to = takes_x.amax
+    if takes_dy is not None:
+        takes_dy.amax_algo = AMAX_PRECOMPUTED
+        nxt.dx_amax_to = takes_dy.amax
