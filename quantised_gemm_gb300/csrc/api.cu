@@ -1679,8 +1679,8 @@ fp8lin_status fp8lin_layer_norm_backward(const void* dy, int64_t lddy, const voi
       (db != nullptr && !param_ok(db, param_f32)))
     return FP8LIN_EINVAL;
   if (!aligned4(dx_amax) || (dx_amax != nullptr && dx == nullptr && rows > 0)) return FP8LIN_EINVAL;
-  // Partial column sums need room for four groups (the rows that a CTA takes).
-  const size_t room = sizeof(float) * 2 * 4 * static_cast<size_t>(cols);
+  // Partial column sums: room for those of one CTA at least.
+  const size_t room = sizeof(float) * 2 * static_cast<size_t>(cols + 7);
   if (!ws_ok(ws) || ws_bytes < kWsSplitOffset + room) return FP8LIN_EINVAL;
   if (rows > 0) {
     if (!bf16_rows_ok(dy, cols, lddy) || !bf16_rows_ok(x, cols, ldx)) return FP8LIN_EINVAL;

@@ -58,9 +58,8 @@ __device__ __forceinline__ uint4 first_values(uint4 u, int n) {
 }
 
 // How many of the eight values from column c on lie in a row of `cols`.
-__device__ __forceinline__ int values_at(int64_t c, int64_t cols) {
-  const int64_t n = cols - c;
-  return n <= 0 ? 0 : n >= 8 ? 8 : static_cast<int>(n);
+__device__ __forceinline__ int values_at(int c, int cols) {
+  return min(max(cols - c, 0), 8);
 }
 
 // The n values at p, the others 0.  kAligned: p is 16-byte aligned and n 0 or 8.
