@@ -53,15 +53,16 @@
  *     wait for other CTAs of their own launch and count on the whole GPU.  Two
  *     of them at the same time on different streams may each hold SMs that
  *     the other needs until the waits run out, so keep them on one stream.
- *     The 4-bit operands, the gradient calls and the layer norm have no such
- *     limit.
+ *     The 4-bit operands, the gradient calls, the layer norm and the adapters
+ *     have no such limit.
  *   - Alignment: every device pointer 16-byte aligned; bf16 row strides a
  *     multiple of 8 elements; columns a multiple of 16; rows a multiple of 16
  *     wherever a transposed copy (or a GEMM operand) has them as its row
  *     length.  In practice: M, K, N multiples of 16.
  *   - Inputs are NaN-free by contract; NaN propagation is not specified.
- *     The 4-bit operands, the gradient calls and the layer norm say below what
- *     they do with NaN and infinities, and which sizes and alignments they take.
+ *     The 4-bit operands, the gradient calls, the layer norm and the adapters say
+ *     below what they do with NaN and infinities, and which sizes and alignments
+ *     they take.
  *   - Per-device set-up (kernel shared-memory attributes, occupancy counts,
  *     the device address of fp8lin_amax_noalloc's static array) is done by
  *     the first call on each device and kept for the life of the process,
@@ -663,6 +664,71 @@ fp8lin_status fp8lin_layer_norm_backward(const void* dy, int64_t lddy, const voi
                                          float* dx_amax, void* ws, size_t ws_bytes,
                                          cudaStream_t stream);
 
+/* ---- low-rank adapters ------------------------------------------------------ */
+
+/* A bank of `count` low-rank adapters beside one Linear of k inputs and n
+ * outputs: adapter g adds s_g B_g A_g to its weight.  The struct is host memory;
+ * the pointers are caller-owned device buffers.
+ *   a      bf16 [count, rank, k] dense
+ *   b      bf16 [count, n, rank] dense
+ *   scale  fp32 [count]
+ * count 1 to 1024, rank 1 to 128, k and n 1 to 2^22; any alignment of the
+ * elements (a and b 16-byte aligned, k and n multiples of 8, and rank a multiple
+ * of 4 up to 16 or of 8 above, are faster).  Adapters of a smaller rank are padded
+ * with zeros. */
+typedef struct fp8lin_adapters {
+  const void* a;
+  const void* b;
+  const float* scale;
+  int64_t count;
+  int64_t k;
+  int64_t n;
+  int32_t rank;
+} fp8lin_adapters;
+
+/* Each row of a batch has an adapter: index[i], int32 on the device; a number
+ * outside [0, count) means none.  The calls below sort the rows by adapter first,
+ * in one launch, unless they are given a route: what fp8lin_adapter_route made of
+ * the same index, rows and count, for a program that uses one batch's index
+ * beside several Linears.  route: device buffer of
+ * fp8lin_adapter_route_bytes(rows, count) bytes, 4-byte aligned.  A route of
+ * another index, rows or count gives wrong results or reads out of bounds.
+ * rows: 0 to 2^24. */
+size_t fp8lin_adapter_route_bytes(int64_t rows, int64_t count);
+fp8lin_status fp8lin_adapter_route(const int32_t* index, int64_t rows, int64_t count, void* route,
+                                   cudaStream_t stream);
+
+/* The adapters' part of a Linear's forward, added to that of the shared weight:
+ *   h_i = A_g x_i               fp32 [rows, rank] dense, written
+ *   y_i = bf16(base_i + B_g (s_g h_i))      g = index[i]
+ * x: bf16 [rows, k], base (NULL: zeros) and y: bf16 [rows, n], any row strides and
+ * alignments; y may be base with the same stride, and overlaps nothing else.  A row
+ * without an adapter has h_i = 0 and y_i = base_i, bit for bit.  Products are
+ * accumulated in fp32; s_g h_i goes in as two bf16 numbers, hi + lo (2^-17).  The
+ * order of all sums is fixed by the sizes and the index.  Up to 64 rows take one
+ * launch and no route.  NaN and infinities stay in their rows. */
+fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, int64_t ldx,
+                                    const int32_t* index, const void* route, int64_t rows,
+                                    const void* base, int64_t ldbase, void* y, int64_t ldy, float* h,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The adapters' part of the backward, from the forward's x and h:
+ *   dh_i = s_g B_g^T dy_i                       fp32 [rows, rank] dense, written
+ *   dx_i = bf16(base_i + A_g^T dh_i)            base: the shared weight's part of dx, or NULL
+ *   dA_g = bf16(sum over g's rows of dh_i x_i^T)
+ *   dB_g = bf16(sum over g's rows of dy_i (s_g h_i)^T)
+ * dy: bf16 [rows, n]; x, base, dx: bf16 [rows, k]; da, db: dense, of the shapes of
+ * a and b, zeros for adapters that no row has.  dx, da and db may each be NULL (x
+ * is needed for da, h for db only).  dx may be base with the same stride; nothing
+ * else may overlap what is written.  dh and s_g h go into the products as hi + lo.
+ * The order of all sums is fixed by the sizes, the index and ws_bytes. */
+fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy, int64_t lddy,
+                                      const void* x, int64_t ldx, const float* h,
+                                      const int32_t* index, const void* route, int64_t rows,
+                                      const void* base, int64_t ldbase, void* dx, int64_t lddx,
+                                      float* dh, void* da, void* db, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream);
+
 /* ---- measurement hooks ------------------------------------------------ */
 
 /* Count of kernels this library has launched in the process. */
@@ -682,7 +748,8 @@ enum {
 };
 /* The 4-bit quantisations count as CAST (CAST_FUSED where they compute the
  * amax too), the 4-bit products as GEMM, the gradient norm as AMAX, the
- * gradient scaling as SCALE, and the layer norm and its backward as CAST. */
+ * gradient scaling as SCALE, the layer norm and its backward as CAST, and the
+ * adapters' kernels as GEMM (SMALL_M for a few rows, SCALE for the sorting). */
 void fp8lin_profile_enable(int on);
 fp8lin_status fp8lin_profile_collect(double* ms, int64_t* count);
 

@@ -43,6 +43,7 @@ __all__ = [
     "NVFP4", "MXFP4", "Fp4Tensor", "Fp4Linear", "fp4_quantise", "fp4_dequantise", "fp4_gemm",
     "fp4_linear", "grad_norm", "clip_grads", "clip_grad_norm",
     "LayerNorm", "layer_norm", "layer_norm_backward",
+    "Adapters", "AdapterRoute", "adapter_linear", "adapter_backward",
 ]
 
 
@@ -345,3 +346,4 @@ from .fp4 import (Fp4Linear, Fp4Tensor, fp4_dequantise, fp4_gemm, fp4_linear,  #
                   fp4_quantise)
 from .clip import clip_grad_norm, clip_grads, grad_norm  # noqa: E402
 from .norm import LayerNorm, layer_norm, layer_norm_backward  # noqa: E402
+from .adapters import AdapterRoute, Adapters, adapter_backward, adapter_linear  # noqa: E402

@@ -77,6 +77,19 @@ class GradC(ctypes.Structure):
     ]
 
 
+class AdaptersC(ctypes.Structure):
+    """Mirror of struct fp8lin_adapters."""
+    _fields_ = [
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+        ("rank", ctypes.c_int32),
+    ]
+
+
 class Fp8linError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -97,6 +110,7 @@ _ST = ctypes.POINTER(ScalingStateC)
 _T4 = ctypes.POINTER(Fp4TensorC)
 _GR = ctypes.c_void_p  # GradC array, or its address
 _F = ctypes.c_float
+_AD = ctypes.POINTER(AdaptersC)
 
 _SIGNATURES = {
     "fp8lin_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -140,6 +154,12 @@ _SIGNATURES = {
                                          _P, _I64, _P, _P, _P, _P]),
     "fp8lin_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _I64, _I64, _P,
                                                   _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "fp8lin_adapter_route_bytes": (_SZ, [_I64, _I64]),
+    "fp8lin_adapter_route": (ctypes.c_int, [_P, _I64, _I64, _P, _P]),
+    "fp8lin_adapter_linear": (ctypes.c_int, [_AD, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P,
+                                             _SZ, _P]),
+    "fp8lin_adapter_backward": (ctypes.c_int, [_AD, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P,
+                                               _I64, _P, _P, _P, _P, _SZ, _P]),
     "fp8lin_launch_count": (ctypes.c_uint64, []),
     "fp8lin_profile_enable": (None, [ctypes.c_int]),
     "fp8lin_profile_collect": (ctypes.c_int, [_P, _P]),

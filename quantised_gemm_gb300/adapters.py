@@ -1,0 +1,159 @@
+"""Low-rank adapters of many requests beside a shared Linear, and their
+training: row i of a batch has adapter index[i] of a bank, or none.
+
+  h_i = A x_i                         fp32, kept for the backward
+  y_i = base_i + s B h_i              base: what the shared weight gave
+  dh_i = s B^T dy_i,  dx_i = base_i + A^T dh_i
+  dA = sum of dh_i x_i^T,  dB = sum of s dy_i h_i^T   over the adapter's rows
+
+The shared product is fp4_linear(), Fp4Linear, Fp8Linear or any other; its y (or
+dx) is the base and may be the output too.  Any sizes, row strides and
+alignments, ranks up to 128; ``include/fp8lin.h`` has the numerics.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from . import Workspace, _dev, _stream
+from .fp4 import _matrix
+from .norm import _here, _rows_like
+
+_load = _lib.load
+
+
+def _whole(t: torch.Tensor, name: str, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s" % (name, list(shape)))
+    return _dev(t, name, dtype)
+
+
+class Adapters:
+    """A bank of adapters of one Linear: a (bf16 [count, rank, K]), b (bf16
+    [count, N, rank]) and scale (fp32 [count]).  An adapter of a smaller rank is
+    padded with zeros.  The tensors' values may change between calls (training);
+    other tensors take another bank."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor):
+        if a.dim() != 3 or b.dim() != 3:
+            raise ValueError("a [count, rank, K] and b [count, N, rank] expected")
+        count, rank, k = a.shape
+        n = b.shape[1]
+        c = _lib.AdaptersC()
+        c.a = _whole(a, "a", (count, rank, k), torch.bfloat16)
+        c.b = _whole(b, "b", (count, n, rank), torch.bfloat16)
+        c.scale = _whole(scale, "scale", (count,), torch.float32)
+        if not (1 <= count <= 1024 and 1 <= rank <= 128 and k >= 1 and n >= 1):
+            raise ValueError("1 to 1024 adapters of rank 1 to 128 expected, and K and N of at least 1")
+        self._a, self._b, self._scale = a, b, scale
+        self.count, self.rank, self.K, self.N = count, rank, k, n
+        c.count, c.k, c.n, c.rank = count, k, n, rank
+        self._c = c
+        self._ref = ctypes.byref(c)
+
+    @property
+    def a(self) -> torch.Tensor:
+        return self._a
+
+    @property
+    def b(self) -> torch.Tensor:
+        return self._b
+
+    @property
+    def scale(self) -> torch.Tensor:
+        return self._scale
+
+
+class AdapterRoute:
+    """A batch's rows sorted by adapter, made once by set(index) and given to the
+    calls beside every Linear that the batch goes through.  It is for `rows`
+    rows and banks of `count` adapters."""
+
+    def __init__(self, rows: int, count: int, device="cuda"):
+        self.rows, self.count = rows, count
+        nbytes = int(_load().fp8lin_adapter_route_bytes(rows, count))
+        if nbytes == 0:
+            raise ValueError("0 to 2^24 rows and 1 to 1024 adapters expected")
+        self.buf = torch.zeros(nbytes // 4, dtype=torch.int32, device=device)
+        self._set = False
+
+    def set(self, index: torch.Tensor, stream=None) -> AdapterRoute:
+        _here(index, self.buf)
+        self._set = False
+        st = _load().fp8lin_adapter_route(_index(index, self.rows), self.rows, self.count,
+                                          self.buf.data_ptr(), _stream(stream))
+        _lib.check(st, "fp8lin_adapter_route")
+        self._set = True
+        return self
+
+
+def _index(index: torch.Tensor, rows: int):
+    return _whole(index, "index", (rows,), torch.int32)
+
+
+def _route(route: AdapterRoute | None, rows: int, bank: Adapters):
+    if route is None:
+        return None
+    if (route.rows, route.count) != (rows, bank.count):
+        raise ValueError("the route is for %d rows and %d adapters, not %d and %d"
+                         % (route.rows, route.count, rows, bank.count))
+    if not route._set:
+        raise ValueError("the route has no index yet")
+    return route.buf.data_ptr()
+
+
+def adapter_linear(x: torch.Tensor, index: torch.Tensor, bank: Adapters, y: torch.Tensor,
+                   h: torch.Tensor, ws: Workspace, *, base: torch.Tensor | None = None,
+                   route: AdapterRoute | None = None, stream=None) -> torch.Tensor:
+    """y = base + the adapters' part for x (bf16 [M, K]).  index: int32 [M], a
+    number outside [0, count) for a row without an adapter; base: bf16 [M, N] or
+    None for zeros, and may be y; h (fp32 [M, rank]) receives A x, for the
+    backward.  route: index sorted before, where several calls share it."""
+    px, rows, k, ldx = _matrix(x, "x")
+    if ws is None:
+        raise ValueError("a Workspace is required")
+    if k != bank.K:
+        raise ValueError("x must be [M, %d]" % bank.K)
+    _here(x, index, bank.a, y, h, base, ws.buf, None if route is None else route.buf)
+    py, ldy = _rows_like(y, "y", rows, bank.N)
+    pb, ldb = _rows_like(base, "base", rows, bank.N)
+    st = _load().fp8lin_adapter_linear(bank._ref, px, ldx, _index(index, rows), _route(route, rows, bank),
+                                       rows, pb, ldb, py, ldy,
+                                       _whole(h, "h", (rows, bank.rank), torch.float32), ws.ptr,
+                                       ws.nbytes, _stream(stream))
+    _lib.check(st, "fp8lin_adapter_linear")
+    return y
+
+
+def adapter_backward(dy: torch.Tensor, x: torch.Tensor | None, h: torch.Tensor | None,
+                     index: torch.Tensor, bank: Adapters, dh: torch.Tensor,
+                     dx: torch.Tensor | None, da: torch.Tensor | None, db: torch.Tensor | None,
+                     ws: Workspace, *, base: torch.Tensor | None = None,
+                     route: AdapterRoute | None = None, stream=None):
+    """dx = base + the adapters' part, dA and dB (bf16, of the bank's shapes; zeros
+    for adapters that no row has), from the forward's x and h; each of the three
+    may be None, x is needed for da only and h for db.  dh: fp32 [M, rank]
+    receives s B^T dy.  base may be dx."""
+    pdy, rows, n, lddy = _matrix(dy, "dy")
+    if ws is None:
+        raise ValueError("a Workspace is required")
+    if n != bank.N:
+        raise ValueError("dy must be [M, %d]" % bank.N)
+    if (da is not None and x is None) or (db is not None and h is None):
+        raise ValueError("da needs x, and db needs h")
+    _here(dy, x, h, index, bank.a, dh, dx, da, db, base, ws.buf, None if route is None else route.buf)
+    px, ldx = _rows_like(x, "x", rows, bank.K)
+    pdx, lddx = _rows_like(dx, "dx", rows, bank.K)
+    pb, ldb = _rows_like(base, "base", rows, bank.K)
+    low = (rows, bank.rank)
+    st = _load().fp8lin_adapter_backward(
+        bank._ref, pdy, lddy, px, ldx, None if h is None else _whole(h, "h", low, torch.float32),
+        _index(index, rows), _route(route, rows, bank), rows, pb, ldb, pdx, lddx,
+        _whole(dh, "dh", low, torch.float32),
+        None if da is None else _whole(da, "da", bank.a.shape, torch.bfloat16),
+        None if db is None else _whole(db, "db", bank.b.shape, torch.bfloat16), ws.ptr, ws.nbytes,
+        _stream(stream))
+    _lib.check(st, "fp8lin_adapter_backward")
+    return dx, da, db

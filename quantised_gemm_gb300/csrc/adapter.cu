@@ -1,0 +1,474 @@
+// adapter.cu -- the low-rank adapters' launchers, the sorting of rows by adapter
+// and the one-launch forward of a few rows.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include "adapter_kernels.cuh"
+#include "internal.h"
+
+namespace fp8lin {
+namespace {
+
+// ---------------------------------------------------------------- route
+
+constexpr int kRouteWarps = 32;
+
+// The rows sorted by adapter, each adapter's in order (a counting sort by one
+// CTA: warp w takes the w-th run of rows).  8192 rows: see adapter_route below.
+__global__ void __launch_bounds__(32 * kRouteWarps)
+    adapter_route_kernel(const int32_t* index, int rows, int count, int32_t* first, int32_t* sorted) {
+  extern __shared__ int table[];  // [warp][group]: how many, then where the next one goes
+  __shared__ int warp_total[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int groups = count + 1;
+  for (int i = static_cast<int>(threadIdx.x); i < groups * kRouteWarps; i += 32 * kRouteWarps) table[i] = 0;
+  __syncthreads();
+  const int run = ((rows + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
+  const int64_t begin = int64_t(warp) * run;
+  int* const mine = table + warp * groups;
+  auto group_at = [&](int64_t i) {
+    if (i >= rows) return -1;
+    const int a = __ldg(index + i);
+    return a >= 0 && a < count ? a : count;
+  };
+  for (int64_t i = begin + lane; i - lane < begin + run; i += 32) {
+    const int g = i < begin + run ? group_at(i) : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, g);
+    if (g >= 0 && __ffs(static_cast<int>(same)) - 1 == lane) mine[g] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // Group by group, warp by warp: exclusive sums.
+  int before = 0;
+  for (int base = 0; base < groups; base += 32 * kRouteWarps) {
+    const int g = base + static_cast<int>(threadIdx.x);
+    int total = 0;
+    if (g < groups)
+      for (int w = 0; w < kRouteWarps; ++w) total += table[w * groups + g];
+    int up = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xFFFFFFFFu, up, o);
+      if (lane >= o) up += a;
+    }
+    if (lane == 31) warp_total[warp] = up;
+    __syncthreads();
+    int warps_before = 0, all = 0;
+    for (int w = 0; w < kRouteWarps; ++w) {
+      if (w < warp) warps_before += warp_total[w];
+      all += warp_total[w];
+    }
+    int at = before + warps_before + up - total;
+    if (g < groups) {
+      first[g] = at;
+      for (int w = 0; w < kRouteWarps; ++w) {
+        const int n = table[w * groups + g];
+        table[w * groups + g] = at;
+        at += n;
+      }
+      if (g == groups - 1) first[groups] = rows;
+    }
+    before += all;
+    __syncthreads();
+  }
+  for (int64_t i = begin + lane; i - lane < begin + run; i += 32) {
+    const int g = i < begin + run ? group_at(i) : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, g);
+    if (g >= 0) sorted[mine[g] + __popc(same & ((1u << lane) - 1u))] = static_cast<int32_t>(i);
+    __syncwarp();
+    if (g >= 0 && __ffs(static_cast<int>(same)) - 1 == lane) mine[g] += __popc(same);
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------- a few rows
+
+// One row a cluster: each CTA takes a part of K for the low product, the parts'
+// sums go to every CTA of the cluster through distributed shared memory, and
+// each CTA takes a part of N for the high product.  Bound by reading A and B
+// once, and by latency: one launch.
+struct FewArgs {
+  const uint16_t *x, *a, *b, *base;
+  uint16_t* y;
+  const float* scale;
+  const int32_t* index;
+  float* low;
+  int64_t ldx, ldbase, ldy;
+  int k, n, rank, count;
+};
+constexpr int kFewWarps = 8, kFewCluster = 8;  // a warp has one rank at least: kRanks >= kFewWarps
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum) {
+  float x[8], y[8];
+  bf16x8_to_f32(a, x);
+  bf16x8_to_f32(b, y);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = fmaf(x[j], y[j], sum);
+  return sum;
+}
+
+// kLanes: lanes a column of B, eight ranks each.
+template <int kLanes, bool kAligned>
+__global__ void __launch_bounds__(32 * kFewWarps) adapter_few_kernel(const __grid_constant__ FewArgs p) {
+  constexpr int kRanks = 8 * kLanes;
+  __shared__ float sums[kFewCluster][kRanks];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int64_t row = blockIdx.x / kFewCluster;
+  const int part = static_cast<int>(blockIdx.x) % kFewCluster;
+  const int adapter = __ldg(p.index + row);
+  const bool none = adapter < 0 || adapter >= p.count;
+  // The columns of y that this CTA writes, and of x that it reads: multiples of 8.
+  const int n_part = ((p.n + kFewCluster - 1) / kFewCluster + 7) / 8 * 8;
+  const int n0 = part * n_part, n1 = min(n0 + n_part, p.n);
+  const uint16_t* const base = p.base == nullptr ? nullptr : p.base + row * p.ldbase;
+  uint16_t* const y = p.y + row * p.ldy;
+  if (none) {
+    if (part == 0)
+      for (int j = static_cast<int>(threadIdx.x); j < p.rank; j += 32 * kFewWarps) p.low[row * p.rank + j] = 0.0f;
+    if (y != base)
+      for (int c = n0 + static_cast<int>(threadIdx.x); c < n1; c += 32 * kFewWarps)
+        y[c] = base == nullptr ? uint16_t(0) : base[c];
+    return;  // all CTAs of the cluster
+  }
+  cluster_arrive();  // this CTA has begun: its shared memory may be written
+  const uint16_t* const a = p.a + int64_t(adapter) * p.rank * p.k;
+  const uint16_t* const b = p.b + int64_t(adapter) * p.rank * p.n;
+  const uint16_t* const x = p.x + row * p.ldx;
+  const int k_part = ((p.k + kFewCluster - 1) / kFewCluster + 7) / 8 * 8;
+  const int k0 = part * k_part, k1 = min(k0 + k_part, p.k);
+  bool begun = false;
+  for (int j = warp; j < kRanks; j += kFewWarps) {
+    float sum = 0.0f;
+    if (j < p.rank) {
+#pragma unroll 2
+      for (int c = k0 + 8 * lane; c < k1; c += 256) {
+        const int n = kAligned ? 8 : min(8, k1 - c);
+        sum = dot8(load_values<kAligned>(x + c, n), load_values<kAligned>(a + int64_t(j) * p.k + c, n), sum);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
+    if (!begun) cluster_wait();
+    begun = true;
+    if (lane < kFewCluster)
+      st_shared_cluster_u32(map_to_cta(smem_addr(&sums[part][j]), lane), __float_as_uint(sum));
+  }
+  cluster_sync_all();
+  const int sub = lane % kLanes, at = lane / kLanes;
+  constexpr int kCols = 32 / kLanes;  // columns a warp takes at a time
+  float low[8];
+  const float scale = __ldg(p.scale + adapter);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    low[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kFewCluster; ++i) low[j] += sums[i][8 * sub + j];
+  }
+  if (part == 0 && warp == 0 && at == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (8 * sub + j < p.rank) p.low[row * p.rank + 8 * sub + j] = low[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) low[j] *= scale;
+  const int ranks = min(max(p.rank - 8 * sub, 0), 8);
+#pragma unroll 8
+  for (int c0 = n0 + warp * kCols; c0 < n1; c0 += kFewWarps * kCols) {
+    const int c = c0 + at;
+    float sum = 0.0f;
+    if (c < n1) {
+      float w[8];
+      bf16x8_to_f32(load_values<kAligned>(b + int64_t(c) * p.rank + 8 * sub, kAligned && ranks > 0 ? 8 : ranks), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(low[j], w[j], sum);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (c < n1 && sub == 0) {
+      if (base != nullptr) sum += bf16lo_to_f32(base[c]);
+      y[c] = static_cast<uint16_t>(cvt_bf16x2(sum, 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSumThreads) adapter_sum_kernel(const __grid_constant__ SumArgs a,
+                                                                  const __grid_constant__ SumArgs b,
+                                                                  int blocks_a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int block = static_cast<int>(blockIdx.x), group = static_cast<int>(blockIdx.y);
+  if (block < blocks_a)
+    sum_partials(a, group, block, blocks_a);
+  else
+    sum_partials(b, group, block - blocks_a, static_cast<int>(gridDim.x) - blocks_a);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool rows_aligned(const void* p, int64_t ld, int64_t cols) {
+  return p == nullptr || (aligned16(p) && ld % 8 == 0 && cols % 8 == 0);
+}
+
+// 1, 2, 4, 8 or 16 tiles of eight ranks.
+int rank_tiles(int rank) {
+  int t = 1;
+  while (8 * t < rank) t *= 2;
+  return t;
+}
+
+template <int kValue>
+using Int = std::integral_constant<int, kValue>;
+
+template <typename Run>
+cudaError_t with_rank_tiles(int rank, Run run) {
+  switch (rank_tiles(rank)) {
+    case 1: return run(Int<1>());
+    case 2: return run(Int<2>());
+    case 4: return run(Int<4>());
+    case 8: return run(Int<8>());
+    default: return run(Int<16>());
+  }
+}
+
+// Tiles of `size` rows, at most: each adapter with rows may end inside one.
+int64_t most_tiles(int64_t rows, int64_t groups, int64_t size) {
+  const int64_t t = rows / size + groups;
+  return t < rows ? t : rows;
+}
+
+// Whether the rows are enough for tiles of 32 to be mostly full.
+bool wide_tiles(const AdapterArgs& a) { return a.rows > 16 * a.count; }
+
+Route route_of(const AdapterArgs& a) {
+  return Route{a.route, a.route + a.count + 2, static_cast<int>(a.count) + 1};
+}
+
+// B's rows of `rank` values, as the kernels load them.
+bool b_aligned(const AdapterArgs& a) { return aligned16(a.b) && a.rank % (a.rank <= 16 ? 4 : 8) == 0; }
+bool a_aligned(const AdapterArgs& a) { return aligned16(a.a) && a.k % 8 == 0; }
+
+}  // namespace
+
+cudaError_t launch_adapter_route(const int32_t* index, int64_t rows, int64_t count, int32_t* route,
+                                 const DeviceInfo& dev, cudaStream_t stream) {
+  set_error_site("adapter_route_kernel");
+  const size_t bytes = sizeof(int) * kRouteWarps * static_cast<size_t>(count + 1);
+  if (bytes > 40 * 1024) {
+    static std::mutex mu;
+    static bool done[64];
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev.device]) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(adapter_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(sizeof(int) * kRouteWarps * (kAdapterMaxCount + 1)));
+      if (e != cudaSuccess) return e;
+      done[dev.device] = true;
+    }
+  }
+  return launch_kernel(adapter_route_kernel, dim3(1), dim3(32 * kRouteWarps), bytes, stream, 1, false,
+                       index, static_cast<int>(rows), static_cast<int>(count), route, route + count + 2);
+}
+
+bool adapter_few_fits(const AdapterArgs& a) { return a.rows <= 64; }
+
+cudaError_t launch_adapter_few(const AdapterArgs& a, const int32_t* index, const uint16_t* x, int64_t ldx,
+                               const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
+                               float* low, cudaStream_t stream) {
+  set_error_site("adapter_few_kernel");
+  FewArgs p = {};
+  p.x = x;
+  p.a = a.a;
+  p.b = a.b;
+  p.base = base;
+  p.y = y;
+  p.scale = a.scale;
+  p.index = index;
+  p.low = low;
+  p.ldx = ldx;
+  p.ldbase = ldbase;
+  p.ldy = ldy;
+  p.k = static_cast<int>(a.k);
+  p.n = static_cast<int>(a.n);
+  p.rank = a.rank;
+  p.count = static_cast<int>(a.count);
+  const bool aligned = rows_aligned(x, ldx, a.k) && a_aligned(a) && aligned16(a.b) && a.rank % 8 == 0;
+  const dim3 grid(static_cast<unsigned>(a.rows) * kFewCluster), block(32 * kFewWarps);
+  return with_rank_tiles(a.rank, [&](auto lanes) {
+    constexpr int kLanes = decltype(lanes)::value;
+    return aligned ? launch_kernel(adapter_few_kernel<kLanes, true>, grid, block, 0, stream, kFewCluster, false, p)
+                   : launch_kernel(adapter_few_kernel<kLanes, false>, grid, block, 0, stream, kFewCluster, false, p);
+  });
+}
+
+cudaError_t launch_adapter_low(const AdapterArgs& a, bool backward, const uint16_t* x, int64_t ldx,
+                               float* low, const DeviceInfo& dev, cudaStream_t stream) {
+  set_error_site("adapter_low_kernel");
+  LowArgs p = {};
+  p.x = x;
+  p.ldx = ldx;
+  p.w = backward ? a.b : a.a;
+  p.scale = backward ? a.scale : nullptr;
+  p.low = low;
+  p.cols = static_cast<int>(backward ? a.n : a.k);
+  p.rank = a.rank;
+  p.route = route_of(a);
+  p.w_aligned = backward ? b_aligned(a) : a_aligned(a);
+  const bool aligned = rows_aligned(x, ldx, p.cols);
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    constexpr int kRankTiles = decltype(ranks)::value;
+    auto run = [&](auto tiles) {
+      constexpr int kTiles = decltype(tiles)::value;
+      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles);
+      // Enough CTAs for two an SM, and 32 columns a warp at least.
+      p.parts = 1;
+      while (p.parts < 8 && most * p.parts < 2 * dev.num_sms && 32 * kLowWarps * 2 * p.parts <= p.cols)
+        p.parts *= 2;
+      const dim3 grid(static_cast<unsigned>(most * p.parts)), block(32 * kLowWarps);
+      auto go = [&](auto* kernel) {
+        return launch_kernel(kernel, grid, block, 0, stream, p.parts, false, p);
+      };
+      if (backward)
+        return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, false, true>)
+                       : go(adapter_low_kernel<kTiles, kRankTiles, false, false>);
+      return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, true, true>)
+                     : go(adapter_low_kernel<kTiles, kRankTiles, true, false>);
+    };
+    if constexpr (kRankTiles <= 8)
+      if (wide_tiles(a)) return run(Int<2>());
+    return run(Int<1>());
+  });
+}
+
+cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
+                                const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
+                                const DeviceInfo& dev, cudaStream_t stream) {
+  set_error_site("adapter_high_kernel");
+  HighArgs p = {};
+  p.low = low;
+  p.w = backward ? a.a : a.b;
+  p.scale = backward ? nullptr : a.scale;
+  p.base = base;
+  p.y = y;
+  p.ldbase = ldbase;
+  p.ldy = ldy;
+  p.cols = static_cast<int>(backward ? a.k : a.n);
+  p.rank = a.rank;
+  p.route = route_of(a);
+  p.w_aligned = backward ? a_aligned(a) : b_aligned(a);
+  p.low_aligned = aligned16(low) && a.rank % 4 == 0;
+  const bool aligned = rows_aligned(base, ldbase, p.cols) && rows_aligned(y, ldy, p.cols);
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    constexpr int kSteps = decltype(ranks)::value <= 2 ? 1 : decltype(ranks)::value / 2;
+    auto run = [&](auto tiles) {
+      constexpr int kTiles = decltype(tiles)::value;
+      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles);
+      // Slabs of whole rounds of the warps, and some CTAs an SM.
+      constexpr int kRound = 32 * kHighWarps;
+      const int rounds = (p.cols + kRound - 1) / kRound;
+      int64_t slabs = (4 * int64_t(dev.num_sms) + most - 1) / most;
+      if (slabs > rounds) slabs = rounds;
+      const int per = static_cast<int>((rounds + slabs - 1) / slabs);
+      p.slab = per * kRound;
+      const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>((rounds + per - 1) / per));
+      auto go = [&](auto* kernel) {
+        return launch_kernel(kernel, grid, dim3(32 * kHighWarps), 0, stream, 1, false, p);
+      };
+      if (backward)
+        return aligned ? go(adapter_high_kernel<kTiles, kSteps, false, true>)
+                       : go(adapter_high_kernel<kTiles, kSteps, false, false>);
+      return aligned ? go(adapter_high_kernel<kTiles, kSteps, true, true>)
+                     : go(adapter_high_kernel<kTiles, kSteps, true, false>);
+    };
+    if constexpr (kSteps <= 4)
+      if (wide_tiles(a)) return run(Int<2>());
+    return run(Int<1>());
+  });
+}
+
+int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev) {
+  const int64_t cols = da ? a.k : a.n;
+  const int64_t slab = weight_slab(rank_tiles(a.rank)), slabs = (cols + slab - 1) / slab;
+  // Two CTAs an SM, tiles of kWeightRows rows, and the partials of 2 rows / tile
+  // slots in the workspace.
+  int64_t rows = (a.rows * slabs + 2 * dev.num_sms - 1) / (2 * dev.num_sms);
+  rows = (rows + kWeightRows - 1) / kWeightRows * kWeightRows;
+  const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));
+  if (slots < 4) return a.rows;  // no room: every adapter's rows in one tile
+  const int64_t least = (2 * a.rows + slots - 1) / slots;
+  if (rows < least) rows = (least + kWeightRows - 1) / kWeightRows * kWeightRows;
+  return rows < a.rows ? rows : a.rows;
+}
+
+cudaError_t launch_adapter_weight(const AdapterArgs& a, bool da, const uint16_t* x, int64_t ldx,
+                                  const float* low, int64_t tile_rows, uint16_t* dw, float* partials,
+                                  cudaStream_t stream) {
+  set_error_site("adapter_weight_kernel");
+  WeightArgs p = {};
+  p.x = x;
+  p.ldx = ldx;
+  p.low = low;
+  p.scale = da ? nullptr : a.scale;
+  p.dw = dw;
+  p.partials = partials;
+  p.cols = static_cast<int>(da ? a.k : a.n);
+  p.rank = a.rank;
+  p.tile_rows = static_cast<int>(tile_rows);
+  p.route = route_of(a);
+  // dA's rows are written as vectors.
+  const bool aligned = rows_aligned(x, ldx, p.cols) && (!da || aligned16(dw));
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    constexpr int kRankTiles = decltype(ranks)::value;
+    constexpr int kSlab = weight_slab(kRankTiles);
+    const dim3 grid(static_cast<unsigned>(most_tiles(a.rows, a.count, tile_rows)),
+                    static_cast<unsigned>((p.cols + kSlab - 1) / kSlab));
+    auto go = [&](auto* kernel) {
+      return launch_kernel(kernel, grid, dim3(32 * kWeightWarps), 0, stream, 1, false, p);
+    };
+    if (da)
+      return aligned ? go(adapter_weight_kernel<kRankTiles, false, true>)
+                     : go(adapter_weight_kernel<kRankTiles, false, false>);
+    return aligned ? go(adapter_weight_kernel<kRankTiles, true, true>)
+                   : go(adapter_weight_kernel<kRankTiles, true, false>);
+  });
+}
+
+cudaError_t launch_adapter_sum(const AdapterArgs& a, uint16_t* da, const float* da_partials,
+                               int64_t da_rows, uint16_t* db, const float* db_partials,
+                               int64_t db_rows, cudaStream_t stream) {
+  set_error_site("adapter_sum_kernel");
+  auto job = [&](uint16_t* dw, const float* partials, int64_t rows, int64_t cols) {
+    SumArgs s = {};
+    s.dw = dw;
+    s.partials = partials;
+    s.size = cols * a.rank;
+    s.tile_rows = static_cast<int>(rows);
+    s.route = route_of(a);
+    return s;
+  };
+  const SumArgs sa = job(da, da_partials, da_rows, a.k), sb = job(db, db_partials, db_rows, a.n);
+  auto blocks = [&](const SumArgs& s) {
+    if (s.dw == nullptr) return 0;
+    const int64_t n = (s.size + kSumThreads - 1) / kSumThreads;
+    return static_cast<int>(n < 1024 ? n : 1024);
+  };
+  const int na = blocks(sa), nb = blocks(sb);
+  return launch_kernel(adapter_sum_kernel, dim3(static_cast<unsigned>(na + nb), static_cast<unsigned>(a.count)),
+                       dim3(kSumThreads), 0, stream, 1, false, sa, sb, na);
+}
+
+}  // namespace fp8lin

@@ -1731,6 +1731,191 @@ fp8lin_status fp8lin_layer_norm_backward(const void* dy, int64_t lddy, const voi
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 
+// ---- low-rank adapters
+
+namespace {
+
+// The bank and its rows' adapters.
+fp8lin_status check_adapters(const fp8lin_adapters* ad, int64_t rows, const int32_t* index,
+                             const void* route) {
+  if (ad == nullptr || ad->count < 1 || ad->k < 1 || ad->n < 1 || ad->rank < 1 || rows < 0)
+    return FP8LIN_EINVAL;
+  if (ad->count > kAdapterMaxCount || ad->rank > kAdapterMaxRank || ad->k > kAdapterMaxDim ||
+      ad->n > kAdapterMaxDim || rows > kAdapterMaxRows)
+    return FP8LIN_EUNSUPPORTED;
+  for (const void* p : {ad->a, ad->b})
+    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 1u) != 0) return FP8LIN_EINVAL;
+  if (ad->scale == nullptr || !aligned4(ad->scale)) return FP8LIN_EINVAL;
+  if (!aligned4(index) || !aligned4(route)) return FP8LIN_EINVAL;
+  if (rows > 0 && index == nullptr && route == nullptr) return FP8LIN_EINVAL;
+  return FP8LIN_OK;
+}
+
+AdapterArgs adapter_args(const fp8lin_adapters* ad, int64_t rows) {
+  AdapterArgs a = {};
+  a.a = static_cast<const uint16_t*>(ad->a);
+  a.b = static_cast<const uint16_t*>(ad->b);
+  a.scale = ad->scale;
+  a.count = ad->count;
+  a.k = ad->k;
+  a.n = ad->n;
+  a.rank = ad->rank;
+  a.rows = rows;
+  return a;
+}
+
+// The caller's route, or one made at the start of the workspace's room, which
+// then begins behind it.
+fp8lin_status route_rows(AdapterArgs& a, const int32_t* index, const void* route, uint8_t*& room,
+                         size_t& room_bytes, const DeviceInfo& dev, cudaStream_t stream) {
+  a.route = static_cast<const int32_t*>(route);
+  if (route != nullptr) return FP8LIN_OK;
+  const size_t bytes = adapter_route_bytes(a.rows, a.count);
+  if (bytes > room_bytes) return FP8LIN_EUNSUPPORTED;
+  ProfScope ps(FP8LIN_PROF_SCALE, stream);
+  int32_t* made = reinterpret_cast<int32_t*>(room);
+  cudaError_t e = launch_adapter_route(index, a.rows, a.count, made, dev, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  a.route = made;
+  room += bytes;
+  room_bytes -= bytes;
+  return FP8LIN_OK;
+}
+
+}  // namespace
+
+size_t fp8lin_adapter_route_bytes(int64_t rows, int64_t count) {
+  if (rows < 0 || rows > kAdapterMaxRows || count < 1 || count > kAdapterMaxCount) return 0;
+  return adapter_route_bytes(rows, count);
+}
+
+fp8lin_status fp8lin_adapter_route(const int32_t* index, int64_t rows, int64_t count, void* route,
+                                   cudaStream_t stream) {
+  if (rows < 0 || count < 1) return FP8LIN_EINVAL;
+  if (rows > kAdapterMaxRows || count > kAdapterMaxCount) return FP8LIN_EUNSUPPORTED;
+  if (!aligned4(index) || (rows > 0 && index == nullptr) || route == nullptr || !aligned4(route))
+    return FP8LIN_EINVAL;
+  DeviceInfo dev;
+  fp8lin_status s = get_dev(&dev);
+  if (s != FP8LIN_OK) return s;
+  ProfScope ps(FP8LIN_PROF_SCALE, stream);
+  cudaError_t e = launch_adapter_route(index, rows, count, static_cast<int32_t*>(route), dev, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, int64_t ldx,
+                                    const int32_t* index, const void* route, int64_t rows,
+                                    const void* base, int64_t ldbase, void* y, int64_t ldy, float* h,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream) {
+  fp8lin_status s = check_adapters(ad, rows, index, route);
+  if (s != FP8LIN_OK) return s;
+  if (!ws_ok(ws) || ws_bytes < kWsFixedBytes) return FP8LIN_EINVAL;
+  if (rows > 0) {
+    if (!bf16_rows_ok(x, ad->k, ldx) || !bf16_rows_ok(y, ad->n, ldy)) return FP8LIN_EINVAL;
+    if (base != nullptr && !bf16_rows_ok(base, ad->n, ldbase)) return FP8LIN_EINVAL;
+    if (y == base && ldy != ldbase && rows > 1) return FP8LIN_EINVAL;
+    if (h == nullptr || !aligned4(h)) return FP8LIN_EINVAL;
+  }
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  if (rows == 0) return FP8LIN_OK;
+  AdapterArgs a = adapter_args(ad, rows);
+  const uint16_t* xs = static_cast<const uint16_t*>(x);
+  const uint16_t* bases = static_cast<const uint16_t*>(base);
+  uint16_t* ys = static_cast<uint16_t*>(y);
+  if (index != nullptr && adapter_few_fits(a)) {
+    ProfScope ps(FP8LIN_PROF_SMALL_M, stream);
+    cudaError_t e = launch_adapter_few(a, index, xs, ldx, bases, ldbase, ys, ldy, h, stream);
+    return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+  }
+  uint8_t* room = static_cast<uint8_t*>(ws) + kWsSplitOffset;
+  size_t room_bytes = ws_bytes > kWsSplitOffset ? ws_bytes - kWsSplitOffset : 0;
+  if ((s = route_rows(a, index, route, room, room_bytes, dev, stream)) != FP8LIN_OK) return s;
+  {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    cudaError_t e = launch_adapter_low(a, false, xs, ldx, h, dev, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  ProfScope ps(FP8LIN_PROF_GEMM, stream);
+  cudaError_t e = launch_adapter_high(a, false, h, bases, ldbase, ys, ldy, dev, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+}
+
+fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy, int64_t lddy,
+                                      const void* x, int64_t ldx, const float* h,
+                                      const int32_t* index, const void* route, int64_t rows,
+                                      const void* base, int64_t ldbase, void* dx, int64_t lddx,
+                                      float* dh, void* da, void* db, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream) {
+  fp8lin_status s = check_adapters(ad, rows, index, route);
+  if (s != FP8LIN_OK) return s;
+  if (!ws_ok(ws) || ws_bytes < kWsFixedBytes) return FP8LIN_EINVAL;
+  for (const void* p : {static_cast<const void*>(da), static_cast<const void*>(db)})
+    if ((reinterpret_cast<uintptr_t>(p) & 1u) != 0) return FP8LIN_EINVAL;
+  if (rows > 0) {
+    if (!bf16_rows_ok(dy, ad->n, lddy)) return FP8LIN_EINVAL;
+    if (da != nullptr && !bf16_rows_ok(x, ad->k, ldx)) return FP8LIN_EINVAL;
+    if (db != nullptr && (h == nullptr || !aligned4(h))) return FP8LIN_EINVAL;
+    if (base != nullptr && !bf16_rows_ok(base, ad->k, ldbase)) return FP8LIN_EINVAL;
+    if (dx != nullptr && !bf16_rows_ok(dx, ad->k, lddx)) return FP8LIN_EINVAL;
+    if (dx != nullptr && dx == base && lddx != ldbase && rows > 1) return FP8LIN_EINVAL;
+    if (dh == nullptr || !aligned4(dh)) return FP8LIN_EINVAL;
+  }
+  DeviceInfo dev;
+  if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
+  const size_t da_bytes = static_cast<size_t>(ad->count) * ad->rank * ad->k * 2;
+  const size_t db_bytes = static_cast<size_t>(ad->count) * ad->rank * ad->n * 2;
+  if (rows == 0) {
+    if ((s = zero_async(da, da_bytes, stream)) != FP8LIN_OK) return s;
+    return zero_async(db, db_bytes, stream);
+  }
+  AdapterArgs a = adapter_args(ad, rows);
+  const uint16_t* dys = static_cast<const uint16_t*>(dy);
+  uint8_t* room = static_cast<uint8_t*>(ws) + kWsSplitOffset;
+  size_t room_bytes = ws_bytes > kWsSplitOffset ? ws_bytes - kWsSplitOffset : 0;
+  if ((s = route_rows(a, index, route, room, room_bytes, dev, stream)) != FP8LIN_OK) return s;
+  cudaError_t e;
+  {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_low(a, true, dys, lddy, dh, dev, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  // The room for partial sums: shared as the sizes of dA and dB are.
+  const size_t for_da = da == nullptr ? 0
+                        : db == nullptr
+                            ? room_bytes
+                            : static_cast<size_t>(static_cast<double>(room_bytes) * ad->k / (ad->k + ad->n)) / 256 * 256;
+  float* const da_part = reinterpret_cast<float*>(room);
+  float* const db_part = reinterpret_cast<float*>(room + for_da);
+  int64_t da_rows = 1, db_rows = 1;
+  if (db != nullptr) {
+    db_rows = adapter_weight_rows(a, false, room_bytes - for_da, dev);
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_weight(a, false, dys, lddy, h, db_rows, static_cast<uint16_t*>(db), db_part, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (da != nullptr) {
+    da_rows = adapter_weight_rows(a, true, for_da, dev);
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_weight(a, true, static_cast<const uint16_t*>(x), ldx, dh, da_rows,
+                              static_cast<uint16_t*>(da), da_part, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (dx != nullptr) {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_high(a, true, dh, static_cast<const uint16_t*>(base), ldbase,
+                            static_cast<uint16_t*>(dx), lddx, dev, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (da != nullptr || db != nullptr) {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_sum(a, static_cast<uint16_t*>(da), da_part, da_rows, static_cast<uint16_t*>(db),
+                           db_part, db_rows, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return FP8LIN_OK;
+}
+
 uint64_t fp8lin_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 void fp8lin_profile_enable(int on) {

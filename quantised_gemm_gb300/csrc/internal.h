@@ -468,4 +468,45 @@ struct LayerNormBackwardArgs {
 cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const DeviceInfo& dev,
                                        cudaStream_t stream, int* launches);
 
+// ---- low-rank adapters (adapter.cu)
+
+constexpr int64_t kAdapterMaxCount = 1024, kAdapterMaxDim = int64_t(1) << 22, kAdapterMaxRows = int64_t(1) << 24;
+constexpr int kAdapterMaxRank = 128;
+// Rows and the bank of adapters that they choose from.
+struct AdapterArgs {
+  const uint16_t* a;   // [count, rank, k]
+  const uint16_t* b;   // [count, n, rank]
+  const float* scale;  // [count]
+  int64_t count, k, n, rows;
+  int rank;
+  const int32_t* route;  // count + 2 words, then the rows sorted by adapter
+};
+inline size_t adapter_route_bytes(int64_t rows, int64_t count) {
+  return (static_cast<size_t>(rows + count + 2) * sizeof(int32_t) + 255) / 256 * 256;
+}
+cudaError_t launch_adapter_route(const int32_t* index, int64_t rows, int64_t count, int32_t* route,
+                                 const DeviceInfo& dev, cudaStream_t stream);
+// The forward of a few rows in one launch, without a route.
+bool adapter_few_fits(const AdapterArgs& a);
+cudaError_t launch_adapter_few(const AdapterArgs& a, const int32_t* index, const uint16_t* x, int64_t ldx,
+                               const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
+                               float* low, cudaStream_t stream);
+// low = x A^T, or (backward) low = s x B with x the output's gradient.
+cudaError_t launch_adapter_low(const AdapterArgs& a, bool backward, const uint16_t* x, int64_t ldx,
+                               float* low, const DeviceInfo& dev, cudaStream_t stream);
+// y = base + s low B^T, or (backward) y = base + low A.
+cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
+                                const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
+                                const DeviceInfo& dev, cudaStream_t stream);
+// dA (x the input, low = dh) or dB (x the output's gradient, low = h): tiles of
+// adapter_weight_rows rows; an adapter with several leaves partials, one slot of
+// cols * rank numbers a tile, for launch_adapter_sum.
+int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev);
+cudaError_t launch_adapter_weight(const AdapterArgs& a, bool da, const uint16_t* x, int64_t ldx,
+                                  const float* low, int64_t tile_rows, uint16_t* dw, float* partials,
+                                  cudaStream_t stream);
+cudaError_t launch_adapter_sum(const AdapterArgs& a, uint16_t* da, const float* da_partials,
+                               int64_t da_rows, uint16_t* db, const float* db_partials,
+                               int64_t db_rows, cudaStream_t stream);
+
 }  // namespace fp8lin

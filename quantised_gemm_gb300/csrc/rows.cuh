@@ -83,22 +83,22 @@ __device__ __forceinline__ uint16_t value_of(const uint4& u, int i) {
   return static_cast<uint16_t>(i & 1 ? w >> 16 : w & 0xFFFFu);
 }
 
-// The lanes' values to p, n of them each; lane l's p lies 16 bytes behind lane
-// l - 1's, and no lane has values where one before it has fewer than eight.
-// All lanes of the warp call it.
-template <bool kAligned>
+// The lanes' values to p, n of them each, in spans of kSpan lanes: a lane's p lies
+// 16 bytes behind that of the lane before it in the span, and no lane has values
+// where one before it has fewer than eight.  All lanes of the warp call it.
+template <bool kAligned, int kSpan = 32>
 __device__ __forceinline__ void store_values(uint16_t* p, const uint4& u, int n) {
   if constexpr (kAligned) {
     if (n > 0) *reinterpret_cast<uint4*>(p) = u;
   } else {
     const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
-    const int lane = static_cast<int>(threadIdx.x & 31u);
+    const int lane = static_cast<int>(threadIdx.x) & (kSpan - 1);
     uint4 before;
-    before.x = __shfl_up_sync(0xFFFFFFFFu, u.x, 1);
-    before.y = __shfl_up_sync(0xFFFFFFFFu, u.y, 1);
-    before.z = __shfl_up_sync(0xFFFFFFFFu, u.z, 1);
-    before.w = __shfl_up_sync(0xFFFFFFFFu, u.w, 1);
-    const int n_before = __shfl_up_sync(0xFFFFFFFFu, n, 1);
+    before.x = __shfl_up_sync(0xFFFFFFFFu, u.x, 1, kSpan);
+    before.y = __shfl_up_sync(0xFFFFFFFFu, u.y, 1, kSpan);
+    before.z = __shfl_up_sync(0xFFFFFFFFu, u.z, 1, kSpan);
+    before.w = __shfl_up_sync(0xFFFFFFFFu, u.w, 1, kSpan);
+    const int n_before = __shfl_up_sync(0xFFFFFFFFu, n, 1, kSpan);
     // The aligned vector at p - off: the last `off` values of the lane before,
     // then the first 8 - off of this one.
     const int own = 8 - static_cast<int>(off);
@@ -112,7 +112,7 @@ __device__ __forceinline__ void store_values(uint16_t* p, const uint4& u, int n)
       if (lane > 0)
         for (int i = own; i < n_before; ++i) p[i - 8] = value_of(before, i);
     }
-    if (lane == 31)
+    if (lane == kSpan - 1)
       for (int i = own; i < n; ++i) p[i] = value_of(u, i);
   }
 }
