@@ -31,17 +31,29 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   const int run = ((rows + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
   const int64_t begin = int64_t(warp) * run;
   int* const mine = table + warp * groups;
-  auto group_at = [&](int64_t i) {
-    if (i >= rows) return -1;
-    const int a = __ldg(index + i);
-    return a >= 0 && a < count ? a : count;
+  // Eight loads of a lane are in flight together.
+  constexpr int kLoads = 8;
+  auto each = [&](auto fn) {
+    for (int64_t i0 = begin; i0 < begin + run && i0 < rows; i0 += 32 * kLoads) {
+      int a[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int64_t i = i0 + 32 * j + lane;
+        a[j] = i < begin + run && i < rows ? __ldg(index + i) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int64_t i = i0 + 32 * j + lane;
+        const int g = i < begin + run && i < rows ? (a[j] >= 0 && a[j] < count ? a[j] : count) : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, g);
+        if (i0 + 32 * j < begin + run && i0 + 32 * j < rows) fn(i, g, same);
+      }
+    }
   };
-  for (int64_t i = begin + lane; i - lane < begin + run; i += 32) {
-    const int g = i < begin + run ? group_at(i) : -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, g);
+  each([&](int64_t, int g, uint32_t same) {
     if (g >= 0 && __ffs(static_cast<int>(same)) - 1 == lane) mine[g] += __popc(same);
     __syncwarp();
-  }
+  });
   __syncthreads();
   // Group by group, warp by warp: exclusive sums.
   int before = 0;
@@ -76,14 +88,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     before += all;
     __syncthreads();
   }
-  for (int64_t i = begin + lane; i - lane < begin + run; i += 32) {
-    const int g = i < begin + run ? group_at(i) : -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, g);
+  each([&](int64_t i, int g, uint32_t same) {
     if (g >= 0) sorted[mine[g] + __popc(same & ((1u << lane) - 1u))] = static_cast<int32_t>(i);
     __syncwarp();
     if (g >= 0 && __ffs(static_cast<int>(same)) - 1 == lane) mine[g] += __popc(same);
     __syncwarp();
-  }
+  });
 }
 
 // ---------------------------------------------------------------- a few rows
@@ -250,8 +260,8 @@ int64_t most_tiles(int64_t rows, int64_t groups, int64_t size) {
   return t < rows ? t : rows;
 }
 
-// Whether the rows are enough for tiles of 32 to be mostly full.
-bool wide_tiles(const AdapterArgs& a) { return a.rows > 16 * a.count; }
+// Whether an adapter has rows for tiles of several warps, on average.
+bool wide_tiles(const AdapterArgs& a) { return a.rows >= 64 * a.count; }
 
 Route route_of(const AdapterArgs& a) {
   return Route{a.route, a.route + a.count + 2, static_cast<int>(a.count) + 1};
@@ -327,30 +337,29 @@ cudaError_t launch_adapter_low(const AdapterArgs& a, bool backward, const uint16
   p.cols = static_cast<int>(backward ? a.n : a.k);
   p.rank = a.rank;
   p.route = route_of(a);
-  p.w_aligned = backward ? b_aligned(a) : a_aligned(a);
-  const bool aligned = rows_aligned(x, ldx, p.cols);
+  const bool aligned = rows_aligned(x, ldx, p.cols) && (backward ? b_aligned(a) : a_aligned(a));
   return with_rank_tiles(a.rank, [&](auto ranks) {
     constexpr int kRankTiles = decltype(ranks)::value;
-    auto run = [&](auto tiles) {
-      constexpr int kTiles = decltype(tiles)::value;
-      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles);
-      // Enough CTAs for two an SM, and 32 columns a warp at least.
+    auto run = [&](auto tiles, auto row_warps) {
+      constexpr int kTiles = decltype(tiles)::value, kRowWarps = decltype(row_warps)::value;
+      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles * kRowWarps);
+      // One wave of two CTAs an SM, as far as the rows have tiles (a CTA spends 8 us
+      // on finding its rows and on the sums), and 32 columns a warp at least.
+      constexpr int kTurn = 32 * kLowWarps / kRowWarps;
       p.parts = 1;
-      while (p.parts < 8 && most * p.parts < 2 * dev.num_sms && 32 * kLowWarps * 2 * p.parts <= p.cols)
-        p.parts *= 2;
+      while (p.parts < 8 && most * p.parts * 2 <= 2 * dev.num_sms && kTurn * 2 * p.parts <= p.cols) p.parts *= 2;
       const dim3 grid(static_cast<unsigned>(most * p.parts)), block(32 * kLowWarps);
       auto go = [&](auto* kernel) {
         return launch_kernel(kernel, grid, block, 0, stream, p.parts, false, p);
       };
       if (backward)
-        return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, false, true>)
-                       : go(adapter_low_kernel<kTiles, kRankTiles, false, false>);
-      return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, true, true>)
-                     : go(adapter_low_kernel<kTiles, kRankTiles, true, false>);
+        return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, false, true>)
+                       : go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, false, false>);
+      return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, true, true>)
+                     : go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, true, false>);
     };
-    if constexpr (kRankTiles <= 8)
-      if (wide_tiles(a)) return run(Int<2>());
-    return run(Int<1>());
+    if (!wide_tiles(a)) return run(Int<1>(), Int<1>());
+    return run(Int<kRankTiles <= 4 ? 2 : 1>(), Int<kRankTiles <= 4 ? 2 : 4>());
   });
 }
 
@@ -369,18 +378,18 @@ cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float
   p.cols = static_cast<int>(backward ? a.k : a.n);
   p.rank = a.rank;
   p.route = route_of(a);
-  p.w_aligned = backward ? a_aligned(a) : b_aligned(a);
+  const bool w_aligned = backward ? a_aligned(a) : b_aligned(a);
   p.low_aligned = aligned16(low) && a.rank % 4 == 0;
   const bool aligned = rows_aligned(base, ldbase, p.cols) && rows_aligned(y, ldy, p.cols);
   return with_rank_tiles(a.rank, [&](auto ranks) {
     constexpr int kSteps = decltype(ranks)::value <= 2 ? 1 : decltype(ranks)::value / 2;
-    auto run = [&](auto tiles) {
-      constexpr int kTiles = decltype(tiles)::value;
-      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles);
+    auto run = [&](auto tiles, auto row_warps) {
+      constexpr int kTiles = decltype(tiles)::value, kRowWarps = decltype(row_warps)::value;
+      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles * kRowWarps);
       // Slabs of whole rounds of the warps, and some CTAs an SM.
-      constexpr int kRound = 32 * kHighWarps;
+      constexpr int kRound = 32 * kHighWarps / kRowWarps;
       const int rounds = (p.cols + kRound - 1) / kRound;
-      int64_t slabs = (4 * int64_t(dev.num_sms) + most - 1) / most;
+      int64_t slabs = (8 * int64_t(dev.num_sms) + most - 1) / most;
       if (slabs > rounds) slabs = rounds;
       const int per = static_cast<int>((rounds + slabs - 1) / slabs);
       p.slab = per * kRound;
@@ -388,79 +397,107 @@ cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float
       auto go = [&](auto* kernel) {
         return launch_kernel(kernel, grid, dim3(32 * kHighWarps), 0, stream, 1, false, p);
       };
-      if (backward)
-        return aligned ? go(adapter_high_kernel<kTiles, kSteps, false, true>)
-                       : go(adapter_high_kernel<kTiles, kSteps, false, false>);
-      return aligned ? go(adapter_high_kernel<kTiles, kSteps, true, true>)
-                     : go(adapter_high_kernel<kTiles, kSteps, true, false>);
+      if (backward) {  // rows of A are aligned where rows of dx can be
+        return aligned && w_aligned ? go(adapter_high_kernel<kTiles, kSteps, kRowWarps, false, true, true>)
+                                    : go(adapter_high_kernel<kTiles, kSteps, kRowWarps, false, false, false>);
+      }
+      if (!w_aligned) return go(adapter_high_kernel<kTiles, kSteps, kRowWarps, true, false, false>);
+      return aligned ? go(adapter_high_kernel<kTiles, kSteps, kRowWarps, true, true, true>)
+                     : go(adapter_high_kernel<kTiles, kSteps, kRowWarps, true, false, true>);
     };
-    if constexpr (kSteps <= 4)
-      if (wide_tiles(a)) return run(Int<2>());
-    return run(Int<1>());
+    if (!wide_tiles(a)) return run(Int<1>(), Int<1>());
+    return run(Int<kSteps == 1 ? 2 : 1>(), Int<4>());
   });
 }
 
 int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev) {
   const int64_t cols = da ? a.k : a.n;
-  const int64_t slab = weight_slab(rank_tiles(a.rank)), slabs = (cols + slab - 1) / slab;
-  // Two CTAs an SM, tiles of kWeightRows rows, and the partials of 2 rows / tile
-  // slots in the workspace.
-  int64_t rows = (a.rows * slabs + 2 * dev.num_sms - 1) / (2 * dev.num_sms);
-  rows = (rows + kWeightRows - 1) / kWeightRows * kWeightRows;
+  int64_t slab = 0;
+  with_rank_tiles(a.rank, [&](auto ranks) {
+    slab = WeightShape<decltype(ranks)::value>::kSlab;
+    return cudaSuccess;
+  });
+  const int64_t slabs = (cols + slab - 1) / slab;
+  // Three CTAs an SM, tiles of 128 rows at least.
+  int64_t rows = (a.rows * slabs + 3 * dev.num_sms - 1) / (3 * dev.num_sms);
+  rows = (rows + 127) / 128 * 128;
+  // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
+  // them, and at most a.rows / rows and one for each adapter.
   const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));
-  if (slots < 4) return a.rows;  // no room: every adapter's rows in one tile
-  const int64_t least = (2 * a.rows + slots - 1) / slots;
-  if (rows < least) rows = (least + kWeightRows - 1) / kWeightRows * kWeightRows;
+  if (slots < 2) return a.rows;  // no room: every adapter's rows in one tile
+  int64_t least = (2 * a.rows + slots - 1) / slots;
+  if (slots > a.count) {
+    const int64_t other = (a.rows + slots - a.count - 1) / (slots - a.count);
+    if (other < least) least = other;
+  }
+  if (rows < least) rows = (least + 15) / 16 * 16;
   return rows < a.rows ? rows : a.rows;
 }
 
-cudaError_t launch_adapter_weight(const AdapterArgs& a, bool da, const uint16_t* x, int64_t ldx,
-                                  const float* low, int64_t tile_rows, uint16_t* dw, float* partials,
-                                  cudaStream_t stream) {
-  set_error_site("adapter_weight_kernel");
-  WeightArgs p = {};
-  p.x = x;
-  p.ldx = ldx;
-  p.low = low;
-  p.scale = da ? nullptr : a.scale;
-  p.dw = dw;
-  p.partials = partials;
-  p.cols = static_cast<int>(da ? a.k : a.n);
-  p.rank = a.rank;
-  p.tile_rows = static_cast<int>(tile_rows);
-  p.route = route_of(a);
-  // dA's rows are written as vectors.
-  const bool aligned = rows_aligned(x, ldx, p.cols) && (!da || aligned16(dw));
+size_t adapter_packed_bytes(const AdapterArgs& a) {
+  return static_cast<size_t>(most_tiles(a.rows, a.count, 16)) * rank_tiles(a.rank) * 32 * sizeof(uint4);
+}
+
+cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
+                                cudaStream_t stream) {
+  set_error_site("adapter_pack_kernel");
+  const int blocks = static_cast<int>(most_tiles(a.rows, a.count, 16));
+  const PackArgs pa = {da.low, nullptr, static_cast<uint4*>(da.packed)};
+  const PackArgs pb = {db.low, a.scale, static_cast<uint4*>(db.packed)};
+  const int both = da.packed != nullptr ? 2 : 1;
+  const dim3 grid(static_cast<unsigned>((both * int64_t(blocks) + kPackWarps - 1) / kPackWarps));
   return with_rank_tiles(a.rank, [&](auto ranks) {
-    constexpr int kRankTiles = decltype(ranks)::value;
-    constexpr int kSlab = weight_slab(kRankTiles);
-    const dim3 grid(static_cast<unsigned>(most_tiles(a.rows, a.count, tile_rows)),
-                    static_cast<unsigned>((p.cols + kSlab - 1) / kSlab));
-    auto go = [&](auto* kernel) {
-      return launch_kernel(kernel, grid, dim3(32 * kWeightWarps), 0, stream, 1, false, p);
-    };
-    if (da)
-      return aligned ? go(adapter_weight_kernel<kRankTiles, false, true>)
-                     : go(adapter_weight_kernel<kRankTiles, false, false>);
-    return aligned ? go(adapter_weight_kernel<kRankTiles, true, true>)
-                   : go(adapter_weight_kernel<kRankTiles, true, false>);
+    return launch_kernel(adapter_pack_kernel<decltype(ranks)::value>, grid, dim3(32 * kPackWarps), 0, stream,
+                         1, false, pb, pa, route_of(a), a.rank, blocks);
   });
 }
 
-cudaError_t launch_adapter_sum(const AdapterArgs& a, uint16_t* da, const float* da_partials,
-                               int64_t da_rows, uint16_t* db, const float* db_partials,
-                               int64_t db_rows, cudaStream_t stream) {
+cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
+                                  cudaStream_t stream) {
+  set_error_site("adapter_weight_kernel");
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    constexpr int kRankTiles = decltype(ranks)::value;
+    constexpr int kSlab = WeightShape<kRankTiles>::kSlab;
+    auto job = [&](const AdapterWeight& j, bool is_da) {
+      WeightArgs p = {};
+      if (j.dw == nullptr) return p;
+      p.x = j.x;
+      p.ldx = j.ldx;
+      p.low = j.low;
+      p.scale = is_da ? nullptr : a.scale;
+      p.dw = j.dw;
+      p.partials = j.partials;
+      p.cols = static_cast<int>(is_da ? a.k : a.n);
+      p.rank = a.rank;
+      p.tile_rows = static_cast<int>(j.tile_rows);
+      p.packed = static_cast<const uint4*>(j.packed);
+      p.tiles = static_cast<int>(most_tiles(a.rows, a.count, j.tile_rows));
+      p.slabs = (p.cols + kSlab - 1) / kSlab;
+      p.along = !is_da;
+      p.aligned = rows_aligned(j.x, j.ldx, p.cols);
+      p.dw_aligned = is_da && aligned16(j.dw) && p.cols % 8 == 0;
+      return p;
+    };
+    const WeightArgs b = job(db, false), c = job(da, true);
+    const dim3 grid(static_cast<unsigned>(int64_t(b.tiles) * b.slabs + int64_t(c.tiles) * c.slabs));
+    return launch_kernel(adapter_weight_kernel<kRankTiles>, grid, dim3(32 * kWeightWarps), 0, stream, 1,
+                         false, b, c, route_of(a));
+  });
+}
+
+cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
+                               cudaStream_t stream) {
   set_error_site("adapter_sum_kernel");
-  auto job = [&](uint16_t* dw, const float* partials, int64_t rows, int64_t cols) {
+  auto job = [&](const AdapterWeight& j, int64_t cols) {
     SumArgs s = {};
-    s.dw = dw;
-    s.partials = partials;
+    s.dw = j.dw;
+    s.partials = j.partials;
     s.size = cols * a.rank;
-    s.tile_rows = static_cast<int>(rows);
+    s.tile_rows = static_cast<int>(j.tile_rows);
     s.route = route_of(a);
     return s;
   };
-  const SumArgs sa = job(da, da_partials, da_rows, a.k), sb = job(db, db_partials, db_rows, a.n);
+  const SumArgs sa = job(da, a.k), sb = job(db, a.n);
   auto blocks = [&](const SumArgs& s) {
     if (s.dw == nullptr) return 0;
     const int64_t n = (s.size + kSumThreads - 1) / kSumThreads;

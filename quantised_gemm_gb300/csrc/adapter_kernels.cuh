@@ -74,6 +74,7 @@ struct RowTile {
   int begin;  // in rows[]
   int count;
   int slot;   // index among the tiles of groups with several
+  int block;  // index of its first 16 rows among the blocks of 16 of all groups
   bool only;  // the group's only tile
 };
 
@@ -81,7 +82,7 @@ struct RowTile {
 // has none).  All lanes of a warp call it and get the same.
 __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int size, int want) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
-  int before = 0, several_before = 0;
+  int before = 0, several_before = 0, blocks_before = 0;
   for (int base = 0; base < groups; base += 32) {
     const int g = base + lane;
     int begin = 0, count = 0;
@@ -90,14 +91,17 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
       count = __ldg(r.first + g + 1) - begin;
     }
     const int tiles = (count + size - 1) / size, several = tiles > 1 ? tiles : 0;
-    int up = tiles, several_up = several;
+    const int blocks = (count + 15) / 16;
+    int up = tiles, several_up = several, blocks_up = blocks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int a = __shfl_up_sync(0xFFFFFFFFu, up, o);
       const int b = __shfl_up_sync(0xFFFFFFFFu, several_up, o);
+      const int c = __shfl_up_sync(0xFFFFFFFFu, blocks_up, o);
       if (lane >= o) {
         up += a;
         several_up += b;
+        blocks_up += c;
       }
     }
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before + up > want);
@@ -108,22 +112,25 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
       t.group = base + at;
       t.only = __shfl_sync(0xFFFFFFFFu, tiles, at) == 1;
       t.slot = several_before + __shfl_sync(0xFFFFFFFFu, several_up - several, at) + inside;
+      t.block = blocks_before + __shfl_sync(0xFFFFFFFFu, blocks_up - blocks, at) + inside * (size / 16);
       t.begin = __shfl_sync(0xFFFFFFFFu, begin, at) + inside * size;
       t.count = min(size, __shfl_sync(0xFFFFFFFFu, count, at) - inside * size);
       return t;
     }
     before += __shfl_sync(0xFFFFFFFFu, up, 31);
     several_before += __shfl_sync(0xFFFFFFFFu, several_up, 31);
+    blocks_before += __shfl_sync(0xFFFFFFFFu, blocks_up, 31);
   }
-  return RowTile{-1, 0, 0, 0, false};
+  return RowTile{-1, 0, 0, 0, 0, false};
 }
 
 // ---------------------------------------------------------------- low = x W^T
 
 // low[i][j] = scale_a * sum_c x[i][c] w_a[j][c] for the rows i of one tile, 16 *
-// kTiles of them.  kAlong: w_a is [r, cols] (A: contiguous along the contraction);
-// else [cols, r] (B).  The CTA's warps take 32 columns each in turn, and so do
-// the CTAs of a cluster; their sums meet in shared memory.
+// kTiles of them for each of kRowWarps warps.  kAlong: w_a is [r, cols] (A:
+// contiguous along the contraction); else [cols, r] (B).  The other warps, and the
+// CTAs of a cluster, take other columns, 32 each in turn; their sums meet in
+// shared memory.  Warps of the same columns read w_a from L1 after the first.
 struct LowArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -133,7 +140,6 @@ struct LowArgs {
   int cols, rank;
   int parts;  // CTAs of a cluster
   Route route;
-  bool w_aligned;
 };
 
 constexpr int kLowWarps = 8;
@@ -141,34 +147,37 @@ constexpr int kLowWarps = 8;
 // Ranks a lane holds side by side of a [cols, r] weight.
 constexpr int ranks_a_lane(int rank_tiles) { return rank_tiles >= 4 ? 8 : 2 * rank_tiles; }
 
-template <int kTiles, int kRankTiles, bool kAlong, bool kAligned>
-__global__ void __launch_bounds__(32 * kLowWarps)
+template <int kTiles, int kRankTiles, int kRowWarps, bool kAlong, bool kAligned>
+__global__ void __launch_bounds__(32 * kLowWarps, kRankTiles <= 8 ? 2 : 1)
     adapter_low_kernel(const __grid_constant__ LowArgs p) {
-  __shared__ float sums[kLowWarps / 2][kTiles * kRankTiles * 4][32];
+  constexpr int kColWarps = kLowWarps / kRowWarps, kSums = kTiles * kRankTiles * 4;
+  constexpr int kRoom = kColWarps > 1 ? kLowWarps / 2 : kLowWarps;
+  __shared__ float sums[kRoom][kSums][32];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int row_warp = warp % kRowWarps, col_warp = warp / kRowWarps;
   const int g = lane >> 2, t = lane & 3;
   const int parts = p.parts, part = static_cast<int>(blockIdx.x) % parts;
-  const RowTile tile =
-      find_tile(p.route, p.route.groups, 16 * kTiles, static_cast<int>(blockIdx.x) / parts);
+  const RowTile tile = find_tile(p.route, p.route.groups, 16 * kTiles * kRowWarps,
+                                 static_cast<int>(blockIdx.x) / parts);
   if (tile.group < 0) return;  // all CTAs of the cluster
-  int64_t row[kTiles][2];
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = m * 16 + i * 8 + g;
-      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
-    }
-  const bool none = tile.group == p.route.groups - 1;
-  if (none) {
+  if (tile.group == p.route.groups - 1) {  // rows without an adapter
     if (part == 0)
       for (int at = warp; at < tile.count; at += kLowWarps)
         for (int j = lane; j < p.rank; j += 32)
           p.low[int64_t(__ldg(p.route.rows + tile.begin + at)) * p.rank + j] = 0.0f;
     return;
   }
+  int64_t row[kTiles][2];
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = (row_warp * kTiles + m) * 16 + i * 8 + g;
+      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
+    }
+  const bool idle = row_warp * kTiles * 16 >= tile.count;
   const uint16_t* const w = p.w + int64_t(tile.group) * p.rank * p.cols;
   float acc[kTiles][kRankTiles][4];
 #pragma unroll
@@ -178,132 +187,145 @@ __global__ void __launch_bounds__(32 * kLowWarps)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
   constexpr int kWide = ranks_a_lane(kRankTiles);
-  const int step = 32 * kLowWarps * parts;
-#pragma unroll 2
-  for (int c = 32 * (part * kLowWarps + warp); c < p.cols; c += step) {
+  const int step = 32 * kColWarps * parts;
+  // A lane's x and w of 32 columns.  w along the contraction: rank 8 j + g, the
+  // lane's eight columns; across it: row k of a product's tile is column
+  // 8 (k / 2) + 4 s + k % 2 of the 32, and two more in its second half (the order
+  // in which a lane holds x), and a lane has kWide ranks of it.
+  constexpr int kBlocks = (kRankTiles + 3) / 4;
+  constexpr int kLoads = kAlong ? kRankTiles : 4 * kBlocks;
+  auto load_x = [&](int c, uint4 (&x)[kTiles][2]) {
     const int col = c + 8 * t;
     const int n = kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
-    uint4 x[kTiles][2];
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        x[m][i] = row[m][i] >= 0 ? load_values<kAligned>(p.x + row[m][i] * p.ldx + col, n)
-                                 : make_uint4(0, 0, 0, 0);
+        x[m][i] = load_values<kAligned>(p.x + row[m][i] * p.ldx + col, row[m][i] >= 0 ? n : 0);
+  };
+  auto load_w = [&](int c, uint4 (&b)[kLoads]) {
     if constexpr (kAlong) {
+      const int col = c + 8 * t;
+      const int n = kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
 #pragma unroll
       for (int j = 0; j < kRankTiles; ++j) {
         const int rank = 8 * j + g;
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (rank < p.rank) {
-          const uint16_t* from = w + int64_t(rank) * p.cols + col;
-          b = p.w_aligned ? load_values<true>(from, n) : load_values<false>(from, n);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int m = 0; m < kTiles; ++m)
-            mma_bf16(acc[m][j], word(x[m][0], 2 * s), word(x[m][1], 2 * s), word(x[m][0], 2 * s + 1),
-                     word(x[m][1], 2 * s + 1), word(b, 2 * s), word(b, 2 * s + 1));
+        b[j] = load_values<kAligned>(w + int64_t(rank) * p.cols + col, rank < p.rank ? n : 0);
       }
     } else {
-      // Row k of a product's tile is column 8 (k / 2) + 4 s + k % 2 of the 32,
-      // and two more in its second half: the order in which a lane holds x.
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int block = 0; block < (kRankTiles + 3) / 4; ++block) {
-          uint4 b[2];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int from_col = c + 8 * (g >> 1) + 4 * s + 2 * half + (g & 1);
-            const int rank = 32 * block + kWide * t;
-            b[half] = make_uint4(0, 0, 0, 0);
-            if (from_col < p.cols && rank < p.rank) {
-              const uint16_t* from = w + int64_t(from_col) * p.rank + rank;
-              if (!p.w_aligned) {
-                b[half] = load_values<false>(from, min(kWide, p.rank - rank));
-              } else if constexpr (kWide == 8) {
-                b[half] = *reinterpret_cast<const uint4*>(from);
-              } else if constexpr (kWide == 4) {
-                const uint2 v = *reinterpret_cast<const uint2*>(from);
-                b[half] = make_uint4(v.x, v.y, 0, 0);
-              } else {
-                b[half].x = *reinterpret_cast<const uint32_t*>(from);
-              }
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < kWide / 2; ++q) {
-            const uint32_t b0 = turn_tile(word(b[0], q)), b1 = turn_tile(word(b[1], q));
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-              mma_bf16(acc[m][4 * block + q], word(x[m][0], 2 * s), word(x[m][1], 2 * s),
-                       word(x[m][0], 2 * s + 1), word(x[m][1], 2 * s + 1), b0, b1);
-          }
+      for (int i = 0; i < kLoads; ++i) {  // block, step, half
+        const int col = c + 8 * (g >> 1) + 2 * (i & 3) + (g & 1);
+        const int rank = 32 * (i >> 2) + kWide * t;
+        const bool on = col < p.cols && rank < p.rank;
+        const uint16_t* from = w + int64_t(col) * p.rank + rank;
+        if constexpr (!kAligned) {
+          b[i] = load_values<false>(from, on ? min(kWide, p.rank - rank) : 0);
+        } else if constexpr (kWide == 8) {
+          b[i] = load_if(from, on);
+        } else if constexpr (kWide == 4) {
+          const uint2 v = load2_if(from, on);
+          b[i] = make_uint4(v.x, v.y, 0, 0);
+        } else {
+          b[i] = make_uint4(load1_if(from, on), 0, 0, 0);
         }
       }
     }
-  }
-  // The warps' sums: the upper half's to shared memory, added by the lower.
+  };
+  auto add = [&](const uint4 (&x)[kTiles][2], const uint4 (&b)[kLoads]) {
 #pragma unroll
-  for (int half = kLowWarps / 2; half > 0; half >>= 1) {
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < kRankTiles; ++j) {
+        uint32_t b0, b1;
+        if constexpr (kAlong) {
+          b0 = word(b[j], 2 * s);
+          b1 = word(b[j], 2 * s + 1);
+        } else {
+          b0 = turn_tile(word(b[4 * (j >> 2) + 2 * s], j & 3));
+          b1 = turn_tile(word(b[4 * (j >> 2) + 2 * s + 1], j & 3));
+        }
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+          mma_bf16(acc[m][j], word(x[m][0], 2 * s), word(x[m][1], 2 * s), word(x[m][0], 2 * s + 1),
+                   word(x[m][1], 2 * s + 1), b0, b1);
+      }
+  };
+  // kAhead turns of x (and of w, where it is small) are on their way: 2 KB a turn
+  // of a warp, 16 warps an SM, and HBM takes a microsecond.
+  constexpr bool kRingW = kRankTiles <= 4;
+  constexpr int kAhead = kRankTiles <= 2 ? 3 : 2;
+  int c = idle ? p.cols : 32 * (part * kColWarps + col_warp);
+  uint4 x[kAhead][kTiles][2], b[kRingW ? kAhead : 1][kLoads];
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) {
+    load_x(c + d * step, x[d]);
+    if constexpr (kRingW) load_w(c + d * step, b[d]);
+  }
+  while (c < p.cols) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      if (c < p.cols) {
+        if constexpr (!kRingW) load_w(c, b[0]);
+        add(x[d], b[kRingW ? d : 0]);
+        load_x(c + kAhead * step, x[d]);
+        if constexpr (kRingW) load_w(c + kAhead * step, b[d]);
+        c += step;
+      }
+    }
+  }
+  float* const mine = &acc[0][0][0];
+  // Sums of the warps of the same rows: the upper half's to shared memory, added
+  // by the lower.
+#pragma unroll
+  for (int half = kLowWarps / 2; half >= kRowWarps; half >>= 1) {
     if (warp >= half && warp < 2 * half) {
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sums[warp - half][(m * kRankTiles + j) * 4 + i][lane] = acc[m][j][i];
+      for (int i = 0; i < kSums; ++i) sums[warp - half][i][lane] = mine[i];
     }
     __syncthreads();
     if (warp < half) {
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][j][i] += sums[warp][(m * kRankTiles + j) * 4 + i][lane];
+      for (int i = 0; i < kSums; ++i) mine[i] += sums[warp][i][lane];
     }
     __syncthreads();
   }
-  if (parts > 1) {  // the cluster's: every other CTA's from its shared memory, in order
-    if (warp == 0 && part != 0) {
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sums[0][(m * kRankTiles + j) * 4 + i][lane] = acc[m][j][i];
-    }
-    cluster_sync_all();
-    if (warp == 0 && part == 0) {
-      for (int from = 1; from < parts; ++from) {
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-          for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[m][j][i] += __uint_as_float(ld_shared_cluster_u32(
-                  map_to_cta(smem_addr(&sums[0][(m * kRankTiles + j) * 4 + i][lane]), from)));
-      }
-    }
-    cluster_sync_all();
-  }
-  if (warp != 0 || part != 0) return;
   const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
+  auto rank_of = [&](int j, int i, int t) {
+    return kAlong ? 8 * j + 2 * t + (i & 1) : 32 * (j >> 2) + kWide * t + 2 * (j & 3) + (i & 1);
+  };
+  if (parts == 1) {
+    if (warp >= kRowWarps) return;
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+    for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int j = 0; j < kRankTiles; ++j)
+      for (int j = 0; j < kRankTiles; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t to = row[m][i >> 1];
-        const int rank = kAlong ? 8 * j + 2 * t + (i & 1)
-                                : 32 * (j >> 2) + kWide * t + 2 * (j & 3) + (i & 1);
-        if (to >= 0 && rank < p.rank) p.low[to * p.rank + rank] = scale * acc[m][j][i];
-      }
+        for (int i = 0; i < 4; ++i) {
+          const int64_t to = row[m][i >> 1];
+          const int rank = rank_of(j, i, t);
+          if (to >= 0 && rank < p.rank) p.low[to * p.rank + rank] = scale * acc[m][j][i];
+        }
+    return;
+  }
+  // The cluster's sums: every CTA adds a part of the numbers, in the CTAs' order.
+  if (warp < kRowWarps) {
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) sums[warp][i][lane] = mine[i];
+  }
+  cluster_sync_all();
+  const int each = kRowWarps * kSums / parts;  // numbers of a lane; parts divides kRowWarps * kSums
+  for (int k = part * each + warp; k < (part + 1) * each; k += kLowWarps) {
+    const int of = k / kSums, m = k % kSums / (4 * kRankTiles), j = k / 4 % kRankTiles, i = k % 4;
+    const uint32_t at = smem_addr(&sums[of][k % kSums][lane]);
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int from = 0; from < parts; ++from) sum += __uint_as_float(ld_shared_cluster_u32(map_to_cta(at, from)));
+    const int which = (of * kTiles + m) * 16 + 8 * (i >> 1) + g, rank = rank_of(j, i, t);
+    if (which < tile.count && rank < p.rank)
+      p.low[int64_t(__ldg(p.route.rows + tile.begin + which)) * p.rank + rank] = scale * sum;
+  }
+  cluster_sync_all();
 }
 
 // ---------------------------------------------------------------- y = base + low W
@@ -325,7 +347,7 @@ struct HighArgs {
   int64_t ldbase, ldy;
   int cols, rank, slab;
   Route route;
-  bool w_aligned, low_aligned;
+  bool low_aligned;
 };
 
 constexpr int kHighWarps = 8;
@@ -346,28 +368,54 @@ __device__ __forceinline__ float4 load_ranks(const float* from, int n, bool alig
   return v;
 }
 
-template <int kTiles, int kSteps, bool kAlong, bool kAligned>
-__global__ void __launch_bounds__(32 * kHighWarps)
+template <int kTiles, int kSteps, int kRowWarps, bool kAlong, bool kAligned, bool kWAligned>
+__global__ void __launch_bounds__(32 * kHighWarps, kSteps <= 4 ? 2 : 1)
     adapter_high_kernel(const __grid_constant__ HighArgs p) {
+  constexpr int kColWarps = kHighWarps / kRowWarps;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int row_warp = warp % kRowWarps, col_warp = warp / kRowWarps;
   const int g = lane >> 2, t = lane & 3;
-  const RowTile tile = find_tile(p.route, p.route.groups, 16 * kTiles, static_cast<int>(blockIdx.x));
-  if (tile.group < 0) return;
+  const RowTile tile =
+      find_tile(p.route, p.route.groups, 16 * kTiles * kRowWarps, static_cast<int>(blockIdx.x));
+  if (tile.group < 0 || row_warp * kTiles * 16 >= tile.count) return;
   const bool none = tile.group == p.route.groups - 1;
   if (none && p.y == p.base) return;
   const int begin = static_cast<int>(blockIdx.y) * p.slab;
   const int end = min(begin + p.slab, p.cols);
   int64_t row[kTiles][2];
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = (row_warp * kTiles + m) * 16 + i * 8 + g;
+      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
+    }
+  // The base of a warp's next turns is on its way while it computes.
+  auto values = [&](int c) {
+    const int col = c + 8 * t;
+    return c >= end ? 0 : kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
+  };
+  constexpr int kAhead = 2, kTurn = 32 * kColWarps;
+  uint4 base[kAhead][kTiles][2];
+  auto fetch = [&](int c, uint4 (&into)[kTiles][2]) {
+    const int n = values(c);
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        into[m][i] = load_values<kAligned>(p.base + row[m][i] * p.ldbase + c + 8 * t,
+                                           p.base != nullptr && row[m][i] >= 0 ? n : 0);
+  };
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) fetch(begin + 32 * col_warp + d * kTurn, base[d]);
   LowFragments<kTiles, kSteps> f;
   const float scale = none || p.scale == nullptr ? 1.0f : __ldg(p.scale + tile.group);
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = m * 16 + i * 8 + g;
-      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int rank = rank_at<kSteps>(s, t);
@@ -377,19 +425,16 @@ __global__ void __launch_bounds__(32 * kHighWarps)
         split_pair(v.x * scale, v.y * scale, f.hi[m][s][i], f.lo[m][s][i]);
         split_pair(v.z * scale, v.w * scale, f.hi[m][s][i + 2], f.lo[m][s][i + 2]);
       }
-    }
   const uint16_t* const w = none ? nullptr : p.w + int64_t(tile.group) * p.rank * p.cols;
-  for (int c = begin + 32 * warp; c < end; c += 32 * kHighWarps) {
+  auto turn = [&](int c, uint4 (&next)[kTiles][2]) {
     const int col = c + 8 * t;
-    const int n = kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
-    uint4 base[kTiles][2];
+    const int n = values(c);
+    uint4 out[kTiles][2];
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        base[m][i] = p.base != nullptr && row[m][i] >= 0
-                         ? load_values<kAligned>(p.base + row[m][i] * p.ldbase + col, n)
-                         : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 2; ++i) out[m][i] = next[m][i];
+    fetch(c + kAhead * kTurn, next);
     if (!none) {
       float acc[kTiles][4][4];
 #pragma unroll
@@ -408,17 +453,16 @@ __global__ void __launch_bounds__(32 * kHighWarps)
             const int from_col = c + 8 * (g >> 1) + 2 * q + (g & 1);
             const int rank = rank_at<kSteps>(2 * block, t);
             constexpr int kWide = kSteps == 1 ? 4 : 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (from_col < p.cols && rank < p.rank) {
-              const uint16_t* from = w + int64_t(from_col) * p.rank + rank;
-              if (!p.w_aligned) {
-                v = load_values<false>(from, min(kWide, p.rank - rank));
-              } else if constexpr (kWide == 8) {
-                v = *reinterpret_cast<const uint4*>(from);
-              } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(from);
-                v = make_uint4(u.x, u.y, 0, 0);
-              }
+            const bool on = from_col < p.cols && rank < p.rank;
+            const uint16_t* from = w + int64_t(from_col) * p.rank + rank;
+            uint4 v;
+            if constexpr (!kWAligned) {
+              v = load_values<false>(from, on ? min(kWide, p.rank - rank) : 0);
+            } else if constexpr (kWide == 8) {
+              v = load_if(from, on);
+            } else {
+              const uint2 u = load2_if(from, on);
+              v = make_uint4(u.x, u.y, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[q][i] = word(v, i);
@@ -427,11 +471,7 @@ __global__ void __launch_bounds__(32 * kHighWarps)
 #pragma unroll
           for (int i = 0; i < (kSteps == 1 ? 2 : 4); ++i) {
             const int rank = rank_at<kSteps>(2 * block + (i >> 1), g >> 1) + 2 * (i & 1) + (g & 1);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (rank < p.rank) {
-              const uint16_t* from = w + int64_t(rank) * p.cols + col;
-              v = p.w_aligned ? load_values<true>(from, n) : load_values<false>(from, n);
-            }
+            const uint4 v = load_values<kWAligned>(w + int64_t(rank) * p.cols + col, rank < p.rank ? n : 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) b[q][i] = turn_tile(word(v, q));
           }
@@ -453,30 +493,36 @@ __global__ void __launch_bounds__(32 * kHighWarps)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float v[8];
-          bf16x8_to_f32(base[m][i], v);
+          bf16x8_to_f32(out[m][i], v);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             v[2 * q] += acc[m][q][2 * i];
             v[2 * q + 1] += acc[m][q][2 * i + 1];
           }
-          base[m][i] = f32_to_bf16x8(v);
+          out[m][i] = f32_to_bf16x8(v);
         }
     }
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        store_values<kAligned, 4>(p.y + (row[m][i] < 0 ? 0 : row[m][i]) * p.ldy + col, base[m][i],
+        store_values<kAligned, 4>(p.y + (row[m][i] < 0 ? 0 : row[m][i]) * p.ldy + col, out[m][i],
                                   row[m][i] < 0 ? 0 : n);
+  };
+  for (int c = begin + 32 * col_warp; c < end; c += kAhead * kTurn) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+      if (c + d * kTurn < end) turn(c + d * kTurn, base[d]);
   }
 }
 
 // ---------------------------------------------------------------- dW = x^T low
 
 // dw[c][j] = sum over the rows i of one adapter of x[i][c] scale_a low[i][j], for
-// `slab` columns c.  A tile of rows that is its adapter's only one is written as
-// bf16 into dw; else its sums go to the partials, one slot a tile, which
-// adapter_sum_kernel adds up.  kAlong: dw is [cols, r] (dB), else [r, cols] (dA).
+// a slab of columns c.  The CTA's warps take blocks of 16 rows in turn (kRowWarps
+// of them) and columns side by side (the others); a tile of rows that is its
+// adapter's only one is written as bf16 into dw, else its sums go to the
+// partials, one slot a tile, which adapter_sum_kernel adds up.
 struct WeightArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -484,95 +530,182 @@ struct WeightArgs {
   const float* scale;  // null: 1
   uint16_t* dw;
   float* partials;  // [slot][cols * rank]
-  int cols, rank, tile_rows;
-  Route route;
+  int cols, rank, tile_rows, tiles, slabs;
+  const uint4* packed;  // low as adapter_pack_kernel left it, or null
+  bool along;    // dw is [cols, r] (dB), else [r, cols] (dA)
+  bool aligned;  // x's rows
+  bool dw_aligned;
 };
 
 constexpr int kWeightWarps = 8;
-constexpr int kWeightRows = 64;  // rows of low in shared memory at a time
 
-// 16-column tiles of x that a warp holds sums for.
-constexpr int weight_tiles(int rank_tiles) { return rank_tiles >= 8 ? 2 : 4; }
-constexpr int weight_slab(int rank_tiles) { return kWeightWarps * 16 * weight_tiles(rank_tiles); }
+// With a small rank the rows' numbers are few beside x, and splitting the rows
+// leaves fewer partial sums; with a large one warps of the same rows share them.
+template <int kRankTiles>
+struct WeightShape {
+  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
+  static constexpr int kColWarps = kWeightWarps / kRowWarps;
+  static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
+  static constexpr int kSlab = 32 * kChunks * kColWarps;
+  static constexpr int kSums = 2 * kChunks * kRankTiles * 4;  // a lane's
+};
 
-template <int kRankTiles, bool kAlong, bool kAligned>
-__global__ void __launch_bounds__(32 * kWeightWarps)
-    adapter_weight_kernel(const __grid_constant__ WeightArgs p) {
-  constexpr int kTiles = weight_tiles(kRankTiles), kChunks = kTiles / 2;
-  constexpr int kRanks = 8 * kRankTiles;
-  // Rows 2 k and 2 k + 1 of low side by side: [hi, lo][k][rank]; the padding
-  // spreads the four k of a quarter-warp over the banks.
-  constexpr int kPitch = kRanks % 32 == 8 ? kRanks : (kRanks + 31) / 32 * 32 + 8;
-  __shared__ uint32_t low[2][kWeightRows / 2][kPitch];
+// What a lane needs of rank tile j of 16 rows of low: rows 2 t, 2 t + 1 and 2 t + 8,
+// 2 t + 9 of rank 8 j + g, as pairs hi (x, y) and lo (z, w).
+__device__ __forceinline__ uint4 low_operand(float a, float b, float c, float d) {
+  uint4 v;
+  split_pair(a, b, v.x, v.z);
+  split_pair(c, d, v.y, v.w);
+  return v;
+}
+
+// low of one or two calls to adapter_weight_kernel in that form, block by block of
+// 16 rows of an adapter: a warp a block.
+struct PackArgs {
+  const float* low;
+  const float* scale;
+  uint4* packed;
+};
+constexpr int kPackWarps = 4;
+
+template <int kRankTiles>
+__global__ void __launch_bounds__(32 * kPackWarps)
+    adapter_pack_kernel(const PackArgs a, const PackArgs b, const Route route, int rank, int blocks) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const int at = static_cast<int>(blockIdx.x) * kPackWarps + static_cast<int>(threadIdx.x >> 5);
   const int g = lane >> 2, t = lane & 3;
-  const RowTile tile = find_tile(p.route, p.route.groups - 1, p.tile_rows, static_cast<int>(blockIdx.x));
-  if (tile.group < 0) return;
-  const int col0 = (static_cast<int>(blockIdx.y) * kWeightWarps + warp) * 16 * kTiles;
+  const PackArgs& p = at < blocks ? a : b;
+  const RowTile tile = find_tile(route, route.groups - 1, 16, at < blocks ? at : at - blocks);
+  if (p.packed == nullptr || tile.group < 0) return;
   const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
-  float acc[kTiles][kRankTiles][4];
+  float v[kRankTiles][4];
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+  for (int e = 0; e < 4; ++e) {
+    const int of = 2 * t + (e & 1) + 8 * (e >> 1);
+    const float* from =
+        of < tile.count ? p.low + int64_t(__ldg(route.rows + tile.begin + of)) * rank : nullptr;
+#pragma unroll
+    for (int j = 0; j < kRankTiles; ++j)
+      v[j][e] = from != nullptr && 8 * j + g < rank ? scale * from[8 * j + g] : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < kRankTiles; ++j)
+    p.packed[(int64_t(tile.block) * kRankTiles + j) * 32 + lane] = low_operand(v[j][0], v[j][1], v[j][2], v[j][3]);
+}
+
+template <int kRankTiles, bool kAligned>
+__device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& route, int block,
+                                            float (*sums)[WeightShape<kRankTiles>::kSums][32]) {
+  using S = WeightShape<kRankTiles>;
+  constexpr int kChunks = S::kChunks, kSums = S::kSums;
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int col_warp = warp % S::kColWarps, row_warp = warp / S::kColWarps;
+  const int g = lane >> 2, t = lane & 3;
+  // The last rows first: they are what is left in L2 of the pass before.
+  const RowTile tile = find_tile(route, route.groups - 1, p.tile_rows, p.tiles - 1 - block / p.slabs);
+  if (tile.group < 0) return;
+  const int col0 = ((block % p.slabs) * S::kColWarps + col_warp) * 32 * kChunks;
+  const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
+  float acc[2 * kChunks][kRankTiles][4];
+#pragma unroll
+  for (int m = 0; m < 2 * kChunks; ++m)
 #pragma unroll
     for (int j = 0; j < kRankTiles; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-  for (int r0 = 0; r0 < tile.count; r0 += kWeightRows) {
-    const int rows = min(kWeightRows, tile.count - r0);
-    __syncthreads();
-    for (int i = static_cast<int>(threadIdx.x); i < kWeightRows / 2 * kRanks; i += 32 * kWeightWarps) {
-      const int k = i / kRanks, j = i % kRanks;
-      float v[2];
+  const int32_t* const rows = route.rows + tile.begin;
+  // x of the next blocks and the row numbers of one more are on their way.
+  constexpr int kStep = 16 * S::kRowWarps, kAhead = kRankTiles <= 8 ? 3 : 2;
+  int at[2];
+  uint4 ring[kAhead][kChunks][2];
+  auto find = [&](int r) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        v[e] = 0.0f;
-        if (2 * k + e < rows && j < p.rank)
-          v[e] = scale * p.low[int64_t(__ldg(p.route.rows + tile.begin + r0 + 2 * k + e)) * p.rank + j];
-      }
-      split_pair(v[0], v[1], low[0][k][j], low[1][k][j]);
+    for (int i = 0; i < 2; ++i) {
+      const int of = r + 8 * i + g;
+      at[i] = of < tile.count ? __ldg(rows + of) : -1;
     }
-    __syncthreads();
-    if (col0 >= p.cols) continue;
-    for (int r = 0; r < rows; r += 16) {
-      int64_t row[2];
+  };
+  auto fetch = [&](uint4 (&into)[kChunks][2]) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int at = r + i * 8 + g;
-        row[i] = at < rows ? __ldg(p.route.rows + tile.begin + r0 + at) : -1;
+        const int col = col0 + 32 * c + 8 * t;
+        const int n = at[i] < 0 ? 0 : values_at(col, p.cols);
+        into[c][i] = load_values<kAligned>(p.x + at[i] * p.ldx + col, n);
       }
-      uint4 x[kChunks][2];
+  };
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) {
+    find(16 * row_warp + d * kStep);
+    fetch(ring[d]);
+  }
+  find(16 * row_warp + kAhead * kStep);
+  auto turn = [&](int r, uint4 (&x)[kChunks][2]) {
+    uint4 low[kRankTiles];
+    if (p.packed != nullptr) {
+      const uint4* from = p.packed + (int64_t(tile.block + r / 16) * kRankTiles) * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < kRankTiles; ++j) low[j] = __ldg(from + 32 * j);
+    } else {
+      float v[kRankTiles][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int of = r + 2 * t + (e & 1) + 8 * (e >> 1);
+        const float* from = of < tile.count ? p.low + int64_t(__ldg(rows + of)) * p.rank : nullptr;
+#pragma unroll
+        for (int j = 0; j < kRankTiles; ++j)
+          v[j][e] = from != nullptr && 8 * j + g < p.rank ? scale * __ldg(from + 8 * j + g) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kRankTiles; ++j) low[j] = low_operand(v[j][0], v[j][1], v[j][2], v[j][3]);
+    }
+    uint32_t a[kChunks][4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[c][q][i] = turn_tile(word(x[c][i], q));
+    fetch(x);
+    find(r + (kAhead + 1) * kStep);
+#pragma unroll
+    for (int j = 0; j < kRankTiles; ++j) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = col0 + 32 * c + 8 * t;
-          const int n = kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
-          x[c][i] = row[i] >= 0 ? load_values<kAligned>(p.x + row[i] * p.ldx + col, n)
-                                : make_uint4(0, 0, 0, 0);
+        for (int m = 0; m < 2; ++m) {
+          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
+                   a[c][2 * m + 1][1], low[j].z, low[j].w);
+          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
+                   a[c][2 * m + 1][1], low[j].x, low[j].y);
         }
+    }
+  };
+  for (int r = 16 * row_warp; r < tile.count; r += kAhead * kStep) {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        uint32_t a[4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
+    for (int d = 0; d < kAhead; ++d)
+      if (r + d * kStep < tile.count) turn(r + d * kStep, ring[d]);
+  }
+  if constexpr (S::kRowWarps > 1) {
+    float* const mine = &acc[0][0][0];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+    for (int half = kWeightWarps / 2; half >= S::kColWarps; half >>= 1) {
+      if (warp >= half && warp < 2 * half) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) a[q][i] = turn_tile(word(x[c][i], q));
-#pragma unroll
-        for (int j = 0; j < kRankTiles; ++j) {
-#pragma unroll
-          for (int part = 1; part >= 0; --part) {
-            const uint32_t b0 = low[part][r / 2 + t][8 * j + g], b1 = low[part][r / 2 + 4 + t][8 * j + g];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-              mma_bf16(acc[2 * c + m][j], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], b0, b1);
-          }
-        }
+        for (int i = 0; i < kSums; ++i) sums[warp - half][i][lane] = mine[i];
       }
+      __syncthreads();
+      if (warp < half) {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) mine[i] += sums[warp][i][lane];
+      }
+      __syncthreads();
     }
   }
-  if (col0 >= p.cols) return;
+  if (row_warp != 0 || col0 >= p.cols) return;
   const int64_t size = int64_t(p.cols) * p.rank;
   uint16_t* const dw = p.dw + tile.group * size;
   float* const part = tile.only ? nullptr : p.partials + tile.slot * size;
@@ -582,7 +715,7 @@ __global__ void __launch_bounds__(32 * kWeightWarps)
   for (int c = 0; c < kChunks; ++c)
 #pragma unroll
     for (int j = 0; j < kRankTiles; ++j) {
-      if constexpr (kAlong) {
+      if (p.along) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int col = col0 + 32 * c + 8 * (g >> 1) + 2 * q + (g & 1);
@@ -591,48 +724,65 @@ __global__ void __launch_bounds__(32 * kWeightWarps)
             const int rank = 8 * j + 2 * t + e;
             if (col >= p.cols || rank >= p.rank) continue;
             const float v = acc[2 * c + (q >> 1)][j][2 * (q & 1) + e];
-            const int64_t at = int64_t(col) * p.rank + rank;
+            const int64_t to = int64_t(col) * p.rank + rank;
             if (part != nullptr)
-              part[at] = v;
+              part[to] = v;
             else
-              dw[at] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+              dw[to] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
           }
         }
-      } else {
-        // Lanes of neighbouring g swap, so that one has eight columns side by
-        // side of the first rank and the other of the second.
-        float v[8];
-        const int e = g & 1;
+        continue;
+      }
+      // Lanes of neighbouring g swap, so that one has eight columns side by side
+      // of the first rank and the other of the second.
+      float v[8];
+      const int e = g & 1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float* a = acc[2 * c + (q >> 1)][j] + 2 * (q & 1);
-          const float got = __shfl_xor_sync(0xFFFFFFFFu, e ? a[0] : a[1], 4);
-          v[2 * q] = e ? got : a[0];
-          v[2 * q + 1] = e ? a[1] : got;
+      for (int q = 0; q < 4; ++q) {
+        const float* a = acc[2 * c + (q >> 1)][j] + 2 * (q & 1);
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, e ? a[0] : a[1], 4);
+        v[2 * q] = e ? got : a[0];
+        v[2 * q + 1] = e ? a[1] : got;
+      }
+      const int col = col0 + 32 * c + 8 * (g >> 1), rank = 8 * j + 2 * t + e;
+      const int64_t to = int64_t(rank) * p.cols + col;
+      if (rank < p.rank && p.dw_aligned && col < p.cols) {
+        if (part != nullptr) {
+          float4* put = reinterpret_cast<float4*>(part + to);
+          put[0] = make_float4(v[0], v[1], v[2], v[3]);
+          put[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4*>(dw + to) = f32_to_bf16x8(v);
         }
-        const int col = col0 + 32 * c + 8 * (g >> 1), rank = 8 * j + 2 * t + e;
-        if (rank >= p.rank) continue;
-        const int64_t at = int64_t(rank) * p.cols + col;
-        if (kAligned && col < p.cols) {
-          if (part != nullptr) {
-            float4* to = reinterpret_cast<float4*>(part + at);
-            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-            to[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            *reinterpret_cast<uint4*>(dw + at) = f32_to_bf16x8(v);
-          }
-          continue;
-        }
+      } else if (rank < p.rank) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (col + i >= p.cols) continue;
           if (part != nullptr)
-            part[at + i] = v[i];
+            part[to + i] = v[i];
           else
-            dw[at + i] = static_cast<uint16_t>(cvt_bf16x2(v[i], 0.0f) & 0xFFFFu);
+            dw[to + i] = static_cast<uint16_t>(cvt_bf16x2(v[i], 0.0f) & 0xFFFFu);
         }
       }
     }
+}
+
+// dB (blocks from 0 on) and dA (the others) in one launch; either may have none.
+template <int kRankTiles>
+__global__ void __launch_bounds__(32 * kWeightWarps, kRankTiles <= 2 ? 2 : 1)
+    adapter_weight_kernel(const __grid_constant__ WeightArgs db, const __grid_constant__ WeightArgs da,
+                          const Route route) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int block = static_cast<int>(blockIdx.x), first = db.tiles * db.slabs;
+  const bool is_db = block < first;
+  using S = WeightShape<kRankTiles>;
+  __shared__ float sums[S::kRowWarps > 1 ? kWeightWarps / 2 : 1][S::kSums][32];
+  const WeightArgs& p = is_db ? db : da;
+  if (p.aligned)
+    weight_tile<kRankTiles, true>(p, route, is_db ? block : block - first, sums);
+  else
+    weight_tile<kRankTiles, false>(p, route, is_db ? block : block - first, sums);
 }
 
 // The partials of adapters with several tiles, added in order, and zeros for

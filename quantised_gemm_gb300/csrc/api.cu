@@ -1880,40 +1880,59 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     e = launch_adapter_low(a, true, dys, lddy, dh, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
+  // The weight gradients' operands from h and dh, laid out once where they leave
+  // three quarters of the room for the partial sums.
+  AdapterWeight wa, wb;
+  const size_t packed = adapter_packed_bytes(a);
+  if ((da != nullptr || db != nullptr) && 8 * packed <= room_bytes) {
+    for (AdapterWeight* w : {&wa, &wb}) {
+      if ((w == &wa ? da : db) == nullptr) continue;
+      w->packed = room;
+      room += packed;
+      room_bytes -= packed;
+    }
+  }
   // The room for partial sums: shared as the sizes of dA and dB are.
   const size_t for_da = da == nullptr ? 0
                         : db == nullptr
                             ? room_bytes
                             : static_cast<size_t>(static_cast<double>(room_bytes) * ad->k / (ad->k + ad->n)) / 256 * 256;
-  float* const da_part = reinterpret_cast<float*>(room);
-  float* const db_part = reinterpret_cast<float*>(room + for_da);
-  int64_t da_rows = 1, db_rows = 1;
-  if (db != nullptr) {
-    db_rows = adapter_weight_rows(a, false, room_bytes - for_da, dev);
-    ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_weight(a, false, dys, lddy, h, db_rows, static_cast<uint16_t*>(db), db_part, stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  if (da != nullptr) {
-    da_rows = adapter_weight_rows(a, true, for_da, dev);
-    ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_weight(a, true, static_cast<const uint16_t*>(x), ldx, dh, da_rows,
-                              static_cast<uint16_t*>(da), da_part, stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
   if (dx != nullptr) {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
     e = launch_adapter_high(a, true, dh, static_cast<const uint16_t*>(base), ldbase,
                             static_cast<uint16_t*>(dx), lddx, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  if (da != nullptr || db != nullptr) {
+  if (da == nullptr && db == nullptr) return FP8LIN_OK;
+  if (da != nullptr) {
+    wa.dw = static_cast<uint16_t*>(da);
+    wa.x = static_cast<const uint16_t*>(x);
+    wa.ldx = ldx;
+    wa.low = dh;
+    wa.tile_rows = adapter_weight_rows(a, true, for_da, dev);
+    wa.partials = reinterpret_cast<float*>(room);
+  }
+  if (db != nullptr) {
+    wb.dw = static_cast<uint16_t*>(db);
+    wb.x = dys;
+    wb.ldx = lddy;
+    wb.low = h;
+    wb.tile_rows = adapter_weight_rows(a, false, room_bytes - for_da, dev);
+    wb.partials = reinterpret_cast<float*>(room + for_da);
+  }
+  if (wa.packed != nullptr || wb.packed != nullptr) {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_sum(a, static_cast<uint16_t*>(da), da_part, da_rows, static_cast<uint16_t*>(db),
-                           db_part, db_rows, stream);
+    e = launch_adapter_pack(a, wb, wa, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  return FP8LIN_OK;
+  {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_weight(a, wb, wa, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  ProfScope ps(FP8LIN_PROF_GEMM, stream);
+  e = launch_adapter_sum(a, wb, wa, stream);
+  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 
 uint64_t fp8lin_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

@@ -62,18 +62,53 @@ __device__ __forceinline__ int values_at(int c, int cols) {
   return min(max(cols - c, 0), 8);
 }
 
+// The 16 bytes at p, or zeros, without a branch: loads in branches wait for one
+// another at the join.
+__device__ __forceinline__ uint4 load_if(const void* p, bool on) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<int>(on)));
+  return v;
+}
+
+__device__ __forceinline__ uint2 load2_if(const void* p, bool on) {
+  uint2 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y)
+      : "l"(p), "r"(static_cast<int>(on)));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t load1_if(const void* p, bool on) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "@p ld.global.b32 %0, [%1];\n\t}"
+      : "=&r"(v)
+      : "l"(p), "r"(static_cast<int>(on)));
+  return v;
+}
+
 // The n values at p, the others 0.  kAligned: p is 16-byte aligned and n 0 or 8.
 template <bool kAligned>
 __device__ __forceinline__ uint4 load_values(const uint16_t* p, int n) {
-  if (n == 0) return make_uint4(0, 0, 0, 0);
   if constexpr (kAligned) {
-    return *reinterpret_cast<const uint4*>(p);
+    return load_if(p, n > 0);
   } else {
     const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
     const uint4* v = reinterpret_cast<const uint4*>(p - off);
-    const uint4 lo = v[0];
-    uint4 hi = make_uint4(0, 0, 0, 0);
-    if (static_cast<int>(off) + n > 8) hi = v[1];
+    const uint4 lo = load_if(v, n > 0), hi = load_if(v + 1, n > 0 && static_cast<int>(off) + n > 8);
     return first_values(shift_values(lo, hi, off), n);
   }
 }
