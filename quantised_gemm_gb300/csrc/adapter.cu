@@ -1,5 +1,5 @@
-// adapter.cu -- the low-rank adapters' launchers, the sorting of rows by adapter
-// and the one-launch forward of a few rows.
+// adapter.cu -- the low-rank adapters' rows sorted by adapter, and the one-launch
+// forward of a few rows.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -215,62 +215,6 @@ __global__ void __launch_bounds__(32 * kFewWarps) adapter_few_kernel(const __gri
   }
 }
 
-__global__ void __launch_bounds__(kSumThreads) adapter_sum_kernel(const __grid_constant__ SumArgs a,
-                                                                  const __grid_constant__ SumArgs b,
-                                                                  int blocks_a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int block = static_cast<int>(blockIdx.x), group = static_cast<int>(blockIdx.y);
-  if (block < blocks_a)
-    sum_partials(a, group, block, blocks_a);
-  else
-    sum_partials(b, group, block - blocks_a, static_cast<int>(gridDim.x) - blocks_a);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool rows_aligned(const void* p, int64_t ld, int64_t cols) {
-  return p == nullptr || (aligned16(p) && ld % 8 == 0 && cols % 8 == 0);
-}
-
-// 1, 2, 4, 8 or 16 tiles of eight ranks.
-int rank_tiles(int rank) {
-  int t = 1;
-  while (8 * t < rank) t *= 2;
-  return t;
-}
-
-template <int kValue>
-using Int = std::integral_constant<int, kValue>;
-
-template <typename Run>
-cudaError_t with_rank_tiles(int rank, Run run) {
-  switch (rank_tiles(rank)) {
-    case 1: return run(Int<1>());
-    case 2: return run(Int<2>());
-    case 4: return run(Int<4>());
-    case 8: return run(Int<8>());
-    default: return run(Int<16>());
-  }
-}
-
-// Tiles of `size` rows, at most: each adapter with rows may end inside one.
-int64_t most_tiles(int64_t rows, int64_t groups, int64_t size) {
-  const int64_t t = rows / size + groups;
-  return t < rows ? t : rows;
-}
-
-// Whether an adapter has rows for tiles of several warps, on average.
-bool wide_tiles(const AdapterArgs& a) { return a.rows >= 64 * a.count; }
-
-Route route_of(const AdapterArgs& a) {
-  return Route{a.route, a.route + a.count + 2, static_cast<int>(a.count) + 1};
-}
-
-// B's rows of `rank` values, as the kernels load them.
-bool b_aligned(const AdapterArgs& a) { return aligned16(a.b) && a.rank % (a.rank <= 16 ? 4 : 8) == 0; }
-bool a_aligned(const AdapterArgs& a) { return aligned16(a.a) && a.k % 8 == 0; }
-
 }  // namespace
 
 cudaError_t launch_adapter_route(const int32_t* index, int64_t rows, int64_t count, int32_t* route,
@@ -323,189 +267,6 @@ cudaError_t launch_adapter_few(const AdapterArgs& a, const int32_t* index, const
     return aligned ? launch_kernel(adapter_few_kernel<kLanes, true>, grid, block, 0, stream, kFewCluster, false, p)
                    : launch_kernel(adapter_few_kernel<kLanes, false>, grid, block, 0, stream, kFewCluster, false, p);
   });
-}
-
-cudaError_t launch_adapter_low(const AdapterArgs& a, bool backward, const uint16_t* x, int64_t ldx,
-                               float* low, const DeviceInfo& dev, cudaStream_t stream) {
-  set_error_site("adapter_low_kernel");
-  LowArgs p = {};
-  p.x = x;
-  p.ldx = ldx;
-  p.w = backward ? a.b : a.a;
-  p.scale = backward ? a.scale : nullptr;
-  p.low = low;
-  p.cols = static_cast<int>(backward ? a.n : a.k);
-  p.rank = a.rank;
-  p.route = route_of(a);
-  const bool aligned = rows_aligned(x, ldx, p.cols) && (backward ? b_aligned(a) : a_aligned(a));
-  return with_rank_tiles(a.rank, [&](auto ranks) {
-    constexpr int kRankTiles = decltype(ranks)::value;
-    auto run = [&](auto tiles, auto row_warps) {
-      constexpr int kTiles = decltype(tiles)::value, kRowWarps = decltype(row_warps)::value;
-      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles * kRowWarps);
-      // One wave of two CTAs an SM, as far as the rows have tiles (a CTA spends 8 us
-      // on finding its rows and on the sums), and 32 columns a warp at least.
-      constexpr int kTurn = 32 * kLowWarps / kRowWarps;
-      p.parts = 1;
-      while (p.parts < 8 && most * p.parts * 2 <= 2 * dev.num_sms && kTurn * 2 * p.parts <= p.cols) p.parts *= 2;
-      const dim3 grid(static_cast<unsigned>(most * p.parts)), block(32 * kLowWarps);
-      auto go = [&](auto* kernel) {
-        return launch_kernel(kernel, grid, block, 0, stream, p.parts, false, p);
-      };
-      if (backward)
-        return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, false, true>)
-                       : go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, false, false>);
-      return aligned ? go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, true, true>)
-                     : go(adapter_low_kernel<kTiles, kRankTiles, kRowWarps, true, false>);
-    };
-    if (!wide_tiles(a)) return run(Int<1>(), Int<1>());
-    return run(Int<kRankTiles <= 4 ? 2 : 1>(), Int<kRankTiles <= 4 ? 2 : 4>());
-  });
-}
-
-cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
-                                const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
-                                const DeviceInfo& dev, cudaStream_t stream) {
-  set_error_site("adapter_high_kernel");
-  HighArgs p = {};
-  p.low = low;
-  p.w = backward ? a.a : a.b;
-  p.scale = backward ? nullptr : a.scale;
-  p.base = base;
-  p.y = y;
-  p.ldbase = ldbase;
-  p.ldy = ldy;
-  p.cols = static_cast<int>(backward ? a.k : a.n);
-  p.rank = a.rank;
-  p.route = route_of(a);
-  const bool w_aligned = backward ? a_aligned(a) : b_aligned(a);
-  p.low_aligned = aligned16(low) && a.rank % 4 == 0;
-  const bool aligned = rows_aligned(base, ldbase, p.cols) && rows_aligned(y, ldy, p.cols);
-  return with_rank_tiles(a.rank, [&](auto ranks) {
-    constexpr int kSteps = decltype(ranks)::value <= 2 ? 1 : decltype(ranks)::value / 2;
-    auto run = [&](auto tiles, auto row_warps) {
-      constexpr int kTiles = decltype(tiles)::value, kRowWarps = decltype(row_warps)::value;
-      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles * kRowWarps);
-      // Slabs of whole rounds of the warps, and some CTAs an SM.
-      constexpr int kRound = 32 * kHighWarps / kRowWarps;
-      const int rounds = (p.cols + kRound - 1) / kRound;
-      int64_t slabs = (8 * int64_t(dev.num_sms) + most - 1) / most;
-      if (slabs > rounds) slabs = rounds;
-      const int per = static_cast<int>((rounds + slabs - 1) / slabs);
-      p.slab = per * kRound;
-      const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>((rounds + per - 1) / per));
-      auto go = [&](auto* kernel) {
-        return launch_kernel(kernel, grid, dim3(32 * kHighWarps), 0, stream, 1, false, p);
-      };
-      if (backward) {  // rows of A are aligned where rows of dx can be
-        return aligned && w_aligned ? go(adapter_high_kernel<kTiles, kSteps, kRowWarps, false, true, true>)
-                                    : go(adapter_high_kernel<kTiles, kSteps, kRowWarps, false, false, false>);
-      }
-      if (!w_aligned) return go(adapter_high_kernel<kTiles, kSteps, kRowWarps, true, false, false>);
-      return aligned ? go(adapter_high_kernel<kTiles, kSteps, kRowWarps, true, true, true>)
-                     : go(adapter_high_kernel<kTiles, kSteps, kRowWarps, true, false, true>);
-    };
-    if (!wide_tiles(a)) return run(Int<1>(), Int<1>());
-    return run(Int<kSteps == 1 ? 2 : 1>(), Int<4>());
-  });
-}
-
-int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev) {
-  const int64_t cols = da ? a.k : a.n;
-  int64_t slab = 0;
-  with_rank_tiles(a.rank, [&](auto ranks) {
-    slab = WeightShape<decltype(ranks)::value>::kSlab;
-    return cudaSuccess;
-  });
-  const int64_t slabs = (cols + slab - 1) / slab;
-  // Three CTAs an SM, tiles of 128 rows at least.
-  int64_t rows = (a.rows * slabs + 3 * dev.num_sms - 1) / (3 * dev.num_sms);
-  rows = (rows + 127) / 128 * 128;
-  // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
-  // them, and at most a.rows / rows and one for each adapter.
-  const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));
-  if (slots < 2) return a.rows;  // no room: every adapter's rows in one tile
-  int64_t least = (2 * a.rows + slots - 1) / slots;
-  if (slots > a.count) {
-    const int64_t other = (a.rows + slots - a.count - 1) / (slots - a.count);
-    if (other < least) least = other;
-  }
-  if (rows < least) rows = (least + 15) / 16 * 16;
-  return rows < a.rows ? rows : a.rows;
-}
-
-size_t adapter_packed_bytes(const AdapterArgs& a) {
-  return static_cast<size_t>(most_tiles(a.rows, a.count, 16)) * rank_tiles(a.rank) * 32 * sizeof(uint4);
-}
-
-cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                cudaStream_t stream) {
-  set_error_site("adapter_pack_kernel");
-  const int blocks = static_cast<int>(most_tiles(a.rows, a.count, 16));
-  const PackArgs pa = {da.low, nullptr, static_cast<uint4*>(da.packed)};
-  const PackArgs pb = {db.low, a.scale, static_cast<uint4*>(db.packed)};
-  const int both = da.packed != nullptr ? 2 : 1;
-  const dim3 grid(static_cast<unsigned>((both * int64_t(blocks) + kPackWarps - 1) / kPackWarps));
-  return with_rank_tiles(a.rank, [&](auto ranks) {
-    return launch_kernel(adapter_pack_kernel<decltype(ranks)::value>, grid, dim3(32 * kPackWarps), 0, stream,
-                         1, false, pb, pa, route_of(a), a.rank, blocks);
-  });
-}
-
-cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                  cudaStream_t stream) {
-  set_error_site("adapter_weight_kernel");
-  return with_rank_tiles(a.rank, [&](auto ranks) {
-    constexpr int kRankTiles = decltype(ranks)::value;
-    constexpr int kSlab = WeightShape<kRankTiles>::kSlab;
-    auto job = [&](const AdapterWeight& j, bool is_da) {
-      WeightArgs p = {};
-      if (j.dw == nullptr) return p;
-      p.x = j.x;
-      p.ldx = j.ldx;
-      p.low = j.low;
-      p.scale = is_da ? nullptr : a.scale;
-      p.dw = j.dw;
-      p.partials = j.partials;
-      p.cols = static_cast<int>(is_da ? a.k : a.n);
-      p.rank = a.rank;
-      p.tile_rows = static_cast<int>(j.tile_rows);
-      p.packed = static_cast<const uint4*>(j.packed);
-      p.tiles = static_cast<int>(most_tiles(a.rows, a.count, j.tile_rows));
-      p.slabs = (p.cols + kSlab - 1) / kSlab;
-      p.along = !is_da;
-      p.aligned = rows_aligned(j.x, j.ldx, p.cols);
-      p.dw_aligned = is_da && aligned16(j.dw) && p.cols % 8 == 0;
-      return p;
-    };
-    const WeightArgs b = job(db, false), c = job(da, true);
-    const dim3 grid(static_cast<unsigned>(int64_t(b.tiles) * b.slabs + int64_t(c.tiles) * c.slabs));
-    return launch_kernel(adapter_weight_kernel<kRankTiles>, grid, dim3(32 * kWeightWarps), 0, stream, 1,
-                         false, b, c, route_of(a));
-  });
-}
-
-cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                               cudaStream_t stream) {
-  set_error_site("adapter_sum_kernel");
-  auto job = [&](const AdapterWeight& j, int64_t cols) {
-    SumArgs s = {};
-    s.dw = j.dw;
-    s.partials = j.partials;
-    s.size = cols * a.rank;
-    s.tile_rows = static_cast<int>(j.tile_rows);
-    s.route = route_of(a);
-    return s;
-  };
-  const SumArgs sa = job(da, a.k), sb = job(db, a.n);
-  auto blocks = [&](const SumArgs& s) {
-    if (s.dw == nullptr) return 0;
-    const int64_t n = (s.size + kSumThreads - 1) / kSumThreads;
-    return static_cast<int>(n < 1024 ? n : 1024);
-  };
-  const int na = blocks(sa), nb = blocks(sb);
-  return launch_kernel(adapter_sum_kernel, dim3(static_cast<unsigned>(na + nb), static_cast<unsigned>(a.count)),
-                       dim3(kSumThreads), 0, stream, 1, false, sa, sb, na);
 }
 
 }  // namespace fp8lin

@@ -1,0 +1,224 @@
+// adapter_high.cu -- the adapters' product over the ranks, added to a base:
+//   y[i][c] = base[i][c] + sum_j s_a low[i][j] w_a(j, c)
+// y = base + s h B^T in the forward, dx = base + dh A in the backward.
+#include "adapter_kernels.cuh"
+
+#ifndef HIGH_CTAS
+#define HIGH_CTAS 4
+#endif
+namespace fp8lin {
+namespace {
+
+struct HighArgs {
+  const float* low;
+  const uint16_t* w;
+  const float* scale;    // null: 1
+  const uint16_t* base;  // null: 0
+  uint16_t* y;
+  int64_t ldbase, ldy;
+  int cols, rank, slab;
+  Route route;
+  bool low_aligned;
+};
+
+// A tile of 16 * kTiles rows for each of kRowWarps warps, and `slab` columns, of
+// which every other warp takes 32 a turn.  kSteps products of 16 ranks, each for
+// hi and lo.  kAlong: w_a is [cols, r] (B), else [r, cols] (A).
+template <int kTiles, int kSteps, int kRowWarps, bool kAligned>
+struct HighShape {
+  static constexpr int kColWarps = kAdapterWarps / kRowWarps;
+  static constexpr int kShared = kColWarps * 2 * kSteps * 32;
+  static constexpr size_t kStage = sizeof(uint4) * (2 * kTiles * kAdapterThreads + kShared);
+  using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAligned>;
+};
+
+__device__ __forceinline__ float2 load_ranks(const float* from, int n, bool aligned) {
+  if (aligned && n >= 2) return *reinterpret_cast<const float2*>(from);
+  float2 v = make_float2(0.0f, 0.0f);
+  if (n > 0) v.x = from[0];
+  if (n > 1) v.y = from[1];
+  return v;
+}
+
+template <int kTiles, int kSteps, int kRowWarps, bool kAlong, bool kAligned, bool kWAligned>
+__global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
+    adapter_high_kernel(const __grid_constant__ HighArgs p) {
+  using Shape = HighShape<kTiles, kSteps, kRowWarps, kAligned>;
+  using S = typename Shape::S;
+  constexpr int kColWarps = Shape::kColWarps, kRankTiles = 2 * kSteps, kTurn = 32 * kColWarps;
+  extern __shared__ uint4 shared[];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int row_warp = warp % kRowWarps, col_warp = warp / kRowWarps;
+  const int g = lane >> 2, t = lane & 3;
+  const RowTile tile =
+      find_tile(p.route, p.route.groups, 16 * kTiles * kRowWarps, static_cast<int>(blockIdx.x));
+  if (tile.group < 0) return;
+  const bool none = tile.group == p.route.groups - 1;
+  if (none && p.y == p.base) return;
+  const int begin = static_cast<int>(blockIdx.y) * p.slab;
+  const int end = min(begin + p.slab, p.cols);
+  const int turns = (end - begin + kTurn - 1) / kTurn;
+  int64_t row[kTiles][2];
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = (row_warp * kTiles + m) * 16 + i * 8 + g;
+      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
+    }
+  const bool idle = row_warp * kTiles * 16 >= tile.count;
+  const uint16_t* const w = none ? nullptr : p.w + int64_t(tile.group) * p.rank * p.cols;
+  S stages(shared);
+  auto copy_base = [&](int turn) {
+    const int c = begin + turn * kTurn + 32 * col_warp + 8 * t;
+    stages.copy(turn, [&](int v, int& n) {
+      const int64_t of = row[v >> 1][v & 1];
+      n = p.base == nullptr || of < 0 || turn >= turns ? 0 : values_at(c, p.cols);
+      return p.base + (of < 0 ? 0 : of) * p.ldbase + c;
+    });
+  };
+  auto copy_w = [&](int turn) {
+    const int c = begin + turn * kTurn;
+    if (turn < turns && !none) {
+      if constexpr (kAlong)
+        stage_columns<kRankTiles, kColWarps, kWAligned>(stages.shared_of(turn), w, c, p.cols, p.rank);
+      else
+        stage_ranks<kRankTiles, kColWarps, kWAligned>(stages.shared_of(turn), w, c, p.cols, p.rank);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < S::kCount - 1; ++i) {
+    copy_w(i);
+    if (kAligned || i == 0) copy_base(i);
+    copies_end();
+  }
+  uint32_t hi[kTiles][kSteps][4], lo[kTiles][kSteps][4];  // low of the rows, as an operand
+  const float scale = none || p.scale == nullptr ? 1.0f : __ldg(p.scale + tile.group);
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int rank = 16 * s + 8 * (i >> 1) + 2 * t;
+        float2 v = make_float2(0.0f, 0.0f);
+        if (row[m][i & 1] >= 0 && !none)
+          v = load_ranks(p.low + row[m][i & 1] * p.rank + rank, p.rank - rank, p.low_aligned);
+        split_pair(v.x * scale, v.y * scale, hi[m][s][i], lo[m][s][i]);
+      }
+  for (int turn = 0; turn < turns; ++turn) {
+    stages.wait();
+    uint4 out[2 * kTiles];
+    stages.take(turn, out);
+    copy_w(turn + S::kCount - 1);
+    copy_base(kAligned ? turn + S::kCount - 1 : turn + 1);
+    copies_end();
+    const int col = begin + turn * kTurn + 32 * col_warp + 8 * t;
+    if (idle) continue;
+    if (!none) {
+      const uint4* const ws = stages.shared_of(turn) + col_warp * kRankTiles * 32;
+      float acc[kTiles][4][4];
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.0f;
+      // Column k of product q is column 8 (k / 2) + 2 q + k % 2 of the 32.
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t b[2][4];  // ranks 16 s to 16 s + 7 and the next eight, of the four products
+        if constexpr (kAlong) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) load_tiles<false>(b[i], ws + place_vector<kRankTiles>(lane, 2 * s + i));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = ws[(16 * s + 8 * i + g) * 4 + t];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) b[i][q] = turn_tile(word(v, q));
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) {
+            mma_bf16(acc[m][q], lo[m][s][0], lo[m][s][1], lo[m][s][2], lo[m][s][3], b[0][q], b[1][q]);
+            mma_bf16(acc[m][q], hi[m][s][0], hi[m][s][1], hi[m][s][2], hi[m][s][3], b[0][q], b[1][q]);
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v[8];
+          bf16x8_to_f32(out[2 * m + i], v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[2 * q] += acc[m][q][2 * i];
+            v[2 * q + 1] += acc[m][q][2 * i + 1];
+          }
+          out[2 * m + i] = f32_to_bf16x8(v);
+        }
+    }
+    const int n = values_at(col, p.cols);
+#pragma unroll
+    for (int v = 0; v < 2 * kTiles; ++v) {
+      const int64_t of = row[v >> 1][v & 1];
+      store_values<kAligned, 4>(p.y + (of < 0 ? 0 : of) * p.ldy + col, out[v], of < 0 ? 0 : n);
+    }
+  }
+  copies_wait<0>();
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
+                                const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
+                                const DeviceInfo& dev, cudaStream_t stream) {
+  set_error_site("adapter_high_kernel");
+  HighArgs p = {};
+  p.low = low;
+  p.w = backward ? a.a : a.b;
+  p.scale = backward ? nullptr : a.scale;
+  p.base = base;
+  p.y = y;
+  p.ldbase = base != nullptr ? ldbase : 0;
+  p.ldy = ldy;
+  p.cols = static_cast<int>(backward ? a.k : a.n);
+  p.rank = a.rank;
+  p.route = route_of(a);
+  p.low_aligned = aligned16(low) && a.rank % 2 == 0;
+  const bool aligned = rows_aligned(base, ldbase, p.cols) && rows_aligned(y, ldy, p.cols);
+  const bool w_aligned = backward ? a_aligned(a) : b_aligned(a);
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    constexpr int kSteps = decltype(ranks)::value <= 2 ? 1 : decltype(ranks)::value / 2;
+    auto run = [&](auto tiles, auto row_warps) {
+      constexpr int kTiles = decltype(tiles)::value, kRowWarps = decltype(row_warps)::value;
+      const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles * kRowWarps);
+      // Slabs of whole turns, and some CTAs an SM.
+      constexpr int kTurn = 32 * kAdapterWarps / kRowWarps;
+      const int turns = (p.cols + kTurn - 1) / kTurn;
+      int64_t slabs = (HIGH_CTAS * int64_t(dev.num_sms) + most - 1) / most;
+      if (slabs > turns) slabs = turns;
+      const int per = static_cast<int>((turns + slabs - 1) / slabs);
+      p.slab = per * kTurn;
+      const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>((turns + per - 1) / per));
+      auto go = [&](auto along, auto whole, auto w_whole) {
+        constexpr bool kAligned = decltype(whole)::value;
+        return launch_staged<adapter_high_kernel<kTiles, kSteps, kRowWarps, decltype(along)::value, kAligned,
+                                                 decltype(w_whole)::value>>(
+            grid, HighShape<kTiles, kSteps, kRowWarps, kAligned>::S::kBytes, dev, stream, 1, p);
+      };
+      if (!w_aligned) return backward ? go(No(), No(), No()) : go(Yes(), No(), No());
+      if (backward) return aligned ? go(No(), Yes(), Yes()) : go(No(), No(), Yes());
+      return aligned ? go(Yes(), Yes(), Yes()) : go(Yes(), No(), Yes());
+    };
+    if (!wide_tiles(a)) return run(Int<1>(), Int<1>());
+    return run(Int<kSteps <= 2 ? 2 : 1>(), Int<4>());
+  });
+}
+
+}  // namespace fp8lin

@@ -1,26 +1,32 @@
-// adapter_kernels.cuh -- low-rank adapters of many requests beside a shared
-// projection: row i has adapter a(i) of a bank (A_a [r, K], B_a [N, r], s_a) or none.
+// adapter_kernels.cuh -- what the kernels of the low-rank adapters share.  Row i
+// has adapter a(i) of a bank (A_a [r, K], B_a [N, r], s_a) or none:
 //   forward    h_i = A_a x_i,  y_i = base_i + B_a (s_a h_i)
 //   backward   dh_i = s_a B_a^T dy_i,  dx_i = base_i + A_a^T dh_i
 //              dA_a = sum over a's rows of dh_i x_i^T,  dB_a = sum of s_a dy_i h_i^T
 //
 // With a rank of at most 128 every one of these is bound by reading or writing
-// the long side (x, dy, base, y) once, so there is no tile of it in shared
-// memory: the tensor cores take their fragments from registers as they were
-// loaded, 16 bytes a lane.  The order of a contraction is free, so a lane's
-// eight consecutive values are the k index of two products, and the order of
-// the columns of a product is free, so a lane's results are eight consecutive
-// columns.  Where a product contracts over the axis that is not contiguous in
-// memory, movmatrix turns the 8 x 8 tiles in registers.  mma.sync instead of
-// tcgen05: the operands need no trip through shared memory and the accumulators
-// none through tensor memory, and with K = 16 to 128 a product is finished
-// before a tcgen05 pipeline would have started.
+// the long side (x, dy, base, y) once.  So no tile of it is shared: a lane has
+// eight consecutive values of a row, through slots in shared memory of its own
+// that cp.async fills some turns ahead, and they are its part of a fragment as
+// they are.  The order of a contraction is free, so those eight are the k index
+// of two products, and the order of a product's columns is free, so a lane's
+// results are eight consecutive columns.  Where a product contracts over the axis
+// that is not contiguous in memory, movmatrix or ldmatrix turns 8 x 8 tiles.  What
+// the warps of a CTA have in common (A, B, the rows' low numbers) goes through a
+// shared part of the same stages.  mma.sync instead of tcgen05: the operand from
+// the long side needs no layout in shared memory and the accumulators no trip
+// through tensor memory, and a product over 16 to 128 ranks is done before such a
+// pipeline would have started.
 // h and dh are fp32; where they are an operand they go in as two bf16 numbers,
 // hi + lo, which keeps 16 bits of them (the lost part, 2^-17, is below the
 // rounding of y, 2^-8); x, dy, A and B are bf16 as they are.  Sums are fp32.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "rows.cuh"
@@ -52,6 +58,19 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   if (!(fabsf(rx) <= fabsf(x))) rx = 0.0f;  // an infinity is all in hi
   if (!(fabsf(ry) <= fabsf(y))) ry = 0.0f;
   lo = cvt_bf16x2(rx, ry);
+}
+
+// Four 8 x 8 tiles from shared memory, lane l giving the row l % 8 of tile l / 8;
+// a lane (g, t) gets of each columns 2t and 2t + 1 of row g, or, turned, rows 2t and
+// 2t + 1 of column g.
+template <bool kTurn>
+__device__ __forceinline__ void load_tiles(uint32_t (&v)[4], const void* row) {
+  if constexpr (kTurn)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(smem_addr(row)) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(smem_addr(row)) : "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
@@ -124,701 +143,186 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
   return RowTile{-1, 0, 0, 0, 0, false};
 }
 
-// ---------------------------------------------------------------- low = x W^T
+// ---------------------------------------------------------------- stages
 
-// low[i][j] = scale_a * sum_c x[i][c] w_a[j][c] for the rows i of one tile, 16 *
-// kTiles of them for each of kRowWarps warps.  kAlong: w_a is [r, cols] (A:
-// contiguous along the contraction); else [cols, r] (B).  The other warps, and the
-// CTAs of a cluster, take other columns, 32 each in turn; their sums meet in
-// shared memory.  Warps of the same columns read w_a from L1 after the first.
-struct LowArgs {
-  const uint16_t* x;
-  int64_t ldx;
-  const uint16_t* w;
-  const float* scale;  // null: 1
-  float* low;          // [rows, rank] dense
-  int cols, rank;
-  int parts;  // CTAs of a cluster
-  Route route;
-};
+constexpr int kAdapterThreads = 256, kAdapterWarps = 8;
 
-constexpr int kLowWarps = 8;
+// Stages of a turn each: kVecs vectors a thread, its own, and kShared for all.
+// A turn's copies begin kStages - 1 turns before it is due; turn i:
+//   wait(); begin turn i + kStages - 1; read turn i
+// wait() ends with a barrier, after which the stage of turn i - 1 may be filled.
+// Rows that are not 16-byte aligned take registers instead of their own vectors,
+// one turn ahead.
+template <int kStages, int kVecs, int kShared, bool kAligned>
+struct Stages {
+  static constexpr int kOwn = kAligned ? kVecs * kAdapterThreads : 0, kSize = kOwn + kShared;
+  static constexpr size_t kBytes = sizeof(uint4) * kStages * kSize;
+  static constexpr int kCount = kStages;
+  uint4* const base;
+  uint4 next[kVecs];
 
-// Ranks a lane holds side by side of a [cols, r] weight.
-constexpr int ranks_a_lane(int rank_tiles) { return rank_tiles >= 4 ? 8 : 2 * rank_tiles; }
-
-template <int kTiles, int kRankTiles, int kRowWarps, bool kAlong, bool kAligned>
-__global__ void __launch_bounds__(32 * kLowWarps, kRankTiles <= 8 ? 2 : 1)
-    adapter_low_kernel(const __grid_constant__ LowArgs p) {
-  constexpr int kColWarps = kLowWarps / kRowWarps, kSums = kTiles * kRankTiles * 4;
-  constexpr int kRoom = kColWarps > 1 ? kLowWarps / 2 : kLowWarps;
-  __shared__ float sums[kRoom][kSums][32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
-  const int row_warp = warp % kRowWarps, col_warp = warp / kRowWarps;
-  const int g = lane >> 2, t = lane & 3;
-  const int parts = p.parts, part = static_cast<int>(blockIdx.x) % parts;
-  const RowTile tile = find_tile(p.route, p.route.groups, 16 * kTiles * kRowWarps,
-                                 static_cast<int>(blockIdx.x) / parts);
-  if (tile.group < 0) return;  // all CTAs of the cluster
-  if (tile.group == p.route.groups - 1) {  // rows without an adapter
-    if (part == 0)
-      for (int at = warp; at < tile.count; at += kLowWarps)
-        for (int j = lane; j < p.rank; j += 32)
-          p.low[int64_t(__ldg(p.route.rows + tile.begin + at)) * p.rank + j] = 0.0f;
-    return;
+  __device__ __forceinline__ explicit Stages(uint4* shared) : base(shared) {}
+  __device__ __forceinline__ uint4* shared_of(int turn) const {
+    return base + turn % kStages * kSize + kOwn;
   }
-  int64_t row[kTiles][2];
+  // The thread's own vectors of a turn: from(vector, n) gives a pointer and how
+  // many values it has.  Unaligned: into registers, called one turn ahead.
+  template <typename From>
+  __device__ __forceinline__ void copy(int turn, From from) {
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = (row_warp * kTiles + m) * 16 + i * 8 + g;
-      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
-    }
-  const bool idle = row_warp * kTiles * 16 >= tile.count;
-  const uint16_t* const w = p.w + int64_t(tile.group) * p.rank * p.cols;
-  float acc[kTiles][kRankTiles][4];
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-  constexpr int kWide = ranks_a_lane(kRankTiles);
-  const int step = 32 * kColWarps * parts;
-  // A lane's x and w of 32 columns.  w along the contraction: rank 8 j + g, the
-  // lane's eight columns; across it: row k of a product's tile is column
-  // 8 (k / 2) + 4 s + k % 2 of the 32, and two more in its second half (the order
-  // in which a lane holds x), and a lane has kWide ranks of it.
-  constexpr int kBlocks = (kRankTiles + 3) / 4;
-  constexpr int kLoads = kAlong ? kRankTiles : 4 * kBlocks;
-  auto load_x = [&](int c, uint4 (&x)[kTiles][2]) {
-    const int col = c + 8 * t;
-    const int n = kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        x[m][i] = load_values<kAligned>(p.x + row[m][i] * p.ldx + col, row[m][i] >= 0 ? n : 0);
-  };
-  auto load_w = [&](int c, uint4 (&b)[kLoads]) {
-    if constexpr (kAlong) {
-      const int col = c + 8 * t;
-      const int n = kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
-#pragma unroll
-      for (int j = 0; j < kRankTiles; ++j) {
-        const int rank = 8 * j + g;
-        b[j] = load_values<kAligned>(w + int64_t(rank) * p.cols + col, rank < p.rank ? n : 0);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {  // block, step, half
-        const int col = c + 8 * (g >> 1) + 2 * (i & 3) + (g & 1);
-        const int rank = 32 * (i >> 2) + kWide * t;
-        const bool on = col < p.cols && rank < p.rank;
-        const uint16_t* from = w + int64_t(col) * p.rank + rank;
-        if constexpr (!kAligned) {
-          b[i] = load_values<false>(from, on ? min(kWide, p.rank - rank) : 0);
-        } else if constexpr (kWide == 8) {
-          b[i] = load_if(from, on);
-        } else if constexpr (kWide == 4) {
-          const uint2 v = load2_if(from, on);
-          b[i] = make_uint4(v.x, v.y, 0, 0);
-        } else {
-          b[i] = make_uint4(load1_if(from, on), 0, 0, 0);
-        }
-      }
-    }
-  };
-  auto add = [&](const uint4 (&x)[kTiles][2], const uint4 (&b)[kLoads]) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < kRankTiles; ++j) {
-        uint32_t b0, b1;
-        if constexpr (kAlong) {
-          b0 = word(b[j], 2 * s);
-          b1 = word(b[j], 2 * s + 1);
-        } else {
-          b0 = turn_tile(word(b[4 * (j >> 2) + 2 * s], j & 3));
-          b1 = turn_tile(word(b[4 * (j >> 2) + 2 * s + 1], j & 3));
-        }
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-          mma_bf16(acc[m][j], word(x[m][0], 2 * s), word(x[m][1], 2 * s), word(x[m][0], 2 * s + 1),
-                   word(x[m][1], 2 * s + 1), b0, b1);
-      }
-  };
-  // kAhead turns of x (and of w, where it is small) are on their way: 2 KB a turn
-  // of a warp, 16 warps an SM, and HBM takes a microsecond.
-  constexpr bool kRingW = kRankTiles <= 4;
-  constexpr int kAhead = kRankTiles <= 2 ? 3 : 2;
-  int c = idle ? p.cols : 32 * (part * kColWarps + col_warp);
-  uint4 x[kAhead][kTiles][2], b[kRingW ? kAhead : 1][kLoads];
-#pragma unroll
-  for (int d = 0; d < kAhead; ++d) {
-    load_x(c + d * step, x[d]);
-    if constexpr (kRingW) load_w(c + d * step, b[d]);
-  }
-  while (c < p.cols) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      if (c < p.cols) {
-        if constexpr (!kRingW) load_w(c, b[0]);
-        add(x[d], b[kRingW ? d : 0]);
-        load_x(c + kAhead * step, x[d]);
-        if constexpr (kRingW) load_w(c + kAhead * step, b[d]);
-        c += step;
-      }
+    for (int v = 0; v < kVecs; ++v) {
+      int n;
+      const uint16_t* p = from(v, n);
+      if constexpr (kAligned)
+        copy16(base + turn % kStages * kSize + v * kAdapterThreads + threadIdx.x, p, n > 0);
+      else
+        next[v] = load_values<false>(p, n);
     }
   }
-  float* const mine = &acc[0][0][0];
-  // Sums of the warps of the same rows: the upper half's to shared memory, added
-  // by the lower.
+  __device__ __forceinline__ void take(int turn, uint4 (&out)[kVecs]) const {
 #pragma unroll
-  for (int half = kLowWarps / 2; half >= kRowWarps; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-#pragma unroll
-      for (int i = 0; i < kSums; ++i) sums[warp - half][i][lane] = mine[i];
-    }
-    __syncthreads();
-    if (warp < half) {
-#pragma unroll
-      for (int i = 0; i < kSums; ++i) mine[i] += sums[warp][i][lane];
-    }
+    for (int v = 0; v < kVecs; ++v)
+      out[v] = kAligned ? base[turn % kStages * kSize + v * kAdapterThreads + threadIdx.x] : next[v];
+  }
+  __device__ __forceinline__ void wait() const {
+    copies_wait<kStages - 2>();
     __syncthreads();
   }
-  const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
-  auto rank_of = [&](int j, int i, int t) {
-    return kAlong ? 8 * j + 2 * t + (i & 1) : 32 * (j >> 2) + kWide * t + 2 * (j & 3) + (i & 1);
-  };
-  if (parts == 1) {
-    if (warp >= kRowWarps) return;
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t to = row[m][i >> 1];
-          const int rank = rank_of(j, i, t);
-          if (to >= 0 && rank < p.rank) p.low[to * p.rank + rank] = scale * acc[m][j][i];
-        }
-    return;
-  }
-  // The cluster's sums: every CTA adds a part of the numbers, in the CTAs' order.
-  if (warp < kRowWarps) {
-#pragma unroll
-    for (int i = 0; i < kSums; ++i) sums[warp][i][lane] = mine[i];
-  }
-  cluster_sync_all();
-  const int each = kRowWarps * kSums / parts;  // numbers of a lane; parts divides kRowWarps * kSums
-  for (int k = part * each + warp; k < (part + 1) * each; k += kLowWarps) {
-    const int of = k / kSums, m = k % kSums / (4 * kRankTiles), j = k / 4 % kRankTiles, i = k % 4;
-    const uint32_t at = smem_addr(&sums[of][k % kSums][lane]);
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int from = 0; from < parts; ++from) sum += __uint_as_float(ld_shared_cluster_u32(map_to_cta(at, from)));
-    const int which = (of * kTiles + m) * 16 + 8 * (i >> 1) + g, rank = rank_of(j, i, t);
-    if (which < tile.count && rank < p.rank)
-      p.low[int64_t(__ldg(p.route.rows + tile.begin + which)) * p.rank + rank] = scale * sum;
-  }
-  cluster_sync_all();
-}
-
-// ---------------------------------------------------------------- y = base + low W
-
-// The ranks of a lane in step s of a product over ranks: four side by side.
-template <int kSteps>
-__device__ __forceinline__ int rank_at(int s, int t) {
-  return kSteps == 1 ? 4 * t : 32 * (s >> 1) + 8 * t + 4 * (s & 1);
-}
-
-// y[i][c] = base[i][c] + sum_j scale_a low[i][j] w_a(j, c) for one tile of rows
-// and `slab` columns.  kAlong: w_a is [cols, r] (B), else [r, cols] (A).
-struct HighArgs {
-  const float* low;
-  const uint16_t* w;
-  const float* scale;    // null: 1
-  const uint16_t* base;  // null: 0
-  uint16_t* y;
-  int64_t ldbase, ldy;
-  int cols, rank, slab;
-  Route route;
-  bool low_aligned;
 };
 
-constexpr int kHighWarps = 8;
+// As many stages as `bytes` hold, 2 to 8.
+constexpr int stages_in(size_t bytes, size_t stage) {
+  const size_t n = bytes / stage;
+  return n < 2 ? 2 : n > 8 ? 8 : static_cast<int>(n);
+}
+// Two CTAs an SM.
+constexpr size_t kStageRoom = 96 * 1024;
 
-// The operand of low: 16 * kTiles rows, hi and lo.
-template <int kTiles, int kSteps>
-struct LowFragments {
-  uint32_t hi[kTiles][kSteps][4], lo[kTiles][kSteps][4];
-};
-
-__device__ __forceinline__ float4 load_ranks(const float* from, int n, bool aligned) {
-  if (aligned && n >= 4) return *reinterpret_cast<const float4*>(from);
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (n > 0) v.x = from[0];
-  if (n > 1) v.y = from[1];
-  if (n > 2) v.z = from[2];
-  if (n > 3) v.w = from[3];
-  return v;
+// 8 bytes to shared memory, as copy16.
+__device__ __forceinline__ void copy8(void* to, const void* from, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_addr(to)), "l"(from),
+               "r"(on ? 8 : 0)
+               : "memory");
 }
 
-template <int kTiles, int kSteps, int kRowWarps, bool kAlong, bool kAligned, bool kWAligned>
-__global__ void __launch_bounds__(32 * kHighWarps, kSteps <= 4 ? 2 : 1)
-    adapter_high_kernel(const __grid_constant__ HighArgs p) {
-  constexpr int kColWarps = kHighWarps / kRowWarps;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
-  const int row_warp = warp % kRowWarps, col_warp = warp / kRowWarps;
-  const int g = lane >> 2, t = lane & 3;
-  const RowTile tile =
-      find_tile(p.route, p.route.groups, 16 * kTiles * kRowWarps, static_cast<int>(blockIdx.x));
-  if (tile.group < 0 || row_warp * kTiles * 16 >= tile.count) return;
-  const bool none = tile.group == p.route.groups - 1;
-  if (none && p.y == p.base) return;
-  const int begin = static_cast<int>(blockIdx.y) * p.slab;
-  const int end = min(begin + p.slab, p.cols);
-  int64_t row[kTiles][2];
+// A stage of a weight whose rows lie along the long side (A, [r, cols]): kSpans
+// times 32 columns from c on, 8 * kRankTiles ranks.  Rank j of span s is at
+// (s * 8 * kRankTiles + j) * 4, four vectors of eight columns.
+template <int kRankTiles, int kSpans, bool kAligned>
+__device__ __forceinline__ void stage_ranks(uint4* to, const uint16_t* w, int c, int cols, int rank) {
+  constexpr int kVecs = kSpans * kRankTiles * 32;
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = (row_warp * kTiles + m) * 16 + i * 8 + g;
-      row[m][i] = at < tile.count ? __ldg(p.route.rows + tile.begin + at) : -1;
-    }
-  // The base of a warp's next turns is on its way while it computes.
-  auto values = [&](int c) {
-    const int col = c + 8 * t;
-    return c >= end ? 0 : kAligned ? (col < p.cols ? 8 : 0) : values_at(col, p.cols);
-  };
-  constexpr int kAhead = 2, kTurn = 32 * kColWarps;
-  uint4 base[kAhead][kTiles][2];
-  auto fetch = [&](int c, uint4 (&into)[kTiles][2]) {
-    const int n = values(c);
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        into[m][i] = load_values<kAligned>(p.base + row[m][i] * p.ldbase + c + 8 * t,
-                                           p.base != nullptr && row[m][i] >= 0 ? n : 0);
-  };
-#pragma unroll
-  for (int d = 0; d < kAhead; ++d) fetch(begin + 32 * col_warp + d * kTurn, base[d]);
-  LowFragments<kTiles, kSteps> f;
-  const float scale = none || p.scale == nullptr ? 1.0f : __ldg(p.scale + tile.group);
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int rank = rank_at<kSteps>(s, t);
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row[m][i] >= 0 && !none)
-          v = load_ranks(p.low + row[m][i] * p.rank + rank, p.rank - rank, p.low_aligned);
-        split_pair(v.x * scale, v.y * scale, f.hi[m][s][i], f.lo[m][s][i]);
-        split_pair(v.z * scale, v.w * scale, f.hi[m][s][i + 2], f.lo[m][s][i + 2]);
-      }
-  const uint16_t* const w = none ? nullptr : p.w + int64_t(tile.group) * p.rank * p.cols;
-  auto turn = [&](int c, uint4 (&next)[kTiles][2]) {
-    const int col = c + 8 * t;
-    const int n = values(c);
-    uint4 out[kTiles][2];
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) out[m][i] = next[m][i];
-    fetch(c + kAhead * kTurn, next);
-    if (!none) {
-      float acc[kTiles][4][4];
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.0f;
-      // Column k of product q is column 8 (k / 2) + 2 q + k % 2 of the 32.
-#pragma unroll
-      for (int block = 0; block < (kSteps + 1) / 2; ++block) {
-        uint32_t b[4][4];  // of product q: the two halves of one step or of two
-        if constexpr (kAlong) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int from_col = c + 8 * (g >> 1) + 2 * q + (g & 1);
-            const int rank = rank_at<kSteps>(2 * block, t);
-            constexpr int kWide = kSteps == 1 ? 4 : 8;
-            const bool on = from_col < p.cols && rank < p.rank;
-            const uint16_t* from = w + int64_t(from_col) * p.rank + rank;
-            uint4 v;
-            if constexpr (!kWAligned) {
-              v = load_values<false>(from, on ? min(kWide, p.rank - rank) : 0);
-            } else if constexpr (kWide == 8) {
-              v = load_if(from, on);
-            } else {
-              const uint2 u = load2_if(from, on);
-              v = make_uint4(u.x, u.y, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[q][i] = word(v, i);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < (kSteps == 1 ? 2 : 4); ++i) {
-            const int rank = rank_at<kSteps>(2 * block + (i >> 1), g >> 1) + 2 * (i & 1) + (g & 1);
-            const uint4 v = load_values<kWAligned>(w + int64_t(rank) * p.cols + col, rank < p.rank ? n : 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) b[q][i] = turn_tile(word(v, q));
-          }
-        }
-#pragma unroll
-        for (int s = 2 * block; s < 2 * block + (kSteps == 1 ? 1 : 2); ++s)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t b0 = b[q][2 * (s - 2 * block)], b1 = b[q][2 * (s - 2 * block) + 1];
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-              mma_bf16(acc[m][q], f.lo[m][s][0], f.lo[m][s][1], f.lo[m][s][2], f.lo[m][s][3], b0, b1);
-              mma_bf16(acc[m][q], f.hi[m][s][0], f.hi[m][s][1], f.hi[m][s][2], f.hi[m][s][3], b0, b1);
-            }
-          }
-      }
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float v[8];
-          bf16x8_to_f32(out[m][i], v);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[2 * q] += acc[m][q][2 * i];
-            v[2 * q + 1] += acc[m][q][2 * i + 1];
-          }
-          out[m][i] = f32_to_bf16x8(v);
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        store_values<kAligned, 4>(p.y + (row[m][i] < 0 ? 0 : row[m][i]) * p.ldy + col, out[m][i],
-                                  row[m][i] < 0 ? 0 : n);
-  };
-  for (int c = begin + 32 * col_warp; c < end; c += kAhead * kTurn) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-      if (c + d * kTurn < end) turn(c + d * kTurn, base[d]);
+  for (int i0 = 0; i0 < kVecs; i0 += kAdapterThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    if (kVecs % kAdapterThreads != 0 && i >= kVecs) break;
+    const int span = i / (kRankTiles * 32), j = i / 4 % (8 * kRankTiles), col = c + 32 * span + 8 * (i & 3);
+    const uint16_t* from = w + int64_t(j < rank ? j : 0) * cols + col;
+    if constexpr (kAligned)
+      copy16(to + i, from, j < rank && col < cols);
+    else
+      to[i] = load_values<false>(from, j < rank ? values_at(col, cols) : 0);
   }
 }
 
-// ---------------------------------------------------------------- dW = x^T low
-
-// dw[c][j] = sum over the rows i of one adapter of x[i][c] scale_a low[i][j], for
-// a slab of columns c.  The CTA's warps take blocks of 16 rows in turn (kRowWarps
-// of them) and columns side by side (the others); a tile of rows that is its
-// adapter's only one is written as bf16 into dw, else its sums go to the
-// partials, one slot a tile, which adapter_sum_kernel adds up.
-struct WeightArgs {
-  const uint16_t* x;
-  int64_t ldx;
-  const float* low;
-  const float* scale;  // null: 1
-  uint16_t* dw;
-  float* partials;  // [slot][cols * rank]
-  int cols, rank, tile_rows, tiles, slabs;
-  const uint4* packed;  // low as adapter_pack_kernel left it, or null
-  bool along;    // dw is [cols, r] (dB), else [r, cols] (dA)
-  bool aligned;  // x's rows
-  bool dw_aligned;
-};
-
-constexpr int kWeightWarps = 8;
-
-// With a small rank the rows' numbers are few beside x, and splitting the rows
-// leaves fewer partial sums; with a large one warps of the same rows share them.
+// A stage of a weight whose rows are the ranks of a column (B, [cols, r]): vectors
+// of eight ranks.  The products take the eight columns 8 (k / 2) + 2 q + k % 2 of 32
+// together, so these lie side by side, as place 8 q + k, and a column's vectors are
+// in an order turned by its place, so that the eight lie in different banks.
+__device__ __forceinline__ int column_place(int col) {
+  return (col & ~31) + ((col >> 1 & 3) << 3) + (col >> 3 & 3) * 2 + (col & 1);
+}
 template <int kRankTiles>
-struct WeightShape {
-  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
-  static constexpr int kColWarps = kWeightWarps / kRowWarps;
-  static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
-  static constexpr int kSlab = 32 * kChunks * kColWarps;
-  static constexpr int kSums = 2 * kChunks * kRankTiles * 4;  // a lane's
-};
-
-// What a lane needs of rank tile j of 16 rows of low: rows 2 t, 2 t + 1 and 2 t + 8,
-// 2 t + 9 of rank 8 j + g, as pairs hi (x, y) and lo (z, w).
-__device__ __forceinline__ uint4 low_operand(float a, float b, float c, float d) {
-  uint4 v;
-  split_pair(a, b, v.x, v.z);
-  split_pair(c, d, v.y, v.w);
-  return v;
+__device__ __forceinline__ int place_vector(int place, int piece) {
+  constexpr int kTurns = kRankTiles < 8 ? kRankTiles : 8;
+  return place * kRankTiles + (piece ^ ((place & 7) * kTurns / 8));
 }
-
-// low of one or two calls to adapter_weight_kernel in that form, block by block of
-// 16 rows of an adapter: a warp a block.
-struct PackArgs {
-  const float* low;
-  const float* scale;
-  uint4* packed;
-};
-constexpr int kPackWarps = 4;
-
-template <int kRankTiles>
-__global__ void __launch_bounds__(32 * kPackWarps)
-    adapter_pack_kernel(const PackArgs a, const PackArgs b, const Route route, int rank, int blocks) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x & 31u);
-  const int at = static_cast<int>(blockIdx.x) * kPackWarps + static_cast<int>(threadIdx.x >> 5);
-  const int g = lane >> 2, t = lane & 3;
-  const PackArgs& p = at < blocks ? a : b;
-  const RowTile tile = find_tile(route, route.groups - 1, 16, at < blocks ? at : at - blocks);
-  if (p.packed == nullptr || tile.group < 0) return;
-  const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
-  float v[kRankTiles][4];
+template <int kRankTiles, int kSpans, bool kAligned>
+__device__ __forceinline__ void stage_columns(uint4* to, const uint16_t* w, int c, int cols, int rank) {
+  constexpr int kVecs = kSpans * kRankTiles * 32;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int of = 2 * t + (e & 1) + 8 * (e >> 1);
-    const float* from =
-        of < tile.count ? p.low + int64_t(__ldg(route.rows + tile.begin + of)) * rank : nullptr;
-#pragma unroll
-    for (int j = 0; j < kRankTiles; ++j)
-      v[j][e] = from != nullptr && 8 * j + g < rank ? scale * from[8 * j + g] : 0.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < kRankTiles; ++j)
-    p.packed[(int64_t(tile.block) * kRankTiles + j) * 32 + lane] = low_operand(v[j][0], v[j][1], v[j][2], v[j][3]);
-}
-
-template <int kRankTiles, bool kAligned>
-__device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& route, int block,
-                                            float (*sums)[WeightShape<kRankTiles>::kSums][32]) {
-  using S = WeightShape<kRankTiles>;
-  constexpr int kChunks = S::kChunks, kSums = S::kSums;
-  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
-  const int col_warp = warp % S::kColWarps, row_warp = warp / S::kColWarps;
-  const int g = lane >> 2, t = lane & 3;
-  // The last rows first: they are what is left in L2 of the pass before.
-  const RowTile tile = find_tile(route, route.groups - 1, p.tile_rows, p.tiles - 1 - block / p.slabs);
-  if (tile.group < 0) return;
-  const int col0 = ((block % p.slabs) * S::kColWarps + col_warp) * 32 * kChunks;
-  const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
-  float acc[2 * kChunks][kRankTiles][4];
-#pragma unroll
-  for (int m = 0; m < 2 * kChunks; ++m)
-#pragma unroll
-    for (int j = 0; j < kRankTiles; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-  const int32_t* const rows = route.rows + tile.begin;
-  // x of the next blocks and the row numbers of one more are on their way.
-  constexpr int kStep = 16 * S::kRowWarps, kAhead = kRankTiles <= 8 ? 3 : 2;
-  int at[2];
-  uint4 ring[kAhead][kChunks][2];
-  auto find = [&](int r) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int of = r + 8 * i + g;
-      at[i] = of < tile.count ? __ldg(rows + of) : -1;
-    }
-  };
-  auto fetch = [&](uint4 (&into)[kChunks][2]) {
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = col0 + 32 * c + 8 * t;
-        const int n = at[i] < 0 ? 0 : values_at(col, p.cols);
-        into[c][i] = load_values<kAligned>(p.x + at[i] * p.ldx + col, n);
-      }
-  };
-#pragma unroll
-  for (int d = 0; d < kAhead; ++d) {
-    find(16 * row_warp + d * kStep);
-    fetch(ring[d]);
-  }
-  find(16 * row_warp + kAhead * kStep);
-  auto turn = [&](int r, uint4 (&x)[kChunks][2]) {
-    uint4 low[kRankTiles];
-    if (p.packed != nullptr) {
-      const uint4* from = p.packed + (int64_t(tile.block + r / 16) * kRankTiles) * 32 + lane;
-#pragma unroll
-      for (int j = 0; j < kRankTiles; ++j) low[j] = __ldg(from + 32 * j);
-    } else {
-      float v[kRankTiles][4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int of = r + 2 * t + (e & 1) + 8 * (e >> 1);
-        const float* from = of < tile.count ? p.low + int64_t(__ldg(rows + of)) * p.rank : nullptr;
-#pragma unroll
-        for (int j = 0; j < kRankTiles; ++j)
-          v[j][e] = from != nullptr && 8 * j + g < p.rank ? scale * __ldg(from + 8 * j + g) : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < kRankTiles; ++j) low[j] = low_operand(v[j][0], v[j][1], v[j][2], v[j][3]);
-    }
-    uint32_t a[kChunks][4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) a[c][q][i] = turn_tile(word(x[c][i], q));
-    fetch(x);
-    find(r + (kAhead + 1) * kStep);
-#pragma unroll
-    for (int j = 0; j < kRankTiles; ++j) {
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
-                   a[c][2 * m + 1][1], low[j].z, low[j].w);
-          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
-                   a[c][2 * m + 1][1], low[j].x, low[j].y);
-        }
-    }
-  };
-  for (int r = 16 * row_warp; r < tile.count; r += kAhead * kStep) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-      if (r + d * kStep < tile.count) turn(r + d * kStep, ring[d]);
-  }
-  if constexpr (S::kRowWarps > 1) {
-    float* const mine = &acc[0][0][0];
-#pragma unroll
-    for (int half = kWeightWarps / 2; half >= S::kColWarps; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
-#pragma unroll
-        for (int i = 0; i < kSums; ++i) sums[warp - half][i][lane] = mine[i];
-      }
-      __syncthreads();
-      if (warp < half) {
-#pragma unroll
-        for (int i = 0; i < kSums; ++i) mine[i] += sums[warp][i][lane];
-      }
-      __syncthreads();
+  for (int i0 = 0; i0 < kVecs; i0 += kAdapterThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    if (kVecs % kAdapterThreads != 0 && i >= kVecs) break;
+    const int k = i / kRankTiles, piece = i % kRankTiles, col = c + k;
+    const int n = col < cols ? values_at(8 * piece, rank) : 0;
+    const uint16_t* from = w + int64_t(n > 0 ? col : 0) * rank + (n > 0 ? 8 * piece : 0);
+    uint4* put = to + place_vector<kRankTiles>(column_place(k), piece);
+    if constexpr (!kAligned) {
+      *put = load_values<false>(from, n);
+    } else if (rank % 8 == 0) {
+      copy16(put, from, n > 0);
+    } else {  // a multiple of 4
+      copy8(put, from, n > 0);
+      copy8(reinterpret_cast<uint2*>(put) + 1, n > 4 ? from + 4 : from, n > 4);
     }
   }
-  if (row_warp != 0 || col0 >= p.cols) return;
-  const int64_t size = int64_t(p.cols) * p.rank;
-  uint16_t* const dw = p.dw + tile.group * size;
-  float* const part = tile.only ? nullptr : p.partials + tile.slot * size;
-  // A lane has of product (c, j) columns 8 (g / 2) + 2 q + g % 2, q = 0 .. 3, of
-  // ranks 8 j + 2 t and the next.
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-    for (int j = 0; j < kRankTiles; ++j) {
-      if (p.along) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = col0 + 32 * c + 8 * (g >> 1) + 2 * q + (g & 1);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int rank = 8 * j + 2 * t + e;
-            if (col >= p.cols || rank >= p.rank) continue;
-            const float v = acc[2 * c + (q >> 1)][j][2 * (q & 1) + e];
-            const int64_t to = int64_t(col) * p.rank + rank;
-            if (part != nullptr)
-              part[to] = v;
-            else
-              dw[to] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
-          }
-        }
-        continue;
-      }
-      // Lanes of neighbouring g swap, so that one has eight columns side by side
-      // of the first rank and the other of the second.
-      float v[8];
-      const int e = g & 1;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* a = acc[2 * c + (q >> 1)][j] + 2 * (q & 1);
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, e ? a[0] : a[1], 4);
-        v[2 * q] = e ? got : a[0];
-        v[2 * q + 1] = e ? a[1] : got;
-      }
-      const int col = col0 + 32 * c + 8 * (g >> 1), rank = 8 * j + 2 * t + e;
-      const int64_t to = int64_t(rank) * p.cols + col;
-      if (rank < p.rank && p.dw_aligned && col < p.cols) {
-        if (part != nullptr) {
-          float4* put = reinterpret_cast<float4*>(part + to);
-          put[0] = make_float4(v[0], v[1], v[2], v[3]);
-          put[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-          *reinterpret_cast<uint4*>(dw + to) = f32_to_bf16x8(v);
-        }
-      } else if (rank < p.rank) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (col + i >= p.cols) continue;
-          if (part != nullptr)
-            part[to + i] = v[i];
-          else
-            dw[to + i] = static_cast<uint16_t>(cvt_bf16x2(v[i], 0.0f) & 0xFFFFu);
-        }
-      }
+}
+
+// ---------------------------------------------------------------- launching
+
+// Launches a kernel that may need more dynamic shared memory than the default.
+template <auto* kKernel, typename... Args>
+cudaError_t launch_staged(dim3 grid, size_t bytes, const DeviceInfo& dev, cudaStream_t stream, int cluster,
+                          const Args&... args) {
+  if (bytes > 0) {
+    static std::mutex mu;
+    static bool done[64];  // devices on which the kernel may have that much
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev.device]) {
+      const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(bytes));
+      if (e != cudaSuccess) return e;
+      done[dev.device] = true;
     }
-}
-
-// dB (blocks from 0 on) and dA (the others) in one launch; either may have none.
-template <int kRankTiles>
-__global__ void __launch_bounds__(32 * kWeightWarps, kRankTiles <= 2 ? 2 : 1)
-    adapter_weight_kernel(const __grid_constant__ WeightArgs db, const __grid_constant__ WeightArgs da,
-                          const Route route) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int block = static_cast<int>(blockIdx.x), first = db.tiles * db.slabs;
-  const bool is_db = block < first;
-  using S = WeightShape<kRankTiles>;
-  __shared__ float sums[S::kRowWarps > 1 ? kWeightWarps / 2 : 1][S::kSums][32];
-  const WeightArgs& p = is_db ? db : da;
-  if (p.aligned)
-    weight_tile<kRankTiles, true>(p, route, is_db ? block : block - first, sums);
-  else
-    weight_tile<kRankTiles, false>(p, route, is_db ? block : block - first, sums);
-}
-
-// The partials of adapters with several tiles, added in order, and zeros for
-// those without rows.  One CTA row an adapter.
-struct SumArgs {
-  const float* partials;
-  uint16_t* dw;
-  int64_t size;  // cols * rank
-  int tile_rows;
-  Route route;
-};
-constexpr int kSumThreads = 256;
-
-__device__ __forceinline__ void sum_partials(const SumArgs& p, int group, int block, int blocks) {
-  // Slots before this adapter's: a sum over the groups before it.
-  int mine = 0, before = 0;
-  const int lane = static_cast<int>(threadIdx.x & 31u);
-  for (int g = lane; g <= group; g += 32) {
-    const int count = __ldg(p.route.first + g + 1) - __ldg(p.route.first + g);
-    const int tiles = (count + p.tile_rows - 1) / p.tile_rows;
-    if (g == group)
-      mine = tiles;
-    else if (tiles > 1)
-      before += tiles;
   }
-  before = __reduce_add_sync(0xFFFFFFFFu, before);
-  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  if (mine == 1) return;  // written already
-  uint16_t* const dw = p.dw + group * p.size;
-  const float* const from = p.partials + before * p.size;
-  for (int64_t i = int64_t(block) * kSumThreads + threadIdx.x; i < p.size; i += int64_t(blocks) * kSumThreads) {
-    float v = 0.0f;
-#pragma unroll 8
-    for (int s = 0; s < mine; ++s) v += __ldcg(from + s * p.size + i);
-    dw[i] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+  return launch_kernel(kKernel, grid, dim3(kAdapterThreads), bytes, stream, cluster, false, args...);
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool rows_aligned(const void* p, int64_t ld, int64_t cols) {
+  return p == nullptr || (aligned16(p) && ld % 8 == 0 && cols % 8 == 0);
+}
+
+// 1, 2, 4, 8 or 16 tiles of eight ranks.
+inline int rank_tiles(int rank) {
+  int t = 1;
+  while (8 * t < rank) t *= 2;
+  return t;
+}
+
+template <int kValue>
+using Int = std::integral_constant<int, kValue>;
+using Yes = std::true_type;
+using No = std::false_type;
+
+template <typename Run>
+cudaError_t with_rank_tiles(int rank, Run run) {
+  switch (rank_tiles(rank)) {
+    case 1: return run(Int<1>());
+    case 2: return run(Int<2>());
+    case 4: return run(Int<4>());
+    case 8: return run(Int<8>());
+    default: return run(Int<16>());
   }
 }
+
+// Tiles of `size` rows, at most: each adapter with rows may end inside one.
+inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t size) {
+  const int64_t t = rows / size + groups;
+  return t < rows ? t : rows;
+}
+
+// Whether an adapter has rows for tiles of several warps, on average.
+inline bool wide_tiles(const AdapterArgs& a) { return a.rows >= 64 * a.count; }
+
+inline Route route_of(const AdapterArgs& a) {
+  return Route{a.route, a.route + a.count + 2, static_cast<int>(a.count) + 1};
+}
+
+// Whether a stage of A or B can be filled by copies.
+inline bool a_aligned(const AdapterArgs& a) { return aligned16(a.a) && a.k % 8 == 0; }
+inline bool b_aligned(const AdapterArgs& a) { return aligned16(a.b) && a.rank % 4 == 0; }
 
 }  // namespace fp8lin

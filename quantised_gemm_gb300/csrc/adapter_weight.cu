@@ -1,0 +1,438 @@
+// adapter_weight.cu -- the gradients of the adapters' weights:
+//   dw[c][j] = sum over the rows i of one adapter of x[i][c] s_a low[i][j]
+// dB (x = dy, low = h) and dA (x the input, low = dh, turned) in one launch.
+#include "adapter_kernels.cuh"
+
+namespace fp8lin {
+namespace {
+
+// A tile of rows of one adapter and a slab of columns.  The CTA's warps take
+// blocks of 16 rows side by side (kRowWarps of them) and columns side by side (the
+// others); a tile that is its adapter's only one is written as bf16 into dw, else
+// its sums go to the partials, one slot a tile, which adapter_sum_kernel adds up.
+struct WeightArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const float* low;
+  const float* scale;  // null: 1
+  uint16_t* dw;
+  float* partials;  // [slot][cols * rank]
+  int cols, rank, tile_rows, tiles, slabs;
+  const uint4* packed;  // low as adapter_pack_kernel left it, or null
+  bool along;    // dw is [cols, r] (dB), else [r, cols] (dA)
+  bool aligned;  // x's rows
+  bool dw_aligned;
+};
+
+// With a small rank the rows' numbers are few beside x, and splitting the rows
+// leaves fewer partial sums; with a large one warps of the same rows share them.
+template <int kRankTiles>
+struct WeightShape {
+  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
+  static constexpr int kColWarps = kAdapterWarps / kRowWarps;
+  static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
+  static constexpr int kSlab = 32 * kChunks * kColWarps;
+  static constexpr int kSums = 2 * kChunks * kRankTiles * 4;  // a lane's
+  static constexpr int kShared = kRowWarps * kRankTiles * 32;  // a turn's low operands
+  static constexpr size_t kStage = sizeof(uint4) * (2 * kChunks * kAdapterThreads + kShared);
+  static constexpr int kStages = stages_in(kRankTiles <= 2 ? kStageRoom - 16 * 1024 : kStageRoom, kStage);
+};
+
+// What a lane needs of rank tile j of 16 rows of low: rows 2 t, 2 t + 1 and 2 t + 8,
+// 2 t + 9 of rank 8 j + g, as pairs hi (x, y) and lo (z, w).
+__device__ __forceinline__ uint4 low_operand(float a, float b, float c, float d) {
+  uint4 v;
+  split_pair(a, b, v.x, v.z);
+  split_pair(c, d, v.y, v.w);
+  return v;
+}
+
+// low of one or two calls to adapter_weight_kernel in that form, block by block of
+// 16 rows of an adapter: a warp a block.
+struct PackArgs {
+  const float* low;
+  const float* scale;
+  uint4* packed;
+};
+constexpr int kPackWarps = 4;
+
+template <int kRankTiles>
+__global__ void __launch_bounds__(32 * kPackWarps)
+    adapter_pack_kernel(const PackArgs a, const PackArgs b, const Route route, int rank, int blocks) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const int at = static_cast<int>(blockIdx.x) * kPackWarps + static_cast<int>(threadIdx.x >> 5);
+  const int g = lane >> 2, t = lane & 3;
+  const PackArgs& p = at < blocks ? a : b;
+  const RowTile tile = find_tile(route, route.groups - 1, 16, at < blocks ? at : at - blocks);
+  if (p.packed == nullptr || tile.group < 0) return;
+  const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
+  float v[kRankTiles][4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int of = 2 * t + (e & 1) + 8 * (e >> 1);
+    const float* from =
+        of < tile.count ? p.low + int64_t(__ldg(route.rows + tile.begin + of)) * rank : nullptr;
+#pragma unroll
+    for (int j = 0; j < kRankTiles; ++j)
+      v[j][e] = from != nullptr && 8 * j + g < rank ? scale * from[8 * j + g] : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < kRankTiles; ++j)
+    p.packed[(int64_t(tile.block) * kRankTiles + j) * 32 + lane] = low_operand(v[j][0], v[j][1], v[j][2], v[j][3]);
+}
+
+template <int kRankTiles, bool kAligned>
+__device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& route, int block,
+                                            float (*sums)[WeightShape<kRankTiles>::kSums][32],
+                                            uint4* shared) {
+  using S = WeightShape<kRankTiles>;
+  constexpr int kChunks = S::kChunks, kSums = S::kSums;
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int col_warp = warp % S::kColWarps, row_warp = warp / S::kColWarps;
+  const int g = lane >> 2, t = lane & 3;
+  // The last rows first: they are what is left in L2 of the pass before.
+  const RowTile tile = find_tile(route, route.groups - 1, p.tile_rows, p.tiles - 1 - block / p.slabs);
+  if (tile.group < 0) return;
+  const int col0 = ((block % p.slabs) * S::kColWarps + col_warp) * 32 * kChunks;
+  const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
+  float acc[2 * kChunks][kRankTiles][4];
+#pragma unroll
+  for (int m = 0; m < 2 * kChunks; ++m)
+#pragma unroll
+    for (int j = 0; j < kRankTiles; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+  const int32_t* const rows = route.rows + tile.begin;
+  // x, the low operands and, one turn more, the row numbers are on their way.
+  constexpr int kStep = 16 * S::kRowWarps;
+  const int turns = (tile.count + kStep - 1) / kStep;
+  using T = Stages<S::kStages, 2 * kChunks, S::kShared, kAligned>;
+  T stages(shared);
+  constexpr int kBefore = kAligned ? T::kCount - 1 : 1;
+  int number[2];
+  auto find = [&](int turn) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int of = turn * kStep + 16 * row_warp + 8 * i + g;
+      number[i] = of < tile.count ? __ldg(rows + of) : -1;
+    }
+  };
+  auto copy_x = [&](int turn) {
+    stages.copy(turn, [&](int v, int& n) {
+      const int col = col0 + 32 * (v >> 1) + 8 * t, row = number[v & 1];
+      n = row < 0 ? 0 : values_at(col, p.cols);
+      return p.x + (row < 0 ? 0 : row) * p.ldx + (n > 0 ? col : 0);
+    });
+  };
+  auto copy_low = [&](int turn) {
+    uint4* const to = stages.shared_of(turn);
+#pragma unroll
+    for (int i0 = 0; i0 < S::kShared; i0 += kAdapterThreads) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      if (S::kShared % kAdapterThreads != 0 && i >= S::kShared) break;
+      const int r = turn * kStep + 16 * (i / (kRankTiles * 32));  // the block's first row
+      if (p.packed != nullptr) {
+        const bool on = r < tile.count;
+        copy16(to + i, p.packed + (on ? int64_t(tile.block + r / 16) * (kRankTiles * 32) + i % (kRankTiles * 32) : 0), on);
+        continue;
+      }
+      const int j = i / 32 % kRankTiles;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int of = r + 2 * (i & 3) + (e & 1) + 8 * (e >> 1), rank = 8 * j + (i >> 2 & 7);
+        v[e] = of < tile.count && rank < p.rank ? scale * __ldg(p.low + int64_t(__ldg(rows + of)) * p.rank + rank) : 0.0f;
+      }
+      to[i] = low_operand(v[0], v[1], v[2], v[3]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < T::kCount - 1; ++i) {
+    if (i < turns) copy_low(i);
+    if (kAligned || i == 0) {
+      find(i);
+      copy_x(i);
+    }
+    copies_end();
+  }
+  find(kBefore);
+  for (int turn = 0; turn < turns; ++turn) {
+    stages.wait();
+    uint4 x[2 * kChunks];
+    stages.take(turn, x);
+    if (turn + T::kCount - 1 < turns) copy_low(turn + T::kCount - 1);
+    copy_x(turn + kBefore);
+    copies_end();
+    find(turn + kBefore + 1);
+    const uint4* const operand = stages.shared_of(turn) + row_warp * kRankTiles * 32 + lane;
+    uint32_t a[kChunks][4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[c][q][i] = turn_tile(word(x[2 * c + i], q));
+#pragma unroll
+    for (int j = 0; j < kRankTiles; ++j) {
+      const uint4 low = operand[32 * j];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
+                   a[c][2 * m + 1][1], low.z, low.w);
+          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
+                   a[c][2 * m + 1][1], low.x, low.y);
+        }
+    }
+  }
+  copies_wait<0>();
+  if constexpr (S::kRowWarps > 1) {
+    float* const mine = &acc[0][0][0];
+#pragma unroll
+    for (int half = kAdapterWarps / 2; half >= S::kColWarps; half >>= 1) {
+      if (warp >= half && warp < 2 * half) {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sums[warp - half][i][lane] = mine[i];
+      }
+      __syncthreads();
+      if (warp < half) {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) mine[i] += sums[warp][i][lane];
+      }
+      __syncthreads();
+    }
+  }
+  if (row_warp != 0 || col0 >= p.cols) return;
+  const int64_t size = int64_t(p.cols) * p.rank;
+  uint16_t* const dw = p.dw + tile.group * size;
+  float* const part = tile.only ? nullptr : p.partials + tile.slot * size;
+  // A lane has of product (c, j) columns 8 (g / 2) + 2 q + g % 2, q = 0 .. 3, of
+  // ranks 8 j + 2 t and the next.
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+    for (int j = 0; j < kRankTiles; ++j) {
+      if (p.along) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = col0 + 32 * c + 8 * (g >> 1) + 2 * q + (g & 1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rank = 8 * j + 2 * t + e;
+            if (col >= p.cols || rank >= p.rank) continue;
+            const float v = acc[2 * c + (q >> 1)][j][2 * (q & 1) + e];
+            const int64_t to = int64_t(col) * p.rank + rank;
+            if (part != nullptr)
+              part[to] = v;
+            else
+              dw[to] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+          }
+        }
+        continue;
+      }
+      // Lanes of neighbouring g swap, so that one has eight columns side by side
+      // of the first rank and the other of the second.
+      float v[8];
+      const int e = g & 1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* a = acc[2 * c + (q >> 1)][j] + 2 * (q & 1);
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, e ? a[0] : a[1], 4);
+        v[2 * q] = e ? got : a[0];
+        v[2 * q + 1] = e ? a[1] : got;
+      }
+      const int col = col0 + 32 * c + 8 * (g >> 1), rank = 8 * j + 2 * t + e;
+      const int64_t to = int64_t(rank) * p.cols + col;
+      if (rank < p.rank && p.dw_aligned && col < p.cols) {
+        if (part != nullptr) {
+          float4* put = reinterpret_cast<float4*>(part + to);
+          put[0] = make_float4(v[0], v[1], v[2], v[3]);
+          put[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4*>(dw + to) = f32_to_bf16x8(v);
+        }
+      } else if (rank < p.rank) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (col + i >= p.cols) continue;
+          if (part != nullptr)
+            part[to + i] = v[i];
+          else
+            dw[to + i] = static_cast<uint16_t>(cvt_bf16x2(v[i], 0.0f) & 0xFFFFu);
+        }
+      }
+    }
+}
+
+// dB (blocks from 0 on) and dA (the others) in one launch; either may have none.
+template <int kRankTiles>
+__global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 2 ? 2 : 1)
+    adapter_weight_kernel(const __grid_constant__ WeightArgs db, const __grid_constant__ WeightArgs da,
+                          const Route route) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int block = static_cast<int>(blockIdx.x), first = db.tiles * db.slabs;
+  const bool is_db = block < first;
+  using S = WeightShape<kRankTiles>;
+  extern __shared__ uint4 shared[];
+  __shared__ float sums[S::kRowWarps > 1 ? kAdapterWarps / 2 : 1][S::kSums][32];
+  const WeightArgs& p = is_db ? db : da;
+  if (p.aligned)
+    weight_tile<kRankTiles, true>(p, route, is_db ? block : block - first, sums, shared);
+  else
+    weight_tile<kRankTiles, false>(p, route, is_db ? block : block - first, sums, shared);
+}
+
+// The partials of adapters with several tiles, added in order, and zeros for
+// those without rows.  One CTA row an adapter.
+struct SumArgs {
+  const float* partials;
+  uint16_t* dw;
+  int64_t size;  // cols * rank
+  int tile_rows;
+  Route route;
+};
+constexpr int kSumThreads = 256;
+
+__device__ __forceinline__ void sum_partials(const SumArgs& p, int group, int block, int blocks) {
+  // Slots before this adapter's: a sum over the groups before it.
+  int mine = 0, before = 0;
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  for (int g = lane; g <= group; g += 32) {
+    const int count = __ldg(p.route.first + g + 1) - __ldg(p.route.first + g);
+    const int tiles = (count + p.tile_rows - 1) / p.tile_rows;
+    if (g == group)
+      mine = tiles;
+    else if (tiles > 1)
+      before += tiles;
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+  if (mine == 1) return;  // written already
+  uint16_t* const dw = p.dw + group * p.size;
+  const float* const from = p.partials + before * p.size;
+  for (int64_t i = int64_t(block) * kSumThreads + threadIdx.x; i < p.size; i += int64_t(blocks) * kSumThreads) {
+    float v = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < mine; ++s) v += __ldcg(from + s * p.size + i);
+    dw[i] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+  }
+}
+
+__global__ void __launch_bounds__(kSumThreads) adapter_sum_kernel(const __grid_constant__ SumArgs a,
+                                                                  const __grid_constant__ SumArgs b,
+                                                                  int blocks_a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int block = static_cast<int>(blockIdx.x), group = static_cast<int>(blockIdx.y);
+  if (block < blocks_a)
+    sum_partials(a, group, block, blocks_a);
+  else
+    sum_partials(b, group, block - blocks_a, static_cast<int>(gridDim.x) - blocks_a);
+}
+
+}  // namespace
+
+int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev) {
+  const int64_t cols = da ? a.k : a.n;
+  int64_t slab = 0;
+  with_rank_tiles(a.rank, [&](auto ranks) {
+    slab = WeightShape<decltype(ranks)::value>::kSlab;
+    return cudaSuccess;
+  });
+  const int64_t slabs = (cols + slab - 1) / slab;
+  // Three CTAs an SM, tiles of 128 rows at least.
+  int64_t rows = (a.rows * slabs + 3 * dev.num_sms - 1) / (3 * dev.num_sms);
+  rows = (rows + 127) / 128 * 128;
+  // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
+  // them, and at most a.rows / rows and one for each adapter.
+  const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));
+  if (slots < 2) return a.rows;  // no room: every adapter's rows in one tile
+  int64_t least = (2 * a.rows + slots - 1) / slots;
+  if (slots > a.count) {
+    const int64_t other = (a.rows + slots - a.count - 1) / (slots - a.count);
+    if (other < least) least = other;
+  }
+  if (rows < least) rows = (least + 15) / 16 * 16;
+  return rows < a.rows ? rows : a.rows;
+}
+
+size_t adapter_packed_bytes(const AdapterArgs& a) {
+  return static_cast<size_t>(most_tiles(a.rows, a.count, 16)) * rank_tiles(a.rank) * 32 * sizeof(uint4);
+}
+
+cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
+                                cudaStream_t stream) {
+  set_error_site("adapter_pack_kernel");
+  const int blocks = static_cast<int>(most_tiles(a.rows, a.count, 16));
+  const PackArgs pa = {da.low, nullptr, static_cast<uint4*>(da.packed)};
+  const PackArgs pb = {db.low, a.scale, static_cast<uint4*>(db.packed)};
+  const int both = da.packed != nullptr ? 2 : 1;
+  const dim3 grid(static_cast<unsigned>((both * int64_t(blocks) + kPackWarps - 1) / kPackWarps));
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    return launch_kernel(adapter_pack_kernel<decltype(ranks)::value>, grid, dim3(32 * kPackWarps), 0, stream,
+                         1, false, pb, pa, route_of(a), a.rank, blocks);
+  });
+}
+
+cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
+                                  const DeviceInfo& dev, cudaStream_t stream) {
+  set_error_site("adapter_weight_kernel");
+  return with_rank_tiles(a.rank, [&](auto ranks) {
+    constexpr int kRankTiles = decltype(ranks)::value;
+    constexpr int kSlab = WeightShape<kRankTiles>::kSlab;
+    auto job = [&](const AdapterWeight& j, bool is_da) {
+      WeightArgs p = {};
+      if (j.dw == nullptr) return p;
+      p.x = j.x;
+      p.ldx = j.ldx;
+      p.low = j.low;
+      p.scale = is_da ? nullptr : a.scale;
+      p.dw = j.dw;
+      p.partials = j.partials;
+      p.cols = static_cast<int>(is_da ? a.k : a.n);
+      p.rank = a.rank;
+      p.tile_rows = static_cast<int>(j.tile_rows);
+      p.packed = static_cast<const uint4*>(j.packed);
+      p.tiles = static_cast<int>(most_tiles(a.rows, a.count, j.tile_rows));
+      p.slabs = (p.cols + kSlab - 1) / kSlab;
+      p.along = !is_da;
+      p.aligned = rows_aligned(j.x, j.ldx, p.cols);
+      p.dw_aligned = is_da && aligned16(j.dw) && p.cols % 8 == 0;
+      return p;
+    };
+    const WeightArgs b = job(db, false), c = job(da, true);
+    const dim3 grid(static_cast<unsigned>(int64_t(b.tiles) * b.slabs + int64_t(c.tiles) * c.slabs));
+    using S = WeightShape<kRankTiles>;
+    return launch_staged<adapter_weight_kernel<kRankTiles>>(
+        grid, Stages<S::kStages, 2 * S::kChunks, S::kShared, true>::kBytes, dev, stream, 1, b, c, route_of(a));
+  });
+}
+
+cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
+                               cudaStream_t stream) {
+  set_error_site("adapter_sum_kernel");
+  auto job = [&](const AdapterWeight& j, int64_t cols) {
+    SumArgs s = {};
+    s.dw = j.dw;
+    s.partials = j.partials;
+    s.size = cols * a.rank;
+    s.tile_rows = static_cast<int>(j.tile_rows);
+    s.route = route_of(a);
+    return s;
+  };
+  const SumArgs sa = job(da, a.k), sb = job(db, a.n);
+  auto blocks = [&](const SumArgs& s) {
+    if (s.dw == nullptr) return 0;
+    const int64_t n = (s.size + kSumThreads - 1) / kSumThreads;
+    return static_cast<int>(n < 1024 ? n : 1024);
+  };
+  const int na = blocks(sa), nb = blocks(sb);
+  return launch_kernel(adapter_sum_kernel, dim3(static_cast<unsigned>(na + nb), static_cast<unsigned>(a.count)),
+                       dim3(kSumThreads), 0, stream, 1, false, sa, sb, na);
+}
+
+}  // namespace fp8lin

@@ -1927,7 +1927,7 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
   }
   {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_weight(a, wb, wa, stream);
+    e = launch_adapter_weight(a, wb, wa, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   ProfScope ps(FP8LIN_PROF_GEMM, stream);

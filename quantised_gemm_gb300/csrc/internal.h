@@ -516,7 +516,7 @@ cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, c
                                 cudaStream_t stream);
 int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev);
 cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                  cudaStream_t stream);
+                                  const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
                                cudaStream_t stream);
 

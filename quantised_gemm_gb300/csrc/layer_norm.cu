@@ -289,15 +289,6 @@ struct Ahead {
   static constexpr size_t kBytes = kRows * kRowBytes;
 };
 
-__device__ __forceinline__ void copy_ahead(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // What lies past the row's end needs no care: x, dy and w are loaded as 0 there,
 // so g and dy are 0 and add nothing to any sum, and dx is not stored.
 template <int kThreads, int kVecs, bool kAligned, bool kResidual, typename P>
@@ -333,7 +324,7 @@ __global__ void __launch_bounds__(Group<kThreads>::kBlock)
 #pragma unroll
           for (int k = 0; k < kVecs; ++k) {
             const int c = (k * kThreads + t) * 8;
-            if (c < p.cols) copy_ahead(slot(stage, i, k), from[i] + row * ld[i] + c);
+            if (c < p.cols) copy16(slot(stage, i, k), from[i] + row * ld[i] + c, true);
           }
       }
       copies_end();

@@ -100,6 +100,21 @@ __device__ __forceinline__ uint32_t load1_if(const void* p, bool on) {
   return v;
 }
 
+// Copies of 16 bytes to shared memory that are on their way while the thread goes
+// on; on = false writes zeros.  Slots that only one thread writes and reads need
+// no barrier but that thread's own wait.  Registers loaded ahead wait for one
+// another where they share one of the warp's few scoreboards; these do not.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The n values at p, the others 0.  kAligned: p is 16-byte aligned and n 0 or 8.
 template <bool kAligned>
 __device__ __forceinline__ uint4 load_values(const uint16_t* p, int n) {
