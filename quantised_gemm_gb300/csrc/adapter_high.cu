@@ -4,7 +4,7 @@
 #include "adapter_kernels.cuh"
 
 #ifndef HIGH_CTAS
-#define HIGH_CTAS 4
+#define HIGH_CTAS 2
 #endif
 namespace fp8lin {
 namespace {
@@ -27,9 +27,13 @@ struct HighArgs {
 template <int kTiles, int kSteps, int kRowWarps, bool kAligned>
 struct HighShape {
   static constexpr int kColWarps = kAdapterWarps / kRowWarps;
-  static constexpr int kShared = kColWarps * 2 * kSteps * 32;
-  static constexpr size_t kStage = sizeof(uint4) * (2 * kTiles * kAdapterThreads + kShared);
-  using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAligned>;
+  // Where the weight is small beside y each warp has its own, and there are no barriers.
+  static constexpr bool kAlone = kSteps == 1 || kRowWarps == 1;
+  static constexpr int kSpans = kAlone ? 1 : kColWarps;
+  static constexpr int kShared = kSpans * 2 * kSteps * 32;
+  static constexpr size_t kStage =
+      sizeof(uint4) * (2 * kTiles * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
+  using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAlone, kAligned>;
 };
 
 __device__ __forceinline__ float2 load_ranks(const float* from, int n, bool aligned) {
@@ -73,26 +77,26 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
   S stages(shared);
   auto copy_base = [&](int turn) {
     const int c = begin + turn * kTurn + 32 * col_warp + 8 * t;
-    stages.copy(turn, [&](int v, int& n) {
+    stages.copy([&](int v, int& n) {
       const int64_t of = row[v >> 1][v & 1];
       n = p.base == nullptr || of < 0 || turn >= turns ? 0 : values_at(c, p.cols);
       return p.base + (of < 0 ? 0 : of) * p.ldbase + c;
     });
   };
   auto copy_w = [&](int turn) {
-    const int c = begin + turn * kTurn;
-    if (turn < turns && !none) {
+    const int c = begin + turn * kTurn + (Shape::kAlone ? 32 * col_warp : 0);
+    if (turn < turns && !none && !(Shape::kAlone && idle)) {
       if constexpr (kAlong)
-        stage_columns<kRankTiles, kColWarps, kWAligned>(stages.shared_of(turn), w, c, p.cols, p.rank);
+        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
       else
-        stage_ranks<kRankTiles, kColWarps, kWAligned>(stages.shared_of(turn), w, c, p.cols, p.rank);
+        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
     }
   };
 #pragma unroll
   for (int i = 0; i < S::kCount - 1; ++i) {
     copy_w(i);
     if (kAligned || i == 0) copy_base(i);
-    copies_end();
+    stages.filled();
   }
   uint32_t hi[kTiles][kSteps][4], lo[kTiles][kSteps][4];  // low of the rows, as an operand
   const float scale = none || p.scale == nullptr ? 1.0f : __ldg(p.scale + tile.group);
@@ -108,17 +112,17 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
           v = load_ranks(p.low + row[m][i & 1] * p.rank + rank, p.rank - rank, p.low_aligned);
         split_pair(v.x * scale, v.y * scale, hi[m][s][i], lo[m][s][i]);
       }
-  for (int turn = 0; turn < turns; ++turn) {
+  for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     uint4 out[2 * kTiles];
-    stages.take(turn, out);
+    stages.take(out);
     copy_w(turn + S::kCount - 1);
     copy_base(kAligned ? turn + S::kCount - 1 : turn + 1);
-    copies_end();
+    stages.filled();
     const int col = begin + turn * kTurn + 32 * col_warp + 8 * t;
     if (idle) continue;
     if (!none) {
-      const uint4* const ws = stages.shared_of(turn) + col_warp * kRankTiles * 32;
+      const uint4* const ws = stages.shared_due() + (Shape::kAlone ? 0 : col_warp * kRankTiles * 32);
       float acc[kTiles][4][4];
 #pragma unroll
       for (int m = 0; m < kTiles; ++m)
@@ -198,11 +202,11 @@ cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float
     auto run = [&](auto tiles, auto row_warps) {
       constexpr int kTiles = decltype(tiles)::value, kRowWarps = decltype(row_warps)::value;
       const int64_t most = most_tiles(a.rows, a.count + 1, 16 * kTiles * kRowWarps);
-      // Slabs of whole turns, and some CTAs an SM.
+      // Slabs of whole turns; one wave of two CTAs an SM, as far as the rows have tiles.
       constexpr int kTurn = 32 * kAdapterWarps / kRowWarps;
       const int turns = (p.cols + kTurn - 1) / kTurn;
-      int64_t slabs = (HIGH_CTAS * int64_t(dev.num_sms) + most - 1) / most;
-      if (slabs > turns) slabs = turns;
+      int64_t slabs = HIGH_CTAS * int64_t(dev.num_sms) / most;
+      slabs = slabs < 1 ? 1 : slabs > turns ? turns : slabs;
       const int per = static_cast<int>((turns + slabs - 1) / slabs);
       p.slab = per * kTurn;
       const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>((turns + per - 1) / per));

@@ -147,47 +147,64 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
 
 constexpr int kAdapterThreads = 256, kAdapterWarps = 8;
 
-// Stages of a turn each: kVecs vectors a thread, its own, and kShared for all.
-// A turn's copies begin kStages - 1 turns before it is due; turn i:
-//   wait(); begin turn i + kStages - 1; read turn i
-// wait() ends with a barrier, after which the stage of turn i - 1 may be filled.
-// Rows that are not 16-byte aligned take registers instead of their own vectors,
-// one turn ahead.
-template <int kStages, int kVecs, int kShared, bool kAligned>
+// Stages of a turn each: kVecs vectors a thread, its own, and kShared for all
+// threads, or (kAlone) that many for each warp.  A turn's copies begin kStages - 1
+// turns before it is due:
+//   fill the stages 0 to kStages - 2;  each turn: wait(), take(), fill the stage that
+//   the turn before left, next()
+// wait() ends with a barrier (of the warp where it is alone), after which that stage
+// may be filled.  Rows that are not 16-byte aligned take registers instead of their
+// own vectors, one turn ahead.
+template <int kStages, int kVecs, int kShared, bool kAlone, bool kAligned>
 struct Stages {
-  static constexpr int kOwn = kAligned ? kVecs * kAdapterThreads : 0, kSize = kOwn + kShared;
+  static constexpr int kOwn = kAligned ? kVecs * kAdapterThreads : 0;
+  static constexpr int kSize = kOwn + (kAlone ? kAdapterWarps : 1) * kShared;
   static constexpr size_t kBytes = sizeof(uint4) * kStages * kSize;
   static constexpr int kCount = kStages;
   uint4* const base;
-  uint4 next[kVecs];
+  int due = 0, filling = 0;  // offsets of stages
+  uint4 next_row[kVecs];
 
   __device__ __forceinline__ explicit Stages(uint4* shared) : base(shared) {}
-  __device__ __forceinline__ uint4* shared_of(int turn) const {
-    return base + turn % kStages * kSize + kOwn;
+  __device__ __forceinline__ static void step(int& stage) {
+    stage = stage == (kStages - 1) * kSize ? 0 : stage + kSize;
   }
-  // The thread's own vectors of a turn: from(vector, n) gives a pointer and how
-  // many values it has.  Unaligned: into registers, called one turn ahead.
+  __device__ __forceinline__ uint4* shared_at(int stage) const {
+    return base + stage + kOwn + (kAlone ? (threadIdx.x >> 5) * kShared : 0);
+  }
+  __device__ __forceinline__ uint4* shared_filling() const { return shared_at(filling); }
+  __device__ __forceinline__ const uint4* shared_due() const { return shared_at(due); }
+  // The thread's own vectors of the turn that is filled (unaligned: of the next
+  // one): from(vector, n) gives a pointer and how many values it has.
   template <typename From>
-  __device__ __forceinline__ void copy(int turn, From from) {
+  __device__ __forceinline__ void copy(From from) {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       int n;
       const uint16_t* p = from(v, n);
       if constexpr (kAligned)
-        copy16(base + turn % kStages * kSize + v * kAdapterThreads + threadIdx.x, p, n > 0);
+        copy16(base + filling + v * kAdapterThreads + threadIdx.x, p, n > 0);
       else
-        next[v] = load_values<false>(p, n);
+        next_row[v] = load_values<false>(p, n);
     }
   }
-  __device__ __forceinline__ void take(int turn, uint4 (&out)[kVecs]) const {
+  __device__ __forceinline__ void filled() {
+    copies_end();
+    step(filling);
+  }
+  __device__ __forceinline__ void take(uint4 (&out)[kVecs]) const {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
-      out[v] = kAligned ? base[turn % kStages * kSize + v * kAdapterThreads + threadIdx.x] : next[v];
+      out[v] = kAligned ? base[due + v * kAdapterThreads + threadIdx.x] : next_row[v];
   }
   __device__ __forceinline__ void wait() const {
     copies_wait<kStages - 2>();
-    __syncthreads();
+    if constexpr (kAlone)
+      __syncwarp();
+    else
+      __syncthreads();
   }
+  __device__ __forceinline__ void next() { step(due); }
 };
 
 // As many stages as `bytes` hold, 2 to 8.
@@ -205,16 +222,16 @@ __device__ __forceinline__ void copy8(void* to, const void* from, bool on) {
                : "memory");
 }
 
-// A stage of a weight whose rows lie along the long side (A, [r, cols]): kSpans
-// times 32 columns from c on, 8 * kRankTiles ranks.  Rank j of span s is at
+// A stage of a weight whose rows lie along the long side (A, [r, cols]), filled by
+// the CTA or (kAlone) by each warp for itself: kSpans times 32 columns from c on, 8 * kRankTiles ranks.  Rank j of span s is at
 // (s * 8 * kRankTiles + j) * 4, four vectors of eight columns.
-template <int kRankTiles, int kSpans, bool kAligned>
+template <int kRankTiles, int kSpans, bool kAlone, bool kAligned>
 __device__ __forceinline__ void stage_ranks(uint4* to, const uint16_t* w, int c, int cols, int rank) {
-  constexpr int kVecs = kSpans * kRankTiles * 32;
+  constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
 #pragma unroll
-  for (int i0 = 0; i0 < kVecs; i0 += kAdapterThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x);
-    if (kVecs % kAdapterThreads != 0 && i >= kVecs) break;
+  for (int i0 = 0; i0 < kVecs; i0 += kThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
+    if (kVecs % kThreads != 0 && i >= kVecs) break;
     const int span = i / (kRankTiles * 32), j = i / 4 % (8 * kRankTiles), col = c + 32 * span + 8 * (i & 3);
     const uint16_t* from = w + int64_t(j < rank ? j : 0) * cols + col;
     if constexpr (kAligned)
@@ -236,13 +253,13 @@ __device__ __forceinline__ int place_vector(int place, int piece) {
   constexpr int kTurns = kRankTiles < 8 ? kRankTiles : 8;
   return place * kRankTiles + (piece ^ ((place & 7) * kTurns / 8));
 }
-template <int kRankTiles, int kSpans, bool kAligned>
+template <int kRankTiles, int kSpans, bool kAlone, bool kAligned>
 __device__ __forceinline__ void stage_columns(uint4* to, const uint16_t* w, int c, int cols, int rank) {
-  constexpr int kVecs = kSpans * kRankTiles * 32;
+  constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
 #pragma unroll
-  for (int i0 = 0; i0 < kVecs; i0 += kAdapterThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x);
-    if (kVecs % kAdapterThreads != 0 && i >= kVecs) break;
+  for (int i0 = 0; i0 < kVecs; i0 += kThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
+    if (kVecs % kThreads != 0 && i >= kVecs) break;
     const int k = i / kRankTiles, piece = i % kRankTiles, col = c + k;
     const int n = col < cols ? values_at(8 * piece, rank) : 0;
     const uint16_t* from = w + int64_t(n > 0 ? col : 0) * rank + (n > 0 ? 8 * piece : 0);

@@ -23,9 +23,13 @@ struct LowArgs {
 template <int kTiles, int kRankTiles, int kRowWarps, bool kAligned>
 struct LowShape {
   static constexpr int kColWarps = kAdapterWarps / kRowWarps;
-  static constexpr int kShared = kColWarps * kRankTiles * 32;
-  static constexpr size_t kStage = sizeof(uint4) * (2 * kTiles * kAdapterThreads + kShared);
-  using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAligned>;
+  // Where the weight is small beside x each warp has its own, and there are no barriers.
+  static constexpr bool kAlone = kRankTiles <= 2 || kRowWarps == 1;
+  static constexpr int kSpans = kAlone ? 1 : kColWarps;
+  static constexpr int kShared = kSpans * kRankTiles * 32;
+  static constexpr size_t kStage =
+      sizeof(uint4) * (2 * kTiles * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
+  using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAlone, kAligned>;
 };
 
 template <int kTiles, int kRankTiles, int kRowWarps, bool kAlong, bool kAligned, bool kWAligned>
@@ -76,35 +80,35 @@ __global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 8 ? 2 : 1)
   S stages(shared);
   auto copy_x = [&](int turn) {
     const int c = first + turn * step + 32 * col_warp;
-    stages.copy(turn, [&](int v, int& n) {
+    stages.copy([&](int v, int& n) {
       n = row[v >> 1][v & 1] < 0 ? 0 : values_at(c + 8 * t, p.cols);
       return from[v >> 1][v & 1] + c;
     });
   };
   auto copy_w = [&](int turn) {
-    const int c = first + turn * step;
-    if (turn < turns) {
+    const int c = first + turn * step + (Shape::kAlone ? 32 * col_warp : 0);
+    if (turn < turns && !(Shape::kAlone && idle)) {
       if constexpr (kAlong)
-        stage_ranks<kRankTiles, kColWarps, kWAligned>(stages.shared_of(turn), w, c, p.cols, p.rank);
+        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
       else
-        stage_columns<kRankTiles, kColWarps, kWAligned>(stages.shared_of(turn), w, c, p.cols, p.rank);
+        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
     }
   };
 #pragma unroll
   for (int i = 0; i < S::kCount - 1; ++i) {
     copy_w(i);
     if (kAligned || i == 0) copy_x(i);
-    copies_end();
+    stages.filled();
   }
-  for (int turn = 0; turn < turns; ++turn) {
+  for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     uint4 x[2 * kTiles];
-    stages.take(turn, x);
+    stages.take(x);
     copy_w(turn + S::kCount - 1);
     copy_x(kAligned ? turn + S::kCount - 1 : turn + 1);
-    copies_end();
+    stages.filled();
     if (idle) continue;
-    const uint4* const ws = stages.shared_of(turn) + col_warp * kRankTiles * 32;
+    const uint4* const ws = stages.shared_due() + (Shape::kAlone ? 0 : col_warp * kRankTiles * 32);
     if constexpr (kAlong) {
 #pragma unroll
       for (int j = 0; j < kRankTiles; ++j) {

@@ -3,6 +3,12 @@
 // dB (x = dy, low = h) and dA (x the input, low = dh, turned) in one launch.
 #include "adapter_kernels.cuh"
 
+#ifndef W_RW
+#define W_RW 4
+#endif
+#ifndef W_CTAS
+#define W_CTAS 3
+#endif
 namespace fp8lin {
 namespace {
 
@@ -28,13 +34,15 @@ struct WeightArgs {
 // leaves fewer partial sums; with a large one warps of the same rows share them.
 template <int kRankTiles>
 struct WeightShape {
-  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
+  static constexpr int kRowWarps = kRankTiles <= 2 ? W_RW : kRankTiles == 4 ? 2 : 1;
   static constexpr int kColWarps = kAdapterWarps / kRowWarps;
   static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
   static constexpr int kSlab = 32 * kChunks * kColWarps;
   static constexpr int kSums = 2 * kChunks * kRankTiles * 4;  // a lane's
-  static constexpr int kShared = kRowWarps * kRankTiles * 32;  // a turn's low operands
-  static constexpr size_t kStage = sizeof(uint4) * (2 * kChunks * kAdapterThreads + kShared);
+  static constexpr bool kAlone = kRankTiles <= 2;  // each warp has its own low operands
+  static constexpr int kShared = (kAlone ? 1 : kRowWarps) * kRankTiles * 32;  // of a turn
+  static constexpr size_t kStage =
+      sizeof(uint4) * (2 * kChunks * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
   static constexpr int kStages = stages_in(kRankTiles <= 2 ? kStageRoom - 16 * 1024 : kStageRoom, kStage);
 };
 
@@ -108,7 +116,7 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
   // x, the low operands and, one turn more, the row numbers are on their way.
   constexpr int kStep = 16 * S::kRowWarps;
   const int turns = (tile.count + kStep - 1) / kStep;
-  using T = Stages<S::kStages, 2 * kChunks, S::kShared, kAligned>;
+  using T = Stages<S::kStages, 2 * kChunks, S::kShared, S::kAlone, kAligned>;
   T stages(shared);
   constexpr int kBefore = kAligned ? T::kCount - 1 : 1;
   int number[2];
@@ -119,20 +127,22 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
       number[i] = of < tile.count ? __ldg(rows + of) : -1;
     }
   };
-  auto copy_x = [&](int turn) {
-    stages.copy(turn, [&](int v, int& n) {
+  auto copy_x = [&]() {
+    stages.copy([&](int v, int& n) {
       const int col = col0 + 32 * (v >> 1) + 8 * t, row = number[v & 1];
       n = row < 0 ? 0 : values_at(col, p.cols);
       return p.x + (row < 0 ? 0 : row) * p.ldx + (n > 0 ? col : 0);
     });
   };
   auto copy_low = [&](int turn) {
-    uint4* const to = stages.shared_of(turn);
+    uint4* const to = stages.shared_filling();
+    constexpr int kThreads = S::kAlone ? 32 : kAdapterThreads;
 #pragma unroll
-    for (int i0 = 0; i0 < S::kShared; i0 += kAdapterThreads) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      if (S::kShared % kAdapterThreads != 0 && i >= S::kShared) break;
-      const int r = turn * kStep + 16 * (i / (kRankTiles * 32));  // the block's first row
+    for (int i0 = 0; i0 < S::kShared; i0 += kThreads) {
+      const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
+      if (S::kShared % kThreads != 0 && i >= S::kShared) break;
+      const int block = S::kAlone ? row_warp : i / (kRankTiles * 32);
+      const int r = turn * kStep + 16 * block;  // the block's first row
       if (p.packed != nullptr) {
         const bool on = r < tile.count;
         copy16(to + i, p.packed + (on ? int64_t(tile.block + r / 16) * (kRankTiles * 32) + i % (kRankTiles * 32) : 0), on);
@@ -153,20 +163,20 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
     if (i < turns) copy_low(i);
     if (kAligned || i == 0) {
       find(i);
-      copy_x(i);
+      copy_x();
     }
-    copies_end();
+    stages.filled();
   }
   find(kBefore);
-  for (int turn = 0; turn < turns; ++turn) {
+  for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     uint4 x[2 * kChunks];
-    stages.take(turn, x);
+    stages.take(x);
     if (turn + T::kCount - 1 < turns) copy_low(turn + T::kCount - 1);
-    copy_x(turn + kBefore);
-    copies_end();
+    copy_x();
+    stages.filled();
     find(turn + kBefore + 1);
-    const uint4* const operand = stages.shared_of(turn) + row_warp * kRankTiles * 32 + lane;
+    const uint4* const operand = stages.shared_due() + (S::kAlone ? 0 : row_warp * kRankTiles * 32) + lane;
     uint32_t a[kChunks][4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
@@ -345,7 +355,7 @@ int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes,
   });
   const int64_t slabs = (cols + slab - 1) / slab;
   // Three CTAs an SM, tiles of 128 rows at least.
-  int64_t rows = (a.rows * slabs + 3 * dev.num_sms - 1) / (3 * dev.num_sms);
+  int64_t rows = (a.rows * slabs + W_CTAS * dev.num_sms - 1) / (W_CTAS * dev.num_sms);
   rows = (rows + 127) / 128 * 128;
   // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
   // them, and at most a.rows / rows and one for each adapter.
@@ -408,7 +418,7 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
     const dim3 grid(static_cast<unsigned>(int64_t(b.tiles) * b.slabs + int64_t(c.tiles) * c.slabs));
     using S = WeightShape<kRankTiles>;
     return launch_staged<adapter_weight_kernel<kRankTiles>>(
-        grid, Stages<S::kStages, 2 * S::kChunks, S::kShared, true>::kBytes, dev, stream, 1, b, c, route_of(a));
+        grid, Stages<S::kStages, 2 * S::kChunks, S::kShared, S::kAlone, true>::kBytes, dev, stream, 1, b, c, route_of(a));
   });
 }
 
