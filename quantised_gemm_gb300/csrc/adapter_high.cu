@@ -32,7 +32,7 @@ struct HighShape {
   static constexpr int kSpans = kAlone ? 1 : kColWarps;
   static constexpr int kShared = kSpans * 2 * kSteps * 32;
   static constexpr size_t kStage =
-      sizeof(uint4) * (2 * kTiles * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
+      sizeof(uint4) * ((kAligned ? 2 : 4) * kTiles * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
   using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAlone, kAligned>;
 };
 
@@ -63,7 +63,10 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
   if (none && p.y == p.base) return;
   const int begin = static_cast<int>(blockIdx.y) * p.slab;
   const int end = min(begin + p.slab, p.cols);
-  const int turns = (end - begin + kTurn - 1) / kTurn;
+  // A warp's turns: every kColWarps-th 32 columns, or, where rows of y are not
+  // aligned, 32 after 32, so that what a turn leaves of a vector the next one writes.
+  const int span = kAligned ? 32 : p.slab / kColWarps, apart = kAligned ? kTurn : 32;
+  const int turns = kAligned ? (end - begin + kTurn - 1) / kTurn : min(span, end - begin + 31) / 32;
   int64_t row[kTiles][2];
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
@@ -75,27 +78,27 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
   const bool idle = row_warp * kTiles * 16 >= tile.count;
   const uint16_t* const w = none ? nullptr : p.w + int64_t(tile.group) * p.rank * p.cols;
   S stages(shared);
-  auto copy_base = [&](int turn) {
-    const int c = begin + turn * kTurn + 32 * col_warp + 8 * t;
-    stages.copy([&](int v, int& n) {
+  const int begin_warp = begin + span * col_warp, end_warp = kAligned ? end : min(begin_warp + span, end);
+  auto base_of = [&](int turn) {
+    return [&, c = begin_warp + turn * apart + 8 * t](int v, int& n) {
       const int64_t of = row[v >> 1][v & 1];
-      n = p.base == nullptr || of < 0 || turn >= turns ? 0 : values_at(c, p.cols);
+      n = p.base == nullptr || of < 0 || turn >= turns ? 0 : values_at(c, end_warp);
       return p.base + (of < 0 ? 0 : of) * p.ldbase + c;
-    });
+    };
   };
   auto copy_w = [&](int turn) {
-    const int c = begin + turn * kTurn + (Shape::kAlone ? 32 * col_warp : 0);
+    const int c = (Shape::kAlone ? begin_warp : begin) + turn * apart;
     if (turn < turns && !none && !(Shape::kAlone && idle)) {
       if constexpr (kAlong)
-        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
+        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, span, p.cols, p.rank);
       else
-        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
+        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, span, p.cols, p.rank);
     }
   };
 #pragma unroll
   for (int i = 0; i < S::kCount - 1; ++i) {
     copy_w(i);
-    if (kAligned || i == 0) copy_base(i);
+    stages.copy(base_of(i));
     stages.filled();
   }
   uint32_t hi[kTiles][kSteps][4], lo[kTiles][kSteps][4];  // low of the rows, as an operand
@@ -112,14 +115,15 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
           v = load_ranks(p.low + row[m][i & 1] * p.rank + rank, p.rank - rank, p.low_aligned);
         split_pair(v.x * scale, v.y * scale, hi[m][s][i], lo[m][s][i]);
       }
+  StoreRun<4> runs[kAligned ? 1 : 2 * kTiles];
   for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     uint4 out[2 * kTiles];
-    stages.take(out);
+    stages.take(out, base_of(turn));
     copy_w(turn + S::kCount - 1);
-    copy_base(kAligned ? turn + S::kCount - 1 : turn + 1);
+    stages.copy(base_of(turn + S::kCount - 1));
     stages.filled();
-    const int col = begin + turn * kTurn + 32 * col_warp + 8 * t;
+    const int col = begin_warp + turn * apart + 8 * t;
     if (idle) continue;
     if (!none) {
       const uint4* const ws = stages.shared_due() + (Shape::kAlone ? 0 : col_warp * kRankTiles * 32);
@@ -167,12 +171,21 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
           out[2 * m + i] = f32_to_bf16x8(v);
         }
     }
-    const int n = values_at(col, p.cols);
+    const int n = values_at(col, end_warp);
 #pragma unroll
     for (int v = 0; v < 2 * kTiles; ++v) {
       const int64_t of = row[v >> 1][v & 1];
-      store_values<kAligned, 4>(p.y + (of < 0 ? 0 : of) * p.ldy + col, out[v], of < 0 ? 0 : n);
+      uint16_t* const to = p.y + (of < 0 ? 0 : of) * p.ldy + col;
+      if constexpr (kAligned) {
+        if (of >= 0 && n > 0) *reinterpret_cast<uint4*>(to) = out[v];
+      } else {
+        runs[v].store(to, out[v], of < 0 ? 0 : n);
+      }
     }
+  }
+  if constexpr (!kAligned) {
+#pragma unroll
+    for (int v = 0; v < 2 * kTiles; ++v) runs[v].end();
   }
   copies_wait<0>();
 }

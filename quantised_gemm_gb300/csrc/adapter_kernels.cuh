@@ -153,17 +153,17 @@ constexpr int kAdapterThreads = 256, kAdapterWarps = 8;
 //   fill the stages 0 to kStages - 2;  each turn: wait(), take(), fill the stage that
 //   the turn before left, next()
 // wait() ends with a barrier (of the warp where it is alone), after which that stage
-// may be filled.  Rows that are not 16-byte aligned take registers instead of their
-// own vectors, one turn ahead.
+// may be filled.  Where rows are not 16-byte aligned a vector is two, those that its
+// values lie in.
 template <int kStages, int kVecs, int kShared, bool kAlone, bool kAligned>
 struct Stages {
-  static constexpr int kOwn = kAligned ? kVecs * kAdapterThreads : 0;
+  static constexpr int kEach = kAligned ? 1 : 2;
+  static constexpr int kOwn = kEach * kVecs * kAdapterThreads;
   static constexpr int kSize = kOwn + (kAlone ? kAdapterWarps : 1) * kShared;
   static constexpr size_t kBytes = sizeof(uint4) * kStages * kSize;
   static constexpr int kCount = kStages;
   uint4* const base;
   int due = 0, filling = 0;  // offsets of stages
-  uint4 next_row[kVecs];
 
   __device__ __forceinline__ explicit Stages(uint4* shared) : base(shared) {}
   __device__ __forceinline__ static void step(int& stage) {
@@ -174,28 +174,43 @@ struct Stages {
   }
   __device__ __forceinline__ uint4* shared_filling() const { return shared_at(filling); }
   __device__ __forceinline__ const uint4* shared_due() const { return shared_at(due); }
-  // The thread's own vectors of the turn that is filled (unaligned: of the next
-  // one): from(vector, n) gives a pointer and how many values it has.
+  // The thread's own vectors of the turn that is filled: from(vector, n) gives a
+  // pointer and how many values it has.
   template <typename From>
   __device__ __forceinline__ void copy(From from) {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       int n;
       const uint16_t* p = from(v, n);
-      if constexpr (kAligned)
-        copy16(base + filling + v * kAdapterThreads + threadIdx.x, p, n > 0);
-      else
-        next_row[v] = load_values<false>(p, n);
+      uint4* const to = base + filling + kEach * v * kAdapterThreads + threadIdx.x;
+      if constexpr (kAligned) {
+        copy16(to, p, n > 0);
+      } else {
+        const int off = offset(p);
+        copy16(to, p - off, n > 0);
+        copy16(to + kAdapterThreads, p - off + 8, n > 0 && off + n > 8);
+      }
     }
   }
   __device__ __forceinline__ void filled() {
     copies_end();
     step(filling);
   }
-  __device__ __forceinline__ void take(uint4 (&out)[kVecs]) const {
+  // The vectors of the turn that is due, with the same from().
+  template <typename From>
+  __device__ __forceinline__ void take(uint4 (&out)[kVecs], From from) const {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-      out[v] = kAligned ? base[due + v * kAdapterThreads + threadIdx.x] : next_row[v];
+    for (int v = 0; v < kVecs; ++v) {
+      const uint4* const at = base + due + kEach * v * kAdapterThreads + threadIdx.x;
+      if constexpr (kAligned) {
+        out[v] = at[0];
+      } else {
+        int n;
+        const uint16_t* p = from(v, n);
+        out[v] = shift_values(at[0], at[kAdapterThreads], static_cast<uint32_t>(offset(p)));
+        if (n < 8) out[v] = first_values(out[v], n);
+      }
+    }
   }
   __device__ __forceinline__ void wait() const {
     copies_wait<kStages - 2>();
@@ -205,6 +220,12 @@ struct Stages {
       __syncthreads();
   }
   __device__ __forceinline__ void next() { step(due); }
+
+ private:
+  // Values between a pointer and the 16-byte boundary before it.
+  __device__ __forceinline__ static int offset(const uint16_t* p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+  }
 };
 
 // As many stages as `bytes` hold, 2 to 8.
@@ -223,16 +244,17 @@ __device__ __forceinline__ void copy8(void* to, const void* from, bool on) {
 }
 
 // A stage of a weight whose rows lie along the long side (A, [r, cols]), filled by
-// the CTA or (kAlone) by each warp for itself: kSpans times 32 columns from c on, 8 * kRankTiles ranks.  Rank j of span s is at
+// the CTA or (kAlone) by each warp for itself: kSpans times 32 columns, `apart` apart,
+// from c on, 8 * kRankTiles ranks.  Rank j of span s is at
 // (s * 8 * kRankTiles + j) * 4, four vectors of eight columns.
 template <int kRankTiles, int kSpans, bool kAlone, bool kAligned>
-__device__ __forceinline__ void stage_ranks(uint4* to, const uint16_t* w, int c, int cols, int rank) {
+__device__ __forceinline__ void stage_ranks(uint4* to, const uint16_t* w, int c, int apart, int cols, int rank) {
   constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
 #pragma unroll
   for (int i0 = 0; i0 < kVecs; i0 += kThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
     if (kVecs % kThreads != 0 && i >= kVecs) break;
-    const int span = i / (kRankTiles * 32), j = i / 4 % (8 * kRankTiles), col = c + 32 * span + 8 * (i & 3);
+    const int span = i / (kRankTiles * 32), j = i / 4 % (8 * kRankTiles), col = c + apart * span + 8 * (i & 3);
     const uint16_t* from = w + int64_t(j < rank ? j : 0) * cols + col;
     if constexpr (kAligned)
       copy16(to + i, from, j < rank && col < cols);
@@ -254,13 +276,13 @@ __device__ __forceinline__ int place_vector(int place, int piece) {
   return place * kRankTiles + (piece ^ ((place & 7) * kTurns / 8));
 }
 template <int kRankTiles, int kSpans, bool kAlone, bool kAligned>
-__device__ __forceinline__ void stage_columns(uint4* to, const uint16_t* w, int c, int cols, int rank) {
+__device__ __forceinline__ void stage_columns(uint4* to, const uint16_t* w, int c, int apart, int cols, int rank) {
   constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
 #pragma unroll
   for (int i0 = 0; i0 < kVecs; i0 += kThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
     if (kVecs % kThreads != 0 && i >= kVecs) break;
-    const int k = i / kRankTiles, piece = i % kRankTiles, col = c + k;
+    const int k = i / kRankTiles, piece = i % kRankTiles, col = c + (k >> 5) * apart + (k & 31);
     const int n = col < cols ? values_at(8 * piece, rank) : 0;
     const uint16_t* from = w + int64_t(n > 0 ? col : 0) * rank + (n > 0 ? 8 * piece : 0);
     uint4* put = to + place_vector<kRankTiles>(column_place(k), piece);

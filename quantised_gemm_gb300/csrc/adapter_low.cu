@@ -28,7 +28,7 @@ struct LowShape {
   static constexpr int kSpans = kAlone ? 1 : kColWarps;
   static constexpr int kShared = kSpans * kRankTiles * 32;
   static constexpr size_t kStage =
-      sizeof(uint4) * (2 * kTiles * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
+      sizeof(uint4) * ((kAligned ? 2 : 4) * kTiles * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
   using S = Stages<stages_in(kStageRoom, kStage), 2 * kTiles, kShared, kAlone, kAligned>;
 };
 
@@ -78,34 +78,33 @@ __global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 8 ? 2 : 1)
   const int first = 32 * kColWarps * part, step = 32 * kColWarps * parts;
   const int turns = first < p.cols ? (p.cols - first + step - 1) / step : 0;
   S stages(shared);
-  auto copy_x = [&](int turn) {
-    const int c = first + turn * step + 32 * col_warp;
-    stages.copy([&](int v, int& n) {
+  auto x_of = [&](int turn) {
+    return [&, c = first + turn * step + 32 * col_warp](int v, int& n) {
       n = row[v >> 1][v & 1] < 0 ? 0 : values_at(c + 8 * t, p.cols);
       return from[v >> 1][v & 1] + c;
-    });
+    };
   };
   auto copy_w = [&](int turn) {
     const int c = first + turn * step + (Shape::kAlone ? 32 * col_warp : 0);
     if (turn < turns && !(Shape::kAlone && idle)) {
       if constexpr (kAlong)
-        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
+        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, 32, p.cols, p.rank);
       else
-        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, p.cols, p.rank);
+        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, 32, p.cols, p.rank);
     }
   };
 #pragma unroll
   for (int i = 0; i < S::kCount - 1; ++i) {
     copy_w(i);
-    if (kAligned || i == 0) copy_x(i);
+    stages.copy(x_of(i));
     stages.filled();
   }
   for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     uint4 x[2 * kTiles];
-    stages.take(x);
+    stages.take(x, x_of(turn));
     copy_w(turn + S::kCount - 1);
-    copy_x(kAligned ? turn + S::kCount - 1 : turn + 1);
+    stages.copy(x_of(turn + S::kCount - 1));
     stages.filled();
     if (idle) continue;
     const uint4* const ws = stages.shared_due() + (Shape::kAlone ? 0 : col_warp * kRankTiles * 32);

@@ -41,9 +41,11 @@ struct WeightShape {
   static constexpr int kSums = 2 * kChunks * kRankTiles * 4;  // a lane's
   static constexpr bool kAlone = kRankTiles <= 2;  // each warp has its own low operands
   static constexpr int kShared = (kAlone ? 1 : kRowWarps) * kRankTiles * 32;  // of a turn
-  static constexpr size_t kStage =
-      sizeof(uint4) * (2 * kChunks * kAdapterThreads + (kAlone ? kAdapterWarps : 1) * kShared);
-  static constexpr int kStages = stages_in(kRankTiles <= 2 ? kStageRoom - 16 * 1024 : kStageRoom, kStage);
+  template <bool kAligned>
+  using T = Stages<stages_in(kAlone ? kStageRoom - 16 * 1024 : kStageRoom,
+                             sizeof(uint4) * ((kAligned ? 2 : 4) * kChunks * kAdapterThreads +
+                                              (kAlone ? kAdapterWarps : 1) * kShared)),
+                   2 * kChunks, kShared, kAlone, kAligned>;
 };
 
 // What a lane needs of rank tile j of 16 rows of low: rows 2 t, 2 t + 1 and 2 t + 8,
@@ -116,23 +118,24 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
   // x, the low operands and, one turn more, the row numbers are on their way.
   constexpr int kStep = 16 * S::kRowWarps;
   const int turns = (tile.count + kStep - 1) / kStep;
-  using T = Stages<S::kStages, 2 * kChunks, S::kShared, S::kAlone, kAligned>;
+  using T = typename S::template T<kAligned>;
   T stages(shared);
-  constexpr int kBefore = kAligned ? T::kCount - 1 : 1;
+  constexpr int kBefore = T::kCount - 1;
   int number[2];
-  auto find = [&](int turn) {
+  auto find = [&](int (&to)[2], int turn) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int of = turn * kStep + 16 * row_warp + 8 * i + g;
-      number[i] = of < tile.count ? __ldg(rows + of) : -1;
+      to[i] = of < tile.count ? __ldg(rows + of) : -1;
     }
   };
-  auto copy_x = [&]() {
-    stages.copy([&](int v, int& n) {
-      const int col = col0 + 32 * (v >> 1) + 8 * t, row = number[v & 1];
+  // The rows of the turn that is due are needed again where they are not aligned.
+  auto x_of = [&](const int (&of)[2]) {
+    return [&](int v, int& n) {
+      const int col = col0 + 32 * (v >> 1) + 8 * t, row = of[v & 1];
       n = row < 0 ? 0 : values_at(col, p.cols);
       return p.x + (row < 0 ? 0 : row) * p.ldx + (n > 0 ? col : 0);
-    });
+    };
   };
   auto copy_low = [&](int turn) {
     uint4* const to = stages.shared_filling();
@@ -161,21 +164,21 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
 #pragma unroll
   for (int i = 0; i < T::kCount - 1; ++i) {
     if (i < turns) copy_low(i);
-    if (kAligned || i == 0) {
-      find(i);
-      copy_x();
-    }
+    find(number, i);
+    stages.copy(x_of(number));
     stages.filled();
   }
-  find(kBefore);
+  find(number, kBefore);
   for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     uint4 x[2 * kChunks];
-    stages.take(x);
-    if (turn + T::kCount - 1 < turns) copy_low(turn + T::kCount - 1);
-    copy_x();
+    int due[2] = {0, 0};
+    if constexpr (!kAligned) find(due, turn);
+    stages.take(x, x_of(due));
+    if (turn + kBefore < turns) copy_low(turn + kBefore);
+    stages.copy(x_of(number));
     stages.filled();
-    find(turn + kBefore + 1);
+    find(number, turn + kBefore + 1);
     const uint4* const operand = stages.shared_due() + (S::kAlone ? 0 : row_warp * kRankTiles * 32) + lane;
     uint32_t a[kChunks][4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
 #pragma unroll
@@ -417,8 +420,9 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
     const WeightArgs b = job(db, false), c = job(da, true);
     const dim3 grid(static_cast<unsigned>(int64_t(b.tiles) * b.slabs + int64_t(c.tiles) * c.slabs));
     using S = WeightShape<kRankTiles>;
-    return launch_staged<adapter_weight_kernel<kRankTiles>>(
-        grid, Stages<S::kStages, 2 * S::kChunks, S::kShared, S::kAlone, true>::kBytes, dev, stream, 1, b, c, route_of(a));
+    constexpr size_t kA = S::template T<true>::kBytes, kB = S::template T<false>::kBytes;
+    return launch_staged<adapter_weight_kernel<kRankTiles>>(grid, kA > kB ? kA : kB, dev, stream, 1, b, c,
+                                                            route_of(a));
   });
 }
 

@@ -167,6 +167,48 @@ __device__ __forceinline__ void store_values(uint16_t* p, const uint4& u, int n)
   }
 }
 
+// As store_values for unaligned rows whose spans follow one another: a span's first
+// lane also has the last values of the call before, and the last lane's stay in the
+// run until the next call or end().  n values a lane, 8 but at a row's end.
+template <int kSpan>
+struct StoreRun {
+  uint4 kept = make_uint4(0, 0, 0, 0);
+  int n_kept = 0;
+  uint16_t* last = nullptr;
+
+  __device__ __forceinline__ void store(uint16_t* p, const uint4& u, int n) {
+    const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
+    const int lane = static_cast<int>(threadIdx.x) & (kSpan - 1);
+    // The lane before, or for the first one the last one's values of before.
+    const bool give = lane == kSpan - 1;
+    const int from = lane == 0 ? kSpan - 1 : lane - 1;
+    const uint4 mine = give ? kept : u;
+    uint4 before;
+    before.x = __shfl_sync(0xFFFFFFFFu, mine.x, from, kSpan);
+    before.y = __shfl_sync(0xFFFFFFFFu, mine.y, from, kSpan);
+    before.z = __shfl_sync(0xFFFFFFFFu, mine.z, from, kSpan);
+    before.w = __shfl_sync(0xFFFFFFFFu, mine.w, from, kSpan);
+    const int n_before = __shfl_sync(0xFFFFFFFFu, give ? n_kept : n, from, kSpan);
+    const int own = 8 - static_cast<int>(off);
+    if (off == 0 && n == 8) {
+      *reinterpret_cast<uint4*>(p) = u;
+    } else if (off != 0 && n_before == 8 && n >= own) {
+      *reinterpret_cast<uint4*>(p - off) = shift_values(before, u, own);
+    } else {
+      for (int i = 0; i < own && i < n; ++i) p[i] = value_of(u, i);
+      for (int i = own; i < n_before; ++i) p[i - 8] = value_of(before, i);
+    }
+    kept = u;
+    n_kept = n;
+    last = p;
+  }
+  __device__ __forceinline__ void end() const {
+    if ((static_cast<int>(threadIdx.x) & (kSpan - 1)) != kSpan - 1 || last == nullptr) return;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(last) & 15u) >> 1);
+    for (int i = 8 - off; i < n_kept; ++i) last[i] = value_of(kept, i);
+  }
+};
+
 // Eight parameters (bf16 or fp32) from p on, n of them in the tensor.
 template <typename P>
 __device__ __forceinline__ void load_params(const P* p, int n, float (&v)[8]) {
