@@ -17,17 +17,10 @@ import ctypes
 import torch
 
 from . import _lib
-from . import Workspace, _dev, _stream
-from .fp4 import _matrix
-from .norm import _here, _rows_like
+from . import Workspace, _stream
+from .norm import _current_device, _on, _rows, _rows_like, _whole
 
 _load = _lib.load
-
-
-def _whole(t: torch.Tensor, name: str, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be contiguous %s" % (name, list(shape)))
-    return _dev(t, name, dtype)
 
 
 class Adapters:
@@ -42,9 +35,12 @@ class Adapters:
         count, rank, k = a.shape
         n = b.shape[1]
         c = _lib.AdaptersC()
-        c.a = _whole(a, "a", (count, rank, k), torch.bfloat16)
-        c.b = _whole(b, "b", (count, n, rank), torch.bfloat16)
-        c.scale = _whole(scale, "scale", (count,), torch.float32)
+        self.device = a.get_device()
+        c.a = _whole(a, "a", (count, rank, k), torch.bfloat16, self.device)
+        c.b = _whole(b, "b", (count, n, rank), torch.bfloat16, self.device)
+        c.scale = _whole(scale, "scale", (count,), torch.float32, self.device)
+        if self.device < 0:
+            raise ValueError("a, b and scale must be CUDA tensors")
         if not (1 <= count <= 1024 and 1 <= rank <= 128 and k >= 1 and n >= 1):
             raise ValueError("1 to 1024 adapters of rank 1 to 128 expected, and K and N of at least 1")
         self._a, self._b, self._scale = a, b, scale
@@ -80,20 +76,16 @@ class AdapterRoute:
         self._set = False
 
     def set(self, index: torch.Tensor, stream=None) -> AdapterRoute:
-        _here(index, self.buf)
+        dev = _current_device()
         self._set = False
-        st = _load().fp8lin_adapter_route(_index(index, self.rows), self.rows, self.count,
-                                          self.buf.data_ptr(), _stream(stream))
+        st = _load().fp8lin_adapter_route(_whole(index, "index", (self.rows,), torch.int32, dev), self.rows,
+                                          self.count, _on(self.buf, "the route", dev), _stream(stream))
         _lib.check(st, "fp8lin_adapter_route")
         self._set = True
         return self
 
 
-def _index(index: torch.Tensor, rows: int):
-    return _whole(index, "index", (rows,), torch.int32)
-
-
-def _route(route: AdapterRoute | None, rows: int, bank: Adapters):
+def _route(route: AdapterRoute | None, rows: int, bank: Adapters, dev: int):
     if route is None:
         return None
     if (route.rows, route.count) != (rows, bank.count):
@@ -101,7 +93,33 @@ def _route(route: AdapterRoute | None, rows: int, bank: Adapters):
                          % (route.rows, route.count, rows, bank.count))
     if not route._set:
         raise ValueError("the route has no index yet")
-    return route.buf.data_ptr()
+    return _on(route.buf, "the route", dev)
+
+
+def _bank(bank: Adapters, dev: int):
+    if bank.device != dev:
+        raise ValueError("the adapters are on cuda:%d, but the current device is cuda:%d"
+                         % (bank.device, dev))
+    return bank._ref
+
+
+def _linear_args(x, index, bank, y, h, ws, base, route, stream):
+    dev = _current_device()
+    px, rows, k, ldx = _rows(x, "x", dev)
+    if ws is None:
+        raise ValueError("a Workspace is required")
+    if k != bank.K:
+        raise ValueError("x must be [M, %d]" % bank.K)
+    py, ldy = _rows_like(y, "y", rows, bank.N, dev)
+    pb, ldb = _rows_like(base, "base", rows, bank.N, dev)
+    return (_bank(bank, dev), px, ldx, _whole(index, "index", (rows,), torch.int32, dev),
+            _route(route, rows, bank, dev), rows, pb, ldb, py, ldy,
+            _whole(h, "h", (rows, bank.rank), torch.float32, dev), _on(ws.buf, "ws", dev), ws.nbytes,
+            _stream(stream))
+
+
+def _linear(args):
+    _lib.check(_load().fp8lin_adapter_linear(*args), "fp8lin_adapter_linear")
 
 
 def adapter_linear(x: torch.Tensor, index: torch.Tensor, bank: Adapters, y: torch.Tensor,
@@ -111,19 +129,7 @@ def adapter_linear(x: torch.Tensor, index: torch.Tensor, bank: Adapters, y: torc
     number outside [0, count) for a row without an adapter; base: bf16 [M, N] or
     None for zeros, and may be y; h (fp32 [M, rank]) receives A x, for the
     backward.  route: index sorted before, where several calls share it."""
-    px, rows, k, ldx = _matrix(x, "x")
-    if ws is None:
-        raise ValueError("a Workspace is required")
-    if k != bank.K:
-        raise ValueError("x must be [M, %d]" % bank.K)
-    _here(x, index, bank.a, y, h, base, ws.buf, None if route is None else route.buf)
-    py, ldy = _rows_like(y, "y", rows, bank.N)
-    pb, ldb = _rows_like(base, "base", rows, bank.N)
-    st = _load().fp8lin_adapter_linear(bank._ref, px, ldx, _index(index, rows), _route(route, rows, bank),
-                                       rows, pb, ldb, py, ldy,
-                                       _whole(h, "h", (rows, bank.rank), torch.float32), ws.ptr,
-                                       ws.nbytes, _stream(stream))
-    _lib.check(st, "fp8lin_adapter_linear")
+    _linear(_linear_args(x, index, bank, y, h, ws, base, route, stream))
     return y
 
 
@@ -136,24 +142,23 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor | None, h: torch.Tensor |
     for adapters that no row has), from the forward's x and h; each of the three
     may be None, x is needed for da only and h for db.  dh: fp32 [M, rank]
     receives s B^T dy.  base may be dx."""
-    pdy, rows, n, lddy = _matrix(dy, "dy")
+    dev = _current_device()
+    pdy, rows, n, lddy = _rows(dy, "dy", dev)
     if ws is None:
         raise ValueError("a Workspace is required")
     if n != bank.N:
         raise ValueError("dy must be [M, %d]" % bank.N)
     if (da is not None and x is None) or (db is not None and h is None):
         raise ValueError("da needs x, and db needs h")
-    _here(dy, x, h, index, bank.a, dh, dx, da, db, base, ws.buf, None if route is None else route.buf)
-    px, ldx = _rows_like(x, "x", rows, bank.K)
-    pdx, lddx = _rows_like(dx, "dx", rows, bank.K)
-    pb, ldb = _rows_like(base, "base", rows, bank.K)
-    low = (rows, bank.rank)
+    px, ldx = _rows_like(x, "x", rows, bank.K, dev)
+    pdx, lddx = _rows_like(dx, "dx", rows, bank.K, dev)
+    pb, ldb = _rows_like(base, "base", rows, bank.K, dev)
+    low, f32 = (rows, bank.rank), torch.float32
     st = _load().fp8lin_adapter_backward(
-        bank._ref, pdy, lddy, px, ldx, None if h is None else _whole(h, "h", low, torch.float32),
-        _index(index, rows), _route(route, rows, bank), rows, pb, ldb, pdx, lddx,
-        _whole(dh, "dh", low, torch.float32),
-        None if da is None else _whole(da, "da", bank.a.shape, torch.bfloat16),
-        None if db is None else _whole(db, "db", bank.b.shape, torch.bfloat16), ws.ptr, ws.nbytes,
+        _bank(bank, dev), pdy, lddy, px, ldx, _whole(h, "h", low, f32, dev),
+        _whole(index, "index", (rows,), torch.int32, dev), _route(route, rows, bank, dev), rows, pb, ldb,
+        pdx, lddx, _whole(dh, "dh", low, f32, dev), _whole(da, "da", bank.a.shape, torch.bfloat16, dev),
+        _whole(db, "db", bank.b.shape, torch.bfloat16, dev), _on(ws.buf, "ws", dev), ws.nbytes,
         _stream(stream))
     _lib.check(st, "fp8lin_adapter_backward")
     return dx, da, db

@@ -16,19 +16,20 @@ namespace {
 
 constexpr int kRouteWarps = 32;
 
-// The rows sorted by adapter, each adapter's in order (a counting sort by one
-// CTA: warp w takes the w-th run of rows).  8192 rows: see adapter_route below.
+// The rows sorted by adapter, each adapter's in order: a counting sort by one CTA,
+// of which warp w takes the w-th run of rows.  Latency: two trips to L2, a few
+// barriers and some 100 cycles for 32 rows of a warp.
 __global__ void __launch_bounds__(32 * kRouteWarps)
     adapter_route_kernel(const int32_t* index, int rows, int count, int32_t* first, int32_t* sorted) {
   extern __shared__ int table[];  // [warp][group]: how many, then where the next one goes
-  __shared__ int warp_total[32];
+  __shared__ int warp_total[kRouteWarps];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
-  const int groups = count + 1;
-  for (int i = static_cast<int>(threadIdx.x); i < groups * kRouteWarps; i += 32 * kRouteWarps) table[i] = 0;
+  const int groups = count + 1, threads = static_cast<int>(blockDim.x), warps = threads / 32;
+  for (int i = static_cast<int>(threadIdx.x); i < groups * warps; i += threads) table[i] = 0;
   __syncthreads();
-  const int run = ((rows + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
+  const int run = ((rows + warps - 1) / warps + 31) / 32 * 32;
   const int64_t begin = int64_t(warp) * run;
   int* const mine = table + warp * groups;
   // Eight loads of a lane are in flight together.
@@ -57,11 +58,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   __syncthreads();
   // Group by group, warp by warp: exclusive sums.
   int before = 0;
-  for (int base = 0; base < groups; base += 32 * kRouteWarps) {
+  for (int base = 0; base < groups; base += threads) {
     const int g = base + static_cast<int>(threadIdx.x);
-    int total = 0;
-    if (g < groups)
-      for (int w = 0; w < kRouteWarps; ++w) total += table[w * groups + g];
+    int n[kRouteWarps], total = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) n[w] = w < warps && g < groups ? table[w * groups + g] : 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) total += n[w];
     int up = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -70,18 +73,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     }
     if (lane == 31) warp_total[warp] = up;
     __syncthreads();
-    int warps_before = 0, all = 0;
-    for (int w = 0; w < kRouteWarps; ++w) {
-      if (w < warp) warps_before += warp_total[w];
-      all += warp_total[w];
-    }
+    const int of_warp = lane < warps ? warp_total[lane] : 0;
+    const int warps_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp : 0);
+    const int all = __reduce_add_sync(0xFFFFFFFFu, of_warp);
     int at = before + warps_before + up - total;
     if (g < groups) {
       first[g] = at;
+#pragma unroll
       for (int w = 0; w < kRouteWarps; ++w) {
-        const int n = table[w * groups + g];
-        table[w * groups + g] = at;
-        at += n;
+        if (w < warps) table[w * groups + g] = at;
+        at += n[w];
       }
       if (g == groups - 1) first[groups] = rows;
     }
@@ -111,7 +112,9 @@ struct FewArgs {
   int64_t ldx, ldbase, ldy;
   int k, n, rank, count;
 };
-constexpr int kFewWarps = 8, kFewCluster = 8;  // a warp has one rank at least: kRanks >= kFewWarps
+constexpr int kFewWarps = 16, kFewCluster = 8;
+// Steps of B that a warp loads before it waits for the low product.
+constexpr int few_ahead(int lanes) { return lanes <= 2 ? 8 : 4; }
 
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -131,7 +134,8 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum)
 
 // kLanes: lanes a column of B, eight ranks each.
 template <int kLanes, bool kAligned>
-__global__ void __launch_bounds__(32 * kFewWarps) adapter_few_kernel(const __grid_constant__ FewArgs p) {
+__global__ void __launch_bounds__(32 * kFewWarps, 2)  // 32 rows are 256 CTAs, all resident
+    adapter_few_kernel(const __grid_constant__ FewArgs p) {
   constexpr int kRanks = 8 * kLanes;
   __shared__ float sums[kFewCluster][kRanks];
   griddep_wait();
@@ -160,26 +164,50 @@ __global__ void __launch_bounds__(32 * kFewWarps) adapter_few_kernel(const __gri
   const uint16_t* const x = p.x + row * p.ldx;
   const int k_part = ((p.k + kFewCluster - 1) / kFewCluster + 7) / 8 * 8;
   const int k0 = part * k_part, k1 = min(k0 + k_part, p.k);
-  bool begun = false;
-  for (int j = warp; j < kRanks; j += kFewWarps) {
-    float sum = 0.0f;
-    if (j < p.rank) {
-#pragma unroll 2
-      for (int c = k0 + 8 * lane; c < k1; c += 256) {
-        const int n = kAligned ? 8 : min(8, k1 - c);
-        sum = dot8(load_values<kAligned>(x + c, n), load_values<kAligned>(a + int64_t(j) * p.k + c, n), sum);
+  // B's first steps are on their way during the low product.
+  constexpr int kCols = 32 / kLanes;  // columns a warp takes a step
+  constexpr int kStep = kFewWarps * kCols;
+  const int sub = lane % kLanes, at = lane / kLanes;
+  const int ranks = min(max(p.rank - 8 * sub, 0), 8);
+  auto load_b = [&](int c) {
+    return load_values<kAligned>(b + int64_t(c) * p.rank + 8 * sub, c < n1 ? ranks : 0);
+  };
+  const int c0 = n0 + warp * kCols + at;
+  constexpr int kAhead = few_ahead(kLanes);
+  uint4 ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ahead[i] = load_b(c0 + i * kStep);
+  // A warp's ranks together: x is read once, and all loads of a turn are in flight.
+  constexpr int kPer = kRanks > kFewWarps ? kRanks / kFewWarps : 1;
+  float part_sum[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) part_sum[i] = 0.0f;
+  if (warp < p.rank) {
+    for (int c = k0 + 8 * lane; c - 8 * lane < k1; c += 256) {
+      const int n = values_at(c, k1);
+      const uint4 v = load_values<kAligned>(x + c, n);
+      uint4 w[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int j = warp + i * kFewWarps;
+        w[i] = load_values<kAligned>(a + int64_t(j) * p.k + c, j < p.rank ? n : 0);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      for (int i = 0; i < kPer; ++i) part_sum[i] = dot8(v, w[i], part_sum[i]);
     }
-    if (!begun) cluster_wait();
-    begun = true;
-    if (lane < kFewCluster)
-      st_shared_cluster_u32(map_to_cta(smem_addr(&sums[part][j]), lane), __float_as_uint(sum));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part_sum[i] += __shfl_xor_sync(0xFFFFFFFFu, part_sum[i], o);
+  }
+  cluster_wait();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = warp + i * kFewWarps;
+    if (lane < kFewCluster && j < kRanks)
+      st_shared_cluster_u32(map_to_cta(smem_addr(&sums[part][j]), lane), __float_as_uint(part_sum[i]));
   }
   cluster_sync_all();
-  const int sub = lane % kLanes, at = lane / kLanes;
-  constexpr int kCols = 32 / kLanes;  // columns a warp takes at a time
   float low[8];
   const float scale = __ldg(p.scale + adapter);
 #pragma unroll
@@ -195,22 +223,24 @@ __global__ void __launch_bounds__(32 * kFewWarps) adapter_few_kernel(const __gri
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) low[j] *= scale;
-  const int ranks = min(max(p.rank - 8 * sub, 0), 8);
-#pragma unroll 8
-  for (int c0 = n0 + warp * kCols; c0 < n1; c0 += kFewWarps * kCols) {
-    const int c = c0 + at;
-    float sum = 0.0f;
-    if (c < n1) {
-      float w[8];
-      bf16x8_to_f32(load_values<kAligned>(b + int64_t(c) * p.rank + 8 * sub, kAligned && ranks > 0 ? 8 : ranks), w);
+  auto column = [&](int c, const uint4& v) {
+    float w[8], sum = 0.0f;
+    bf16x8_to_f32(v, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(low[j], w[j], sum);
-    }
+    for (int j = 0; j < 8; ++j) sum = fmaf(low[j], w[j], sum);
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (c < n1 && sub == 0) {
       if (base != nullptr) sum += bf16lo_to_f32(base[c]);
       y[c] = static_cast<uint16_t>(cvt_bf16x2(sum, 0.0f) & 0xFFFFu);
+    }
+  };
+  for (int c = c0; c - at < n1; c += kAhead * kStep) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) column(c + i * kStep, ahead[i]);
+    if (c - at + kAhead * kStep < n1) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ahead[i] = load_b(c + (i + kAhead) * kStep);
     }
   }
 }
@@ -220,7 +250,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) adapter_few_kernel(const __gri
 cudaError_t launch_adapter_route(const int32_t* index, int64_t rows, int64_t count, int32_t* route,
                                  const DeviceInfo& dev, cudaStream_t stream) {
   set_error_site("adapter_route_kernel");
-  const size_t bytes = sizeof(int) * kRouteWarps * static_cast<size_t>(count + 1);
+  // 32 rows a warp where there are few.
+  int64_t warps = (rows + 31) / 32;
+  warps = warps < 4 ? 4 : warps > kRouteWarps ? kRouteWarps : warps;
+  const size_t bytes = sizeof(int) * static_cast<size_t>(warps * (count + 1));
   if (bytes > 40 * 1024) {
     static std::mutex mu;
     static bool done[64];
@@ -234,11 +267,15 @@ cudaError_t launch_adapter_route(const int32_t* index, int64_t rows, int64_t cou
       done[dev.device] = true;
     }
   }
-  return launch_kernel(adapter_route_kernel, dim3(1), dim3(32 * kRouteWarps), bytes, stream, 1, false,
+  return launch_kernel(adapter_route_kernel, dim3(1), dim3(static_cast<unsigned>(32 * warps)), bytes, stream, 1, false,
                        index, static_cast<int>(rows), static_cast<int>(count), route, route + count + 2);
 }
 
-bool adapter_few_fits(const AdapterArgs& a) { return a.rows <= 64; }
+bool adapter_few_fits(const AdapterArgs& a) {
+  // Rows do not share what they read, and 32 of them fill the GPU once: 64 x 4096 x 4096
+  // with 32 adapters takes 11 us so and 16 sorted at rank 16, 22 and 17 at rank 64.
+  return a.rows <= 64 && a.rows * 8 * rank_tiles(a.rank) <= 2048;
+}
 
 cudaError_t launch_adapter_few(const AdapterArgs& a, const int32_t* index, const uint16_t* x, int64_t ldx,
                                const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,

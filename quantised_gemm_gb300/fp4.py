@@ -21,6 +21,7 @@ import torch
 from . import _lib
 from . import (AMAX_AUTO, DELAYED, DYNAMIC, E4M3, MXFP4, NVFP4, ScalingState, Workspace, _dev,
                _stream, scale_many)
+from .adapters import AdapterRoute, Adapters, _linear, _linear_args
 
 _load = _lib.load
 
@@ -175,19 +176,28 @@ def fp4_gemm(a: Fp4Tensor, b: Fp4Tensor, out: torch.Tensor, ws: Workspace,
 
 
 def fp4_linear(x: torch.Tensor, x4: Fp4Tensor, w4: Fp4Tensor, y: torch.Tensor, ws: Workspace,
-               stream=None) -> torch.Tensor:
+               stream=None, *, adapters: Adapters | None = None, index: torch.Tensor | None = None,
+               h: torch.Tensor | None = None, route: AdapterRoute | None = None) -> torch.Tensor:
     """y = x W^T for a weight kept in 4 bits: x is quantised into x4, then
-    multiplied with w4."""
+    multiplied with w4.  With adapters, y += the part of each row's adapter as
+    adapter_linear(x, index, adapters, y, h, ws, base=y, route=route) adds it."""
     px, rows, cols, ld = _matrix(x, "x")
     if rows != x4.rows or cols != x4.cols:
         raise ValueError("x4 must be [%d, %d]" % (rows, cols))
     py, ldy = _product_out(y, "y", rows, w4.rows)
+    if (adapters is None) != (index is None) or (adapters is None) != (h is None):
+        raise ValueError("adapters, index and h must be given together")
+    low = None
+    if adapters is not None:
+        low = _linear_args(x, index, adapters, y, h, ws, y, route, stream)
     state = _source_state(x4)
     st = _load().fp8lin_fp4_linear(px, ld, _state_arg(state), x4._ref, w4._ref, py, ldy, ws.ptr,
                                    ws.nbytes, _stream(stream))
     if state is not None:
         state._pull()
     _lib.check(st, "fp8lin_fp4_linear")
+    if low is not None:
+        _linear(low)
     return y
 
 

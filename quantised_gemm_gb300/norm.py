@@ -15,55 +15,69 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from . import Workspace, _dev, _stream
-from .fp4 import _matrix
+from . import Workspace, _stream
 
 _load = _lib.load
 
+_BF16 = torch.bfloat16
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
+_current_device = torch._C._cuda_getDevice
 
 
-def _here(*tensors):
-    """Refuses tensors of another device than the current one, on whose stream the call runs."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
-            raise ValueError("a tensor on cuda:%d, but the current device is cuda:%d"
-                             % (t.get_device(), dev))
+def _on(t: torch.Tensor, name: str, dev: int):
+    """Refuses a tensor of another device than the current one, on whose stream the call runs."""
+    at = t.get_device()
+    if at != dev:
+        raise ValueError("%s must be a CUDA tensor" % name if at < 0 else
+                         "%s is on cuda:%d, but the current device is cuda:%d" % (name, at, dev))
+    return t.data_ptr()
 
 
-def _param(t: torch.Tensor | None, name: str, cols: int, dtype=None):
-    if t is None:
-        return None
-    if t.dtype not in _F32 or (dtype is not None and t.dtype != dtype):
-        raise TypeError("%s must be %s, got %s" % (name, dtype or "bf16 or fp32", t.dtype))
-    if t.dim() != 1 or t.shape[0] != cols or (cols > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be contiguous [%d]" % (name, cols))
-    return _dev(t, name)
+def _rows(t: torch.Tensor, name: str, dev: int):
+    """(pointer, rows, cols, row stride) of a 2-D bf16 tensor with unit column stride."""
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D" % name)
+    rows, cols = shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if ld < cols:
+        if rows > 1:
+            raise ValueError("%s must not have overlapping rows" % name)
+        ld = cols
+    return _on(t, name, dev), rows, cols, ld
 
 
-def _rows_like(t: torch.Tensor | None, name: str, rows: int, cols: int):
+def _rows_like(t: torch.Tensor | None, name: str, rows: int, cols: int, dev: int):
     """(pointer, row stride) of a bf16 [rows, cols] tensor; (None, 0) for None."""
     if t is None:
         return None, 0
-    p, r, c, ld = _matrix(t, name)
-    if (r, c) != (rows, cols):
+    p, r, c, ld = _rows(t, name, dev)
+    if r != rows or c != cols:
         raise ValueError("%s must be [%d, %d]" % (name, rows, cols))
     return p, ld
 
 
-def _stats(t: torch.Tensor | None, rows: int):
+def _whole(t: torch.Tensor | None, name: str, shape, dtype, dev: int):
+    """The pointer of a contiguous tensor of this shape and type; None for None."""
     if t is None:
         return None
-    if tuple(t.shape) != (2, rows) or not t.is_contiguous():
-        raise ValueError("stats must be contiguous [2, %d]" % rows)
-    return _dev(t, "stats", torch.float32)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s" % (name, list(shape)))
+    return _on(t, name, dev)
 
 
-def _amax(t: torch.Tensor | None, name: str):
-    if t is not None and t.numel() != 1:
-        raise ValueError("%s must have one element" % name)
-    return _dev(t, name, torch.float32)
+def _amax(t: torch.Tensor | None, name: str, dev: int):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() != 1:
+        raise ValueError("%s must be fp32 with one element" % name)
+    return _on(t, name, dev)
 
 
 def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None, y: torch.Tensor,
@@ -75,20 +89,24 @@ def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None, y: torc
     written too.  w, b: bf16 or fp32 [K]; stats (fp32 [2, M]) receives the rows'
     means and inverse deviations, for the backward; y_amax (fp32[1]) max |y|,
     for which ws is needed.  h may be x or residual, and y may be x or h."""
-    px, rows, cols, ldx = _matrix(x, "x")
-    _here(x, w, b, y, stats, residual, h, y_amax, None if ws is None else ws.buf)
+    dev = _current_device()
+    px, rows, cols, ldx = _rows(x, "x", dev)
     if (residual is None) != (h is None):
         raise ValueError("residual and h must be given together")
     if y_amax is not None and ws is None:
         raise ValueError("y_amax needs a Workspace")
-    pr, ldr = _rows_like(residual, "residual", rows, cols)
-    ph, ldh = _rows_like(h, "h", rows, cols)
-    py, ldy = _rows_like(y, "y", rows, cols)
-    pw = _param(w, "w", cols)
-    st = _load().fp8lin_layer_norm(px, ldx, pr, ldr, ph, ldh, pw, _param(b, "b", cols, w.dtype),
-                                   _F32[w.dtype], rows, cols, eps, py, ldy, _stats(stats, rows),
-                                   _amax(y_amax, "y_amax"), None if ws is None else ws.ptr,
-                                   _stream(stream))
+    f32 = _F32.get(w.dtype)
+    if f32 is None:
+        raise TypeError("w must be bf16 or fp32, got %s" % w.dtype)
+    pr, ldr = _rows_like(residual, "residual", rows, cols, dev)
+    ph, ldh = _rows_like(h, "h", rows, cols, dev)
+    py, ldy = _rows_like(y, "y", rows, cols, dev)
+    pw = _whole(w, "w", (cols,), w.dtype, dev)
+    pb = _whole(b, "b", (cols,), w.dtype, dev)
+    st = _load().fp8lin_layer_norm(px, ldx, pr, ldr, ph, ldh, pw, pb, f32, rows, cols, eps, py, ldy,
+                                   _whole(stats, "stats", (2, rows), torch.float32, dev),
+                                   _amax(y_amax, "y_amax", dev),
+                                   None if ws is None else _on(ws.buf, "ws", dev), _stream(stream))
     _lib.check(st, "fp8lin_layer_norm")
     return y
 
@@ -101,20 +119,27 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, stat
     a residual) and left stats; each may be None.  dres is added to dx: the
     gradient that reaches h past the norm.  dw and db have w's type.  dx may be
     dy or dres."""
-    pdy, rows, cols, lddy = _matrix(dy, "dy")
+    dev = _current_device()
+    pdy, rows, cols, lddy = _rows(dy, "dy", dev)
     if ws is None:
         raise ValueError("a Workspace is required")
-    _here(dy, x, w, stats, dx, dw, db, dres, dx_amax, ws.buf)
     if dx_amax is not None and dx is None:
         raise ValueError("dx_amax needs dx")
-    px, ldx = _rows_like(x, "x", rows, cols)
-    pr, ldr = _rows_like(dres, "dres", rows, cols)
-    pdx, lddx = _rows_like(dx, "dx", rows, cols)
-    pw = _param(w, "w", cols)
+    if stats is None:
+        raise ValueError("stats is required")
+    dtype = w.dtype
+    f32 = _F32.get(dtype)
+    if f32 is None:
+        raise TypeError("w must be bf16 or fp32, got %s" % dtype)
+    px, ldx = _rows_like(x, "x", rows, cols, dev)
+    pr, ldr = _rows_like(dres, "dres", rows, cols, dev)
+    pdx, lddx = _rows_like(dx, "dx", rows, cols, dev)
+    one = (cols,)
     st = _load().fp8lin_layer_norm_backward(
-        pdy, lddy, px, ldx, pw, _F32[w.dtype], _stats(stats, rows), rows, cols, pr, ldr, pdx, lddx,
-        _param(dw, "dw", cols, w.dtype), _param(db, "db", cols, w.dtype), _amax(dx_amax, "dx_amax"),
-        ws.ptr, ws.nbytes, _stream(stream))
+        pdy, lddy, px, ldx, _whole(w, "w", one, dtype, dev), f32,
+        _whole(stats, "stats", (2, rows), torch.float32, dev), rows, cols, pr, ldr, pdx, lddx,
+        _whole(dw, "dw", one, dtype, dev), _whole(db, "db", one, dtype, dev),
+        _amax(dx_amax, "dx_amax", dev), _on(ws.buf, "ws", dev), ws.nbytes, _stream(stream))
     _lib.check(st, "fp8lin_layer_norm_backward")
     return dx, dw, db
 
