@@ -97,8 +97,10 @@ struct RowTile {
   bool only;  // the group's only tile
 };
 
-// Tile `want` of tiles of `size` rows of one group each (a group without rows
-// has none).  All lanes of a warp call it and get the same.
+// Tile `want` of tiles of `size` rows of one group each (a group without rows has
+// none); behind the last one, with kEmpty, the groups without rows, a tile of none
+// each.  All lanes of a warp call it and get the same.
+template <bool kEmpty = false>
 __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int size, int want) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
   int before = 0, several_before = 0, blocks_before = 0;
@@ -140,6 +142,20 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
     several_before += __shfl_sync(0xFFFFFFFFu, several_up, 31);
     blocks_before += __shfl_sync(0xFFFFFFFFu, blocks_up, 31);
   }
+  if constexpr (kEmpty) {
+    int skip = want - before;
+    for (int base = 0; base < groups; base += 32) {
+      const int g = base + lane;
+      const bool empty = g < groups && __ldg(r.first + g) == __ldg(r.first + g + 1);
+      uint32_t mask = __ballot_sync(0xFFFFFFFFu, empty);
+      if (skip >= __popc(mask)) {
+        skip -= __popc(mask);
+        continue;
+      }
+      for (; skip > 0; --skip) mask &= mask - 1;
+      return RowTile{base + __ffs(static_cast<int>(mask)) - 1, 0, 0, 0, 0, true};
+    }
+  }
   return RowTile{-1, 0, 0, 0, 0, false};
 }
 
@@ -155,7 +171,9 @@ constexpr int kAdapterThreads = 256, kAdapterWarps = 8;
 // wait() ends with a barrier (of the warp where it is alone), after which that stage
 // may be filled.  Where rows are not 16-byte aligned a vector is two, those that its
 // values lie in.
-template <int kStages, int kVecs, int kShared, bool kAlone, bool kAligned>
+// kTurned: lanes (g, t) of a warp have the t-th vector of row g, and the vectors lie
+// so that the eight of one t are in different banks, for load_tiles() over them.
+template <int kStages, int kVecs, int kShared, bool kAlone, bool kAligned, bool kTurned = false>
 struct Stages {
   static constexpr int kEach = kAligned ? 1 : 2;
   static constexpr int kOwn = kEach * kVecs * kAdapterThreads;
@@ -166,6 +184,23 @@ struct Stages {
   int due = 0, filling = 0;  // offsets of stages
 
   __device__ __forceinline__ explicit Stages(uint4* shared) : base(shared) {}
+  __device__ __forceinline__ static int slot() {
+    const int i = static_cast<int>(threadIdx.x);
+    return kTurned ? i ^ (i >> 3 & 3) : i;
+  }
+  // The 16 x 16 tile of vectors v (rows 0 to 7) and v + 1 (8 to 15) and the t-th eight
+  // columns and the next, turned: the operand whose rows are the columns.
+  __device__ __forceinline__ void turned(uint32_t (&a)[4], int v, int t) const {
+    const int lane = static_cast<int>(threadIdx.x & 31u), of = lane >> 3, row = lane & 7;
+    load_tiles<true>(a, base + due + kEach * (v + (of >> 1)) * kAdapterThreads + (threadIdx.x & ~31u) +
+                            4 * row + ((t + (of & 1)) ^ (row >> 1)));
+  }
+  // Puts vectors that take() has shifted into place, for turned().
+  __device__ __forceinline__ void put_back(const uint4 (&x)[kVecs]) const {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) base[due + kEach * v * kAdapterThreads + slot()] = x[v];
+    __syncwarp();
+  }
   __device__ __forceinline__ static void step(int& stage) {
     stage = stage == (kStages - 1) * kSize ? 0 : stage + kSize;
   }
@@ -182,7 +217,7 @@ struct Stages {
     for (int v = 0; v < kVecs; ++v) {
       int n;
       const uint16_t* p = from(v, n);
-      uint4* const to = base + filling + kEach * v * kAdapterThreads + threadIdx.x;
+      uint4* const to = base + filling + kEach * v * kAdapterThreads + slot();
       if constexpr (kAligned) {
         copy16(to, p, n > 0);
       } else {
@@ -201,7 +236,7 @@ struct Stages {
   __device__ __forceinline__ void take(uint4 (&out)[kVecs], From from) const {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      const uint4* const at = base + due + kEach * v * kAdapterThreads + threadIdx.x;
+      const uint4* const at = base + due + kEach * v * kAdapterThreads + slot();
       if constexpr (kAligned) {
         out[v] = at[0];
       } else {

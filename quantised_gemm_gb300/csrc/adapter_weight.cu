@@ -6,6 +6,9 @@
 #ifndef W_RW
 #define W_RW 4
 #endif
+#ifndef W_MIN
+#define W_MIN 256
+#endif
 #ifndef W_CTAS
 #define W_CTAS 3
 #endif
@@ -16,6 +19,7 @@ namespace {
 // blocks of 16 rows side by side (kRowWarps of them) and columns side by side (the
 // others); a tile that is its adapter's only one is written as bf16 into dw, else
 // its sums go to the partials, one slot a tile, which adapter_sum_kernel adds up.
+// An adapter without rows has a tile too: zeros.
 struct WeightArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -27,7 +31,6 @@ struct WeightArgs {
   const uint4* packed;  // low as adapter_pack_kernel left it, or null
   bool along;    // dw is [cols, r] (dB), else [r, cols] (dA)
   bool aligned;  // x's rows
-  bool dw_aligned;
 };
 
 // With a small rank the rows' numbers are few beside x, and splitting the rows
@@ -45,7 +48,7 @@ struct WeightShape {
   using T = Stages<stages_in(kAlone ? kStageRoom - 16 * 1024 : kStageRoom,
                              sizeof(uint4) * ((kAligned ? 2 : 4) * kChunks * kAdapterThreads +
                                               (kAlone ? kAdapterWarps : 1) * kShared)),
-                   2 * kChunks, kShared, kAlone, kAligned>;
+                   2 * kChunks, kShared, kAlone, kAligned, true>;
 };
 
 // What a lane needs of rank tile j of 16 rows of low: rows 2 t, 2 t + 1 and 2 t + 8,
@@ -102,8 +105,7 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int col_warp = warp % S::kColWarps, row_warp = warp / S::kColWarps;
   const int g = lane >> 2, t = lane & 3;
-  // The last rows first: they are what is left in L2 of the pass before.
-  const RowTile tile = find_tile(route, route.groups - 1, p.tile_rows, p.tiles - 1 - block / p.slabs);
+  const RowTile tile = find_tile<true>(route, route.groups - 1, p.tile_rows, block / p.slabs);
   if (tile.group < 0) return;
   const int col0 = ((block % p.slabs) * S::kColWarps + col_warp) * 32 * kChunks;
   const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
@@ -171,34 +173,29 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
   find(number, kBefore);
   for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
-    uint4 x[2 * kChunks];
-    int due[2] = {0, 0};
-    if constexpr (!kAligned) find(due, turn);
-    stages.take(x, x_of(due));
+    if constexpr (!kAligned) {
+      uint4 x[2 * kChunks];
+      int due[2];
+      find(due, turn);
+      stages.take(x, x_of(due));
+      stages.put_back(x);
+    }
+    uint32_t a[2 * kChunks][4];  // 16 columns and 16 rows each
+#pragma unroll
+    for (int m = 0; m < 2 * kChunks; ++m) stages.turned(a[m], m & ~1, 2 * (m & 1));
     if (turn + kBefore < turns) copy_low(turn + kBefore);
     stages.copy(x_of(number));
     stages.filled();
     find(number, turn + kBefore + 1);
     const uint4* const operand = stages.shared_due() + (S::kAlone ? 0 : row_warp * kRankTiles * 32) + lane;
-    uint32_t a[kChunks][4][2];  // of columns 8 (k / 2) + 2 q + k % 2, rows 0-7 and 8-15
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) a[c][q][i] = turn_tile(word(x[2 * c + i], q));
 #pragma unroll
     for (int j = 0; j < kRankTiles; ++j) {
       const uint4 low = operand[32 * j];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
-                   a[c][2 * m + 1][1], low.z, low.w);
-          mma_bf16(acc[2 * c + m][j], a[c][2 * m][0], a[c][2 * m + 1][0], a[c][2 * m][1],
-                   a[c][2 * m + 1][1], low.x, low.y);
-        }
+      for (int m = 0; m < 2 * kChunks; ++m) {
+        mma_bf16(acc[m][j], a[m][0], a[m][1], a[m][2], a[m][3], low.z, low.w);
+        mma_bf16(acc[m][j], a[m][0], a[m][1], a[m][2], a[m][3], low.x, low.y);
+      }
     }
   }
   copies_wait<0>();
@@ -222,70 +219,33 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
   const int64_t size = int64_t(p.cols) * p.rank;
   uint16_t* const dw = p.dw + tile.group * size;
   float* const part = tile.only ? nullptr : p.partials + tile.slot * size;
-  // A lane has of product (c, j) columns 8 (g / 2) + 2 q + g % 2, q = 0 .. 3, of
-  // ranks 8 j + 2 t and the next.
+  // A lane has of product (m, j) columns 16 m + g and 16 m + g + 8 of ranks 8 j + 2 t and
+  // the next.
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c)
+  for (int m = 0; m < 2 * kChunks; ++m)
 #pragma unroll
-    for (int j = 0; j < kRankTiles; ++j) {
-      if (p.along) {
+    for (int j = 0; j < kRankTiles; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = col0 + 32 * c + 8 * (g >> 1) + 2 * q + (g & 1);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int rank = 8 * j + 2 * t + e;
-            if (col >= p.cols || rank >= p.rank) continue;
-            const float v = acc[2 * c + (q >> 1)][j][2 * (q & 1) + e];
-            const int64_t to = int64_t(col) * p.rank + rank;
-            if (part != nullptr)
-              part[to] = v;
-            else
-              dw[to] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
-          }
-        }
-        continue;
+      for (int i = 0; i < 4; ++i) {
+        const int col = col0 + 16 * m + 8 * (i >> 1) + g, rank = 8 * j + 2 * t + (i & 1);
+        if (col >= p.cols || rank >= p.rank) continue;
+        const int64_t to = p.along ? int64_t(col) * p.rank + rank : int64_t(rank) * p.cols + col;
+        if (part != nullptr)
+          part[to] = acc[m][j][i];
+        else
+          dw[to] = static_cast<uint16_t>(cvt_bf16x2(acc[m][j][i], 0.0f) & 0xFFFFu);
       }
-      // Lanes of neighbouring g swap, so that one has eight columns side by side
-      // of the first rank and the other of the second.
-      float v[8];
-      const int e = g & 1;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* a = acc[2 * c + (q >> 1)][j] + 2 * (q & 1);
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, e ? a[0] : a[1], 4);
-        v[2 * q] = e ? got : a[0];
-        v[2 * q + 1] = e ? a[1] : got;
-      }
-      const int col = col0 + 32 * c + 8 * (g >> 1), rank = 8 * j + 2 * t + e;
-      const int64_t to = int64_t(rank) * p.cols + col;
-      if (rank < p.rank && p.dw_aligned && col < p.cols) {
-        if (part != nullptr) {
-          float4* put = reinterpret_cast<float4*>(part + to);
-          put[0] = make_float4(v[0], v[1], v[2], v[3]);
-          put[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-          *reinterpret_cast<uint4*>(dw + to) = f32_to_bf16x8(v);
-        }
-      } else if (rank < p.rank) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (col + i >= p.cols) continue;
-          if (part != nullptr)
-            part[to + i] = v[i];
-          else
-            dw[to + i] = static_cast<uint16_t>(cvt_bf16x2(v[i], 0.0f) & 0xFFFFu);
-        }
-      }
-    }
 }
 
 // dB (blocks from 0 on) and dA (the others) in one launch; either may have none.
 template <int kRankTiles>
 __global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 2 ? 2 : 1)
     adapter_weight_kernel(const __grid_constant__ WeightArgs db, const __grid_constant__ WeightArgs da,
-                          const Route route) {
-  griddep_wait();
+                          const Route route, bool early) {
+  // early: the launch before this one writes nothing that this one touches, and all
+  // before that is done once its CTAs let this one begin.  The wait then comes at the
+  // end, so that what follows still finds everything before it done.
+  if (!early) griddep_wait();
   griddep_launch_dependents();
   const int block = static_cast<int>(blockIdx.x), first = db.tiles * db.slabs;
   const bool is_db = block < first;
@@ -297,10 +257,11 @@ __global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 2 ? 2 : 1)
     weight_tile<kRankTiles, true>(p, route, is_db ? block : block - first, sums, shared);
   else
     weight_tile<kRankTiles, false>(p, route, is_db ? block : block - first, sums, shared);
+  if (early) griddep_wait();
 }
 
-// The partials of adapters with several tiles, added in order, and zeros for
-// those without rows.  One CTA row an adapter.
+// The partials of adapters with several tiles, added in order.  One CTA row an
+// adapter.
 struct SumArgs {
   const float* partials;
   uint16_t* dw;
@@ -324,7 +285,7 @@ __device__ __forceinline__ void sum_partials(const SumArgs& p, int group, int bl
   }
   before = __reduce_add_sync(0xFFFFFFFFu, before);
   mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  if (mine == 1) return;  // written already
+  if (mine <= 1) return;  // written already
   uint16_t* const dw = p.dw + group * p.size;
   const float* const from = p.partials + before * p.size;
   for (int64_t i = int64_t(block) * kSumThreads + threadIdx.x; i < p.size; i += int64_t(blocks) * kSumThreads) {
@@ -357,9 +318,9 @@ int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes,
     return cudaSuccess;
   });
   const int64_t slabs = (cols + slab - 1) / slab;
-  // Three CTAs an SM, tiles of 128 rows at least.
+  // Three CTAs an SM, tiles of W_MIN rows at least.
   int64_t rows = (a.rows * slabs + W_CTAS * dev.num_sms - 1) / (W_CTAS * dev.num_sms);
-  rows = (rows + 127) / 128 * 128;
+  rows = rows < W_MIN ? W_MIN : (rows + 127) / 128 * 128;
   // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
   // them, and at most a.rows / rows and one for each adapter.
   const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));
@@ -392,7 +353,7 @@ cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, c
 }
 
 cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                  const DeviceInfo& dev, cudaStream_t stream) {
+                                  bool early, const DeviceInfo& dev, cudaStream_t stream) {
   set_error_site("adapter_weight_kernel");
   return with_rank_tiles(a.rank, [&](auto ranks) {
     constexpr int kRankTiles = decltype(ranks)::value;
@@ -410,11 +371,10 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
       p.rank = a.rank;
       p.tile_rows = static_cast<int>(j.tile_rows);
       p.packed = static_cast<const uint4*>(j.packed);
-      p.tiles = static_cast<int>(most_tiles(a.rows, a.count, j.tile_rows));
+      p.tiles = static_cast<int>(a.rows / j.tile_rows + a.count);
       p.slabs = (p.cols + kSlab - 1) / kSlab;
       p.along = !is_da;
       p.aligned = rows_aligned(j.x, j.ldx, p.cols);
-      p.dw_aligned = is_da && aligned16(j.dw) && p.cols % 8 == 0;
       return p;
     };
     const WeightArgs b = job(db, false), c = job(da, true);
@@ -422,7 +382,7 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
     using S = WeightShape<kRankTiles>;
     constexpr size_t kA = S::template T<true>::kBytes, kB = S::template T<false>::kBytes;
     return launch_staged<adapter_weight_kernel<kRankTiles>>(grid, kA > kB ? kA : kB, dev, stream, 1, b, c,
-                                                            route_of(a));
+                                                            route_of(a), early);
   });
 }
 

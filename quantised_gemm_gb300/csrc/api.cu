@@ -1880,11 +1880,11 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     e = launch_adapter_low(a, true, dys, lddy, dh, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  // The weight gradients' operands from h and dh, laid out once where they leave
-  // three quarters of the room for the partial sums.
+  // The weight gradients' operands from h and dh, laid out once where many rows pay for
+  // that launch and they leave three quarters of the room for the partial sums.
   AdapterWeight wa, wb;
   const size_t packed = adapter_packed_bytes(a);
-  if ((da != nullptr || db != nullptr) && 8 * packed <= room_bytes) {
+  if ((da != nullptr || db != nullptr) && rows >= 2048 && 8 * packed <= room_bytes) {
     for (AdapterWeight* w : {&wa, &wb}) {
       if ((w == &wa ? da : db) == nullptr) continue;
       w->packed = room;
@@ -1897,13 +1897,6 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
                         : db == nullptr
                             ? room_bytes
                             : static_cast<size_t>(static_cast<double>(room_bytes) * ad->k / (ad->k + ad->n)) / 256 * 256;
-  if (dx != nullptr) {
-    ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_high(a, true, dh, static_cast<const uint16_t*>(base), ldbase,
-                            static_cast<uint16_t*>(dx), lddx, dev, stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  if (da == nullptr && db == nullptr) return FP8LIN_OK;
   if (da != nullptr) {
     wa.dw = static_cast<uint16_t*>(da);
     wa.x = static_cast<const uint16_t*>(x);
@@ -1925,11 +1918,22 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     e = launch_adapter_pack(a, wb, wa, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  {
+  if (dx != nullptr) {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_weight(a, wb, wa, dev, stream);
+    e = launch_adapter_high(a, true, dh, static_cast<const uint16_t*>(base), ldbase,
+                            static_cast<uint16_t*>(dx), lddx, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
+  if (da == nullptr && db == nullptr) return FP8LIN_OK;
+  {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_weight(a, wb, wa, dx != nullptr, dev, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  // A gradient without partial sums leaves the sum nothing to do.
+  if (wa.tile_rows >= rows) wa.dw = nullptr;
+  if (wb.tile_rows >= rows) wb.dw = nullptr;
+  if (wa.dw == nullptr && wb.dw == nullptr) return FP8LIN_OK;
   ProfScope ps(FP8LIN_PROF_GEMM, stream);
   e = launch_adapter_sum(a, wb, wa, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);

@@ -501,7 +501,7 @@ cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float
 // One of dA (x the input, low = dh) and dB (x the output's gradient, low = h); dw
 // null: not wanted.  Tiles of adapter_weight_rows rows; an adapter with several
 // leaves partials, one slot of cols * rank numbers a tile, for
-// launch_adapter_sum, which also clears the adapters without rows.
+// launch_adapter_sum (none does where tile_rows is the number of rows).
 struct AdapterWeight {
   uint16_t* dw = nullptr;
   const uint16_t* x = nullptr;
@@ -516,7 +516,7 @@ cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, c
                                 cudaStream_t stream);
 int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev);
 cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                  const DeviceInfo& dev, cudaStream_t stream);
+                                  bool early, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
                                cudaStream_t stream);
 
