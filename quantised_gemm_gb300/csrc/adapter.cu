@@ -14,11 +14,12 @@ namespace {
 
 // ---------------------------------------------------------------- route
 
-constexpr int kRouteWarps = 32;
+constexpr int kRouteWarps = 32, kRouteCluster = 8;
 
-// The rows sorted by adapter, each adapter's in order: a counting sort by one CTA,
-// of which warp w takes the w-th run of rows.  Latency: two trips to L2, a few
-// barriers and some 100 cycles for 32 rows of a warp.
+// The rows sorted by adapter, each adapter's in order: a counting sort by one CTA or
+// by one cluster of them, of whose warps the w-th takes the w-th run of rows.
+// Latency: two trips to L2, a few barriers and some 100 cycles for 32 rows of a warp.
+template <bool kClustered>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     adapter_route_kernel(const int32_t* index, int rows, int count, int32_t* first, int32_t* sorted) {
   extern __shared__ int table[];  // [warp][group]: how many, then where the next one goes
@@ -27,10 +28,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int groups = count + 1, threads = static_cast<int>(blockDim.x), warps = threads / 32;
+  constexpr int ctas = kClustered ? kRouteCluster : 1;
+  const int cta = kClustered ? static_cast<int>(blockIdx.x) : 0;
+  int* const totals = table + warps * groups;  // [cta][group] of a cluster
   for (int i = static_cast<int>(threadIdx.x); i < groups * warps; i += threads) table[i] = 0;
   __syncthreads();
-  const int run = ((rows + warps - 1) / warps + 31) / 32 * 32;
-  const int64_t begin = int64_t(warp) * run;
+  const int run = ((rows + warps * ctas - 1) / (warps * ctas) + 31) / 32 * 32;
+  const int64_t begin = int64_t(cta * warps + warp) * run;
   int* const mine = table + warp * groups;
   // Eight loads of a lane are in flight together.
   constexpr int kLoads = 8;
@@ -56,15 +60,38 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     __syncwarp();
   });
   __syncthreads();
-  // Group by group, warp by warp: exclusive sums.
+  auto of_warps = [&](int g, int (&n)[kRouteWarps]) {
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) {
+      n[w] = w < warps && g < groups ? table[w * groups + g] : 0;
+      total += n[w];
+    }
+    return total;
+  };
+  if constexpr (kClustered) {  // every CTA's numbers to all
+    cluster_sync_all();
+    for (int g = static_cast<int>(threadIdx.x); g < groups; g += threads) {
+      int n[kRouteWarps];
+      const int total = of_warps(g, n);
+      const uint32_t at = smem_addr(totals + cta * groups + g);
+      for (int to = 0; to < ctas; ++to) st_shared_cluster_u32(map_to_cta(at, to), static_cast<uint32_t>(total));
+    }
+    cluster_sync_all();
+  }
+  // Group by group, CTA by CTA, warp by warp: exclusive sums.
   int before = 0;
   for (int base = 0; base < groups; base += threads) {
     const int g = base + static_cast<int>(threadIdx.x);
-    int n[kRouteWarps], total = 0;
-#pragma unroll
-    for (int w = 0; w < kRouteWarps; ++w) n[w] = w < warps && g < groups ? table[w * groups + g] : 0;
-#pragma unroll
-    for (int w = 0; w < kRouteWarps; ++w) total += n[w];
+    int n[kRouteWarps], ctas_before = 0;
+    int total = of_warps(g, n);
+    if constexpr (kClustered) {
+      total = 0;
+      for (int c = 0; c < ctas && g < groups; ++c) {
+        if (c < cta) ctas_before += totals[c * groups + g];
+        total += totals[c * groups + g];
+      }
+    }
     int up = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -78,13 +105,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     const int all = __reduce_add_sync(0xFFFFFFFFu, of_warp);
     int at = before + warps_before + up - total;
     if (g < groups) {
-      first[g] = at;
+      if (cta == 0) {
+        first[g] = at;
+        if (g == groups - 1) first[groups] = rows;
+      }
+      at += ctas_before;
 #pragma unroll
       for (int w = 0; w < kRouteWarps; ++w) {
         if (w < warps) table[w * groups + g] = at;
         at += n[w];
       }
-      if (g == groups - 1) first[groups] = rows;
     }
     before += all;
     __syncthreads();
@@ -250,25 +280,32 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)  // 32 rows are 256 CTAs, a
 cudaError_t launch_adapter_route(const int32_t* index, int64_t rows, int64_t count, int32_t* route,
                                  const DeviceInfo& dev, cudaStream_t stream) {
   set_error_site("adapter_route_kernel");
-  // 32 rows a warp where there are few.
+  // 32 rows a warp where there are few, a cluster where there are many (65536 rows of
+  // 4 adapters: 8 us, by one CTA 29; 8192 rows 6 us either way).
   int64_t warps = (rows + 31) / 32;
   warps = warps < 4 ? 4 : warps > kRouteWarps ? kRouteWarps : warps;
-  const size_t bytes = sizeof(int) * static_cast<size_t>(warps * (count + 1));
+  const bool clustered = rows > 8192;
+  const int ctas = clustered ? kRouteCluster : 1;
+  const size_t bytes = sizeof(int) * static_cast<size_t>((warps + ctas) * (count + 1));
   if (bytes > 40 * 1024) {
     static std::mutex mu;
     static bool done[64];
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev.device]) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(adapter_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(sizeof(int) * kRouteWarps * (kAdapterMaxCount + 1)));
+      const int most = static_cast<int>(sizeof(int) * (kRouteWarps + kRouteCluster) * (kAdapterMaxCount + 1));
+      cudaError_t e = cudaFuncSetAttribute(adapter_route_kernel<false>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(adapter_route_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return e;
       done[dev.device] = true;
     }
   }
-  return launch_kernel(adapter_route_kernel, dim3(1), dim3(static_cast<unsigned>(32 * warps)), bytes, stream, 1, false,
-                       index, static_cast<int>(rows), static_cast<int>(count), route, route + count + 2);
+  return launch_kernel(clustered ? adapter_route_kernel<true> : adapter_route_kernel<false>,
+                       dim3(static_cast<unsigned>(ctas)), dim3(static_cast<unsigned>(32 * warps)), bytes, stream,
+                       ctas, false, index, static_cast<int>(rows), static_cast<int>(count), route,
+                       route + count + 2);
 }
 
 bool adapter_few_fits(const AdapterArgs& a) {

@@ -3,9 +3,6 @@
 // y = base + s h B^T in the forward, dx = base + dh A in the backward.
 #include "adapter_kernels.cuh"
 
-#ifndef HIGH_CTAS
-#define HIGH_CTAS 2
-#endif
 namespace fp8lin {
 namespace {
 
@@ -218,7 +215,7 @@ cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float
       // Slabs of whole turns; one wave of two CTAs an SM, as far as the rows have tiles.
       constexpr int kTurn = 32 * kAdapterWarps / kRowWarps;
       const int turns = (p.cols + kTurn - 1) / kTurn;
-      int64_t slabs = HIGH_CTAS * int64_t(dev.num_sms) / most;
+      int64_t slabs = 2 * int64_t(dev.num_sms) / most;
       slabs = slabs < 1 ? 1 : slabs > turns ? turns : slabs;
       const int per = static_cast<int>((turns + slabs - 1) / slabs);
       p.slab = per * kTurn;

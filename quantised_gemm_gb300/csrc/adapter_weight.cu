@@ -3,15 +3,6 @@
 // dB (x = dy, low = h) and dA (x the input, low = dh, turned) in one launch.
 #include "adapter_kernels.cuh"
 
-#ifndef W_RW
-#define W_RW 4
-#endif
-#ifndef W_MIN
-#define W_MIN 256
-#endif
-#ifndef W_CTAS
-#define W_CTAS 3
-#endif
 namespace fp8lin {
 namespace {
 
@@ -37,7 +28,7 @@ struct WeightArgs {
 // leaves fewer partial sums; with a large one warps of the same rows share them.
 template <int kRankTiles>
 struct WeightShape {
-  static constexpr int kRowWarps = kRankTiles <= 2 ? W_RW : kRankTiles == 4 ? 2 : 1;
+  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
   static constexpr int kColWarps = kAdapterWarps / kRowWarps;
   static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
   static constexpr int kSlab = 32 * kChunks * kColWarps;
@@ -45,6 +36,7 @@ struct WeightShape {
   static constexpr bool kAlone = kRankTiles <= 2;  // each warp has its own low operands
   static constexpr int kShared = (kAlone ? 1 : kRowWarps) * kRankTiles * 32;  // of a turn
   template <bool kAligned>
+  // More stages than 80 KB hold cost a short sum more than they give a long one.
   using T = Stages<stages_in(kAlone ? kStageRoom - 16 * 1024 : kStageRoom,
                              sizeof(uint4) * ((kAligned ? 2 : 4) * kChunks * kAdapterThreads +
                                               (kAlone ? kAdapterWarps : 1) * kShared)),
@@ -117,13 +109,16 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
   const int32_t* const rows = route.rows + tile.begin;
-  // x, the low operands and, one turn more, the row numbers are on their way.
+  // x and the low operands are on their way, and for two turns more the row numbers.
   constexpr int kStep = 16 * S::kRowWarps;
   const int turns = (tile.count + kStep - 1) / kStep;
   using T = typename S::template T<kAligned>;
   T stages(shared);
   constexpr int kBefore = T::kCount - 1;
-  int number[2];
+  int n_of[kChunks];  // values of the lane's columns
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) n_of[c] = values_at(col0 + 32 * c + 8 * t, p.cols);
+  const uint16_t* const column = p.x + (n_of[0] > 0 ? col0 + 8 * t : 0);
   auto find = [&](int (&to)[2], int turn) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -131,26 +126,29 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
       to[i] = of < tile.count ? __ldg(rows + of) : -1;
     }
   };
-  // The rows of the turn that is due are needed again where they are not aligned.
   auto x_of = [&](const int (&of)[2]) {
-    return [&](int v, int& n) {
-      const int col = col0 + 32 * (v >> 1) + 8 * t, row = of[v & 1];
-      n = row < 0 ? 0 : values_at(col, p.cols);
-      return p.x + (row < 0 ? 0 : row) * p.ldx + (n > 0 ? col : 0);
+    const uint16_t* const at[2] = {column + max(of[0], 0) * p.ldx, column + max(of[1], 0) * p.ldx};
+    const bool on[2] = {of[0] >= 0, of[1] >= 0};
+    return [=, &n_of](int v, int& n) {
+      n = on[v & 1] ? n_of[v >> 1] : 0;
+      return at[v & 1] + 32 * (v >> 1);
     };
   };
-  auto copy_low = [&](int turn) {
-    uint4* const to = stages.shared_filling();
-    constexpr int kThreads = S::kAlone ? 32 : kAdapterThreads;
+  constexpr int kThreads = S::kAlone ? 32 : kAdapterThreads, kBlock = kRankTiles * 32;
+  const int me = static_cast<int>(threadIdx.x) % kThreads;
+  const uint4* packed = p.packed == nullptr
+                            ? nullptr
+                            : p.packed + int64_t(tile.block + (S::kAlone ? row_warp : 0)) * kBlock + me;
+  int next_low = 0;  // the first row of the turn that copy_low() is for
+  auto copy_low = [&]() {
+    uint4* const to = stages.shared_filling() + me;
 #pragma unroll
     for (int i0 = 0; i0 < S::kShared; i0 += kThreads) {
-      const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
-      if (S::kShared % kThreads != 0 && i >= S::kShared) break;
-      const int block = S::kAlone ? row_warp : i / (kRankTiles * 32);
-      const int r = turn * kStep + 16 * block;  // the block's first row
-      if (p.packed != nullptr) {
-        const bool on = r < tile.count;
-        copy16(to + i, p.packed + (on ? int64_t(tile.block + r / 16) * (kRankTiles * 32) + i % (kRankTiles * 32) : 0), on);
+      if (S::kShared % kThreads != 0 && i0 + me >= S::kShared) break;
+      const int i = i0 + me;
+      const int r = next_low + 16 * (S::kAlone ? row_warp : i / kBlock);  // the block's first row
+      if (packed != nullptr) {
+        copy16(to + i0, packed + i0, r < tile.count);
         continue;
       }
       const int j = i / 32 % kRankTiles;
@@ -158,19 +156,25 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int of = r + 2 * (i & 3) + (e & 1) + 8 * (e >> 1), rank = 8 * j + (i >> 2 & 7);
-        v[e] = of < tile.count && rank < p.rank ? scale * __ldg(p.low + int64_t(__ldg(rows + of)) * p.rank + rank) : 0.0f;
+        v[e] = of < tile.count && rank < p.rank
+                   ? scale * __ldg(p.low + int64_t(__ldg(rows + of)) * p.rank + rank)
+                   : 0.0f;
       }
-      to[i] = low_operand(v[0], v[1], v[2], v[3]);
+      to[i0] = low_operand(v[0], v[1], v[2], v[3]);
     }
+    next_low += kStep;
+    if (packed != nullptr) packed += S::kRowWarps * kBlock;
   };
+  int number[2], later[2];
 #pragma unroll
-  for (int i = 0; i < T::kCount - 1; ++i) {
-    if (i < turns) copy_low(i);
+  for (int i = 0; i < kBefore; ++i) {
+    copy_low();
     find(number, i);
     stages.copy(x_of(number));
     stages.filled();
   }
   find(number, kBefore);
+  find(later, kBefore + 1);
   for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     if constexpr (!kAligned) {
@@ -183,10 +187,12 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
     uint32_t a[2 * kChunks][4];  // 16 columns and 16 rows each
 #pragma unroll
     for (int m = 0; m < 2 * kChunks; ++m) stages.turned(a[m], m & ~1, 2 * (m & 1));
-    if (turn + kBefore < turns) copy_low(turn + kBefore);
+    copy_low();
     stages.copy(x_of(number));
     stages.filled();
-    find(number, turn + kBefore + 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) number[i] = later[i];
+    find(later, turn + kBefore + 2);
     const uint4* const operand = stages.shared_due() + (S::kAlone ? 0 : row_warp * kRankTiles * 32) + lane;
 #pragma unroll
     for (int j = 0; j < kRankTiles; ++j) {
@@ -318,9 +324,10 @@ int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes,
     return cudaSuccess;
   });
   const int64_t slabs = (cols + slab - 1) / slab;
-  // Three CTAs an SM, tiles of W_MIN rows at least.
-  int64_t rows = (a.rows * slabs + W_CTAS * dev.num_sms - 1) / (W_CTAS * dev.num_sms);
-  rows = rows < W_MIN ? W_MIN : (rows + 127) / 128 * 128;
+  // Three CTAs an SM; tiles of 256 rows at least, fewer of which are no faster than
+  // their sum.
+  int64_t rows = (a.rows * slabs + 3 * dev.num_sms - 1) / (3 * dev.num_sms);
+  rows = rows < 256 ? 256 : (rows + 127) / 128 * 128;
   // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
   // them, and at most a.rows / rows and one for each adapter.
   const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));

@@ -363,7 +363,7 @@ def test_no_rows():
     assert route.buf[:4].tolist() == [0, 0, 0, 0]
 
 
-@pytest.mark.parametrize("rows,count,kind", [(1, 1, "same"), (33, 4, "random"), (5000, 1024, "random"), (70001, 7, "runs"),
+@pytest.mark.parametrize("rows,count,kind", [(1, 1, "same"), (33, 4, "random"), (20000, 1024, "random"), (8193, 1, "same"), (5000, 1024, "random"), (70001, 7, "runs"),
                                              (4096, 3, "none"), (1000, 1000, "bad")])
 def test_route(rows, count, kind):
     import quantised_gemm_gb300 as q
