@@ -133,6 +133,65 @@ __device__ __forceinline__ uint16_t value_of(const uint4& u, int i) {
   return static_cast<uint16_t>(i & 1 ? w >> 16 : w & 0xFFFFu);
 }
 
+// The first n of the eight values to p, whose n-th place is 16-byte aligned (n < 8).
+__device__ __forceinline__ void store_head(uint16_t* p, const uint4& u, int n) {
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  if (n & 1) *p = static_cast<uint16_t>(u.x);
+  const uint4 v = shift_values(u, none, n & 1);
+  p += n & 1;
+  if (n & 2) *reinterpret_cast<uint32_t*>(p) = v.x;
+  const uint4 w = shift_values(v, none, n & 2);
+  p += n & 2;
+  if (n & 4) *reinterpret_cast<uint2*>(p) = make_uint2(w.x, w.y);
+}
+
+// The last n of the eight values to p, which is 16-byte aligned (n < 8).
+__device__ __forceinline__ void store_tail(uint16_t* p, const uint4& u, int n) {
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 v = shift_values(u, none, static_cast<uint32_t>(8 - n) & 7u);
+  if (n & 4) *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+  v = shift_values(v, none, n & 4);
+  p += n & 4;
+  if (n & 2) *reinterpret_cast<uint32_t*>(p) = v.x;
+  v = shift_values(v, none, n & 2);
+  p += n & 2;
+  if (n & 1) *p = static_cast<uint16_t>(v.x);
+}
+
+// What an unaligned lane writes of its n values at p and of the n_before ones before
+// them (its neighbour's, at p - 8): the aligned vector that ends its neighbour's and
+// begins its own.  off: values of the neighbour's in it.
+__device__ __forceinline__ void store_joined(uint16_t* p, const uint4& u, int n, const uint4& before,
+                                             int n_before, int off) {
+  const int own = 8 - off;
+  if (off == 0 && n == 8) {
+    *reinterpret_cast<uint4*>(p) = u;
+  } else if (off != 0 && n_before == 8 && n >= own) {
+    *reinterpret_cast<uint4*>(p - off) = shift_values(before, u, own);
+  } else {
+    if (off != 0 && n >= own)
+      store_head(p, u, own);
+    else
+      for (int i = 0; i < own && i < n; ++i) p[i] = value_of(u, i);
+    if (off != 0 && n_before == 8)
+      store_tail(p - off, before, off);
+    else
+      for (int i = own; i < n_before; ++i) p[i - 8] = value_of(before, i);
+  }
+}
+
+// The values of a span's last lane that no lane behind it writes.
+__device__ __forceinline__ void store_rest(uint16_t* p, const uint4& u, int n, int off) {
+  if (off != 0 && n == 8)
+    store_tail(p + 8 - off, u, off);
+  else
+    for (int i = 8 - off; i < n; ++i) p[i] = value_of(u, i);
+}
+
+__device__ __forceinline__ int misaligned_values(const void* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+}
+
 // The lanes' values to p, n of them each, in spans of kSpan lanes: a lane's p lies
 // 16 bytes behind that of the lane before it in the span, and no lane has values
 // where one before it has fewer than eight.  All lanes of the warp call it.
@@ -141,29 +200,15 @@ __device__ __forceinline__ void store_values(uint16_t* p, const uint4& u, int n)
   if constexpr (kAligned) {
     if (n > 0) *reinterpret_cast<uint4*>(p) = u;
   } else {
-    const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
-    const int lane = static_cast<int>(threadIdx.x) & (kSpan - 1);
+    const int off = misaligned_values(p), lane = static_cast<int>(threadIdx.x) & (kSpan - 1);
     uint4 before;
     before.x = __shfl_up_sync(0xFFFFFFFFu, u.x, 1, kSpan);
     before.y = __shfl_up_sync(0xFFFFFFFFu, u.y, 1, kSpan);
     before.z = __shfl_up_sync(0xFFFFFFFFu, u.z, 1, kSpan);
     before.w = __shfl_up_sync(0xFFFFFFFFu, u.w, 1, kSpan);
     const int n_before = __shfl_up_sync(0xFFFFFFFFu, n, 1, kSpan);
-    // The aligned vector at p - off: the last `off` values of the lane before,
-    // then the first 8 - off of this one.
-    const int own = 8 - static_cast<int>(off);
-    const uint4 v = shift_values(before, u, off == 0 ? 0 : own);
-    if (off == 0 && n == 8) {
-      *reinterpret_cast<uint4*>(p) = u;
-    } else if (off != 0 && lane > 0 && n_before == 8 && n >= own) {
-      *reinterpret_cast<uint4*>(p - off) = v;
-    } else {
-      for (int i = 0; i < own && i < n; ++i) p[i] = value_of(u, i);
-      if (lane > 0)
-        for (int i = own; i < n_before; ++i) p[i - 8] = value_of(before, i);
-    }
-    if (lane == kSpan - 1)
-      for (int i = own; i < n; ++i) p[i] = value_of(u, i);
+    store_joined(p, u, n, before, lane > 0 ? n_before : 0, off);
+    if (lane == kSpan - 1) store_rest(p, u, n, off);
   }
 }
 
@@ -177,7 +222,6 @@ struct StoreRun {
   uint16_t* last = nullptr;
 
   __device__ __forceinline__ void store(uint16_t* p, const uint4& u, int n) {
-    const uint32_t off = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u) >> 1;
     const int lane = static_cast<int>(threadIdx.x) & (kSpan - 1);
     // The lane before, or for the first one the last one's values of before.
     const bool give = lane == kSpan - 1;
@@ -189,23 +233,14 @@ struct StoreRun {
     before.z = __shfl_sync(0xFFFFFFFFu, mine.z, from, kSpan);
     before.w = __shfl_sync(0xFFFFFFFFu, mine.w, from, kSpan);
     const int n_before = __shfl_sync(0xFFFFFFFFu, give ? n_kept : n, from, kSpan);
-    const int own = 8 - static_cast<int>(off);
-    if (off == 0 && n == 8) {
-      *reinterpret_cast<uint4*>(p) = u;
-    } else if (off != 0 && n_before == 8 && n >= own) {
-      *reinterpret_cast<uint4*>(p - off) = shift_values(before, u, own);
-    } else {
-      for (int i = 0; i < own && i < n; ++i) p[i] = value_of(u, i);
-      for (int i = own; i < n_before; ++i) p[i - 8] = value_of(before, i);
-    }
+    store_joined(p, u, n, before, n_before, misaligned_values(p));
     kept = u;
     n_kept = n;
     last = p;
   }
   __device__ __forceinline__ void end() const {
     if ((static_cast<int>(threadIdx.x) & (kSpan - 1)) != kSpan - 1 || last == nullptr) return;
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(last) & 15u) >> 1);
-    for (int i = 8 - off; i < n_kept; ++i) last[i] = value_of(kept, i);
+    store_rest(last, kept, n_kept, misaligned_values(last));
   }
 };
 
