@@ -83,14 +83,10 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
       return p.base + (of < 0 ? 0 : of) * p.ldbase + c;
     };
   };
+  const WeightStage<kRankTiles, Shape::kSpans, kAlong, Shape::kAlone, kWAligned> weight(w, span, p.cols, p.rank);
   auto copy_w = [&](int turn) {
-    const int c = (Shape::kAlone ? begin_warp : begin) + turn * apart;
-    if (turn < turns && !none && !(Shape::kAlone && idle)) {
-      if constexpr (kAlong)
-        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, span, p.cols, p.rank);
-      else
-        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, span, p.cols, p.rank);
-    }
+    if (turn < turns && !none && !(Shape::kAlone && idle))
+      weight.copy(stages.shared_filling(), (Shape::kAlone ? begin_warp : begin) + turn * apart);
   };
 #pragma unroll
   for (int i = 0; i < S::kCount - 1; ++i) {

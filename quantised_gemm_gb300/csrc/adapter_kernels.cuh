@@ -278,30 +278,14 @@ __device__ __forceinline__ void copy8(void* to, const void* from, bool on) {
                : "memory");
 }
 
-// A stage of a weight whose rows lie along the long side (A, [r, cols]), filled by
-// the CTA or (kAlone) by each warp for itself: kSpans times 32 columns, `apart` apart,
-// from c on, 8 * kRankTiles ranks.  Rank j of span s is at
-// (s * 8 * kRankTiles + j) * 4, four vectors of eight columns.
-template <int kRankTiles, int kSpans, bool kAlone, bool kAligned>
-__device__ __forceinline__ void stage_ranks(uint4* to, const uint16_t* w, int c, int apart, int cols, int rank) {
-  constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
-#pragma unroll
-  for (int i0 = 0; i0 < kVecs; i0 += kThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
-    if (kVecs % kThreads != 0 && i >= kVecs) break;
-    const int span = i / (kRankTiles * 32), j = i / 4 % (8 * kRankTiles), col = c + apart * span + 8 * (i & 3);
-    const uint16_t* from = w + int64_t(j < rank ? j : 0) * cols + col;
-    if constexpr (kAligned)
-      copy16(to + i, from, j < rank && col < cols);
-    else
-      to[i] = load_values<false>(from, j < rank ? values_at(col, cols) : 0);
-  }
-}
-
-// A stage of a weight whose rows are the ranks of a column (B, [cols, r]): vectors
-// of eight ranks.  The products take the eight columns 8 (k / 2) + 2 q + k % 2 of 32
-// together, so these lie side by side, as place 8 q + k, and a column's vectors are
-// in an order turned by its place, so that the eight lie in different banks.
+// A stage of a weight, kSpans times 32 columns that lie `apart` apart and all ranks,
+// filled by the CTA or (kAlone) by each warp for itself.
+//   kColumns = false: A, [r, cols].  Rank j of span s is at (s * 8 * kRankTiles + j) * 4,
+//     four vectors of eight columns.
+//   kColumns = true: B, [cols, r], vectors of eight ranks.  The products take the
+//     eight columns 8 (k / 2) + 2 q + k % 2 of 32 together, so these lie side by side,
+//     as place 8 q + k, and a column's vectors are in an order turned by its place, so
+//     that the eight lie in different banks.
 __device__ __forceinline__ int column_place(int col) {
   return (col & ~31) + ((col >> 1 & 3) << 3) + (col >> 3 & 3) * 2 + (col & 1);
 }
@@ -310,27 +294,65 @@ __device__ __forceinline__ int place_vector(int place, int piece) {
   constexpr int kTurns = kRankTiles < 8 ? kRankTiles : 8;
   return place * kRankTiles + (piece ^ ((place & 7) * kTurns / 8));
 }
-template <int kRankTiles, int kSpans, bool kAlone, bool kAligned>
-__device__ __forceinline__ void stage_columns(uint4* to, const uint16_t* w, int c, int apart, int cols, int rank) {
-  constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
+
+template <int kRankTiles, int kSpans, bool kColumns, bool kAlone, bool kAligned>
+struct WeightStage {
+  static constexpr int kVecs = kSpans * kRankTiles * 32, kThreads = kAlone ? 32 : kAdapterThreads;
+  static constexpr int kPieces = (kVecs + kThreads - 1) / kThreads;
+  static constexpr bool kKept = kPieces <= 2;  // few enough to keep what does not change
+  struct Piece {
+    int from, col, n, to;  // offset in w, column (both from c on), values a vector has, place
+  };
+  const uint16_t* const w;
+  const int apart, cols, rank;
+  Piece kept[kKept ? kPieces : 1];
+
+  __device__ __forceinline__ WeightStage(const uint16_t* weight, int between, int columns, int ranks)
+      : w(weight), apart(between), cols(columns), rank(ranks) {
+    if constexpr (kKept) {
 #pragma unroll
-  for (int i0 = 0; i0 < kVecs; i0 += kThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x) % kThreads;
-    if (kVecs % kThreads != 0 && i >= kVecs) break;
-    const int k = i / kRankTiles, piece = i % kRankTiles, col = c + (k >> 5) * apart + (k & 31);
-    const int n = col < cols ? values_at(8 * piece, rank) : 0;
-    const uint16_t* from = w + int64_t(n > 0 ? col : 0) * rank + (n > 0 ? 8 * piece : 0);
-    uint4* put = to + place_vector<kRankTiles>(column_place(k), piece);
-    if constexpr (!kAligned) {
-      *put = load_values<false>(from, n);
-    } else if (rank % 8 == 0) {
-      copy16(put, from, n > 0);
-    } else {  // a multiple of 4
-      copy8(put, from, n > 0);
-      copy8(reinterpret_cast<uint2*>(put) + 1, n > 4 ? from + 4 : from, n > 4);
+      for (int i = 0; i < kPieces; ++i) kept[i] = piece(i);
     }
   }
-}
+  __device__ __forceinline__ Piece piece(int of) const {
+    const int i = of * kThreads + static_cast<int>(threadIdx.x) % kThreads;
+    Piece p;
+    if constexpr (kColumns) {
+      const int k = i / kRankTiles, part = i % kRankTiles;
+      p.col = (k >> 5) * apart + (k & 31);
+      p.n = values_at(8 * part, rank);
+      p.from = p.col * rank + (p.n > 0 ? 8 * part : 0);
+      p.to = place_vector<kRankTiles>(column_place(k), part);
+    } else {
+      const int j = i / 4 % (8 * kRankTiles);
+      p.col = apart * (i / (kRankTiles * 32)) + 8 * (i & 3);
+      p.n = j < rank ? 8 : 0;
+      p.from = (j < rank ? j : 0) * cols + p.col;
+      p.to = i;
+    }
+    if (kVecs % kThreads != 0 && i >= kVecs) p.n = -1;  // no such vector
+    return p;
+  }
+  // Columns c on into a stage.
+  __device__ __forceinline__ void copy(uint4* to, int c) const {
+    const uint16_t* const at = w + (kColumns ? int64_t(c) * rank : int64_t(c));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const Piece p = kKept ? kept[kKept ? i : 0] : piece(i);
+      if (kVecs % kThreads != 0 && p.n < 0) continue;
+      const bool on = p.n > 0 && c + p.col < cols;
+      const uint16_t* const from = at + p.from;
+      if constexpr (!kAligned) {
+        to[p.to] = load_values<false>(from, !on ? 0 : kColumns ? p.n : values_at(c + p.col, cols));
+      } else if (!kColumns || rank % 8 == 0) {
+        copy16(to + p.to, from, on);
+      } else {  // a multiple of 4
+        copy8(to + p.to, from, on);
+        copy8(reinterpret_cast<uint2*>(to + p.to) + 1, p.n > 4 ? from + 4 : from, on && p.n > 4);
+      }
+    }
+  }
+};
 
 // ---------------------------------------------------------------- launching
 

@@ -84,14 +84,10 @@ __global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 8 ? 2 : 1)
       return from[v >> 1][v & 1] + c;
     };
   };
+  const WeightStage<kRankTiles, Shape::kSpans, !kAlong, Shape::kAlone, kWAligned> weight(w, 32, p.cols, p.rank);
   auto copy_w = [&](int turn) {
-    const int c = first + turn * step + (Shape::kAlone ? 32 * col_warp : 0);
-    if (turn < turns && !(Shape::kAlone && idle)) {
-      if constexpr (kAlong)
-        stage_ranks<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, 32, p.cols, p.rank);
-      else
-        stage_columns<kRankTiles, Shape::kSpans, Shape::kAlone, kWAligned>(stages.shared_filling(), w, c, 32, p.cols, p.rank);
-    }
+    if (turn < turns && !(Shape::kAlone && idle))
+      weight.copy(stages.shared_filling(), first + turn * step + (Shape::kAlone ? 32 * col_warp : 0));
   };
 #pragma unroll
   for (int i = 0; i < S::kCount - 1; ++i) {
