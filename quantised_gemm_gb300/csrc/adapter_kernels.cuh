@@ -98,9 +98,10 @@ struct RowTile {
 };
 
 // Tile `want` of tiles of `size` rows of one group each (a group without rows has
-// none); behind the last one, with kEmpty, the groups without rows, a tile of none
-// each.  All lanes of a warp call it and get the same.
-template <bool kEmpty = false>
+// none).  kEven: a group's tiles have as many rows each, but for rounding up to 16,
+// and behind the last tile come the groups without rows, a tile of none each.  All
+// lanes of a warp call it and get the same.
+template <bool kEven = false>
 __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int size, int want) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
   int before = 0, several_before = 0, blocks_before = 0;
@@ -133,16 +134,19 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
       t.group = base + at;
       t.only = __shfl_sync(0xFFFFFFFFu, tiles, at) == 1;
       t.slot = several_before + __shfl_sync(0xFFFFFFFFu, several_up - several, at) + inside;
-      t.block = blocks_before + __shfl_sync(0xFFFFFFFFu, blocks_up - blocks, at) + inside * (size / 16);
-      t.begin = __shfl_sync(0xFFFFFFFFu, begin, at) + inside * size;
-      t.count = min(size, __shfl_sync(0xFFFFFFFFu, count, at) - inside * size);
+      int each = size;
+      if (kEven && tiles > 0) each = ((count + tiles - 1) / tiles + 15) / 16 * 16;
+      each = __shfl_sync(0xFFFFFFFFu, each, at);
+      t.block = blocks_before + __shfl_sync(0xFFFFFFFFu, blocks_up - blocks, at) + inside * (each / 16);
+      t.begin = __shfl_sync(0xFFFFFFFFu, begin, at) + inside * each;
+      t.count = min(each, __shfl_sync(0xFFFFFFFFu, count, at) - inside * each);
       return t;
     }
     before += __shfl_sync(0xFFFFFFFFu, up, 31);
     several_before += __shfl_sync(0xFFFFFFFFu, several_up, 31);
     blocks_before += __shfl_sync(0xFFFFFFFFu, blocks_up, 31);
   }
-  if constexpr (kEmpty) {
+  if constexpr (kEven) {
     int skip = want - before;
     for (int base = 0; base < groups; base += 32) {
       const int g = base + lane;

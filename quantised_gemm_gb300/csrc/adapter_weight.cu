@@ -165,16 +165,17 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
     next_low += kStep;
     if (packed != nullptr) packed += S::kRowWarps * kBlock;
   };
-  int number[2], later[2];
+  int numbers[kBefore + 2][2];
+#pragma unroll
+  for (int i = 0; i < kBefore + 2; ++i) find(numbers[i], i);
 #pragma unroll
   for (int i = 0; i < kBefore; ++i) {
+    stages.copy(x_of(numbers[i]));
     copy_low();
-    find(number, i);
-    stages.copy(x_of(number));
     stages.filled();
   }
-  find(number, kBefore);
-  find(later, kBefore + 1);
+  int number[2] = {numbers[kBefore][0], numbers[kBefore][1]};
+  int later[2] = {numbers[kBefore + 1][0], numbers[kBefore + 1][1]};
   for (int turn = 0; turn < turns; ++turn, stages.next()) {
     stages.wait();
     if constexpr (!kAligned) {
@@ -274,6 +275,7 @@ struct SumArgs {
   int64_t size;  // cols * rank
   int tile_rows;
   Route route;
+  bool vectors;  // four numbers at a time
 };
 constexpr int kSumThreads = 256;
 
@@ -294,7 +296,23 @@ __device__ __forceinline__ void sum_partials(const SumArgs& p, int group, int bl
   if (mine <= 1) return;  // written already
   uint16_t* const dw = p.dw + group * p.size;
   const float* const from = p.partials + before * p.size;
-  for (int64_t i = int64_t(block) * kSumThreads + threadIdx.x; i < p.size; i += int64_t(blocks) * kSumThreads) {
+  const int64_t first = int64_t(block) * kSumThreads + threadIdx.x, step = int64_t(blocks) * kSumThreads;
+  if (p.vectors) {
+    for (int64_t i = first; i < p.size / 4; i += step) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int s = 0; s < mine; ++s) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(from + s * p.size) + i);
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      reinterpret_cast<uint2*>(dw)[i] = make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
+    }
+    return;
+  }
+  for (int64_t i = first; i < p.size; i += step) {
     float v = 0.0f;
 #pragma unroll 8
     for (int s = 0; s < mine; ++s) v += __ldcg(from + s * p.size + i);
@@ -324,9 +342,9 @@ int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes,
     return cudaSuccess;
   });
   const int64_t slabs = (cols + slab - 1) / slab;
-  // Three CTAs an SM; tiles of 256 rows at least, fewer of which are no faster than
+  // Two CTAs an SM; tiles of 256 rows at least, fewer of which are no faster than
   // their sum.
-  int64_t rows = (a.rows * slabs + 3 * dev.num_sms - 1) / (3 * dev.num_sms);
+  int64_t rows = (a.rows * slabs + 2 * dev.num_sms - 1) / (2 * dev.num_sms);
   rows = rows < 256 ? 256 : (rows + 127) / 128 * 128;
   // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
   // them, and at most a.rows / rows and one for each adapter.
@@ -401,6 +419,7 @@ cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, co
     s.dw = j.dw;
     s.partials = j.partials;
     s.size = cols * a.rank;
+    s.vectors = s.size % 4 == 0 && (reinterpret_cast<uintptr_t>(j.dw) & 7u) == 0;
     s.tile_rows = static_cast<int>(j.tile_rows);
     s.route = route_of(a);
     return s;
@@ -408,7 +427,7 @@ cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, co
   const SumArgs sa = job(da, a.k), sb = job(db, a.n);
   auto blocks = [&](const SumArgs& s) {
     if (s.dw == nullptr) return 0;
-    const int64_t n = (s.size + kSumThreads - 1) / kSumThreads;
+    const int64_t n = ((s.vectors ? s.size / 4 : s.size) + kSumThreads - 1) / kSumThreads;
     return static_cast<int>(n < 1024 ? n : 1024);
   };
   const int na = blocks(sa), nb = blocks(sb);
