@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 // One row a cluster: each CTA takes a part of K for the low product, the parts'
 // sums go to every CTA of the cluster through distributed shared memory, and
 // each CTA takes a part of N for the high product.  Bound by reading A and B
-// once, and by latency: one launch.
+// once, and by latency: one launch.  32 x 4096 x 14336 with rank 16 and an adapter a
+// row: 6.6 us (9.7 with B loaded after the low product), one row 5.0.
 struct FewArgs {
   const uint16_t *x, *a, *b, *base;
   uint16_t* y;

@@ -414,9 +414,6 @@ inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t size) {
   return t < rows ? t : rows;
 }
 
-// Whether an adapter has rows for tiles of several warps, on average.
-inline bool wide_tiles(const AdapterArgs& a) { return a.rows >= 64 * a.count; }
-
 inline Route route_of(const AdapterArgs& a) {
   return Route{a.route, a.route + a.count + 2, static_cast<int>(a.count) + 1};
 }
