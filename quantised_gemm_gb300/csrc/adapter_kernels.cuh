@@ -92,19 +92,14 @@ struct RowTile {
   int group;  // -1: no such tile
   int begin;  // in rows[]
   int count;
-  int slot;   // index among the tiles of groups with several
   int block;  // index of its first 16 rows among the blocks of 16 of all groups
-  bool only;  // the group's only tile
 };
 
-// Tile `want` of tiles of `size` rows of one group each (a group without rows has
-// none).  kEven: a group's tiles have as many rows each, but for rounding up to 16,
-// and behind the last tile come the groups without rows, a tile of none each.  All
-// lanes of a warp call it and get the same.
-template <bool kEven = false>
+// Tile `want` of tiles of `size` rows (a multiple of 16) of one group each; a group
+// without rows has none.  All lanes of a warp call it and get the same.
 __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int size, int want) {
   const int lane = static_cast<int>(threadIdx.x & 31u);
-  int before = 0, several_before = 0, blocks_before = 0;
+  int before = 0, blocks_before = 0;
   for (int base = 0; base < groups; base += 32) {
     const int g = base + lane;
     int begin = 0, count = 0;
@@ -112,18 +107,15 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
       begin = __ldg(r.first + g);
       count = __ldg(r.first + g + 1) - begin;
     }
-    const int tiles = (count + size - 1) / size, several = tiles > 1 ? tiles : 0;
-    const int blocks = (count + 15) / 16;
-    int up = tiles, several_up = several, blocks_up = blocks;
+    const int tiles = (count + size - 1) / size, blocks = (count + 15) / 16;
+    int up = tiles, blocks_up = blocks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int a = __shfl_up_sync(0xFFFFFFFFu, up, o);
-      const int b = __shfl_up_sync(0xFFFFFFFFu, several_up, o);
-      const int c = __shfl_up_sync(0xFFFFFFFFu, blocks_up, o);
+      const int b = __shfl_up_sync(0xFFFFFFFFu, blocks_up, o);
       if (lane >= o) {
         up += a;
-        several_up += b;
-        blocks_up += c;
+        blocks_up += b;
       }
     }
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before + up > want);
@@ -132,35 +124,30 @@ __device__ __forceinline__ RowTile find_tile(const Route& r, int groups, int siz
       const int inside = want - before - __shfl_sync(0xFFFFFFFFu, up - tiles, at);
       RowTile t;
       t.group = base + at;
-      t.only = __shfl_sync(0xFFFFFFFFu, tiles, at) == 1;
-      t.slot = several_before + __shfl_sync(0xFFFFFFFFu, several_up - several, at) + inside;
-      int each = size;
-      if (kEven && tiles > 0) each = ((count + tiles - 1) / tiles + 15) / 16 * 16;
-      each = __shfl_sync(0xFFFFFFFFu, each, at);
-      t.block = blocks_before + __shfl_sync(0xFFFFFFFFu, blocks_up - blocks, at) + inside * (each / 16);
-      t.begin = __shfl_sync(0xFFFFFFFFu, begin, at) + inside * each;
-      t.count = min(each, __shfl_sync(0xFFFFFFFFu, count, at) - inside * each);
+      t.block = blocks_before + __shfl_sync(0xFFFFFFFFu, blocks_up - blocks, at) + inside * (size / 16);
+      t.begin = __shfl_sync(0xFFFFFFFFu, begin, at) + inside * size;
+      t.count = min(size, __shfl_sync(0xFFFFFFFFu, count, at) - inside * size);
       return t;
     }
     before += __shfl_sync(0xFFFFFFFFu, up, 31);
-    several_before += __shfl_sync(0xFFFFFFFFu, several_up, 31);
     blocks_before += __shfl_sync(0xFFFFFFFFu, blocks_up, 31);
   }
-  if constexpr (kEven) {
-    int skip = want - before;
-    for (int base = 0; base < groups; base += 32) {
-      const int g = base + lane;
-      const bool empty = g < groups && __ldg(r.first + g) == __ldg(r.first + g + 1);
-      uint32_t mask = __ballot_sync(0xFFFFFFFFu, empty);
-      if (skip >= __popc(mask)) {
-        skip -= __popc(mask);
-        continue;
-      }
-      for (; skip > 0; --skip) mask &= mask - 1;
-      return RowTile{base + __ffs(static_cast<int>(mask)) - 1, 0, 0, 0, 0, true};
-    }
-  }
-  return RowTile{-1, 0, 0, 0, 0, false};
+  return RowTile{-1, 0, 0, 0};
+}
+
+// Part `part` of `parts` of a group's rows, as many blocks of 16 each but for the last.
+__device__ __forceinline__ RowTile group_part(const Route& r, int group, int part, int parts) {
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  int blocks = 0;
+  for (int g = lane; g < group; g += 32) blocks += (__ldg(r.first + g + 1) - __ldg(r.first + g) + 15) / 16;
+  const int begin = __ldg(r.first + group), count = __ldg(r.first + group + 1) - begin;
+  const int each = ((count + 15) / 16 + parts - 1) / parts * 16;
+  RowTile t;
+  t.group = group;
+  t.block = __reduce_add_sync(0xFFFFFFFFu, blocks) + part * (each / 16);
+  t.begin = begin + part * each;
+  t.count = max(min(each, count - part * each), 0);
+  return t;
 }
 
 // ---------------------------------------------------------------- stages

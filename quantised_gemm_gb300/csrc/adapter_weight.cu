@@ -2,35 +2,33 @@
 //   dw[c][j] = sum over the rows i of one adapter of x[i][c] s_a low[i][j]
 // dB (x = dy, low = h) and dA (x the input, low = dh) in one launch.
 //
-// Bound by reading x again: 16384 rows of 14336 and 4096 columns with rank 16 take 123
-// us (4.9 TB/s), half of the last wave of CTAs idle, as the adapters' rows do not
-// divide evenly among them (smaller tiles cost more in partial sums than they give:
-// 268 instead of 259 us for the whole backward with three times as many).
+// Bound by reading x again: 16384 rows of 14336 and 4096 columns with rank 16 take some
+// 110 us (5.5 TB/s).  A cluster shares the rows of a large adapter; partial sums in
+// the workspace and a launch that adds them took 259 us instead of 248 for the whole
+// backward, and 510 instead of 357 for 8192 x 4096 x 4096 with rank 128.
 #include "adapter_kernels.cuh"
 
 namespace fp8lin {
 namespace {
 
-// A tile of rows of one adapter and a slab of columns.  The CTA's warps take
-// blocks of 16 rows side by side (kRowWarps of them) and columns side by side (the
-// others); a tile that is its adapter's only one is written as bf16 into dw, else
-// its sums go to the partials, one slot a tile, which adapter_sum_kernel adds up.
-// An adapter without rows has a tile too: zeros.
+// A slab of columns of one adapter's gradient, by a CTA or by a cluster of them that
+// share the adapter's rows.  The CTA's warps take blocks of 16 rows side by side
+// (kRowWarps of them) and columns side by side (the others); their sums meet in
+// shared memory, and those of a cluster's CTAs in distributed shared memory.
 struct WeightArgs {
   const uint16_t* x;
   int64_t ldx;
   const float* low;
   const float* scale;  // null: 1
   uint16_t* dw;
-  float* partials;  // [slot][cols * rank]
-  int cols, rank, tile_rows, tiles, slabs;
+  int cols, rank, slabs;
   const uint4* packed;  // low as adapter_pack_kernel left it, or null
   bool along;    // dw is [cols, r] (dB), else [r, cols] (dA)
   bool aligned;  // x's rows
 };
 
-// With a small rank the rows' numbers are few beside x, and splitting the rows
-// leaves fewer partial sums; with a large one warps of the same rows share them.
+// With a small rank the rows' numbers are few beside x, and splitting the rows leaves
+// fewer CTAs to a cluster; with a large one warps of the same rows share them.
 template <int kRankTiles>
 struct WeightShape {
   static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
@@ -38,11 +36,12 @@ struct WeightShape {
   static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
   static constexpr int kSlab = 32 * kChunks * kColWarps;
   static constexpr int kSums = 2 * kChunks * kRankTiles * 4;  // a lane's
+  static constexpr int kCtaSums = kRowWarps > 1 ? kSums : 1;  // that warps of a CTA add up
   static constexpr bool kAlone = kRankTiles <= 2;  // each warp has its own low operands
   static constexpr int kShared = (kAlone ? 1 : kRowWarps) * kRankTiles * 32;  // of a turn
   template <bool kAligned>
   // More stages than 80 KB hold cost a short sum more than they give a long one.
-  using T = Stages<stages_in(kAlone ? kStageRoom - 16 * 1024 : kStageRoom,
+  using T = Stages<stages_in(kAlone ? kStageRoom - 16 * 1024 : kRankTiles == 4 ? kStageRoom - 32 * 1024 : kStageRoom,
                              sizeof(uint4) * ((kAligned ? 2 : 4) * kChunks * kAdapterThreads +
                                               (kAlone ? kAdapterWarps : 1) * kShared)),
                    2 * kChunks, kShared, kAlone, kAligned, true>;
@@ -95,16 +94,16 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 
 template <int kRankTiles, bool kAligned>
 __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& route, int block,
-                                            float (*sums)[WeightShape<kRankTiles>::kSums][32],
+                                            int part, int parts,
+                                            float (*sums)[WeightShape<kRankTiles>::kCtaSums][32],
                                             uint4* shared) {
   using S = WeightShape<kRankTiles>;
   constexpr int kChunks = S::kChunks, kSums = S::kSums;
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int col_warp = warp % S::kColWarps, row_warp = warp / S::kColWarps;
   const int g = lane >> 2, t = lane & 3;
-  const RowTile tile = find_tile<true>(route, route.groups - 1, p.tile_rows, block / p.slabs);
-  if (tile.group < 0) return;
-  const int col0 = ((block % p.slabs) * S::kColWarps + col_warp) * 32 * kChunks;
+  const RowTile tile = group_part(route, block / p.slabs, part, parts);
+  const int slab0 = block % p.slabs * S::kSlab, col0 = slab0 + col_warp * 32 * kChunks;
   const float scale = p.scale != nullptr ? __ldg(p.scale + tile.group) : 1.0f;
   float acc[2 * kChunks][kRankTiles][4];
 #pragma unroll
@@ -227,142 +226,68 @@ __device__ __forceinline__ void weight_tile(const WeightArgs& p, const Route& ro
       __syncthreads();
     }
   }
-  if (row_warp != 0 || col0 >= p.cols) return;
-  const int64_t size = int64_t(p.cols) * p.rank;
-  uint16_t* const dw = p.dw + tile.group * size;
-  float* const part = tile.only ? nullptr : p.partials + tile.slot * size;
-  // A lane has of product (m, j) columns 16 m + g and 16 m + g + 8 of ranks 8 j + 2 t and
-  // the next.
+  uint16_t* const dw = p.dw + tile.group * (int64_t(p.cols) * p.rank);
+  // Number i of a lane of col_warp: product (m, j) has columns 16 m + g and 16 m + g + 8
+  // of ranks 8 j + 2 t and the next.
+  auto put = [&](int of_warp, int i, float v) {
+    const int m = i / (4 * kRankTiles), j = i / 4 % kRankTiles, e = i % 4;
+    const int col = slab0 + of_warp * 32 * kChunks + 16 * m + 8 * (e >> 1) + g, rank = 8 * j + 2 * t + (e & 1);
+    if (col >= p.cols || rank >= p.rank) return;
+    dw[p.along ? int64_t(col) * p.rank + rank : int64_t(rank) * p.cols + col] =
+        static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+  };
+  if (parts == 1) {
+    if (row_warp != 0) return;
 #pragma unroll
-  for (int m = 0; m < 2 * kChunks; ++m)
+    for (int m = 0; m < 2 * kChunks; ++m)
 #pragma unroll
-    for (int j = 0; j < kRankTiles; ++j)
+      for (int j = 0; j < kRankTiles; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = col0 + 16 * m + 8 * (i >> 1) + g, rank = 8 * j + 2 * t + (i & 1);
-        if (col >= p.cols || rank >= p.rank) continue;
-        const int64_t to = p.along ? int64_t(col) * p.rank + rank : int64_t(rank) * p.cols + col;
-        if (part != nullptr)
-          part[to] = acc[m][j][i];
-        else
-          dw[to] = static_cast<uint16_t>(cvt_bf16x2(acc[m][j][i], 0.0f) & 0xFFFFu);
-      }
+        for (int i = 0; i < 4; ++i) put(col_warp, (m * kRankTiles + j) * 4 + i, acc[m][j][i]);
+    return;
+  }
+  // The cluster's sums: every CTA adds a part of the numbers, in the CTAs' order.
+  __syncthreads();  // the stages are read
+  float* const of_cta = reinterpret_cast<float*>(shared);
+  if (row_warp == 0) {
+    const float* const mine = &acc[0][0][0];
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) of_cta[(col_warp * kSums + i) * 32 + lane] = mine[i];
+  }
+  cluster_sync_all();
+  constexpr int kAll = S::kColWarps * kSums;
+  const int each = (kAll + parts - 1) / parts, last = min((part + 1) * each, kAll);
+  for (int k = part * each + warp; k < last; k += kAdapterWarps) {
+    const uint32_t at = smem_addr(of_cta + k * 32 + lane);
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int cta = 0; cta < parts; ++cta) sum += __uint_as_float(ld_shared_cluster_u32(map_to_cta(at, cta)));
+    put(k / kSums, k % kSums, sum);
+  }
+  cluster_sync_all();
 }
 
 // dB (blocks from 0 on) and dA (the others) in one launch; either may have none.
 template <int kRankTiles>
-__global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kAdapterThreads, kRankTiles <= 8 ? 2 : 1)
     adapter_weight_kernel(const __grid_constant__ WeightArgs db, const __grid_constant__ WeightArgs da,
-                          const Route route, bool early) {
-  // early: the launch before this one writes nothing that this one touches, and all
-  // before that is done once its CTAs let this one begin.  The wait then comes at the
-  // end, so that what follows still finds everything before it done.
-  if (!early) griddep_wait();
+                          const Route route, int parts) {
+  griddep_wait();
   griddep_launch_dependents();
-  const int block = static_cast<int>(blockIdx.x), first = db.tiles * db.slabs;
+  const int block = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
+  const int first = db.slabs * (route.groups - 1);
   const bool is_db = block < first;
   using S = WeightShape<kRankTiles>;
   extern __shared__ uint4 shared[];
-  __shared__ float sums[S::kRowWarps > 1 ? kAdapterWarps / 2 : 1][S::kSums][32];
+  __shared__ float sums[S::kRowWarps > 1 ? kAdapterWarps / 2 : 1][S::kCtaSums][32];
   const WeightArgs& p = is_db ? db : da;
   if (p.aligned)
-    weight_tile<kRankTiles, true>(p, route, is_db ? block : block - first, sums, shared);
+    weight_tile<kRankTiles, true>(p, route, is_db ? block : block - first, part, parts, sums, shared);
   else
-    weight_tile<kRankTiles, false>(p, route, is_db ? block : block - first, sums, shared);
-  if (early) griddep_wait();
-}
-
-// The partials of adapters with several tiles, added in order.  One CTA row an
-// adapter.
-struct SumArgs {
-  const float* partials;
-  uint16_t* dw;
-  int64_t size;  // cols * rank
-  int tile_rows;
-  Route route;
-  bool vectors;  // four numbers at a time
-};
-constexpr int kSumThreads = 256;
-
-__device__ __forceinline__ void sum_partials(const SumArgs& p, int group, int block, int blocks) {
-  // Slots before this adapter's: a sum over the groups before it.
-  int mine = 0, before = 0;
-  const int lane = static_cast<int>(threadIdx.x & 31u);
-  for (int g = lane; g <= group; g += 32) {
-    const int count = __ldg(p.route.first + g + 1) - __ldg(p.route.first + g);
-    const int tiles = (count + p.tile_rows - 1) / p.tile_rows;
-    if (g == group)
-      mine = tiles;
-    else if (tiles > 1)
-      before += tiles;
-  }
-  before = __reduce_add_sync(0xFFFFFFFFu, before);
-  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  if (mine <= 1) return;  // written already
-  uint16_t* const dw = p.dw + group * p.size;
-  const float* const from = p.partials + before * p.size;
-  const int64_t first = int64_t(block) * kSumThreads + threadIdx.x, step = int64_t(blocks) * kSumThreads;
-  if (p.vectors) {
-    for (int64_t i = first; i < p.size / 4; i += step) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int s = 0; s < mine; ++s) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(from + s * p.size) + i);
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
-      }
-      reinterpret_cast<uint2*>(dw)[i] = make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
-    }
-    return;
-  }
-  for (int64_t i = first; i < p.size; i += step) {
-    float v = 0.0f;
-#pragma unroll 8
-    for (int s = 0; s < mine; ++s) v += __ldcg(from + s * p.size + i);
-    dw[i] = static_cast<uint16_t>(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
-  }
-}
-
-__global__ void __launch_bounds__(kSumThreads) adapter_sum_kernel(const __grid_constant__ SumArgs a,
-                                                                  const __grid_constant__ SumArgs b,
-                                                                  int blocks_a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int block = static_cast<int>(blockIdx.x), group = static_cast<int>(blockIdx.y);
-  if (block < blocks_a)
-    sum_partials(a, group, block, blocks_a);
-  else
-    sum_partials(b, group, block - blocks_a, static_cast<int>(gridDim.x) - blocks_a);
+    weight_tile<kRankTiles, false>(p, route, is_db ? block : block - first, part, parts, sums, shared);
 }
 
 }  // namespace
-
-int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev) {
-  const int64_t cols = da ? a.k : a.n;
-  int64_t slab = 0;
-  with_rank_tiles(a.rank, [&](auto ranks) {
-    slab = WeightShape<decltype(ranks)::value>::kSlab;
-    return cudaSuccess;
-  });
-  const int64_t slabs = (cols + slab - 1) / slab;
-  // Two CTAs an SM; tiles of 256 rows at least, fewer of which are no faster than
-  // their sum.
-  int64_t rows = (a.rows * slabs + 2 * dev.num_sms - 1) / (2 * dev.num_sms);
-  rows = rows < 256 ? 256 : (rows + 127) / 128 * 128;
-  // The tiles of adapters with several need a slot each: at most 2 a.rows / rows of
-  // them, and at most a.rows / rows and one for each adapter.
-  const int64_t slots = static_cast<int64_t>(partial_bytes / (sizeof(float) * static_cast<size_t>(cols) * a.rank));
-  if (slots < 2) return a.rows;  // no room: every adapter's rows in one tile
-  int64_t least = (2 * a.rows + slots - 1) / slots;
-  if (slots > a.count) {
-    const int64_t other = (a.rows + slots - a.count - 1) / (slots - a.count);
-    if (other < least) least = other;
-  }
-  if (rows < least) rows = (least + 15) / 16 * 16;
-  return rows < a.rows ? rows : a.rows;
-}
 
 size_t adapter_packed_bytes(const AdapterArgs& a) {
   return static_cast<size_t>(most_tiles(a.rows, a.count, 16)) * rank_tiles(a.rank) * 32 * sizeof(uint4);
@@ -383,11 +308,11 @@ cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, c
 }
 
 cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                  bool early, const DeviceInfo& dev, cudaStream_t stream) {
+                                  const DeviceInfo& dev, cudaStream_t stream) {
   set_error_site("adapter_weight_kernel");
   return with_rank_tiles(a.rank, [&](auto ranks) {
     constexpr int kRankTiles = decltype(ranks)::value;
-    constexpr int kSlab = WeightShape<kRankTiles>::kSlab;
+    using S = WeightShape<kRankTiles>;
     auto job = [&](const AdapterWeight& j, bool is_da) {
       WeightArgs p = {};
       if (j.dw == nullptr) return p;
@@ -396,48 +321,32 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
       p.low = j.low;
       p.scale = is_da ? nullptr : a.scale;
       p.dw = j.dw;
-      p.partials = j.partials;
       p.cols = static_cast<int>(is_da ? a.k : a.n);
       p.rank = a.rank;
-      p.tile_rows = static_cast<int>(j.tile_rows);
       p.packed = static_cast<const uint4*>(j.packed);
-      p.tiles = static_cast<int>(a.rows / j.tile_rows + a.count);
-      p.slabs = (p.cols + kSlab - 1) / kSlab;
+      p.slabs = (p.cols + S::kSlab - 1) / S::kSlab;
       p.along = !is_da;
       p.aligned = rows_aligned(j.x, j.ldx, p.cols);
       return p;
     };
     const WeightArgs b = job(db, false), c = job(da, true);
-    const dim3 grid(static_cast<unsigned>(int64_t(b.tiles) * b.slabs + int64_t(c.tiles) * c.slabs));
-    using S = WeightShape<kRankTiles>;
+    const int64_t slabs = (int64_t(b.slabs) + c.slabs) * a.count;
+    // More CTAs than are resident, so that an adapter with many rows does not keep the
+    // others waiting, but with enough rows each for their start and their sums.  The
+    // whole backward with four CTAs an SM and with eight: 16384 x 4096 x 14336, rank
+    // 16, 248 and 264 us; 4096 x 4096 x 4096, rank 64, 124 and 117.  With 128 rows and
+    // with 256: 1267 x 1600 x 2501, rank 12, 28 and 33; 1024 x 4096 x 4096, rank 64, 58
+    // and 51.
+    const int64_t most = (a.rank <= 32 ? 4 : 8) * int64_t(dev.num_sms), least = a.rank <= 16 ? 128 : 256;
+    int parts = 1;
+    while (parts < 8 && slabs * parts * 2 <= most && a.rows >= least * 2 * parts * a.count) parts *= 2;
+    const dim3 grid(static_cast<unsigned>(slabs * parts));
     constexpr size_t kA = S::template T<true>::kBytes, kB = S::template T<false>::kBytes;
-    return launch_staged<adapter_weight_kernel<kRankTiles>>(grid, kA > kB ? kA : kB, dev, stream, 1, b, c,
-                                                            route_of(a), early);
+    constexpr size_t kSum = sizeof(float) * 32 * S::kColWarps * S::kSums;
+    constexpr size_t kStages = kA > kB ? kA : kB;
+    return launch_staged<adapter_weight_kernel<kRankTiles>>(grid, kStages > kSum ? kStages : kSum, dev, stream, parts,
+                                                            b, c, route_of(a), parts);
   });
-}
-
-cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                               cudaStream_t stream) {
-  set_error_site("adapter_sum_kernel");
-  auto job = [&](const AdapterWeight& j, int64_t cols) {
-    SumArgs s = {};
-    s.dw = j.dw;
-    s.partials = j.partials;
-    s.size = cols * a.rank;
-    s.vectors = s.size % 4 == 0 && (reinterpret_cast<uintptr_t>(j.dw) & 7u) == 0;
-    s.tile_rows = static_cast<int>(j.tile_rows);
-    s.route = route_of(a);
-    return s;
-  };
-  const SumArgs sa = job(da, a.k), sb = job(db, a.n);
-  auto blocks = [&](const SumArgs& s) {
-    if (s.dw == nullptr) return 0;
-    const int64_t n = ((s.vectors ? s.size / 4 : s.size) + kSumThreads - 1) / kSumThreads;
-    return static_cast<int>(n < 1024 ? n : 1024);
-  };
-  const int na = blocks(sa), nb = blocks(sb);
-  return launch_kernel(adapter_sum_kernel, dim3(static_cast<unsigned>(na + nb), static_cast<unsigned>(a.count)),
-                       dim3(kSumThreads), 0, stream, 1, false, sa, sb, na);
 }
 
 }  // namespace fp8lin

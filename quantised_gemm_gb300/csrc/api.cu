@@ -1837,7 +1837,7 @@ fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, in
     if (e != cudaSuccess) return cuda_fail(e);
   }
   ProfScope ps(FP8LIN_PROF_GEMM, stream);
-  cudaError_t e = launch_adapter_high(a, false, h, bases, ldbase, ys, ldy, dev, stream);
+  cudaError_t e = launch_adapter_high(a, false, h, bases, ldbase, ys, ldy, false, dev, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 
@@ -1882,63 +1882,45 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
   }
   // The weight gradients' operands from h and dh, laid out once where the rows pay for
   // that launch (16384 x 4096 x 14336 with rank 16: 256 us with it, 363 without; 1024 x
-  // 4096 x 4096: 31 and 33; 256 rows: 16.8 and 16.5) and they leave three quarters of
-  // the room for the partial sums.
+  // 4096 x 4096: 31 and 33; 256 rows: 16.8 and 16.5) and the workspace has room.
   AdapterWeight wa, wb;
-  const size_t packed = adapter_packed_bytes(a);
-  if ((da != nullptr || db != nullptr) && rows >= 512 && 8 * packed <= room_bytes) {
-    for (AdapterWeight* w : {&wa, &wb}) {
-      if ((w == &wa ? da : db) == nullptr) continue;
-      w->packed = room;
-      room += packed;
-      room_bytes -= packed;
-    }
-  }
-  // The room for partial sums: shared as the sizes of dA and dB are.
-  const size_t for_da = da == nullptr ? 0
-                        : db == nullptr
-                            ? room_bytes
-                            : static_cast<size_t>(static_cast<double>(room_bytes) * ad->k / (ad->k + ad->n)) / 256 * 256;
   if (da != nullptr) {
     wa.dw = static_cast<uint16_t*>(da);
     wa.x = static_cast<const uint16_t*>(x);
     wa.ldx = ldx;
     wa.low = dh;
-    wa.tile_rows = adapter_weight_rows(a, true, for_da, dev);
-    wa.partials = reinterpret_cast<float*>(room);
   }
   if (db != nullptr) {
     wb.dw = static_cast<uint16_t*>(db);
     wb.x = dys;
     wb.ldx = lddy;
     wb.low = h;
-    wb.tile_rows = adapter_weight_rows(a, false, room_bytes - for_da, dev);
-    wb.partials = reinterpret_cast<float*>(room + for_da);
+  }
+  const size_t packed = (adapter_packed_bytes(a) + 255) / 256 * 256;
+  for (AdapterWeight* w : {&wa, &wb}) {
+    if (w->dw == nullptr || rows < 512 || packed > room_bytes) continue;
+    w->packed = room;
+    room += packed;
+    room_bytes -= packed;
   }
   if (wa.packed != nullptr || wb.packed != nullptr) {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
     e = launch_adapter_pack(a, wb, wa, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  if (dx != nullptr) {
+  const bool weights = da != nullptr || db != nullptr;
+  if (weights) {
+    ProfScope ps(FP8LIN_PROF_GEMM, stream);
+    e = launch_adapter_weight(a, wb, wa, dev, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (dx != nullptr) {  // beside the weight gradients
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
     e = launch_adapter_high(a, true, dh, static_cast<const uint16_t*>(base), ldbase,
-                            static_cast<uint16_t*>(dx), lddx, dev, stream);
+                            static_cast<uint16_t*>(dx), lddx, weights, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  if (da == nullptr && db == nullptr) return FP8LIN_OK;
-  {
-    ProfScope ps(FP8LIN_PROF_GEMM, stream);
-    e = launch_adapter_weight(a, wb, wa, dx != nullptr, dev, stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  // A gradient without partial sums leaves the sum nothing to do.
-  if (wa.tile_rows >= rows) wa.dw = nullptr;
-  if (wb.tile_rows >= rows) wb.dw = nullptr;
-  if (wa.dw == nullptr && wb.dw == nullptr) return FP8LIN_OK;
-  ProfScope ps(FP8LIN_PROF_GEMM, stream);
-  e = launch_adapter_sum(a, wb, wa, stream);
-  return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
+  return FP8LIN_OK;
 }
 
 uint64_t fp8lin_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

@@ -494,30 +494,24 @@ cudaError_t launch_adapter_few(const AdapterArgs& a, const int32_t* index, const
 // low = x A^T, or (backward) low = s x B with x the output's gradient.
 cudaError_t launch_adapter_low(const AdapterArgs& a, bool backward, const uint16_t* x, int64_t ldx,
                                float* low, const DeviceInfo& dev, cudaStream_t stream);
-// y = base + s low B^T, or (backward) y = base + low A.
+// y = base + s low B^T, or (backward) y = base + low A.  early: the launch before it in
+// the stream is the adapters' and touches neither low nor y.
 cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
                                 const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
-                                const DeviceInfo& dev, cudaStream_t stream);
+                                bool early, const DeviceInfo& dev, cudaStream_t stream);
 // One of dA (x the input, low = dh) and dB (x the output's gradient, low = h); dw
-// null: not wanted.  Tiles of adapter_weight_rows rows; an adapter with several
-// leaves partials, one slot of cols * rank numbers a tile, for
-// launch_adapter_sum (none does where tile_rows is the number of rows).
+// null: not wanted.
 struct AdapterWeight {
   uint16_t* dw = nullptr;
   const uint16_t* x = nullptr;
   int64_t ldx = 0;
   const float* low = nullptr;
-  int64_t tile_rows = 1;
-  float* partials = nullptr;
   void* packed = nullptr;  // adapter_packed_bytes, which launch_adapter_pack fills from low
 };
 size_t adapter_packed_bytes(const AdapterArgs& a);
 cudaError_t launch_adapter_pack(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
                                 cudaStream_t stream);
-int64_t adapter_weight_rows(const AdapterArgs& a, bool da, size_t partial_bytes, const DeviceInfo& dev);
 cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                                  bool early, const DeviceInfo& dev, cudaStream_t stream);
-cudaError_t launch_adapter_sum(const AdapterArgs& a, const AdapterWeight& db, const AdapterWeight& da,
-                               cudaStream_t stream);
+                                  const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace fp8lin
