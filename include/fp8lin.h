@@ -637,7 +637,7 @@ fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, flo
  * y_amax: NULL, or fp32[1] that receives max |y| over the stored values (0 for
  * no rows; it needs ws): point it at the amax of the following Linear's input
  * state and give that state FP8LIN_AMAX_PRECOMPUTED.
- * h may be x or r, and y may be x or h, with the same stride; no other overlap is
+ * h may be x or r, and y may be x, r or h, with the same stride; no other overlap is
  * allowed.  A NaN or an infinity in a row makes that row of y NaN and no other;
  * the amax shows it. */
 fp8lin_status fp8lin_layer_norm(const void* x, int64_t ldx, const void* r, int64_t ldr, void* h,
@@ -705,8 +705,10 @@ fp8lin_status fp8lin_adapter_route(const int32_t* index, int64_t rows, int64_t c
  * alignments; y may be base with the same stride, and overlaps nothing else.  A row
  * without an adapter has h_i = 0 and y_i = base_i, bit for bit.  Products are
  * accumulated in fp32; s_g h_i goes in as two bf16 numbers, hi + lo (2^-17).  The
- * order of all sums is fixed by the sizes and the index.  Up to 64 rows take one
- * launch and no route.  NaN and infinities stay in their rows. */
+ * order of all sums is fixed by the sizes and the index.  A few rows
+ * (64 at most, 16 of rank 128) take one launch and no sorting.  FP8LIN_EUNSUPPORTED
+ * where no route is given and the workspace has no room for one, which some 4 million
+ * rows fill.  NaN and infinities stay in their rows. */
 fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, int64_t ldx,
                                     const int32_t* index, const void* route, int64_t rows,
                                     const void* base, int64_t ldbase, void* y, int64_t ldy, float* h,

@@ -7,7 +7,8 @@ training: row i of a batch has adapter index[i] of a bank, or none.
   dA = sum of dh_i x_i^T,  dB = sum of s dy_i h_i^T   over the adapter's rows
 
 The shared product is fp4_linear(), Fp4Linear, Fp8Linear or any other; its y (or
-dx) is the base and may be the output too.  Any sizes, row strides and
+dx) is the base and may be the output too.  A maximum of the base that the product
+delivered to a linked layer (link_linears()) is not that of the output.  Any sizes, row strides and
 alignments, ranks up to 128; ``include/fp8lin.h`` has the numerics.
 """
 from __future__ import annotations
@@ -17,8 +18,8 @@ import ctypes
 import torch
 
 from . import _lib
-from . import Workspace, _stream
-from .norm import _current_device, _on, _rows, _rows_like, _whole
+from . import Workspace
+from .norm import _current_device, _on, _rows, _rows_like, _stream_on, _whole
 
 _load = _lib.load
 
@@ -47,6 +48,7 @@ class Adapters:
         self.count, self.rank, self.K, self.N = count, rank, k, n
         c.count, c.k, c.n, c.rank = count, k, n, rank
         self._c = c
+        self._at = (c.a, c.b, c.scale)
         self._ref = ctypes.byref(c)
 
     @property
@@ -79,7 +81,7 @@ class AdapterRoute:
         dev = _current_device()
         self._set = False
         st = _load().fp8lin_adapter_route(_whole(index, "index", (self.rows,), torch.int32, dev), self.rows,
-                                          self.count, _on(self.buf, "the route", dev), _stream(stream))
+                                          self.count, _on(self.buf, "the route", dev), _stream_on(dev, stream))
         _lib.check(st, "fp8lin_adapter_route")
         self._set = True
         return self
@@ -100,6 +102,8 @@ def _bank(bank: Adapters, dev: int):
     if bank.device != dev:
         raise ValueError("the adapters are on cuda:%d, but the current device is cuda:%d"
                          % (bank.device, dev))
+    if (bank._a.data_ptr(), bank._b.data_ptr(), bank._scale.data_ptr()) != bank._at:
+        raise ValueError("the bank's tensors have other storage now: make another bank")
     return bank._ref
 
 
@@ -115,7 +119,7 @@ def _linear_args(x, index, bank, y, h, ws, base, route, stream):
     return (_bank(bank, dev), px, ldx, _whole(index, "index", (rows,), torch.int32, dev),
             _route(route, rows, bank, dev), rows, pb, ldb, py, ldy,
             _whole(h, "h", (rows, bank.rank), torch.float32, dev), _on(ws.buf, "ws", dev), ws.nbytes,
-            _stream(stream))
+            _stream_on(dev, stream))
 
 
 def _linear(args):
@@ -159,6 +163,6 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor | None, h: torch.Tensor |
         _whole(index, "index", (rows,), torch.int32, dev), _route(route, rows, bank, dev), rows, pb, ldb,
         pdx, lddx, _whole(dh, "dh", low, f32, dev), _whole(da, "da", bank.a.shape, torch.bfloat16, dev),
         _whole(db, "db", bank.b.shape, torch.bfloat16, dev), _on(ws.buf, "ws", dev), ws.nbytes,
-        _stream(stream))
+        _stream_on(dev, stream))
     _lib.check(st, "fp8lin_adapter_backward")
     return dx, da, db

@@ -1610,6 +1610,11 @@ bool bf16_rows_ok(const void* p, int64_t cols, int64_t ld) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 1u) == 0 && ld >= cols;
 }
 
+// Of an output that may be an input too: it then has the same rows.
+bool same_rows(const void* out, int64_t ldout, const void* in, int64_t ldin, int64_t rows) {
+  return out == nullptr || out != in || ldout == ldin || rows <= 1;
+}
+
 bool param_ok(const void* p, int32_t f32) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0;
 }
@@ -1635,6 +1640,10 @@ fp8lin_status fp8lin_layer_norm(const void* x, int64_t ldx, const void* r, int64
   if (rows > 0) {
     if (!bf16_rows_ok(x, cols, ldx) || !bf16_rows_ok(y, cols, ldy)) return FP8LIN_EINVAL;
     if (r != nullptr && (!bf16_rows_ok(r, cols, ldr) || !bf16_rows_ok(h, cols, ldh)))
+      return FP8LIN_EINVAL;
+    if (!same_rows(h, ldh, x, ldx, rows) || !same_rows(h, ldh, r, ldr, rows) ||
+        !same_rows(y, ldy, x, ldx, rows) || !same_rows(y, ldy, r, ldr, rows) ||
+        !same_rows(y, ldy, h, ldh, rows))
       return FP8LIN_EINVAL;
   }
   DeviceInfo dev;
@@ -1686,6 +1695,7 @@ fp8lin_status fp8lin_layer_norm_backward(const void* dy, int64_t lddy, const voi
     if (!bf16_rows_ok(dy, cols, lddy) || !bf16_rows_ok(x, cols, ldx)) return FP8LIN_EINVAL;
     if (dres != nullptr && !bf16_rows_ok(dres, cols, lddres)) return FP8LIN_EINVAL;
     if (dx != nullptr && !bf16_rows_ok(dx, cols, lddx)) return FP8LIN_EINVAL;
+    if (!same_rows(dx, lddx, dy, lddy, rows) || !same_rows(dx, lddx, dres, lddres, rows)) return FP8LIN_EINVAL;
     if (stats == nullptr || !aligned4(stats)) return FP8LIN_EINVAL;
   }
   DeviceInfo dev;
@@ -1813,7 +1823,7 @@ fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, in
   if (rows > 0) {
     if (!bf16_rows_ok(x, ad->k, ldx) || !bf16_rows_ok(y, ad->n, ldy)) return FP8LIN_EINVAL;
     if (base != nullptr && !bf16_rows_ok(base, ad->n, ldbase)) return FP8LIN_EINVAL;
-    if (y == base && ldy != ldbase && rows > 1) return FP8LIN_EINVAL;
+    if (!same_rows(y, ldy, base, ldbase, rows) || y == x) return FP8LIN_EINVAL;
     if (h == nullptr || !aligned4(h)) return FP8LIN_EINVAL;
   }
   DeviceInfo dev;
@@ -1858,7 +1868,8 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     if (db != nullptr && (h == nullptr || !aligned4(h))) return FP8LIN_EINVAL;
     if (base != nullptr && !bf16_rows_ok(base, ad->k, ldbase)) return FP8LIN_EINVAL;
     if (dx != nullptr && !bf16_rows_ok(dx, ad->k, lddx)) return FP8LIN_EINVAL;
-    if (dx != nullptr && dx == base && lddx != ldbase && rows > 1) return FP8LIN_EINVAL;
+    if (!same_rows(dx, lddx, base, ldbase, rows)) return FP8LIN_EINVAL;
+    if (dx != nullptr && (dx == dy || (da != nullptr && dx == x))) return FP8LIN_EINVAL;
     if (dh == nullptr || !aligned4(dh)) return FP8LIN_EINVAL;
   }
   DeviceInfo dev;

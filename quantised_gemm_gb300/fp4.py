@@ -187,6 +187,8 @@ def fp4_linear(x: torch.Tensor, x4: Fp4Tensor, w4: Fp4Tensor, y: torch.Tensor, w
     py, ldy = _product_out(y, "y", rows, w4.rows)
     if (adapters is None) != (index is None) or (adapters is None) != (h is None):
         raise ValueError("adapters, index and h must be given together")
+    if route is not None and adapters is None:
+        raise ValueError("a route needs adapters")
     low = None
     if adapters is not None:
         low = _linear_args(x, index, adapters, y, h, ws, y, route, stream)

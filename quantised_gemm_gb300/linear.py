@@ -16,6 +16,7 @@ import ctypes
 import torch
 
 from . import _lib
+from .norm import LayerNorm
 from . import (AMAX_AUTO, AMAX_PRECOMPUTED, DELAYED, DYNAMIC, E4M3, E5M2, ScalingState,
                Workspace, _stream, backward, forward, scale, scale_many)
 
@@ -173,8 +174,12 @@ def link_linears(prev, nxt):
     once instead of twice.  Both states must use dynamic scaling, and the
     caller must feed exactly prev.y / nxt.dx to the linked layer.
 
+    An adapter's part that is added to prev.y or nxt.dx afterwards is not in that
+    maximum: such a pair is not linked on that side.
+
     One of the two may be a LayerNorm, which delivers its maxima and takes
-    none; an Fp4Linear in NVFP4 may take a LayerNorm's."""
+    none; an Fp4Linear in NVFP4 may take a LayerNorm's.  A LayerNorm delivers each
+    of them to one layer: of several that read its y, one is linked."""
     if prev.N != nxt.K or prev.M != nxt.M:
         raise ValueError("prev [M, N] output must be nxt's [M, K] input")
     takes_x, takes_dy = getattr(nxt, "sx", None), getattr(prev, "sdy", None)
@@ -185,6 +190,9 @@ def link_linears(prev, nxt):
             raise ValueError("%s does not deliver the amax of its output" % type(giver).__name__)
         if state is not None and state.kind != DYNAMIC:
             raise ValueError("a producer-computed amax needs dynamic scaling")
+        taken = getattr(giver, to) if state is not None and isinstance(giver, LayerNorm) else None
+        if taken is not None and taken.data_ptr() != state.amax.data_ptr():
+            raise ValueError("the LayerNorm is linked to another layer already")
     if takes_x is not None:
         takes_x.amax_algo = AMAX_PRECOMPUTED
         prev.y_amax_to = takes_x.amax

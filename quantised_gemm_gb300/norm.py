@@ -15,13 +15,17 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from . import Workspace, _stream
+from . import Workspace, _raw_stream, _stream
 
 _load = _lib.load
 
 _BF16 = torch.bfloat16
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
 _current_device = torch._C._cuda_getDevice
+
+
+def _stream_on(dev: int, stream) -> int:
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _on(t: torch.Tensor, name: str, dev: int):
@@ -88,7 +92,7 @@ def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None, y: torc
     """y = layer norm of x (bf16 [M, K]), or of h = bf16(x + residual), which is
     written too.  w, b: bf16 or fp32 [K]; stats (fp32 [2, M]) receives the rows'
     means and inverse deviations, for the backward; y_amax (fp32[1]) max |y|,
-    for which ws is needed.  h may be x or residual, and y may be x or h."""
+    for which ws is needed.  h may be x or residual, and y may be any of the three."""
     dev = _current_device()
     px, rows, cols, ldx = _rows(x, "x", dev)
     if (residual is None) != (h is None):
@@ -106,7 +110,7 @@ def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None, y: torc
     st = _load().fp8lin_layer_norm(px, ldx, pr, ldr, ph, ldh, pw, pb, f32, rows, cols, eps, py, ldy,
                                    _whole(stats, "stats", (2, rows), torch.float32, dev),
                                    _amax(y_amax, "y_amax", dev),
-                                   None if ws is None else _on(ws.buf, "ws", dev), _stream(stream))
+                                   None if ws is None else _on(ws.buf, "ws", dev), _stream_on(dev, stream))
     _lib.check(st, "fp8lin_layer_norm")
     return y
 
@@ -139,7 +143,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, stat
         pdy, lddy, px, ldx, _whole(w, "w", one, dtype, dev), f32,
         _whole(stats, "stats", (2, rows), torch.float32, dev), rows, cols, pr, ldr, pdx, lddx,
         _whole(dw, "dw", one, dtype, dev), _whole(db, "db", one, dtype, dev),
-        _amax(dx_amax, "dx_amax", dev), _on(ws.buf, "ws", dev), ws.nbytes, _stream(stream))
+        _amax(dx_amax, "dx_amax", dev), _on(ws.buf, "ws", dev), ws.nbytes, _stream_on(dev, stream))
     _lib.check(st, "fp8lin_layer_norm_backward")
     return dx, dw, db
 

@@ -82,3 +82,12 @@ def test_route_refusals(lib):
     assert lib.fp8lin_adapter_route(P, (1 << 24) + 1, 3, P, None) == L.EUNSUPPORTED
     for index, route in ((None, P), (HALF, P), (P, None), (P, HALF)):
         assert lib.fp8lin_adapter_route(index, 10, 3, route, None) == L.EINVAL
+
+
+def test_outputs_over_what_is_still_read(lib):
+    import quantised_gemm_gb300._lib as L
+    square = bank(k=48)
+    R = ctypes.c_void_p(0x30000)
+    assert forward(lib, square, y=P, base=Q, ldx=48) == L.EINVAL  # y is x
+    for change in (dict(dx=P, dy=P, x=R), dict(dx=R, x=R)):
+        assert backward(lib, square, base=Q, **change) == L.EINVAL, change

@@ -406,3 +406,21 @@ def test_refusals():
         q.AdapterRoute(4, 1025)
     with pytest.raises(errors):
         q.AdapterRoute(-1, 2)
+
+
+def test_a_bank_whose_tensors_moved_is_refused():
+    import quantised_gemm_gb300 as q
+    c = Case(4, 64, 48, 8, 2)
+    y = torch.empty((4, 48), dtype=BF, device="cuda")
+    dx, da, db = c.like()
+    kept = c.bank.b.data
+    c.bank.b.data = kept.clone()
+    with pytest.raises(ValueError):
+        q.adapter_linear(c.x, c.index, c.bank, y, c.h, c.ws)
+    with pytest.raises(ValueError):
+        q.adapter_backward(c.dy, c.x, c.h, c.index, c.bank, c.dh, dx, da, db, c.ws)
+    c.bank.b.data = kept
+    q.adapter_linear(c.x, c.index, c.bank, y, c.h, c.ws)
+    with pytest.raises(q.Fp8linError):
+        q.adapter_linear(c.x, c.index, q.Adapters(c.bank.a, c.bank.a.transpose(1, 2).contiguous(), c.bank.scale), c.x,
+                         c.h, c.ws)  # y is x

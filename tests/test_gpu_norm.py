@@ -354,3 +354,30 @@ def test_refusals():
         norm.forward(x[:3], w, b)
     with pytest.raises(ValueError):
         norm.backward(x)  # the forward before was refused
+
+
+@pytest.mark.parametrize("cols", [96, 1531])
+def test_forward_over_the_residual(cols):
+    import quantised_gemm_gb300 as q
+    x, r, (w, b) = make(70, cols, 81), make(70, cols, 82), params(cols, F32, 83)
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    q.layer_norm(x, w, b, y, residual=r, h=h)
+    h2 = torch.empty_like(h)
+    q.layer_norm(x, w, b, r, residual=r, h=h2)
+    assert torch.equal(r, y) and torch.equal(h2, h)
+
+
+def test_a_norm_delivers_its_maximum_to_one_layer():
+    """A second layer would leave the first one's scale to a maximum that nothing writes."""
+    import quantised_gemm_gb300 as q
+    norm, first, second = q.LayerNorm(32, 64), q.Fp8Linear(32, 64, 96), q.Fp8Linear(32, 64, 96)
+    q.link_linears(norm, first)
+    q.link_linears(norm, first)
+    with pytest.raises(ValueError):
+        q.link_linears(norm, second)
+    assert second.sx.amax_algo != q.AMAX_PRECOMPUTED
+    before, other = q.Fp8Linear(32, 128, 64), q.Fp8Linear(32, 128, 64)
+    q.link_linears(before, norm)
+    with pytest.raises(ValueError):
+        q.link_linears(other, norm)
+    assert other.sdy.amax_algo != q.AMAX_PRECOMPUTED and other.y_amax_to is None

@@ -85,3 +85,11 @@ def test_training_step(kind):
     out = torch.empty(1, device="cuda")
     q.clip_grad_norm(grads, total / 2, out, ws)
     assert abs(float(out) - total) <= 1e-5 * total
+
+
+def test_a_route_without_adapters_is_refused():
+    import quantised_gemm_gb300 as q
+    x, ws, y = make(8, 64, 21), q.Workspace(), torch.empty((8, 32), dtype=BF, device="cuda")
+    w4, x4 = q.Fp4Tensor(32, 64, q.NVFP4), q.Fp4Tensor(8, 64, q.NVFP4)
+    with pytest.raises(ValueError):
+        q.fp4_linear(x, x4, w4, y, ws, route=q.AdapterRoute(8, 2))

@@ -54,3 +54,14 @@ def test_backward_refusals(lib):
         assert backward(lib, **change) == L.EINVAL, change
     assert backward(lib, cols=16385, lddy=1 << 20, ldx=1 << 20, lddx=1 << 20) == L.EUNSUPPORTED
     assert backward(lib, cols=0) == L.EUNSUPPORTED
+
+
+def test_an_output_over_an_input_has_its_rows(lib):
+    import quantised_gemm_gb300._lib as L
+    Q = ctypes.c_void_p(0x20000)
+    R = ctypes.c_void_p(0x30000)
+    for change in (dict(ldy=72), dict(y=Q, r=Q, ldr=72, h=R, ldh=64), dict(y=Q, r=R, ldr=64, h=Q, ldh=72),
+                   dict(y=Q, r=R, ldr=64, h=P, ldh=72), dict(y=Q, r=R, ldr=64, h=R, ldh=72)):
+        assert forward(lib, **change) == L.EINVAL, change
+    for change in (dict(lddx=72), dict(dx=Q, dres=Q, lddres=72)):
+        assert backward(lib, **change) == L.EINVAL, change
