@@ -2,8 +2,8 @@
 //   dw[c][j] = sum over the rows i of one adapter of x[i][c] s_a low[i][j]
 // dB (x = dy, low = h) and dA (x the input, low = dh) in one launch.
 //
-// Bound by reading x again: 16384 rows of 14336 and 4096 columns with rank 16 take some
-// 110 us (5.5 TB/s).  A cluster shares the rows of a large adapter; partial sums in
+// Bound by reading x again: 16384 rows of 14336 and 4096 columns with rank 16 take
+// 118 us (5.2 TB/s).  A cluster shares the rows of a large adapter; partial sums in
 // the workspace and a launch that adds them took 259 us instead of 248 for the whole
 // backward, and 510 instead of 357 for 8192 x 4096 x 4096 with rank 128.
 #include "adapter_kernels.cuh"
@@ -28,10 +28,12 @@ struct WeightArgs {
 };
 
 // With a small rank the rows' numbers are few beside x, and splitting the rows leaves
-// fewer CTAs to a cluster; with a large one warps of the same rows share them.
+// fewer CTAs to a cluster; with a large one warps of the same rows share them.  Rank 64
+// with all warps on the same rows took 52 us instead of 38 for the backward of 608 x 793
+// x 777, where a turn's latency counts, and 125 instead of 122 for 4096 x 4096 x 4096.
 template <int kRankTiles>
 struct WeightShape {
-  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles == 4 ? 2 : 1;
+  static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles <= 8 ? 2 : 1;
   static constexpr int kColWarps = kAdapterWarps / kRowWarps;
   static constexpr int kChunks = kRankTiles <= 4 ? 2 : 1;  // of 32 columns a warp
   static constexpr int kSlab = 32 * kChunks * kColWarps;
@@ -41,7 +43,7 @@ struct WeightShape {
   static constexpr int kShared = (kAlone ? 1 : kRowWarps) * kRankTiles * 32;  // of a turn
   template <bool kAligned>
   // More stages than 80 KB hold cost a short sum more than they give a long one.
-  using T = Stages<stages_in(kAlone ? kStageRoom - 16 * 1024 : kRankTiles == 4 ? kStageRoom - 32 * 1024 : kStageRoom,
+  using T = Stages<stages_in(kAlone || kRankTiles == 8 ? kStageRoom - 16 * 1024 : kRankTiles == 4 ? kStageRoom - 32 * 1024 : kStageRoom,
                              sizeof(uint4) * ((kAligned ? 2 : 4) * kChunks * kAdapterThreads +
                                               (kAlone ? kAdapterWarps : 1) * kShared)),
                    2 * kChunks, kShared, kAlone, kAligned, true>;
@@ -334,7 +336,7 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
     // More CTAs than are resident, so that an adapter with many rows does not keep the
     // others waiting, but with enough rows each for their start and their sums.  The
     // whole backward with four CTAs an SM and with eight: 16384 x 4096 x 14336, rank
-    // 16, 248 and 264 us; 4096 x 4096 x 4096, rank 64, 124 and 117.  With 128 rows and
+    // 16, 248 and 264 us; 4096 x 4096 x 4096, rank 64, 124 and 122.  With 128 rows and
     // with 256: 1267 x 1600 x 2501, rank 12, 28 and 33; 1024 x 4096 x 4096, rank 64, 58
     // and 51.
     const int64_t most = (a.rank <= 32 ? 4 : 8) * int64_t(dev.num_sms), least = a.rank <= 16 ? 128 : 256;

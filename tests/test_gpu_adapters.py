@@ -424,3 +424,26 @@ def test_a_bank_whose_tensors_moved_is_refused():
     with pytest.raises(q.Fp8linError):
         q.adapter_linear(c.x, c.index, q.Adapters(c.bank.a, c.bank.a.transpose(1, 2).contiguous(), c.bank.scale), c.x,
                          c.h, c.ws)  # y is x
+
+
+UNEVEN = [[96, 328, 0, 3672], [1, 3100, 15], [1040, 1040, 1040], [0, 0, 4100, 0], [2048, 2047, 1], [130, 0, 130, 2, 5000]]
+
+
+@pytest.mark.parametrize("lengths", UNEVEN, ids=lambda n: "-".join(map(str, n)))
+@pytest.mark.parametrize("k,n,rank", [(1300, 1400, 16), (2600, 72, 5), (2600, 2704, 32), (1288, 1400, 64), (700, 901, 128),
+                                      (40, 64, 16)])
+def test_gradients_of_uneven_adapters(k, n, rank, lengths):
+    """Rows that are split evenly whatever an adapter has: one over many CTAs, several in one."""
+    count = len(lengths)
+    rows = sum(lengths) + 33
+    c = Case(rows, k, n, rank, count)
+    of = torch.arange(-1, count, dtype=torch.int32, device="cuda")
+    index = of.repeat_interleave(torch.tensor([33] + lengths, device="cuda"))
+    c.index = index[torch.randperm(rows, generator=torch.Generator(device="cuda").manual_seed(9), device="cuda")]
+    c.forward(torch.empty((rows, n), dtype=BF, device="cuda"))
+    dx, da, db = c.like()
+    c.backward(dx, da, db)
+    c.check_backward(dx, da, db)
+    more = c.like()
+    c.backward(*more)
+    assert all(torch.equal(a, b) for a, b in zip((dx, da, db), more))
