@@ -1893,7 +1893,9 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
   }
   // The weight gradients' operands from h and dh, laid out once where the rows pay for
   // that launch (16384 x 4096 x 14336 with rank 16: 256 us with it, 363 without; 1024 x
-  // 4096 x 4096: 31 and 33; 256 rows: 16.8 and 16.5) and the workspace has room.
+  // 4096 x 4096: 31 and 33; 256 rows: 16.8 and 16.5; with rank 32, 318 x 5954 x 1857 of
+  // three adapters: 33.5 and 36.4; with rank 64, 201 x 5550 x 185 of six: 31.5 and 28.4)
+  // and the workspace has room.
   AdapterWeight wa, wb;
   if (da != nullptr) {
     wa.dw = static_cast<uint16_t*>(da);
@@ -1907,9 +1909,10 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     wb.ldx = lddy;
     wb.low = h;
   }
+  const int64_t pays = ad->rank > 16 && 64 * ad->count < 512 ? 64 * ad->count : 512;
   const size_t packed = (adapter_packed_bytes(a) + 255) / 256 * 256;
   for (AdapterWeight* w : {&wa, &wb}) {
-    if (w->dw == nullptr || rows < 512 || packed > room_bytes) continue;
+    if (w->dw == nullptr || rows < pays || packed > room_bytes) continue;
     w->packed = room;
     room += packed;
     room_bytes -= packed;
