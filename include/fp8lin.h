@@ -722,7 +722,7 @@ fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, in
  * dy: bf16 [rows, n]; x, base, dx: bf16 [rows, k]; da, db: dense, of the shapes of
  * a and b, zeros for adapters that no row has.  dx, da and db may each be NULL (x
  * is needed for da, h for db only).  dx may be base with the same stride; nothing
- * else may overlap what is written.  dh and s_g h go into the products as hi + lo.
+ * else may overlap what is written (dh over an h that db needs is refused).  dh and s_g h go into the products as hi + lo.
  * The order of all sums is fixed by the sizes and the index. */
 fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy, int64_t lddy,
                                       const void* x, int64_t ldx, const float* h,

@@ -145,7 +145,7 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor | None, h: torch.Tensor |
     """dx = base + the adapters' part, dA and dB (bf16, of the bank's shapes; zeros
     for adapters that no row has), from the forward's x and h; each of the three
     may be None, x is needed for da only and h for db.  dh: fp32 [M, rank]
-    receives s B^T dy.  base may be dx."""
+    receives s B^T dy, and is not h.  base may be dx."""
     dev = _current_device()
     pdy, rows, n, lddy = _rows(dy, "dy", dev)
     if ws is None:

@@ -1615,6 +1615,12 @@ bool same_rows(const void* out, int64_t ldout, const void* in, int64_t ldin, int
   return out == nullptr || out != in || ldout == ldin || rows <= 1;
 }
 
+// Whether two buffers of `bytes` each have any in common.
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q ? q - p < bytes : p - q < bytes;
+}
+
 bool param_ok(const void* p, int32_t f32) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0;
 }
@@ -1871,6 +1877,8 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     if (!same_rows(dx, lddx, base, ldbase, rows)) return FP8LIN_EINVAL;
     if (dx != nullptr && (dx == dy || (da != nullptr && dx == x))) return FP8LIN_EINVAL;
     if (dh == nullptr || !aligned4(dh)) return FP8LIN_EINVAL;
+    // dh is written before dB reads h.
+    if (db != nullptr && overlap(dh, h, static_cast<size_t>(rows) * ad->rank * sizeof(float))) return FP8LIN_EINVAL;
   }
   DeviceInfo dev;
   if ((s = get_dev(&dev)) != FP8LIN_OK) return s;
