@@ -22,7 +22,7 @@ struct HighArgs {
   int64_t ldbase, ldy;
   int cols, rank, slab;
   Route route;
-  bool low_aligned, early;
+  bool low_aligned;
 };
 
 // A tile of 16 * kTiles rows for each of kRowWarps warps, and `slab` columns, of
@@ -55,10 +55,7 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
   using S = typename Shape::S;
   constexpr int kColWarps = Shape::kColWarps, kRankTiles = 2 * kSteps, kTurn = 32 * kColWarps;
   extern __shared__ uint4 shared[];
-  // early: the launch before this one writes nothing that this one touches, and all
-  // before that is done once its CTAs let this one begin.  The wait then comes at the
-  // end, so that what follows still finds everything before it done.
-  if (!p.early) griddep_wait();
+  griddep_wait();
   griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int row_warp = warp % kRowWarps, col_warp = warp / kRowWarps;
@@ -66,10 +63,7 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
   const RowTile tile =
       find_tile(p.route, p.route.groups, 16 * kTiles * kRowWarps, static_cast<int>(blockIdx.x));
   const bool none = tile.group == p.route.groups - 1;
-  if (tile.group < 0 || (none && p.y == p.base)) {
-    if (p.early) griddep_wait();
-    return;
-  }
+  if (tile.group < 0 || (none && p.y == p.base)) return;
   const int begin = static_cast<int>(blockIdx.y) * p.slab;
   const int end = min(begin + p.slab, p.cols);
   // A warp's turns: every kColWarps-th 32 columns, or, where rows of y are not
@@ -193,14 +187,13 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
     for (int v = 0; v < 2 * kTiles; ++v) runs[v].end();
   }
   copies_wait<0>();
-  if (p.early) griddep_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
                                 const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
-                                bool early, const DeviceInfo& dev, cudaStream_t stream) {
+                                const DeviceInfo& dev, cudaStream_t stream) {
   set_error_site("adapter_high_kernel");
   HighArgs p = {};
   p.low = low;
@@ -213,7 +206,6 @@ cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float
   p.cols = static_cast<int>(backward ? a.k : a.n);
   p.rank = a.rank;
   p.route = route_of(a);
-  p.early = early;
   p.low_aligned = aligned16(low) && a.rank % 2 == 0;
   const bool aligned = rows_aligned(base, ldbase, p.cols) && rows_aligned(y, ldy, p.cols);
   const bool w_aligned = backward ? a_aligned(a) : b_aligned(a);

@@ -1853,7 +1853,7 @@ fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, in
     if (e != cudaSuccess) return cuda_fail(e);
   }
   ProfScope ps(FP8LIN_PROF_GEMM, stream);
-  cudaError_t e = launch_adapter_high(a, false, h, bases, ldbase, ys, ldy, false, dev, stream);
+  cudaError_t e = launch_adapter_high(a, false, h, bases, ldbase, ys, ldy, dev, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
 }
 
@@ -1930,16 +1930,15 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     e = launch_adapter_pack(a, wb, wa, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  const bool weights = da != nullptr || db != nullptr;
-  if (weights) {
+  if (da != nullptr || db != nullptr) {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
     e = launch_adapter_weight(a, wb, wa, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  if (dx != nullptr) {  // beside the weight gradients
+  if (dx != nullptr) {
     ProfScope ps(FP8LIN_PROF_GEMM, stream);
     e = launch_adapter_high(a, true, dh, static_cast<const uint16_t*>(base), ldbase,
-                            static_cast<uint16_t*>(dx), lddx, weights, dev, stream);
+                            static_cast<uint16_t*>(dx), lddx, dev, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return FP8LIN_OK;

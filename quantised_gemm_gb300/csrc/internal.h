@@ -494,11 +494,10 @@ cudaError_t launch_adapter_few(const AdapterArgs& a, const int32_t* index, const
 // low = x A^T, or (backward) low = s x B with x the output's gradient.
 cudaError_t launch_adapter_low(const AdapterArgs& a, bool backward, const uint16_t* x, int64_t ldx,
                                float* low, const DeviceInfo& dev, cudaStream_t stream);
-// y = base + s low B^T, or (backward) y = base + low A.  early: the launch before it in
-// the stream is the adapters' and touches neither low nor y.
+// y = base + s low B^T, or (backward) y = base + low A.
 cudaError_t launch_adapter_high(const AdapterArgs& a, bool backward, const float* low,
                                 const uint16_t* base, int64_t ldbase, uint16_t* y, int64_t ldy,
-                                bool early, const DeviceInfo& dev, cudaStream_t stream);
+                                const DeviceInfo& dev, cudaStream_t stream);
 // One of dA (x the input, low = dh) and dB (x the output's gradient, low = h); dw
 // null: not wanted.
 struct AdapterWeight {
