@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)  // 32 rows are 256 CTAs, a
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int j = warp + i * kFewWarps;
+    if (j >= p.rank) part_sum[i] = 0.0f;  // an infinity in x times the 0 past the ranks is not
     if (lane < kFewCluster && j < kRanks)
       st_shared_cluster_u32(map_to_cta(smem_addr(&sums[part][j]), lane), __float_as_uint(part_sum[i]));
   }
