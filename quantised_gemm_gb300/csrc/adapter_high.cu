@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
     stages.filled();
     const int col = begin_warp + turn * apart + 8 * t;
     if (idle) continue;
-    if (!none) {
+    // Adds the products to out.  kGuarded: lo only where the weight is finite.
+    auto add_products = [&](auto guarded) {
       const uint4* const ws = stages.shared_due() + (Shape::kAlone ? 0 : col_warp * kRankTiles * 32);
       float acc[kTiles][4][4];
 #pragma unroll
@@ -152,7 +153,11 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int m = 0; m < kTiles; ++m) {
-            mma_bf16(acc[m][q], lo[m][s][0], lo[m][s][1], lo[m][s][2], lo[m][s][3], b[0][q], b[1][q]);
+            if constexpr (decltype(guarded)::value)
+              mma_bf16(acc[m][q], lo[m][s][0], lo[m][s][1], lo[m][s][2], lo[m][s][3], finite_values(b[0][q]),
+                       finite_values(b[1][q]));
+            else
+              mma_bf16(acc[m][q], lo[m][s][0], lo[m][s][1], lo[m][s][2], lo[m][s][3], b[0][q], b[1][q]);
             mma_bf16(acc[m][q], hi[m][s][0], hi[m][s][1], hi[m][s][2], hi[m][s][3], b[0][q], b[1][q]);
           }
       }
@@ -169,18 +174,30 @@ __global__ void __launch_bounds__(kAdapterThreads, kSteps <= 4 ? 2 : 1)
           }
           out[2 * m + i] = f32_to_bf16x8(v);
         }
-    }
+    };
     const int n = values_at(col, end_warp);
+    auto store = [&]() {
 #pragma unroll
-    for (int v = 0; v < 2 * kTiles; ++v) {
-      const int64_t of = row[v >> 1][v & 1];
-      uint16_t* const to = p.y + (of < 0 ? 0 : of) * p.ldy + col;
-      if constexpr (kAligned) {
-        if (of >= 0 && n > 0) *reinterpret_cast<uint4*>(to) = out[v];
-      } else {
-        runs[v].store(to, out[v], of < 0 ? 0 : n);
+      for (int v = 0; v < 2 * kTiles; ++v) {
+        const int64_t of = row[v >> 1][v & 1];
+        uint16_t* const to = p.y + (of < 0 ? 0 : of) * p.ldy + col;
+        if constexpr (kAligned) {
+          if (of >= 0 && n > 0) *reinterpret_cast<uint4*>(to) = out[v];
+        } else {
+          runs[v].store(to, out[v], of < 0 ? 0 : n);
+        }
       }
+    };
+    if (!none) add_products(No());
+    // hi w + lo w is NaN for an infinite w unless hi and lo have the same sign.  Aligned rows are
+    // looked at while they are on their way out, and then written again.
+    if constexpr (kAligned) store();
+    if (!none && __any_sync(0xFFFFFFFFu, any_not_finite(out))) {
+      stages.take(out, base_of(turn));
+      add_products(Yes());
+      if constexpr (kAligned) store();
     }
+    if constexpr (!kAligned) store();
   }
   if constexpr (!kAligned) {
 #pragma unroll

@@ -60,6 +60,27 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   lo = cvt_bf16x2(rx, ry);
 }
 
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Two bf16 values, 0 for one that is infinite or NaN.
+__device__ __forceinline__ uint32_t finite_values(uint32_t v) {
+  const uint32_t e = v & 0x7F807F80u;
+  return ((e & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu) | (e >= 0x7F800000u ? 0u : v & 0xFFFF0000u);
+}
+
+// Whether one of the vectors' values is infinite or NaN: such a value times 0 is NaN, any other is 0.
+template <int kVecs>
+__device__ __forceinline__ bool any_not_finite(const uint4 (&v)[kVecs]) {
+  uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[j]) : "r"(word(v[i], j)), "r"(0u));
+  return (sum[0] | sum[1] | sum[2] | sum[3]) != 0;
+}
+
 // Four 8 x 8 tiles from shared memory, lane l giving the row l % 8 of tile l / 8;
 // a lane (g, t) gets of each columns 2t and 2t + 1 of row g, or, turned, rows 2t and
 // 2t + 1 of column g.
@@ -71,10 +92,6 @@ __device__ __forceinline__ void load_tiles(uint32_t (&v)[4], const void* row) {
   else
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(smem_addr(row)) : "memory");
-}
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // ---------------------------------------------------------------- rows by adapter

@@ -59,3 +59,41 @@ def test_an_infinity_in_x_is_one_in_y(rank, rows):
     assert torch.equal(c.h[3], sign * float("inf"))
     assert torch.equal(y[3].float(), torch.full((c.n,), float("inf"), device="cuda"))
     assert torch.isfinite(y[:3]).all() and torch.isfinite(y[4:]).all()
+
+
+def signed_infinity(v):
+    return torch.where(v == 0, torch.nan, torch.sign(v) * float("inf"))
+
+
+@pytest.mark.parametrize("rows", [16, 40, 300, 3000])
+@pytest.mark.parametrize("k,n,rank", [(200, 104, 16), (200, 101, 16), (192, 200, 8), (256, 512, 64), (130, 77, 33), (64, 72, 128), (321, 97, 5)])
+def test_an_infinity_in_a_bank(k, n, rank, rows):
+    """An infinity of B or A is one of the sign of what it is multiplied with, whatever bits that has:
+    in its column, and the other columns keep theirs."""
+    c = Case(rows, k, n, rank, 2, "random", 71)
+    y, y2 = (torch.empty((rows, n), dtype=BF, device="cuda") for _ in range(2))
+    c.x[1::3, 1:] = 0.0  # of these rows h has only bf16's bits
+    c.forward(y)
+    dx, da, db = c.like()
+    c.backward(dx, da, db)
+    has = c.index == 1
+    ranks = (rank - 1, rank // 2)
+    cols = (n - 1, n // 3)
+    for j, col, sign in zip(ranks, cols, (1.0, -1.0)):
+        c.bank.b[1, col, j] = sign * float("inf")
+    c.forward(y2)
+    want = y.float()
+    for j, col, sign in zip(ranks, cols, (1.0, -1.0)):
+        want[has, col] = signed_infinity(sign * c.h[has, j])
+    assert torch.equal(y2.float().nan_to_num(5.0, 7.0, -7.0), want.nan_to_num(5.0, 7.0, -7.0))
+    c.bank.b[1, cols[0], ranks[0]] = c.bank.b[1, cols[1], ranks[1]] = 0.0
+    dx2 = c.like()[0]
+    c.backward(dx, None, None)
+    cols = (k - 1, k // 3)
+    for j, col, sign in zip(ranks, cols, (1.0, -1.0)):
+        c.bank.a[1, j, col] = sign * float("inf")
+    c.backward(dx2, None, None)
+    want = dx.float()
+    for j, col, sign in zip(ranks, cols, (1.0, -1.0)):
+        want[has, col] = signed_infinity(sign * c.dh[has, j])
+    assert torch.equal(dx2.float().nan_to_num(5.0, 7.0, -7.0), want.nan_to_num(5.0, 7.0, -7.0))
