@@ -704,11 +704,12 @@ fp8lin_status fp8lin_adapter_route(const int32_t* index, int64_t rows, int64_t c
  * x: bf16 [rows, k], base (NULL: zeros) and y: bf16 [rows, n], any row strides and
  * alignments; y may be base with the same stride, and overlaps nothing else.  A row
  * without an adapter has h_i = 0 and y_i = base_i, bit for bit.  Products are
- * accumulated in fp32; s_g h_i goes in as two bf16 numbers, hi + lo (2^-17).  The
- * order of all sums is fixed by the sizes and the index.  A few rows
- * (64 at most, 16 of rank 128) take one launch and no sorting.  FP8LIN_EUNSUPPORTED
+ * accumulated in fp32; s_g h_i goes in as two bf16 numbers, hi + lo (2^-17; infinite
+ * from 3.396e38 on, where hi rounds past bf16's largest), but for a few rows (64 at most, 16 of
+ * rank 128), which take one launch and no sorting and keep it in fp32.  The order of all sums is fixed by the sizes and the index.  FP8LIN_EUNSUPPORTED
  * where no route is given and the workspace has no room for one, which some 4 million
- * rows fill.  NaN and infinities stay in their rows. */
+ * rows fill.  NaN and infinities in x stay in their rows, those of A and B in the rows
+ * of their adapter; they give what the formulas give. */
 fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, int64_t ldx,
                                     const int32_t* index, const void* route, int64_t rows,
                                     const void* base, int64_t ldbase, void* y, int64_t ldy, float* h,
@@ -723,7 +724,10 @@ fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, in
  * a and b, zeros for adapters that no row has.  dx, da and db may each be NULL (x
  * is needed for da, h for db only).  dx may be base with the same stride; nothing
  * else may overlap what is written (dh over an h that db needs is refused).  dh and s_g h go into the products as hi + lo.
- * The order of all sums is fixed by the sizes and the index. */
+ * The order of all sums is fixed by the sizes and the index.  dh and dx are to NaN
+ * and infinities what h and y are in the forward; an infinity in x, dy, h or dh makes
+ * the numbers of dA and dB that it enters infinite or NaN (where lo is 0 or of the other
+ * sign than hi) and no others. */
 fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy, int64_t lddy,
                                       const void* x, int64_t ldx, const float* h,
                                       const int32_t* index, const void* route, int64_t rows,

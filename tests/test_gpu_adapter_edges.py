@@ -97,3 +97,30 @@ def test_an_infinity_in_a_bank(k, n, rank, rows):
     for j, col, sign in zip(ranks, cols, (1.0, -1.0)):
         want[has, col] = signed_infinity(sign * c.dh[has, j])
     assert torch.equal(dx2.float().nan_to_num(5.0, 7.0, -7.0), want.nan_to_num(5.0, 7.0, -7.0))
+
+
+@pytest.mark.parametrize("rows", [16, 100, 700, 3000])
+@pytest.mark.parametrize("k,n,rank", [(200, 104, 16), (201, 101, 16), (192, 200, 8), (256, 512, 64), (130, 77, 33), (64, 72, 128), (321, 97, 5)])
+def test_an_infinity_in_x_or_dy_is_seen_in_the_gradients(k, n, rank, rows):
+    """An infinity in x makes its column of dA infinite or NaN, one in dy its row of dB, in the adapter of
+    that row of the batch; the other numbers keep their bits."""
+    c = Case(rows, k, n, rank, 3, "random", 81)
+    c.index[7], c.index[11] = 1, 2
+    c.x[1::3, 1:] = 0.0
+    c.forward(torch.empty((rows, n), dtype=BF, device="cuda"))
+    _, da, db = c.like()
+    c.backward(None, da, db)
+    _, da2, db2 = c.like()
+    c.x[7, k // 3], c.x[11, k - 1] = float("inf"), float("-inf")
+    c.backward(None, da2, db2)
+    seen = torch.zeros(da.shape, dtype=torch.bool, device="cuda")
+    seen[1, :, k // 3] = seen[2, :, k - 1] = True
+    assert torch.equal(db2, db)
+    assert torch.equal(~torch.isfinite(da2), seen) and torch.equal(da2[~seen], da[~seen])
+    c.x[7, k // 3] = c.x[11, k - 1] = 0.0
+    c.dy[7, n // 3], c.dy[11, n - 1] = float("-inf"), float("inf")
+    c.backward(None, da2, db2)
+    seen = torch.zeros(db.shape, dtype=torch.bool, device="cuda")
+    seen[1, n // 3] = seen[2, n - 1] = True
+    assert torch.equal(~torch.isfinite(db2), seen) and torch.equal(db2[~seen], db[~seen])
+    assert torch.equal(da2[0], da[0]) and not torch.isfinite(da2[1:]).any()
