@@ -12,11 +12,11 @@ once, through PyTorch; the library itself allocates nothing.
 from __future__ import annotations
 
 import ctypes
+import weakref
 
 import torch
 
 from . import _lib
-from .norm import LayerNorm
 from . import (AMAX_AUTO, AMAX_PRECOMPUTED, DELAYED, DYNAMIC, E4M3, E5M2, ScalingState,
                Workspace, _stream, backward, forward, scale, scale_many)
 
@@ -178,8 +178,11 @@ def link_linears(prev, nxt):
     maximum: such a pair is not linked on that side.
 
     One of the two may be a LayerNorm, which delivers its maxima and takes
-    none; an Fp4Linear in NVFP4 may take a LayerNorm's.  A LayerNorm delivers each
-    of them to one layer: of several that read its y, one is linked."""
+    none; an Fp4Linear in NVFP4 may take a LayerNorm's.  A layer delivers each
+    of its maxima to one other and takes each of its own from one: of several that
+    read its y, one is linked.  A layer may be linked anew when the other one is
+    gone, or has another amax_algo (a taker) or no amax of this one to deliver to
+    (a giver)."""
     if prev.N != nxt.K or prev.M != nxt.M:
         raise ValueError("prev [M, N] output must be nxt's [M, K] input")
     takes_x, takes_dy = getattr(nxt, "sx", None), getattr(prev, "sdy", None)
@@ -190,12 +193,34 @@ def link_linears(prev, nxt):
             raise ValueError("%s does not deliver the amax of its output" % type(giver).__name__)
         if state is not None and state.kind != DYNAMIC:
             raise ValueError("a producer-computed amax needs dynamic scaling")
-        taken = getattr(giver, to) if state is not None and isinstance(giver, LayerNorm) else None
-        if taken is not None and taken.data_ptr() != state.amax.data_ptr():
-            raise ValueError("the LayerNorm is linked to another layer already")
-    if takes_x is not None:
-        takes_x.amax_algo = AMAX_PRECOMPUTED
-        prev.y_amax_to = takes_x.amax
-    if takes_dy is not None:
-        takes_dy.amax_algo = AMAX_PRECOMPUTED
-        nxt.dx_amax_to = takes_dy.amax
+        if state is not None and (_delivers_elsewhere(giver, to, state) or _taken_elsewhere(giver, to, state)):
+            raise ValueError("the %s is linked to another layer already" % type(giver).__name__)
+    for state, giver, to in ((takes_x, prev, "y_amax_to"), (takes_dy, nxt, "dx_amax_to")):
+        if state is not None:
+            state.amax_algo = AMAX_PRECOMPUTED
+            setattr(giver, to, state.amax)
+            setattr(giver, "_state_of_" + to, weakref.ref(state))
+            state._amax_from = weakref.ref(giver)
+
+
+def _delivers_elsewhere(giver, to, state):
+    """Whether another state still counts on the maximum that giver would deliver to this one."""
+    amax = getattr(giver, to)
+    if amax is None or amax.data_ptr() == state.amax.data_ptr():
+        return False
+    ref = getattr(giver, "_state_of_" + to, None)
+    if ref is None:
+        return True  # set by hand
+    other = ref()
+    return other is not None and (other.amax.data_ptr() != amax.data_ptr() or
+                                  other.amax_algo == AMAX_PRECOMPUTED)
+
+
+def _taken_elsewhere(giver, to, state):
+    """Whether another layer still delivers its maximum to this state."""
+    ref = getattr(state, "_amax_from", None)
+    other = ref() if ref is not None else None
+    if other is None or other is giver:
+        return False
+    amax = getattr(other, to)
+    return amax is not None and amax.data_ptr() == state.amax.data_ptr()
