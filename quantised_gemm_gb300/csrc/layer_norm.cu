@@ -152,6 +152,14 @@ struct NormParams {
   uint32_t *amax, *acc, *ticket;  // amax null: not wanted
 };
 
+// sum / cols: the product with 1 / cols and what the remainder adds to it (a division took
+// 15.0 us for 12288 x 1600 instead of 14.8).  The sum of equal values is exact (8 bits and 14
+// for their number), and so is their mean then.
+__device__ __forceinline__ float mean_of(float sum, const NormParams& p) {
+  const float q = sum * p.inv_cols;
+  return fmaf(fmaf(-q, static_cast<float>(p.cols), sum), p.inv_cols, q);
+}
+
 // Two rows of a group at a time: their loads are in flight together, they share
 // the barriers, and w and b are read once for both.
 template <int kThreads, int kVecs, bool kAligned, bool kResidual, typename P>
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(Group<kThreads>::kBlock)
       sum[i] = s.f.x + s.f.y;
     }
     group_sum<kThreads>(sum[0], sum[1], turn++);
-    const float mean[2] = {sum[0] * p.inv_cols, sum[1] * p.inv_cols};
+    const float mean[2] = {mean_of(sum[0], p), mean_of(sum[1], p)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       F2 s = pair(0.0f, 0.0f);
