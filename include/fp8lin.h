@@ -628,7 +628,8 @@ fp8lin_status fp8lin_grad_clip_norm(const fp8lin_grad* grads, int32_t count, flo
  *   h = bf16(x + r)  where r is given, else h = x
  *   mean = sum_j h_j / cols,  rstd = 1 / sqrt(sum_j (h_j - mean)^2 / cols + eps)
  *   y = bf16((h - mean) * rstd * w + b)
- * with sums and statistics in fp32.  x, r (the residual; NULL: none), h (written
+ * with sums and statistics in fp32, of 2^-72 of the values where a row of finite ones
+ * leaves fp32's range.  x, r (the residual; NULL: none), h (written
  * where r is given, else NULL) and y: [rows, cols], any row stride >= cols and
  * any alignment of their elements (16-byte aligned rows are faster); cols from 1
  * to 16384.  w, b: [cols], fp32 where param_f32 is nonzero, else bf16; b may be

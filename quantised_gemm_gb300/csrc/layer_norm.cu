@@ -152,8 +152,10 @@ struct NormParams {
   uint32_t *amax, *acc, *ticket;  // amax null: not wanted
 };
 
+constexpr float kInf = __builtin_huge_valf(), kDown = 0x1p-72f;
+
 // sum / cols: the product with 1 / cols and what the remainder adds to it (a division took
-// 15.0 us for 12288 x 1600 instead of 14.8).  The sum of equal values is exact (8 bits and 14
+// 15.0 us for 12288 x 1600 instead of 14.9).  The sum of equal values is exact (8 bits and 14
 // for their number), and so is their mean then.
 __device__ __forceinline__ float mean_of(float sum, const NormParams& p) {
   const float q = sum * p.inv_cols;
@@ -212,42 +214,76 @@ __global__ void __launch_bounds__(Group<kThreads>::kBlock)
       }
     }
     F2 d[2][kVecs][4];  // the values, then their deviations from the mean
-    float sum[2], sq[2];
+    float mean[2], sq[2];
+    float down[2] = {1.0f, 1.0f};
+    auto deviations = [&](auto scaled) {
+      float sum[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      F2 s = pair(0.0f, 0.0f);
+      for (int i = 0; i < 2; ++i) {
+        F2 s = pair(0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        unpack(v[i][k], d[i][k]);
+        for (int k = 0; k < kVecs; ++k) {
+          unpack(v[i][k], d[i][k]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s = s + d[i][k][j];
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (decltype(scaled)::value) d[i][k][j] = d[i][k][j] * pair(down[i], down[i]);
+            s = s + d[i][k][j];
+          }
+        }
+        sum[i] = s.f.x + s.f.y;
       }
-      sum[i] = s.f.x + s.f.y;
-    }
-    group_sum<kThreads>(sum[0], sum[1], turn++);
-    const float mean[2] = {mean_of(sum[0], p), mean_of(sum[1], p)};
+      group_sum<kThreads>(sum[0], sum[1], turn++);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      F2 s = pair(0.0f, 0.0f);
+      for (int i = 0; i < 2; ++i) {
+        mean[i] = mean_of(sum[i], p);
+        F2 s = pair(0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        const int n = values_of<kAligned>((k * kThreads + t) * 8, p.cols);
-        const float less = n > 0 ? -mean[i] : 0.0f;  // 0 stays 0 past the row's end
+        for (int k = 0; k < kVecs; ++k) {
+          const int n = values_of<kAligned>((k * kThreads + t) * 8, p.cols);
+          const float less = n > 0 ? -mean[i] : 0.0f;  // 0 stays 0 past the row's end
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          d[i][k][j] = d[i][k][j] + pair(less, !kAligned && 2 * j + 1 >= n ? 0.0f : less);
-          if (!kAligned && 2 * j >= n) d[i][k][j].f.x = 0.0f;
-          s = fma2(d[i][k][j], d[i][k][j], s);
+          for (int j = 0; j < 4; ++j) {
+            d[i][k][j] = d[i][k][j] + pair(less, !kAligned && 2 * j + 1 >= n ? 0.0f : less);
+            if (!kAligned && 2 * j >= n) d[i][k][j].f.x = 0.0f;
+            s = fma2(d[i][k][j], d[i][k][j], s);
+          }
+        }
+        sq[i] = s.f.x + s.f.y;
+      }
+      group_sum<kThreads>(sq[0], sq[1], turn++);
+    };
+    deviations(std::false_type());
+    float rstd[2] = {__frsqrt_rn(sq[0] * p.inv_cols + p.eps), __frsqrt_rn(sq[1] * p.inv_cols + p.eps)};
+    float rstd_out[2] = {rstd[0], rstd[1]};
+    if (!(sq[0] < kInf) || !(sq[1] < kInf)) {
+      // A row whose sums leave fp32's range (or that has a NaN or an infinity): the same with
+      // 2^-72 of its values, whose squares' sum is at most 2^(2 (128 - 72) + 14).  The values are
+      // read again, as they are not kept.
+      __syncwarp();  // the neighbour may have written some of the lane's part of h
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!(sq[i] < kInf)) down[i] = kDown;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          const int c = (k * kThreads + t) * 8;
+          v[i][k] = load_values<kAligned>((kResidual ? p.h + at[i] * p.ldh : p.x + at[i] * p.ldx) + c,
+                                          i == 0 || second ? values_of<kAligned>(c, p.cols) : 0);
         }
       }
-      sq[i] = s.f.x + s.f.y;
+      deviations(std::true_type());
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float var = fmaf(sq[i], p.inv_cols, p.eps * down[i] * down[i]);
+        // Without deviations eps decides, too small to be scaled, and the deviations are 0.
+        const bool equal = var == 0.0f && p.eps > 0.0f;
+        rstd[i] = equal ? 0.0f : __frsqrt_rn(var);
+        rstd_out[i] = equal ? __frsqrt_rn(p.eps) : rstd[i] * down[i];
+        mean[i] *= 1.0f / down[i];
+      }
     }
-    group_sum<kThreads>(sq[0], sq[1], turn++);
-    const float rstd[2] = {__frsqrt_rn(sq[0] * p.inv_cols + p.eps),
-                           __frsqrt_rn(sq[1] * p.inv_cols + p.eps)};
     if (p.stats != nullptr && t < 2 && (t == 0 || second)) {
       p.stats[t == 0 ? at[0] : at[1]] = t == 0 ? mean[0] : mean[1];
-      p.stats[p.rows + (t == 0 ? at[0] : at[1])] = t == 0 ? rstd[0] : rstd[1];
+      p.stats[p.rows + (t == 0 ? at[0] : at[1])] = t == 0 ? rstd_out[0] : rstd_out[1];
     }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
