@@ -341,7 +341,8 @@ struct Ahead {
 };
 
 // What lies past the row's end needs no care: x, dy and w are loaded as 0 there,
-// so g and dy are 0 and add nothing to any sum, and dx is not stored.
+// so g and dy are 0 and add nothing to any sum as long as mean * rstd is finite, and dx
+// is not stored.
 template <int kThreads, int kVecs, bool kAligned, bool kResidual, typename P>
 __global__ void __launch_bounds__(Group<kThreads>::kBlock)
     layer_norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
@@ -416,6 +417,9 @@ __global__ void __launch_bounds__(Group<kThreads>::kBlock)
     uint4 res[kVecs];
     F2 g[kVecs][4], xhat[kVecs][4];
     F2 s1 = pair(0.0f, 0.0f), s2 = pair(0.0f, 0.0f);
+    // Only rows of equal values (xhat = 0) leave fp32's range here: different ones of 8 bits
+    // deviate by 2^-9 |mean| / sqrt(cols) at least.
+    const float r = fabsf(mean) * rstd < kInf ? rstd : 0.0f;
     if constexpr (kAligned) {
       copies_wait<kAhead - 2>();  // this row's; the thread's own, so no barrier
       fetch(row + (kAhead - 1) * step, stage == 0 ? kAhead - 1 : stage - 1);
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(Group<kThreads>::kBlock)
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        xhat[k][j] = (xhat[k][j] + pair(-mean, -mean)) * pair(rstd, rstd);
+        xhat[k][j] = (xhat[k][j] + pair(-mean, -mean)) * pair(r, r);
         g[k][j] = a[j] * w[k][j];
         dw[k][j] = fma2(a[j], xhat[k][j], dw[k][j]);
         db[k][j] = db[k][j] + a[j];

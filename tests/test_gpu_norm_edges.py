@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_gpu_norm import BF, F32, check_forward, make, params
+from test_gpu_norm import BF, F32, check_backward, check_forward, make, params
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,14 @@ def test_rows_beyond_the_range_of_their_squares(cols, shift, residual):
     into = x.clone()  # in place
     q.layer_norm(into, w, b, into, residual=r, h=None if r is None else into)
     assert torch.equal(into, y)
+
+
+@pytest.mark.parametrize("cols,shift", [(96, 0), (1531, 0), (4096, 3), (9001, 2), (16384, 0)])
+def test_the_backward_of_such_rows(cols, shift):
+    import quantised_gemm_gb300 as q
+    x, dy, (w, b) = wide_rows(cols, shift), make(20, cols, 7, 1e-2), params(cols, F32, 8)
+    y, stats, dx = torch.empty_like(x), torch.empty((2, 20), device="cuda"), torch.empty_like(x)
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    q.layer_norm(x, w, b, y, stats)
+    q.layer_norm_backward(dy, x, w, stats, dx, dw, db, q.Workspace())
+    check_backward(q, dy, x, w, stats, dx, dw, db)
