@@ -124,3 +124,49 @@ def test_an_infinity_in_x_or_dy_is_seen_in_the_gradients(k, n, rank, rows):
     seen[1, n // 3] = seen[2, n - 1] = True
     assert torch.equal(~torch.isfinite(db2), seen) and torch.equal(db2[~seen], db[~seen])
     assert torch.equal(da2[0], da[0]) and not torch.isfinite(da2[1:]).any()
+
+
+@pytest.mark.parametrize("rows", [20, 100, 700, 5000])
+@pytest.mark.parametrize("k,n,rank", [(200, 104, 16), (99, 57, 6), (256, 320, 64), (72, 136, 128), (40, 64, 32)])
+def test_sums_that_cancel_are_exact(k, n, rank, rows):
+    """Whole numbers of 16 bits as h and dh, which hi + lo holds.  From column 3 on they meet 1 and -1 in
+    pairs (of ranks in y and dx, of rows in dA and dB) that cancel but for some units; every product and
+    partial sum is a whole number below 2^24, and in columns 0 to 2 of y and dx at most 2^23 times 1 or 256,
+    so the results are the formulas' rounded once.  A bit of lo lost would be seen."""
+    import quantised_gemm_gb300 as q
+    g = torch.Generator(device="cuda").manual_seed(91)
+    ints = lambda lo, hi, shape: torch.randint(lo, hi + 1, shape, generator=g, device="cuda").float()  # noqa: E731
+    zeros = lambda *shape: torch.zeros(shape, dtype=BF, device="cuda")  # noqa: E731
+    a, b, x, dy = zeros(2, rank, k), zeros(2, n, rank), zeros(rows, k), zeros(rows, n)
+    # h_j = 256 x0 + x1, and x2 more for odd j; B has ones of changing sign, and so has A from column 3 on.
+    a[:, :, 0], a[:, :, 1], a[:, 1::2, 2] = 256.0, 1.0, 1.0
+    sign = torch.ones(rank, device="cuda")
+    sign[1::2] = -1.0
+    b[:, 3:, :] = sign
+    a[:, :, 3:] = sign[:, None]
+    b[:, 0], b[:, 1], b[:, 2, 1::2] = 256.0, 1.0, 1.0
+    pair = torch.arange(rows, device="cuda") // 2
+    index = torch.randint(0, 2, (rows // 2 + 1,), generator=g, device="cuda")[pair].to(torch.int32)
+    one = torch.where(torch.arange(rows, device="cuda") % 2 == 0, 1.0, -1.0)  # the rows of a pair
+    for t in (x, dy):
+        t[:, 0], t[:, 1] = ints(128, 250, (rows // 2 + 1,))[pair], ints(0, 250, (rows // 2 + 1,))[pair]
+        t[:, 2] = ints(1, 3, (rows,))
+    x[:, 3:], dy[:, 3:] = one[:, None], one[:, None]
+    bank = q.Adapters(a, b, torch.ones(2, device="cuda"))
+    c = Case(rows, k, n, rank, 2)  # its buffers
+    c.x, c.dy, c.bank, c.index = x, dy, bank, index
+    y = torch.empty((rows, n), dtype=BF, device="cuda")
+    c.forward(y, base=None)
+    h = torch.zeros((rows, rank), dtype=torch.float64, device="cuda")
+    dh = torch.zeros_like(h)
+    ref, dref = (torch.zeros((rows, cols), dtype=torch.float64, device="cuda") for cols in (n, k))
+    dx, da, db = c.like()
+    c.backward(dx, da, db, base=None)
+    for i, r in enumerate(c.groups()):
+        h[r], dh[r] = x[r].double() @ a[i].double().t(), dy[r].double() @ b[i].double()
+        ref[r], dref[r] = h[r] @ b[i].double().t(), dh[r] @ a[i].double()
+        assert torch.equal(da[i][:, 3:], (dh[r].t() @ x[r].double())[:, 3:].to(BF)), "dA"
+        assert torch.equal(db[i][3:], (dy[r].double().t() @ h[r])[3:].to(BF)), "dB"
+    assert float(h.abs().max()) < 2 ** 16 and float(dh.abs().max()) < 2 ** 16
+    assert torch.equal(c.h.double(), h) and torch.equal(c.dh.double(), dh)
+    assert torch.equal(y, ref.to(BF)) and torch.equal(dx, dref.to(BF))
