@@ -76,30 +76,6 @@ __device__ __forceinline__ uint4 load_if(const void* p, bool on) {
   return v;
 }
 
-__device__ __forceinline__ uint2 load2_if(const void* p, bool on) {
-  uint2 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-      "@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y)
-      : "l"(p), "r"(static_cast<int>(on)));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t load1_if(const void* p, bool on) {
-  uint32_t v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %2, 0;\n\t"
-      "mov.b32 %0, 0;\n\t"
-      "@p ld.global.b32 %0, [%1];\n\t}"
-      : "=&r"(v)
-      : "l"(p), "r"(static_cast<int>(on)));
-  return v;
-}
-
 // Copies of 16 bytes to shared memory that are on their way while the thread goes
 // on; on = false writes zeros.  Slots that only one thread writes and reads need
 // no barrier but that thread's own wait.  Registers loaded ahead wait for one
