@@ -653,8 +653,8 @@ fp8lin_status fp8lin_layer_norm(const void* x, int64_t ldx, const void* r, int64
  * dres: NULL, or the gradient that h receives past the norm (bf16 [rows, cols]):
  * dx is then the gradient of x and of r alike.  dx, dw, db: each may be NULL; dw
  * and db [cols] have w's type (param_f32).  Column sums are fp32, first over the
- * rows of a CTA and then over the CTAs, in an order that the sizes fix: the same
- * call gives the same bits.  No rows give zeros in dw and db.
+ * rows of a CTA and then over the CTAs, in an order that the sizes, ws_bytes and the
+ * number of SMs fix: the same call on the same kind of device gives the same bits.  No rows give zeros in dw and db.
  * dx_amax: NULL, or fp32[1] that receives max |dx| (it needs dx): the amax of the
  * grad_output state of the Linear whose output x is.
  * dx may be dy or dres with the same stride; no other overlap is allowed. */
@@ -706,10 +706,11 @@ fp8lin_status fp8lin_adapter_route(const int32_t* index, int64_t rows, int64_t c
  * alignments; y may be base with the same stride, and overlaps nothing else.  A row
  * without an adapter has h_i = 0 and y_i = base_i, bit for bit.  Products are
  * accumulated in fp32; s_g h_i goes in as two bf16 numbers, hi + lo (2^-17; infinite
- * from 3.396e38 on, where hi rounds past bf16's largest), but for a few rows (64 at most, 16 of
- * rank 128), which take one launch and no sorting and keep it in fp32.  The order of all sums is fixed by the sizes and the index.  FP8LIN_EUNSUPPORTED
- * where no route is given and the workspace has no room for one, which some 4 million
- * rows fill.  NaN and infinities in x stay in their rows, those of A and B in the rows
+ * from 3.396e38 on, where hi rounds past bf16's largest), but for a few rows (64 at
+ * most, 16 of rank 128), which take one launch and no sorting and keep it in fp32.  The
+ * order of all sums is fixed by the sizes and the index, on one kind of device.
+ * FP8LIN_EUNSUPPORTED where no route is given and the workspace has no room for one,
+ * which some 4 million rows fill.  NaN and infinities in x stay in their rows, those of A and B in the rows
  * of their adapter; they give what the formulas give. */
 fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, int64_t ldx,
                                     const int32_t* index, const void* route, int64_t rows,
@@ -724,9 +725,10 @@ fp8lin_status fp8lin_adapter_linear(const fp8lin_adapters* ad, const void* x, in
  * dy: bf16 [rows, n]; x, base, dx: bf16 [rows, k]; da, db: dense, of the shapes of
  * a and b, zeros for adapters that no row has.  dx, da and db may each be NULL (x
  * is needed for da, h for db only).  dx may be base with the same stride; nothing
- * else may overlap what is written (dh over an h that db needs is refused).  dh and s_g h go into the products as hi + lo.
- * The order of all sums is fixed by the sizes and the index.  dh and dx are to NaN
- * and infinities what h and y are in the forward; an infinity in x, dy, h or dh makes
+ * else may overlap what is written (dh over an h that db needs is refused).  dh and
+ * s_g h go into the products as hi + lo.  The order of all sums is fixed by the sizes,
+ * the index and the workspace's room, on one kind of device.  dh and dx are to NaN and
+ * infinities what h and y are in the forward; an infinity in x, dy, h or dh makes
  * the numbers of dA and dB that it enters infinite or NaN (where lo is 0 or of the other
  * sign than hi) and no others. */
 fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy, int64_t lddy,

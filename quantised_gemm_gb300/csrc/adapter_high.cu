@@ -3,7 +3,7 @@
 // y = base + s h B^T in the forward, dx = base + dh A in the backward.
 //
 // Bound by reading base and writing y: 16384 x 4096 with rank 16 takes 49 us (5.5 TB/s);
-// 8192 x 4096 with rank 64 46 us, of which the products of hi and lo are 14 of tensor
+// 8192 x 4096 with rank 64 47 us, of which the products of hi and lo are 14 of tensor
 // pipe and their operands' loads as much again.  A and B go through shared stages
 // (loaded from L2 for each product, rank 64 took 51 us with the operands' latency bare).
 // Rows of y that are not 16-byte aligned: 777 x 4801 with rank 8 takes 15 us; each lane

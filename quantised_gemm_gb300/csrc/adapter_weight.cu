@@ -4,8 +4,8 @@
 //
 // Bound by reading x again: 16384 rows of 14336 and 4096 columns with rank 16 take
 // 118 us (5.2 TB/s).  A cluster shares the rows of a large adapter; partial sums in
-// the workspace and a launch that adds them took 259 us instead of 248 for the whole
-// backward, and 510 instead of 357 for 8192 x 4096 x 4096 with rank 128.
+// the workspace and a launch that adds them took 11 us more, and 153 more for 8192 x 4096
+// x 4096 with rank 128.
 #include "adapter_kernels.cuh"
 
 namespace fp8lin {
@@ -29,8 +29,8 @@ struct WeightArgs {
 
 // With a small rank the rows' numbers are few beside x, and splitting the rows leaves
 // fewer CTAs to a cluster; with a large one warps of the same rows share them.  Rank 64
-// with all warps on the same rows took 52 us instead of 38 for the backward of 608 x 793
-// x 777, where a turn's latency counts, and 125 instead of 122 for 4096 x 4096 x 4096.
+// with all warps on the same rows took 14 us more for the backward of 608 x 793 x 777 (45
+// us), where a turn's latency counts, and 3 more for 4096 x 4096 x 4096 (125).
 template <int kRankTiles>
 struct WeightShape {
   static constexpr int kRowWarps = kRankTiles <= 2 ? 4 : kRankTiles <= 8 ? 2 : 1;
@@ -336,9 +336,9 @@ cudaError_t launch_adapter_weight(const AdapterArgs& a, const AdapterWeight& db,
     // More CTAs than are resident, so that an adapter with many rows does not keep the
     // others waiting, but with enough rows each for their start and their sums.  The
     // whole backward with four CTAs an SM and with eight: 16384 x 4096 x 14336, rank
-    // 16, 248 and 264 us; 4096 x 4096 x 4096, rank 64, 124 and 122.  With 128 rows and
-    // with 256: 1267 x 1600 x 2501, rank 12, 28 and 33; 1024 x 4096 x 4096, rank 64, 58
-    // and 51.
+    // 16, 264 and 262 us; 4096 x 4096 x 4096, rank 64, 129 and 125.  With 128 rows and
+    // with 256: 1267 x 1600 x 2501, rank 12 and four adapters, 33 and 36; 1024 x 4096 x
+    // 4096 of one adapter, rank 64, 48 and 45 (rank 16: 31 and 27).
     const int64_t most = (a.rank <= 32 ? 4 : 8) * int64_t(dev.num_sms), least = a.rank <= 16 ? 128 : 256;
     int parts = 1;
     while (parts < 8 && slabs * parts * 2 <= most && a.rows >= least * 2 * parts * a.count) parts *= 2;

@@ -1900,10 +1900,11 @@ fp8lin_status fp8lin_adapter_backward(const fp8lin_adapters* ad, const void* dy,
     if (e != cudaSuccess) return cuda_fail(e);
   }
   // The weight gradients' operands from h and dh, laid out once where the rows pay for
-  // that launch (16384 x 4096 x 14336 with rank 16: 256 us with it, 363 without; 1024 x
-  // 4096 x 4096: 31 and 33; 256 rows: 16.8 and 16.5; with rank 32, 318 x 5954 x 1857 of
-  // three adapters: 33.5 and 36.4; with rank 64, 201 x 5550 x 185 of six: 31.5 and 28.4)
-  // and the workspace has room.
+  // that launch (16384 x 4096 x 14336 with rank 16: 264 us with it, 386 without; 1024 x
+  // 4096 x 4096: 31 and 32; with rank 32, 318 x 5954 x 1857 of three adapters: 38.5 and
+  // 40.2) and the workspace has room.  Below that it is one launch less for the same time
+  // (256 rows of one adapter 18.9 and 19.1; with rank 64, 201 x 5550 x 185 of six 34.9 and
+  // 35.4).
   AdapterWeight wa, wb;
   if (da != nullptr) {
     wa.dw = static_cast<uint16_t*>(da);

@@ -8,13 +8,15 @@
 //
 // Bound by memory: each tensor is read or written once.  65536 x 4096 with a
 // residual: forward 303 us (7.1 TB/s), backward 350 us (6.1 TB/s) and 5 for the sums
-// over the CTAs; 12288 x 1600 from L2 15 us, of which the issue of instructions is 10.
+// over the CTAs; 12288 x 1600 from L2 14 us, of which the issue of instructions is 10.
 // Few rows are latency: 16 x 4096 takes 3 us, the backward of 256 x 4096 8 us in two
-// launches.
+// launches.  4096 x 16384 takes 102 us forward and 188 backward with a residual (5.3 and
+// 2.9 TB/s): 1024 threads leave 64 registers each, and the row's values spill.
 // A group of threads holds a row in registers, eight consecutive values a vector, so
 // the second look at the values (the deviations; the backward's dx) costs no second
 // read, and the variance is the mean of squared deviations, not a difference of
-// large sums.  Statistics and column sums are fp32, in packed pairs (half the
+// large sums.  A finite row whose sums leave fp32's range is computed once more from 2^-72
+// of its values.  Statistics and column sums are fp32, in packed pairs (half the
 // instructions); y, h and dx are rounded once.  The forward takes two rows of a group
 // at a time and one CTA a pair: 304 us where CTAs that loop over rows took 328.
 // In the backward a thread owns the same columns of every row that its CTA takes and
