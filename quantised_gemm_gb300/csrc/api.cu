@@ -1318,10 +1318,9 @@ Fp4GemmArgs fp4_gemm_args(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b
   return g;
 }
 
-// b_early: the launch before this one in the stream does not write b.
 fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* b, void* d,
                            int64_t ldd, void* ws, size_t ws_bytes, const DeviceInfo& dev,
-                           cudaStream_t stream, bool b_early = false) {
+                           cudaStream_t stream) {
   if (a->rows == 0 || b->rows == 0) return FP8LIN_OK;
   if (a->cols == 0) {
     cudaError_t e = cudaMemset2DAsync(d, static_cast<size_t>(ldd) * 2, 0,
@@ -1330,7 +1329,6 @@ fp8lin_status run_fp4_gemm(const fp8lin_fp4_tensor* a, const fp8lin_fp4_tensor* 
     return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
   }
   Fp4GemmArgs g = fp4_gemm_args(a, b, d, ldd, ws, ws_bytes);
-  g.b_early = b_early;
   ProfScope ps(FP8LIN_PROF_GEMM, stream);
   cudaError_t e = launch_fp4_gemm(g, dev, stream);
   return e == cudaSuccess ? FP8LIN_OK : cuda_fail(e);
@@ -1354,8 +1352,7 @@ fp8lin_status run_fp4_linear(const QuantJob& job, const fp8lin_fp4_tensor* w4, v
   }
   fp8lin_status s;
   if ((s = run_quantise(&job, 1, ws, dev, stream)) != FP8LIN_OK) return s;
-  // The launch before the product is x's quantisation, which does not write w4.
-  return run_fp4_gemm(job.out, w4, y, ldy, ws, ws_bytes, dev, stream, !empty);
+  return run_fp4_gemm(job.out, w4, y, ldy, ws, ws_bytes, dev, stream);
 }
 
 // Whether two 4-bit tensors are one tensor and its transpose, by their sizes.

@@ -260,9 +260,7 @@ __device__ __forceinline__ void join_partials(const Fp4GemmParams& p, const floa
 // more of 32 x 4096 x 14336.)
 //
 // Bound by reading the weight (0.56 bytes a value): the split brings enough
-// CTAs, two an SM, to keep that many loads in flight.  With `early` the
-// preceding kernel of the stream is known not to write A, so its first
-// stages are loaded before that kernel has finished.
+// CTAs, two an SM, to keep that many loads in flight.
 //
 // 32 x 4096 x 14336 9.5 us in NVFP4, the weight at 3.5 TB/s (the launch and
 // the join take 4 us of it); 1 x 4096 x 4096 5.6 us; 128 x 4096 x 4096 7.7 and
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<kFmt, BN, STAGES>::kPerSm)
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmSa,
                         const __grid_constant__ CUtensorMap tmSb,
-                        const __grid_constant__ Fp4GemmParams p, const int split, const bool early) {
+                        const __grid_constant__ Fp4GemmParams p, const int split) {
   using C = FewCfg<kFmt, BN, STAGES>;
   constexpr int kKt = stage_ktiles<kFmt>();
   extern __shared__ uint8_t smem_raw[];
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, FewCfg<kFmt, BN, STAGES>::kPerSm)
     tma_load_2d(sSa + stage * C::kScBytes, &tmSa, &full[stage], kb * kKt * kScElems, m_blk);
   };
   if (threadIdx.x == 0) {  // the weight's first stages, before anything else
-    if (!early) griddep_wait();
+    griddep_wait();
     for (int i = 0; i < nkb && i < STAGES; ++i) load_a(i, kb0 + i);
   }
   if (warp == 1) {
@@ -1496,7 +1494,7 @@ cudaError_t run_few(const Fp4GemmArgs& g, Fp4GemmParams p, const DeviceInfo& dev
   set_error_site("gemm_fp4_few_kernel");
   return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * split)), dim3(kThreads),
                        C::kSmemBytes + joined_bytes<BN>(split), stream, split, false, tmA, tmB, tmSa,
-                       tmSb, p, split, g.b_early);
+                       tmSb, p, split);
 }
 
 // How the fused product runs these sizes; stages 0: it does not.

@@ -372,7 +372,6 @@ struct Fp4GemmArgs {
   void* d;
   int64_t ldd;
   int* ws_error;
-  bool b_early = false;  // the kernel before this one in the stream does not write b
   int* ws_tickets = nullptr;  // as GemmArgs': no K split of a last wave without
   int* ws_begun = nullptr;
   float* ws_split = nullptr;

@@ -30,3 +30,11 @@ def test_a_kernel_waits_before_it_reads(name):
         before = body[:at]
         assert not re.search(r"__ld|find_tile|load_|copy|\*\w|\w\[(?!\])", re.sub(r"__shared__[^;]*;", "", before)), (kernel, before)
         assert body.index("griddep_launch_dependents();") > at
+
+
+def test_no_wait_depends_on_the_launch():
+    """What a launch two before wrote is no more visible without the wait than what the last one wrote."""
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            for line in f:
+                assert not re.search(r"if \(!?[\w.]+\) griddep_wait\(\)", line), (name, line)
